@@ -22,8 +22,9 @@ LIB_PATH = os.path.join(_HERE, "libbqmm_san.so" if os.environ.get("BQMM_SANITIZE
 
 BQ_OK, BQ_EINVAL, BQ_EUNSUPPORTED, BQ_EALIGN, BQ_EHIP = 0, -1, -2, -3, -4
 
-# name -> (restype, argtypes); P = pointer, U32/U64 = unsigned ints, I = int
+# name -> (restype, argtypes); P = pointer, U32/U64 = unsigned ints, I = int, F/D = float/double
 _P, _U32, _U64, _I = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int
+_F, _D = ctypes.c_float, ctypes.c_double
 EXPORTS = {
     "bq_last_error": (ctypes.c_char_p, []),
     "bq_status_string": (ctypes.c_char_p, [_I]),
@@ -46,6 +47,15 @@ EXPORTS = {
     "q4k_gemv_vec": (_I, [_P, _P, _P, _U32, _U32, _P]),
     "quantize_weight_q4k": (_I, [_P, _P, _U32, _U32, _P]),
     "silu_mul_bf16": (_I, [_P, _P, _P, _U64, _P]),
+    "int8_rows_bytes": (_U64, [_U32, _U32]),
+    "gated_delta_rule_workspace_bytes": (_U64, [_U32] * 6),
+    "add_rms_norm_bf16": (_I, [_P, _P, _P, _P, _U32, _U32, _D, _P]),
+    "add_rms_norm_quantize_q8_1": (_I, [_P, _P, _P, _P, _U32, _U32, _D, _P]),
+    "add_rms_norm_quantize_int8": (_I, [_P, _P, _P, _P, _U32, _U32, _D, _P]),
+    "quantize_rows_int8": (_I, [_P, _P, _U32, _U32, _P]),
+    "w8a8_gemm": (_I, [_P, _P, _P, _P, _U32, _U32, _U32, _P]),
+    "gated_delta_rule_recurrent": (_I, [_P] * 10 + [_U32] * 7 + [_U64] * 6 + [_F, _I, _P]),
+    "gated_delta_rule_chunked": (_I, [_P] * 11 + [_U64] + [_U32] * 7 + [_U64] * 6 + [_F, _I, _P]),
     "q2_0_mmq_blockdots": (_I, [_P, _P, _P, _U32, _U32, _U32, _U32, _U32, _U32, _U32, _P]),
     "q4k_mmq_blockdots": (_I, [_P, _P, _P, _U32, _U32, _U32, _U32, _U32, _U32, _U32, _P]),
 }
@@ -288,6 +298,116 @@ def silu_mul_bf16(gate, up, out, count: int | None = None, stream=None):
     for t, what in ((gate, "gate"), (up, "up"), (out, "out")):
         _need(_bf16(t, what), 2 * count, what)
     _check(lib().silu_mul_bf16(*_ptrs(gate, up, out), count, _stream(stream)))
+
+
+def int8_rows_bytes(rows: int, k: int) -> int:
+    return int(lib().int8_rows_bytes(rows, k))
+
+
+def gated_delta_rule_workspace_bytes(tokens: int, count: int, hk: int, hv: int, dk: int, dv: int) -> int:
+    return int(lib().gated_delta_rule_workspace_bytes(tokens, count, hk, hv, dk, dv))
+
+
+def _norm(fn, x, residual, weight, out, m, k, eps, stream):
+    _need(_bf16(x, "x"), _bf(m, k), "x")
+    if residual is not None:
+        _need(_bf16(residual, "residual"), _bf(m, k), "residual")
+    _need(_bf16(weight, "weight"), _bf(1, k), "weight")
+    _check(fn(*_ptrs(x, residual, weight, out), m, k, eps, _stream(stream)))
+
+
+def add_rms_norm_bf16(x, residual, weight, out, m: int, k: int, eps: float = 1e-6, stream=None):
+    """residual is updated in place; None: a plain norm of x."""
+    _need(_bf16(out, "out"), _bf(m, k), "out")
+    _norm(lib().add_rms_norm_bf16, x, residual, weight, out, m, k, eps, stream)
+
+
+def add_rms_norm_quantize_q8_1(x, residual, weight, out_q8, m: int, k: int, eps: float = 1e-6, stream=None):
+    _need(_u8(out_q8, "out_q8"), q8_1_act_bytes(m, k), "out_q8")
+    _norm(lib().add_rms_norm_quantize_q8_1, x, residual, weight, out_q8, m, k, eps, stream)
+
+
+def add_rms_norm_quantize_int8(x, residual, weight, out_i8, m: int, k: int, eps: float = 1e-6, stream=None):
+    _need(_u8(out_i8, "out_i8"), int8_rows_bytes(m, k), "out_i8")
+    _norm(lib().add_rms_norm_quantize_int8, x, residual, weight, out_i8, m, k, eps, stream)
+
+
+def quantize_rows_int8(x, out_i8, rows: int, k: int, stream=None):
+    _need(_bf16(x, "x"), _bf(rows, k), "x")
+    _need(_u8(out_i8, "out_i8"), int8_rows_bytes(rows, k), "out_i8")
+    _check(lib().quantize_rows_int8(*_ptrs(x, out_i8), rows, k, _stream(stream)))
+
+
+def w8a8_gemm(act_i8, w_i8, out, m: int, n: int, k: int, bias=None, stream=None):
+    _need(_u8(act_i8, "act_i8"), int8_rows_bytes(m, k), "act_i8")
+    _need(_u8(w_i8, "w_i8"), int8_rows_bytes(n, k), "w_i8")
+    _need(_bf16(out, "out"), _bf(m, n), "out")
+    if bias is not None:
+        _need(_bf16(bias, "bias"), _bf(1, n), "bias")
+    _check(lib().w8a8_gemm(*_ptrs(act_i8, w_i8, bias, out), m, n, k, _stream(stream)))
+
+
+def _typed(t, dtype, shape, what):
+    """A contiguous tensor of this type and shape (None passes through)."""
+    if t is None:
+        return t
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+    return t
+
+
+def _heads(t, shape, what):
+    """A [tokens, heads, d] bf16 tensor, its last dimension contiguous: (token stride, head stride)."""
+    _bf16(t, what)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+    token, head, one = t.stride()
+    if (shape[2] > 1 and one != 1) or token < 0 or head < 0:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return token, head
+
+
+def _delta(fn, q, k, v, g, beta, out, state, starts, slots, fresh, workspace, scale, l2norm, stream):
+    import torch
+    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4 or starts.dim() != 1 or starts.numel() < 1:
+        raise ValueError("expected q, k, v as [tokens, heads, d], state as [slots, hv, dk, dv], starts as [count + 1]")
+    (tokens, hk, dk), (hv, dv), count = q.shape, v.shape[1:], starts.numel() - 1
+    _typed(g, torch.float32, (tokens, hv), "g")
+    _typed(beta, torch.float32, (tokens, hv), "beta")
+    _typed(out, torch.bfloat16, (tokens, hv, dv), "out")
+    _typed(state, torch.float32, (state.shape[0], hv, dk, dv), "state")
+    _typed(starts, torch.int32, (count + 1,), "starts")
+    _typed(slots, torch.int32, (count,), "slots")
+    _typed(fresh, torch.uint8, (count,), "fresh")
+    strides = [*_heads(q, (tokens, hk, dk), "q"), *_heads(k, (tokens, hk, dk), "k"), *_heads(v, (tokens, hv, dv), "v")]
+    if not (q.is_cuda and k.is_cuda and v.is_cuda):
+        raise ValueError("expected a device tensor")
+    _same_device(q, k, v, g, beta, out, state, starts, slots, fresh, *workspace)
+    if slots is None and state.shape[0] < count:
+        raise ValueError(f"state: {state.shape[0]} slots for {count} sequences")
+    rest = [_ptr(t) for t in (g, beta, out, state, starts, slots, fresh)]
+    room = [x for w in workspace for x in (_ptr(w), _nbytes(w))]
+    scale = dk ** -0.5 if scale is None else scale
+    _check(fn(*(ctypes.c_void_p(t.data_ptr()) for t in (q, k, v)), *rest, *room, tokens, count, state.shape[0],
+              hk, hv, dk, dv, *strides, scale, int(bool(l2norm)), _stream(stream)))
+
+
+def gated_delta_rule_recurrent(q, k, v, g, beta, out, state, starts, slots=None, fresh=None, l2norm: bool = True,
+                               scale: float | None = None, stream=None):
+    """q, k: [tokens, hk, dk], v: [tokens, hv, dv] bf16, each head's values contiguous; g, beta: [tokens, hv]
+    float32; out: [tokens, hv, dv] bf16; state: [slots, hv, dk, dv] float32, updated in place; starts: [count + 1],
+    slots: [count] int32; fresh: [count] uint8.  scale: dk ** -0.5 by default."""
+    _delta(lib().gated_delta_rule_recurrent, q, k, v, g, beta, out, state, starts, slots, fresh, (), scale, l2norm,
+           stream)
+
+
+def gated_delta_rule_chunked(q, k, v, g, beta, out, state, starts, workspace, slots=None, fresh=None,
+                             l2norm: bool = True, scale: float | None = None, stream=None):
+    """As gated_delta_rule_recurrent, for prompts; workspace: gated_delta_rule_workspace_bytes(...) bytes, uint8."""
+    _delta(lib().gated_delta_rule_chunked, q, k, v, g, beta, out, state, starts, slots, fresh,
+           (_u8(workspace, "workspace"),), scale, l2norm, stream)
 
 
 def _blockdots(fn, act_q8, w, w_bytes, out_i32, m0, mt, n0, nt, m, n, k, stream):

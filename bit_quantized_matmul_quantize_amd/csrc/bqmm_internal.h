@@ -134,5 +134,35 @@ hipError_t launch_q4k_mmq(const void *act_q8, const void *w, void *out, int32_t 
                           uint32_t n, uint32_t k, uint32_t ldc, hipStream_t s);
 hipError_t launch_dense_gemm_bf16(const void *a, const void *w, void *out, uint32_t m, uint32_t n,
                                   uint32_t k, hipStream_t s);
+// residual may be null
+hipError_t launch_add_rms_norm_bf16(const void *x, void *residual, const void *weight, void *out, uint32_t m,
+                                    uint32_t k, double eps, hipStream_t s);
+hipError_t launch_add_rms_norm_quantize_int8(const void *x, void *residual, const void *weight, void *out,
+                                             uint32_t m, uint32_t k, double eps, hipStream_t s);
+hipError_t launch_add_rms_norm_quantize_q8_1(const void *x, void *residual, const void *weight, void *out,
+                                             uint32_t m, uint32_t k, double eps, hipStream_t s);
+hipError_t launch_quantize_rows_int8(const void *x, void *out, uint32_t rows, uint32_t k, hipStream_t s);
+// bias may be null
+hipError_t launch_w8a8_gemm(const void *act, const void *w, const void *bias, void *out, uint32_t m, uint32_t n,
+                            uint32_t k, hipStream_t s);
+
+// The gated delta rule's arguments: strides in values, heads of q and k are
+// shared by hv / hk value heads; slots and fresh may be null.
+struct DeltaArgs {
+  const uint16_t *q, *k, *v;
+  const float *g, *beta;
+  uint16_t *out;
+  float *state;
+  const int32_t *starts, *slots;
+  const uint8_t *fresh;
+  uint8_t *workspace;
+  uint64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  uint32_t tokens, count, state_slots, hk, hv, dk, dv;
+  float scale;
+  int l2norm;
+};
+hipError_t launch_delta_recurrent(const DeltaArgs &a, hipStream_t s);
+hipError_t launch_delta_chunked(const DeltaArgs &a, hipStream_t s);
+uint64_t delta_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hk, uint32_t hv, uint32_t dk);
 
 }  // namespace bqmm

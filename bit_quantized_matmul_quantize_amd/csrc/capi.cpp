@@ -467,3 +467,226 @@ int silu_mul_bf16(const void *gate, const void *up, void *out, uint64_t count, v
 }
 
 }  // extern "C"
+
+// ---- norm, int8 product and gated delta rule -------------------------------
+
+namespace {
+
+bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1u)) == 0u; }
+
+uint64_t i8_bytes(uint32_t rows, uint32_t k) { return (uint64_t)rows * (((uint64_t)k + 127u) / 128u * 128u + 4u); }
+
+int check_norm(const char *name, const void *x, const void *residual, const void *weight, const void *out, uint32_t m,
+               uint32_t k, double eps, uint64_t nout) {
+  REQUIRE(x && weight && out, BQ_EINVAL, "%s: null pointer", name);
+  REQUIRE(m >= 1 && k >= 1, BQ_EINVAL, "%s: m=%u k=%u must be >= 1", name, m, k);
+  REQUIRE(k <= kMaxK && m < kMaxRows, BQ_EINVAL, "%s: m=%u k=%u too large", name, m, k);
+  REQUIRE(eps >= 0.0 && eps <= 1e30, BQ_EINVAL, "%s: eps=%g must be a number >= 0", name, eps);
+  REQUIRE(aligned16(x) && aligned16(residual) && aligned16(weight) && aligned16(out), BQ_EALIGN,
+          "%s: buffers must be 16-byte aligned", name);
+  REQUIRE_DISJOINT(name, out, nout, x, bf16_bytes(m, k), "the input");
+  REQUIRE_DISJOINT(name, out, nout, weight, bf16_bytes(1, k), "the weight");
+  if (residual) {
+    REQUIRE_DISJOINT(name, out, nout, residual, bf16_bytes(m, k), "the residual");
+    REQUIRE(!overlap(residual, bf16_bytes(m, k), x, bf16_bytes(m, k)) &&
+                !overlap(residual, bf16_bytes(m, k), weight, bf16_bytes(1, k)),
+            BQ_EINVAL, "%s: the residual overlaps an input", name);
+  }
+  return BQ_OK;
+}
+
+// Bytes from the first value of a strided [tokens][heads][d] bf16 array to
+// past its last; ~0 where that passes 2^62.
+uint64_t heads_span(uint32_t tokens, uint32_t heads, uint32_t d, uint64_t token, uint64_t head) {
+  const unsigned __int128 last =
+      (unsigned __int128)(tokens - 1u) * token + (unsigned __int128)(heads - 1u) * head + d;
+  return last >= ((unsigned __int128)1 << 61) ? ~0ull : 2u * (uint64_t)last;
+}
+
+// What the two forms of the delta rule check alike; *nothing is set where
+// there is nothing to do.
+int check_delta(const char *name, const bqmm::DeltaArgs &a, bool *nothing) {
+  *nothing = a.count == 0u;
+  REQUIRE(a.hk >= 1 && a.hv >= 1 && a.hv % a.hk == 0, BQ_EINVAL, "%s: hk=%u must divide hv=%u", name, a.hk, a.hv);
+  REQUIRE(a.dk >= 1 && a.dv >= 1, BQ_EINVAL, "%s: dk=%u dv=%u must be >= 1", name, a.dk, a.dv);
+  REQUIRE(a.dk <= 128, BQ_EUNSUPPORTED, "%s: dk=%u > 128", name, a.dk);
+  REQUIRE(a.hv <= 65535u && a.dv <= 65535u && a.tokens < kMaxRows && a.count < kMaxRows && a.state_slots < kMaxRows,
+          BQ_EINVAL, "%s: tokens=%u count=%u slots=%u hv=%u dv=%u too large", name, a.tokens, a.count, a.state_slots,
+          a.hv, a.dv);
+  // one grid dimension: a workgroup for at most eight columns of a head's state
+  REQUIRE((uint64_t)a.count * a.hv < (1ull << 31) / ((a.dv + 7u) / 8u), BQ_EINVAL,
+          "%s: count=%u hv=%u dv=%u too large", name, a.count, a.hv, a.dv);
+  if (*nothing) return BQ_OK;
+  REQUIRE(a.starts, BQ_EINVAL, "%s: null pointer", name);
+  REQUIRE(a.state || a.state_slots == 0, BQ_EINVAL, "%s: null state", name);
+  REQUIRE(aligned_to(a.state, 4) && aligned_to(a.starts, 4) && aligned_to(a.slots, 4) && aligned_to(a.g, 4) &&
+              aligned_to(a.beta, 4),
+          BQ_EALIGN, "%s: binary32 and int32 arrays must be 4-byte aligned", name);
+  const uint64_t nstate = 4ull * a.hv * a.dk * a.dv * a.state_slots;
+  REQUIRE(!a.state_slots || nstate / a.state_slots == 4ull * a.hv * a.dk * a.dv, BQ_EINVAL, "%s: the state is too large",
+          name);
+  REQUIRE_DISJOINT(name, a.state, nstate, a.starts, 4ull * a.count + 4u, "starts");
+  REQUIRE(!a.slots || !overlap(a.state, nstate, a.slots, 4ull * a.count), BQ_EINVAL, "%s: the state overlaps slots", name);
+  REQUIRE(!a.fresh || !overlap(a.state, nstate, a.fresh, a.count), BQ_EINVAL, "%s: the state overlaps fresh", name);
+  if (a.tokens == 0) return BQ_OK;
+  REQUIRE(a.q && a.k && a.v && a.g && a.beta && a.out, BQ_EINVAL, "%s: null pointer", name);
+  REQUIRE(aligned_to(a.q, 2) && aligned_to(a.k, 2) && aligned_to(a.v, 2) && aligned_to(a.out, 2), BQ_EALIGN,
+          "%s: bf16 arrays must be 2-byte aligned", name);
+  const uint64_t nout = bf16_bytes((uint64_t)a.tokens * a.hv, a.dv), ng = 4ull * a.tokens * a.hv;
+  const struct {
+    const void *p;
+    uint64_t n;
+    const char *what;
+  } in[5] = {{a.q, heads_span(a.tokens, a.hk, a.dk, a.q_token, a.q_head), "q"},
+             {a.k, heads_span(a.tokens, a.hk, a.dk, a.k_token, a.k_head), "k"},
+             {a.v, heads_span(a.tokens, a.hv, a.dv, a.v_token, a.v_head), "v"},
+             {a.g, ng, "g"},
+             {a.beta, ng, "beta"}};
+  for (const auto &i : in) {
+    REQUIRE(i.n < (1ull << 62), BQ_EINVAL, "%s: the strides of %s are too large", name, i.what);
+    REQUIRE_DISJOINT(name, a.out, nout, i.p, i.n, i.what);
+    REQUIRE(!overlap(a.state, nstate, i.p, i.n), BQ_EINVAL, "%s: the state overlaps %s", name, i.what);
+  }
+  REQUIRE(!overlap(a.state, nstate, a.out, nout), BQ_EINVAL, "%s: the state overlaps the output", name);
+  REQUIRE_DISJOINT(name, a.out, nout, a.starts, 4ull * a.count + 4u, "starts");
+  REQUIRE(!a.slots || !overlap(a.out, nout, a.slots, 4ull * a.count), BQ_EINVAL, "%s: the output overlaps slots", name);
+  REQUIRE(!a.fresh || !overlap(a.out, nout, a.fresh, a.count), BQ_EINVAL, "%s: the output overlaps fresh", name);
+  return BQ_OK;
+}
+
+bqmm::DeltaArgs delta_args(const void *q, const void *k, const void *v, const float *g, const float *beta, void *out,
+                           float *state, const int32_t *starts, const int32_t *slots, const uint8_t *fresh,
+                           void *workspace, uint32_t tokens, uint32_t count, uint32_t state_slots, uint32_t hk,
+                           uint32_t hv, uint32_t dk, uint32_t dv, uint64_t q_token, uint64_t q_head, uint64_t k_token,
+                           uint64_t k_head, uint64_t v_token, uint64_t v_head, float scale, int l2norm) {
+  return {static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(k), static_cast<const uint16_t *>(v), g, beta,
+          static_cast<uint16_t *>(out), state, starts, slots, fresh, static_cast<uint8_t *>(workspace), q_token, q_head,
+          k_token, k_head, v_token, v_head, tokens, count, state_slots, hk, hv, dk, dv, scale, l2norm};
+}
+
+}  // namespace
+
+extern "C" {
+
+uint64_t int8_rows_bytes(uint32_t rows, uint32_t k) { return k > kMaxK ? 0 : i8_bytes(rows, k); }
+
+int add_rms_norm_bf16(const void *x_bf16, void *residual_bf16, const void *weight_bf16, void *out_bf16, uint32_t m,
+                      uint32_t k, double eps, void *stream) {
+  const char *name = "add_rms_norm_bf16";
+  const int st = check_norm(name, x_bf16, residual_bf16, weight_bf16, out_bf16, m, k, eps, bf16_bytes(m, k));
+  if (st != BQ_OK) return st;
+  return hip_status(
+      bqmm::launch_add_rms_norm_bf16(x_bf16, residual_bf16, weight_bf16, out_bf16, m, k, eps, as_stream(stream)), name);
+}
+
+int add_rms_norm_quantize_q8_1(const void *x_bf16, void *residual_bf16, const void *weight_bf16, void *out_q8,
+                               uint32_t m, uint32_t k, double eps, void *stream) {
+  const char *name = "add_rms_norm_quantize_q8_1";
+  const int st = check_norm(name, x_bf16, residual_bf16, weight_bf16, out_q8, m, k, eps, q8_bytes(m, k));
+  if (st != BQ_OK) return st;
+  return hip_status(bqmm::launch_add_rms_norm_quantize_q8_1(x_bf16, residual_bf16, weight_bf16, out_q8, m, k, eps,
+                                                            as_stream(stream)),
+                    name);
+}
+
+int add_rms_norm_quantize_int8(const void *x_bf16, void *residual_bf16, const void *weight_bf16, void *out_i8,
+                               uint32_t m, uint32_t k, double eps, void *stream) {
+  const char *name = "add_rms_norm_quantize_int8";
+  const int st = check_norm(name, x_bf16, residual_bf16, weight_bf16, out_i8, m, k, eps, i8_bytes(m, k));
+  if (st != BQ_OK) return st;
+  return hip_status(bqmm::launch_add_rms_norm_quantize_int8(x_bf16, residual_bf16, weight_bf16, out_i8, m, k, eps,
+                                                            as_stream(stream)),
+                    name);
+}
+
+int quantize_rows_int8(const void *x_bf16, void *out_i8, uint32_t rows, uint32_t k, void *stream) {
+  const char *name = "quantize_rows_int8";
+  REQUIRE(x_bf16 && out_i8, BQ_EINVAL, "%s: null pointer", name);
+  REQUIRE(rows >= 1 && k >= 1, BQ_EINVAL, "%s: rows=%u k=%u must be >= 1", name, rows, k);
+  REQUIRE(k <= kMaxK && rows < kMaxRows, BQ_EINVAL, "%s: rows=%u k=%u too large", name, rows, k);
+  REQUIRE(aligned16(x_bf16) && aligned16(out_i8), BQ_EALIGN, "%s: buffers must be 16-byte aligned", name);
+  REQUIRE_DISJOINT(name, out_i8, i8_bytes(rows, k), x_bf16, bf16_bytes(rows, k), "the input");
+  return hip_status(bqmm::launch_quantize_rows_int8(x_bf16, out_i8, rows, k, as_stream(stream)), name);
+}
+
+int w8a8_gemm(const void *act_i8, const void *w_i8, const void *bias_bf16, void *out_bf16, uint32_t m, uint32_t n,
+              uint32_t k, void *stream) {
+  const char *name = "w8a8_gemm";
+  REQUIRE(act_i8 && w_i8 && out_bf16, BQ_EINVAL, "%s: null pointer", name);
+  REQUIRE(m >= 1 && n >= 1 && k >= 1, BQ_EINVAL, "%s: m=%u n=%u k=%u must be >= 1", name, m, n, k);
+  REQUIRE(k <= 131071u, BQ_EINVAL, "%s: k=%u too large for exact int32 sums (at most 131071)", name, k);
+  REQUIRE(m < kMaxRows && ((uint64_t)n + 127u) / 128u <= kMaxGridY, BQ_EINVAL, "%s: m=%u n=%u too large", name, m, n);
+  REQUIRE(aligned16(act_i8) && aligned16(w_i8) && aligned16(out_bf16) && aligned_to(bias_bf16, 2), BQ_EALIGN,
+          "%s: buffers must be 16-byte aligned (the bias 2-byte)", name);
+  REQUIRE_DISJOINT(name, out_bf16, bf16_bytes(m, n), act_i8, i8_bytes(m, k), "the activations");
+  REQUIRE_DISJOINT(name, out_bf16, bf16_bytes(m, n), w_i8, i8_bytes(n, k), "the weight");
+  REQUIRE(!bias_bf16 || !overlap(out_bf16, bf16_bytes(m, n), bias_bf16, bf16_bytes(1, n)), BQ_EINVAL,
+          "%s: the output overlaps the bias", name);
+  return hip_status(bqmm::launch_w8a8_gemm(act_i8, w_i8, bias_bf16, out_bf16, m, n, k, as_stream(stream)), name);
+}
+
+uint64_t gated_delta_rule_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hk, uint32_t hv, uint32_t dk,
+                                          uint32_t dv) {
+  if (hk == 0 || hv == 0 || hv % hk != 0 || dk == 0 || dk > 128 || dv == 0 || hv > 65535u || dv > 65535u ||
+      tokens >= kMaxRows || count >= kMaxRows)
+    return 0;
+  return bqmm::delta_workspace_bytes(tokens, count, hk, hv, dk);
+}
+
+int gated_delta_rule_recurrent(const void *q_bf16, const void *k_bf16, const void *v_bf16, const float *g,
+                               const float *beta, void *out_bf16, float *state, const int32_t *starts,
+                               const int32_t *slots, const uint8_t *fresh, uint32_t tokens, uint32_t count,
+                               uint32_t state_slots, uint32_t hk, uint32_t hv, uint32_t dk, uint32_t dv,
+                               uint64_t q_token, uint64_t q_head, uint64_t k_token, uint64_t k_head, uint64_t v_token,
+                               uint64_t v_head, float scale, int l2norm, void *stream) {
+  const bqmm::DeltaArgs a =
+      delta_args(q_bf16, k_bf16, v_bf16, g, beta, out_bf16, state, starts, slots, fresh, nullptr, tokens, count,
+                 state_slots, hk, hv, dk, dv, q_token, q_head, k_token, k_head, v_token, v_head, scale, l2norm);
+  bool nothing = false;
+  const int st = check_delta("gated_delta_rule_recurrent", a, &nothing);
+  if (st != BQ_OK) return st;
+  return hip_status(nothing ? hipSuccess : bqmm::launch_delta_recurrent(a, as_stream(stream)),
+                    "gated_delta_rule_recurrent");
+}
+
+int gated_delta_rule_chunked(const void *q_bf16, const void *k_bf16, const void *v_bf16, const float *g,
+                             const float *beta, void *out_bf16, float *state, const int32_t *starts,
+                             const int32_t *slots, const uint8_t *fresh, void *workspace, uint64_t workspace_bytes,
+                             uint32_t tokens, uint32_t count, uint32_t state_slots, uint32_t hk, uint32_t hv,
+                             uint32_t dk, uint32_t dv, uint64_t q_token, uint64_t q_head, uint64_t k_token,
+                             uint64_t k_head, uint64_t v_token, uint64_t v_head, float scale, int l2norm,
+                             void *stream) {
+  const char *name = "gated_delta_rule_chunked";
+  const bqmm::DeltaArgs a =
+      delta_args(q_bf16, k_bf16, v_bf16, g, beta, out_bf16, state, starts, slots, fresh, workspace, tokens, count,
+                 state_slots, hk, hv, dk, dv, q_token, q_head, k_token, k_head, v_token, v_head, scale, l2norm);
+  bool nothing = false;
+  const int st = check_delta(name, a, &nothing);
+  if (st != BQ_OK) return st;
+  if (!nothing) {
+    const uint64_t need = gated_delta_rule_workspace_bytes(tokens, count, hk, hv, dk, dv);
+    REQUIRE(workspace, BQ_EINVAL, "%s: null workspace", name);
+    REQUIRE(workspace_bytes >= need, BQ_EINVAL, "%s: the workspace holds %llu bytes, %llu are needed", name,
+            (unsigned long long)workspace_bytes, (unsigned long long)need);
+    REQUIRE(aligned16(workspace), BQ_EALIGN, "%s: the workspace must be 16-byte aligned", name);
+    const struct {
+      const void *p;
+      uint64_t n;
+      const char *what;
+    } other[8] = {{q_bf16, tokens ? heads_span(tokens, hk, dk, q_token, q_head) : 0, "q"},
+                  {k_bf16, tokens ? heads_span(tokens, hk, dk, k_token, k_head) : 0, "k"},
+                  {v_bf16, tokens ? heads_span(tokens, hv, dv, v_token, v_head) : 0, "v"},
+                  {g, 4ull * tokens * hv, "g"},
+                  {beta, 4ull * tokens * hv, "beta"},
+                  {out_bf16, bf16_bytes((uint64_t)tokens * hv, dv), "the output"},
+                  {state, 4ull * hv * dk * dv * state_slots, "the state"},
+                  {starts, 4ull * count + 4u, "starts"}};
+    for (const auto &o : other)
+      REQUIRE(!overlap(workspace, need, o.p, o.n), BQ_EINVAL, "%s: the workspace overlaps %s", name, o.what);
+    REQUIRE(!(slots && overlap(workspace, need, slots, 4ull * count)) && !(fresh && overlap(workspace, need, fresh, count)),
+            BQ_EINVAL, "%s: the workspace overlaps slots or fresh", name);
+  }
+  return hip_status(nothing ? hipSuccess : bqmm::launch_delta_chunked(a, as_stream(stream)), name);
+}
+
+}  // extern "C"

@@ -1,0 +1,165 @@
+// The gated delta rule, token by token.
+//
+// Per value head, with the state S [dk][dv] in binary32 and for each token
+// a = exp(g), b = beta (and with l2norm q, k divided by sqrt(|.|^2 + 1e-6)):
+//   u = b (v - a k^T S),   S' = a S + k u,   o = scale q^T S'.
+// With k^T S, q^T S and q.k from one look at S, o = scale (a q^T S + (q.k) u):
+// S is read once and updated once per token.  The norms of q and k are common
+// factors of those sums, so q and k stay as they were read (exact bf16).
+//
+// The columns of S are independent of each other, so a wave takes one head's
+// 4 kQuads columns and all dk rows: a lane holds four columns (16-byte loads)
+// of kRows consecutive rows, and the sums over rows end in a butterfly over
+// the 64 / kQuads lanes that share the columns.  The state stays in registers
+// over a sequence's tokens.
+//
+// Bound by memory where the batch is large: 8 dk dv bytes of state move for
+// 6 dk dv operations per token.
+#include "delta_common.h"
+
+namespace bqmm {
+namespace {
+
+constexpr float kNormEps = 1e-6f;
+
+struct __attribute__((packed, aligned(4))) Float4 {
+  float v[4];
+};
+template <int N>
+struct __attribute__((packed, aligned(2))) Bf16s {
+  uint16_t v[N];
+};
+
+// N bf16 values from row r0 of dk; rows past dk are zero.
+template <int N>
+__device__ __forceinline__ void load_rows(const uint16_t *p, uint32_t r0, uint32_t dk, float (&v)[N]) {
+  if (r0 + N <= dk) {
+    const Bf16s<N> a = *reinterpret_cast<const Bf16s<N> *>(p + r0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = bf16_to_f32(a.v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = r0 + i < dk ? bf16_to_f32(p[r0 + i]) : 0.0f;
+  }
+}
+
+template <int kDk, int kQuads>
+__global__ __launch_bounds__(64) void delta_recurrent_kernel(const DeltaArgs a) {
+  constexpr int kGroups = 64 / kQuads;
+  constexpr int kRows = kDk / kGroups;
+  const uint32_t quad = threadIdx.x % kQuads, r0 = threadIdx.x / kQuads * kRows;
+  const uint32_t blocks = (a.dv + 4u * kQuads - 1u) / (4u * kQuads);
+  const uint32_t head_seq = blockIdx.x / blocks;
+  const uint32_t hv = head_seq % a.hv, seq = head_seq / a.hv;
+  const uint32_t hk = hv / (a.hv / a.hk);
+  const uint32_t c0 = (blockIdx.x - head_seq * blocks) * (4u * kQuads) + quad * 4u;
+  const uint32_t cols = c0 < a.dv ? min(a.dv - c0, 4u) : 0u;
+
+  const DeltaSeq sq = delta_sequence(a, seq);
+  if (sq.begin >= sq.end && !sq.fresh) return;  // nothing changes
+
+  float4 s[kRows];
+  float *state = a.state + ((uint64_t)max(sq.slot, 0) * a.hv + hv) * a.dk * a.dv + c0;
+  const bool from_state = sq.slot >= 0 && !sq.fresh;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    s[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (from_state && r0 + i < a.dk) {
+      const float *p = state + (uint64_t)(r0 + i) * a.dv;
+      if (cols == 4u) {
+        const Float4 f = *reinterpret_cast<const Float4 *>(p);
+        s[i] = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
+      } else {
+        if (cols > 0u) s[i].x = p[0];
+        if (cols > 1u) s[i].y = p[1];
+        if (cols > 2u) s[i].z = p[2];
+      }
+    }
+  }
+
+  for (uint32_t t = sq.begin; t < sq.end; ++t) {
+    float q[kRows], k[kRows], v[4];
+    load_rows<kRows>(a.q + (uint64_t)t * a.q_token + (uint64_t)hk * a.q_head, r0, a.dk, q);
+    load_rows<kRows>(a.k + (uint64_t)t * a.k_token + (uint64_t)hk * a.k_head, r0, a.dk, k);
+    const uint16_t *vp = a.v + (uint64_t)t * a.v_token + (uint64_t)hv * a.v_head + c0;
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) v[j] = j < cols ? bf16_to_f32(vp[j]) : 0.0f;
+    const float decay = expf(a.g[(uint64_t)t * a.hv + hv]), beta = a.beta[(uint64_t)t * a.hv + hv];
+
+    // k^T S, q^T S (four columns each), |k|^2, |q|^2, q.k
+    float sum[11];
+#pragma unroll
+    for (int j = 0; j < 11; ++j) sum[j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      sum[0] = fmaf(k[i], s[i].x, sum[0]);
+      sum[1] = fmaf(k[i], s[i].y, sum[1]);
+      sum[2] = fmaf(k[i], s[i].z, sum[2]);
+      sum[3] = fmaf(k[i], s[i].w, sum[3]);
+      sum[4] = fmaf(q[i], s[i].x, sum[4]);
+      sum[5] = fmaf(q[i], s[i].y, sum[5]);
+      sum[6] = fmaf(q[i], s[i].z, sum[6]);
+      sum[7] = fmaf(q[i], s[i].w, sum[7]);
+      sum[8] = fmaf(k[i], k[i], sum[8]);
+      sum[9] = fmaf(q[i], q[i], sum[9]);
+      sum[10] = fmaf(q[i], k[i], sum[10]);
+    }
+#pragma unroll
+    for (int d = kQuads; d < 64; d <<= 1)
+#pragma unroll
+      for (int j = 0; j < 11; ++j) sum[j] += __shfl_xor(sum[j], d);
+    const float rk = a.l2norm ? 1.0f / sqrtf(sum[8] + kNormEps) : 1.0f;
+    const float rq = (a.l2norm ? 1.0f / sqrtf(sum[9] + kNormEps) : 1.0f) * a.scale;
+
+    float u[4], o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u[j] = rk * (beta * (v[j] - decay * (rk * sum[j])));  // with k's factor for the update
+      o[j] = rq * fmaf(sum[10], u[j], decay * sum[4 + j]);
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      s[i].x = fmaf(k[i], u[0], decay * s[i].x);
+      s[i].y = fmaf(k[i], u[1], decay * s[i].y);
+      s[i].z = fmaf(k[i], u[2], decay * s[i].z);
+      s[i].w = fmaf(k[i], u[3], decay * s[i].w);
+    }
+    if (threadIdx.x < kQuads) {
+      uint16_t *op = a.out + ((uint64_t)t * a.hv + hv) * a.dv + c0;
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j)
+        if (j < cols) op[j] = (uint16_t)f32_to_bf16_rne(o[j]);
+    }
+  }
+
+  if (sq.slot < 0) return;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (r0 + i >= a.dk) continue;
+    float *p = state + (uint64_t)(r0 + i) * a.dv;
+    if (cols == 4u) {
+      Float4 f;
+      f.v[0] = s[i].x; f.v[1] = s[i].y; f.v[2] = s[i].z; f.v[3] = s[i].w;
+      *reinterpret_cast<Float4 *>(p) = f;
+    } else {
+      if (cols > 0u) p[0] = s[i].x;
+      if (cols > 1u) p[1] = s[i].y;
+      if (cols > 2u) p[2] = s[i].z;
+    }
+  }
+}
+
+template <int kDk, int kQuads>
+hipError_t launch_recurrent(const DeltaArgs &a, hipStream_t s) {
+  const uint64_t blocks = (uint64_t)a.count * a.hv * ((a.dv + 4ull * kQuads - 1u) / (4ull * kQuads));
+  hipLaunchKernelGGL((delta_recurrent_kernel<kDk, kQuads>), dim3((uint32_t)blocks), dim3(64), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_recurrent(const DeltaArgs &a, hipStream_t s) {
+  return a.dk <= 64u ? launch_recurrent<64, 8>(a, s) : launch_recurrent<128, 8>(a, s);
+}
+
+}  // namespace bqmm

@@ -27,6 +27,11 @@
  *     ties away from zero), s = fp16(d * sum q); padding values are zero.
  *     Total q8_1_act_bytes(m, k) = 1.125*m*kpad bytes.
  *
+ *   int8 rows [rows][k], kpad = ceil(k/128)*128: codes plane, int8
+ *     [rows][kpad] at byte 0, then a binary32 scale per row at byte rows*kpad +
+ *     4*r.  Value = scale * code, |code| <= 127; padding codes are zero.  Total
+ *     int8_rows_bytes(rows, k) = rows*(kpad + 4) bytes.
+ *
  *   Q2_0 weight [n][k], group G (G = 128 for the matmul kernels):
  *     codes plane, n*k/4 bytes at byte 0: row r, group g occupies bytes
  *     [r*k/4 + g*G/4, +G/4); byte t of a group holds the 2-bit codes of
@@ -99,6 +104,16 @@ uint64_t q2_0_weight_bytes(uint32_t n, uint32_t k, uint32_t group);
 /* Bytes of a Q4_K weight [n][k]: n*(k/256)*144 (page layers/ops/q4k_mmq.rs,
  * fn q4k_weight_bytes).  0 if k % 256 != 0 or on overflow. */
 uint64_t q4k_weight_bytes(uint32_t n, uint32_t k);
+
+/* Bytes of the int8 rows of [rows][k]: rows*(kpad + 4), kpad = ceil(k/128)*128.
+ * 0 on overflow (k > 2^30). */
+uint64_t int8_rows_bytes(uint32_t rows, uint32_t k);
+
+/* Workspace of gated_delta_rule_chunked for these sizes (an upper bound over
+ * every split of `tokens` into `count` sequences).  0 where the call would
+ * refuse the sizes. */
+uint64_t gated_delta_rule_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hk, uint32_t hv,
+                                          uint32_t dk, uint32_t dv);
 
 /* ---- the hot path -------------------------------------------------------- */
 
@@ -276,6 +291,87 @@ int quantize_weight_q4k(const void *w_bf16, void *out_q4k, uint32_t n, uint32_t 
  * [page layers/dense_ffn_decode_batch.rs, fn forward_km_q2: silu_mul over
  *  m * intermediate elements with the output over the gate buffer.] */
 int silu_mul_bf16(const void *gate, const void *up, void *out, uint64_t count, void *stream);
+
+/* ---- norm, int8 product and gated delta rule around the projections -------- */
+
+/* RMS norm with the residual's addition:
+ *   h = bf16_rne(x + residual), written back to residual (h = x where residual is NULL),
+ *   y[i][j] = h[i][j] * weight[j] / sqrt(mean_j(h[i][j]^2) + eps),
+ * the mean and the root in binary64.  x, residual: [m][k] bf16; weight: [k] bf16.
+ * The output:
+ *   add_rms_norm_bf16           [m][k] bf16_rne(y)
+ *   add_rms_norm_quantize_q8_1  the q8_1 form of those bf16 values, as
+ *                               quantize_act_q8_1 gives it (q8_1_act_bytes(m, k) bytes)
+ *   add_rms_norm_quantize_int8  int8 rows of y (int8_rows_bytes(m, k) bytes): per row,
+ *                               with t = h * weight and top = max |t|, code =
+ *                               rint(127 t / top) (exact quotient, ties to even) and
+ *                               scale = top / (127 sqrt(...)); zero codes where top is 0.
+ * A row that holds a NaN or an infinity gives NaN: in bf16 where the formula
+ * does, in int8 rows as a NaN scale; its q8_1 bytes are unspecified.  m, k >= 1;
+ * any k.  No two buffers may overlap. */
+int add_rms_norm_bf16(const void *x_bf16, void *residual_bf16, const void *weight_bf16, void *out_bf16,
+                      uint32_t m, uint32_t k, double eps, void *stream);
+int add_rms_norm_quantize_q8_1(const void *x_bf16, void *residual_bf16, const void *weight_bf16, void *out_q8,
+                               uint32_t m, uint32_t k, double eps, void *stream);
+int add_rms_norm_quantize_int8(const void *x_bf16, void *residual_bf16, const void *weight_bf16, void *out_i8,
+                               uint32_t m, uint32_t k, double eps, void *stream);
+
+/* bf16 rows [rows][k] -> int8 rows (weights [n][k] or activations [m][k]):
+ * top = max |x| of the row, code = rint(127 x / top) (exact quotient, ties to
+ * even), scale = top / 127; zero codes where top is 0.  A row that holds a NaN
+ * or an infinity gets that as its scale, and zero codes.  rows, k >= 1. */
+int quantize_rows_int8(const void *x_bf16, void *out_i8, uint32_t rows, uint32_t k, void *stream);
+
+/* out[i][j] (bf16, [m][n]) = sum_t a[i][t] * w[j][t] * sa[i] * sw[j] + bias[j]:
+ * the sum of code products exact in int32 on the int8 matrix cores, scales and
+ * bias in binary32, one rounding to bf16.  act_i8: int8 rows [m][k]; w_i8: int8
+ * rows [n][k]; bias_bf16: [n] or NULL.  m, n >= 1, 1 <= k <= 131071 (beyond it
+ * the sum of 131072 products could pass int32). */
+int w8a8_gemm(const void *act_i8, const void *w_i8, const void *bias_bf16, void *out_bf16,
+              uint32_t m, uint32_t n, uint32_t k, void *stream);
+
+/* The gated delta rule over packed sequences.  Sequence i holds the tokens
+ * [starts[i], starts[i + 1]) of q, k, v, g, beta and out.  Per value head h
+ * (it reads key head h / (hv / hk)), with its state S [dk][dv] in binary32 and
+ * for each token a = exp(g[token][h]), b = beta[token][h]:
+ *   S = a S;  S = S + k (b (v - k^T S))^T;  out[token][h] = bf16_rne(scale q^T S).
+ * With l2norm != 0, q and k are divided by sqrt(|.|^2 + 1e-6) first.
+ *
+ * q, k: bf16, head i of token t starts at t * q_token + i * q_head (values), its
+ * dk values are consecutive; v likewise with dv.  g, beta: binary32
+ * [tokens][hv], g <= 0 (-infinity forgets everything).  out: bf16
+ * [tokens][hv][dv].  state: binary32 [state_slots][hv][dk][dv], updated in place;
+ * sequence i owns slot slots[i] (i itself where slots is NULL), no two
+ * sequences the same one.  A slot outside [0, state_slots) starts from zeros and
+ * its final state is not kept.  fresh: a byte per sequence, not 0: it starts
+ * from zeros, whatever its slot holds; NULL: none does.  starts: [count + 1]
+ * int32 on the device, ascending; ranges outside [0, tokens) are cut off.  Tokens
+ * of no sequence are left alone.  An empty sequence keeps its state (zeros where
+ * it is fresh).
+ *
+ * 1 <= dk <= 128, dv >= 1, hk divides hv.  q, k, v, out 2-byte aligned, the
+ * binary32 and int32 arrays 4-byte.  out and state overlap nothing else.
+ * tokens = 0 is allowed (the token arrays may be NULL), and count = 0 (nothing
+ * is done).  Captured into a graph, a call reads starts, slots and fresh at
+ * each replay.
+ *
+ * _recurrent takes the tokens of a sequence one by one: for decoding, and for
+ * a few tokens.  _chunked takes them in chunks of 64, within a chunk by matrix
+ * products: for prompts.  workspace: gated_delta_rule_workspace_bytes(...) bytes,
+ * 16-byte aligned, for this call alone until it has run. */
+int gated_delta_rule_recurrent(const void *q_bf16, const void *k_bf16, const void *v_bf16, const float *g,
+                               const float *beta, void *out_bf16, float *state, const int32_t *starts,
+                               const int32_t *slots, const uint8_t *fresh, uint32_t tokens, uint32_t count,
+                               uint32_t state_slots, uint32_t hk, uint32_t hv, uint32_t dk, uint32_t dv,
+                               uint64_t q_token, uint64_t q_head, uint64_t k_token, uint64_t k_head,
+                               uint64_t v_token, uint64_t v_head, float scale, int l2norm, void *stream);
+int gated_delta_rule_chunked(const void *q_bf16, const void *k_bf16, const void *v_bf16, const float *g,
+                             const float *beta, void *out_bf16, float *state, const int32_t *starts,
+                             const int32_t *slots, const uint8_t *fresh, void *workspace, uint64_t workspace_bytes,
+                             uint32_t tokens, uint32_t count, uint32_t state_slots, uint32_t hk, uint32_t hv,
+                             uint32_t dk, uint32_t dv, uint64_t q_token, uint64_t q_head, uint64_t k_token,
+                             uint64_t k_head, uint64_t v_token, uint64_t v_head, float scale, int l2norm,
+                             void *stream);
 
 /* ---- test hooks: integer block dot products ---------------------------- */
 

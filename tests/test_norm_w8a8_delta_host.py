@@ -1,0 +1,196 @@
+"""Host-side refusals (no GPU) of the norms, the int8 product and the gated delta rule: the C ABI's argument checks,
+which run before any HIP call, and the binding's checks of types, shapes and sizes."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def bq():
+    import os
+    import bit_quantized_matmul_quantize_amd as m
+    if not os.path.exists(m.LIB_PATH):
+        from bit_quantized_matmul_quantize_amd import build
+        build.build()
+    return m
+
+
+P = ctypes.c_void_p
+
+
+def at(i):
+    return P(0x10000000 * i)  # fake device addresses, far apart: every call below is refused before they are used
+
+
+A, B, C, D, MIS, ODD = at(1), at(2), at(3), at(4), P(0x10000008), P(0x10000001)
+
+NORMS = ("add_rms_norm_bf16", "add_rms_norm_quantize_q8_1", "add_rms_norm_quantize_int8")
+
+
+@pytest.mark.parametrize("name", NORMS)
+@pytest.mark.parametrize("args,status,needle", [
+    ((None, B, C, D, 4, 64, 1e-6, None), -1, "null"),
+    ((A, B, None, D, 4, 64, 1e-6, None), -1, "null"),
+    ((A, B, C, None, 4, 64, 1e-6, None), -1, "null"),
+    ((A, B, C, D, 0, 64, 1e-6, None), -1, "m=0"),
+    ((A, B, C, D, 4, 0, 1e-6, None), -1, "k=0"),
+    ((A, B, C, D, 4, (1 << 30) + 1, 1e-6, None), -1, "too large"),
+    ((A, B, C, D, 1 << 31, 64, 1e-6, None), -1, "too large"),
+    ((A, B, C, D, 4, 64, -1.0, None), -1, "eps"),
+    ((A, B, C, D, 4, 64, float("nan"), None), -1, "eps"),
+    ((MIS, B, C, D, 4, 64, 1e-6, None), -3, "aligned"),
+    ((A, MIS, C, D, 4, 64, 1e-6, None), -3, "aligned"),
+    ((A, B, C, A, 4, 64, 1e-6, None), -1, "overlaps the input"),
+    ((A, B, C, B, 4, 64, 1e-6, None), -1, "overlaps the residual"),
+    ((A, B, C, C, 4, 64, 1e-6, None), -1, "overlaps the weight"),
+    ((A, A, C, D, 4, 64, 1e-6, None), -1, "residual overlaps"),
+])
+def test_norm_refusals(bq, name, args, status, needle):
+    assert getattr(bq.lib(), name)(*args) == status
+    assert needle in bq.lib().bq_last_error().decode()
+
+
+@pytest.mark.parametrize("call,status,needle", [
+    (lambda l: l.quantize_rows_int8(None, B, 4, 64, None), -1, "null"),
+    (lambda l: l.quantize_rows_int8(A, B, 0, 64, None), -1, "rows=0"),
+    (lambda l: l.quantize_rows_int8(A, B, 4, (1 << 30) + 1, None), -1, "too large"),
+    (lambda l: l.quantize_rows_int8(A, MIS, 4, 64, None), -3, "aligned"),
+    (lambda l: l.quantize_rows_int8(A, P(0x10000000 + 256), 4, 64, None), -1, "overlaps"),
+    (lambda l: l.w8a8_gemm(A, B, None, None, 4, 64, 64, None), -1, "null"),
+    (lambda l: l.w8a8_gemm(A, B, None, C, 0, 64, 64, None), -1, "m=0"),
+    (lambda l: l.w8a8_gemm(A, B, None, C, 4, 0, 64, None), -1, "n=0"),
+    (lambda l: l.w8a8_gemm(A, B, None, C, 4, 64, 0, None), -1, "k=0"),
+    (lambda l: l.w8a8_gemm(A, B, None, C, 4, 64, 131072, None), -1, "131071"),
+    (lambda l: l.w8a8_gemm(A, B, None, C, 4, 65535 * 128 + 1, 64, None), -1, "too large"),
+    (lambda l: l.w8a8_gemm(A, B, None, MIS, 4, 64, 64, None), -3, "aligned"),
+    (lambda l: l.w8a8_gemm(A, B, ODD, C, 4, 64, 64, None), -3, "bias"),
+    (lambda l: l.w8a8_gemm(A, B, None, A, 4, 64, 64, None), -1, "overlaps the activations"),
+    (lambda l: l.w8a8_gemm(A, B, None, B, 4, 64, 64, None), -1, "overlaps the weight"),
+    (lambda l: l.w8a8_gemm(A, B, P(0x30000000 + 16), C, 4, 64, 64, None), -1, "overlaps the bias"),
+])
+def test_int8_refusals(bq, call, status, needle):
+    assert call(bq.lib()) == status
+    assert needle in bq.lib().bq_last_error().decode()
+
+
+def delta_args(**change):
+    d = dict(q=at(1), k=at(2), v=at(3), g=at(4), beta=at(5), out=at(6), state=at(7), starts=at(8), slots=at(9),
+             fresh=at(10), tokens=70, count=2, state_slots=3, hk=2, hv=4, dk=64, dv=32, q_token=128, q_head=64,
+             k_token=128, k_head=64, v_token=128, v_head=32, scale=0.125, l2norm=1, stream=None)
+    d.update(change)
+    return d
+
+
+DELTA = [
+    (dict(q=None), -1, "null"), (dict(beta=None), -1, "null"), (dict(out=None), -1, "null"),
+    (dict(starts=None), -1, "null"), (dict(state=None), -1, "null state"),
+    (dict(hk=0), -1, "hk=0"), (dict(hk=3), -1, "must divide"), (dict(dk=0), -1, "dk=0"), (dict(dv=0), -1, "dv=0"),
+    (dict(dk=129), -2, "129"), (dict(hv=65536, hk=1), -1, "too large"), (dict(tokens=1 << 31), -1, "too large"),
+    (dict(count=(1 << 31) - 1), -1, "too large"),
+    (dict(q=ODD), -3, "2-byte"), (dict(g=P(0x40000002)), -3, "4-byte"), (dict(state=P(0x70000002)), -3, "4-byte"),
+    (dict(q_token=1 << 62), -1, "strides of q"), (dict(v_head=(1 << 64) - 1), -1, "strides of v"),
+    (dict(out=at(1)), -1, "overlaps q"), (dict(out=at(4)), -1, "overlaps g"), (dict(state=at(3)), -1, "overlaps v"),
+    (dict(state=at(6)), -1, "overlaps the output"), (dict(state=at(8)), -1, "overlaps starts"),
+    (dict(state=at(9)), -1, "overlaps slots"), (dict(out=at(8)), -1, "overlaps starts"),
+    (dict(out=at(10)), -1, "overlaps fresh"),
+    # q's rows lie apart: it is the strides that make it reach the output
+    (dict(q_token=0x50000000 // 2 // 69), -1, "overlaps q"),
+]
+
+
+@pytest.mark.parametrize("change,status,needle", DELTA)
+@pytest.mark.parametrize("chunked", [False, True])
+def test_delta_refusals(bq, chunked, change, status, needle):
+    d = delta_args(**change)
+    v = list(d.values())
+    if chunked:
+        v[10:10] = [at(12), 1 << 28]
+        got = bq.lib().gated_delta_rule_chunked(*v)
+    else:
+        got = bq.lib().gated_delta_rule_recurrent(*v)
+    assert got == status
+    assert needle in bq.lib().bq_last_error().decode()
+
+
+@pytest.mark.parametrize("workspace,size,status,needle", [
+    (None, 1 << 28, -1, "null workspace"), (at(12), 100, -1, "are needed"), (P(0x1008), 1 << 28, -3, "16-byte"),
+    (at(7), 1 << 28, -1, "overlaps the state"), (at(2), 1 << 28, -1, "overlaps k"),
+    (at(9), 1 << 28, -1, "overlaps slots"),
+])
+def test_chunked_workspace_refusals(bq, workspace, size, status, needle):
+    v = list(delta_args().values())
+    v[10:10] = [workspace, size]
+    assert bq.lib().gated_delta_rule_chunked(*v) == status
+    assert needle in bq.lib().bq_last_error().decode()
+
+
+def test_empty_batch_is_no_error(bq):
+    v = list(delta_args(count=0, tokens=0, q=None, k=None, v=None, g=None, beta=None, out=None).values())
+    assert bq.lib().gated_delta_rule_recurrent(*v) == 0
+
+
+def test_sizes(bq):
+    assert bq.int8_rows_bytes(3, 1) == 3 * 132 and bq.int8_rows_bytes(5, 129) == 5 * 260
+    assert bq.int8_rows_bytes(4096, 17408) == 4096 * 17412 and bq.int8_rows_bytes(1, (1 << 30) + 1) == 0
+    assert bq.gated_delta_rule_workspace_bytes(64, 1, 2, 3, 64, 64) == 0  # hk does not divide hv
+    assert bq.gated_delta_rule_workspace_bytes(64, 1, 1, 1, 129, 64) == 0
+    big, small = (bq.gated_delta_rule_workspace_bytes(t, 1, 16, 32, 128, 128) for t in (16384, 64))
+    assert 0 < small < big
+
+
+def bf(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def u8(n):
+    return torch.zeros(n, dtype=torch.uint8)
+
+
+def test_binding_checks_sizes_and_types(bq):
+    m, k, n = 3, 130, 17
+    rows = bq.int8_rows_bytes
+    short = [
+        (lambda: bq.add_rms_norm_bf16(bf(m * k - 1), None, bf(k), bf(m * k), m, k), "x"),
+        (lambda: bq.add_rms_norm_bf16(bf(m * k), bf(m * k - 1), bf(k), bf(m * k), m, k), "residual"),
+        (lambda: bq.add_rms_norm_bf16(bf(m * k), None, bf(k - 1), bf(m * k), m, k), "weight"),
+        (lambda: bq.add_rms_norm_bf16(bf(m * k), None, bf(k), bf(m * k - 1), m, k), "out"),
+        (lambda: bq.add_rms_norm_quantize_q8_1(bf(m * k), None, bf(k), u8(bq.q8_1_act_bytes(m, k) - 1), m, k), "out_q8"),
+        (lambda: bq.add_rms_norm_quantize_int8(bf(m * k), None, bf(k), u8(rows(m, k) - 1), m, k), "out_i8"),
+        (lambda: bq.quantize_rows_int8(bf(m * k), u8(rows(m, k) - 1), m, k), "out_i8"),
+        (lambda: bq.w8a8_gemm(u8(rows(m, k) - 1), u8(rows(n, k)), bf(m * n), m, n, k), "act_i8"),
+        (lambda: bq.w8a8_gemm(u8(rows(m, k)), u8(rows(n, k) - 1), bf(m * n), m, n, k), "w_i8"),
+        (lambda: bq.w8a8_gemm(u8(rows(m, k)), u8(rows(n, k)), bf(m * n), m, n, k, bias=bf(n - 1)), "bias"),
+    ]
+    for call, what in short:
+        with pytest.raises(ValueError) as e:
+            call()
+        assert str(e.value).startswith(what + ":") and "address" in str(e.value)
+    with pytest.raises(TypeError, match="bfloat16"):
+        bq.add_rms_norm_bf16(torch.zeros(m * k), None, bf(k), bf(m * k), m, k)
+    with pytest.raises(ValueError, match="device tensor"):
+        bq.w8a8_gemm(u8(rows(m, k)), u8(rows(n, k)), bf(m * n), m, n, k)
+
+
+def test_binding_checks_delta_shapes(bq):
+    t, hk, hv, dk, dv, c = 5, 1, 2, 16, 24, 2
+    ok = dict(q=bf(t, hk, dk), k=bf(t, hk, dk), v=bf(t, hv, dv), g=torch.zeros(t, hv), beta=torch.zeros(t, hv),
+              out=bf(t, hv, dv), state=torch.zeros(c, hv, dk, dv), starts=torch.zeros(c + 1, dtype=torch.int32))
+    for change, err, needle in [
+        (dict(q=bf(t, dk)), ValueError, "tokens, heads"),
+        (dict(k=bf(t, hk, dk + 1)), ValueError, "k:"),
+        (dict(v=bf(t + 1, hv, dv)), ValueError, "v:"),
+        (dict(g=torch.zeros(t, hv, dtype=torch.float64)), TypeError, "g:"),
+        (dict(beta=torch.zeros(t, hv + 1)), ValueError, "beta:"),
+        (dict(out=torch.zeros(t, hv, dv)), TypeError, "out:"),
+        (dict(state=torch.zeros(c, hv, dv, dk)), ValueError, "state:"),
+        (dict(state=torch.zeros(c - 1, hv, dk, dv)), ValueError, "device tensor|slots for"),
+        (dict(starts=torch.zeros(c + 1, dtype=torch.int64)), TypeError, "starts:"),
+        (dict(slots=torch.zeros(c + 1, dtype=torch.int32)), ValueError, "slots:"),
+        (dict(fresh=torch.zeros(c, dtype=torch.bool)), TypeError, "fresh:"),
+        (dict(), ValueError, "device tensor"),
+    ]:
+        with pytest.raises(err, match=needle):
+            bq.gated_delta_rule_recurrent(**{**ok, **change})
+    with pytest.raises(TypeError, match="workspace"):
+        bq.gated_delta_rule_chunked(**ok, workspace=bf(16))
