@@ -156,7 +156,7 @@ struct DeltaArgs {
   const int32_t *starts, *slots;
   const uint8_t *fresh;
   uint8_t *workspace;
-  uint64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  uint32_t q_token, q_head, k_token, k_head, v_token, v_head;
   uint32_t tokens, count, state_slots, hk, hv, dk, dv;
   float scale;
   int l2norm;

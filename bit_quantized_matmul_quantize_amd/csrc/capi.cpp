@@ -496,11 +496,9 @@ int check_norm(const char *name, const void *x, const void *residual, const void
 }
 
 // Bytes from the first value of a strided [tokens][heads][d] bf16 array to
-// past its last; ~0 where that passes 2^62.
-uint64_t heads_span(uint32_t tokens, uint32_t heads, uint32_t d, uint64_t token, uint64_t head) {
-  const unsigned __int128 last =
-      (unsigned __int128)(tokens - 1u) * token + (unsigned __int128)(heads - 1u) * head + d;
-  return last >= ((unsigned __int128)1 << 61) ? ~0ull : 2u * (uint64_t)last;
+// past its last (the sum stays below 2^56: the strides are below 2^24 and 2^31).
+uint64_t heads_span(uint32_t tokens, uint32_t heads, uint32_t d, uint32_t token, uint32_t head) {
+  return tokens ? 2u * ((tokens - 1ull) * token + (heads - 1ull) * head + d) : 0u;
 }
 
 // What the two forms of the delta rule check alike; *nothing is set where
@@ -510,7 +508,7 @@ int check_delta(const char *name, const bqmm::DeltaArgs &a, bool *nothing) {
   REQUIRE(a.hk >= 1 && a.hv >= 1 && a.hv % a.hk == 0, BQ_EINVAL, "%s: hk=%u must divide hv=%u", name, a.hk, a.hv);
   REQUIRE(a.dk >= 1 && a.dv >= 1, BQ_EINVAL, "%s: dk=%u dv=%u must be >= 1", name, a.dk, a.dv);
   REQUIRE(a.dk <= 128, BQ_EUNSUPPORTED, "%s: dk=%u > 128", name, a.dk);
-  REQUIRE(a.hv <= 65535u && a.dv <= 65535u && a.tokens < kMaxRows && a.count < kMaxRows && a.state_slots < kMaxRows,
+  REQUIRE(a.hv <= 65535u && a.dv <= 65535u && (uint64_t)a.hv * a.dv < (1ull << 24) && a.tokens < kMaxRows && a.count < kMaxRows && a.state_slots < kMaxRows,
           BQ_EINVAL, "%s: tokens=%u count=%u slots=%u hv=%u dv=%u too large", name, a.tokens, a.count, a.state_slots,
           a.hv, a.dv);
   // one grid dimension: a workgroup for at most eight columns of a head's state
@@ -543,7 +541,6 @@ int check_delta(const char *name, const bqmm::DeltaArgs &a, bool *nothing) {
              {a.g, ng, "g"},
              {a.beta, ng, "beta"}};
   for (const auto &i : in) {
-    REQUIRE(i.n < (1ull << 62), BQ_EINVAL, "%s: the strides of %s are too large", name, i.what);
     REQUIRE_DISJOINT(name, a.out, nout, i.p, i.n, i.what);
     REQUIRE(!overlap(a.state, nstate, i.p, i.n), BQ_EINVAL, "%s: the state overlaps %s", name, i.what);
   }
@@ -554,14 +551,52 @@ int check_delta(const char *name, const bqmm::DeltaArgs &a, bool *nothing) {
   return BQ_OK;
 }
 
-bqmm::DeltaArgs delta_args(const void *q, const void *k, const void *v, const float *g, const float *beta, void *out,
-                           float *state, const int32_t *starts, const int32_t *slots, const uint8_t *fresh,
-                           void *workspace, uint32_t tokens, uint32_t count, uint32_t state_slots, uint32_t hk,
-                           uint32_t hv, uint32_t dk, uint32_t dv, uint64_t q_token, uint64_t q_head, uint64_t k_token,
-                           uint64_t k_head, uint64_t v_token, uint64_t v_head, float scale, int l2norm) {
-  return {static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(k), static_cast<const uint16_t *>(v), g, beta,
-          static_cast<uint16_t *>(out), state, starts, slots, fresh, static_cast<uint8_t *>(workspace), q_token, q_head,
-          k_token, k_head, v_token, v_head, tokens, count, state_slots, hk, hv, dk, dv, scale, l2norm};
+// The arguments as the kernels take them.  A stride that is never used (one
+// token, one head) counts as zero, whatever it is.
+int delta_args(const char *name, bqmm::DeltaArgs *args, const void *q, const void *k, const void *v, const float *g,
+               const float *beta, void *out, float *state, const int32_t *starts, const int32_t *slots,
+               const uint8_t *fresh, void *workspace, uint32_t tokens, uint32_t count, uint32_t state_slots, uint32_t hk,
+               uint32_t hv, uint32_t dk, uint32_t dv, uint64_t q_token, uint64_t q_head, uint64_t k_token,
+               uint64_t k_head, uint64_t v_token, uint64_t v_head, float scale, int l2norm) {
+  const struct {
+    uint64_t *token, *head;
+    uint32_t heads;
+    const char *what;
+  } strides[3] = {{&q_token, &q_head, hk, "q"}, {&k_token, &k_head, hk, "k"}, {&v_token, &v_head, hv, "v"}};
+  for (const auto &s : strides) {
+    if (tokens <= 1u) *s.token = 0;
+    if (s.heads <= 1u) *s.head = 0;
+    // (the offset of a chunk's 64th token is a 32-bit one)
+    REQUIRE(*s.token < (1ull << 24) && *s.head < (1ull << 31), BQ_EINVAL, "%s: the strides of %s are too large", name,
+            s.what);
+  }
+  *args = {static_cast<const uint16_t *>(q),
+           static_cast<const uint16_t *>(k),
+           static_cast<const uint16_t *>(v),
+           g,
+           beta,
+           static_cast<uint16_t *>(out),
+           state,
+           starts,
+           slots,
+           fresh,
+           static_cast<uint8_t *>(workspace),
+           (uint32_t)q_token,
+           (uint32_t)q_head,
+           (uint32_t)k_token,
+           (uint32_t)k_head,
+           (uint32_t)v_token,
+           (uint32_t)v_head,
+           tokens,
+           count,
+           state_slots,
+           hk,
+           hv,
+           dk,
+           dv,
+           scale,
+           l2norm};
+  return BQ_OK;
 }
 
 }  // namespace
@@ -627,7 +662,7 @@ int w8a8_gemm(const void *act_i8, const void *w_i8, const void *bias_bf16, void 
 
 uint64_t gated_delta_rule_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hk, uint32_t hv, uint32_t dk,
                                           uint32_t dv) {
-  if (hk == 0 || hv == 0 || hv % hk != 0 || dk == 0 || dk > 128 || dv == 0 || hv > 65535u || dv > 65535u ||
+  if (hk == 0 || hv == 0 || hv % hk != 0 || dk == 0 || dk > 128 || dv == 0 || hv > 65535u || dv > 65535u || (uint64_t)hv * dv >= (1ull << 24) ||
       tokens >= kMaxRows || count >= kMaxRows)
     return 0;
   return bqmm::delta_workspace_bytes(tokens, count, hk, hv, dk);
@@ -639,11 +674,11 @@ int gated_delta_rule_recurrent(const void *q_bf16, const void *k_bf16, const voi
                                uint32_t state_slots, uint32_t hk, uint32_t hv, uint32_t dk, uint32_t dv,
                                uint64_t q_token, uint64_t q_head, uint64_t k_token, uint64_t k_head, uint64_t v_token,
                                uint64_t v_head, float scale, int l2norm, void *stream) {
-  const bqmm::DeltaArgs a =
-      delta_args(q_bf16, k_bf16, v_bf16, g, beta, out_bf16, state, starts, slots, fresh, nullptr, tokens, count,
+  bqmm::DeltaArgs a{};
+  int st = delta_args("gated_delta_rule_recurrent", &a, q_bf16, k_bf16, v_bf16, g, beta, out_bf16, state, starts, slots, fresh, nullptr, tokens, count,
                  state_slots, hk, hv, dk, dv, q_token, q_head, k_token, k_head, v_token, v_head, scale, l2norm);
   bool nothing = false;
-  const int st = check_delta("gated_delta_rule_recurrent", a, &nothing);
+  if (st == BQ_OK) st = check_delta("gated_delta_rule_recurrent", a, &nothing);
   if (st != BQ_OK) return st;
   return hip_status(nothing ? hipSuccess : bqmm::launch_delta_recurrent(a, as_stream(stream)),
                     "gated_delta_rule_recurrent");
@@ -657,11 +692,11 @@ int gated_delta_rule_chunked(const void *q_bf16, const void *k_bf16, const void 
                              uint64_t k_head, uint64_t v_token, uint64_t v_head, float scale, int l2norm,
                              void *stream) {
   const char *name = "gated_delta_rule_chunked";
-  const bqmm::DeltaArgs a =
-      delta_args(q_bf16, k_bf16, v_bf16, g, beta, out_bf16, state, starts, slots, fresh, workspace, tokens, count,
+  bqmm::DeltaArgs a{};
+  int st = delta_args(name, &a, q_bf16, k_bf16, v_bf16, g, beta, out_bf16, state, starts, slots, fresh, workspace, tokens, count,
                  state_slots, hk, hv, dk, dv, q_token, q_head, k_token, k_head, v_token, v_head, scale, l2norm);
   bool nothing = false;
-  const int st = check_delta(name, a, &nothing);
+  if (st == BQ_OK) st = check_delta(name, a, &nothing);
   if (st != BQ_OK) return st;
   if (!nothing) {
     REQUIRE(((uint64_t)tokens / 64u + count) * hv < (1ull << 31), BQ_EINVAL, "%s: tokens=%u count=%u hv=%u too large",
@@ -675,9 +710,9 @@ int gated_delta_rule_chunked(const void *q_bf16, const void *k_bf16, const void 
       const void *p;
       uint64_t n;
       const char *what;
-    } other[8] = {{q_bf16, tokens ? heads_span(tokens, hk, dk, q_token, q_head) : 0, "q"},
-                  {k_bf16, tokens ? heads_span(tokens, hk, dk, k_token, k_head) : 0, "k"},
-                  {v_bf16, tokens ? heads_span(tokens, hv, dv, v_token, v_head) : 0, "v"},
+    } other[8] = {{q_bf16, heads_span(tokens, hk, dk, a.q_token, a.q_head), "q"},
+                  {k_bf16, heads_span(tokens, hk, dk, a.k_token, a.k_head), "k"},
+                  {v_bf16, heads_span(tokens, hv, dv, a.v_token, a.v_head), "v"},
                   {g, 4ull * tokens * hv, "g"},
                   {beta, 4ull * tokens * hv, "beta"},
                   {out_bf16, bf16_bytes((uint64_t)tokens * hv, dv), "the output"},

@@ -56,6 +56,12 @@ __device__ __forceinline__ uint32_t triangle_fragment(uint32_t w, uint32_t ks) {
 // below tokens / 64 + count.
 __device__ __forceinline__ uint32_t first_place(uint32_t begin, uint32_t seq) { return begin / kChunk + seq; }
 
+// Row r of 16 of the state's tile T, among its dk: a wave's result rows are
+// then the rows of a matrix operand of 32 in their natural order.
+__device__ __forceinline__ uint32_t state_row(uint32_t tile, uint32_t r) {
+  return 32u * (tile >> 1) + (r >> 2) * 8u + (tile & 1u) * 4u + (r & 3u);
+}
+
 // x = sum of N bf16 parts, for two values side by side (each part one packed register).
 template <int N>
 __device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[N]) {
@@ -222,7 +228,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
                    ((uint64_t)place * a.hk + khead) * key_bytes(kDk) + w * (kTiles * 2 * kFragment) + lane * 16u;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      const uint32_t row = kTiles == 2 ? 32u * w + (lr >> 2) * 8u + t * 4u + (lr & 3u) : 16u * w + lr;
+      const uint32_t row = state_row(w * kTiles + t, lr);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         uint32_t x[8];
@@ -331,239 +337,388 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
 
 // ---- second launch: the state along the chunks ------------------------------------
 
-// What a wave w needs of a chunk.  The state's rows are split over the waves
-// (rows 32w.. for dk 128, 16w.. for 64): each multiplies its rows by the
-// chunk's keys and queries, and the four partial sums meet in LDS.
-template <int kTiles>
-struct Operands {
-  uint4 k[4], q[4];          // 64 tokens x the wave's rows (for one tile 8 bytes of each)
-  uint4 t[2][3], inner[2][2];  // rows 16w.. of T and of the q.k triangle
-  uint4 kt[kTiles][2];       // the wave's rows x 64 tokens
-  float4 f[4];               // factors of tokens 16w + 4 (lane / 16) + i
-  float decay;
-  uint32_t v[4];
+// Eight waves.  The first four carry the state: wave w keeps rows of it
+// (32 for dk 128, 16 for 64) in registers, multiplies them by the chunk's keys,
+// the four partial sums meet in LDS, and tokens 16w.. of R and U are its own
+// from there on.  The other four make the output of tokens 16w.. from the
+// state's parts and U, which they find in LDS, beside that chain.  The operands
+// of the next chunk are loaded into the registers of this one's as soon as
+// those have been used: the loads are spread over the step and have most of
+// its time to arrive.
+//
+// What bounds it is the chain itself: three exchanges through LDS per chunk,
+// and on one wave per SIMD an instruction at most every four cycles.
+constexpr int kScanThreads = 512;
+
+// What both kinds of waves know of their work.
+struct ScanPlace {
+  DeltaSeq sq;
+  uint32_t head, khead, col, place0, chunks, last;  // last: tokens of the last chunk
+  bool col_in;
 };
 
+// Loads of 16 (or 8) bytes from a uniform base and a lane's 32-bit offset.
+__device__ __forceinline__ uint4 load16(const uint8_t *base, uint32_t off) {
+  const Bf16x8 x = *reinterpret_cast<const Bf16x8 *>(base + off);
+  return make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+}
+__device__ __forceinline__ uint4 fragment(const uint8_t *base, uint32_t off) {
+  return *reinterpret_cast<const uint4 *>(base + off);
+}
+
+// N bf16 (8 or 4) of a row of q or k from value d0 on, zeros past dk; off in bytes.
+template <int N, bool kWhole>
+__device__ __forceinline__ uint4 load_row(const uint8_t *base, uint32_t off, uint32_t d0, uint32_t dk) {
+  if constexpr (!kWhole) {
+    uint32_t x[8];
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i)
+      x[i] = i < (uint32_t)N && d0 + i < dk ? *reinterpret_cast<const uint16_t *>(base + off + 2u * i) : 0u;
+    return make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
+  } else if constexpr (N == 8) {
+    return load16(base, off);
+  } else {
+    const Bf16x4 x = *reinterpret_cast<const Bf16x4 *>(base + off);
+    return make_uint4(x.w[0], x.w[1], 0u, 0u);
+  }
+}
+
+template <int kTiles>
+struct ScanLds {
+  float4 part[16][64];          // partial K S0: [token tile * 4 + wave][lane]
+  uint8_t r[3][2][1024];        // R, decayed U and U as operands: [part][32 tokens][lane]
+  uint8_t decayed[3][2][1024];
+  uint8_t u[2][2][1024];
+  uint8_t s[2][2 * kTiles][1024];  // the state's two leading parts: [part][32 rows][lane]
+};
+
+__device__ __forceinline__ v8bf as_bf(uint4 x) { return __builtin_bit_cast(v8bf, x); }
+
 template <int kTiles, bool kWhole>
-__global__ __launch_bounds__(kThreads) void delta_scan_kernel(const DeltaArgs a) {
+__device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace &pl, ScanLds<kTiles> &lds, uint32_t w,
+                                            uint32_t lane) {
   constexpr int kDk = 64 * kTiles;
-  constexpr int kRows = 16 * kTiles;  // rows of the state per wave
-  // partial sums [token tile][wave][lane], R and U as operands [part][32 tokens][lane]
-  __shared__ __attribute__((aligned(16))) float4 part_k[16][64], part_q[16][64];
-  __shared__ __attribute__((aligned(16))) uint8_t lds_r[3][2][1024], lds_u[2][2][1024], lds_s[3][2][1024];
-
-  const uint32_t tid = threadIdx.x, lane = tid & 63u, lr = lane & 15u, lq = lane >> 4;
-  const uint32_t w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // Workgroups go round the eight XCDs: the column blocks of a head all to one,
-  // so that its L2 serves the chunk's operands to all of them.
-  const uint32_t blocks = (a.dv + 15u) / 16u;
-  const uint32_t j = blockIdx.x >> 3, pair = (j / blocks) * 8u + (blockIdx.x & 7u);
-  if (pair >= a.count * a.hv) return;
-  const uint32_t seq = pair / a.hv, head = pair - seq * a.hv, khead = head / (a.hv / a.hk);
-  const uint32_t col = (j % blocks) * 16u + lr;
-  const bool col_in = col < a.dv;
-  const DeltaSeq sq = delta_sequence(a, seq);
-  if (sq.begin >= sq.end && !sq.fresh) return;  // nothing changes
-
-  // row of result register i of tile t, among the state's dk
-  auto state_row = [&](int t, int i) -> uint32_t {
-    return kTiles == 2 ? 32u * w + lq * 8u + t * 4u + i : 16u * w + lq * 4u + i;
-  };
-  float *state = a.state + ((uint64_t)max(sq.slot, 0) * a.hv + head) * a.dk * a.dv + col;
+  const uint32_t lr = lane & 15u, lq = lane >> 4;
+  const v4f zero = {0, 0, 0, 0};
+  float *state = a.state + ((uint64_t)max(pl.sq.slot, 0) * a.hv + pl.head) * a.dk * a.dv + pl.col;
   v4f s[kTiles];
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t r = state_row(t, i);
-      s[t][i] = sq.slot >= 0 && !sq.fresh && col_in && r < a.dk ? state[(uint64_t)r * a.dv] : 0.0f;
-    }
-
-  const uint32_t place0 = first_place(sq.begin, seq);
-  const uint32_t chunks = (sq.end - sq.begin + kChunk - 1u) / kChunk;
-  const uint8_t *key_base = a.workspace + (uint64_t)(a.tokens / kChunk + a.count) * a.hv * kHeadBytes;
-
-  // Rows past the chunk's end read its last token: their factors are zero.
-  auto load = [&](uint32_t c, Operands<kTiles> &o) {
-    const uint32_t t0 = sq.begin + c * kChunk, n = min(sq.end - t0, (uint32_t)kChunk);
-    const uint8_t *mine = a.workspace + ((uint64_t)(place0 + c) * a.hv + head) * kHeadBytes;
-    const uint8_t *kt = key_base + ((uint64_t)(place0 + c) * a.hk + khead) * key_bytes(kDk) + w * (kTiles * 2 * kFragment);
-    const uint32_t dk0 = kRows * w + lq * (kTiles * 4);
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const uint64_t t = t0 + min(16u * m + lr, n - 1u);
-      const uint16_t *kp = a.k + t * a.k_token + (uint64_t)khead * a.k_head + dk0;
-      const uint16_t *qp = a.q + t * a.q_token + (uint64_t)khead * a.q_head + dk0;
-      if constexpr (!kWhole) {
-        uint32_t x[8], y[8];
-#pragma unroll
-        for (uint32_t i = 0; i < 8; ++i) {
-          const bool in = i < kTiles * 4u && dk0 + i < a.dk;
-          x[i] = in ? kp[i] : 0u;
-          y[i] = in ? qp[i] : 0u;
-        }
-        o.k[m] = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
-        o.q[m] = make_uint4(y[0] | y[1] << 16, y[2] | y[3] << 16, y[4] | y[5] << 16, y[6] | y[7] << 16);
-      } else if constexpr (kTiles == 2) {
-        const Bf16x8 x = *reinterpret_cast<const Bf16x8 *>(kp), y = *reinterpret_cast<const Bf16x8 *>(qp);
-        o.k[m] = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
-        o.q[m] = make_uint4(y.w[0], y.w[1], y.w[2], y.w[3]);
-      } else {
-        const Bf16x4 x = *reinterpret_cast<const Bf16x4 *>(kp), y = *reinterpret_cast<const Bf16x4 *>(qp);
-        o.k[m] = make_uint4(x.w[0], x.w[1], 0u, 0u);
-        o.q[m] = make_uint4(y.w[0], y.w[1], 0u, 0u);
-      }
-    }
-#pragma unroll
-    for (uint32_t ks = 0; ks < 2; ++ks) {
-      const uint32_t f = triangle_fragment(w, ks);  // the upper waves' second half is not used
-#pragma unroll
-      for (int i = 0; i < 3; ++i) o.t[ks][i] = *reinterpret_cast<const uint4 *>(mine + (f * 3 + i) * kFragment + lane * 16u);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        o.inner[ks][i] = *reinterpret_cast<const uint4 *>(mine + kTBytes + (f * 2 + i) * kFragment + lane * 16u);
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) o.kt[t][ks] = *reinterpret_cast<const uint4 *>(kt + (t * 2 + ks) * kFragment + lane * 16u);
-    }
-    const float4 *factors = reinterpret_cast<const float4 *>(mine + kTBytes + kInnerBytes);
+  for (uint32_t t = 0; t < kTiles; ++t)
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i) {
-      const uint32_t r = 16u * w + lq * 4u + i;
-      o.f[i] = factors[r];
-      o.v[i] = a.v[(uint64_t)(t0 + min(r, n - 1u)) * a.v_token + (uint64_t)head * a.v_head + min(col, a.dv - 1u)];
+      const uint32_t r = state_row(w * kTiles + t, lq * 4u + i);
+      s[t][i] = pl.sq.slot >= 0 && !pl.sq.fresh && pl.col_in && r < a.dk ? state[(uint64_t)r * a.dv] : 0.0f;
     }
-    o.decay = *reinterpret_cast<const float *>(factors + kChunk);
+
+  // bases of the next chunk to load, and this lane's offsets in bytes
+  const uint8_t *mine = a.workspace + ((uint64_t)pl.place0 * a.hv + pl.head) * kHeadBytes;
+  const uint8_t *kt = a.workspace + (uint64_t)(a.tokens / kChunk + a.count) * a.hv * kHeadBytes +
+                      ((uint64_t)pl.place0 * a.hk + pl.khead) * key_bytes(kDk) + w * (kTiles * 2 * kFragment);
+  const uint8_t *keys = reinterpret_cast<const uint8_t *>(a.k + (uint64_t)pl.khead * a.k_head + (uint64_t)pl.sq.begin * a.k_token);
+  const uint8_t *vals = reinterpret_cast<const uint8_t *>(a.v + (uint64_t)pl.head * a.v_head + (uint64_t)pl.sq.begin * a.v_token);
+  const uint32_t dk0 = state_row(w * kTiles, lq * 4u), lane16 = lane * 16u;
+  const uint32_t t_off[2] = {triangle_fragment(w, 0) * 3u * kFragment + lane16, triangle_fragment(w, 1) * 3u * kFragment + lane16};
+  const uint32_t f_off = kTBytes + kInnerBytes + (16u * w + lq * 4u) * 16u;
+  uint32_t k_off[4], v_off[4];
+  // rows past the sequence's end read its last token: their factors are zero
+  auto token_offsets = [&](uint32_t n) {
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+      k_off[i] = 2u * (min(16u * i + lr, n - 1u) * a.k_token + dk0);
+      v_off[i] = 2u * (min(16u * w + lq * 4u + i, n - 1u) * a.v_token + min(pl.col, a.dv - 1u));
+    }
+  };
+
+  uint4 op_k[4], op_t[2][3], op_kt[kTiles][2];
+  float4 factor[4];
+  uint16_t val[4];
+  float decay;
+  auto load_keys = [&]() {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) op_k[m] = load_row<4 * kTiles, kWhole>(keys, k_off[m], dk0, a.dk);
+  };
+  auto load_values = [&]() {
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+      factor[i] = *reinterpret_cast<const float4 *>(mine + (f_off + i * 16u));
+      val[i] = *reinterpret_cast<const uint16_t *>(vals + v_off[i]);
+    }
+    decay = *reinterpret_cast<const float *>(mine + kTBytes + kInnerBytes + kChunk * 16);
+  };
+  // (waves 0 and 1 have no second half of T: they read the first again and do not use it)
+  auto load_inverse = [&]() {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (uint32_t i = 0; i < 3; ++i) op_t[ks][i] = fragment(mine, t_off[ks] + i * kFragment);
+  };
+  auto load_transposed = [&]() {
+#pragma unroll
+    for (uint32_t t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (uint32_t ks = 0; ks < 2; ++ks) op_kt[t][ks] = fragment(kt, (t * 2u + ks) * kFragment + lane16);
   };
 
   // place of this lane's four rows in an operand of 64 tokens
   const uint32_t put = (w >> 1) * 1024u + ((w & 1u) * 2u + (lq >> 1)) * 256u + lr * 16u + (lq & 1u) * 8u;
-  auto bf = [](uint4 x) { return __builtin_bit_cast(v8bf, x); };
-
-  auto step = [&](uint32_t c, const Operands<kTiles> &o) {
-    // K S0 and Q S0 over the wave's rows of the state
+  token_offsets(pl.chunks == 1u ? pl.last : (uint32_t)kChunk);
+  load_keys();
+  load_values();
+  load_inverse();
+  load_transposed();
+  for (uint32_t c = 0; c < pl.chunks; ++c) {
+    // past the end the last chunk is loaded again
+    if (c + 1u < pl.chunks) {
+      mine += (uint64_t)a.hv * kHeadBytes;
+      kt += (uint64_t)a.hk * key_bytes(kDk);
+      keys += (uint64_t)kChunk * 2u * a.k_token;
+      vals += (uint64_t)kChunk * 2u * a.v_token;
+      if (c + 2u == pl.chunks) token_offsets(pl.last);
+    }
+    // K S0 over the wave's rows of the state
     uint32_t sp[kTiles][2][3];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
       split2<3>(s[t][0], s[t][1], sp[t][0]);
       split2<3>(s[t][2], s[t][3], sp[t][1]);
     }
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      v4f x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+    v4f x[4];
+    if constexpr (kTiles == 2) {
 #pragma unroll
       for (int i = 2; i >= 0; --i) {
-        if constexpr (kTiles == 2) {
-          const v8bf b = bf(make_uint4(sp[0][0][i], sp[0][1][i], sp[1][0][i], sp[1][1][i]));
-          x = mfma32(bf(o.k[m]), b, x);
-          if (i < 2) y = mfma32(bf(o.q[m]), b, y);
-        } else {
-          const v4s b = __builtin_bit_cast(v4s, make_uint2(sp[0][0][i], sp[0][1][i]));
-          x = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(v4s, make_uint2(o.k[m].x, o.k[m].y)), b, x, 0, 0, 0);
-          if (i < 2)
-            y = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(v4s, make_uint2(o.q[m].x, o.q[m].y)), b, y, 0, 0, 0);
-        }
+        const uint4 b = make_uint4(sp[0][0][i], sp[0][1][i], sp[1][0][i], sp[1][1][i]);
+        if (i < 2) *reinterpret_cast<uint4 *>(&lds.s[i][w][lane16]) = b;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) x[m] = mfma32(as_bf(op_k[m]), as_bf(b), i == 2 ? zero : x[m]);
       }
-      part_k[m * 4 + w][lane] = make_float4(x[0], x[1], x[2], x[3]);
-      part_q[m * 4 + w][lane] = make_float4(y[0], y[1], y[2], y[3]);
+    } else {
+      // 16 rows: two parts of the state side by side make an operand of 32
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<uint2 *>(&lds.s[i][w >> 1][lane16 + (w & 1u) * 8u]) = make_uint2(sp[0][0][i], sp[0][1][i]);
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        x[m] = mfma32(as_bf(op_k[m]), as_bf(make_uint4(sp[0][0][2], sp[0][1][2], 0u, 0u)), zero);
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        x[m] = mfma32(as_bf(make_uint4(op_k[m].x, op_k[m].y, op_k[m].x, op_k[m].y)),
+                      as_bf(make_uint4(sp[0][0][1], sp[0][1][1], sp[0][0][0], sp[0][1][0])), x[m]);
     }
+    __builtin_amdgcn_sched_barrier(0);
+    load_keys();
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) *reinterpret_cast<v4f *>(&lds.part[m * 4 + w][lane]) = x[m];
     __syncthreads();
     // R for tokens 16w..
-    float r[4], qs[4];
-    {
-      float4 x = part_k[w * 4][lane], y = part_q[w * 4][lane];
+    v4f p[4], r;
 #pragma unroll
-      for (int p = 1; p < 4; ++p) {
-        const float4 u = part_k[w * 4 + p][lane], v = part_q[w * 4 + p][lane];
-        x.x += u.x; x.y += u.y; x.z += u.z; x.w += u.w;
-        y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
-      }
-      const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        r[i] = o.f[i].x * bf16_to_f32(o.v[i]) - o.f[i].y * xs[i];
-        qs[i] = o.f[i].z * ys[i];
-      }
-    }
+    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const v4f *>(&lds.part[w * 4 + i][lane]);
+    p[0] = (p[0] + p[1]) + (p[2] + p[3]);
     uint32_t lo[3], hi[3];
+    float own[4];  // e^(G_L - G) rk, for the update
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r[i] = factor[i].x * bf16_to_f32(val[i]) - factor[i].y * p[0][i];
+      own[i] = factor[i].w;
+    }
     split2<3>(r[0], r[1], lo);
     split2<3>(r[2], r[3], hi);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2 *>(&lds_r[i][0][0] + put) = make_uint2(lo[i], hi[i]);
+    for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2 *>(&lds.r[i][0][0] + put) = make_uint2(lo[i], hi[i]);
+    const float keep = decay;
+    __builtin_amdgcn_sched_barrier(0);
+    load_values();
     __syncthreads();
     // U = T R for tokens 16w..; columns past 16w + 15 of T are zero
-    v4f u = {0, 0, 0, 0};
+    v8bf rb[3][2];
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      if (ks == 1 && w < 2u) continue;
-      v8bf b[3];
+    for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-      for (int i = 0; i < 3; ++i) b[i] = *reinterpret_cast<const v8bf *>(&lds_r[i][ks][lane * 16u]);
-      u = mfma32(bf(o.t[ks][2]), b[0], u);
-      u = mfma32(bf(o.t[ks][1]), b[1], u);
-      u = mfma32(bf(o.t[ks][0]), b[2], u);
-      u = mfma32(bf(o.t[ks][1]), b[0], u);
-      u = mfma32(bf(o.t[ks][0]), b[1], u);
-      u = mfma32(bf(o.t[ks][0]), b[0], u);
+      for (int i = 0; i < 3; ++i) rb[i][ks] = *reinterpret_cast<const v8bf *>(&lds.r[i][ks][lane16]);
+    v4f u = mfma32(as_bf(op_t[0][2]), rb[0][0], zero), u1 = mfma32(as_bf(op_t[0][1]), rb[0][0], zero);
+    if (w < 2u) {
+      u = mfma32(as_bf(op_t[0][1]), rb[1][0], u);
+      u1 = mfma32(as_bf(op_t[0][0]), rb[1][0], u1);
+      u = mfma32(as_bf(op_t[0][0]), rb[2][0], u);
+      u1 = mfma32(as_bf(op_t[0][0]), rb[0][0], u1);
+      u += u1;
+    } else {
+      v4f u2 = mfma32(as_bf(op_t[1][2]), rb[0][1], zero), u3 = mfma32(as_bf(op_t[1][1]), rb[0][1], zero);
+      u = mfma32(as_bf(op_t[0][1]), rb[1][0], u);
+      u1 = mfma32(as_bf(op_t[0][0]), rb[1][0], u1);
+      u2 = mfma32(as_bf(op_t[1][1]), rb[1][1], u2);
+      u3 = mfma32(as_bf(op_t[1][0]), rb[1][1], u3);
+      u = mfma32(as_bf(op_t[0][0]), rb[2][0], u);
+      u1 = mfma32(as_bf(op_t[0][0]), rb[0][0], u1);
+      u2 = mfma32(as_bf(op_t[1][0]), rb[2][1], u2);
+      u3 = mfma32(as_bf(op_t[1][0]), rb[0][1], u3);
+      u = (u + u2) + (u1 + u3);
     }
-    split2<3>(u[0] * o.f[0].w, u[1] * o.f[1].w, lo);
-    split2<3>(u[2] * o.f[2].w, u[3] * o.f[3].w, hi);
+    split2<3>(u[0] * own[0], u[1] * own[1], lo);
+    split2<3>(u[2] * own[2], u[3] * own[3], hi);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2 *>(&lds_s[i][0][0] + put) = make_uint2(lo[i], hi[i]);
+    for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2 *>(&lds.decayed[i][0][0] + put) = make_uint2(lo[i], hi[i]);
     uint32_t ulo[2], uhi[2];
     split2<2>(u[0], u[1], ulo);
     split2<2>(u[2], u[3], uhi);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) *reinterpret_cast<uint2 *>(&lds_u[i][0][0] + put) = make_uint2(ulo[i], uhi[i]);
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<uint2 *>(&lds.u[i][0][0] + put) = make_uint2(ulo[i], uhi[i]);
+    __builtin_amdgcn_sched_barrier(0);
+    load_inverse();
     __syncthreads();
     // the state
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) s[t] *= o.decay;
+    v8bf sb[3][2];
 #pragma unroll
     for (int i = 2; i >= 0; --i)
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const v8bf b = *reinterpret_cast<const v8bf *>(&lds_s[i][ks][lane * 16u]);
+      for (int ks = 0; ks < 2; ++ks) sb[i][ks] = *reinterpret_cast<const v8bf *>(&lds.decayed[i][ks][lane16]);
+    v4f s1[kTiles];
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) s[t] = mfma32(bf(o.kt[t][ks]), b, s[t]);
+    for (int t = 0; t < kTiles; ++t) s[t] *= keep;
+#pragma unroll
+    for (int i = 2; i >= 0; --i)
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        s1[t] = mfma32(as_bf(op_kt[t][0]), sb[i][0], i == 2 ? zero : s1[t]);
+        s[t] = mfma32(as_bf(op_kt[t][1]), sb[i][1], s[t]);
       }
-    // the output of tokens 16w..
-    v4f y = {qs[0], qs[1], qs[2], qs[3]};
+    __builtin_amdgcn_sched_barrier(0);
+    load_transposed();
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      if (ks == 1 && w < 2u) continue;
-      const v8bf b0 = *reinterpret_cast<const v8bf *>(&lds_u[0][ks][lane * 16u]);
-      const v8bf b1 = *reinterpret_cast<const v8bf *>(&lds_u[1][ks][lane * 16u]);
-      y = mfma32(bf(o.inner[ks][1]), b0, y);
-      y = mfma32(bf(o.inner[ks][0]), b1, y);
-      y = mfma32(bf(o.inner[ks][0]), b0, y);
-    }
-    const uint32_t t0 = sq.begin + c * kChunk, n = min(sq.end - t0, (uint32_t)kChunk);
-    uint16_t *out = a.out + ((uint64_t)(t0 + 16u * w + lq * 4u) * a.hv + head) * a.dv + col;
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i)
-      if (col_in && 16u * w + lq * 4u + i < n) out[(uint64_t)i * a.hv * a.dv] = (uint16_t)f32_to_bf16_rne(y[i]);
-  };
-
-  // The next chunk's operands are on their way while one is computed.
-  Operands<kTiles> even, odd;
-  if (chunks > 0) load(0, even);
-  for (uint32_t c = 0; c < chunks; c += 2) {
-    if (c + 1 < chunks) load(c + 1, odd);
-    step(c, even);
-    if (c + 1 < chunks) {
-      if (c + 2 < chunks) load(c + 2, even);
-      step(c + 1, odd);
-    }
+    for (int t = 0; t < kTiles; ++t) s[t] += s1[t];
   }
 
-  if (sq.slot < 0 || !col_in) return;
+  if (pl.sq.slot < 0 || !pl.col_in) return;
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t)
+  for (uint32_t t = 0; t < kTiles; ++t)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t r = state_row(t, i);
+    for (uint32_t i = 0; i < 4; ++i) {
+      const uint32_t r = state_row(w * kTiles + t, lq * 4u + i);
       if (r < a.dk) state[(uint64_t)r * a.dv] = s[t][i];
     }
+}
+
+template <int kTiles, bool kWhole>
+__device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace &pl, const ScanLds<kTiles> &lds,
+                                            uint32_t w, uint32_t lane) {
+  constexpr int kSteps = 2 * kTiles;  // dk in 32s
+  const uint32_t lr = lane & 15u, lq = lane >> 4, lane16 = lane * 16u;
+  const v4f zero = {0, 0, 0, 0};
+  const uint8_t *mine = a.workspace + ((uint64_t)pl.place0 * a.hv + pl.head) * kHeadBytes;
+  const uint8_t *queries = reinterpret_cast<const uint8_t *>(a.q + (uint64_t)pl.khead * a.q_head + (uint64_t)pl.sq.begin * a.q_token);
+  uint8_t *out = reinterpret_cast<uint8_t *>(a.out + ((uint64_t)pl.sq.begin * a.hv + pl.head) * a.dv);
+  const uint32_t in_off[2] = {kTBytes + triangle_fragment(w, 0) * 2u * kFragment + lane16,
+                              kTBytes + triangle_fragment(w, 1) * 2u * kFragment + lane16};
+  const uint32_t f_off = kTBytes + kInnerBytes + (16u * w + lq * 4u) * 16u + 8u;
+  uint32_t q_off, out_off[4];
+#pragma unroll
+  for (uint32_t i = 0; i < 4; ++i) out_off[i] = 2u * ((16u * w + lq * 4u + i) * a.hv * a.dv + pl.col);
+  auto token_offsets = [&](uint32_t n) { q_off = 2u * (min(16u * w + lr, n - 1u) * a.q_token + lq * 8u); };
+
+  uint4 op_q[kSteps], op_in[2][2];
+  float factor[4];
+  auto load_queries = [&]() {
+#pragma unroll
+    for (uint32_t k = 0; k < kSteps; ++k) op_q[k] = load_row<8, kWhole>(queries, q_off + 64u * k, 32u * k + lq * 8u, a.dk);
+  };
+  auto load_inner = [&]() {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (uint32_t i = 0; i < 2; ++i) op_in[ks][i] = fragment(mine, in_off[ks] + i * kFragment);
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) factor[i] = *reinterpret_cast<const float *>(mine + (f_off + i * 16u));
+  };
+  token_offsets(pl.chunks == 1u ? pl.last : (uint32_t)kChunk);
+  load_queries();
+  load_inner();
+  for (uint32_t c = 0; c < pl.chunks; ++c) {
+    if (c + 1u < pl.chunks) {
+      mine += (uint64_t)a.hv * kHeadBytes;
+      queries += (uint64_t)kChunk * 2u * a.q_token;
+      if (c + 2u == pl.chunks) token_offsets(pl.last);
+    }
+    __syncthreads();
+    // Q S0 for tokens 16w..
+    v8bf sb[2][kSteps];
+#pragma unroll
+    for (int i = 1; i >= 0; --i)
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) sb[i][k] = *reinterpret_cast<const v8bf *>(&lds.s[i][k][lane16]);
+    v4f o = zero, o1 = zero;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      o = mfma32(as_bf(op_q[k]), sb[1][k], o);
+      o1 = mfma32(as_bf(op_q[k]), sb[0][k], o1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    load_queries();
+    __syncthreads();
+    o += o1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] *= factor[i];
+    __syncthreads();
+    // and the chunk's own part; columns past 16w + 15 of the triangle are zero
+    v8bf ub[2][2];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) ub[i][ks] = *reinterpret_cast<const v8bf *>(&lds.u[i][ks][lane16]);
+    o1 = mfma32(as_bf(op_in[0][0]), ub[1][0], zero);
+    o = mfma32(as_bf(op_in[0][1]), ub[0][0], o);
+    if (w >= 2u) {
+      o1 = mfma32(as_bf(op_in[1][1]), ub[0][1], o1);
+      o = mfma32(as_bf(op_in[1][0]), ub[1][1], o);
+      o1 = mfma32(as_bf(op_in[1][0]), ub[0][1], o1);
+    }
+    o = mfma32(as_bf(op_in[0][0]), ub[0][0], o);
+    __builtin_amdgcn_sched_barrier(0);
+    load_inner();
+    o += o1;
+    uint32_t lo[1], hi[1];
+    split2<1>(o[0], o[1], lo);
+    split2<1>(o[2], o[3], hi);
+    const uint32_t n = c + 1u == pl.chunks ? pl.last : (uint32_t)kChunk, row = 16u * w + lq * 4u;
+    if (pl.col_in && row < n) *reinterpret_cast<uint16_t *>(out + out_off[0]) = (uint16_t)lo[0];
+    if (pl.col_in && row + 1u < n) *reinterpret_cast<uint16_t *>(out + out_off[1]) = (uint16_t)(lo[0] >> 16);
+    if (pl.col_in && row + 2u < n) *reinterpret_cast<uint16_t *>(out + out_off[2]) = (uint16_t)hi[0];
+    if (pl.col_in && row + 3u < n) *reinterpret_cast<uint16_t *>(out + out_off[3]) = (uint16_t)(hi[0] >> 16);
+    out += (uint64_t)kChunk * 2u * a.hv * a.dv;
+  }
+}
+
+template <int kTiles, bool kWhole>
+__global__ __launch_bounds__(kScanThreads) void delta_scan_kernel(const DeltaArgs a) {
+  __shared__ __attribute__((aligned(16))) ScanLds<kTiles> lds;
+  const uint32_t lane = threadIdx.x & 63u, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // Workgroups go round the eight XCDs: the column blocks of a head all to one,
+  // so that its L2 serves the chunk's operands to all of them.
+  const uint32_t blocks = (a.dv + 15u) / 16u;
+  const uint32_t j = blockIdx.x >> 3, pair = (j / blocks) * 8u + (blockIdx.x & 7u);
+  if (pair >= a.count * a.hv) return;
+  const uint32_t seq = pair / a.hv;
+  ScanPlace pl;
+  pl.sq = delta_sequence(a, seq);
+  pl.head = pair - seq * a.hv;
+  pl.khead = pl.head / (a.hv / a.hk);
+  pl.col = (j % blocks) * 16u + (lane & 15u);
+  pl.col_in = pl.col < a.dv;
+  pl.place0 = first_place(pl.sq.begin, seq);
+  const uint32_t tokens = pl.sq.end - pl.sq.begin;
+  if (tokens == 0u) {  // an empty sequence keeps its state, or loses it
+    if (pl.sq.fresh && pl.sq.slot >= 0 && pl.col_in)
+      for (uint32_t r = threadIdx.x >> 4; r < a.dk; r += kScanThreads / 16)
+        a.state[(((uint64_t)pl.sq.slot * a.hv + pl.head) * a.dk + r) * a.dv + pl.col] = 0.0f;
+    return;
+  }
+  pl.chunks = (tokens + kChunk - 1u) / kChunk;
+  pl.last = tokens - (pl.chunks - 1u) * kChunk;
+  // both take part in every barrier: three per chunk
+  if (w < 4u)
+    carry_state<kTiles, kWhole>(a, pl, lds, w, lane);
+  else
+    make_output<kTiles, kWhole>(a, pl, lds, w - 4u, lane);
 }
 
 template <int kTiles>
@@ -577,9 +732,9 @@ hipError_t launch_chunked(const DeltaArgs &a, hipStream_t s) {
   const uint64_t pairs = ((uint64_t)a.count * a.hv + 7u) / 8u * 8u;
   const dim3 grid((uint32_t)(pairs * ((a.dv + 15u) / 16u)));
   if (a.dk == 64u * kTiles)
-    hipLaunchKernelGGL((delta_scan_kernel<kTiles, true>), grid, dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((delta_scan_kernel<kTiles, true>), grid, dim3(kScanThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((delta_scan_kernel<kTiles, false>), grid, dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((delta_scan_kernel<kTiles, false>), grid, dim3(kScanThreads), 0, s, a);
   return hipGetLastError();
 }
 

@@ -338,7 +338,8 @@ int w8a8_gemm(const void *act_i8, const void *w_i8, const void *bias_bf16, void 
  * With l2norm != 0, q and k are divided by sqrt(|.|^2 + 1e-6) first.
  *
  * q, k: bf16, head i of token t starts at t * q_token + i * q_head (values), its
- * dk values are consecutive; v likewise with dv.  g, beta: binary32
+ * dk values are consecutive; v likewise with dv (token strides below
+ * 2^24, head strides below 2^31).  g, beta: binary32
  * [tokens][hv], g <= 0 (-infinity forgets everything).  out: bf16
  * [tokens][hv][dv].  state: binary32 [state_slots][hv][dk][dv], updated in place;
  * sequence i owns slot slots[i] (i itself where slots is NULL), no two
@@ -349,7 +350,7 @@ int w8a8_gemm(const void *act_i8, const void *w_i8, const void *bias_bf16, void 
  * of no sequence are left alone.  An empty sequence keeps its state (zeros where
  * it is fresh).
  *
- * 1 <= dk <= 128, dv >= 1, hk divides hv.  q, k, v, out 2-byte aligned, the
+ * 1 <= dk <= 128, dv >= 1, hk divides hv, hv * dv < 2^24.  q, k, v, out 2-byte aligned, the
  * binary32 and int32 arrays 4-byte.  out and state overlap nothing else.
  * tokens = 0 is allowed (the token arrays may be NULL), and count = 0 (nothing
  * is done).  Captured into a graph, a call reads starts, slots and fresh at
