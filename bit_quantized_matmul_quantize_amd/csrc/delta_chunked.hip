@@ -9,7 +9,7 @@
 //
 // Two launches.  The first takes every chunk of every value head at once and
 // leaves what does not depend on the state in the workspace: T, the decayed
-// q.k triangle, a few factors per token, and the keys transposed.  The second
+// q.k triangle and a few factors per token.  The second
 // walks each head's chunks in order, a workgroup for 16 columns of the state
 // (columns do not depend on each other).
 //
@@ -45,9 +45,9 @@ constexpr uint32_t kFragment = 1024;
 constexpr uint32_t kTriangle = 6;
 constexpr uint32_t kTBytes = kTriangle * 3 * kFragment;
 constexpr uint32_t kInnerBytes = kTriangle * 2 * kFragment;
-constexpr uint32_t kFactorBytes = kChunk * 16 + 256;  // (b, b e^G rk, scale e^G rq, e^(G_L - G) rk) per token, then e^G_L
+constexpr uint32_t kFactorRow = kChunk * 4;  // rows b, b e^G rk, e^(G_L - G) rk, scale e^G rq of 64 tokens, then e^G_L
+constexpr uint32_t kFactorBytes = 4 * kFactorRow + 256;
 constexpr uint32_t kHeadBytes = kTBytes + kInnerBytes + kFactorBytes;
-__host__ __device__ constexpr uint32_t key_bytes(int kd) { return kd * kChunk * 2; }  // the keys transposed
 
 __device__ __forceinline__ uint32_t triangle_fragment(uint32_t w, uint32_t ks) { return w < 2u ? w : 2u * w - 2u + ks; }
 
@@ -127,7 +127,7 @@ __device__ __forceinline__ void put_triangle(const float *m, uint8_t *out, uint3
     *reinterpret_cast<uint4 *>(p + i * kFragment) = make_uint4(parts[0][i], parts[1][i], parts[2][i], parts[3][i]);
 }
 
-// One workgroup for a chunk and value head; the first value head of a key head also transposes the keys.
+// One workgroup for a chunk and value head.
 template <int kDk>
 __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a) {
   constexpr int kRow = kDk + 8;  // bf16 per staged row
@@ -221,24 +221,6 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
       norm_q[r] = (a.l2norm ? 1.0f / sqrtf(sq2 + kNormEps) : 1.0f) * a.scale;
     }
   }
-  // the keys transposed: rows are dk as the state's lie in the second launch, columns tokens
-  if (head == khead * ratio) {
-    constexpr int kTiles = kDk / 64;
-    uint8_t *out = a.workspace + (uint64_t)(a.tokens / kChunk + a.count) * a.hv * kHeadBytes +
-                   ((uint64_t)place * a.hk + khead) * key_bytes(kDk) + w * (kTiles * 2 * kFragment) + lane * 16u;
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      const uint32_t row = state_row(w * kTiles + t, lr);
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        uint32_t x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = keys[(32 * ks + lq * 8 + j) * kRow + row];
-        *reinterpret_cast<uint4 *>(out + (t * 2 + ks) * kFragment) =
-            make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
-      }
-    }
-  }
   // k.k and q.k: rows 16w.. by the wave, the tiles of the lower triangle
   v4f kk[4], qk[4];
 #pragma unroll
@@ -261,13 +243,12 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
   if (w == 0) {
     const double g = sum_g[lane];
     const float e = expf((float)g);
-    float4 f;
-    f.x = betas[lane];
-    f.y = betas[lane] * e * norm_k[lane];
-    f.z = lane < n ? e * norm_q[lane] : 0.0f;
-    f.w = lane < n ? expf((float)(sum_g[kChunk - 1] - g)) * norm_k[lane] : 0.0f;
-    *reinterpret_cast<float4 *>(mine + kTBytes + kInnerBytes + lane * 16u) = f;
-    if (lane == kChunk - 1) *reinterpret_cast<float *>(mine + kTBytes + kInnerBytes + kChunk * 16) = e;
+    float *f = reinterpret_cast<float *>(mine + kTBytes + kInnerBytes) + lane;
+    f[0] = betas[lane];
+    f[kChunk] = betas[lane] * e * norm_k[lane];
+    f[2 * kChunk] = lane < n ? expf((float)(sum_g[kChunk - 1] - g)) * norm_k[lane] : 0.0f;
+    f[3 * kChunk] = lane < n ? e * norm_q[lane] : 0.0f;
+    if (lane == kChunk - 1) f[3 * kChunk + 1] = e;
   }
 #pragma unroll
   for (uint32_t j = 0; j < 4; ++j) {
@@ -383,12 +364,22 @@ __device__ __forceinline__ uint4 load_row(const uint8_t *base, uint32_t off, uin
   }
 }
 
+// bytes per token of a wave's rows of the keys; the pad spreads banks
+template <int kTiles>
+constexpr int kKeyRow = 32 * kTiles + 16;
+
 template <int kTiles>
 struct ScanLds {
   float4 part[16][64];          // partial K S0: [token tile * 4 + wave][lane]
   uint8_t r[3][2][1024];        // R, decayed U and U as operands: [part][32 tokens][lane]
   uint8_t decayed[3][2][1024];
   uint8_t u[2][2][1024];
+  struct __attribute__((aligned(16))) {
+    float value[kChunk][16];    // b v
+    float factor[3][kChunk];    // b e^G rk, e^(G_L - G) rk, scale e^G rq
+    float decay;                // e^G_L
+  } tokens[2];                  // of this chunk and of the next
+  uint8_t keys[4][kChunk][kKeyRow<kTiles>];
   uint8_t s[2][2 * kTiles][1024];  // the state's two leading parts: [part][32 rows][lane]
 };
 
@@ -397,7 +388,6 @@ __device__ __forceinline__ v8bf as_bf(uint4 x) { return __builtin_bit_cast(v8bf,
 template <int kTiles, bool kWhole>
 __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace &pl, ScanLds<kTiles> &lds, uint32_t w,
                                             uint32_t lane) {
-  constexpr int kDk = 64 * kTiles;
   const uint32_t lr = lane & 15u, lq = lane >> 4;
   const v4f zero = {0, 0, 0, 0};
   float *state = a.state + ((uint64_t)max(pl.sq.slot, 0) * a.hv + pl.head) * a.dk * a.dv + pl.col;
@@ -412,67 +402,51 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
 
   // bases of the next chunk to load, and this lane's offsets in bytes
   const uint8_t *mine = a.workspace + ((uint64_t)pl.place0 * a.hv + pl.head) * kHeadBytes;
-  const uint8_t *kt = a.workspace + (uint64_t)(a.tokens / kChunk + a.count) * a.hv * kHeadBytes +
-                      ((uint64_t)pl.place0 * a.hk + pl.khead) * key_bytes(kDk) + w * (kTiles * 2 * kFragment);
   const uint8_t *keys = reinterpret_cast<const uint8_t *>(a.k + (uint64_t)pl.khead * a.k_head + (uint64_t)pl.sq.begin * a.k_token);
-  const uint8_t *vals = reinterpret_cast<const uint8_t *>(a.v + (uint64_t)pl.head * a.v_head + (uint64_t)pl.sq.begin * a.v_token);
   const uint32_t dk0 = state_row(w * kTiles, lq * 4u), lane16 = lane * 16u;
   const uint32_t t_off[2] = {triangle_fragment(w, 0) * 3u * kFragment + lane16, triangle_fragment(w, 1) * 3u * kFragment + lane16};
-  const uint32_t f_off = kTBytes + kInnerBytes + (16u * w + lq * 4u) * 16u;
-  uint32_t k_off[4], v_off[4];
+  uint32_t k_off[4];
   // rows past the sequence's end read its last token: their factors are zero
   auto token_offsets = [&](uint32_t n) {
 #pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) {
-      k_off[i] = 2u * (min(16u * i + lr, n - 1u) * a.k_token + dk0);
-      v_off[i] = 2u * (min(16u * w + lq * 4u + i, n - 1u) * a.v_token + min(pl.col, a.dv - 1u));
-    }
+    for (uint32_t i = 0; i < 4; ++i) k_off[i] = 2u * (min(16u * i + lr, n - 1u) * a.k_token + dk0);
   };
 
-  uint4 op_k[4], op_t[2][3], op_kt[kTiles][2];
-  float4 factor[4];
-  uint16_t val[4];
-  float decay;
+  uint4 op_k[4], op_t[2][3];
   auto load_keys = [&]() {
 #pragma unroll
     for (int m = 0; m < 4; ++m) op_k[m] = load_row<4 * kTiles, kWhole>(keys, k_off[m], dk0, a.dk);
   };
-  auto load_values = [&]() {
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) {
-      factor[i] = *reinterpret_cast<const float4 *>(mine + (f_off + i * 16u));
-      val[i] = *reinterpret_cast<const uint16_t *>(vals + v_off[i]);
-    }
-    decay = *reinterpret_cast<const float *>(mine + kTBytes + kInnerBytes + kChunk * 16);
-  };
-  // (waves 0 and 1 have no second half of T: they read the first again and do not use it)
   auto load_inverse = [&]() {
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
+    for (uint32_t i = 0; i < 3; ++i) op_t[0][i] = fragment(mine, t_off[0] + i * kFragment);
+    if (w >= 2u) {
 #pragma unroll
-      for (uint32_t i = 0; i < 3; ++i) op_t[ks][i] = fragment(mine, t_off[ks] + i * kFragment);
-  };
-  auto load_transposed = [&]() {
-#pragma unroll
-    for (uint32_t t = 0; t < kTiles; ++t)
-#pragma unroll
-      for (uint32_t ks = 0; ks < 2; ++ks) op_kt[t][ks] = fragment(kt, (t * 2u + ks) * kFragment + lane16);
+      for (uint32_t i = 0; i < 3; ++i) op_t[1][i] = fragment(mine, t_off[1] + i * kFragment);
+    }
   };
 
   // place of this lane's four rows in an operand of 64 tokens
   const uint32_t put = (w >> 1) * 1024u + ((w & 1u) * 2u + (lq >> 1)) * 256u + lr * 16u + (lq & 1u) * 8u;
   token_offsets(pl.chunks == 1u ? pl.last : (uint32_t)kChunk);
   load_keys();
-  load_values();
   load_inverse();
-  load_transposed();
+  // The update takes the keys with dk as rows: they go through LDS, where each
+  // wave keeps its own rows of all tokens and reads them back transposed
+  // (a group of 16 lanes reads 4 tokens x 16 rows, and lane i gets row i's 4).
+  uint8_t *keys_put = &lds.keys[w][lr][0] + lq * (8u * kTiles);
+  const uint8_t *keys_get = &lds.keys[w][lq * 8u + (lr >> 2)][0] + (lr & 3u) * (8u * kTiles);
+  auto transposed = [&](int t, int ks) -> v8bf {
+    const uint8_t *from = keys_get + 32 * ks * kKeyRow<kTiles> + t * 8;
+    const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)from);
+    const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)(from + 4 * kKeyRow<kTiles>));
+    return __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
   for (uint32_t c = 0; c < pl.chunks; ++c) {
     // past the end the last chunk is loaded again
     if (c + 1u < pl.chunks) {
       mine += (uint64_t)a.hv * kHeadBytes;
-      kt += (uint64_t)a.hk * key_bytes(kDk);
       keys += (uint64_t)kChunk * 2u * a.k_token;
-      vals += (uint64_t)kChunk * 2u * a.v_token;
       if (c + 2u == pl.chunks) token_offsets(pl.last);
     }
     // K S0 over the wave's rows of the state
@@ -504,31 +478,36 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
         x[m] = mfma32(as_bf(make_uint4(op_k[m].x, op_k[m].y, op_k[m].x, op_k[m].y)),
                       as_bf(make_uint4(sp[0][0][1], sp[0][1][1], sp[0][0][0], sp[0][1][0])), x[m]);
     }
-    __builtin_amdgcn_sched_barrier(0);
-    load_keys();
-    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      if constexpr (kTiles == 2)
+        *reinterpret_cast<uint4 *>(keys_put + 16 * m * kKeyRow<kTiles>) = op_k[m];
+      else
+        *reinterpret_cast<uint2 *>(keys_put + 16 * m * kKeyRow<kTiles>) = make_uint2(op_k[m].x, op_k[m].y);
+    }
 #pragma unroll
     for (int m = 0; m < 4; ++m) *reinterpret_cast<v4f *>(&lds.part[m * 4 + w][lane]) = x[m];
     __syncthreads();
     // R for tokens 16w..
+    const auto &tok = lds.tokens[c & 1u];
     v4f p[4], r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const v4f *>(&lds.part[w * 4 + i][lane]);
+    const v4f from_state = *reinterpret_cast<const v4f *>(&tok.factor[0][16u * w + lq * 4u]);
+    const v4f to_state = *reinterpret_cast<const v4f *>(&tok.factor[1][16u * w + lq * 4u]);
+    const float keep = tok.decay;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = tok.value[16u * w + lq * 4u + i][lr];
+    __builtin_amdgcn_sched_barrier(0);
+    load_keys();
+    __builtin_amdgcn_sched_barrier(0);
     p[0] = (p[0] + p[1]) + (p[2] + p[3]);
     uint32_t lo[3], hi[3];
-    float own[4];  // e^(G_L - G) rk, for the update
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      r[i] = factor[i].x * bf16_to_f32(val[i]) - factor[i].y * p[0][i];
-      own[i] = factor[i].w;
-    }
+    r -= from_state * p[0];
     split2<3>(r[0], r[1], lo);
     split2<3>(r[2], r[3], hi);
 #pragma unroll
     for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2 *>(&lds.r[i][0][0] + put) = make_uint2(lo[i], hi[i]);
-    const float keep = decay;
-    __builtin_amdgcn_sched_barrier(0);
-    load_values();
     __syncthreads();
     // U = T R for tokens 16w..; columns past 16w + 15 of T are zero
     v8bf rb[3][2];
@@ -555,8 +534,8 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
       u3 = mfma32(as_bf(op_t[1][0]), rb[0][1], u3);
       u = (u + u2) + (u1 + u3);
     }
-    split2<3>(u[0] * own[0], u[1] * own[1], lo);
-    split2<3>(u[2] * own[2], u[3] * own[3], hi);
+    split2<3>(u[0] * to_state[0], u[1] * to_state[1], lo);
+    split2<3>(u[2] * to_state[2], u[3] * to_state[3], hi);
 #pragma unroll
     for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2 *>(&lds.decayed[i][0][0] + put) = make_uint2(lo[i], hi[i]);
     uint32_t ulo[2], uhi[2];
@@ -564,8 +543,6 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
     split2<2>(u[2], u[3], uhi);
 #pragma unroll
     for (int i = 0; i < 2; ++i) *reinterpret_cast<uint2 *>(&lds.u[i][0][0] + put) = make_uint2(ulo[i], uhi[i]);
-    __builtin_amdgcn_sched_barrier(0);
-    load_inverse();
     __syncthreads();
     // the state
     v8bf sb[3][2];
@@ -573,6 +550,14 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
     for (int i = 2; i >= 0; --i)
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) sb[i][ks] = *reinterpret_cast<const v8bf *>(&lds.decayed[i][ks][lane16]);
+    v8bf kt[kTiles][2];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) kt[t][ks] = transposed(t, ks);
+    __builtin_amdgcn_sched_barrier(0);
+    load_inverse();
+    __builtin_amdgcn_sched_barrier(0);
     v4f s1[kTiles];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) s[t] *= keep;
@@ -580,11 +565,9 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
     for (int i = 2; i >= 0; --i)
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
-        s1[t] = mfma32(as_bf(op_kt[t][0]), sb[i][0], i == 2 ? zero : s1[t]);
-        s[t] = mfma32(as_bf(op_kt[t][1]), sb[i][1], s[t]);
+        s1[t] = mfma32(kt[t][0], sb[i][0], i == 2 ? zero : s1[t]);
+        s[t] = mfma32(kt[t][1], sb[i][1], s[t]);
       }
-    __builtin_amdgcn_sched_barrier(0);
-    load_transposed();
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) s[t] += s1[t];
   }
@@ -600,7 +583,7 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
 }
 
 template <int kTiles, bool kWhole>
-__device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace &pl, const ScanLds<kTiles> &lds,
+__device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace &pl, ScanLds<kTiles> &lds,
                                             uint32_t w, uint32_t lane) {
   constexpr int kSteps = 2 * kTiles;  // dk in 32s
   const uint32_t lr = lane & 15u, lq = lane >> 4, lane16 = lane * 16u;
@@ -610,42 +593,76 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
   uint8_t *out = reinterpret_cast<uint8_t *>(a.out + ((uint64_t)pl.sq.begin * a.hv + pl.head) * a.dv);
   const uint32_t in_off[2] = {kTBytes + triangle_fragment(w, 0) * 2u * kFragment + lane16,
                               kTBytes + triangle_fragment(w, 1) * 2u * kFragment + lane16};
-  const uint32_t f_off = kTBytes + kInnerBytes + (16u * w + lq * 4u) * 16u + 8u;
-  uint32_t q_off, out_off[4];
+  // factors: a lane takes row lane / 16 of token 16w + lane % 16 (rows 1 to 3, and then the decay), and the b of token
+  // 16w + lane / 4, of which it takes v's columns 4 (lane % 4)..
+  const uint8_t *vals = reinterpret_cast<const uint8_t *>(a.v + (uint64_t)pl.head * a.v_head + (uint64_t)pl.sq.begin * a.v_token);
+  const uint32_t f_off = kTBytes + kInnerBytes + (lq == 3u ? 4u * kFactorRow : (lq + 1u) * kFactorRow + (16u * w + lr) * 4u);
+  const uint32_t b_off = kTBytes + kInnerBytes + (16u * w + (lane >> 2)) * 4u;
+  const uint32_t v_col = pl.col - lr + (lane & 3u) * 4u;
+  uint32_t q_off, v_off, out_off[4];
 #pragma unroll
   for (uint32_t i = 0; i < 4; ++i) out_off[i] = 2u * ((16u * w + lq * 4u + i) * a.hv * a.dv + pl.col);
-  auto token_offsets = [&](uint32_t n) { q_off = 2u * (min(16u * w + lr, n - 1u) * a.q_token + lq * 8u); };
+  auto token_offsets = [&](uint32_t n) {
+    q_off = 2u * (min(16u * w + lr, n - 1u) * a.q_token + lq * 8u);
+    v_off = 2u * (min(16u * w + (lane >> 2), n - 1u) * a.v_token + v_col);
+  };
 
   uint4 op_q[kSteps], op_in[2][2];
-  float factor[4];
+  uint4 val;
+  float factor, beta;
+  auto load_tokens = [&]() {
+    val = load_row<4, kWhole>(vals, v_off, v_col, a.dv);
+    factor = *reinterpret_cast<const float *>(mine + f_off);
+    beta = *reinterpret_cast<const float *>(mine + b_off);
+  };
+  // the loaded tokens into LDS, for both kinds of waves
+  auto put_tokens = [&](uint32_t c) {
+    auto &tok = lds.tokens[c & 1u];
+    const v4f v = {__uint_as_float(val.x << 16), __uint_as_float(val.x & 0xFFFF0000u), __uint_as_float(val.y << 16),
+                   __uint_as_float(val.y & 0xFFFF0000u)};
+    *reinterpret_cast<v4f *>(&tok.value[16u * w + (lane >> 2)][(lane & 3u) * 4u]) = v * beta;
+    if (lq < 3u)
+      tok.factor[lq][16u * w + lr] = factor;
+    else if (lr == 0u && w == 0u)
+      tok.decay = factor;
+  };
   auto load_queries = [&]() {
 #pragma unroll
     for (uint32_t k = 0; k < kSteps; ++k) op_q[k] = load_row<8, kWhole>(queries, q_off + 64u * k, 32u * k + lq * 8u, a.dk);
   };
   auto load_inner = [&]() {
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
+    for (uint32_t i = 0; i < 2; ++i) op_in[0][i] = fragment(mine, in_off[0] + i * kFragment);
+    if (w >= 2u) {
 #pragma unroll
-      for (uint32_t i = 0; i < 2; ++i) op_in[ks][i] = fragment(mine, in_off[ks] + i * kFragment);
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) factor[i] = *reinterpret_cast<const float *>(mine + (f_off + i * 16u));
+      for (uint32_t i = 0; i < 2; ++i) op_in[1][i] = fragment(mine, in_off[1] + i * kFragment);
+    }
+  };
+  // The tokens run one chunk ahead of the rest: they are loaded in one step,
+  // put into LDS at the end of the next, and used in the one after.
+  auto advance = [&](uint32_t c) {  // bases of chunk c
+    mine += (uint64_t)a.hv * kHeadBytes;
+    queries += (uint64_t)kChunk * 2u * a.q_token;
+    vals += (uint64_t)kChunk * 2u * a.v_token;
+    if (c + 1u == pl.chunks) token_offsets(pl.last);
   };
   token_offsets(pl.chunks == 1u ? pl.last : (uint32_t)kChunk);
+  load_tokens();
   load_queries();
   load_inner();
+  put_tokens(0);
+  if (pl.chunks > 1u) advance(1);
+  load_tokens();
   for (uint32_t c = 0; c < pl.chunks; ++c) {
-    if (c + 1u < pl.chunks) {
-      mine += (uint64_t)a.hv * kHeadBytes;
-      queries += (uint64_t)kChunk * 2u * a.q_token;
-      if (c + 2u == pl.chunks) token_offsets(pl.last);
-    }
     __syncthreads();
-    // Q S0 for tokens 16w..
+    __syncthreads();
+    // Q S0 for tokens 16w.., beside the chain's longest phase
     v8bf sb[2][kSteps];
 #pragma unroll
     for (int i = 1; i >= 0; --i)
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) sb[i][k] = *reinterpret_cast<const v8bf *>(&lds.s[i][k][lane16]);
+    const v4f scale = *reinterpret_cast<const v4f *>(&lds.tokens[c & 1u].factor[2][16u * w + lq * 4u]);
     v4f o = zero, o1 = zero;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
@@ -653,12 +670,10 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
       o1 = mfma32(as_bf(op_q[k]), sb[0][k], o1);
     }
     __builtin_amdgcn_sched_barrier(0);
+    __syncthreads();
+    put_tokens(c + 1u);
     load_queries();
-    __syncthreads();
-    o += o1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] *= factor[i];
-    __syncthreads();
+    o = (o + o1) * scale;
     // and the chunk's own part; columns past 16w + 15 of the triangle are zero
     v8bf ub[2][2];
 #pragma unroll
@@ -675,6 +690,8 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
     o = mfma32(as_bf(op_in[0][0]), ub[0][0], o);
     __builtin_amdgcn_sched_barrier(0);
     load_inner();
+    if (c + 2u < pl.chunks) advance(c + 2u);
+    load_tokens();
     o += o1;
     uint32_t lo[1], hi[1];
     split2<1>(o[0], o[1], lo);
@@ -731,7 +748,7 @@ hipError_t launch_chunked(const DeltaArgs &a, hipStream_t s) {
   }
   const uint64_t pairs = ((uint64_t)a.count * a.hv + 7u) / 8u * 8u;
   const dim3 grid((uint32_t)(pairs * ((a.dv + 15u) / 16u)));
-  if (a.dk == 64u * kTiles)
+  if (a.dk == 64u * kTiles && a.dv % 16u == 0u)
     hipLaunchKernelGGL((delta_scan_kernel<kTiles, true>), grid, dim3(kScanThreads), 0, s, a);
   else
     hipLaunchKernelGGL((delta_scan_kernel<kTiles, false>), grid, dim3(kScanThreads), 0, s, a);
@@ -742,7 +759,7 @@ hipError_t launch_chunked(const DeltaArgs &a, hipStream_t s) {
 
 uint64_t delta_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hk, uint32_t hv, uint32_t dk) {
   const uint64_t places = tokens / kChunk + (uint64_t)count;
-  return places * ((uint64_t)hv * kHeadBytes + (uint64_t)hk * key_bytes(dk <= 64u ? 64 : 128));
+  return places * hv * kHeadBytes;
 }
 
 hipError_t launch_delta_chunked(const DeltaArgs &a, hipStream_t s) {
