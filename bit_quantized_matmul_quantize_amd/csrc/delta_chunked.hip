@@ -334,7 +334,7 @@ constexpr int kScanThreads = 512;
 // What both kinds of waves know of their work.
 struct ScanPlace {
   DeltaSeq sq;
-  uint32_t head, khead, col, place0, chunks, last;  // last: tokens of the last chunk
+  uint32_t head, khead, block, col, place0, chunks, last;  // last: tokens of the last chunk
   bool col_in;
 };
 
@@ -646,15 +646,38 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
     vals += (uint64_t)kChunk * 2u * a.v_token;
     if (c + 1u == pl.chunks) token_offsets(pl.last);
   };
+  // The column blocks of a head run side by side on one XCD: each touches its
+  // share of the cache lines of the chunk after the next, so that its L2 has
+  // them by the time they are loaded (a step is shorter than memory's latency).
+  const uint32_t blocks = (a.dv + 15u) / 16u;
+  uint32_t touched = 0, touched_row = 0;  // read a step later, so that nothing waits for them
+  auto touch = [&](uint32_t c) {
+    c = min(c, pl.chunks - 1u);
+    const uint32_t line = pl.block + blocks * (w * 64u + lane);
+    if (line < kHeadBytes / 128u)
+      touched = *reinterpret_cast<const uint32_t *>(a.workspace + ((uint64_t)(pl.place0 + c) * a.hv + pl.head) * kHeadBytes + line * 128u);
+    const uint32_t row = pl.block + blocks * ((3u - w) * 64u + lane);  // token, half, and which of q, k, v
+    if (row < kChunk * 6u) {
+      const uint64_t t = min(pl.sq.begin + c * kChunk + row / 6u, pl.sq.end - 1u);
+      const uint32_t what = row % 6u / 2u, half = row & 1u;
+      const uint16_t *at = what == 0u ? a.q + t * a.q_token + (uint64_t)pl.khead * a.q_head
+                           : what == 1u ? a.k + t * a.k_token + (uint64_t)pl.khead * a.k_head
+                                        : a.v + t * a.v_token + (uint64_t)pl.head * a.v_head;
+      touched_row = at[half * min(64u, (what == 2u ? a.dv : a.dk) - 1u)];
+    }
+  };
   token_offsets(pl.chunks == 1u ? pl.last : (uint32_t)kChunk);
   load_tokens();
   load_queries();
   load_inner();
   put_tokens(0);
+  touch(1);
   if (pl.chunks > 1u) advance(1);
   load_tokens();
   for (uint32_t c = 0; c < pl.chunks; ++c) {
     __syncthreads();
+    asm volatile("" ::"v"(touched), "v"(touched_row));
+    touch(c + 2u);
     __syncthreads();
     // Q S0 for tokens 16w.., beside the chain's longest phase
     v8bf sb[2][kSteps];
@@ -719,7 +742,8 @@ __global__ __launch_bounds__(kScanThreads) void delta_scan_kernel(const DeltaArg
   pl.sq = delta_sequence(a, seq);
   pl.head = pair - seq * a.hv;
   pl.khead = pl.head / (a.hv / a.hk);
-  pl.col = (j % blocks) * 16u + (lane & 15u);
+  pl.block = j % blocks;
+  pl.col = pl.block * 16u + (lane & 15u);
   pl.col_in = pl.col < a.dv;
   pl.place0 = first_place(pl.sq.begin, seq);
   const uint32_t tokens = pl.sq.end - pl.sq.begin;
