@@ -1,12 +1,18 @@
 // Matrix product of 8-bit integers with a scale per token and per channel:
 //   out[i][j] = bf16_rne(float(sum_t a[i][t] w[j][t]) * sa[i] * sw[j] + bias[j]),
-// the sum exact in int32 on the int8 matrix cores.
+// the sum exact in int32 on the int8 matrix cores, so no tile, split or order
+// changes a bit of it.
 //
-// Tile 128 x 128, four waves of 64 x 64; k is staged 128 at a time through two
-// LDS stages.  The weight is the A operand, so that a lane's accumulators
-// share one output row and are stored as runs of four columns.  Rows past m or
-// n load the last valid row and are not stored.
+// Two kernels.  Few rows (a decoded token, a verified batch) are bound by the
+// weight's bytes: w8a8_rows_kernel streams it once.  Prompts are bound by the
+// matrix cores: w8a8_tile_kernel.
+//
+// In both the weight is the A operand, so that a lane's accumulators share one
+// output row and are runs of four columns.  Rows past m or n load the last
+// valid row and are not stored.
 #include "bqmm_internal.h"
+
+#include <type_traits>
 
 namespace bqmm {
 namespace {
@@ -14,93 +20,292 @@ namespace {
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));
 
-constexpr int BM = 128, BN = 128, KS = 128;
-constexpr int kStride = KS + 16;  // bytes per staged row; the pad spreads banks
-constexpr int kThreads = 256;
-constexpr int kTileBytes = BM * kStride;
+constexpr uint32_t KS = 128;  // bytes of k per step; rows are padded to it
 
-__global__ __launch_bounds__(kThreads, 2) void w8a8_tile_kernel(const uint8_t *__restrict__ act,
-                                                                const uint8_t *__restrict__ w,
-                                                                const uint16_t *__restrict__ bias,
-                                                                uint16_t *__restrict__ out, uint32_t m, uint32_t n,
-                                                                uint32_t kp) {
+// Four columns j.. of output row i.
+struct Scales {
+  const float *sa, *sw;
+  const uint16_t *bias;
+  uint16_t *out;
+  uint32_t m, n;
+};
+__device__ __forceinline__ void store4(const Scales &s, uint32_t i, uint32_t j, int a, int b, int c, int d, float sa) {
+  if (i >= s.m || j >= s.n) return;
+  const int v[4] = {a, b, c, d};
+  uint16_t *p = s.out + (uint64_t)i * s.n + j;
+  if (j + 4u <= s.n && (s.n & 3u) == 0u) {
+    const float4 w = *reinterpret_cast<const float4 *>(s.sw + j);
+    float y[4] = {(float)a * sa * w.x, (float)b * sa * w.y, (float)c * sa * w.z, (float)d * sa * w.w};
+    if (s.bias) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] += bf16_to_f32(s.bias[j + e]);
+    }
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+  } else {
+#pragma unroll
+    for (uint32_t e = 0; e < 4; ++e)
+      if (j + e < s.n) {
+        float y = (float)v[e] * sa * s.sw[j + e];
+        if (s.bias) y += bf16_to_f32(s.bias[j + e]);
+        p[e] = (uint16_t)f32_to_bf16_rne(y);
+      }
+  }
+}
+
+// ---- few rows ---------------------------------------------------------------------
+
+// A workgroup takes 16 kNt output columns and 16 kMt rows; its waves split k
+// and add their sums in LDS.  Both operands come straight from memory into
+// registers, 16 bytes a lane: 16 rows x 64 bytes are a matrix operand.
+template <int kNt, int kMt, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void w8a8_rows_kernel(const uint8_t *__restrict__ act,
+                                                                const uint8_t *__restrict__ w, Scales s, uint32_t kp) {
+  constexpr int kAhead = kNt + kMt <= 2 ? 8 : kNt + kMt <= 3 ? 6 : 4;  // steps of loads in flight
+  __shared__ v4i part[kWaves > 1 ? kWaves - 1 : 1][kNt * kMt][64];
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, r = lane & 15u, q = lane >> 4;
+  const uint32_t n0 = blockIdx.x * (16u * kNt), m0 = blockIdx.y * (16u * kMt);
+  const uint32_t steps = kp / 64u, s0 = steps * wave / kWaves, s1 = steps * (wave + 1u) / kWaves;
+  const uint8_t *wp[kNt], *ap[kMt];
+#pragma unroll
+  for (int t = 0; t < kNt; ++t) wp[t] = w + (uint64_t)min(n0 + 16u * t + r, s.n - 1u) * kp + q * 16u;
+#pragma unroll
+  for (int t = 0; t < kMt; ++t) ap[t] = act + (uint64_t)min(m0 + 16u * t + r, s.m - 1u) * kp + q * 16u;
+  v4i acc[kNt][kMt];
+#pragma unroll
+  for (int i = 0; i < kNt; ++i)
+#pragma unroll
+    for (int j = 0; j < kMt; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+
+  uint32_t k = s0;
+  for (; k + kAhead <= s1; k += kAhead) {
+    v4i A[kAhead][kNt], B[kAhead][kMt];
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) {
+#pragma unroll
+      for (int t = 0; t < kNt; ++t) A[d][t] = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(wp[t] + (k + d) * 64u));
+#pragma unroll
+      for (int t = 0; t < kMt; ++t) B[d][t] = *reinterpret_cast<const v4i *>(ap[t] + (k + d) * 64u);
+    }
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d)
+#pragma unroll
+      for (int i = 0; i < kNt; ++i)
+#pragma unroll
+        for (int j = 0; j < kMt; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[d][i], B[d][j], acc[i][j], 0, 0, 0);
+  }
+  for (; k < s1; ++k)
+#pragma unroll
+    for (int i = 0; i < kNt; ++i) {
+      const v4i A = *reinterpret_cast<const v4i *>(wp[i] + k * 64u);
+#pragma unroll
+      for (int j = 0; j < kMt; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(A, *reinterpret_cast<const v4i *>(ap[j] + k * 64u), acc[i][j], 0, 0, 0);
+    }
+
+  if constexpr (kWaves > 1) {
+    if (wave > 0) {
+#pragma unroll
+      for (int i = 0; i < kNt; ++i)
+#pragma unroll
+        for (int j = 0; j < kMt; ++j) part[wave - 1][i * kMt + j][lane] = acc[i][j];
+    }
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int v = 0; v < kWaves - 1; ++v)
+#pragma unroll
+      for (int i = 0; i < kNt; ++i)
+#pragma unroll
+        for (int j = 0; j < kMt; ++j) acc[i][j] += part[v][i * kMt + j][lane];
+  }
+#pragma unroll
+  for (int j = 0; j < kMt; ++j) {
+    const uint32_t mm = m0 + 16u * j + r;
+    const float sa = s.sa[min(mm, s.m - 1u)];
+#pragma unroll
+    for (int i = 0; i < kNt; ++i)
+      store4(s, mm, n0 + 16u * i + q * 4u, acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], sa);
+  }
+}
+
+// ---- tiles ------------------------------------------------------------------------
+
+// 16 bytes a lane straight from memory into LDS: lane i's go to the wave's
+// destination + 16 i.  Not a builtin, because the compiler waits for all such
+// loads before any read of LDS; here the kernel waits itself, where a stage is
+// complete.  (M0 holds the destination; a wait state lies between its write and
+// its use.)  No register is written, so nothing can be overwritten in flight.
+__device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, const uint8_t *base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
+               : "memory");
+}
+
+// Four waves, two by two, each of 32 kTm rows x 32 kTn columns: 64 kTm x 64 kTn
+// outputs.  k runs in steps of 128 bytes through two LDS stages.  A row's eight
+// 16-byte pieces lie in the order piece ^ (row % 8), which spreads a column of
+// pieces over the banks; the loads that fill the stage write LDS in order and
+// take the pieces from memory in that order instead.
+//
+// Per step four times: the matrix products of 32 bytes of k, and between them
+// the reads of the next 32 bytes.  With the last of them the stage has been
+// read: the waves meet once, then the next stage's first reads and the loads
+// that refill this one go between the products too.
+template <int kTm, int kTn>
+struct Tile {
+  static constexpr uint32_t BM = 64 * kTm, BN = 64 * kTn;
+  static constexpr uint32_t kStage = (BM + BN) * KS;
+  static constexpr int kLoads = 2 * (kTm + kTn);  // per wave and step, 1 KB (8 rows) each
+};
+
+template <int kTm, int kTn>
+__global__ __launch_bounds__(256, 1) void w8a8_tile_kernel(const uint8_t *__restrict__ act,
+                                                           const uint8_t *__restrict__ w, Scales s, uint32_t kp,
+                                                           uint32_t tiles_m, uint32_t tiles_n) {
+  using T = Tile<kTm, kTn>;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
-  const uint32_t wn = wave & 1u, wm = wave >> 1;
-  const uint32_t n_base = blockIdx.y * BN, m_base = blockIdx.x * BM;
-  const uint32_t r0 = tid >> 3, col = (tid & 7u) * 16u;
-  v16i acc[2][2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+  // Workgroups go round the eight XCDs; each XCD takes a run of tiles, eight
+  // rows of tiles at a time, so that the tiles in flight on it share operands.
+  const uint32_t total = tiles_m * tiles_n, each = (total + 7u) / 8u;
+  const uint32_t tile = (blockIdx.x & 7u) * each + (blockIdx.x >> 3);
+  if (tile >= total || (blockIdx.x >> 3) >= each) return;
+  const uint32_t group = tile / (8u * tiles_n), in = tile - group * 8u * tiles_n;
+  const uint32_t gm = min(8u, tiles_m - group * 8u);
+  const uint32_t m0 = (group * 8u + in % gm) * T::BM, n0 = in / gm * T::BN;
 
-  for (uint32_t k0 = 0; k0 < kp; k0 += KS) {
-    uint4 ra[4], rw[4];
+  const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t wn = wave & 1u, wm = wave >> 1, r = lane & 31u, half = lane >> 5;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
+
+  // what this wave loads: rows 8 (wave + 4 i) .. + 7 of the stage, weight rows first
+  const uint8_t *wbase = w + (uint64_t)n0 * kp, *abase = act + (uint64_t)m0 * kp;
+  uint32_t off[T::kLoads];
+  {
+    const uint32_t lr = lane >> 3, piece = ((lane & 7u) ^ lr) * 16u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      ra[i] = *reinterpret_cast<const uint4 *>(act + (uint64_t)min(m_base + r0 + 32u * i, m - 1u) * kp + k0 + col);
-      rw[i] = *reinterpret_cast<const uint4 *>(w + (uint64_t)min(n_base + r0 + 32u * i, n - 1u) * kp + k0 + col);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      *reinterpret_cast<uint4 *>(lds + (r0 + 32 * i) * kStride + col) = ra[i];
-      *reinterpret_cast<uint4 *>(lds + kTileBytes + (r0 + 32 * i) * kStride + col) = rw[i];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < KS / 32; ++kk) {
-      v4i A[2], B[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        A[t] = *reinterpret_cast<const v4i *>(lds + kTileBytes + (wn * 64 + t * 32 + (lane & 31)) * kStride + 32 * kk + 16 * (lane >> 5));
-        B[t] = *reinterpret_cast<const v4i *>(lds + (wm * 64 + t * 32 + (lane & 31)) * kStride + 32 * kk + 16 * (lane >> 5));
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(A[i], B[j], acc[i][j], 0, 0, 0);
+    for (uint32_t i = 0; i < (uint32_t)T::kLoads; ++i) {
+      const uint32_t row = 8u * (wave + 4u * i) + lr;
+      off[i] = (i < 2u * kTn ? min(row, s.n - 1u - n0) : min(row - T::BN, s.m - 1u - m0)) * kp + piece;
     }
   }
+  auto load = [&](int i, uint32_t stage, uint32_t k0) {
+    load_to_lds(lds0 + stage * T::kStage + (wave + 4u * i) * 1024u, off[i], (i < 2 * kTn ? wbase : abase) + k0);
+  };
+  // this lane's place in a row block of 32, for the four pieces of a step
+  uint32_t at[4];
+#pragma unroll
+  for (uint32_t kk = 0; kk < 4; ++kk) at[kk] = r * KS + (((kk * 2u + half) ^ (r & 7u)) * 16u);
+  auto read = [&](uint32_t stage, int kk, int t) -> v4i {  // t < kTn: weight rows, then activation rows
+    const uint32_t row = t < kTn ? wn * (32u * kTn) + 32u * t : T::BN + wm * (32u * kTm) + 32u * (t - kTn);
+    return *reinterpret_cast<const v4i *>(lds + stage * T::kStage + row * KS + at[kk]);
+  };
 
-  const float *sa = reinterpret_cast<const float *>(act + (uint64_t)m * kp);
-  const float *sw = reinterpret_cast<const float *>(w + (uint64_t)n * kp);
+  v16i acc[kTn][kTm];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const uint32_t mm = m_base + wm * 64 + j * 32 + (lane & 31);
-    if (mm >= m) continue;
-    const float s = sa[mm];
-    uint16_t *row = out + (uint64_t)mm * n;
+  for (int i = 0; i < kTn; ++i)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < kTm; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const uint32_t nn = n_base + wn * 64 + i * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        if (nn < n) {
-          float y = (float)acc[i][j][r] * s * sw[nn];
-          if (bias) y += bf16_to_f32(bias[nn]);
-          row[nn] = (uint16_t)f32_to_bf16_rne(y);
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+
+  // A stage's loads go out in two halves: with the last piece of the step that
+  // frees it, and with the first piece of the step after.  Past the end the last
+  // stage is loaded again, so that no step has a branch.
+  constexpr int kHalf = T::kLoads / 2, kProducts = kTn * kTm, kReads = kTn + kTm;
+  constexpr int kSpread = kProducts > 1 ? kProducts / 2 : 1;
+  const uint32_t steps = kp / KS;
+  v4i f[2][kReads];
+  auto step = [&](uint32_t n, auto last) {
+    constexpr bool kLast = decltype(last)::value;
+    const uint32_t stage = n & 1u;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      // the next stage has arrived, this one has been read
+      if (kk == 3 && !kLast) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+      for (int p = 0; p < kProducts; ++p) {
+        const int i = p % kTn, j = p / kTn;
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f[kk & 1][i], f[kk & 1][kTn + j], acc[i][j], 0, 0, 0);
+        // reads of the next piece between the first half of the products, loads between the second
+        if (p < kSpread && (kk < 3 || !kLast)) {
+#pragma unroll
+          for (int t = p * kReads / kSpread; t < (p + 1) * kReads / kSpread; ++t)
+            f[(kk + 1) & 1][t] = kk < 3 ? read(stage, kk + 1, t) : read(stage ^ 1u, 0, t);
         }
+        if (p >= kProducts - kSpread && (kk == 0 || kk == 3) && !kLast) {
+          const int q = p - (kProducts - kSpread);
+#pragma unroll
+          for (int l = q * kHalf / kSpread; l < (q + 1) * kHalf / kSpread; ++l) {
+            if (kk == 3)
+              load(l, stage, min(n + 2u, steps - 1u) * KS);
+            else
+              load(kHalf + l, stage ^ 1u, (n + 1u) * KS);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < T::kLoads; ++i) load(i, 0u, 0u);
+#pragma unroll
+  for (int i = 0; i < kHalf; ++i) load(i, 1u, min(1u, steps - 1u) * KS);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kHalf) : "memory");
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < kReads; ++t) f[0][t] = read(0u, 0, t);
+  for (uint32_t n = 0; n + 1u < steps; ++n) step(n, std::false_type{});
+  step(steps - 1u, std::true_type{});
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way into LDS when the workgroup ends
+
+#pragma unroll
+  for (int j = 0; j < kTm; ++j) {
+    const uint32_t mm = m0 + wm * (32u * kTm) + 32u * j + r;
+    const float sa = s.sa[min(mm, s.m - 1u)];
+#pragma unroll
+    for (int i = 0; i < kTn; ++i) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        store4(s, mm, n0 + wn * (32u * kTn) + 32u * i + 2u * e + 4u * half, acc[i][j][e], acc[i][j][e + 1],
+               acc[i][j][e + 2], acc[i][j][e + 3], sa);
+      __builtin_amdgcn_sched_barrier(0);  // one block's scales at a time in registers
+    }
   }
+}
+
+template <int kTm, int kTn>
+hipError_t launch_tiles(const uint8_t *act, const uint8_t *w, const Scales &s, uint32_t kp, hipStream_t st) {
+  using T = Tile<kTm, kTn>;
+  constexpr int lds = 2 * T::kStage;
+  const void *kernel = reinterpret_cast<const void *>(w8a8_tile_kernel<kTm, kTn>);
+  const hipError_t e = ensure_dynamic_lds(kernel, lds);
+  if (e != hipSuccess) return e;
+  const uint32_t tm = (s.m + T::BM - 1u) / T::BM, tn = (s.n + T::BN - 1u) / T::BN;
+  hipLaunchKernelGGL((w8a8_tile_kernel<kTm, kTn>), dim3((tm * tn + 7u) / 8u * 8u), dim3(256), lds, st, act, w, s, kp, tm,
+                     tn);
+  return hipGetLastError();
+}
+
+template <int kNt, int kMt, int kWaves>
+hipError_t launch_rows(const uint8_t *act, const uint8_t *w, const Scales &s, uint32_t kp, hipStream_t st) {
+  const dim3 grid((s.n + 16u * kNt - 1u) / (16u * kNt), (s.m + 16u * kMt - 1u) / (16u * kMt));
+  hipLaunchKernelGGL((w8a8_rows_kernel<kNt, kMt, kWaves>), grid, dim3(64 * kWaves), 0, st, act, w, s, kp);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_w8a8_gemm(const void *act, const void *w, const void *bias, void *out, uint32_t m, uint32_t n,
-                            uint32_t k, hipStream_t s) {
-  const uint32_t kp = (k + 127u) / 128u * 128u;
-  constexpr int lds = 2 * kTileBytes;
-  const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void *>(w8a8_tile_kernel), lds);
-  if (e != hipSuccess) return e;
-  const dim3 grid((uint32_t)(((uint64_t)m + BM - 1) / BM), (uint32_t)(((uint64_t)n + BN - 1) / BN));
-  hipLaunchKernelGGL(w8a8_tile_kernel, grid, dim3(kThreads), lds, s, static_cast<const uint8_t *>(act),
-                     static_cast<const uint8_t *>(w), static_cast<const uint16_t *>(bias),
-                     static_cast<uint16_t *>(out), m, n, kp);
-  return hipGetLastError();
+                            uint32_t k, hipStream_t st) {
+  const uint32_t kp = (k + KS - 1u) / KS * KS;
+  const uint8_t *ap = static_cast<const uint8_t *>(act), *wp = static_cast<const uint8_t *>(w);
+  const Scales s = {reinterpret_cast<const float *>(ap + (uint64_t)m * kp),
+                    reinterpret_cast<const float *>(wp + (uint64_t)n * kp), static_cast<const uint16_t *>(bias),
+                    static_cast<uint16_t *>(out), m, n};
+  if (m <= 16u) return launch_rows<1, 1, 4>(ap, wp, s, kp, st);
+  if (m <= 32u) return launch_rows<1, 2, 4>(ap, wp, s, kp, st);
+  if (m <= 128u) return launch_tiles<1, 1>(ap, wp, s, kp, st);
+  if (m <= 512u) return launch_tiles<2, 2>(ap, wp, s, kp, st);
+  return launch_tiles<4, 4>(ap, wp, s, kp, st);
 }
 
 }  // namespace bqmm
