@@ -150,6 +150,10 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, const
 // the reads of the next 32 bytes.  With the last of them the stage has been
 // read: the waves meet once, then the next stage's first reads and the loads
 // that refill this one go between the products too.
+struct __attribute__((packed, aligned(2))) Row8 {  // eight results of a row, which starts at any even address
+  uint32_t w[4];
+};
+
 template <int kTm, int kTn>
 struct Tile {
   static constexpr uint32_t BM = 64 * kTm, BN = 64 * kTn;
@@ -213,6 +217,14 @@ __global__ __launch_bounds__(256, 1) void w8a8_tile_kernel(const uint8_t *__rest
   constexpr int kHalf = T::kLoads / 2, kProducts = kTn * kTm, kReads = kTn + kTm;
   constexpr int kSpread = kProducts > 1 ? kProducts / 2 : 1;
   const uint32_t steps = kp / KS;
+  // the tile's scales and biases, for the end
+  float *scale_w = reinterpret_cast<float *>(lds + 2u * T::kStage), *biases = scale_w + T::BN, *scale_a = biases + T::BN;
+  for (uint32_t i = threadIdx.x; i < T::BN; i += 256u) {
+    const uint32_t j = min(n0 + i, s.n - 1u);
+    scale_w[i] = s.sw[j];
+    biases[i] = s.bias ? bf16_to_f32(s.bias[j]) : 0.0f;
+  }
+  for (uint32_t i = threadIdx.x; i < T::BM; i += 256u) scale_a[i] = s.sa[min(m0 + i, s.m - 1u)];
   v4i f[2][kReads];
   auto step = [&](uint32_t n, auto last) {
     constexpr bool kLast = decltype(last)::value;
@@ -257,17 +269,44 @@ __global__ __launch_bounds__(256, 1) void w8a8_tile_kernel(const uint8_t *__rest
   step(steps - 1u, std::true_type{});
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way into LDS when the workgroup ends
 
+  // The results go through LDS, where the stages were (each wave's own part):
+  // a lane has runs of four columns of one row, memory wants whole rows.  The
+  // 16-byte pieces of a row are spread over the banks as in the stages.
+  __syncthreads();
+  constexpr uint32_t kPieces = 4 * kTn, kRowsAtOnce = 64 / kPieces;  // per row of the wave; rows per store
+  uint8_t *mine = lds + wave * (32 * kTm * 64 * kTn);
 #pragma unroll
-  for (int j = 0; j < kTm; ++j) {
-    const uint32_t mm = m0 + wm * (32u * kTm) + 32u * j + r;
-    const float sa = s.sa[min(mm, s.m - 1u)];
+  for (int i = 0; i < kTn; ++i)
 #pragma unroll
-    for (int i = 0; i < kTn; ++i) {
+    for (int e = 0; e < 16; e += 4) {
+      const uint32_t c = wn * (32u * kTn) + 32u * i + 2u * e + 4u * half;
+      const float4 sw = *reinterpret_cast<const float4 *>(scale_w + c), bias = *reinterpret_cast<const float4 *>(biases + c);
 #pragma unroll
-      for (int e = 0; e < 16; e += 4)
-        store4(s, mm, n0 + wn * (32u * kTn) + 32u * i + 2u * e + 4u * half, acc[i][j][e], acc[i][j][e + 1],
-               acc[i][j][e + 2], acc[i][j][e + 3], sa);
-      __builtin_amdgcn_sched_barrier(0);  // one block's scales at a time in registers
+      for (int j = 0; j < kTm; ++j) {
+        const uint32_t row = 32u * j + r;
+        const float sa = scale_a[wm * (32u * kTm) + row];
+        const v16i &v = acc[i][j];
+        const uint2 y = make_uint2(
+            pack_bf16x2((float)v[e] * sa * sw.x + bias.x, (float)v[e + 1] * sa * sw.y + bias.y),
+            pack_bf16x2((float)v[e + 2] * sa * sw.z + bias.z, (float)v[e + 3] * sa * sw.w + bias.w));
+        const uint32_t piece = (4u * i + e / 4u) ^ (row & (kPieces - 1u));
+        *reinterpret_cast<uint2 *>(mine + row * (64u * kTn) + piece * 16u + half * 8u) = y;
+      }
+    }
+  const uint32_t piece = lane % kPieces, col = n0 + wn * (32u * kTn) + piece * 8u;
+#pragma unroll 4
+  for (uint32_t row = lane / kPieces; row < 32u * kTm; row += kRowsAtOnce) {
+    const uint4 y = *reinterpret_cast<const uint4 *>(mine + row * (64u * kTn) + ((piece ^ (row & (kPieces - 1u))) * 16u));
+    const uint32_t mm = m0 + wm * (32u * kTm) + row;
+    if (mm >= s.m) continue;
+    uint16_t *p = s.out + (uint64_t)mm * s.n + col;
+    if (col + 8u <= s.n) {
+      *reinterpret_cast<Row8 *>(p) = Row8{{y.x, y.y, y.z, y.w}};
+    } else {
+      const uint32_t v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (uint32_t q = 0; q < 8; ++q)
+        if (col + q < s.n) p[q] = (uint16_t)(v[q / 2] >> (16u * (q & 1u)));
     }
   }
 }
@@ -275,7 +314,7 @@ __global__ __launch_bounds__(256, 1) void w8a8_tile_kernel(const uint8_t *__rest
 template <int kTm, int kTn>
 hipError_t launch_tiles(const uint8_t *act, const uint8_t *w, const Scales &s, uint32_t kp, hipStream_t st) {
   using T = Tile<kTm, kTn>;
-  constexpr int lds = 2 * T::kStage;
+  constexpr int lds = 2 * T::kStage + (2 * T::BN + T::BM) * 4;  // two stages, scales and biases
   const void *kernel = reinterpret_cast<const void *>(w8a8_tile_kernel<kTm, kTn>);
   const hipError_t e = ensure_dynamic_lds(kernel, lds);
   if (e != hipSuccess) return e;
