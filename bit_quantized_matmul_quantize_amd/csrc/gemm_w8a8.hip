@@ -20,7 +20,7 @@ namespace {
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));
 
-constexpr uint32_t KS = 128;  // bytes of k per step; rows are padded to it
+constexpr uint32_t kRowPad = 128;  // rows are padded to it
 
 // Four columns j.. of output row i.
 struct Scales {
@@ -140,67 +140,72 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, const
                : "memory");
 }
 
+// min(a, b) that the compiler does not see through: it would cut the loop over
+// the steps in three where the min changes sides, and the copies spill.
+__device__ __forceinline__ uint32_t at_most(uint32_t a, uint32_t b) {
+  uint32_t x;
+  asm("s_min_u32 %0, %1, %2" : "=s"(x) : "s"(a), "s"(b) : "scc");
+  return x;
+}
+
 // Four waves, two by two, each of 32 kTm rows x 32 kTn columns: 64 kTm x 64 kTn
-// outputs.  k runs in steps of 128 bytes through two LDS stages.  A row's eight
-// 16-byte pieces lie in the order piece ^ (row % 8), which spreads a column of
-// pieces over the banks; the loads that fill the stage write LDS in order and
-// take the pieces from memory in that order instead.
+// outputs.  k runs in steps of kStep (64 or 128) bytes through kStages LDS
+// stages.  The 16-byte pieces of a row lie in the order piece ^ f(row), which
+// spreads a column of pieces over the banks; the loads that fill the stage
+// write LDS in order and take the pieces from memory in that order instead.
 //
-// Per step four times: the matrix products of 32 bytes of k, and between them
+// Per step once for each 32 bytes of k: its matrix products, and between them
 // the reads of the next 32 bytes.  With the last of them the stage has been
 // read: the waves meet once, then the next stage's first reads and the loads
-// that refill this one go between the products too.
+// that refill this one go between the products too (half of them; the other
+// half goes with the first products of the step after).
+template <int kTm, int kTn, int kStep, int kStages>
+struct Tile {
+  static constexpr uint32_t BM = 64 * kTm, BN = 64 * kTn;
+  static constexpr uint32_t kStage = (BM + BN) * kStep;
+  static constexpr uint32_t kRowsAtOnce = 1024 / kStep;            // rows of one load of a wave, 1 KB
+  static constexpr int kLoadsN = kTn * kStep / 64, kLoads = (kTm + kTn) * kStep / 64;  // per wave and step
+  // stages, scales and biases; the results take the stages' place at the end
+  static constexpr uint32_t kLds = (kStages * kStage > BM * BN * 2 ? kStages * kStage : BM * BN * 2) + (2 * BN + BM) * 4;
+};
+
 struct __attribute__((packed, aligned(2))) Row8 {  // eight results of a row, which starts at any even address
   uint32_t w[4];
 };
 
-template <int kTm, int kTn>
-struct Tile {
-  static constexpr uint32_t BM = 64 * kTm, BN = 64 * kTn;
-  static constexpr uint32_t kStage = (BM + BN) * KS;
-  static constexpr int kLoads = 2 * (kTm + kTn);  // per wave and step, 1 KB (8 rows) each
-};
-
-template <int kTm, int kTn>
-__global__ __launch_bounds__(256, 1) void w8a8_tile_kernel(const uint8_t *__restrict__ act,
-                                                           const uint8_t *__restrict__ w, Scales s, uint32_t kp,
-                                                           uint32_t tiles_m, uint32_t tiles_n) {
-  using T = Tile<kTm, kTn>;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  // Workgroups go round the eight XCDs; each XCD takes a run of tiles, eight
-  // rows of tiles at a time, so that the tiles in flight on it share operands.
-  const uint32_t total = tiles_m * tiles_n, each = (total + 7u) / 8u;
-  const uint32_t tile = (blockIdx.x & 7u) * each + (blockIdx.x >> 3);
-  if (tile >= total || (blockIdx.x >> 3) >= each) return;
-  const uint32_t group = tile / (8u * tiles_n), in = tile - group * 8u * tiles_n;
-  const uint32_t gm = min(8u, tiles_m - group * 8u);
-  const uint32_t m0 = (group * 8u + in % gm) * T::BM, n0 = in / gm * T::BN;
-
+template <int kTm, int kTn, int kStep, int kStages>
+__device__ __forceinline__ void run_tile(const uint8_t *act, const uint8_t *w, const Scales &s, uint32_t kp, uint32_t m0,
+                                         uint32_t n0, uint8_t *lds) {
+  using T = Tile<kTm, kTn, kStep, kStages>;
+  constexpr uint32_t kInRow = kStep / 16;  // pieces of a row
   const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t wn = wave & 1u, wm = wave >> 1, r = lane & 31u, half = lane >> 5;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
+  // 256 bytes of LDS (all banks) hold 2 rows of 128 bytes or 4 of 64
+  auto spread = [](uint32_t row) -> uint32_t { return kStep == 128 ? row & 7u : row >> 2 & 3u; };
 
-  // what this wave loads: rows 8 (wave + 4 i) .. + 7 of the stage, weight rows first
+  // what this wave loads: kRowsAtOnce rows from row (wave + 4 i) kRowsAtOnce on of the stage, weight rows first
   const uint8_t *wbase = w + (uint64_t)n0 * kp, *abase = act + (uint64_t)m0 * kp;
   uint32_t off[T::kLoads];
   {
-    const uint32_t lr = lane >> 3, piece = ((lane & 7u) ^ lr) * 16u;
+    const uint32_t lr = lane / kInRow, piece = ((lane % kInRow) ^ spread(lr)) * 16u;
 #pragma unroll
     for (uint32_t i = 0; i < (uint32_t)T::kLoads; ++i) {
-      const uint32_t row = 8u * (wave + 4u * i) + lr;
-      off[i] = (i < 2u * kTn ? min(row, s.n - 1u - n0) : min(row - T::BN, s.m - 1u - m0)) * kp + piece;
+      const uint32_t row = T::kRowsAtOnce * (wave + 4u * i) + lr;
+      off[i] = (i < (uint32_t)T::kLoadsN ? min(row, s.n - 1u - n0) : min(row - T::BN, s.m - 1u - m0)) * kp + piece;
     }
   }
   auto load = [&](int i, uint32_t stage, uint32_t k0) {
-    load_to_lds(lds0 + stage * T::kStage + (wave + 4u * i) * 1024u, off[i], (i < 2 * kTn ? wbase : abase) + k0);
+    load_to_lds(lds0 + stage * T::kStage + (wave + 4u * i) * 1024u, off[i], (i < T::kLoadsN ? wbase : abase) + k0);
   };
-  // this lane's place in a row block of 32, for the four pieces of a step
-  uint32_t at[4];
+  // this lane's place in a row block of 32, for the pieces of a step
+  constexpr int kParts = kStep / 32;
+  uint32_t at[kParts];
 #pragma unroll
-  for (uint32_t kk = 0; kk < 4; ++kk) at[kk] = r * KS + (((kk * 2u + half) ^ (r & 7u)) * 16u);
+  for (uint32_t kk = 0; kk < (uint32_t)kParts; ++kk) at[kk] = r * kStep + (((kk * 2u + half) ^ spread(r)) * 16u);
   auto read = [&](uint32_t stage, int kk, int t) -> v4i {  // t < kTn: weight rows, then activation rows
     const uint32_t row = t < kTn ? wn * (32u * kTn) + 32u * t : T::BN + wm * (32u * kTm) + 32u * (t - kTn);
-    return *reinterpret_cast<const v4i *>(lds + stage * T::kStage + row * KS + at[kk]);
+    return *reinterpret_cast<const v4i *>(lds + stage * T::kStage + row * kStep + at[kk]);
   };
 
   v16i acc[kTn][kTm];
@@ -211,14 +216,12 @@ __global__ __launch_bounds__(256, 1) void w8a8_tile_kernel(const uint8_t *__rest
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
-  // A stage's loads go out in two halves: with the last piece of the step that
-  // frees it, and with the first piece of the step after.  Past the end the last
-  // stage is loaded again, so that no step has a branch.
   constexpr int kHalf = T::kLoads / 2, kProducts = kTn * kTm, kReads = kTn + kTm;
   constexpr int kSpread = kProducts > 1 ? kProducts / 2 : 1;
-  const uint32_t steps = kp / KS;
+  const uint32_t steps = kp / kStep;
   // the tile's scales and biases, for the end
-  float *scale_w = reinterpret_cast<float *>(lds + 2u * T::kStage), *biases = scale_w + T::BN, *scale_a = biases + T::BN;
+  float *scale_w = reinterpret_cast<float *>(lds + T::kLds - (2 * T::BN + T::BM) * 4);
+  float *biases = scale_w + T::BN, *scale_a = biases + T::BN;
   for (uint32_t i = threadIdx.x; i < T::BN; i += 256u) {
     const uint32_t j = min(n0 + i, s.n - 1u);
     scale_w[i] = s.sw[j];
@@ -228,29 +231,33 @@ __global__ __launch_bounds__(256, 1) void w8a8_tile_kernel(const uint8_t *__rest
   v4i f[2][kReads];
   auto step = [&](uint32_t n, auto last) {
     constexpr bool kLast = decltype(last)::value;
-    const uint32_t stage = n & 1u;
+    const uint32_t stage = n % kStages, next = (n + 1u) % kStages;
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      // the next stage has arrived, this one has been read
-      if (kk == 3 && !kLast) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    for (int kk = 0; kk < kParts; ++kk) {
+      // the next stage has arrived (those after it may be on their way), this one has been read
+      if (kk == kParts - 1 && !kLast)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kStages - 2) * T::kLoads) : "memory");
 #pragma unroll
       for (int p = 0; p < kProducts; ++p) {
         const int i = p % kTn, j = p / kTn;
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f[kk & 1][i], f[kk & 1][kTn + j], acc[i][j], 0, 0, 0);
         // reads of the next piece between the first half of the products, loads between the second
-        if (p < kSpread && (kk < 3 || !kLast)) {
+        if (p < kSpread && (kk < kParts - 1 || !kLast)) {
 #pragma unroll
           for (int t = p * kReads / kSpread; t < (p + 1) * kReads / kSpread; ++t)
-            f[(kk + 1) & 1][t] = kk < 3 ? read(stage, kk + 1, t) : read(stage ^ 1u, 0, t);
+            f[(kk + 1) & 1][t] = kk < kParts - 1 ? read(stage, kk + 1, t) : read(next, 0, t);
         }
-        if (p >= kProducts - kSpread && (kk == 0 || kk == 3) && !kLast) {
+        // (past the end the last step's are loaded again, so that no step has a branch)
+        if (p >= kProducts - kSpread && (kk == 0 || kk == kParts - 1) && !kLast) {
           const int q = p - (kProducts - kSpread);
+          if (kk == 0) {
 #pragma unroll
-          for (int l = q * kHalf / kSpread; l < (q + 1) * kHalf / kSpread; ++l) {
-            if (kk == 3)
-              load(l, stage, min(n + 2u, steps - 1u) * KS);
-            else
-              load(kHalf + l, stage ^ 1u, (n + 1u) * KS);
+            for (int l = q * (T::kLoads - kHalf) / kSpread; l < (q + 1) * (T::kLoads - kHalf) / kSpread; ++l)
+              load(kHalf + l, (n + kStages - 1u) % kStages, at_most(n + kStages - 1u, steps - 1u) * kStep);
+          } else {
+#pragma unroll
+            for (int l = q * kHalf / kSpread; l < (q + 1) * kHalf / kSpread; ++l)
+              load(l, stage, at_most(n + kStages, steps - 1u) * kStep);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -258,16 +265,16 @@ __global__ __launch_bounds__(256, 1) void w8a8_tile_kernel(const uint8_t *__rest
     }
   };
 #pragma unroll
-  for (int i = 0; i < T::kLoads; ++i) load(i, 0u, 0u);
+  for (uint32_t n = 0; n < (uint32_t)kStages; ++n)
 #pragma unroll
-  for (int i = 0; i < kHalf; ++i) load(i, 1u, min(1u, steps - 1u) * KS);
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kHalf) : "memory");
+    for (int i = 0; i < (n + 1u < (uint32_t)kStages ? T::kLoads : kHalf); ++i) load(i, n, min(n, steps - 1u) * kStep);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kStages - 2) * T::kLoads + kHalf) : "memory");
   __syncthreads();
 #pragma unroll
   for (int t = 0; t < kReads; ++t) f[0][t] = read(0u, 0, t);
   for (uint32_t n = 0; n + 1u < steps; ++n) step(n, std::false_type{});
   step(steps - 1u, std::true_type{});
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way into LDS when the workgroup ends
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way into LDS any more
 
   // The results go through LDS, where the stages were (each wave's own part):
   // a lane has runs of four columns of one row, memory wants whole rows.  The
@@ -311,17 +318,62 @@ __global__ __launch_bounds__(256, 1) void w8a8_tile_kernel(const uint8_t *__rest
   }
 }
 
-template <int kTm, int kTn>
-hipError_t launch_tiles(const uint8_t *act, const uint8_t *w, const Scales &s, uint32_t kp, hipStream_t st) {
-  using T = Tile<kTm, kTn>;
-  constexpr int lds = 2 * T::kStage + (2 * T::BN + T::BM) * 4;  // two stages, scales and biases
-  const void *kernel = reinterpret_cast<const void *>(w8a8_tile_kernel<kTm, kTn>);
-  const hipError_t e = ensure_dynamic_lds(kernel, lds);
+// Place of a tile among tiles_m x tiles_n: eight rows of tiles at a time,
+// column by column, so that tiles that follow each other share operands.
+__device__ __forceinline__ void tile_place(uint32_t tile, uint32_t tiles_m, uint32_t tiles_n, uint32_t &tm, uint32_t &tn) {
+  const uint32_t group = tile / (8u * tiles_n), in = tile - group * 8u * tiles_n;
+  const uint32_t rows = min(8u, tiles_m - group * 8u);
+  tm = group * 8u + in % rows;
+  tn = in / rows;
+}
+
+// Workgroups go round the eight XCDs; each XCD takes a run of `each` tiles.
+// Workgroups from `whole` on take a quarter of a tile of 256 x 256 each.
+template <int kTm, int kTn, int kStep, int kStages, bool kQuarters>
+__global__ __launch_bounds__(256, 1) void w8a8_tile_kernel(const uint8_t *__restrict__ act,
+                                                           const uint8_t *__restrict__ w, Scales s, uint32_t kp,
+                                                           uint32_t tiles_m, uint32_t tiles_n, uint32_t whole) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  uint32_t tm, tn;
+  if (kQuarters && blockIdx.x >= whole) {
+    const uint32_t q = blockIdx.x - whole;
+    tile_place(whole + q / 4u, tiles_m, tiles_n, tm, tn);
+    const uint32_t m0 = tm * 256u + (q & 1u) * 128u, n0 = tn * 256u + (q >> 1 & 1u) * 128u;
+    if (m0 < s.m && n0 < s.n) run_tile<2, 2, 64, 4>(act, w, s, kp, m0, n0, lds);
+    return;
+  }
+  const uint32_t each = (whole + 7u) / 8u, tile = (blockIdx.x & 7u) * each + (blockIdx.x >> 3);
+  if (tile >= whole) return;
+  tile_place(tile, tiles_m, tiles_n, tm, tn);
+  run_tile<kTm, kTn, kStep, kStages>(act, w, s, kp, tm * 64u * kTm, tn * 64u * kTn, lds);
+}
+
+template <int kTm, int kTn, int kStep, int kStages, bool kQuarters>
+hipError_t launch_tile_kernel(const uint8_t *act, const uint8_t *w, const Scales &s, uint32_t kp, uint32_t tm, uint32_t tn,
+                              uint32_t whole, uint32_t blocks, hipStream_t st) {
+  constexpr int lds = Tile<kTm, kTn, kStep, kStages>::kLds;
+  const auto kernel = w8a8_tile_kernel<kTm, kTn, kStep, kStages, kQuarters>;
+  const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void *>(kernel), lds);
   if (e != hipSuccess) return e;
-  const uint32_t tm = (s.m + T::BM - 1u) / T::BM, tn = (s.n + T::BN - 1u) / T::BN;
-  hipLaunchKernelGGL((w8a8_tile_kernel<kTm, kTn>), dim3((tm * tn + 7u) / 8u * 8u), dim3(256), lds, st, act, w, s, kp, tm,
-                     tn);
+  hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), lds, st, act, w, s, kp, tm, tn, whole);
   return hipGetLastError();
+}
+
+template <int kTm, int kTn, int kStep, int kStages>
+hipError_t launch_tiles(const uint8_t *act, const uint8_t *w, const Scales &s, uint32_t kp, hipStream_t st) {
+  const uint32_t tm = (s.m + 64u * kTm - 1u) / (64u * kTm), tn = (s.n + 64u * kTn - 1u) / (64u * kTn);
+  return launch_tile_kernel<kTm, kTn, kStep, kStages, false>(act, w, s, kp, tm, tn, tm * tn, (tm * tn + 7u) / 8u * 8u, st);
+}
+
+// Tiles of 256 x 256, one per CU at a time.  Whole rounds of them, and what is
+// left over in quarters, if it is little enough for those to be quicker than
+// another round.
+hipError_t launch_big_tiles(const uint8_t *act, const uint8_t *w, const Scales &s, uint32_t kp, uint32_t cus, hipStream_t st) {
+  const uint32_t tm = (s.m + 255u) / 256u, tn = (s.n + 255u) / 256u, total = tm * tn;
+  const uint32_t whole = total / cus * cus, left = total - whole;
+  if (whole > 0 && left > 0 && 4u * left <= 2u * cus && whole % 8u == 0u)
+    return launch_tile_kernel<4, 4, 128, 2, true>(act, w, s, kp, tm, tn, whole, whole + 4u * left, st);
+  return launch_tile_kernel<4, 4, 128, 2, false>(act, w, s, kp, tm, tn, total, (total + 7u) / 8u * 8u, st);
 }
 
 template <int kNt, int kMt, int kWaves>
@@ -335,16 +387,19 @@ hipError_t launch_rows(const uint8_t *act, const uint8_t *w, const Scales &s, ui
 
 hipError_t launch_w8a8_gemm(const void *act, const void *w, const void *bias, void *out, uint32_t m, uint32_t n,
                             uint32_t k, hipStream_t st) {
-  const uint32_t kp = (k + KS - 1u) / KS * KS;
+  const uint32_t kp = (k + kRowPad - 1u) / kRowPad * kRowPad;
   const uint8_t *ap = static_cast<const uint8_t *>(act), *wp = static_cast<const uint8_t *>(w);
   const Scales s = {reinterpret_cast<const float *>(ap + (uint64_t)m * kp),
                     reinterpret_cast<const float *>(wp + (uint64_t)n * kp), static_cast<const uint16_t *>(bias),
                     static_cast<uint16_t *>(out), m, n};
+  int cus = 0;
+  const hipError_t e = device_cu_count(&cus);
+  if (e != hipSuccess) return e;
   if (m <= 16u) return launch_rows<1, 1, 4>(ap, wp, s, kp, st);
   if (m <= 32u) return launch_rows<1, 2, 4>(ap, wp, s, kp, st);
-  if (m <= 128u) return launch_tiles<1, 1>(ap, wp, s, kp, st);
-  if (m <= 512u) return launch_tiles<2, 2>(ap, wp, s, kp, st);
-  return launch_tiles<4, 4>(ap, wp, s, kp, st);
+  if (m <= 128u) return launch_tiles<1, 1, 64, 8>(ap, wp, s, kp, st);
+  if (m <= 512u) return launch_tiles<2, 2, 64, 4>(ap, wp, s, kp, st);
+  return launch_big_tiles(ap, wp, s, kp, (uint32_t)(cus > 0 ? cus : 1), st);
 }
 
 }  // namespace bqmm
