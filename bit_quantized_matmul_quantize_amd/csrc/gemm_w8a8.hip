@@ -52,84 +52,6 @@ __device__ __forceinline__ void store4(const Scales &s, uint32_t i, uint32_t j, 
   }
 }
 
-// ---- few rows ---------------------------------------------------------------------
-
-// A workgroup takes 16 kNt output columns and 16 kMt rows; its waves split k
-// and add their sums in LDS.  Both operands come straight from memory into
-// registers, 16 bytes a lane: 16 rows x 64 bytes are a matrix operand.
-template <int kNt, int kMt, int kWaves>
-__global__ __launch_bounds__(64 * kWaves) void w8a8_rows_kernel(const uint8_t *__restrict__ act,
-                                                                const uint8_t *__restrict__ w, Scales s, uint32_t kp) {
-  constexpr int kAhead = kNt + kMt <= 2 ? 8 : kNt + kMt <= 3 ? 6 : 4;  // steps of loads in flight
-  __shared__ v4i part[kWaves > 1 ? kWaves - 1 : 1][kNt * kMt][64];
-  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, r = lane & 15u, q = lane >> 4;
-  const uint32_t n0 = blockIdx.x * (16u * kNt), m0 = blockIdx.y * (16u * kMt);
-  const uint32_t steps = kp / 64u, s0 = steps * wave / kWaves, s1 = steps * (wave + 1u) / kWaves;
-  const uint8_t *wp[kNt], *ap[kMt];
-#pragma unroll
-  for (int t = 0; t < kNt; ++t) wp[t] = w + (uint64_t)min(n0 + 16u * t + r, s.n - 1u) * kp + q * 16u;
-#pragma unroll
-  for (int t = 0; t < kMt; ++t) ap[t] = act + (uint64_t)min(m0 + 16u * t + r, s.m - 1u) * kp + q * 16u;
-  v4i acc[kNt][kMt];
-#pragma unroll
-  for (int i = 0; i < kNt; ++i)
-#pragma unroll
-    for (int j = 0; j < kMt; ++j) acc[i][j] = v4i{0, 0, 0, 0};
-
-  uint32_t k = s0;
-  for (; k + kAhead <= s1; k += kAhead) {
-    v4i A[kAhead][kNt], B[kAhead][kMt];
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d) {
-#pragma unroll
-      for (int t = 0; t < kNt; ++t) A[d][t] = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(wp[t] + (k + d) * 64u));
-#pragma unroll
-      for (int t = 0; t < kMt; ++t) B[d][t] = *reinterpret_cast<const v4i *>(ap[t] + (k + d) * 64u);
-    }
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d)
-#pragma unroll
-      for (int i = 0; i < kNt; ++i)
-#pragma unroll
-        for (int j = 0; j < kMt; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[d][i], B[d][j], acc[i][j], 0, 0, 0);
-  }
-  for (; k < s1; ++k)
-#pragma unroll
-    for (int i = 0; i < kNt; ++i) {
-      const v4i A = *reinterpret_cast<const v4i *>(wp[i] + k * 64u);
-#pragma unroll
-      for (int j = 0; j < kMt; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(A, *reinterpret_cast<const v4i *>(ap[j] + k * 64u), acc[i][j], 0, 0, 0);
-    }
-
-  if constexpr (kWaves > 1) {
-    if (wave > 0) {
-#pragma unroll
-      for (int i = 0; i < kNt; ++i)
-#pragma unroll
-        for (int j = 0; j < kMt; ++j) part[wave - 1][i * kMt + j][lane] = acc[i][j];
-    }
-    __syncthreads();
-    if (wave > 0) return;
-#pragma unroll
-    for (int v = 0; v < kWaves - 1; ++v)
-#pragma unroll
-      for (int i = 0; i < kNt; ++i)
-#pragma unroll
-        for (int j = 0; j < kMt; ++j) acc[i][j] += part[v][i * kMt + j][lane];
-  }
-#pragma unroll
-  for (int j = 0; j < kMt; ++j) {
-    const uint32_t mm = m0 + 16u * j + r;
-    const float sa = s.sa[min(mm, s.m - 1u)];
-#pragma unroll
-    for (int i = 0; i < kNt; ++i)
-      store4(s, mm, n0 + 16u * i + q * 4u, acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], sa);
-  }
-}
-
-// ---- tiles ------------------------------------------------------------------------
-
 // 16 bytes a lane straight from memory into LDS: lane i's go to the wave's
 // destination + 16 i.  Not a builtin, because the compiler waits for all such
 // loads before any read of LDS; here the kernel waits itself, where a stage is
@@ -139,6 +61,96 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, const
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
                : "memory");
 }
+
+// Waits until at most n of a wave's loads into LDS are on their way (for the n
+// of a unit of few rows: 5 to 8).
+__device__ __forceinline__ void wait_for_loads(uint32_t n) {
+  switch (n) {
+    case 8u: asm volatile("s_waitcnt vmcnt(8)" ::: "memory"); return;
+    case 7u: asm volatile("s_waitcnt vmcnt(7)" ::: "memory"); return;
+    case 6u: asm volatile("s_waitcnt vmcnt(6)" ::: "memory"); return;
+    case 5u: asm volatile("s_waitcnt vmcnt(5)" ::: "memory"); return;
+    default: asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+}
+
+// ---- few rows ---------------------------------------------------------------------
+
+// At most 16 rows.  A workgroup takes 16 output columns; its waves split k in
+// units of 256 bytes and add their sums in LDS.  A wave brings its units of the
+// weight rows and the activations straight into LDS, two at a time and
+// without a barrier (nobody else reads them), 256 consecutive bytes per row:
+// memory serves such runs, while operands loaded as the matrix cores want them
+// (16 rows x 64 bytes at once) stream at two thirds of the rate.  The 16 pieces
+// of a row lie in the order piece ^ (row % 16), which spreads a column of
+// pieces over the banks.
+constexpr uint32_t kUnit = 256;  // bytes of k
+
+template <int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void w8a8_rows_kernel(const uint8_t *__restrict__ act,
+                                                                const uint8_t *__restrict__ w, Scales s, uint32_t kp,
+                                                                uint32_t stages) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t r = lane & 15u, q = lane >> 4;
+  const uint32_t n0 = blockIdx.x * 16u;
+  const uint32_t units = (kp + kUnit - 1u) / kUnit, u0 = units * wave / kWaves, u1 = units * (wave + 1u) / kWaves;
+  const uint32_t act_loads = (s.m + 3u) / 4u, stage_bytes = (4u + act_loads) * 1024u;
+  uint8_t *mine = lds + wave * stages * stage_bytes;
+  const uint32_t mine0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)mine;
+
+  // a load: 4 rows of 256 bytes.  kp is a multiple of 128: of a last half unit
+  // the second half takes the first half's bytes again, and is not used.
+  const uint8_t *wbase = w + (uint64_t)n0 * kp;
+  auto load = [&](uint32_t u, uint32_t stage) {
+    const uint32_t in_unit = min(kp - u * kUnit, kUnit);
+    const uint32_t at = mine0 + stage * stage_bytes;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+      const uint32_t row = 4u * i + q, piece = (r ^ row) * 16u;
+      load_to_lds(at + i * 1024u, min(row, s.n - 1u - n0) * kp + (piece < in_unit ? piece : piece - 128u), wbase + u * kUnit);
+    }
+    for (uint32_t i = 0; i < act_loads; ++i) {
+      const uint32_t row = 4u * i + q, piece = (r ^ row) * 16u;
+      load_to_lds(at + (4u + i) * 1024u, min(row, s.m - 1u) * kp + (piece < in_unit ? piece : piece - 128u), act + u * kUnit);
+    }
+  };
+
+  v4i acc = {0, 0, 0, 0};
+  // rows of the activations past the loaded ones take the first: their columns of the result are not stored
+  const uint8_t *w_at = mine + r * kUnit, *a_at = mine + 4096u + (r < 4u * act_loads ? r : 0u) * kUnit;
+  const uint32_t a_row = r < 4u * act_loads ? r : 0u;
+  for (uint32_t u = u0; u < min(u0 + stages, u1); ++u) load(u, u - u0);
+  uint32_t stage = 0;
+  for (uint32_t u = u0; u < u1; ++u) {
+    // this unit has arrived; the next may be on its way
+    wait_for_loads(stages == 2u && u1 - u >= 2u ? 4u + act_loads : 0u);
+    const uint32_t parts = min(kp - u * kUnit, kUnit) / 64u;
+    v4i A[4], B[4];
+#pragma unroll
+    for (uint32_t d = 0; d < 4; ++d) {
+      A[d] = *reinterpret_cast<const v4i *>(w_at + stage * stage_bytes + ((d * 4u + q) ^ r) * 16u);
+      B[d] = *reinterpret_cast<const v4i *>(a_at + stage * stage_bytes + ((d * 4u + q) ^ a_row) * 16u);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the stage is filled again
+    if (u + stages < u1) load(u + stages, stage);
+#pragma unroll
+    for (uint32_t d = 0; d < 4; ++d)
+      if (d < 2u || parts == 4u) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[d], B[d], acc, 0, 0, 0);
+    stage = stage + 1u == stages ? 0u : stage + 1u;
+  }
+
+  __syncthreads();  // the stages' place takes the sums
+  v4i *part = reinterpret_cast<v4i *>(lds);
+  part[threadIdx.x] = acc;
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int v = 1; v < kWaves; ++v) acc += part[64 * v + lane];
+  store4(s, r, n0 + q * 4u, acc[0], acc[1], acc[2], acc[3], s.sa[min(r, s.m - 1u)]);
+}
+
+// ---- tiles ------------------------------------------------------------------------
 
 // min(a, b) that the compiler does not see through: it would cut the loop over
 // the steps in three where the min changes sides, and the copies spill.
@@ -376,10 +388,17 @@ hipError_t launch_big_tiles(const uint8_t *act, const uint8_t *w, const Scales &
   return launch_tile_kernel<4, 4, 128, 2, false>(act, w, s, kp, tm, tn, total, (total + 7u) / 8u * 8u, st);
 }
 
-template <int kNt, int kMt, int kWaves>
+template <int kWaves>
 hipError_t launch_rows(const uint8_t *act, const uint8_t *w, const Scales &s, uint32_t kp, hipStream_t st) {
-  const dim3 grid((s.n + 16u * kNt - 1u) / (16u * kNt), (s.m + 16u * kMt - 1u) / (16u * kMt));
-  hipLaunchKernelGGL((w8a8_rows_kernel<kNt, kMt, kWaves>), grid, dim3(64 * kWaves), 0, st, act, w, s, kp);
+  const uint32_t units = (kp + kUnit - 1u) / kUnit, per_wave = (units + kWaves - 1u) / kWaves;
+  // Two units at a time: a third measured 1 to 5% slower (fewer workgroups fit a CU).
+  const uint32_t stages = per_wave < 2u ? per_wave : 2u;
+  const uint32_t need = kWaves * stages * (4u + (s.m + 3u) / 4u) * 1024u;
+  const uint32_t lds = need > 1024u * kWaves ? need : 1024u * kWaves;  // the stages, then a sum per lane
+  const auto kernel = w8a8_rows_kernel<kWaves>;
+  const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void *>(kernel), 65536 * 2);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, dim3((s.n + 15u) / 16u), dim3(64 * kWaves), lds, st, act, w, s, kp, stages);
   return hipGetLastError();
 }
 
@@ -395,8 +414,9 @@ hipError_t launch_w8a8_gemm(const void *act, const void *w, const void *bias, vo
   int cus = 0;
   const hipError_t e = device_cu_count(&cus);
   if (e != hipSuccess) return e;
-  if (m <= 16u) return launch_rows<1, 1, 4>(ap, wp, s, kp, st);
-  if (m <= 32u) return launch_rows<1, 2, 4>(ap, wp, s, kp, st);
+  // Few columns leave most CUs without a workgroup: eight waves then, four
+  // otherwise (n = 1000, k = 5120: 4.0 us against 4.5; n = 17408: 18.1 against 17.5).
+  if (m <= 16u) return n <= 16u * 128u ? launch_rows<8>(ap, wp, s, kp, st) : launch_rows<4>(ap, wp, s, kp, st);
   if (m <= 128u) return launch_tiles<1, 1, 64, 8>(ap, wp, s, kp, st);
   if (m <= 512u) return launch_tiles<2, 2, 64, 4>(ap, wp, s, kp, st);
   return launch_big_tiles(ap, wp, s, kp, (uint32_t)(cus > 0 ? cus : 1), st);
