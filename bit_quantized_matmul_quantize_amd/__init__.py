@@ -90,11 +90,21 @@ def _check(status: int):
         raise BqmmError(status, lib().bq_last_error().decode())
 
 
+_current_stream = None
+
+
 def _stream(stream):
+    """The given stream, or torch's current one, as an address."""
+    global _current_stream
     if stream is not None:
-        return ctypes.c_void_p(int(stream))
-    import torch
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return int(stream)
+    if _current_stream is None:
+        import torch
+        # the address alone: a torch.cuda.Stream object costs 2 us per call, as much as the launch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _current_stream = ((lambda: raw(torch.cuda.current_device())) if raw
+                           else (lambda: torch.cuda.current_stream().cuda_stream))
+    return _current_stream()
 
 
 def _ptr(t):
@@ -104,19 +114,26 @@ def _ptr(t):
         raise ValueError("expected a device tensor")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+_BF16, _U8 = ("torch.bfloat16", "torch.int16", "torch.uint16"), ("torch.uint8",)
+_kinds = {}  # dtype -> its name (str() of a dtype builds it anew)
+
+
+def _kind(t):
+    d = t.dtype
+    return _kinds.get(d) or _kinds.setdefault(d, str(d))
 
 
 def _bf16(t, what):
-    import torch
-    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+    if _kind(t) not in _BF16:
         raise TypeError(f"{what}: expected bfloat16 data, got {t.dtype}")
     return t
 
 
 def _u8(t, what):
-    import torch
-    if t.dtype != torch.uint8:
+    if _kind(t) not in _U8:
         raise TypeError(f"{what}: expected uint8 bytes, got {t.dtype}")
     return t
 
@@ -143,7 +160,7 @@ def q4k_weight_bytes(n: int, k: int) -> int:
 # tensors on one device.
 
 def _nbytes(t) -> int:
-    return t.numel() * t.element_size()
+    return t.nbytes
 
 
 def _need(t, nbytes: int, what: str):
@@ -153,9 +170,9 @@ def _need(t, nbytes: int, what: str):
 
 
 def _same_device(*tensors):
-    devs = {t.device for t in tensors if t is not None and t.is_cuda}
+    devs = {t.get_device() for t in tensors if t is not None and t.is_cuda}
     if len(devs) > 1:
-        raise ValueError(f"tensors on different devices: {sorted(str(d) for d in devs)}")
+        raise ValueError(f"tensors on different devices: {['cuda:%d' % d for d in sorted(devs)]}")
 
 
 def _ptrs(*tensors):
@@ -301,7 +318,7 @@ def silu_mul_bf16(gate, up, out, count: int | None = None, stream=None):
 
 
 def int8_rows_bytes(rows: int, k: int) -> int:
-    return int(lib().int8_rows_bytes(rows, k))
+    return rows * ((k + 127) // 128 * 128 + 4) if k <= 1 << 30 else 0
 
 
 def gated_delta_rule_workspace_bytes(tokens: int, count: int, hk: int, hv: int, dk: int, dv: int) -> int:
@@ -347,51 +364,43 @@ def w8a8_gemm(act_i8, w_i8, out, m: int, n: int, k: int, bias=None, stream=None)
     _check(lib().w8a8_gemm(*_ptrs(act_i8, w_i8, bias, out), m, n, k, _stream(stream)))
 
 
-def _typed(t, dtype, shape, what):
-    """A contiguous tensor of this type and shape (None passes through)."""
-    if t is None:
-        return t
-    if t.dtype != dtype:
-        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+def _typed(t, kind, shape, what):
+    """A tensor of this type and shape (None passes through)."""
+    if t is not None:
+        if _kind(t) != kind:
+            raise TypeError(f"{what}: expected {kind}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
     return t
 
 
 def _heads(t, shape, what):
     """A [tokens, heads, d] bf16 tensor, its last dimension contiguous: (token stride, head stride)."""
-    _bf16(t, what)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
-    token, head, one = t.stride()
-    if (shape[2] > 1 and one != 1) or token < 0 or head < 0:
+    token, head, one = _bf16(t, what).stride()
+    if one != 1 and shape[2] > 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
     return token, head
 
 
 def _delta(fn, q, k, v, g, beta, out, state, starts, slots, fresh, workspace, scale, l2norm, stream):
-    import torch
     if q.dim() != 3 or v.dim() != 3 or state.dim() != 4 or starts.dim() != 1 or starts.numel() < 1:
         raise ValueError("expected q, k, v as [tokens, heads, d], state as [slots, hv, dk, dv], starts as [count + 1]")
-    (tokens, hk, dk), (hv, dv), count = q.shape, v.shape[1:], starts.numel() - 1
-    _typed(g, torch.float32, (tokens, hv), "g")
-    _typed(beta, torch.float32, (tokens, hv), "beta")
-    _typed(out, torch.bfloat16, (tokens, hv, dv), "out")
-    _typed(state, torch.float32, (state.shape[0], hv, dk, dv), "state")
-    _typed(starts, torch.int32, (count + 1,), "starts")
-    _typed(slots, torch.int32, (count,), "slots")
-    _typed(fresh, torch.uint8, (count,), "fresh")
-    strides = [*_heads(q, (tokens, hk, dk), "q"), *_heads(k, (tokens, hk, dk), "k"), *_heads(v, (tokens, hv, dv), "v")]
+    (tokens, hk, dk), (_, hv, dv), places, count = q.shape, v.shape, state.shape[0], starts.shape[0] - 1
+    strides = (*_heads(q, (tokens, hk, dk), "q"), *_heads(k, (tokens, hk, dk), "k"), *_heads(v, (tokens, hv, dv), "v"))
+    rest = (_typed(g, "torch.float32", (tokens, hv), "g"), _typed(beta, "torch.float32", (tokens, hv), "beta"),
+            _typed(out, "torch.bfloat16", (tokens, hv, dv), "out"),
+            _typed(state, "torch.float32", (places, hv, dk, dv), "state"),
+            _typed(starts, "torch.int32", (count + 1,), "starts"), _typed(slots, "torch.int32", (count,), "slots"),
+            _typed(fresh, "torch.uint8", (count,), "fresh"), *workspace)
     if not (q.is_cuda and k.is_cuda and v.is_cuda):
         raise ValueError("expected a device tensor")
-    _same_device(q, k, v, g, beta, out, state, starts, slots, fresh, *workspace)
-    if slots is None and state.shape[0] < count:
-        raise ValueError(f"state: {state.shape[0]} slots for {count} sequences")
-    rest = [_ptr(t) for t in (g, beta, out, state, starts, slots, fresh)]
-    room = [x for w in workspace for x in (_ptr(w), _nbytes(w))]
-    scale = dk ** -0.5 if scale is None else scale
-    _check(fn(*(ctypes.c_void_p(t.data_ptr()) for t in (q, k, v)), *rest, *room, tokens, count, state.shape[0],
-              hk, hv, dk, dv, *strides, scale, int(bool(l2norm)), _stream(stream)))
+    _same_device(q, k, v, *rest)
+    if slots is None and places < count:
+        raise ValueError(f"state: {places} slots for {count} sequences")
+    _check(fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), *map(_ptr, rest), *map(_nbytes, workspace), tokens, count, places,
+              hk, hv, dk, dv, *strides, dk ** -0.5 if scale is None else scale, 1 if l2norm else 0, _stream(stream)))
 
 
 def gated_delta_rule_recurrent(q, k, v, g, beta, out, state, starts, slots=None, fresh=None, l2norm: bool = True,
