@@ -76,7 +76,7 @@ __device__ __forceinline__ void wait_for_loads(uint32_t n) {
 
 // ---- few rows ---------------------------------------------------------------------
 
-// At most 16 rows.  A workgroup takes 16 output columns; its waves split k in
+// A workgroup takes 16 output columns and at most 16 rows; its waves split k in
 // units of 256 bytes and add their sums in LDS.  A wave brings its units of the
 // weight rows and the activations straight into LDS, two at a time and
 // without a barrier (nobody else reads them), 256 consecutive bytes per row:
@@ -93,15 +93,16 @@ __global__ __launch_bounds__(64 * kWaves) void w8a8_rows_kernel(const uint8_t *_
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t r = lane & 15u, q = lane >> 4;
-  const uint32_t n0 = blockIdx.x * 16u;
+  // the row blocks of a column block follow each other: they share its weight rows
+  const uint32_t row_blocks = (s.m + 15u) / 16u, n0 = blockIdx.x / row_blocks * 16u, m0 = blockIdx.x % row_blocks * 16u;
   const uint32_t units = (kp + kUnit - 1u) / kUnit, u0 = units * wave / kWaves, u1 = units * (wave + 1u) / kWaves;
-  const uint32_t act_loads = (s.m + 3u) / 4u, stage_bytes = (4u + act_loads) * 1024u;
+  const uint32_t act_loads = (min(s.m - m0, 16u) + 3u) / 4u, stage_bytes = (4u + act_loads) * 1024u;
   uint8_t *mine = lds + wave * stages * stage_bytes;
   const uint32_t mine0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)mine;
 
   // a load: 4 rows of 256 bytes.  kp is a multiple of 128: of a last half unit
   // the second half takes the first half's bytes again, and is not used.
-  const uint8_t *wbase = w + (uint64_t)n0 * kp;
+  const uint8_t *wbase = w + (uint64_t)n0 * kp, *abase = act + (uint64_t)m0 * kp;
   auto load = [&](uint32_t u, uint32_t stage) {
     const uint32_t in_unit = min(kp - u * kUnit, kUnit);
     const uint32_t at = mine0 + stage * stage_bytes;
@@ -112,7 +113,7 @@ __global__ __launch_bounds__(64 * kWaves) void w8a8_rows_kernel(const uint8_t *_
     }
     for (uint32_t i = 0; i < act_loads; ++i) {
       const uint32_t row = 4u * i + q, piece = (r ^ row) * 16u;
-      load_to_lds(at + (4u + i) * 1024u, min(row, s.m - 1u) * kp + (piece < in_unit ? piece : piece - 128u), act + u * kUnit);
+      load_to_lds(at + (4u + i) * 1024u, min(row, s.m - 1u - m0) * kp + (piece < in_unit ? piece : piece - 128u), abase + u * kUnit);
     }
   };
 
@@ -147,7 +148,7 @@ __global__ __launch_bounds__(64 * kWaves) void w8a8_rows_kernel(const uint8_t *_
   if (wave > 0) return;
 #pragma unroll
   for (int v = 1; v < kWaves; ++v) acc += part[64 * v + lane];
-  store4(s, r, n0 + q * 4u, acc[0], acc[1], acc[2], acc[3], s.sa[min(r, s.m - 1u)]);
+  store4(s, m0 + r, n0 + q * 4u, acc[0], acc[1], acc[2], acc[3], s.sa[min(m0 + r, s.m - 1u)]);
 }
 
 // ---- tiles ------------------------------------------------------------------------
@@ -161,9 +162,10 @@ __device__ __forceinline__ uint32_t at_most(uint32_t a, uint32_t b) {
 }
 
 // Four waves, two by two, each of 32 kTm rows x 32 kTn columns: 64 kTm x 64 kTn
-// outputs.  k runs in steps of kStep (64 or 128) bytes through kStages LDS
-// stages.  The 16-byte pieces of a row lie in the order piece ^ f(row), which
-// spreads a column of pieces over the banks; the loads that fill the stage
+// outputs.  k runs in steps of 128 bytes (whole cache lines: with 64 the
+// weight streams from memory a tenth to a quarter slower) through kStages LDS
+// stages.  The eight 16-byte pieces of a row lie in the order piece ^ (row % 8),
+// which spreads a column of pieces over the banks; the loads that fill the stage
 // write LDS in order and take the pieces from memory in that order instead.
 //
 // Per step once for each 32 bytes of k: its matrix products, and between them
@@ -171,7 +173,9 @@ __device__ __forceinline__ uint32_t at_most(uint32_t a, uint32_t b) {
 // read: the waves meet once, then the next stage's first reads and the loads
 // that refill this one go between the products too (half of them; the other
 // half goes with the first products of the step after).
-template <int kTm, int kTn, int kStep, int kStages>
+constexpr uint32_t kStep = 128;  // bytes of k per step
+
+template <int kTm, int kTn, int kStages>
 struct Tile {
   static constexpr uint32_t BM = 64 * kTm, BN = 64 * kTn;
   static constexpr uint32_t kStage = (BM + BN) * kStep;
@@ -185,22 +189,20 @@ struct __attribute__((packed, aligned(2))) Row8 {  // eight results of a row, wh
   uint32_t w[4];
 };
 
-template <int kTm, int kTn, int kStep, int kStages>
+template <int kTm, int kTn, int kStages>
 __device__ __forceinline__ void run_tile(const uint8_t *act, const uint8_t *w, const Scales &s, uint32_t kp, uint32_t m0,
                                          uint32_t n0, uint8_t *lds) {
-  using T = Tile<kTm, kTn, kStep, kStages>;
+  using T = Tile<kTm, kTn, kStages>;
   constexpr uint32_t kInRow = kStep / 16;  // pieces of a row
   const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t wn = wave & 1u, wm = wave >> 1, r = lane & 31u, half = lane >> 5;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
-  // 256 bytes of LDS (all banks) hold 2 rows of 128 bytes or 4 of 64
-  auto spread = [](uint32_t row) -> uint32_t { return kStep == 128 ? row & 7u : row >> 2 & 3u; };
 
   // what this wave loads: kRowsAtOnce rows from row (wave + 4 i) kRowsAtOnce on of the stage, weight rows first
   const uint8_t *wbase = w + (uint64_t)n0 * kp, *abase = act + (uint64_t)m0 * kp;
   uint32_t off[T::kLoads];
   {
-    const uint32_t lr = lane / kInRow, piece = ((lane % kInRow) ^ spread(lr)) * 16u;
+    const uint32_t lr = lane / kInRow, piece = ((lane % kInRow) ^ (lr & 7u)) * 16u;
 #pragma unroll
     for (uint32_t i = 0; i < (uint32_t)T::kLoads; ++i) {
       const uint32_t row = T::kRowsAtOnce * (wave + 4u * i) + lr;
@@ -214,7 +216,7 @@ __device__ __forceinline__ void run_tile(const uint8_t *act, const uint8_t *w, c
   constexpr int kParts = kStep / 32;
   uint32_t at[kParts];
 #pragma unroll
-  for (uint32_t kk = 0; kk < (uint32_t)kParts; ++kk) at[kk] = r * kStep + (((kk * 2u + half) ^ spread(r)) * 16u);
+  for (uint32_t kk = 0; kk < (uint32_t)kParts; ++kk) at[kk] = r * kStep + (((kk * 2u + half) ^ (r & 7u)) * 16u);
   auto read = [&](uint32_t stage, int kk, int t) -> v4i {  // t < kTn: weight rows, then activation rows
     const uint32_t row = t < kTn ? wn * (32u * kTn) + 32u * t : T::BN + wm * (32u * kTm) + 32u * (t - kTn);
     return *reinterpret_cast<const v4i *>(lds + stage * T::kStage + row * kStep + at[kk]);
@@ -341,7 +343,7 @@ __device__ __forceinline__ void tile_place(uint32_t tile, uint32_t tiles_m, uint
 
 // Workgroups go round the eight XCDs; each XCD takes a run of `each` tiles.
 // Workgroups from `whole` on take a quarter of a tile of 256 x 256 each.
-template <int kTm, int kTn, int kStep, int kStages, bool kQuarters>
+template <int kTm, int kTn, int kStages, bool kQuarters>
 __global__ __launch_bounds__(256, 1) void w8a8_tile_kernel(const uint8_t *__restrict__ act,
                                                            const uint8_t *__restrict__ w, Scales s, uint32_t kp,
                                                            uint32_t tiles_m, uint32_t tiles_n, uint32_t whole) {
@@ -351,41 +353,44 @@ __global__ __launch_bounds__(256, 1) void w8a8_tile_kernel(const uint8_t *__rest
     const uint32_t q = blockIdx.x - whole;
     tile_place(whole + q / 4u, tiles_m, tiles_n, tm, tn);
     const uint32_t m0 = tm * 256u + (q & 1u) * 128u, n0 = tn * 256u + (q >> 1 & 1u) * 128u;
-    if (m0 < s.m && n0 < s.n) run_tile<2, 2, 64, 4>(act, w, s, kp, m0, n0, lds);
+    if (m0 < s.m && n0 < s.n) run_tile<2, 2, 4>(act, w, s, kp, m0, n0, lds);
     return;
   }
   const uint32_t each = (whole + 7u) / 8u, tile = (blockIdx.x & 7u) * each + (blockIdx.x >> 3);
   if (tile >= whole) return;
   tile_place(tile, tiles_m, tiles_n, tm, tn);
-  run_tile<kTm, kTn, kStep, kStages>(act, w, s, kp, tm * 64u * kTm, tn * 64u * kTn, lds);
+  run_tile<kTm, kTn, kStages>(act, w, s, kp, tm * 64u * kTm, tn * 64u * kTn, lds);
 }
 
-template <int kTm, int kTn, int kStep, int kStages, bool kQuarters>
+template <int kTm, int kTn, int kStages, bool kQuarters>
 hipError_t launch_tile_kernel(const uint8_t *act, const uint8_t *w, const Scales &s, uint32_t kp, uint32_t tm, uint32_t tn,
                               uint32_t whole, uint32_t blocks, hipStream_t st) {
-  constexpr int lds = Tile<kTm, kTn, kStep, kStages>::kLds;
-  const auto kernel = w8a8_tile_kernel<kTm, kTn, kStep, kStages, kQuarters>;
+  constexpr int lds = Tile<kTm, kTn, kStages>::kLds;
+  const auto kernel = w8a8_tile_kernel<kTm, kTn, kStages, kQuarters>;
   const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void *>(kernel), lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), lds, st, act, w, s, kp, tm, tn, whole);
   return hipGetLastError();
 }
 
-template <int kTm, int kTn, int kStep, int kStages>
+template <int kTm, int kTn, int kStages>
 hipError_t launch_tiles(const uint8_t *act, const uint8_t *w, const Scales &s, uint32_t kp, hipStream_t st) {
   const uint32_t tm = (s.m + 64u * kTm - 1u) / (64u * kTm), tn = (s.n + 64u * kTn - 1u) / (64u * kTn);
-  return launch_tile_kernel<kTm, kTn, kStep, kStages, false>(act, w, s, kp, tm, tn, tm * tn, (tm * tn + 7u) / 8u * 8u, st);
+  return launch_tile_kernel<kTm, kTn, kStages, false>(act, w, s, kp, tm, tn, tm * tn, (tm * tn + 7u) / 8u * 8u, st);
 }
 
 // Tiles of 256 x 256, one per CU at a time.  Whole rounds of them, and what is
-// left over in quarters, if it is little enough for those to be quicker than
-// another round.
+// left over in quarters where at most two rounds of those suffice (4096 x 17408,
+// k = 5120: 64 of 1088 tiles are left over; 381 us, and 422 with a fifth round).
+bool quarters(uint32_t total, uint32_t cus) {
+  const uint32_t left = total % cus;
+  return total > cus && cus % 8u == 0u && left > 0u && 2u * left <= cus;
+}
 hipError_t launch_big_tiles(const uint8_t *act, const uint8_t *w, const Scales &s, uint32_t kp, uint32_t cus, hipStream_t st) {
-  const uint32_t tm = (s.m + 255u) / 256u, tn = (s.n + 255u) / 256u, total = tm * tn;
-  const uint32_t whole = total / cus * cus, left = total - whole;
-  if (whole > 0 && left > 0 && 4u * left <= 2u * cus && whole % 8u == 0u)
-    return launch_tile_kernel<4, 4, 128, 2, true>(act, w, s, kp, tm, tn, whole, whole + 4u * left, st);
-  return launch_tile_kernel<4, 4, 128, 2, false>(act, w, s, kp, tm, tn, total, (total + 7u) / 8u * 8u, st);
+  const uint32_t tm = (s.m + 255u) / 256u, tn = (s.n + 255u) / 256u, total = tm * tn, whole = total / cus * cus;
+  if (quarters(total, cus))
+    return launch_tile_kernel<4, 4, 2, true>(act, w, s, kp, tm, tn, whole, whole + 4u * (total - whole), st);
+  return launch_tile_kernel<4, 4, 2, false>(act, w, s, kp, tm, tn, total, (total + 7u) / 8u * 8u, st);
 }
 
 template <int kWaves>
@@ -393,13 +398,43 @@ hipError_t launch_rows(const uint8_t *act, const uint8_t *w, const Scales &s, ui
   const uint32_t units = (kp + kUnit - 1u) / kUnit, per_wave = (units + kWaves - 1u) / kWaves;
   // Two units at a time: a third measured 1 to 5% slower (fewer workgroups fit a CU).
   const uint32_t stages = per_wave < 2u ? per_wave : 2u;
-  const uint32_t need = kWaves * stages * (4u + (s.m + 3u) / 4u) * 1024u;
+  const uint32_t rows = s.m < 16u ? s.m : 16u, need = kWaves * stages * (4u + (rows + 3u) / 4u) * 1024u;
   const uint32_t lds = need > 1024u * kWaves ? need : 1024u * kWaves;  // the stages, then a sum per lane
   const auto kernel = w8a8_rows_kernel<kWaves>;
   const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void *>(kernel), 65536 * 2);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kernel, dim3((s.n + 15u) / 16u), dim3(64 * kWaves), lds, st, act, w, s, kp, stages);
+  hipLaunchKernelGGL(kernel, dim3((s.n + 15u) / 16u * ((s.m + 15u) / 16u)), dim3(64 * kWaves), lds, st, act, w, s, kp, stages);
   return hipGetLastError();
+}
+
+// What the forms take, in microseconds, as measured over m = 16 to 4096, n = 64
+// to 17408, k = 200 to 5120: a fixed part, and per 128 bytes of k a part for
+// each round of workgroups that fills the chip (a smaller one for a last round
+// that leaves half the CUs, or half of two workgroups' places, empty).
+struct Form {
+  uint32_t bm, bn, per_cu;
+  float base, round, half;
+};
+enum { kRows, kT11, kT12, kT21, kT22, kT22Pair, kBig, kForms };
+constexpr Form kFormCosts[kForms] = {
+    {16, 16, 0, 2.6f, 0.0003f, 0.0f},  // per workgroup: m 64, n 1000, k 1000: 3.2, against 5.0 of the next
+    {64, 64, 2, 3.2f, 0.43f, 0.245f},  // 256 x 4096, k 4096: 11.2, 13.5 of the next two
+    {64, 128, 1, 3.8f, 0.37f, 0.32f},  // 512 x 4096, k 4096: 15.7, 16.9 of 64 x 64, 18.4 of 128 x 128
+    {128, 64, 1, 3.8f, 0.37f, 0.32f},
+    {128, 128, 1, 4.0f, 0.62f, 0.43f},  // four stages; 1024 x 4096, k 4096: 24.0, 28.2 with two, 30.0 of 64 x 128
+    {128, 128, 2, 4.0f, 1.13f, 0.79f},  // two stages, two workgroups a CU; 2048 x 4096, k 4096: 39.1, 46.8 with four, 53.8 of 256 x 256
+    {256, 256, 1, 6.0f, 2.2f, 2.2f},    // 4096 x 4096, k 4096: 75.6, 86.4 of 128 x 128
+};
+
+float cost(int form, uint32_t m, uint32_t n, uint32_t steps, uint32_t cus) {
+  const Form &f = kFormCosts[form];
+  const uint64_t tiles = (uint64_t)((m + f.bm - 1u) / f.bm) * ((n + f.bn - 1u) / f.bn);
+  if (form == kRows) return f.base + f.round * (float)tiles * (float)steps;
+  const uint64_t slots = (uint64_t)f.per_cu * cus, rounds = tiles / slots, left = tiles % slots;
+  float last = left == 0u ? 0.0f : 2u * left <= slots ? f.half : f.round;
+  if (form == kBig && tiles <= 0xFFFFFFFFu && quarters((uint32_t)tiles, cus))
+    last = 4u * left <= cus ? kFormCosts[kT22].round : 2.0f * kFormCosts[kT22].round;
+  return f.base + (float)steps * ((float)rounds * f.round + last);
 }
 
 }  // namespace
@@ -414,12 +449,24 @@ hipError_t launch_w8a8_gemm(const void *act, const void *w, const void *bias, vo
   int cus = 0;
   const hipError_t e = device_cu_count(&cus);
   if (e != hipSuccess) return e;
-  // Few columns leave most CUs without a workgroup: eight waves then, four
-  // otherwise (n = 1000, k = 5120: 4.0 us against 4.5; n = 17408: 18.1 against 17.5).
-  if (m <= 16u) return n <= 16u * 128u ? launch_rows<8>(ap, wp, s, kp, st) : launch_rows<4>(ap, wp, s, kp, st);
-  if (m <= 128u) return launch_tiles<1, 1, 64, 8>(ap, wp, s, kp, st);
-  if (m <= 512u) return launch_tiles<2, 2, 64, 4>(ap, wp, s, kp, st);
-  return launch_big_tiles(ap, wp, s, kp, (uint32_t)(cus > 0 ? cus : 1), st);
+  const uint32_t c = (uint32_t)(cus > 0 ? cus : 1), steps = kp / kStep;
+  int form = kRows;
+  if (m > 16u)
+    for (int f = kRows + 1; f < kForms; ++f)
+      if (cost(f, m, n, steps, c) < cost(form, m, n, steps, c)) form = f;
+  switch (form) {
+    case kRows:
+      // Few workgroups leave most CUs idle: eight waves each then, four otherwise (one row, k = 5120: n = 1000
+      // takes 4.0 us against 4.5, n = 17408 18.1 against 17.5).
+      return (m + 15u) / 16u * ((n + 15u) / 16u) <= 128u ? launch_rows<8>(ap, wp, s, kp, st)
+                                                          : launch_rows<4>(ap, wp, s, kp, st);
+    case kT11: return launch_tiles<1, 1, 4>(ap, wp, s, kp, st);
+    case kT12: return launch_tiles<1, 2, 4>(ap, wp, s, kp, st);
+    case kT21: return launch_tiles<2, 1, 4>(ap, wp, s, kp, st);
+    case kT22: return launch_tiles<2, 2, 4>(ap, wp, s, kp, st);
+    case kT22Pair: return launch_tiles<2, 2, 2>(ap, wp, s, kp, st);
+    default: return launch_big_tiles(ap, wp, s, kp, c, st);
+  }
 }
 
 }  // namespace bqmm
