@@ -31,9 +31,9 @@ struct __attribute__((packed, aligned(2))) Bf16s {
 };
 
 // N bf16 values from row r0 of dk; rows past dk are zero.
-template <int N>
+template <int N, bool kWhole>
 __device__ __forceinline__ void load_rows(const uint16_t *p, uint32_t r0, uint32_t dk, float (&v)[N]) {
-  if (r0 + N <= dk) {
+  if (kWhole || r0 + N <= dk) {
     const Bf16s<N> a = *reinterpret_cast<const Bf16s<N> *>(p + r0);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = bf16_to_f32(a.v[i]);
@@ -43,7 +43,22 @@ __device__ __forceinline__ void load_rows(const uint16_t *p, uint32_t r0, uint32
   }
 }
 
-template <int kDk, int kQuads>
+// Four columns of a row of the state, those past dv zero.  kWhole: all four
+// are inside, or none (its lanes then work on the first columns, and store nothing).
+template <bool kWhole>
+__device__ __forceinline__ float4 load_columns(const float *p, uint32_t cols) {
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (kWhole || cols == 4u) {
+    const Float4 f = *reinterpret_cast<const Float4 *>(p);
+    return make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
+  }
+  if (cols > 0u) s.x = p[0];
+  if (cols > 1u) s.y = p[1];
+  if (cols > 2u) s.z = p[2];
+  return s;
+}
+
+template <int kDk, int kQuads, bool kWhole>
 __global__ __launch_bounds__(64) void delta_recurrent_kernel(const DeltaArgs a) {
   constexpr int kGroups = 64 / kQuads;
   constexpr int kRows = kDk / kGroups;
@@ -59,31 +74,26 @@ __global__ __launch_bounds__(64) void delta_recurrent_kernel(const DeltaArgs a) 
   if (sq.begin >= sq.end && !sq.fresh) return;  // nothing changes
 
   float4 s[kRows];
-  float *state = a.state + ((uint64_t)max(sq.slot, 0) * a.hv + hv) * a.dk * a.dv + c0;
-  const bool from_state = sq.slot >= 0 && !sq.fresh;
+  const uint32_t c = kWhole && cols == 0u ? 0u : c0;
+  float *state = a.state + ((uint64_t)max(sq.slot, 0) * a.hv + hv) * a.dk * a.dv + c;
+  if (sq.slot >= 0 && !sq.fresh) {
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    s[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (from_state && r0 + i < a.dk) {
-      const float *p = state + (uint64_t)(r0 + i) * a.dv;
-      if (cols == 4u) {
-        const Float4 f = *reinterpret_cast<const Float4 *>(p);
-        s[i] = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
-      } else {
-        if (cols > 0u) s[i].x = p[0];
-        if (cols > 1u) s[i].y = p[1];
-        if (cols > 2u) s[i].z = p[2];
-      }
+    for (int i = 0; i < kRows; ++i) {
+      if (kWhole)  // no branch around the loads: they leave together
+        s[i] = load_columns<true>(state + (uint64_t)(r0 + i) * a.dv, 4u);
+      else
+        s[i] = load_columns<false>(state + (uint64_t)(r0 + i) * a.dv, r0 + i < a.dk ? cols : 0u);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) s[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
 
   for (uint32_t t = sq.begin; t < sq.end; ++t) {
     float q[kRows], k[kRows], v[4];
-    load_rows<kRows>(a.q + (uint64_t)t * a.q_token + (uint64_t)hk * a.q_head, r0, a.dk, q);
-    load_rows<kRows>(a.k + (uint64_t)t * a.k_token + (uint64_t)hk * a.k_head, r0, a.dk, k);
-    const uint16_t *vp = a.v + (uint64_t)t * a.v_token + (uint64_t)hv * a.v_head + c0;
-#pragma unroll
-    for (uint32_t j = 0; j < 4; ++j) v[j] = j < cols ? bf16_to_f32(vp[j]) : 0.0f;
+    load_rows<kRows, kWhole>(a.q + (uint64_t)t * a.q_token + (uint64_t)hk * a.q_head, r0, a.dk, q);
+    load_rows<kRows, kWhole>(a.k + (uint64_t)t * a.k_token + (uint64_t)hk * a.k_head, r0, a.dk, k);
+    load_rows<4, kWhole>(a.v + (uint64_t)t * a.v_token + (uint64_t)hv * a.v_head, c, a.dv, v);
     const float decay = expf(a.g[(uint64_t)t * a.hv + hv]), beta = a.beta[(uint64_t)t * a.hv + hv];
 
     // k^T S, q^T S (four columns each), |k|^2, |q|^2, q.k
@@ -126,23 +136,26 @@ __global__ __launch_bounds__(64) void delta_recurrent_kernel(const DeltaArgs a) 
     }
     if (threadIdx.x < kQuads) {
       uint16_t *op = a.out + ((uint64_t)t * a.hv + hv) * a.dv + c0;
+      if (cols == 4u) {
+        *reinterpret_cast<Bf16s<4> *>(op) =
+            __builtin_bit_cast(Bf16s<4>, make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])));
+      } else {
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j)
-        if (j < cols) op[j] = (uint16_t)f32_to_bf16_rne(o[j]);
+        for (uint32_t j = 0; j < 4; ++j)
+          if (j < cols) op[j] = (uint16_t)f32_to_bf16_rne(o[j]);
+      }
     }
   }
 
-  if (sq.slot < 0) return;
+  if (sq.slot < 0 || cols == 0u) return;
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    if (r0 + i >= a.dk) continue;
+    if (!kWhole && r0 + i >= a.dk) continue;
     float *p = state + (uint64_t)(r0 + i) * a.dv;
-    if (cols == 4u) {
-      Float4 f;
-      f.v[0] = s[i].x; f.v[1] = s[i].y; f.v[2] = s[i].z; f.v[3] = s[i].w;
-      *reinterpret_cast<Float4 *>(p) = f;
+    if (kWhole || cols == 4u) {
+      *reinterpret_cast<Float4 *>(p) = Float4{{s[i].x, s[i].y, s[i].z, s[i].w}};
     } else {
-      if (cols > 0u) p[0] = s[i].x;
+      p[0] = s[i].x;
       if (cols > 1u) p[1] = s[i].y;
       if (cols > 2u) p[2] = s[i].z;
     }
@@ -152,7 +165,10 @@ __global__ __launch_bounds__(64) void delta_recurrent_kernel(const DeltaArgs a) 
 template <int kDk, int kQuads>
 hipError_t launch_recurrent(const DeltaArgs &a, hipStream_t s) {
   const uint64_t blocks = (uint64_t)a.count * a.hv * ((a.dv + 4ull * kQuads - 1u) / (4ull * kQuads));
-  hipLaunchKernelGGL((delta_recurrent_kernel<kDk, kQuads>), dim3((uint32_t)blocks), dim3(64), 0, s, a);
+  if (a.dk == (uint32_t)kDk && a.dv % 4u == 0u)
+    hipLaunchKernelGGL((delta_recurrent_kernel<kDk, kQuads, true>), dim3((uint32_t)blocks), dim3(64), 0, s, a);
+  else
+    hipLaunchKernelGGL((delta_recurrent_kernel<kDk, kQuads, false>), dim3((uint32_t)blocks), dim3(64), 0, s, a);
   return hipGetLastError();
 }
 
