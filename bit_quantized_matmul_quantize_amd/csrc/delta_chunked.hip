@@ -127,23 +127,24 @@ __device__ __forceinline__ void put_triangle(const float *m, uint8_t *out, uint3
     *reinterpret_cast<uint4 *>(p + i * kFragment) = make_uint4(parts[0][i], parts[1][i], parts[2][i], parts[3][i]);
 }
 
-// One workgroup for a chunk and value head.
-template <int kDk>
+// A workgroup takes a chunk, a key head, and kHeads of its value heads, one
+// after the other: they share the keys, the queries and their products.
+template <int kDk, int kHeads>
 __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a) {
   constexpr int kRow = kDk + 8;  // bf16 per staged row
   constexpr uint32_t kBuffer = kChunk * kStride * 4;
   static_assert(kChunk * kRow * 2 <= kBuffer, "the staged keys and queries fit the buffers that replace them");
   __shared__ __attribute__((aligned(16))) uint8_t lds[3 * kBuffer];
-  __shared__ double sum_g[kChunk];
-  __shared__ float norm_k[kChunk], norm_q[kChunk], betas[kChunk];
+  __shared__ double sum_g[kHeads][kChunk];  // of g log2(e): decays are powers of two
+  __shared__ float norm_k[kChunk], norm_q[kChunk], betas[kHeads][kChunk];
   uint16_t *keys = reinterpret_cast<uint16_t *>(lds), *queries = reinterpret_cast<uint16_t *>(lds + kBuffer);
   float *inverse = reinterpret_cast<float *>(lds);             // in the keys' place
   float *inner = reinterpret_cast<float *>(lds + kBuffer);     // in the queries' place
   float *lower = reinterpret_cast<float *>(lds + 2 * kBuffer);
 
   const uint32_t tid = threadIdx.x, lane = tid & 63u, w = tid >> 6, lr = lane & 15u, lq = lane >> 4;
-  const uint32_t place = blockIdx.x / a.hv, head = blockIdx.x - place * a.hv;
-  const uint32_t ratio = a.hv / a.hk, khead = head / ratio;
+  const uint32_t sets = a.hv / kHeads;  // of value heads
+  const uint32_t place = blockIdx.x / sets, head0 = (blockIdx.x - place * sets) * kHeads, khead = head0 / (a.hv / a.hk);
 
   // the sequence whose places hold this one: as many as begin at or before it, less one
   int before = 0;
@@ -160,19 +161,23 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
   if (t0 >= sq.end) return;
   const uint32_t n = min(sq.end - t0, (uint32_t)kChunk);
 
-  // keys and queries into LDS, zeros past the chunk's end and past dk
+  // keys and queries into LDS, zeros past the chunk's end and past dk; their
+  // norms on the way (the lanes of a row lie side by side)
   {
-    const uint32_t vecs = kDk / 8;
-    for (uint32_t i = tid; i < kChunk * vecs; i += kThreads) {
-      const uint32_t r = i / vecs, c = (i - r * vecs) * 8u;
-      uint4 kv = make_uint4(0, 0, 0, 0), qv = kv;
+    constexpr uint32_t kVecs = kDk / 8;
+    const uint16_t *kbase = a.k + (uint64_t)t0 * a.k_token + (uint64_t)khead * a.k_head;
+    const uint16_t *qbase = a.q + (uint64_t)t0 * a.q_token + (uint64_t)khead * a.q_head;
+    uint4 kv[kVecs / 4], qv[kVecs / 4];
+#pragma unroll
+    for (uint32_t i = 0; i < kVecs / 4; ++i) {
+      const uint32_t r = (i * kThreads + tid) / kVecs, c = tid % kVecs * 8u;
+      kv[i] = qv[i] = make_uint4(0, 0, 0, 0);
       if (r < n) {
-        const uint16_t *kp = a.k + (uint64_t)(t0 + r) * a.k_token + (uint64_t)khead * a.k_head + c;
-        const uint16_t *qp = a.q + (uint64_t)(t0 + r) * a.q_token + (uint64_t)khead * a.q_head + c;
+        const uint16_t *kp = kbase + (uint64_t)r * a.k_token + c, *qp = qbase + (uint64_t)r * a.q_token + c;
         if (c + 8u <= a.dk) {
           const Bf16x8 x = *reinterpret_cast<const Bf16x8 *>(kp), y = *reinterpret_cast<const Bf16x8 *>(qp);
-          kv = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
-          qv = make_uint4(y.w[0], y.w[1], y.w[2], y.w[3]);
+          kv[i] = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+          qv[i] = make_uint4(y.w[0], y.w[1], y.w[2], y.w[3]);
         } else {
           uint32_t x[8], y[8];
 #pragma unroll
@@ -180,47 +185,51 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
             x[j] = c + j < a.dk ? kp[j] : 0u;
             y[j] = c + j < a.dk ? qp[j] : 0u;
           }
-          kv = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
-          qv = make_uint4(y[0] | y[1] << 16, y[2] | y[3] << 16, y[4] | y[5] << 16, y[6] | y[7] << 16);
+          kv[i] = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
+          qv[i] = make_uint4(y[0] | y[1] << 16, y[2] | y[3] << 16, y[4] | y[5] << 16, y[6] | y[7] << 16);
         }
       }
-      *reinterpret_cast<uint4 *>(keys + r * kRow + c) = kv;
-      *reinterpret_cast<uint4 *>(queries + r * kRow + c) = qv;
     }
-  }
-  if (w == 0) {
-    const float gt = lane < n ? a.g[(uint64_t)(t0 + lane) * a.hv + head] : 0.0f;
-    double g = (double)(gt < kNoDecay ? kNoDecay : gt);
+    // a wave for each value head: its sums of g, its betas
+    if (w < (uint32_t)kHeads) {
+      const uint64_t at = (uint64_t)(t0 + min(lane, n - 1u)) * a.hv + head0 + w;
+      const float gt = lane < n ? a.g[at] : 0.0f;
+      double g = (double)(gt < kNoDecay ? kNoDecay : gt) * 1.4426950408889634;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const double o = __shfl_up(g, d);
-      g += lane >= (uint32_t)d ? o : 0.0;
+      for (int d = 1; d < 64; d <<= 1) {
+        const double o = __shfl_up(g, d);
+        g += lane >= (uint32_t)d ? o : 0.0;
+      }
+      sum_g[w][lane] = g;
+      betas[w][lane] = lane < n ? a.beta[at] : 0.0f;
     }
-    sum_g[lane] = g;
-    betas[lane] = lane < n ? a.beta[(uint64_t)(t0 + lane) * a.hv + head] : 0.0f;
+#pragma unroll
+    for (uint32_t i = 0; i < kVecs / 4; ++i) {
+      const uint32_t r = (i * kThreads + tid) / kVecs, c = tid % kVecs * 8u;
+      *reinterpret_cast<uint4 *>(keys + r * kRow + c) = kv[i];
+      *reinterpret_cast<uint4 *>(queries + r * kRow + c) = qv[i];
+      const uint32_t kw[4] = {kv[i].x, kv[i].y, kv[i].z, kv[i].w}, qw[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+      float sk = 0.0f, sq2 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x = __uint_as_float(kw[j] << 16), y = __uint_as_float(kw[j] & 0xFFFF0000u);
+        const float u = __uint_as_float(qw[j] << 16), v = __uint_as_float(qw[j] & 0xFFFF0000u);
+        sk = fmaf(x, x, fmaf(y, y, sk));
+        sq2 = fmaf(u, u, fmaf(v, v, sq2));
+      }
+#pragma unroll
+      for (int d = 1; d < (int)kVecs; d <<= 1) {
+        sk += __shfl_xor(sk, d);
+        sq2 += __shfl_xor(sq2, d);
+      }
+      if (c == 0u) {
+        norm_k[r] = a.l2norm ? 1.0f / sqrtf(sk + kNormEps) : 1.0f;
+        norm_q[r] = (a.l2norm ? 1.0f / sqrtf(sq2 + kNormEps) : 1.0f) * a.scale;
+      }
+    }
   }
   __syncthreads();
 
-  uint8_t *mine = a.workspace + ((uint64_t)place * a.hv + head) * kHeadBytes;
-  // norms: four lanes per row
-  {
-    const uint32_t r = tid >> 2, c = (tid & 3u) * (kDk / 4);
-    float sk = 0.0f, sq2 = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kDk / 4; ++j) {
-      const float x = bf16_to_f32(keys[r * kRow + c + j]), y = bf16_to_f32(queries[r * kRow + c + j]);
-      sk = fmaf(x, x, sk);
-      sq2 = fmaf(y, y, sq2);
-    }
-    sk += __shfl_xor(sk, 1);
-    sk += __shfl_xor(sk, 2);
-    sq2 += __shfl_xor(sq2, 1);
-    sq2 += __shfl_xor(sq2, 2);
-    if ((tid & 3u) == 0u) {
-      norm_k[r] = a.l2norm ? 1.0f / sqrtf(sk + kNormEps) : 1.0f;
-      norm_q[r] = (a.l2norm ? 1.0f / sqrtf(sq2 + kNormEps) : 1.0f) * a.scale;
-    }
-  }
   // k.k and q.k: rows 16w.. by the wave, the tiles of the lower triangle
   v4f kk[4], qk[4];
 #pragma unroll
@@ -238,82 +247,101 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
       }
     }
   }
-  __syncthreads();  // the norms are there; keys and queries have been read
 
-  if (w == 0) {
-    const double g = sum_g[lane];
-    const float e = expf((float)g);
-    float *f = reinterpret_cast<float *>(mine + kTBytes + kInnerBytes) + lane;
-    f[0] = betas[lane];
-    f[kChunk] = betas[lane] * e * norm_k[lane];
-    f[2 * kChunk] = lane < n ? expf((float)(sum_g[kChunk - 1] - g)) * norm_k[lane] : 0.0f;
-    f[3 * kChunk] = lane < n ? e * norm_q[lane] : 0.0f;
-    if (lane == kChunk - 1) f[3 * kChunk + 1] = e;
-  }
-#pragma unroll
-  for (uint32_t j = 0; j < 4; ++j) {
-    if (j > w) continue;
-    const uint32_t s = 16u * j + lr;
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) {
-      const uint32_t t = 16u * w + lq * 4u + i;
-      const float decay = s <= t ? expf((float)(sum_g[t] - sum_g[s])) * norm_k[s] : 0.0f;
-      lower[t * kStride + s] = s < t ? betas[t] * norm_k[t] * decay * kk[j][i] : 0.0f;
-      inner[t * kStride + s] = s <= t ? norm_q[t] * decay * qk[j][i] : 0.0f;
+  for (int h = 0; h < kHeads; ++h) {
+    uint8_t *mine = a.workspace + ((uint64_t)place * a.hv + head0 + h) * kHeadBytes;
+    __syncthreads();  // keys and queries, or the last head's matrices, have been read
+    if (w == 0) {
+      const double g = sum_g[h][lane];
+      const float e = exp2f((float)g), beta = betas[h][lane];
+      float *f = reinterpret_cast<float *>(mine + kTBytes + kInnerBytes) + lane;
+      f[0] = beta;
+      f[kChunk] = beta * e * norm_k[lane];
+      f[2 * kChunk] = lane < n ? exp2f((float)(sum_g[h][kChunk - 1] - g)) * norm_k[lane] : 0.0f;
+      f[3 * kChunk] = lane < n ? e * norm_q[lane] : 0.0f;
+      if (lane == kChunk - 1) f[3 * kChunk + 1] = e;
     }
-  }
-  __syncthreads();
-
-  // T: the 16 x 16 blocks on the diagonal by substitution (a lane a column),
-  // then blocks of 16 and of 32 joined in pairs,
-  //   [[a, 0], [c, b]]^-1 = [[a', 0], [-b' c a', b']].
-  if (w == 0) {
-    float t[16];
+    {
+      double g[4];
+      float row_k[4], row_q[4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float *row = lower + (16 * lq + i) * kStride + 16 * lq;
-      float x = (uint32_t)i == lr ? 1.0f : 0.0f, y = 0.0f;
-#pragma unroll
-      for (int m = 0; m < i; ++m) {
-        if (m & 1)
-          y = fmaf(-row[m], t[m], y);
-        else
-          x = fmaf(-row[m], t[m], x);
+      for (uint32_t i = 0; i < 4; ++i) {
+        const uint32_t t = 16u * w + lq * 4u + i;
+        g[i] = sum_g[h][t];
+        row_k[i] = betas[h][t] * norm_k[t];
+        row_q[i] = norm_q[t];
       }
-      t[i] = x + y;
-      inverse[(16 * lq + i) * kStride + 16 * lq + lr] = t[i];
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) {
+        if (j > w) continue;
+        const uint32_t s = 16u * j + lr;
+        const double gs = sum_g[h][s];
+        const float ks = norm_k[s];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+          const uint32_t t = 16u * w + lq * 4u + i;
+          // (rows above the column would grow: their power is not taken)
+          const float decay = s <= t ? __builtin_amdgcn_exp2f((float)(g[i] - gs)) * ks : 0.0f;
+          lower[t * kStride + s] = s < t ? row_k[i] * decay * kk[j][i] : 0.0f;
+          inner[t * kStride + s] = s <= t ? row_q[i] * decay * qk[j][i] : 0.0f;
+        }
+      }
     }
-  } else {
-    // meanwhile the other waves put the q.k triangle away, two fragments each
-    for (uint32_t f = 2u * w - 2u; f < 2u * w; ++f)
-      put_triangle<2>(inner, mine + kTBytes, f < 2u ? f : f / 2u + 1u, f < 2u ? 0u : f & 1u, lane);
-  }
-  __syncthreads();
-  if (w < 2) {
-    const uint32_t o = 32u * w;
-    const v4f x = block_product(lower + (o + 16) * kStride + o, inverse + o * kStride + o, v4f{0, 0, 0, 0}, lr, lq);
-    const v4f y = block_product(inverse + (o + 16) * kStride + o + 16, x, v4f{0, 0, 0, 0}, lr, lq);
+    __syncthreads();
+
+    // T: the 16 x 16 blocks on the diagonal by substitution (a lane a column),
+    // then blocks of 16 and of 32 joined in pairs,
+    //   [[a, 0], [c, b]]^-1 = [[a', 0], [-b' c a', b']].
+    if (w == 0) {
+      float t[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) inverse[(o + 16 + lq * 4 + i) * kStride + o + lr] = -y[i];
-  }
-  __syncthreads();
-  {
-    const uint32_t jt = w & 1u, rt = w >> 1;
-    v4f x[2], y = {0, 0, 0, 0};
+      for (int i = 0; i < 16; ++i) {
+        const float *row = lower + (16 * lq + i) * kStride + 16 * lq;
+        float x[4] = {(uint32_t)i == lr ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (uint32_t r = 0; r < 2; ++r) {
-      x[r] = v4f{0, 0, 0, 0};
-      for (uint32_t kt = jt; kt < 2; ++kt)
-        x[r] = block_product(lower + (32 + 16 * r) * kStride + 16 * kt, inverse + 16 * kt * kStride + 16 * jt, x[r], lr, lq);
+        for (int m = 0; m < i; m += 4) {
+          const float4 f = *reinterpret_cast<const float4 *>(row + m);
+          x[0] = fmaf(-f.x, t[m], x[0]);
+          if (m + 1 < i) x[1] = fmaf(-f.y, t[m + 1], x[1]);
+          if (m + 2 < i) x[2] = fmaf(-f.z, t[m + 2], x[2]);
+          if (m + 3 < i) x[3] = fmaf(-f.w, t[m + 3], x[3]);
+        }
+        t[i] = (x[0] + x[1]) + (x[2] + x[3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) inverse[(16 * lq + i) * kStride + 16 * lq + lr] = t[i];
+    } else {
+      // meanwhile the other waves put the q.k triangle away, two fragments each
+      for (uint32_t f = 2u * w - 2u; f < 2u * w; ++f)
+        put_triangle<2>(inner, mine + kTBytes, f < 2u ? f : f / 2u + 1u, f < 2u ? 0u : f & 1u, lane);
     }
-    y = block_product(inverse + (32 + 16 * rt) * kStride + 32, x[0], y, lr, lq);
-    if (rt == 1u) y = block_product(inverse + 48 * kStride + 48, x[1], y, lr, lq);
+    __syncthreads();
+    if (w < 2) {
+      const uint32_t o = 32u * w;
+      const v4f x = block_product(lower + (o + 16) * kStride + o, inverse + o * kStride + o, v4f{0, 0, 0, 0}, lr, lq);
+      const v4f y = block_product(inverse + (o + 16) * kStride + o + 16, x, v4f{0, 0, 0, 0}, lr, lq);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) inverse[(32 + 16 * rt + lq * 4 + i) * kStride + 16 * jt + lr] = -y[i];
+      for (int i = 0; i < 4; ++i) inverse[(o + 16 + lq * 4 + i) * kStride + o + lr] = -y[i];
+    }
+    __syncthreads();
+    {
+      const uint32_t jt = w & 1u, rt = w >> 1;
+      v4f x[2], y = {0, 0, 0, 0};
+#pragma unroll
+      for (uint32_t r = 0; r < 2; ++r) {
+        x[r] = v4f{0, 0, 0, 0};
+        for (uint32_t kt = jt; kt < 2; ++kt)
+          x[r] = block_product(lower + (32 + 16 * r) * kStride + 16 * kt, inverse + 16 * kt * kStride + 16 * jt, x[r], lr, lq);
+      }
+      y = block_product(inverse + (32 + 16 * rt) * kStride + 32, x[0], y, lr, lq);
+      if (rt == 1u) y = block_product(inverse + 48 * kStride + 48, x[1], y, lr, lq);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) inverse[(32 + 16 * rt + lq * 4 + i) * kStride + 16 * jt + lr] = -y[i];
+    }
+    __syncthreads();
+    for (uint32_t f = w; f < kTriangle; f += 4)
+      put_triangle<3>(inverse, mine, f < 2u ? f : f / 2u + 1u, f < 2u ? 0u : f & 1u, lane);
   }
-  __syncthreads();
-  for (uint32_t f = w; f < kTriangle; f += 4)
-    put_triangle<3>(inverse, mine, f < 2u ? f : f / 2u + 1u, f < 2u ? 0u : f & 1u, lane);
 }
 
 // ---- second launch: the state along the chunks ------------------------------------
@@ -766,7 +794,10 @@ template <int kTiles>
 hipError_t launch_chunked(const DeltaArgs &a, hipStream_t s) {
   const uint64_t places = a.tokens / kChunk + (uint64_t)a.count;
   if (a.tokens > 0) {
-    hipLaunchKernelGGL((delta_chunk_kernel<64 * kTiles>), dim3((uint32_t)(places * a.hv)), dim3(kThreads), 0, s, a);
+    if (a.hv / a.hk % 2u == 0u)
+      hipLaunchKernelGGL((delta_chunk_kernel<64 * kTiles, 2>), dim3((uint32_t)(places * (a.hv / 2u))), dim3(kThreads), 0, s, a);
+    else
+      hipLaunchKernelGGL((delta_chunk_kernel<64 * kTiles, 1>), dim3((uint32_t)(places * a.hv)), dim3(kThreads), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
