@@ -133,14 +133,18 @@ template <int kDk, int kHeads>
 __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a) {
   constexpr int kRow = kDk + 8;  // bf16 per staged row
   constexpr uint32_t kBuffer = kChunk * kStride * 4;
+  static_assert(kHeads <= 2, "two betas fit the pad");
   static_assert(kChunk * kRow * 2 <= kBuffer, "the staged keys and queries fit the buffers that replace them");
   __shared__ __attribute__((aligned(16))) uint8_t lds[3 * kBuffer];
   __shared__ double sum_g[kHeads][kChunk];  // of g log2(e): decays are powers of two
-  __shared__ float norm_k[kChunk], norm_q[kChunk], betas[kHeads][kChunk];
   uint16_t *keys = reinterpret_cast<uint16_t *>(lds), *queries = reinterpret_cast<uint16_t *>(lds + kBuffer);
   float *inverse = reinterpret_cast<float *>(lds);             // in the keys' place
   float *inner = reinterpret_cast<float *>(lds + kBuffer);     // in the queries' place
   float *lower = reinterpret_cast<float *>(lds + 2 * kBuffer);
+  // a token's norms and betas lie in the pad of lower's rows (three workgroups fit a CU that way)
+  auto norm_k = [&](uint32_t t) -> float & { return lower[t * kStride + kChunk]; };
+  auto norm_q = [&](uint32_t t) -> float & { return lower[t * kStride + kChunk + 1]; };
+  auto betas = [&](uint32_t h, uint32_t t) -> float & { return lower[t * kStride + kChunk + 2 + h]; };
 
   const uint32_t tid = threadIdx.x, lane = tid & 63u, w = tid >> 6, lr = lane & 15u, lq = lane >> 4;
   const uint32_t sets = a.hv / kHeads;  // of value heads
@@ -201,7 +205,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
         g += lane >= (uint32_t)d ? o : 0.0;
       }
       sum_g[w][lane] = g;
-      betas[w][lane] = lane < n ? a.beta[at] : 0.0f;
+      betas(w, lane) = lane < n ? a.beta[at] : 0.0f;
     }
 #pragma unroll
     for (uint32_t i = 0; i < kVecs / 4; ++i) {
@@ -223,8 +227,8 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
         sq2 += __shfl_xor(sq2, d);
       }
       if (c == 0u) {
-        norm_k[r] = a.l2norm ? 1.0f / sqrtf(sk + kNormEps) : 1.0f;
-        norm_q[r] = (a.l2norm ? 1.0f / sqrtf(sq2 + kNormEps) : 1.0f) * a.scale;
+        norm_k(r) = a.l2norm ? 1.0f / sqrtf(sk + kNormEps) : 1.0f;
+        norm_q(r) = (a.l2norm ? 1.0f / sqrtf(sq2 + kNormEps) : 1.0f) * a.scale;
       }
     }
   }
@@ -253,12 +257,12 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
     __syncthreads();  // keys and queries, or the last head's matrices, have been read
     if (w == 0) {
       const double g = sum_g[h][lane];
-      const float e = exp2f((float)g), beta = betas[h][lane];
+      const float e = exp2f((float)g), beta = betas(h, lane);
       float *f = reinterpret_cast<float *>(mine + kTBytes + kInnerBytes) + lane;
       f[0] = beta;
-      f[kChunk] = beta * e * norm_k[lane];
-      f[2 * kChunk] = lane < n ? exp2f((float)(sum_g[h][kChunk - 1] - g)) * norm_k[lane] : 0.0f;
-      f[3 * kChunk] = lane < n ? e * norm_q[lane] : 0.0f;
+      f[kChunk] = beta * e * norm_k(lane);
+      f[2 * kChunk] = lane < n ? exp2f((float)(sum_g[h][kChunk - 1] - g)) * norm_k(lane) : 0.0f;
+      f[3 * kChunk] = lane < n ? e * norm_q(lane) : 0.0f;
       if (lane == kChunk - 1) f[3 * kChunk + 1] = e;
     }
     {
@@ -268,15 +272,15 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
       for (uint32_t i = 0; i < 4; ++i) {
         const uint32_t t = 16u * w + lq * 4u + i;
         g[i] = sum_g[h][t];
-        row_k[i] = betas[h][t] * norm_k[t];
-        row_q[i] = norm_q[t];
+        row_k[i] = betas(h, t) * norm_k(t);
+        row_q[i] = norm_q(t);
       }
 #pragma unroll
       for (uint32_t j = 0; j < 4; ++j) {
         if (j > w) continue;
         const uint32_t s = 16u * j + lr;
         const double gs = sum_g[h][s];
-        const float ks = norm_k[s];
+        const float ks = norm_k(s);
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i) {
           const uint32_t t = 16u * w + lq * 4u + i;
@@ -362,7 +366,7 @@ constexpr int kScanThreads = 512;
 // What both kinds of waves know of their work.
 struct ScanPlace {
   DeltaSeq sq;
-  uint32_t head, khead, block, col, place0, chunks, last;  // last: tokens of the last chunk
+  uint32_t head, khead, col, place0, chunks, last;  // last: tokens of the last chunk
   bool col_in;
 };
 
@@ -674,38 +678,15 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
     vals += (uint64_t)kChunk * 2u * a.v_token;
     if (c + 1u == pl.chunks) token_offsets(pl.last);
   };
-  // The column blocks of a head run side by side on one XCD: each touches its
-  // share of the cache lines of the chunk after the next, so that its L2 has
-  // them by the time they are loaded (a step is shorter than memory's latency).
-  const uint32_t blocks = (a.dv + 15u) / 16u;
-  uint32_t touched = 0, touched_row = 0;  // read a step later, so that nothing waits for them
-  auto touch = [&](uint32_t c) {
-    c = min(c, pl.chunks - 1u);
-    const uint32_t line = pl.block + blocks * (w * 64u + lane);
-    if (line < kHeadBytes / 128u)
-      touched = *reinterpret_cast<const uint32_t *>(a.workspace + ((uint64_t)(pl.place0 + c) * a.hv + pl.head) * kHeadBytes + line * 128u);
-    const uint32_t row = pl.block + blocks * ((3u - w) * 64u + lane);  // token, half, and which of q, k, v
-    if (row < kChunk * 6u) {
-      const uint64_t t = min(pl.sq.begin + c * kChunk + row / 6u, pl.sq.end - 1u);
-      const uint32_t what = row % 6u / 2u, half = row & 1u;
-      const uint16_t *at = what == 0u ? a.q + t * a.q_token + (uint64_t)pl.khead * a.q_head
-                           : what == 1u ? a.k + t * a.k_token + (uint64_t)pl.khead * a.k_head
-                                        : a.v + t * a.v_token + (uint64_t)pl.head * a.v_head;
-      touched_row = at[half * min(64u, (what == 2u ? a.dv : a.dk) - 1u)];
-    }
-  };
   token_offsets(pl.chunks == 1u ? pl.last : (uint32_t)kChunk);
   load_tokens();
   load_queries();
   load_inner();
   put_tokens(0);
-  touch(1);
   if (pl.chunks > 1u) advance(1);
   load_tokens();
   for (uint32_t c = 0; c < pl.chunks; ++c) {
     __syncthreads();
-    asm volatile("" ::"v"(touched), "v"(touched_row));
-    touch(c + 2u);
     __syncthreads();
     // Q S0 for tokens 16w.., beside the chain's longest phase
     v8bf sb[2][kSteps];
@@ -770,8 +751,7 @@ __global__ __launch_bounds__(kScanThreads) void delta_scan_kernel(const DeltaArg
   pl.sq = delta_sequence(a, seq);
   pl.head = pair - seq * a.hv;
   pl.khead = pl.head / (a.hv / a.hk);
-  pl.block = j % blocks;
-  pl.col = pl.block * 16u + (lane & 15u);
+  pl.col = (j % blocks) * 16u + (lane & 15u);
   pl.col_in = pl.col < a.dv;
   pl.place0 = first_place(pl.sq.begin, seq);
   const uint32_t tokens = pl.sq.end - pl.sq.begin;
