@@ -177,8 +177,18 @@ def _same_device(*tensors):
 
 def _ptrs(*tensors):
     """Device pointers of the given contiguous tensors (None passes through), all on one device."""
-    _same_device(*tensors)
-    return [_ptr(t) for t in tensors]
+    ptrs, dev = [], None
+    for t in tensors:
+        if t is None:
+            ptrs.append(None)
+            continue
+        d = t.get_device()  # -1: not on a device
+        if (d != dev and (d < 0 or dev is not None)) or not t.is_contiguous():
+            _same_device(*tensors)  # one of these says what is wrong
+            return [_ptr(t) for t in tensors]
+        dev = d
+        ptrs.append(t.data_ptr())
+    return ptrs
 
 
 def _bf(m: int, k: int) -> int:
@@ -365,21 +375,19 @@ def w8a8_gemm(act_i8, w_i8, out, m: int, n: int, k: int, bias=None, stream=None)
 
 
 def _typed(t, kind, shape, what):
-    """A tensor of this type and shape (None passes through)."""
-    if t is not None:
-        if _kind(t) != kind:
-            raise TypeError(f"{what}: expected {kind}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
-    return t
-
-
-def _heads(t, shape, what):
-    """A [tokens, heads, d] bf16 tensor, its last dimension contiguous: (token stride, head stride)."""
+    """Refuses a tensor that is not of this type and shape."""
+    if _kinds.get(t.dtype) != kind and _kind(t) != kind:
+        raise TypeError(f"{what}: expected {kind}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
-    token, head, one = _bf16(t, what).stride()
-    if one != 1 and shape[2] > 1:
+
+
+def _strides(t, what):
+    """Of a [tokens, heads, d] bf16 tensor, its last dimension contiguous: (token stride, head stride)."""
+    if _kinds.get(t.dtype) not in _BF16:
+        _bf16(t, what)
+    token, head, one = t.stride()
+    if one != 1 and t.shape[2] > 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
     return token, head
 
@@ -387,20 +395,37 @@ def _heads(t, shape, what):
 def _delta(fn, q, k, v, g, beta, out, state, starts, slots, fresh, workspace, scale, l2norm, stream):
     if q.dim() != 3 or v.dim() != 3 or state.dim() != 4 or starts.dim() != 1 or starts.numel() < 1:
         raise ValueError("expected q, k, v as [tokens, heads, d], state as [slots, hv, dk, dv], starts as [count + 1]")
-    (tokens, hk, dk), (_, hv, dv), places, count = q.shape, v.shape, state.shape[0], starts.shape[0] - 1
-    strides = (*_heads(q, (tokens, hk, dk), "q"), *_heads(k, (tokens, hk, dk), "k"), *_heads(v, (tokens, hv, dv), "v"))
-    rest = (_typed(g, "torch.float32", (tokens, hv), "g"), _typed(beta, "torch.float32", (tokens, hv), "beta"),
-            _typed(out, "torch.bfloat16", (tokens, hv, dv), "out"),
-            _typed(state, "torch.float32", (places, hv, dk, dv), "state"),
-            _typed(starts, "torch.int32", (count + 1,), "starts"), _typed(slots, "torch.int32", (count,), "slots"),
-            _typed(fresh, "torch.uint8", (count,), "fresh"), *workspace)
-    if not (q.is_cuda and k.is_cuda and v.is_cuda):
-        raise ValueError("expected a device tensor")
-    _same_device(q, k, v, *rest)
-    if slots is None and places < count:
+    qk_shape, v_shape = q.shape, v.shape
+    (tokens, hk, dk), (_, hv, dv), places, count = qk_shape, v_shape, state.shape[0], starts.numel() - 1
+    if k.shape != qk_shape:
+        raise ValueError(f"k: expected shape {tuple(qk_shape)}, got {tuple(k.shape)}")
+    if v_shape[0] != tokens:
+        raise ValueError(f"v: expected {tokens} tokens, got {v_shape[0]}")
+    qt, qh = _strides(q, "q")
+    kt, kh = _strides(k, "k")
+    vt, vh = _strides(v, "v")
+    of_heads = (tokens, hv)
+    _typed(g, "torch.float32", of_heads, "g")
+    _typed(beta, "torch.float32", of_heads, "beta")
+    _typed(out, "torch.bfloat16", v_shape, "out")
+    _typed(state, "torch.float32", (places, hv, dk, dv), "state")
+    _typed(starts, "torch.int32", (count + 1,), "starts")
+    if slots is not None:
+        _typed(slots, "torch.int32", (count,), "slots")
+    elif places < count:
         raise ValueError(f"state: {places} slots for {count} sequences")
-    _check(fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), *map(_ptr, rest), *map(_nbytes, workspace), tokens, count, places,
-              hk, hv, dk, dv, *strides, dk ** -0.5 if scale is None else scale, 1 if l2norm else 0, _stream(stream)))
+    if fresh is not None:
+        _typed(fresh, "torch.uint8", (count,), "fresh")
+    dev = q.get_device()
+    if dev < 0 or k.get_device() != dev or v.get_device() != dev:
+        _same_device(q, k, v)
+        raise ValueError("expected a device tensor")
+    rest = (g, beta, out, state, starts, slots, fresh, *workspace)
+    if g.get_device() != dev:
+        _same_device(q, *rest)
+    _check(fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), *_ptrs(*rest), *map(_nbytes, workspace), tokens, count, places,
+              hk, hv, dk, dv, qt, qh, kt, kh, vt, vh, dk ** -0.5 if scale is None else scale, 1 if l2norm else 0,
+              _stream(stream)))
 
 
 def gated_delta_rule_recurrent(q, k, v, g, beta, out, state, starts, slots=None, fresh=None, l2norm: bool = True,
