@@ -148,7 +148,9 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
 
   const uint32_t tid = threadIdx.x, lane = tid & 63u, w = tid >> 6, lr = lane & 15u, lq = lane >> 4;
   const uint32_t sets = a.hv / kHeads;  // of value heads
-  const uint32_t place = blockIdx.x / sets, head0 = (blockIdx.x - place * sets) * kHeads, khead = head0 / (a.hv / a.hk);
+  // From the last chunk to the first, so that what the second launch begins with was written last and is still in the
+  // caches (16384 tokens of 32 heads leave 262 MB: both launches 517 us, and 553 from the first on).
+  const uint32_t place = gridDim.x / sets - 1u - blockIdx.x / sets, head0 = blockIdx.x % sets * kHeads, khead = head0 / (a.hv / a.hk);
 
   // the sequence whose places hold this one: as many as begin at or before it, less one
   int before = 0;
@@ -359,8 +361,12 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
 // those have been used: the loads are spread over the step and have most of
 // its time to arrive.
 //
-// What bounds it is the chain itself: three exchanges through LDS per chunk,
-// and on one wave per SIMD an instruction at most every four cycles.
+// What bounds it is the chain itself, 1.3 us per chunk with every operand at
+// hand: three exchanges through LDS, and the latency of what lies between them.
+// So where there are more workgroups than CUs two should share one: 128
+// registers per lane allow it (packed prompts of 2322 tokens: the launch 63 us,
+// and 82 with the 142 that the compiler takes unasked; the kernels of odd sizes
+// would spill and keep theirs).
 constexpr int kScanThreads = 512;
 
 // What both kinds of waves know of their work.
@@ -738,7 +744,7 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
 }
 
 template <int kTiles, bool kWhole>
-__global__ __launch_bounds__(kScanThreads) void delta_scan_kernel(const DeltaArgs a) {
+__global__ __launch_bounds__(kScanThreads, kWhole ? 4 : 2) void delta_scan_kernel(const DeltaArgs a) {
   __shared__ __attribute__((aligned(16))) ScanLds<kTiles> lds;
   const uint32_t lane = threadIdx.x & 63u, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // Workgroups go round the eight XCDs: the column blocks of a head all to one,
