@@ -156,13 +156,15 @@ struct DeltaArgs {
   const int32_t *starts, *slots;
   const uint8_t *fresh;
   uint8_t *workspace;
+  float *parts;  // of segments, in the workspace (set by the launch)
   uint32_t q_token, q_head, k_token, k_head, v_token, v_head;
   uint32_t tokens, count, state_slots, hk, hv, dk, dv;
   float scale;
   int l2norm;
+  uint32_t segment;  // chunks that a segment has (set by the launch)
 };
 hipError_t launch_delta_recurrent(const DeltaArgs &a, hipStream_t s);
 hipError_t launch_delta_chunked(const DeltaArgs &a, hipStream_t s);
-uint64_t delta_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hk, uint32_t hv, uint32_t dk);
+uint64_t delta_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hv, uint32_t dk, uint32_t dv);
 
 }  // namespace bqmm

@@ -581,6 +581,7 @@ int delta_args(const char *name, bqmm::DeltaArgs *args, const void *q, const voi
            slots,
            fresh,
            static_cast<uint8_t *>(workspace),
+           nullptr,
            (uint32_t)q_token,
            (uint32_t)q_head,
            (uint32_t)k_token,
@@ -595,7 +596,8 @@ int delta_args(const char *name, bqmm::DeltaArgs *args, const void *q, const voi
            dk,
            dv,
            scale,
-           l2norm};
+           l2norm,
+           0u};
   return BQ_OK;
 }
 
@@ -665,7 +667,7 @@ uint64_t gated_delta_rule_workspace_bytes(uint32_t tokens, uint32_t count, uint3
   if (hk == 0 || hv == 0 || hv % hk != 0 || dk == 0 || dk > 128 || dv == 0 || hv > 65535u || dv > 65535u || (uint64_t)hv * dv >= (1ull << 24) ||
       tokens >= kMaxRows || count >= kMaxRows)
     return 0;
-  return bqmm::delta_workspace_bytes(tokens, count, hk, hv, dk);
+  return bqmm::delta_workspace_bytes(tokens, count, hv, dk, dv);
 }
 
 int gated_delta_rule_recurrent(const void *q_bf16, const void *k_bf16, const void *v_bf16, const float *g,

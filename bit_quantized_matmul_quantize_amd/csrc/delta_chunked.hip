@@ -11,7 +11,8 @@
 // leaves what does not depend on the state in the workspace: T, the decayed
 // q.k triangle and a few factors per token.  The second
 // walks each head's chunks in order, a workgroup for 16 columns of the state
-// (columns do not depend on each other).
+// (columns do not depend on each other); long sequences of few heads it cuts
+// into segments, and a third launch follows.
 //
 // Numbers.  The matrix cores multiply bf16 and add in binary32.  q and k are
 // bf16 as they are: their norms, decays and beta are factors per token that
@@ -35,6 +36,7 @@ typedef float v2f __attribute__((ext_vector_type(2)));
 
 constexpr int kChunk = 64;
 constexpr int kThreads = 256;
+constexpr uint32_t kCus = 256;
 constexpr float kNormEps = 1e-6f;
 constexpr float kNoDecay = -1e6f;  // exp of it is zero; sums of 64 of them stay exact to 2^-26
 
@@ -55,6 +57,25 @@ __device__ __forceinline__ uint32_t triangle_fragment(uint32_t w, uint32_t ks) {
 // from b / 64 + s on.  Places of different sequences never meet, and all lie
 // below tokens / 64 + count.
 __device__ __forceinline__ uint32_t first_place(uint32_t begin, uint32_t seq) { return begin / kChunk + seq; }
+
+// Segments have places likewise, per `segment` chunks.
+__host__ __device__ __forceinline__ uint32_t segment_places(uint32_t tokens, uint32_t count, uint32_t segment) {
+  return tokens / (segment * kChunk) + count;
+}
+
+// How many sequences have their first place, of places of so many tokens, at or
+// below this one: the last of them is the one that the place belongs to.
+template <int kThreads>
+__device__ __forceinline__ int sequences_up_to(const DeltaArgs &a, uint32_t place, uint32_t tokens) {
+  int before = 0;
+  for (uint32_t s0 = 0; s0 < a.count; s0 += kThreads) {
+    const uint32_t s = s0 + threadIdx.x;
+    bool at = false;
+    if (s < a.count) at = min((uint32_t)max(a.starts[s], 0), a.tokens) / tokens + s <= place;
+    before += __syncthreads_count(at);
+  }
+  return before;
+}
 
 // Row r of 16 of the state's tile T, among its dk: a wave's result rows are
 // then the rows of a matrix operand of 32 in their natural order.
@@ -152,14 +173,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
   // caches (16384 tokens of 32 heads leave 262 MB: both launches 517 us, and 553 from the first on).
   const uint32_t place = gridDim.x / sets - 1u - blockIdx.x / sets, head0 = blockIdx.x % sets * kHeads, khead = head0 / (a.hv / a.hk);
 
-  // the sequence whose places hold this one: as many as begin at or before it, less one
-  int before = 0;
-  for (uint32_t s0 = 0; s0 < a.count; s0 += kThreads) {
-    const uint32_t s = s0 + tid;
-    bool at = false;
-    if (s < a.count) at = first_place(min((uint32_t)max(a.starts[s], 0), a.tokens), s) <= place;
-    before += __syncthreads_count(at);
-  }
+  const int before = sequences_up_to<kThreads>(a, place, kChunk);
   if (before == 0) return;
   const uint32_t seq = (uint32_t)before - 1u;
   const DeltaSeq sq = delta_sequence(a, seq);
@@ -369,12 +383,35 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
 // would spill and keep theirs).
 constexpr int kScanThreads = 512;
 
+// Where a few long sequences leave most CUs without work, the chunks of a
+// sequence are cut into segments that run side by side.  The state after a
+// segment is M S + N of the state S before it, with N what the segment makes of
+// an empty state, and M's columns what it makes of the unit vectors without
+// values.  A launch (kParts) runs the first segment of every sequence, and for
+// the others but the last N and M; the next (kRest) finds each segment's state
+// from N and M of those before it, and runs it.
+//
+// That is up to three times the work, for a chain of two segments and a product
+// per segment instead of all chunks: one sequence of 8192 tokens takes 69 us with
+// one head (168 in one chain), 93 with four (182).
+enum { kChain = 0, kParts = 1, kRest = 2 };
+
 // What both kinds of waves know of their work.
 struct ScanPlace {
-  DeltaSeq sq;
+  DeltaSeq sq;  // (the tokens of the segment)
   uint32_t head, khead, col, place0, chunks, last;  // last: tokens of the last chunk
   bool col_in;
+  bool keep;          // of segments: the state after this one is the sequence's
+  bool unit, output;  // kParts: M's columns; the segment's output is made
+  float *parts;       // kParts: where M's or N's columns go, null: nowhere
 };
+
+// M and N of a segment and head: kDk rows each of kDk and of dv (in 16s) values.
+template <int kTiles>
+__device__ __forceinline__ float *segment_parts(const DeltaArgs &a, uint32_t place, uint32_t head) {
+  constexpr uint32_t kDk = 64 * kTiles;
+  return a.parts + ((uint64_t)place * a.hv + head) * kDk * (kDk + (a.dv + 15u) / 16u * 16u);
+}
 
 // Loads of 16 (or 8) bytes from a uniform base and a lane's 32-bit offset.
 __device__ __forceinline__ uint4 load16(const uint8_t *base, uint32_t off) {
@@ -388,13 +425,15 @@ __device__ __forceinline__ uint4 fragment(const uint8_t *base, uint32_t off) {
 // N bf16 (8 or 4) of a row of q or k from value d0 on, zeros past dk; off in bytes.
 template <int N, bool kWhole>
 __device__ __forceinline__ uint4 load_row(const uint8_t *base, uint32_t off, uint32_t d0, uint32_t dk) {
-  if constexpr (!kWhole) {
+  if (!kWhole && d0 >= dk) return make_uint4(0u, 0u, 0u, 0u);
+  if (!kWhole && d0 + N > dk) {
     uint32_t x[8];
 #pragma unroll
     for (uint32_t i = 0; i < 8; ++i)
       x[i] = i < (uint32_t)N && d0 + i < dk ? *reinterpret_cast<const uint16_t *>(base + off + 2u * i) : 0u;
     return make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
-  } else if constexpr (N == 8) {
+  }
+  if constexpr (N == 8) {
     return load16(base, off);
   } else {
     const Bf16x4 x = *reinterpret_cast<const Bf16x4 *>(base + off);
@@ -405,6 +444,9 @@ __device__ __forceinline__ uint4 load_row(const uint8_t *base, uint32_t off, uin
 // bytes per token of a wave's rows of the keys; the pad spreads banks
 template <int kTiles>
 constexpr int kKeyRow = 32 * kTiles + 16;
+// values per column of the state before a segment, likewise
+template <int kTiles>
+constexpr int kJoinedRow = 64 * kTiles + 4;
 
 template <int kTiles>
 struct ScanLds {
@@ -419,11 +461,15 @@ struct ScanLds {
   } tokens[2];                  // of this chunk and of the next
   uint8_t keys[4][kChunk][kKeyRow<kTiles>];
   uint8_t s[2][2 * kTiles][1024];  // the state's two leading parts: [part][32 rows][lane]
+
+  // the state before a segment, column by column; it and its predecessor lie where the chain's operands come later
+  __device__ float *joined(bool other = false) { return reinterpret_cast<float *>(other ? &keys[0][0][0] : reinterpret_cast<uint8_t *>(part)); }
+  static_assert(16 * kJoinedRow<kTiles> * 4 <= 4 * kChunk * kKeyRow<kTiles> && 16 * kJoinedRow<kTiles> * 4 <= 16 * 64 * 16, "");
 };
 
 __device__ __forceinline__ v8bf as_bf(uint4 x) { return __builtin_bit_cast(v8bf, x); }
 
-template <int kTiles, bool kWhole>
+template <int kTiles, bool kWhole, int kMode>
 __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace &pl, ScanLds<kTiles> &lds, uint32_t w,
                                             uint32_t lane) {
   const uint32_t lr = lane & 15u, lq = lane >> 4;
@@ -435,8 +481,14 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i) {
       const uint32_t r = state_row(w * kTiles + t, lq * 4u + i);
-      s[t][i] = pl.sq.slot >= 0 && !pl.sq.fresh && pl.col_in && r < a.dk ? state[(uint64_t)r * a.dv] : 0.0f;
+      if constexpr (kMode == kRest)
+        s[t][i] = lds.joined()[lr * kJoinedRow<kTiles> + r];
+      else
+        s[t][i] = pl.sq.slot >= 0 && !pl.sq.fresh && (kWhole || (pl.col_in && r < a.dk)) ? state[(uint64_t)r * a.dv] : 0.0f;
+      if constexpr (kMode == kParts)
+        if (pl.unit && r == pl.col) s[t][i] = 1.0f;
     }
+  if constexpr (kMode == kRest) __syncthreads();  // read before its place is filled
 
   // bases of the next chunk to load, and this lane's offsets in bytes
   const uint8_t *mine = a.workspace + ((uint64_t)pl.place0 * a.hv + pl.head) * kHeadBytes;
@@ -610,19 +662,30 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
     for (int t = 0; t < kTiles; ++t) s[t] += s1[t];
   }
 
-  if (pl.sq.slot < 0 || !pl.col_in) return;
+  uint32_t r0 = lq * 4u;
+  asm volatile("" : "+v"(r0));  // the places are worked out again, not kept in registers over the loop
+  if constexpr (kMode == kParts)
+    if (pl.parts != nullptr) {
+      const uint32_t stride = pl.unit ? 64u * kTiles : (a.dv + 15u) / 16u * 16u;
+#pragma unroll
+      for (uint32_t t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) pl.parts[state_row(w * kTiles + t, r0 + i) * stride + pl.col] = s[t][i];
+    }
+  if (pl.sq.slot < 0 || !pl.col_in || (kMode != kChain && !pl.keep)) return;
 #pragma unroll
   for (uint32_t t = 0; t < kTiles; ++t)
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i) {
-      const uint32_t r = state_row(w * kTiles + t, lq * 4u + i);
-      if (r < a.dk) state[(uint64_t)r * a.dv] = s[t][i];
+      const uint32_t r = state_row(w * kTiles + t, r0 + i);
+      if (kWhole || r < a.dk) state[(uint64_t)r * a.dv] = s[t][i];
     }
 }
 
-template <int kTiles, bool kWhole>
+template <int kTiles, bool kWhole, int kMode>
 __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace &pl, ScanLds<kTiles> &lds,
                                             uint32_t w, uint32_t lane) {
+  const bool output = kMode != kParts || pl.output;
   constexpr int kSteps = 2 * kTiles;  // dk in 32s
   const uint32_t lr = lane & 15u, lq = lane >> 4, lane16 = lane * 16u;
   const v4f zero = {0, 0, 0, 0};
@@ -649,7 +712,10 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
   uint4 val;
   float factor, beta;
   auto load_tokens = [&]() {
-    val = load_row<4, kWhole>(vals, v_off, v_col, a.dv);
+    if (kMode == kParts && pl.unit)
+      val = make_uint4(0u, 0u, 0u, 0u);
+    else
+      val = load_row<4, kWhole>(vals, v_off, v_col, a.dv);
     factor = *reinterpret_cast<const float *>(mine + f_off);
     beta = *reinterpret_cast<const float *>(mine + b_off);
   };
@@ -665,10 +731,12 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
       tok.decay = factor;
   };
   auto load_queries = [&]() {
+    if (!output) return;
 #pragma unroll
     for (uint32_t k = 0; k < kSteps; ++k) op_q[k] = load_row<8, kWhole>(queries, q_off + 64u * k, 32u * k + lq * 8u, a.dk);
   };
   auto load_inner = [&]() {
+    if (!output) return;
 #pragma unroll
     for (uint32_t i = 0; i < 2; ++i) op_in[0][i] = fragment(mine, in_off[0] + i * kFragment);
     if (w >= 2u) {
@@ -684,6 +752,7 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
     vals += (uint64_t)kChunk * 2u * a.v_token;
     if (c + 1u == pl.chunks) token_offsets(pl.last);
   };
+  if constexpr (kMode == kRest) __syncthreads();
   token_offsets(pl.chunks == 1u ? pl.last : (uint32_t)kChunk);
   load_tokens();
   load_queries();
@@ -694,6 +763,13 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
   for (uint32_t c = 0; c < pl.chunks; ++c) {
     __syncthreads();
     __syncthreads();
+    if (!output) {  // the tokens alone
+      __syncthreads();
+      put_tokens(c + 1u);
+      if (c + 2u < pl.chunks) advance(c + 2u);
+      load_tokens();
+      continue;
+    }
     // Q S0 for tokens 16w.., beside the chain's longest phase
     v8bf sb[2][kSteps];
 #pragma unroll
@@ -743,41 +819,178 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
   }
 }
 
-template <int kTiles, bool kWhole>
+// The state before segment p > 0 of a sequence: N of the first, then M S + N of
+// each in turn, in binary32.  A wave takes 16 rows; the sum over k runs in the
+// order of block_product.  Bound by M, 64 KB that one CU fetches at 33 KB a us:
+// 1.8 us a step.  (As three bf16 parts, 96 KB, 2.9 us; in a launch of its own,
+// which reads each M once, and twice as far ahead, 5% slower at the best cut.)
+template <int kTiles>
+__device__ __forceinline__ void join_segments(const DeltaArgs &a, ScanLds<kTiles> &lds, uint32_t place0, uint32_t p,
+                                              uint32_t head, uint32_t col0, uint32_t w, uint32_t lane) {
+  constexpr uint32_t kDk = 64 * kTiles, kRow = kJoinedRow<kTiles>;
+  const uint32_t lr = lane & 15u, lq = lane >> 4, n_stride = (a.dv + 15u) / 16u * 16u;
+  const bool works = 16u * w < kDk;
+  const uint32_t m_off = (16u * w + lr) * kDk + lq * 4u, n_off = kDk * kDk + (16u * w + lq * 4u) * n_stride + col0 + lr;
+  float4 m[kDk / 16];
+  v4f n;
+  auto load = [&](uint32_t q) {
+    const float *from = segment_parts<kTiles>(a, place0 + q, head);
+    if (q > 0u) {
+#pragma unroll
+      for (uint32_t i = 0; i < kDk / 16; ++i) m[i] = *reinterpret_cast<const float4 *>(from + m_off + 16u * i);
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) n[i] = from[n_off + i * n_stride];
+  };
+  if (works) load(0);
+  for (uint32_t q = 0; q < p; ++q) {
+    // two places in turn; the last state lies where carry_state looks for it
+    const float *before = lds.joined(((p - q) & 1u) != 0u);
+    float *after = lds.joined(((p - q) & 1u) == 0u);
+    if (works) {
+      v4f x = n, y = {0, 0, 0, 0};
+      if (q > 0u) {
+#pragma unroll
+        for (uint32_t i = 0; i < kDk / 16; ++i) {
+          const float4 f = *reinterpret_cast<const float4 *>(before + lr * kRow + 16u * i + lq * 4u);
+          x = __builtin_amdgcn_mfma_f32_16x16x4f32(m[i].x, f.x, x, 0, 0, 0);
+          y = __builtin_amdgcn_mfma_f32_16x16x4f32(m[i].y, f.y, y, 0, 0, 0);
+          x = __builtin_amdgcn_mfma_f32_16x16x4f32(m[i].z, f.z, x, 0, 0, 0);
+          y = __builtin_amdgcn_mfma_f32_16x16x4f32(m[i].w, f.w, y, 0, 0, 0);
+        }
+      }
+      if (q + 1u < p) load(q + 1u);
+      *reinterpret_cast<v4f *>(after + lr * kRow + 16u * w + lq * 4u) = x + y;
+    }
+    __syncthreads();
+  }
+}
+
+template <int kTiles, bool kWhole, int kMode>
 __global__ __launch_bounds__(kScanThreads, kWhole ? 4 : 2) void delta_scan_kernel(const DeltaArgs a) {
   __shared__ __attribute__((aligned(16))) ScanLds<kTiles> lds;
+  constexpr uint32_t kDk = 64 * kTiles;
   const uint32_t lane = threadIdx.x & 63u, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // Workgroups go round the eight XCDs: the column blocks of a head all to one,
   // so that its L2 serves the chunk's operands to all of them.
-  const uint32_t blocks = (a.dv + 15u) / 16u;
-  const uint32_t j = blockIdx.x >> 3, pair = (j / blocks) * 8u + (blockIdx.x & 7u);
-  if (pair >= a.count * a.hv) return;
-  const uint32_t seq = pair / a.hv;
+  const uint32_t v_blocks = (a.dv + 15u) / 16u, blocks = v_blocks + (kMode == kParts ? kDk / 16u : 0u);
+  const uint32_t j = blockIdx.x >> 3, pair = (j / blocks) * 8u + (blockIdx.x & 7u), block = j % blocks;
+  const uint32_t place = pair / a.hv;  // the sequence, or the segment's place
   ScanPlace pl;
+  uint32_t seq = place, p = 0;
+  if constexpr (kMode == kChain) {
+    if (place >= a.count) return;
+  } else {
+    const uint32_t in = a.segment * kChunk;
+    if (place >= segment_places(a.tokens, a.count, a.segment)) return;
+    const int before = sequences_up_to<kScanThreads>(a, place, in);
+    if (before == 0) return;
+    seq = (uint32_t)before - 1u;
+  }
   pl.sq = delta_sequence(a, seq);
-  pl.head = pair - seq * a.hv;
+  pl.head = pair - place * a.hv;
   pl.khead = pl.head / (a.hv / a.hk);
-  pl.col = (j % blocks) * 16u + (lane & 15u);
+  pl.col = block * 16u + (lane & 15u);
   pl.col_in = pl.col < a.dv;
-  pl.place0 = first_place(pl.sq.begin, seq);
+  pl.keep = pl.output = true;
+  pl.unit = false;
+  pl.parts = nullptr;
   const uint32_t tokens = pl.sq.end - pl.sq.begin;
+  pl.chunks = (tokens + kChunk - 1u) / kChunk;
+  pl.last = tokens - (pl.chunks - 1u) * kChunk;
+  pl.place0 = first_place(pl.sq.begin, seq);
+  if constexpr (kMode != kChain) {
+    const uint32_t first = pl.sq.begin / (a.segment * kChunk) + seq;
+    p = place - first;
+    const uint32_t c0 = p * a.segment, all = pl.chunks;
+    if (p > 0u && c0 >= all) return;  // a place of no segment
+    const bool is_last = c0 + a.segment >= all;
+    if (kMode == kParts && (block < v_blocks ? p > 0u && is_last : p == 0u || is_last)) return;
+    if (kMode == kRest && p == 0u) return;
+    if (!is_last) {
+      pl.chunks = a.segment;
+      pl.last = kChunk;
+      pl.keep = false;
+    } else {
+      pl.chunks = all - c0;
+    }
+    if (kMode == kParts) {
+      if (p > 0u) {
+        pl.sq.fresh = true;  // from zeros
+        pl.output = false;
+        pl.unit = block >= v_blocks;
+      }
+      if (!is_last) {
+        if (pl.unit) pl.col -= v_blocks * 16u;
+        pl.parts = segment_parts<kTiles>(a, place, pl.head) + (pl.unit ? 0u : kDk * kDk);
+      }
+    } else {
+      join_segments<kTiles>(a, lds, first, p, pl.head, block * 16u, w, lane);
+    }
+    pl.place0 += c0;
+    pl.sq.begin += c0 * kChunk;
+  }
   if (tokens == 0u) {  // an empty sequence keeps its state, or loses it
     if (pl.sq.fresh && pl.sq.slot >= 0 && pl.col_in)
       for (uint32_t r = threadIdx.x >> 4; r < a.dk; r += kScanThreads / 16)
         a.state[(((uint64_t)pl.sq.slot * a.hv + pl.head) * a.dk + r) * a.dv + pl.col] = 0.0f;
     return;
   }
-  pl.chunks = (tokens + kChunk - 1u) / kChunk;
-  pl.last = tokens - (pl.chunks - 1u) * kChunk;
   // both take part in every barrier: three per chunk
   if (w < 4u)
-    carry_state<kTiles, kWhole>(a, pl, lds, w, lane);
+    carry_state<kTiles, kWhole, kMode>(a, pl, lds, w, lane);
   else
-    make_output<kTiles, kWhole>(a, pl, lds, w - 4u, lane);
+    make_output<kTiles, kWhole, kMode>(a, pl, lds, w - 4u, lane);
+}
+
+// What a launch of the chain takes per chunk, in us, with that many workgroups
+// (two on a CU hardly hide each other's waits).
+double chain_cost(double groups) { return 1.25 * (0.9 * groups > kCus ? 0.9 * groups / kCus : 1.0); }
+
+// Chunks of a segment; 0: the sequences are not cut.  From the sizes alone, as
+// the lengths lie on the device: as if all sequences were equally long.  The
+// constants are fitted to 60 sizes, among them (us, not cut / cut in 4 / 8 / 16
+// / 32 chunks): 1024 tokens of 4 heads 38 / 39 / 45; 2048 of 1 head 54 / 42 /
+// 46 / 62; 8192 of 4 heads 182 / 218 / 118 / 93 / 121; of 8 heads 190 / 386 /
+// 196 / 147 / 138; of 16 heads 203 / 719 / 353 / 249 / 215.
+uint32_t segment_chunks(uint32_t tokens, uint32_t count, uint32_t hv, uint32_t dk, uint32_t dv) {
+  if (count == 0u) return 0u;
+  const double chunks = (double)tokens / kChunk / count, heads = (double)count * hv;
+  const double v = (dv + 15u) / 16u, m = dk <= 64u ? 4.0 : 8.0;
+  double best = 0.97 * chunks * chain_cost(heads * v);
+  uint32_t cut = 0;
+  for (uint32_t n = 2; n <= 64; n *= 2) {
+    const double parts = chunks / n;
+    if (parts < 2.0) break;
+    const double rest = heads * v * (parts - 1.0);  // workgroups of the second launch, which all read M's
+    const double join = 1.8 * (m / 8.0) * (m / 8.0) * (1.5 * rest > kCus ? 1.5 * rest / kCus : 1.0);
+    const double t = n * (chain_cost(heads * (v + (parts - 2.0) * (v + m))) + chain_cost(rest)) + join * (parts - 2.0) + 15.0;
+    if (t < best) {
+      best = t;
+      cut = n;
+    }
+  }
+  return cut;
+}
+
+uint64_t parts_bytes(uint32_t tokens, uint32_t count, uint32_t hv, uint32_t dk, uint32_t dv, uint32_t segment) {
+  const uint64_t rows = dk <= 64u ? 64u : 128u;
+  return segment ? (uint64_t)segment_places(tokens, count, segment) * hv * rows * (rows + (dv + 15u) / 16u * 16u) * 4u : 0u;
+}
+
+template <int kTiles, int kMode>
+hipError_t launch_scan(const DeltaArgs &a, uint64_t places, hipStream_t s) {
+  const uint32_t blocks = (a.dv + 15u) / 16u + (kMode == kParts ? 4u * kTiles : 0u);
+  const dim3 grid((uint32_t)((places * a.hv + 7u) / 8u * 8u * blocks));
+  if (a.dk == 64u * kTiles && a.dv % 16u == 0u)
+    hipLaunchKernelGGL((delta_scan_kernel<kTiles, true, kMode>), grid, dim3(kScanThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((delta_scan_kernel<kTiles, false, kMode>), grid, dim3(kScanThreads), 0, s, a);
+  return hipGetLastError();
 }
 
 template <int kTiles>
-hipError_t launch_chunked(const DeltaArgs &a, hipStream_t s) {
+hipError_t launch_chunked(DeltaArgs a, hipStream_t s) {
   const uint64_t places = a.tokens / kChunk + (uint64_t)a.count;
   if (a.tokens > 0) {
     if (a.hv / a.hk % 2u == 0u)
@@ -787,20 +1000,19 @@ hipError_t launch_chunked(const DeltaArgs &a, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const uint64_t pairs = ((uint64_t)a.count * a.hv + 7u) / 8u * 8u;
-  const dim3 grid((uint32_t)(pairs * ((a.dv + 15u) / 16u)));
-  if (a.dk == 64u * kTiles && a.dv % 16u == 0u)
-    hipLaunchKernelGGL((delta_scan_kernel<kTiles, true>), grid, dim3(kScanThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL((delta_scan_kernel<kTiles, false>), grid, dim3(kScanThreads), 0, s, a);
-  return hipGetLastError();
+  a.segment = segment_chunks(a.tokens, a.count, a.hv, a.dk, a.dv);
+  if (a.segment == 0u) return launch_scan<kTiles, kChain>(a, a.count, s);
+  a.parts = reinterpret_cast<float *>(a.workspace + places * a.hv * kHeadBytes);
+  const uint32_t segments = segment_places(a.tokens, a.count, a.segment);
+  const hipError_t e = launch_scan<kTiles, kParts>(a, segments, s);
+  return e != hipSuccess ? e : launch_scan<kTiles, kRest>(a, segments, s);
 }
 
 }  // namespace
 
-uint64_t delta_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hk, uint32_t hv, uint32_t dk) {
+uint64_t delta_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hv, uint32_t dk, uint32_t dv) {
   const uint64_t places = tokens / kChunk + (uint64_t)count;
-  return places * hv * kHeadBytes;
+  return places * hv * kHeadBytes + parts_bytes(tokens, count, hv, dk, dv, segment_chunks(tokens, count, hv, dk, dv));
 }
 
 hipError_t launch_delta_chunked(const DeltaArgs &a, hipStream_t s) {
