@@ -24,6 +24,8 @@
 // G stay exact next to a strong decay.
 #include "delta_common.h"
 
+#include <type_traits>
+
 namespace bqmm {
 namespace {
 
@@ -148,43 +150,79 @@ __device__ __forceinline__ void put_triangle(const float *m, uint8_t *out, uint3
     *reinterpret_cast<uint4 *>(p + i * kFragment) = make_uint4(parts[0][i], parts[1][i], parts[2][i], parts[3][i]);
 }
 
-// A workgroup takes a chunk, a key head, and kHeads of its value heads, one
-// after the other: they share the keys, the queries and their products.
-template <int kDk, int kHeads>
+// x added over the 8 or 16 lanes of a row of kDk values (eight to a lane).
+template <int kLanes>
+__device__ __forceinline__ float add_lanes(float x) {
+  auto moved = [](float v, auto how) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(how)::value, 0xF, 0xF, true));
+  };
+  x += moved(x, std::integral_constant<int, 0xB1>{});              // the neighbour
+  x += moved(x, std::integral_constant<int, 0x4E>{});              // the other pair of four
+  x += moved(x, std::integral_constant<int, 0x141>{});             // the other four of eight
+  if (kLanes == 16) x += moved(x, std::integral_constant<int, 0x140>{});  // the other eight
+  return x;
+}
+
+// A workgroup takes a chunk, a key head, and kHeads of its value heads, side by
+// side: they share the keys, the queries and their products, and each step's
+// waits.  Bound by those waits, not by memory (2048 tokens of 32 heads leave 33
+// MB in 17 us): two workgroups fit a CU, and one alone takes 8 us.  One head
+// after the other, three workgroups a CU: 19 us, and 10 alone.
+template <int kDk, int kHeads, bool kWhole>
 __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a) {
   constexpr int kRow = kDk + 8;  // bf16 per staged row
   constexpr uint32_t kBuffer = kChunk * kStride * 4;
-  static_assert(kHeads <= 2, "two betas fit the pad");
+  static_assert(kHeads <= 2, "two betas fit the pad, two inverses the keys' and queries' place");
   static_assert(kChunk * kRow * 2 <= kBuffer, "the staged keys and queries fit the buffers that replace them");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[3 * kBuffer];
-  __shared__ double sum_g[kHeads][kChunk];  // of g log2(e): decays are powers of two
+  __shared__ __attribute__((aligned(16))) uint8_t lds[(2 + kHeads) * kBuffer];
+  __shared__ __attribute__((aligned(16))) double sum_g[kHeads][kChunk];  // of g log2(e): decays are powers of two
   uint16_t *keys = reinterpret_cast<uint16_t *>(lds), *queries = reinterpret_cast<uint16_t *>(lds + kBuffer);
-  float *inverse = reinterpret_cast<float *>(lds);             // in the keys' place
-  float *inner = reinterpret_cast<float *>(lds + kBuffer);     // in the queries' place
-  float *lower = reinterpret_cast<float *>(lds + 2 * kBuffer);
-  // a token's norms and betas lie in the pad of lower's rows (three workgroups fit a CU that way)
-  auto norm_k = [&](uint32_t t) -> float & { return lower[t * kStride + kChunk]; };
-  auto norm_q = [&](uint32_t t) -> float & { return lower[t * kStride + kChunk + 1]; };
-  auto betas = [&](uint32_t h, uint32_t t) -> float & { return lower[t * kStride + kChunk + 2 + h]; };
+  auto inverse = [&](uint32_t h) { return reinterpret_cast<float *>(lds + h * kBuffer); };  // where they were
+  auto lower = [&](uint32_t h) { return reinterpret_cast<float *>(lds + (2 + h) * kBuffer); };
+  // a token's norms and betas lie in the pad of the first one's rows
+  auto norm_k = [&](uint32_t t) -> float & { return lower(0)[t * kStride + kChunk]; };
+  auto norm_q = [&](uint32_t t) -> float & { return lower(0)[t * kStride + kChunk + 1]; };
+  auto betas = [&](uint32_t h, uint32_t t) -> float & { return lower(0)[t * kStride + kChunk + 2 + h]; };
 
-  const uint32_t tid = threadIdx.x, lane = tid & 63u, w = tid >> 6, lr = lane & 15u, lq = lane >> 4;
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, w = __builtin_amdgcn_readfirstlane(tid >> 6), lr = lane & 15u, lq = lane >> 4;
   const uint32_t sets = a.hv / kHeads;  // of value heads
   // From the last chunk to the first, so that what the second launch begins with was written last and is still in the
   // caches (16384 tokens of 32 heads leave 262 MB: both launches 517 us, and 553 from the first on).
   const uint32_t place = gridDim.x / sets - 1u - blockIdx.x / sets, head0 = blockIdx.x % sets * kHeads, khead = head0 / (a.hv / a.hk);
 
-  const int before = sequences_up_to<kThreads>(a, place, kChunk);
-  if (before == 0) return;
-  const uint32_t seq = (uint32_t)before - 1u;
-  const DeltaSeq sq = delta_sequence(a, seq);
-  const uint32_t t0 = sq.begin + (place - first_place(sq.begin, seq)) * kChunk;
-  if (t0 >= sq.end) return;
-  const uint32_t n = min(sq.end - t0, (uint32_t)kChunk);
+  // the sequence that the place belongs to: the last whose first place is at or below it
+  __shared__ uint32_t found[3];
+  bool any = false;
+  for (uint32_t s0 = 0; s0 < a.count; s0 += kThreads) {
+    const uint32_t s = s0 + tid;
+    bool at = false;
+    if (s < a.count) {
+      const uint32_t begin = min((uint32_t)max(a.starts[s], 0), a.tokens), end = min((uint32_t)max(a.starts[s + 1u], 0), a.tokens);
+      at = first_place(begin, s) <= place;
+      if (at && (s + 1u == a.count || first_place(end, s + 1u) > place)) {
+        found[0] = begin;
+        found[1] = end;
+        found[2] = first_place(begin, s);
+      }
+    }
+    any |= __syncthreads_or(at) != 0;
+  }
+  if (!any) return;
+  const uint32_t t0 = found[0] + (place - found[2]) * kChunk, t_end = found[1];
+  if (t0 >= t_end) return;
+  const uint32_t n = min(t_end - t0, (uint32_t)kChunk);
 
   // keys and queries into LDS, zeros past the chunk's end and past dk; their
   // norms on the way (the lanes of a row lie side by side)
   {
     constexpr uint32_t kVecs = kDk / 8;
+    // a wave for each value head: its sums of g, its betas (ahead of the keys, whose way it shares)
+    float gt = 0.0f, beta = 0.0f;
+    if (w < (uint32_t)kHeads) {
+      const uint64_t at = (uint64_t)(t0 + min(lane, n - 1u)) * a.hv + head0 + w;
+      gt = a.g[at];
+      beta = a.beta[at];
+    }
     const uint16_t *kbase = a.k + (uint64_t)t0 * a.k_token + (uint64_t)khead * a.k_head;
     const uint16_t *qbase = a.q + (uint64_t)t0 * a.q_token + (uint64_t)khead * a.q_head;
     uint4 kv[kVecs / 4], qv[kVecs / 4];
@@ -192,7 +230,13 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
     for (uint32_t i = 0; i < kVecs / 4; ++i) {
       const uint32_t r = (i * kThreads + tid) / kVecs, c = tid % kVecs * 8u;
       kv[i] = qv[i] = make_uint4(0, 0, 0, 0);
-      if (r < n) {
+      if constexpr (kWhole) {  // (no branch around the loads: they leave together)
+        const uint32_t at = min(r, n - 1u);
+        const Bf16x8 x = *reinterpret_cast<const Bf16x8 *>(kbase + (uint64_t)at * a.k_token + c);
+        const Bf16x8 y = *reinterpret_cast<const Bf16x8 *>(qbase + (uint64_t)at * a.q_token + c);
+        kv[i] = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+        qv[i] = make_uint4(y.w[0], y.w[1], y.w[2], y.w[3]);
+      } else if (r < n) {
         const uint16_t *kp = kbase + (uint64_t)r * a.k_token + c, *qp = qbase + (uint64_t)r * a.q_token + c;
         if (c + 8u <= a.dk) {
           const Bf16x8 x = *reinterpret_cast<const Bf16x8 *>(kp), y = *reinterpret_cast<const Bf16x8 *>(qp);
@@ -210,10 +254,8 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
         }
       }
     }
-    // a wave for each value head: its sums of g, its betas
     if (w < (uint32_t)kHeads) {
-      const uint64_t at = (uint64_t)(t0 + min(lane, n - 1u)) * a.hv + head0 + w;
-      const float gt = lane < n ? a.g[at] : 0.0f;
+      if (lane >= n) gt = 0.0f;
       double g = (double)(gt < kNoDecay ? kNoDecay : gt) * 1.4426950408889634;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
@@ -221,11 +263,12 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
         g += lane >= (uint32_t)d ? o : 0.0;
       }
       sum_g[w][lane] = g;
-      betas(w, lane) = lane < n ? a.beta[at] : 0.0f;
+      betas(w, lane) = lane < n ? beta : 0.0f;
     }
 #pragma unroll
     for (uint32_t i = 0; i < kVecs / 4; ++i) {
       const uint32_t r = (i * kThreads + tid) / kVecs, c = tid % kVecs * 8u;
+      if (kWhole && r >= n) kv[i] = qv[i] = make_uint4(0, 0, 0, 0);
       *reinterpret_cast<uint4 *>(keys + r * kRow + c) = kv[i];
       *reinterpret_cast<uint4 *>(queries + r * kRow + c) = qv[i];
       const uint32_t kw[4] = {kv[i].x, kv[i].y, kv[i].z, kv[i].w}, qw[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
@@ -237,20 +280,22 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
         sk = fmaf(x, x, fmaf(y, y, sk));
         sq2 = fmaf(u, u, fmaf(v, v, sq2));
       }
-#pragma unroll
-      for (int d = 1; d < (int)kVecs; d <<= 1) {
-        sk += __shfl_xor(sk, d);
-        sq2 += __shfl_xor(sq2, d);
-      }
+      sk = add_lanes<kVecs>(sk);
+      sq2 = add_lanes<kVecs>(sq2);
       if (c == 0u) {
-        norm_k(r) = a.l2norm ? 1.0f / sqrtf(sk + kNormEps) : 1.0f;
-        norm_q(r) = (a.l2norm ? 1.0f / sqrtf(sq2 + kNormEps) : 1.0f) * a.scale;
+        norm_k(r) = sk;
+        norm_q(r) = sq2;
       }
     }
   }
   __syncthreads();
+  if (w < 2u) {  // a wave for the keys, one for the queries: the sums' roots
+    float &x = w == 0u ? norm_k(lane) : norm_q(lane);
+    x = (a.l2norm ? 1.0f / sqrtf(x + kNormEps) : 1.0f) * (w == 0u ? 1.0f : a.scale);
+  }
 
-  // k.k and q.k: rows 16w.. by the wave, the tiles of the lower triangle
+  // k.k and k.q for tokens 16w.., the tiles of the lower triangle: a lane has
+  // token 16w + lr and four keys 16j + 4 lq.. in each
   v4f kk[4], qk[4];
 #pragma unroll
   for (uint32_t j = 0; j < 4; ++j) {
@@ -262,105 +307,132 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
         const v8bf kr = *reinterpret_cast<const v8bf *>(keys + (16 * w + lr) * kRow + 32 * ks + lq * 8);
         const v8bf qr = *reinterpret_cast<const v8bf *>(queries + (16 * w + lr) * kRow + 32 * ks + lq * 8);
         const v8bf kc = *reinterpret_cast<const v8bf *>(keys + (16 * j + lr) * kRow + 32 * ks + lq * 8);
-        kk[j] = mfma32(kr, kc, kk[j]);
-        qk[j] = mfma32(qr, kc, qk[j]);
+        kk[j] = mfma32(kc, kr, kk[j]);
+        qk[j] = mfma32(kc, qr, qk[j]);
+      }
+    }
+  }
+  __syncthreads();  // keys and queries have been read
+
+  uint8_t *mine = a.workspace + ((uint64_t)place * a.hv + head0) * kHeadBytes;
+  if (w < (uint32_t)kHeads) {
+    const double g = sum_g[w][lane];
+    const float e = __builtin_amdgcn_exp2f((float)g), beta = betas(w, lane);
+    float *f = reinterpret_cast<float *>(mine + w * kHeadBytes + kTBytes + kInnerBytes) + lane;
+    f[0] = beta;
+    f[kChunk] = beta * e * norm_k(lane);
+    f[2 * kChunk] = lane < n ? __builtin_amdgcn_exp2f((float)(sum_g[w][kChunk - 1] - g)) * norm_k(lane) : 0.0f;
+    f[3 * kChunk] = lane < n ? e * norm_q(lane) : 0.0f;
+    if (lane == kChunk - 1) f[3 * kChunk + 1] = e;
+  }
+
+  // A into LDS; the q.k triangle straight into the workspace: a lane's four
+  // values lie side by side in its fragment.  (All four tiles, those above the
+  // diagonal in vain: without branches between them their waits overlap.)
+  {
+    const uint32_t t = 16u * w + lr;
+    const float tk = norm_k(t), tq = norm_q(t);
+    float sk[4][4];
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j)
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) sk[j][i] = norm_k(16u * j + lq * 4u + i);
+#pragma unroll
+    for (uint32_t h = 0; h < (uint32_t)kHeads; ++h) {
+      const double g = sum_g[h][t];
+      const float row_k = betas(h, t) * tk;
+      double gs[4][4];
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j)
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) gs[j][i] = sum_g[h][16u * j + lq * 4u + i];
+      uint8_t *to = mine + h * kHeadBytes + kTBytes + triangle_fragment(w, 0) * 2u * kFragment + lr * 16u + (lq >> 1) * 256u + (lq & 1u) * 8u;
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) {
+        float x[4], y[4];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+          const uint32_t s = 16u * j + lq * 4u + i;
+          // (keys after the token would grow: their power is not taken)
+          const float decay = s <= t ? __builtin_amdgcn_exp2f((float)(g - gs[j][i])) * sk[j][i] : 0.0f;
+          x[i] = s < t ? row_k * decay * kk[j][i] : 0.0f;
+          y[i] = s <= t ? tq * decay * qk[j][i] : 0.0f;
+        }
+        *reinterpret_cast<float4 *>(lower(h) + t * kStride + 16u * j + lq * 4u) = make_float4(x[0], x[1], x[2], x[3]);
+        if (j >= 2u && w < 2u) continue;  // no such fragment
+        uint32_t lo[2], hi[2];
+        split2<2>(y[0], y[1], lo);
+        split2<2>(y[2], y[3], hi);
+#pragma unroll
+        for (uint32_t i = 0; i < 2; ++i)
+          *reinterpret_cast<uint2 *>(to + ((j >> 1) * 2u + i) * kFragment + (j & 1u) * 512u) = make_uint2(lo[i], hi[i]);
       }
     }
   }
 
-  for (int h = 0; h < kHeads; ++h) {
-    uint8_t *mine = a.workspace + ((uint64_t)place * a.hv + head0 + h) * kHeadBytes;
-    __syncthreads();  // keys and queries, or the last head's matrices, have been read
-    if (w == 0) {
-      const double g = sum_g[h][lane];
-      const float e = exp2f((float)g), beta = betas(h, lane);
-      float *f = reinterpret_cast<float *>(mine + kTBytes + kInnerBytes) + lane;
-      f[0] = beta;
-      f[kChunk] = beta * e * norm_k(lane);
-      f[2 * kChunk] = lane < n ? exp2f((float)(sum_g[h][kChunk - 1] - g)) * norm_k(lane) : 0.0f;
-      f[3 * kChunk] = lane < n ? e * norm_q(lane) : 0.0f;
-      if (lane == kChunk - 1) f[3 * kChunk + 1] = e;
-    }
-    {
-      double g[4];
-      float row_k[4], row_q[4];
+  // T: the 16 x 16 blocks on the diagonal by substitution (a wave has its own
+  // rows' block of every head, a lane a column), then blocks of 16 and of 32
+  // joined in pairs,
+  //   [[a, 0], [c, b]]^-1 = [[a', 0], [-b' c a', b']].
+  {
+    const uint32_t h = lq & (kHeads - 1u);
+    const float *block = lower(h) + 16u * w * kStride + 16u * w;
+    float t[16];
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) {
-        const uint32_t t = 16u * w + lq * 4u + i;
-        g[i] = sum_g[h][t];
-        row_k[i] = betas(h, t) * norm_k(t);
-        row_q[i] = norm_q(t);
+    for (int i = 0; i < 16; ++i) {
+      float x[4] = {(uint32_t)i == lr ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int m = 0; m < i; m += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(block + i * kStride + m);
+        x[0] = fmaf(-f.x, t[m], x[0]);
+        if (m + 1 < i) x[1] = fmaf(-f.y, t[m + 1], x[1]);
+        if (m + 2 < i) x[2] = fmaf(-f.z, t[m + 2], x[2]);
+        if (m + 3 < i) x[3] = fmaf(-f.w, t[m + 3], x[3]);
       }
-#pragma unroll
-      for (uint32_t j = 0; j < 4; ++j) {
-        if (j > w) continue;
-        const uint32_t s = 16u * j + lr;
-        const double gs = sum_g[h][s];
-        const float ks = norm_k(s);
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-          const uint32_t t = 16u * w + lq * 4u + i;
-          // (rows above the column would grow: their power is not taken)
-          const float decay = s <= t ? __builtin_amdgcn_exp2f((float)(g[i] - gs)) * ks : 0.0f;
-          lower[t * kStride + s] = s < t ? row_k[i] * decay * kk[j][i] : 0.0f;
-          inner[t * kStride + s] = s <= t ? row_q[i] * decay * qk[j][i] : 0.0f;
-        }
-      }
+      t[i] = (x[0] + x[1]) + (x[2] + x[3]);
     }
-    __syncthreads();
-
-    // T: the 16 x 16 blocks on the diagonal by substitution (a lane a column),
-    // then blocks of 16 and of 32 joined in pairs,
-    //   [[a, 0], [c, b]]^-1 = [[a', 0], [-b' c a', b']].
-    if (w == 0) {
-      float t[16];
+    if (lq < (uint32_t)kHeads) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float *row = lower + (16 * lq + i) * kStride + 16 * lq;
-        float x[4] = {(uint32_t)i == lr ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int m = 0; m < i; m += 4) {
-          const float4 f = *reinterpret_cast<const float4 *>(row + m);
-          x[0] = fmaf(-f.x, t[m], x[0]);
-          if (m + 1 < i) x[1] = fmaf(-f.y, t[m + 1], x[1]);
-          if (m + 2 < i) x[2] = fmaf(-f.z, t[m + 2], x[2]);
-          if (m + 3 < i) x[3] = fmaf(-f.w, t[m + 3], x[3]);
-        }
-        t[i] = (x[0] + x[1]) + (x[2] + x[3]);
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) inverse[(16 * lq + i) * kStride + 16 * lq + lr] = t[i];
-    } else {
-      // meanwhile the other waves put the q.k triangle away, two fragments each
-      for (uint32_t f = 2u * w - 2u; f < 2u * w; ++f)
-        put_triangle<2>(inner, mine + kTBytes, f < 2u ? f : f / 2u + 1u, f < 2u ? 0u : f & 1u, lane);
+      for (int i = 0; i < 16; ++i) inverse(h)[(16u * w + i) * kStride + 16u * w + lr] = t[i];
     }
-    __syncthreads();
-    if (w < 2) {
-      const uint32_t o = 32u * w;
-      const v4f x = block_product(lower + (o + 16) * kStride + o, inverse + o * kStride + o, v4f{0, 0, 0, 0}, lr, lq);
-      const v4f y = block_product(inverse + (o + 16) * kStride + o + 16, x, v4f{0, 0, 0, 0}, lr, lq);
+  }
+  __syncthreads();
+  if (w < 2u * kHeads) {
+    const float *l = lower(w >> 1);
+    float *v = inverse(w >> 1);
+    const uint32_t o = 32u * (w & 1u);
+    const v4f x = block_product(l + (o + 16) * kStride + o, v + o * kStride + o, v4f{0, 0, 0, 0}, lr, lq);
+    const v4f y = block_product(v + (o + 16) * kStride + o + 16, x, v4f{0, 0, 0, 0}, lr, lq);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) inverse[(o + 16 + lq * 4 + i) * kStride + o + lr] = -y[i];
-    }
-    __syncthreads();
-    {
-      const uint32_t jt = w & 1u, rt = w >> 1;
-      v4f x[2], y = {0, 0, 0, 0};
+    for (int i = 0; i < 4; ++i) v[(o + 16 + lq * 4 + i) * kStride + o + lr] = -y[i];
+  }
+  __syncthreads();
+  {
+    const uint32_t jt = w & 1u, rt = w >> 1;
+    v4f x[kHeads][2], y[kHeads];
+#pragma unroll
+    for (uint32_t h = 0; h < (uint32_t)kHeads; ++h)
 #pragma unroll
       for (uint32_t r = 0; r < 2; ++r) {
-        x[r] = v4f{0, 0, 0, 0};
+        x[h][r] = v4f{0, 0, 0, 0};
+        if (r > rt) continue;
         for (uint32_t kt = jt; kt < 2; ++kt)
-          x[r] = block_product(lower + (32 + 16 * r) * kStride + 16 * kt, inverse + 16 * kt * kStride + 16 * jt, x[r], lr, lq);
+          x[h][r] = block_product(lower(h) + (32 + 16 * r) * kStride + 16 * kt, inverse(h) + 16 * kt * kStride + 16 * jt, x[h][r], lr, lq);
       }
-      y = block_product(inverse + (32 + 16 * rt) * kStride + 32, x[0], y, lr, lq);
-      if (rt == 1u) y = block_product(inverse + 48 * kStride + 48, x[1], y, lr, lq);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) inverse[(32 + 16 * rt + lq * 4 + i) * kStride + 16 * jt + lr] = -y[i];
+    for (uint32_t h = 0; h < (uint32_t)kHeads; ++h) {
+      y[h] = block_product(inverse(h) + (32 + 16 * rt) * kStride + 32, x[h][0], v4f{0, 0, 0, 0}, lr, lq);
+      if (rt == 1u) y[h] = block_product(inverse(h) + 48 * kStride + 48, x[h][1], y[h], lr, lq);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) inverse(h)[(32 + 16 * rt + lq * 4 + i) * kStride + 16 * jt + lr] = -y[h][i];
     }
-    __syncthreads();
-    for (uint32_t f = w; f < kTriangle; f += 4)
-      put_triangle<3>(inverse, mine, f < 2u ? f : f / 2u + 1u, f < 2u ? 0u : f & 1u, lane);
+  }
+  __syncthreads();
+#pragma unroll
+  for (uint32_t i0 = 0; i0 < kTriangle * kHeads; i0 += 4) {
+    const uint32_t i = i0 + w, h = i / kTriangle, f = i % kTriangle;
+    if (i >= kTriangle * kHeads) break;
+    put_triangle<3>(inverse(h), mine + h * kHeadBytes, f < 2u ? f : f / 2u + 1u, f < 2u ? 0u : f & 1u, lane);
   }
 }
 
@@ -993,10 +1065,18 @@ template <int kTiles>
 hipError_t launch_chunked(DeltaArgs a, hipStream_t s) {
   const uint64_t places = a.tokens / kChunk + (uint64_t)a.count;
   if (a.tokens > 0) {
+    const auto launch = [&](auto heads) {
+      constexpr int kHeads = decltype(heads)::value;
+      const dim3 grid((uint32_t)(places * (a.hv / kHeads)));
+      if (a.dk == 64u * kTiles)
+        hipLaunchKernelGGL((delta_chunk_kernel<64 * kTiles, kHeads, true>), grid, dim3(kThreads), 0, s, a);
+      else
+        hipLaunchKernelGGL((delta_chunk_kernel<64 * kTiles, kHeads, false>), grid, dim3(kThreads), 0, s, a);
+    };
     if (a.hv / a.hk % 2u == 0u)
-      hipLaunchKernelGGL((delta_chunk_kernel<64 * kTiles, 2>), dim3((uint32_t)(places * (a.hv / 2u))), dim3(kThreads), 0, s, a);
+      launch(std::integral_constant<int, 2>{});
     else
-      hipLaunchKernelGGL((delta_chunk_kernel<64 * kTiles, 1>), dim3((uint32_t)(places * a.hv)), dim3(kThreads), 0, s, a);
+      launch(std::integral_constant<int, 1>{});
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
