@@ -166,8 +166,8 @@ __device__ __forceinline__ float add_lanes(float x) {
 // A workgroup takes a chunk, a key head, and kHeads of its value heads, side by
 // side: they share the keys, the queries and their products, and each step's
 // waits.  Bound by those waits, not by memory (2048 tokens of 32 heads leave 33
-// MB in 17 us): two workgroups fit a CU, and one alone takes 8 us.  One head
-// after the other, three workgroups a CU: 19 us, and 10 alone.
+// MB in 17 us): two workgroups fit a CU, and one alone takes 9 us.  One head
+// after the other, three workgroups a CU: 19 us, and 12 alone.
 template <int kDk, int kHeads, bool kWhole>
 __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a) {
   constexpr int kRow = kDk + 8;  // bf16 per staged row
@@ -464,8 +464,8 @@ constexpr int kScanThreads = 512;
 // from N and M of those before it, and runs it.
 //
 // That is up to three times the work, for a chain of two segments and a product
-// per segment instead of all chunks: one sequence of 8192 tokens takes 69 us with
-// one head (168 in one chain), 93 with four (182).
+// per segment instead of all chunks: one sequence of 8192 tokens takes 67 us with
+// one head (169 in one chain), 89 with four (182).
 enum { kChain = 0, kParts = 1, kRest = 2 };
 
 // What both kinds of waves know of their work.

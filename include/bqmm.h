@@ -307,8 +307,8 @@ int silu_mul_bf16(const void *gate, const void *up, void *out, uint64_t count, v
  *                               rint(127 t / top) (exact quotient, ties to even) and
  *                               scale = top / (127 sqrt(...)); zero codes where top is 0.
  * A row that holds a NaN or an infinity gives NaN: in bf16 where the formula
- * does, in int8 rows as a NaN scale; its q8_1 bytes are unspecified.  m, k >= 1;
- * any k.  No two buffers may overlap. */
+ * does, in int8 rows as a NaN scale; its q8_1 bytes are unspecified.  |h * weight|
+ * has to stay below 2^128.  m, k >= 1; any k.  No two buffers may overlap. */
 int add_rms_norm_bf16(const void *x_bf16, void *residual_bf16, const void *weight_bf16, void *out_bf16,
                       uint32_t m, uint32_t k, double eps, void *stream);
 int add_rms_norm_quantize_q8_1(const void *x_bf16, void *residual_bf16, const void *weight_bf16, void *out_q8,
@@ -355,6 +355,9 @@ int w8a8_gemm(const void *act_i8, const void *w_i8, const void *bias_bf16, void 
  * tokens = 0 is allowed (the token arrays may be NULL), and count = 0 (nothing
  * is done).  Captured into a graph, a call reads starts, slots and fresh at
  * each replay.
+ *
+ * A NaN or an infinity in a token stays in its sequence and head, and in the
+ * tokens from it on (_chunked: from the beginning of its chunk of 64 on).
  *
  * _recurrent takes the tokens of a sequence one by one: for decoding, and for
  * a few tokens.  _chunked takes them in chunks of 64, within a chunk by matrix
