@@ -825,6 +825,32 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
     if (c + 1u == pl.chunks) token_offsets(pl.last);
   };
   if constexpr (kMode == kRest) __syncthreads();
+  // The column blocks of a head run side by side on one XCD.  Where the first
+  // launch has left more than the caches hold (256 MB, with q, k and v in them),
+  // each touches its share of the lines of the chunk after the next: two waves
+  // the workspace's, two those of q, k and v (16384 tokens of 32 heads: 506 us,
+  // and 517 without; packed prompts of 2128 tokens, 8 heads: 48.2, and 47.0).
+  const uint8_t *touch = mine;
+  uint64_t touch_step = (uint64_t)a.hv * kHeadBytes;
+  bool touches = false;
+  if (kMode == kChain && (uint64_t)(a.tokens / kChunk + a.count) * a.hv > (128u << 20) / kHeadBytes) {
+    const uint32_t mine_of = __builtin_amdgcn_readfirstlane(pl.col >> 4) + (a.dv + 15u) / 16u * ((w & 1u) * 64u + lane);
+    if (w < 2u) {
+      touch += mine_of * 128u;
+      touches = mine_of < kHeadBytes / 128u;
+    } else {  // token, which of the three, half of the row
+      const uint64_t t = pl.sq.begin + mine_of / 6u;
+      const uint32_t what = mine_of % 6u / 2u, token = what == 0u ? a.q_token : what == 1u ? a.k_token : a.v_token;
+      const uint16_t *row = what == 0u   ? a.q + (uint64_t)pl.khead * a.q_head
+                            : what == 1u ? a.k + (uint64_t)pl.khead * a.k_head
+                                         : a.v + (uint64_t)pl.head * a.v_head;
+      touch = reinterpret_cast<const uint8_t *>(row + t * token + (mine_of & 1u) * min(64u, (what == 2u ? a.dv : a.dk) - 1u));
+      touch_step = (uint64_t)kChunk * 2u * token;
+      touches = mine_of < kChunk * 6u;
+    }
+    touch += 2u * touch_step;
+  }
+  uint32_t touched = 0;
   token_offsets(pl.chunks == 1u ? pl.last : (uint32_t)kChunk);
   load_tokens();
   load_queries();
@@ -834,6 +860,11 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
   load_tokens();
   for (uint32_t c = 0; c < pl.chunks; ++c) {
     __syncthreads();
+    if constexpr (kMode == kChain) {
+      asm volatile("" ::"v"(touched));  // (a step later, so that nothing waits for it)
+      if (touches && c + 3u < pl.chunks) touched = *reinterpret_cast<const uint32_t *>(touch);  // (whole chunks alone)
+      touch += touch_step;
+    }
     __syncthreads();
     if (!output) {  // the tokens alone
       __syncthreads();

@@ -125,3 +125,10 @@ def test_graph_reads_the_ranges_anew(gpu):
         assert torch.equal(out, want[0]) and torch.equal(state, want[1]), i
         d["starts"] = [0, middle, 5600]
         check(d, out.cpu(), state.cpu(), [i % 2] * 2)
+
+
+def test_operands_beyond_the_caches(gpu):
+    """So many chunks of heads that the lines of later ones are touched ahead: the same results at every end."""
+    d = make([64 * 40 + 5, 64 * 31, 1, 64], 64, 64, 16, 64, seed=27)
+    assert bq.gated_delta_rule_workspace_bytes(d["starts"][-1], 4, 64, 64, 16, 64) > 128 << 20
+    check(d, *call(gpu, "chunked", d))
