@@ -516,6 +516,17 @@ __device__ __forceinline__ uint4 load_row(const uint8_t *base, uint32_t off, uin
 // bytes per token of a wave's rows of the keys; the pad spreads banks
 template <int kTiles>
 constexpr int kKeyRow = 32 * kTiles + 16;
+
+// Whether four neighbouring lanes load neighbouring pieces of a row of q or k,
+// so that one access of the CU's cache serves them; the keys then go through
+// LDS before their first product, the queries change lanes.  As the operands lie
+// in the lanes each lane's 16 bytes are an access: 2900 a chunk, which is what
+// two workgroups on a CU wait for (packed prompts of 2322 tokens: 82.6 us, and
+// 86.8 so; 16384 tokens: 474 and 504).  A chain of 64 values has fewer, and the
+// way through LDS is longer (2048 tokens, packed, 1 head: 25.5 and 24.2 us);
+// in segments the registers would not do (8192 tokens, 1 head: 70.1 and 67.1).
+template <int kTiles, bool kWhole, int kMode>
+constexpr bool kQuads = kTiles == 2 && kWhole && kMode == 0;
 // values per column of the state before a segment, likewise
 template <int kTiles>
 constexpr int kJoinedRow = 64 * kTiles + 4;
@@ -565,13 +576,16 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
   // bases of the next chunk to load, and this lane's offsets in bytes
   const uint8_t *mine = a.workspace + ((uint64_t)pl.place0 * a.hv + pl.head) * kHeadBytes;
   const uint8_t *keys = reinterpret_cast<const uint8_t *>(a.k + (uint64_t)pl.khead * a.k_head + (uint64_t)pl.sq.begin * a.k_token);
-  const uint32_t dk0 = state_row(w * kTiles, lq * 4u), lane16 = lane * 16u;
+  // the token (of 16) and the piece of its row that this lane loads
+  constexpr bool kByQuads = kQuads<kTiles, kWhole, kMode>;
+  const uint32_t load_t = kByQuads ? lane >> 2 : lr, load_p = kByQuads ? lane & 3u : lq;
+  const uint32_t dk0 = state_row(w * kTiles, load_p * 4u), lane16 = lane * 16u;
   const uint32_t t_off[2] = {triangle_fragment(w, 0) * 3u * kFragment + lane16, triangle_fragment(w, 1) * 3u * kFragment + lane16};
   uint32_t k_off[4];
   // rows past the sequence's end read its last token: their factors are zero
   auto token_offsets = [&](uint32_t n) {
 #pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) k_off[i] = 2u * (min(16u * i + lr, n - 1u) * a.k_token + dk0);
+    for (uint32_t i = 0; i < 4; ++i) k_off[i] = 2u * (min(16u * i + load_t, n - 1u) * a.k_token + dk0);
   };
 
   uint4 op_k[4], op_t[2][3];
@@ -593,10 +607,21 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
   token_offsets(pl.chunks == 1u ? pl.last : (uint32_t)kChunk);
   load_keys();
   load_inverse();
-  // The update takes the keys with dk as rows: they go through LDS, where each
-  // wave keeps its own rows of all tokens and reads them back transposed
-  // (a group of 16 lanes reads 4 tokens x 16 rows, and lane i gets row i's 4).
-  uint8_t *keys_put = &lds.keys[w][lr][0] + lq * (8u * kTiles);
+  // The keys go through LDS, where each wave keeps its own rows of all tokens:
+  // the product with the state takes them with tokens as rows, the update with
+  // dk as rows, read back transposed (a group of 16 lanes reads 4 tokens x 16
+  // rows, and lane i gets row i's 4).
+  uint8_t *keys_put = &lds.keys[w][load_t][0] + load_p * (8u * kTiles);
+  const uint8_t *keys_rows = &lds.keys[w][lr][0] + lq * (8u * kTiles);
+  auto put_keys = [&]() {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      if constexpr (kTiles == 2)
+        *reinterpret_cast<uint4 *>(keys_put + 16 * m * kKeyRow<kTiles>) = op_k[m];
+      else
+        *reinterpret_cast<uint2 *>(keys_put + 16 * m * kKeyRow<kTiles>) = make_uint2(op_k[m].x, op_k[m].y);
+    }
+  };
   const uint8_t *keys_get = &lds.keys[w][lq * 8u + (lr >> 2)][0] + (lr & 3u) * (8u * kTiles);
   auto transposed = [&](int t, int ks) -> v8bf {
     const uint8_t *from = keys_get + 32 * ks * kKeyRow<kTiles> + t * 8;
@@ -612,6 +637,11 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
       if (c + 2u == pl.chunks) token_offsets(pl.last);
     }
     // K S0 over the wave's rows of the state
+    if constexpr (kByQuads) {
+      put_keys();
+#pragma unroll
+      for (int m = 0; m < 4; ++m) op_k[m] = *reinterpret_cast<const uint4 *>(keys_rows + 16 * m * kKeyRow<kTiles>);
+    }
     uint32_t sp[kTiles][2][3];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
@@ -640,13 +670,7 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
         x[m] = mfma32(as_bf(make_uint4(op_k[m].x, op_k[m].y, op_k[m].x, op_k[m].y)),
                       as_bf(make_uint4(sp[0][0][1], sp[0][1][1], sp[0][0][0], sp[0][1][0])), x[m]);
     }
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      if constexpr (kTiles == 2)
-        *reinterpret_cast<uint4 *>(keys_put + 16 * m * kKeyRow<kTiles>) = op_k[m];
-      else
-        *reinterpret_cast<uint2 *>(keys_put + 16 * m * kKeyRow<kTiles>) = make_uint2(op_k[m].x, op_k[m].y);
-    }
+    if constexpr (!kByQuads) put_keys();
 #pragma unroll
     for (int m = 0; m < 4; ++m) *reinterpret_cast<v4f *>(&lds.part[m * 4 + w][lane]) = x[m];
     __syncthreads();
@@ -772,11 +796,21 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
   const uint32_t f_off = kTBytes + kInnerBytes + (lq == 3u ? 4u * kFactorRow : (lq + 1u) * kFactorRow + (16u * w + lr) * 4u);
   const uint32_t b_off = kTBytes + kInnerBytes + (16u * w + (lane >> 2)) * 4u;
   const uint32_t v_col = pl.col - lr + (lane & 3u) * 4u;
-  uint32_t q_off, v_off, out_off[4];
+  // Step k of the product takes 8 values of row lr: those from 32 k + 8 lq on.
+  // By quads it takes those from 32 lq + 8 k on: lane lr loads them of the row
+  // with k in place of its lowest bits, at these bits' place, and they change.
+  constexpr bool kByQuads = kQuads<kTiles, kWhole, kMode>;
+  uint32_t q_off[kByQuads ? kSteps : 1], v_off, out_off[4];
 #pragma unroll
   for (uint32_t i = 0; i < 4; ++i) out_off[i] = 2u * ((16u * w + lq * 4u + i) * a.hv * a.dv + pl.col);
   auto token_offsets = [&](uint32_t n) {
-    q_off = 2u * (min(16u * w + lr, n - 1u) * a.q_token + lq * 8u);
+    if constexpr (kByQuads) {
+#pragma unroll
+      for (uint32_t k = 0; k < kSteps; ++k)
+        q_off[k] = 2u * (min(16u * w + ((lr & ~3u) | k), n - 1u) * a.q_token + 32u * lq + (lr & 3u) * 8u);
+    } else {
+      q_off[0] = 2u * (min(16u * w + lr, n - 1u) * a.q_token + lq * 8u);
+    }
     v_off = 2u * (min(16u * w + (lane >> 2), n - 1u) * a.v_token + v_col);
   };
 
@@ -805,7 +839,24 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
   auto load_queries = [&]() {
     if (!output) return;
 #pragma unroll
-    for (uint32_t k = 0; k < kSteps; ++k) op_q[k] = load_row<8, kWhole>(queries, q_off + 64u * k, 32u * k + lq * 8u, a.dk);
+    for (uint32_t k = 0; k < kSteps; ++k) op_q[k] = kByQuads ? load16(queries, q_off[k]) : load_row<8, kWhole>(queries, q_off[0] + 64u * k, 32u * k + lq * 8u, a.dk);
+  };
+  // a bit of the lane and one of the step change places
+  auto exchange = [&](auto bit) {
+    constexpr uint32_t kBit = decltype(bit)::value;
+    const bool set = (lane & kBit) != 0u;
+    auto swap = [&](uint32_t &lo, uint32_t &hi) {
+      const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(set ? lo : hi), kBit == 1u ? 0xB1 : 0x4E, 0xF, 0xF, true);
+      if (set) lo = got; else hi = got;
+    };
+#pragma unroll
+    for (uint32_t k = 0; k < kSteps; ++k) {
+      if (k & kBit) continue;
+      swap(op_q[k].x, op_q[k | kBit].x);
+      swap(op_q[k].y, op_q[k | kBit].y);
+      swap(op_q[k].z, op_q[k | kBit].z);
+      swap(op_q[k].w, op_q[k | kBit].w);
+    }
   };
   auto load_inner = [&]() {
     if (!output) return;
@@ -865,6 +916,10 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
       if (touches && c + 3u < pl.chunks) touched = *reinterpret_cast<const uint32_t *>(touch);  // (whole chunks alone)
       touch += touch_step;
     }
+    if constexpr (kByQuads) {
+      exchange(std::integral_constant<uint32_t, 1>{});
+      exchange(std::integral_constant<uint32_t, 2>{});
+    }
     __syncthreads();
     if (!output) {  // the tokens alone
       __syncthreads();
@@ -878,7 +933,9 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
 #pragma unroll
     for (int i = 1; i >= 0; --i)
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) sb[i][k] = *reinterpret_cast<const v8bf *>(&lds.s[i][k][lane16]);
+      for (uint32_t k = 0; k < kSteps; ++k) {
+        sb[i][k] = *reinterpret_cast<const v8bf *>(kByQuads ? &lds.s[i][lq][(k * 16u + lr) * 16u] : &lds.s[i][k][lane16]);
+      }
     const v4f scale = *reinterpret_cast<const v4f *>(&lds.tokens[c & 1u].factor[2][16u * w + lq * 4u]);
     v4f o = zero, o1 = zero;
 #pragma unroll
@@ -969,6 +1026,22 @@ __device__ __forceinline__ void join_segments(const DeltaArgs &a, ScanLds<kTiles
   }
 }
 
+// The sequence (of at most 64) that stands at this place when they are ordered
+// by length, the longest first, equal ones as they come.
+__device__ __forceinline__ uint32_t by_length(const DeltaArgs &a, uint32_t place, uint32_t lane) {
+  int length = -1;
+  if (lane < a.count) {
+    const DeltaSeq sq = delta_sequence(a, lane);
+    length = (int)(sq.end - sq.begin);
+  }
+  uint32_t longer = 0;
+  for (uint32_t s = 0; s < a.count; ++s) {
+    const int other = __builtin_amdgcn_readlane(length, s);
+    longer += other > length || (other == length && s < lane) ? 1u : 0u;
+  }
+  return (uint32_t)__builtin_ctzll(__ballot(lane < a.count && longer == place));
+}
+
 template <int kTiles, bool kWhole, int kMode>
 __global__ __launch_bounds__(kScanThreads, kWhole ? 4 : 2) void delta_scan_kernel(const DeltaArgs a) {
   __shared__ __attribute__((aligned(16))) ScanLds<kTiles> lds;
@@ -983,6 +1056,9 @@ __global__ __launch_bounds__(kScanThreads, kWhole ? 4 : 2) void delta_scan_kerne
   uint32_t seq = place, p = 0;
   if constexpr (kMode == kChain) {
     if (place >= a.count) return;
+    // Where the workgroups do not all start at once, the longest chains go first (8 prompts of 2 to 927 tokens, 16
+    // heads: 45.7 us, and 51.8 in their own order).
+    if (a.count > 1u && a.count <= 64u && a.count * a.hv * v_blocks > kCus) seq = by_length(a, place, lane);
   } else {
     const uint32_t in = a.segment * kChunk;
     if (place >= segment_places(a.tokens, a.count, a.segment)) return;
