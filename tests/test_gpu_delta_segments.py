@@ -132,3 +132,44 @@ def test_operands_beyond_the_caches(gpu):
     d = make([64 * 40 + 5, 64 * 31, 1, 64], 64, 64, 16, 64, seed=27)
     assert bq.gated_delta_rule_workspace_bytes(d["starts"][-1], 4, 64, 64, 16, 64) > 128 << 20
     check(d, *call(gpu, "chunked", d))
+
+
+def test_longest_sequences_first(gpu):
+    """More workgroups than start at once: equal lengths, empty sequences and slots outside keep their own results."""
+    d = make([3, 130, 0, 130, 70, 1, 0], 8, 16, 128, 128, seed=28)
+    d["slots"][4] = -1
+    fresh = [0, 1, 1, 0, 1, 0, 0]
+    check(d, *call(gpu, "chunked", d, fresh), fresh)
+    want = call(gpu, "chunked", d, fresh)
+    d["starts"] = [-9, *d["starts"][1:-1], 5000]
+    got = call(gpu, "chunked", d, fresh)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("layout", ["odd rows", "odd start", "heads first"])
+@pytest.mark.parametrize("tokens", [130, 2100])
+def test_strides(gpu, layout, tokens):
+    """The layouts of test_gpu_delta_rule's test at heads of 128, in one chain and in segments."""
+    hk, hv, dk, dv = 1, 2, 128, 48
+    d = make([tokens], hk, hv, dk, dv, seed=29, extra=1 if layout == "odd rows" else 16)
+    plain = [x.contiguous().to(gpu) for x in heads(d, d["packed"])]
+    if layout == "odd rows":
+        other = list(heads(d, d["packed"].to(gpu)))
+    elif layout == "odd start":
+        other = []
+        for x in plain:
+            room = torch.zeros(x.numel() + 1, dtype=torch.bfloat16, device=gpu)
+            room[1:].copy_(x.flatten())
+            other.append(room[1:].view(x.shape))
+    else:
+        other = [x.transpose(0, 1).contiguous().transpose(0, 1) for x in plain]
+    results = []
+    for qkv in (plain, other):
+        out, state = torch.zeros(tokens, hv, dv, dtype=torch.bfloat16, device=gpu), d["state"].to(gpu)
+        work = torch.zeros(bq.gated_delta_rule_workspace_bytes(tokens, 1, hk, hv, dk, dv), dtype=torch.uint8, device=gpu)
+        bq.gated_delta_rule_chunked(*qkv, d["g"].to(gpu), d["beta"].to(gpu), out, state,
+                                    torch.tensor([0, tokens], dtype=torch.int32, device=gpu), work,
+                                    slots=d["slots"].to(gpu))
+        results.append((out.cpu(), state.cpu()))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    check(d, *results[0])
