@@ -166,19 +166,19 @@ __device__ __forceinline__ float add_lanes(float x) {
 // A workgroup takes a chunk, a key head, and kHeads of its value heads, side by
 // side: they share the keys, the queries and their products, and each step's
 // waits.  Bound by those waits, not by memory (2048 tokens of 32 heads leave 33
-// MB in 17 us): two workgroups fit a CU, and one alone takes 9 us.  One head
-// after the other, three workgroups a CU: 19 us, and 12 alone.
+// MB in 16 us, one workgroup alone takes 9), so four workgroups share a CU: A
+// lies where the keys and queries were, T in A's place, 128 registers a lane do.
+// (With places of their own, two a CU: packed prompts of 2322 tokens take 84.8
+// us in both launches, and 78.4 so.)
 template <int kDk, int kHeads, bool kWhole>
-__global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a) {
-  constexpr int kRow = kDk + 8;  // bf16 per staged row
-  constexpr uint32_t kBuffer = kChunk * kStride * 4;
-  static_assert(kHeads <= 2, "two betas fit the pad, two inverses the keys' and queries' place");
-  static_assert(kChunk * kRow * 2 <= kBuffer, "the staged keys and queries fit the buffers that replace them");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[(2 + kHeads) * kBuffer];
+__global__ __launch_bounds__(kThreads, 4) void delta_chunk_kernel(const DeltaArgs a) {
+  constexpr int kRow = 2 * kStride;  // bf16 per staged row, which a row of A takes the place of
+  static_assert(kDk <= 2 * kChunk && kHeads <= 2, "a row fits, its pad holds two norms and two betas; a matrix for each staged one");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][kChunk * kStride * 4];
   __shared__ __attribute__((aligned(16))) double sum_g[kHeads][kChunk];  // of g log2(e): decays are powers of two
-  uint16_t *keys = reinterpret_cast<uint16_t *>(lds), *queries = reinterpret_cast<uint16_t *>(lds + kBuffer);
-  auto inverse = [&](uint32_t h) { return reinterpret_cast<float *>(lds + h * kBuffer); };  // where they were
-  auto lower = [&](uint32_t h) { return reinterpret_cast<float *>(lds + (2 + h) * kBuffer); };
+  uint16_t *keys = reinterpret_cast<uint16_t *>(lds[0]), *queries = reinterpret_cast<uint16_t *>(lds[1]);
+  // A of each value head, where the keys and queries were, and T in its place
+  auto lower = [&](uint32_t h) { return reinterpret_cast<float *>(lds[h]); };
   // a token's norms and betas lie in the pad of the first one's rows
   auto norm_k = [&](uint32_t t) -> float & { return lower(0)[t * kStride + kChunk]; };
   auto norm_q = [&](uint32_t t) -> float & { return lower(0)[t * kStride + kChunk + 1]; };
@@ -373,7 +373,8 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
   // T: the 16 x 16 blocks on the diagonal by substitution (a wave has its own
   // rows' block of every head, a lane a column), then blocks of 16 and of 32
   // joined in pairs,
-  //   [[a, 0], [c, b]]^-1 = [[a', 0], [-b' c a', b']].
+  //   [[a, 0], [c, b]]^-1 = [[a', 0], [-b' c a', b']],
+  // each in the place of what it is the last to read.
   {
     const uint32_t h = lq & (kHeads - 1u);
     const float *block = lower(h) + 16u * w * kStride + 16u * w;
@@ -393,15 +394,14 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
     }
     if (lq < (uint32_t)kHeads) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) inverse(h)[(16u * w + i) * kStride + 16u * w + lr] = t[i];
+      for (int i = 0; i < 16; ++i) lower(h)[(16u * w + i) * kStride + 16u * w + lr] = t[i];
     }
   }
   __syncthreads();
   if (w < 2u * kHeads) {
-    const float *l = lower(w >> 1);
-    float *v = inverse(w >> 1);
+    float *v = lower(w >> 1);
     const uint32_t o = 32u * (w & 1u);
-    const v4f x = block_product(l + (o + 16) * kStride + o, v + o * kStride + o, v4f{0, 0, 0, 0}, lr, lq);
+    const v4f x = block_product(v + (o + 16) * kStride + o, v + o * kStride + o, v4f{0, 0, 0, 0}, lr, lq);
     const v4f y = block_product(v + (o + 16) * kStride + o + 16, x, v4f{0, 0, 0, 0}, lr, lq);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[(o + 16 + lq * 4 + i) * kStride + o + lr] = -y[i];
@@ -417,22 +417,25 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(const DeltaArgs a
         x[h][r] = v4f{0, 0, 0, 0};
         if (r > rt) continue;
         for (uint32_t kt = jt; kt < 2; ++kt)
-          x[h][r] = block_product(lower(h) + (32 + 16 * r) * kStride + 16 * kt, inverse(h) + 16 * kt * kStride + 16 * jt, x[h][r], lr, lq);
+          x[h][r] = block_product(lower(h) + (32 + 16 * r) * kStride + 16 * kt, lower(h) + 16 * kt * kStride + 16 * jt, x[h][r], lr, lq);
       }
 #pragma unroll
     for (uint32_t h = 0; h < (uint32_t)kHeads; ++h) {
-      y[h] = block_product(inverse(h) + (32 + 16 * rt) * kStride + 32, x[h][0], v4f{0, 0, 0, 0}, lr, lq);
-      if (rt == 1u) y[h] = block_product(inverse(h) + 48 * kStride + 48, x[h][1], y[h], lr, lq);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) inverse(h)[(32 + 16 * rt + lq * 4 + i) * kStride + 16 * jt + lr] = -y[h][i];
+      y[h] = block_product(lower(h) + (32 + 16 * rt) * kStride + 32, x[h][0], v4f{0, 0, 0, 0}, lr, lq);
+      if (rt == 1u) y[h] = block_product(lower(h) + 48 * kStride + 48, x[h][1], y[h], lr, lq);
     }
+    __syncthreads();  // c has been read
+#pragma unroll
+    for (uint32_t h = 0; h < (uint32_t)kHeads; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lower(h)[(32 + 16 * rt + lq * 4 + i) * kStride + 16 * jt + lr] = -y[h][i];
   }
   __syncthreads();
 #pragma unroll
   for (uint32_t i0 = 0; i0 < kTriangle * kHeads; i0 += 4) {
     const uint32_t i = i0 + w, h = i / kTriangle, f = i % kTriangle;
     if (i >= kTriangle * kHeads) break;
-    put_triangle<3>(inverse(h), mine + h * kHeadBytes, f < 2u ? f : f / 2u + 1u, f < 2u ? 0u : f & 1u, lane);
+    put_triangle<3>(lower(h), mine + h * kHeadBytes, f < 2u ? f : f / 2u + 1u, f < 2u ? 0u : f & 1u, lane);
   }
 }
 
