@@ -59,7 +59,7 @@ __device__ __forceinline__ void store4(const Scales &s, uint32_t i, uint32_t j, 
 // its use.)  No register is written, so nothing can be overwritten in flight.
 __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, const uint8_t *base) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
-               : "memory");
+               : "memory", "m0");
 }
 
 // Waits until at most n of a wave's loads into LDS are on their way (for the n
