@@ -17,11 +17,12 @@
 // Numbers.  The matrix cores multiply bf16 and add in binary32.  q and k are
 // bf16 as they are: their norms, decays and beta are factors per token that
 // are applied in binary32 outside the products.  A binary32 operand (T, R, U,
-// S) enters as the sum of three bf16 (8 + 8 + 8 bits, nothing lost) wherever
-// the state depends on it; T R keeps the six products above 2^-24.  The output
-// is rounded to bf16, so its products take the two leading parts (2^-16).
-// T is computed in binary32 throughout, the sums G in binary64: differences of
-// G stay exact next to a strong decay.
+// S, the q.k triangle) enters as the sum of three bf16 (8 + 8 + 8 bits, nothing
+// lost); a product of two such operands keeps the six products above 2^-24.
+// That holds for the output too: where large terms cancel, what is left is
+// right (with two parts there, 2^-16, both launches took 67.5 us for 2048 tokens
+// of 32 heads, and take 71.7).  T is computed in binary32 throughout, the sums
+// G in binary64: differences of G stay exact next to a strong decay.
 #include "delta_common.h"
 
 #include <type_traits>
@@ -48,7 +49,7 @@ constexpr float kNoDecay = -1e6f;  // exp of it is zero; sums of 64 of them stay
 constexpr uint32_t kFragment = 1024;
 constexpr uint32_t kTriangle = 6;
 constexpr uint32_t kTBytes = kTriangle * 3 * kFragment;
-constexpr uint32_t kInnerBytes = kTriangle * 2 * kFragment;
+constexpr uint32_t kInnerBytes = kTriangle * 3 * kFragment;
 constexpr uint32_t kFactorRow = kChunk * 4;  // rows b, b e^G rk, e^(G_L - G) rk, scale e^G rq of 64 tokens, then e^G_L
 constexpr uint32_t kFactorBytes = 4 * kFactorRow + 256;
 constexpr uint32_t kHeadBytes = kTBytes + kInnerBytes + kFactorBytes;
@@ -346,7 +347,7 @@ __global__ __launch_bounds__(kThreads, 4) void delta_chunk_kernel(const DeltaArg
       for (uint32_t j = 0; j < 4; ++j)
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i) gs[j][i] = sum_g[h][16u * j + lq * 4u + i];
-      uint8_t *to = mine + h * kHeadBytes + kTBytes + triangle_fragment(w, 0) * 2u * kFragment + lr * 16u + (lq >> 1) * 256u + (lq & 1u) * 8u;
+      uint8_t *to = mine + h * kHeadBytes + kTBytes + triangle_fragment(w, 0) * 3u * kFragment + lr * 16u + (lq >> 1) * 256u + (lq & 1u) * 8u;
 #pragma unroll
       for (uint32_t j = 0; j < 4; ++j) {
         float x[4], y[4];
@@ -360,12 +361,12 @@ __global__ __launch_bounds__(kThreads, 4) void delta_chunk_kernel(const DeltaArg
         }
         *reinterpret_cast<float4 *>(lower(h) + t * kStride + 16u * j + lq * 4u) = make_float4(x[0], x[1], x[2], x[3]);
         if (j >= 2u && w < 2u) continue;  // no such fragment
-        uint32_t lo[2], hi[2];
-        split2<2>(y[0], y[1], lo);
-        split2<2>(y[2], y[3], hi);
+        uint32_t lo[3], hi[3];
+        split2<3>(y[0], y[1], lo);
+        split2<3>(y[2], y[3], hi);
 #pragma unroll
-        for (uint32_t i = 0; i < 2; ++i)
-          *reinterpret_cast<uint2 *>(to + ((j >> 1) * 2u + i) * kFragment + (j & 1u) * 512u) = make_uint2(lo[i], hi[i]);
+        for (uint32_t i = 0; i < 3; ++i)
+          *reinterpret_cast<uint2 *>(to + ((j >> 1) * 3u + i) * kFragment + (j & 1u) * 512u) = make_uint2(lo[i], hi[i]);
       }
     }
   }
@@ -539,14 +540,14 @@ struct ScanLds {
   float4 part[16][64];          // partial K S0: [token tile * 4 + wave][lane]
   uint8_t r[3][2][1024];        // R, decayed U and U as operands: [part][32 tokens][lane]
   uint8_t decayed[3][2][1024];
-  uint8_t u[2][2][1024];
+  uint8_t u[3][2][1024];
   struct __attribute__((aligned(16))) {
     float value[kChunk][16];    // b v
     float factor[3][kChunk];    // b e^G rk, e^(G_L - G) rk, scale e^G rq
     float decay;                // e^G_L
   } tokens[2];                  // of this chunk and of the next
   uint8_t keys[4][kChunk][kKeyRow<kTiles>];
-  uint8_t s[2][2 * kTiles][1024];  // the state's two leading parts: [part][32 rows][lane]
+  uint8_t s[3][2 * kTiles][1024];  // the state's parts: [part][32 rows][lane]
 
   // the state before a segment, column by column; it and its predecessor lie where the chain's operands come later
   __device__ float *joined(bool other = false) { return reinterpret_cast<float *>(other ? &keys[0][0][0] : reinterpret_cast<uint8_t *>(part)); }
@@ -583,7 +584,7 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
   constexpr bool kByQuads = kQuads<kTiles, kWhole, kMode>;
   const uint32_t load_t = kByQuads ? lane >> 2 : lr, load_p = kByQuads ? lane & 3u : lq;
   const uint32_t dk0 = state_row(w * kTiles, load_p * 4u), lane16 = lane * 16u;
-  const uint32_t t_off[2] = {triangle_fragment(w, 0) * 3u * kFragment + lane16, triangle_fragment(w, 1) * 3u * kFragment + lane16};
+  const uint32_t t_at[2] = {triangle_fragment(w, 0) * 3u * kFragment, triangle_fragment(w, 1) * 3u * kFragment};
   uint32_t k_off[4];
   // rows past the sequence's end read its last token: their factors are zero
   auto token_offsets = [&](uint32_t n) {
@@ -598,10 +599,10 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
   };
   auto load_inverse = [&]() {
 #pragma unroll
-    for (uint32_t i = 0; i < 3; ++i) op_t[0][i] = fragment(mine, t_off[0] + i * kFragment);
+    for (uint32_t i = 0; i < 3; ++i) op_t[0][i] = fragment(mine + t_at[0] + i * kFragment, lane16);
     if (w >= 2u) {
 #pragma unroll
-      for (uint32_t i = 0; i < 3; ++i) op_t[1][i] = fragment(mine, t_off[1] + i * kFragment);
+      for (uint32_t i = 0; i < 3; ++i) op_t[1][i] = fragment(mine + t_at[1] + i * kFragment, lane16);
     }
   };
 
@@ -656,14 +657,14 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
 #pragma unroll
       for (int i = 2; i >= 0; --i) {
         const uint4 b = make_uint4(sp[0][0][i], sp[0][1][i], sp[1][0][i], sp[1][1][i]);
-        if (i < 2) *reinterpret_cast<uint4 *>(&lds.s[i][w][lane16]) = b;
+        *reinterpret_cast<uint4 *>(&lds.s[i][w][lane16]) = b;
 #pragma unroll
         for (int m = 0; m < 4; ++m) x[m] = mfma32(as_bf(op_k[m]), as_bf(b), i == 2 ? zero : x[m]);
       }
     } else {
       // 16 rows: two parts of the state side by side make an operand of 32
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 3; ++i)
         *reinterpret_cast<uint2 *>(&lds.s[i][w >> 1][lane16 + (w & 1u) * 8u]) = make_uint2(sp[0][0][i], sp[0][1][i]);
 #pragma unroll
       for (int m = 0; m < 4; ++m)
@@ -727,11 +728,10 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
     split2<3>(u[2] * to_state[2], u[3] * to_state[3], hi);
 #pragma unroll
     for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2 *>(&lds.decayed[i][0][0] + put) = make_uint2(lo[i], hi[i]);
-    uint32_t ulo[2], uhi[2];
-    split2<2>(u[0], u[1], ulo);
-    split2<2>(u[2], u[3], uhi);
+    split2<3>(u[0], u[1], lo);
+    split2<3>(u[2], u[3], hi);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) *reinterpret_cast<uint2 *>(&lds.u[i][0][0] + put) = make_uint2(ulo[i], uhi[i]);
+    for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2 *>(&lds.u[i][0][0] + put) = make_uint2(lo[i], hi[i]);
     __syncthreads();
     // the state
     v8bf sb[3][2];
@@ -791,8 +791,7 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
   const uint8_t *mine = a.workspace + ((uint64_t)pl.place0 * a.hv + pl.head) * kHeadBytes;
   const uint8_t *queries = reinterpret_cast<const uint8_t *>(a.q + (uint64_t)pl.khead * a.q_head + (uint64_t)pl.sq.begin * a.q_token);
   uint8_t *out = reinterpret_cast<uint8_t *>(a.out + ((uint64_t)pl.sq.begin * a.hv + pl.head) * a.dv);
-  const uint32_t in_off[2] = {kTBytes + triangle_fragment(w, 0) * 2u * kFragment + lane16,
-                              kTBytes + triangle_fragment(w, 1) * 2u * kFragment + lane16};
+  const uint32_t in_at[2] = {kTBytes + triangle_fragment(w, 0) * 3u * kFragment, kTBytes + triangle_fragment(w, 1) * 3u * kFragment};
   // factors: a lane takes row lane / 16 of token 16w + lane % 16 (rows 1 to 3, and then the decay), and the b of token
   // 16w + lane / 4, of which it takes v's columns 4 (lane % 4)..
   const uint8_t *vals = reinterpret_cast<const uint8_t *>(a.v + (uint64_t)pl.head * a.v_head + (uint64_t)pl.sq.begin * a.v_token);
@@ -803,9 +802,8 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
   // By quads it takes those from 32 lq + 8 k on: lane lr loads them of the row
   // with k in place of its lowest bits, at these bits' place, and they change.
   constexpr bool kByQuads = kQuads<kTiles, kWhole, kMode>;
-  uint32_t q_off[kByQuads ? kSteps : 1], v_off, out_off[4];
-#pragma unroll
-  for (uint32_t i = 0; i < 4; ++i) out_off[i] = 2u * ((16u * w + lq * 4u + i) * a.hv * a.dv + pl.col);
+  uint32_t q_off[kByQuads ? kSteps : 1], v_off;
+  const uint32_t out_row = 2u * a.hv * a.dv, out_off = (16u * w + lq * 4u) * out_row + 2u * pl.col;
   auto token_offsets = [&](uint32_t n) {
     if constexpr (kByQuads) {
 #pragma unroll
@@ -817,7 +815,7 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
     v_off = 2u * (min(16u * w + (lane >> 2), n - 1u) * a.v_token + v_col);
   };
 
-  uint4 op_q[kSteps], op_in[2][2];
+  uint4 op_q[kSteps], op_in[2][3];
   uint4 val;
   float factor, beta;
   auto load_tokens = [&]() {
@@ -864,10 +862,10 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
   auto load_inner = [&]() {
     if (!output) return;
 #pragma unroll
-    for (uint32_t i = 0; i < 2; ++i) op_in[0][i] = fragment(mine, in_off[0] + i * kFragment);
+    for (uint32_t i = 0; i < 3; ++i) op_in[0][i] = fragment(mine + in_at[0] + i * kFragment, lane16);
     if (w >= 2u) {
 #pragma unroll
-      for (uint32_t i = 0; i < 2; ++i) op_in[1][i] = fragment(mine, in_off[1] + i * kFragment);
+      for (uint32_t i = 0; i < 3; ++i) op_in[1][i] = fragment(mine + in_at[1] + i * kFragment, lane16);
     }
   };
   // The tokens run one chunk ahead of the rest: they are loaded in one step,
@@ -932,19 +930,18 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
       continue;
     }
     // Q S0 for tokens 16w.., beside the chain's longest phase
-    v8bf sb[2][kSteps];
-#pragma unroll
-    for (int i = 1; i >= 0; --i)
-#pragma unroll
-      for (uint32_t k = 0; k < kSteps; ++k) {
-        sb[i][k] = *reinterpret_cast<const v8bf *>(kByQuads ? &lds.s[i][lq][(k * 16u + lr) * 16u] : &lds.s[i][k][lane16]);
-      }
     const v4f scale = *reinterpret_cast<const v4f *>(&lds.tokens[c & 1u].factor[2][16u * w + lq * 4u]);
     v4f o = zero, o1 = zero;
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      o = mfma32(as_bf(op_q[k]), sb[1][k], o);
-      o1 = mfma32(as_bf(op_q[k]), sb[0][k], o1);
+    for (int i = 2; i >= 0; --i) {
+#pragma unroll
+      for (uint32_t k = 0; k < kSteps; ++k) {
+        const v8bf sb = *reinterpret_cast<const v8bf *>(kByQuads ? &lds.s[i][lq][(k * 16u + lr) * 16u] : &lds.s[i][k][lane16]);
+        if (i > 0)
+          o = mfma32(as_bf(op_q[k]), sb, o);
+        else
+          o1 = mfma32(as_bf(op_q[k]), sb, o1);
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     __syncthreads();
@@ -952,19 +949,19 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
     load_queries();
     o = (o + o1) * scale;
     // and the chunk's own part; columns past 16w + 15 of the triangle are zero
-    v8bf ub[2][2];
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
+    for (uint32_t ks = 0; ks < 2; ++ks) {
+      if (ks == 1u && w < 2u) continue;
+      v8bf ub[3];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) ub[i][ks] = *reinterpret_cast<const v8bf *>(&lds.u[i][ks][lane16]);
-    o1 = mfma32(as_bf(op_in[0][0]), ub[1][0], zero);
-    o = mfma32(as_bf(op_in[0][1]), ub[0][0], o);
-    if (w >= 2u) {
-      o1 = mfma32(as_bf(op_in[1][1]), ub[0][1], o1);
-      o = mfma32(as_bf(op_in[1][0]), ub[1][1], o);
-      o1 = mfma32(as_bf(op_in[1][0]), ub[0][1], o1);
+      for (int i = 0; i < 3; ++i) ub[i] = *reinterpret_cast<const v8bf *>(&lds.u[i][ks][lane16]);
+      o1 = mfma32(as_bf(op_in[ks][2]), ub[0], ks == 0u ? zero : o1);
+      o = mfma32(as_bf(op_in[ks][1]), ub[0], o);
+      o1 = mfma32(as_bf(op_in[ks][1]), ub[1], o1);
+      o = mfma32(as_bf(op_in[ks][0]), ub[1], o);
+      o1 = mfma32(as_bf(op_in[ks][0]), ub[2], o1);
+      o = mfma32(as_bf(op_in[ks][0]), ub[0], o);
     }
-    o = mfma32(as_bf(op_in[0][0]), ub[0][0], o);
     __builtin_amdgcn_sched_barrier(0);
     load_inner();
     if (c + 2u < pl.chunks) advance(c + 2u);
@@ -974,10 +971,12 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
     split2<1>(o[0], o[1], lo);
     split2<1>(o[2], o[3], hi);
     const uint32_t n = c + 1u == pl.chunks ? pl.last : (uint32_t)kChunk, row = 16u * w + lq * 4u;
-    if (pl.col_in && row < n) *reinterpret_cast<uint16_t *>(out + out_off[0]) = (uint16_t)lo[0];
-    if (pl.col_in && row + 1u < n) *reinterpret_cast<uint16_t *>(out + out_off[1]) = (uint16_t)(lo[0] >> 16);
-    if (pl.col_in && row + 2u < n) *reinterpret_cast<uint16_t *>(out + out_off[2]) = (uint16_t)hi[0];
-    if (pl.col_in && row + 3u < n) *reinterpret_cast<uint16_t *>(out + out_off[3]) = (uint16_t)(hi[0] >> 16);
+    uint32_t at = out_off;
+    asm volatile("" : "+v"(at));  // (an offset to a uniform base: four addresses in the loop are eight registers)
+    if (pl.col_in && row < n) *reinterpret_cast<uint16_t *>(out + at) = (uint16_t)lo[0];
+    if (pl.col_in && row + 1u < n) *reinterpret_cast<uint16_t *>(out + at + out_row) = (uint16_t)(lo[0] >> 16);
+    if (pl.col_in && row + 2u < n) *reinterpret_cast<uint16_t *>(out + at + 2u * out_row) = (uint16_t)hi[0];
+    if (pl.col_in && row + 3u < n) *reinterpret_cast<uint16_t *>(out + at + 3u * out_row) = (uint16_t)(hi[0] >> 16);
     out += (uint64_t)kChunk * 2u * a.hv * a.dv;
   }
 }

@@ -359,6 +359,8 @@ int w8a8_gemm(const void *act_i8, const void *w_i8, const void *bias_bf16, void 
  * A NaN or an infinity in a token stays in its sequence and head, and in the
  * tokens from it on (_chunked: from the beginning of its chunk of 64 on).
  *
+ * Both forms compute in binary32 (binary32 operands of matrix products as sums of
+ * three bf16) and round out once; they differ by the order of their sums.
  * _recurrent takes the tokens of a sequence one by one: for decoding, and for
  * a few tokens.  _chunked takes them in chunks of 64, within a chunk by matrix
  * products: for prompts.  workspace: gated_delta_rule_workspace_bytes(...) bytes,
