@@ -914,7 +914,7 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
     __syncthreads();
     if constexpr (kMode == kChain) {
       asm volatile("" ::"v"(touched));  // (a step later, so that nothing waits for it)
-      if (touches && c + 3u < pl.chunks) touched = *reinterpret_cast<const uint32_t *>(touch);  // (whole chunks alone)
+      if (touches && c + 3u < pl.chunks) touched = *reinterpret_cast<const uint16_t *>(touch);  // (whole chunks alone; one value of a row, its last at most)
       touch += touch_step;
     }
     if constexpr (kByQuads) {
