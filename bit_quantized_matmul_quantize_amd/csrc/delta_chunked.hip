@@ -102,6 +102,15 @@ __device__ __forceinline__ v4f mfma32(v8bf a, v8bf b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// Between what lanes of a wave write to LDS and what others of the same wave read
+// there (or the other way round).  The hardware keeps a wave's accesses of LDS in
+// order; this keeps the compiler's order, which sees one lane's addresses only.
+__device__ __forceinline__ void wave_exchange() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 struct __attribute__((packed, aligned(2))) Bf16x8 {
   uint32_t w[4];
 };
@@ -371,6 +380,8 @@ __global__ __launch_bounds__(kThreads, 4) void delta_chunk_kernel(const DeltaArg
     }
   }
 
+  wave_exchange();  // A's diagonal blocks: a wave's own rows, by other lanes
+
   // T: the 16 x 16 blocks on the diagonal by substitution (a wave has its own
   // rows' block of every head, a lane a column), then blocks of 16 and of 32
   // joined in pairs,
@@ -393,6 +404,7 @@ __global__ __launch_bounds__(kThreads, 4) void delta_chunk_kernel(const DeltaArg
       }
       t[i] = (x[0] + x[1]) + (x[2] + x[3]);
     }
+    wave_exchange();  // (the blocks have been read)
     if (lq < (uint32_t)kHeads) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) lower(h)[(16u * w + i) * kStride + 16u * w + lr] = t[i];
@@ -642,7 +654,9 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
     }
     // K S0 over the wave's rows of the state
     if constexpr (kByQuads) {
+      wave_exchange();  // (the last chunk's have been read)
       put_keys();
+      wave_exchange();
 #pragma unroll
       for (int m = 0; m < 4; ++m) op_k[m] = *reinterpret_cast<const uint4 *>(keys_rows + 16 * m * kKeyRow<kTiles>);
     }
@@ -674,7 +688,10 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const ScanPlace 
         x[m] = mfma32(as_bf(make_uint4(op_k[m].x, op_k[m].y, op_k[m].x, op_k[m].y)),
                       as_bf(make_uint4(sp[0][0][1], sp[0][1][1], sp[0][0][0], sp[0][1][0])), x[m]);
     }
-    if constexpr (!kByQuads) put_keys();
+    if constexpr (!kByQuads) {
+      wave_exchange();
+      put_keys();
+    }
 #pragma unroll
     for (int m = 0; m < 4; ++m) *reinterpret_cast<v4f *>(&lds.part[m * 4 + w][lane]) = x[m];
     __syncthreads();
