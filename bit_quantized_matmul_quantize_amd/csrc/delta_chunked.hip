@@ -895,14 +895,16 @@ __device__ __forceinline__ void make_output(const DeltaArgs &a, const ScanPlace 
   };
   if constexpr (kMode == kRest) __syncthreads();
   // The column blocks of a head run side by side on one XCD.  Where the first
-  // launch has left more than the caches hold (256 MB, with q, k and v in them),
+  // launch has left more than the caches hold beside q, k, v and the output,
   // each touches its share of the lines of the chunk after the next: two waves
-  // the workspace's, two those of q, k and v (16384 tokens of 32 heads: 506 us,
-  // and 517 without; packed prompts of 2128 tokens, 8 heads: 48.2, and 47.0).
+  // the workspace's, two those of q, k and v.  From 80 MB of workspace on: 8000
+  // tokens of 20 heads (95 MB) 216 us, and 233 without; 16000 of 12 (114 MB) 398,
+  // and 494; 9000 of 16 (86 MB) 233, and 237; 2128 packed tokens of 8 heads (13
+  // MB) 48.2, and 47.0.
   const uint8_t *touch = mine;
   uint64_t touch_step = (uint64_t)a.hv * kHeadBytes;
   bool touches = false;
-  if (kMode == kChain && (uint64_t)(a.tokens / kChunk + a.count) * a.hv > (128u << 20) / kHeadBytes) {
+  if (kMode == kChain && (uint64_t)(a.tokens / kChunk + a.count) * a.hv > (80u << 20) / kHeadBytes) {
     const uint32_t mine_of = __builtin_amdgcn_readfirstlane(pl.col >> 4) + (a.dv + 15u) / 16u * ((w & 1u) * 64u + lane);
     if (w < 2u) {
       touch += mine_of * 128u;

@@ -194,3 +194,32 @@ def test_binding_checks_delta_shapes(bq):
             bq.gated_delta_rule_recurrent(**{**ok, **change})
     with pytest.raises(TypeError, match="workspace"):
         bq.gated_delta_rule_chunked(**ok, workspace=bf(16))
+
+
+def chunked_need(bq, tokens, count, hk, hv, dk, dv):
+    """What the call itself asks for, from its refusal of a workspace of one byte."""
+    v = list(delta_args(tokens=tokens, count=count, hk=hk, hv=hv, dk=dk, dv=dv, q=at(1 << 10), k=at(1 << 11), v=at(1 << 12),
+                        g=at(1 << 13), beta=at(1 << 14), out=at(1 << 15), state=at(1 << 16), starts=at(1 << 17), slots=None,
+                        fresh=None, state_slots=count, q_token=hk * dk, q_head=dk, k_token=hk * dk, k_head=dk,
+                        v_token=hv * dv, v_head=dv).values())
+    v[10:10] = [at(12), 1]
+    assert bq.lib().gated_delta_rule_chunked(*v) == -1
+    return int(bq.lib().bq_last_error().decode().split(", ")[1].split()[0])
+
+
+def test_a_workspace_for_the_largest_call_serves_every_smaller_one(bq):
+    """A program allocates once, for its most tokens and its most sequences."""
+    import random
+    rng = random.Random(5)
+    size = bq.gated_delta_rule_workspace_bytes
+    fixed = [(8192, 4, 8192, 1, (4, 4, 128, 128)), (7104, 1, 7040, 1, (16, 16, 128, 128)), (16384, 8, 7000, 1, (1, 1, 64, 64))]
+    for i in range(600):
+        hk = rng.choice([1, 1, 2, 4, 8, 16])
+        heads = (hk, hk * rng.choice([1, 2]), rng.choice([1, 33, 64, 65, 128]), rng.choice([1, 7, 64, 80, 128, 130]))
+        tokens, count = int(2 ** rng.uniform(0, 15)), int(2 ** rng.uniform(0, 5))
+        less, fewer = rng.randint(1, tokens), rng.randint(1, count)
+        if i < len(fixed):
+            tokens, count, less, fewer, heads = fixed[i]
+        assert size(less, fewer, *heads) <= size(tokens, count, *heads), (tokens, count, less, fewer, heads)
+        need = chunked_need(bq, less, fewer, *heads)
+        assert 0 < need <= size(less, fewer, *heads)
