@@ -332,6 +332,7 @@ def int8_rows_bytes(rows: int, k: int) -> int:
 
 
 def gated_delta_rule_workspace_bytes(tokens: int, count: int, hk: int, hv: int, dk: int, dv: int) -> int:
+    """Enough for every chunked call of at most these tokens and sequences."""
     return int(lib().gated_delta_rule_workspace_bytes(tokens, count, hk, hv, dk, dv))
 
 

@@ -165,6 +165,8 @@ struct DeltaArgs {
 };
 hipError_t launch_delta_recurrent(const DeltaArgs &a, hipStream_t s);
 hipError_t launch_delta_chunked(const DeltaArgs &a, hipStream_t s);
+// of the chunked form: for these sizes, and for these and every smaller tokens and count
+uint64_t delta_workspace_needed(uint32_t tokens, uint32_t count, uint32_t hv, uint32_t dk, uint32_t dv);
 uint64_t delta_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hv, uint32_t dk, uint32_t dv);
 
 }  // namespace bqmm

@@ -703,7 +703,7 @@ int gated_delta_rule_chunked(const void *q_bf16, const void *k_bf16, const void 
   if (!nothing) {
     REQUIRE(((uint64_t)tokens / 64u + count) * hv < (1ull << 31), BQ_EINVAL, "%s: tokens=%u count=%u hv=%u too large",
             name, tokens, count, hv);
-    const uint64_t need = gated_delta_rule_workspace_bytes(tokens, count, hk, hv, dk, dv);
+    const uint64_t need = bqmm::delta_workspace_needed(tokens, count, hv, dk, dv);
     REQUIRE(workspace, BQ_EINVAL, "%s: null workspace", name);
     REQUIRE(workspace_bytes >= need, BQ_EINVAL, "%s: the workspace holds %llu bytes, %llu are needed", name,
             (unsigned long long)workspace_bytes, (unsigned long long)need);

@@ -1147,15 +1147,27 @@ __global__ __launch_bounds__(kScanThreads, kWhole ? 4 : 2) void delta_scan_kerne
 // (two on a CU hardly hide each other's waits).
 double chain_cost(double groups) { return 1.25 * (0.9 * groups > kCus ? 0.9 * groups / kCus : 1.0); }
 
+// The leading five bits of a number of chunks.  The rule below goes by them, so
+// that it can be asked for every smaller number in a few steps.
+uint32_t low_bits(uint32_t chunks) {
+  uint32_t n = 0;
+  while (chunks >> n >= 32u) ++n;
+  return n;
+}
+uint32_t leading_bits(uint32_t chunks) { return chunks >> low_bits(chunks) << low_bits(chunks); }
+
+// Whether the chains alone give every CU work; such sequences are never cut.
+bool fills_the_chip(uint64_t count, uint32_t hv, uint32_t dv) { return 0.9 * count * hv * ((dv + 15u) / 16u) >= kCus; }
+
 // Chunks of a segment; 0: the sequences are not cut.  From the sizes alone, as
 // the lengths lie on the device: as if all sequences were equally long.  The
 // constants are fitted to 60 sizes, among them (us, not cut / cut in 4 / 8 / 16
 // / 32 chunks): 1024 tokens of 4 heads 38 / 39 / 45; 2048 of 1 head 54 / 42 /
 // 46 / 62; 8192 of 4 heads 182 / 218 / 118 / 93 / 121; of 8 heads 190 / 386 /
 // 196 / 147 / 138; of 16 heads 203 / 719 / 353 / 249 / 215.
-uint32_t segment_chunks(uint32_t tokens, uint32_t count, uint32_t hv, uint32_t dk, uint32_t dv) {
-  if (count == 0u) return 0u;
-  const double chunks = (double)tokens / kChunk / count, heads = (double)count * hv;
+uint32_t segment_chunks(uint32_t all, uint32_t count, uint32_t hv, uint32_t dk, uint32_t dv) {
+  if (count == 0u || fills_the_chip(count, hv, dv)) return 0u;
+  const double chunks = (double)leading_bits(all) / count, heads = (double)count * hv;
   const double v = (dv + 15u) / 16u, m = dk <= 64u ? 4.0 : 8.0;
   double best = 0.97 * chunks * chain_cost(heads * v);
   uint32_t cut = 0;
@@ -1173,9 +1185,11 @@ uint32_t segment_chunks(uint32_t tokens, uint32_t count, uint32_t hv, uint32_t d
   return cut;
 }
 
-uint64_t parts_bytes(uint32_t tokens, uint32_t count, uint32_t hv, uint32_t dk, uint32_t dv, uint32_t segment) {
+// M and N of all segments of so many chunks in all.
+uint64_t parts_bytes(uint32_t all, uint32_t count, uint32_t hv, uint32_t dk, uint32_t dv) {
   const uint64_t rows = dk <= 64u ? 64u : 128u;
-  return segment ? (uint64_t)segment_places(tokens, count, segment) * hv * rows * (rows + (dv + 15u) / 16u * 16u) * 4u : 0u;
+  const uint32_t segment = segment_chunks(all, count, hv, dk, dv);
+  return segment ? (uint64_t)(all / segment + count) * hv * rows * (rows + (dv + 15u) / 16u * 16u) * 4u : 0u;
 }
 
 template <int kTiles, int kMode>
@@ -1208,7 +1222,7 @@ hipError_t launch_chunked(DeltaArgs a, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  a.segment = segment_chunks(a.tokens, a.count, a.hv, a.dk, a.dv);
+  a.segment = segment_chunks(a.tokens / kChunk, a.count, a.hv, a.dk, a.dv);
   if (a.segment == 0u) return launch_scan<kTiles, kChain>(a, a.count, s);
   a.parts = reinterpret_cast<float *>(a.workspace + places * a.hv * kHeadBytes);
   const uint32_t segments = segment_places(a.tokens, a.count, a.segment);
@@ -1218,9 +1232,24 @@ hipError_t launch_chunked(DeltaArgs a, hipStream_t s) {
 
 }  // namespace
 
+uint64_t delta_workspace_needed(uint32_t tokens, uint32_t count, uint32_t hv, uint32_t dk, uint32_t dv) {
+  return (tokens / kChunk + (uint64_t)count) * hv * kHeadBytes + parts_bytes(tokens / kChunk, count, hv, dk, dv);
+}
+
+// What every call of at most so many tokens and sequences needs at most.  Fewer
+// tokens or sequences can be cut where these are not, or shorter: the largest
+// of what any of them has of segments.
 uint64_t delta_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hv, uint32_t dk, uint32_t dv) {
-  const uint64_t places = tokens / kChunk + (uint64_t)count;
-  return places * hv * kHeadBytes + parts_bytes(tokens, count, hv, dk, dv, segment_chunks(tokens, count, hv, dk, dv));
+  const uint32_t all = tokens / kChunk;
+  uint64_t parts = 0;
+  for (uint32_t c = 1; c <= count && !fills_the_chip(c, hv, dv); ++c)
+    for (uint64_t x = 0; x <= all;) {  // a run of numbers that the rule does not tell apart, by its last
+      const uint64_t next = leading_bits((uint32_t)x) + (1ull << low_bits((uint32_t)x));
+      const uint64_t bytes = parts_bytes((uint32_t)(next - 1u < all ? next - 1u : all), c, hv, dk, dv);
+      parts = bytes > parts ? bytes : parts;
+      x = next;
+    }
+  return (all + (uint64_t)count) * hv * kHeadBytes + parts;
 }
 
 hipError_t launch_delta_chunked(const DeltaArgs &a, hipStream_t s) {

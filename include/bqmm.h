@@ -109,9 +109,10 @@ uint64_t q4k_weight_bytes(uint32_t n, uint32_t k);
  * 0 on overflow (k > 2^30). */
 uint64_t int8_rows_bytes(uint32_t rows, uint32_t k);
 
-/* Workspace of gated_delta_rule_chunked for these sizes (an upper bound over
- * every split of `tokens` into `count` sequences).  0 where the call would
- * refuse the sizes. */
+/* Workspace of gated_delta_rule_chunked for these heads and at most `tokens`
+ * tokens in at most `count` sequences, however they are split: one that is
+ * allocated for the largest call serves every smaller one.  0 where the call
+ * would refuse the sizes. */
 uint64_t gated_delta_rule_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hk, uint32_t hv,
                                           uint32_t dk, uint32_t dv);
 
@@ -363,7 +364,8 @@ int w8a8_gemm(const void *act_i8, const void *w_i8, const void *bias_bf16, void 
  * three bf16) and round out once; they differ by the order of their sums.
  * _recurrent takes the tokens of a sequence one by one: for decoding, and for
  * a few tokens.  _chunked takes them in chunks of 64, within a chunk by matrix
- * products: for prompts.  workspace: gated_delta_rule_workspace_bytes(...) bytes,
+ * products: for prompts.  workspace: gated_delta_rule_workspace_bytes(...) bytes
+ * for these sizes or larger ones,
  * 16-byte aligned, for this call alone until it has run. */
 int gated_delta_rule_recurrent(const void *q_bf16, const void *k_bf16, const void *v_bf16, const float *g,
                                const float *beta, void *out_bf16, float *state, const int32_t *starts,
