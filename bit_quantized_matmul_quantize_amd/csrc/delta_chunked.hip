@@ -25,6 +25,7 @@
 // G in binary64: differences of G stay exact next to a strong decay.
 #include "delta_common.h"
 
+#include <cmath>
 #include <type_traits>
 
 namespace bqmm {
@@ -1143,9 +1144,9 @@ __global__ __launch_bounds__(kScanThreads, kWhole ? 4 : 2) void delta_scan_kerne
     make_output<kTiles, kWhole, kMode>(a, pl, lds, w - 4u, lane);
 }
 
-// What a launch of the chain takes per chunk, in us, with that many workgroups
-// (two on a CU hardly hide each other's waits).
-double chain_cost(double groups) { return 1.25 * (0.9 * groups > kCus ? 0.9 * groups / kCus : 1.0); }
+// How many times longer than one workgroup a CU so many workgroups take (two on a
+// CU hide little of each other's waits).
+double rounds(double groups) { return groups > kCus ? groups / kCus : 1.0; }
 
 // The leading five bits of a number of chunks.  The rule below goes by them, so
 // that it can be asked for every smaller number in a few steps.
@@ -1157,26 +1158,30 @@ uint32_t low_bits(uint32_t chunks) {
 uint32_t leading_bits(uint32_t chunks) { return chunks >> low_bits(chunks) << low_bits(chunks); }
 
 // Whether the chains alone give every CU work; such sequences are never cut.
-bool fills_the_chip(uint64_t count, uint32_t hv, uint32_t dv) { return 0.9 * count * hv * ((dv + 15u) / 16u) >= kCus; }
+bool fills_the_chip(uint64_t count, uint32_t hv, uint32_t dv) { return 0.8 * count * hv * ((dv + 15u) / 16u) >= kCus; }
 
 // Chunks of a segment; 0: the sequences are not cut.  From the sizes alone, as
-// the lengths lie on the device: as if all sequences were equally long.  The
-// constants are fitted to 60 sizes, among them (us, not cut / cut in 4 / 8 / 16
-// / 32 chunks): 1024 tokens of 4 heads 38 / 39 / 45; 2048 of 1 head 54 / 42 /
-// 46 / 62; 8192 of 4 heads 182 / 218 / 118 / 93 / 121; of 8 heads 190 / 386 /
-// 196 / 147 / 138; of 16 heads 203 / 719 / 353 / 249 / 215.
+// the lengths lie on the device: as if all sequences were equally long.  Whole
+// segments are counted, as whole ones are run.  The constants are fitted to 136
+// sizes, among them (us, not cut / cut in 8 / 16 / 32 / 64 chunks): 9000
+// tokens of 1 head 211 / 79 / 84 / 128 / 230; of 4 heads 221 / 149 / 101 / 140 /
+// 240; 16000 of 8 heads 390 / 497 / 308 / 257 / 278; of 12 heads 395 / 758 / 471 /
+// 402 / 407; of 16 heads 413 / 986 / 610 / 512 / 476.  Over them the choice takes 1% longer than the best one does, and at the
+// worst 3% longer than no cut (16000 tokens of 12 heads).
 uint32_t segment_chunks(uint32_t all, uint32_t count, uint32_t hv, uint32_t dk, uint32_t dv) {
   if (count == 0u || fills_the_chip(count, hv, dv)) return 0u;
   const double chunks = (double)leading_bits(all) / count, heads = (double)count * hv;
   const double v = (dv + 15u) / 16u, m = dk <= 64u ? 4.0 : 8.0;
-  double best = 0.97 * chunks * chain_cost(heads * v);
+  constexpr double kPerChunk = 1.25;  // us
+  double best = 0.85 * chunks * kPerChunk * rounds(0.93 * heads * v);
   uint32_t cut = 0;
   for (uint32_t n = 2; n <= 64; n *= 2) {
-    const double parts = chunks / n;
-    if (parts < 2.0) break;
-    const double rest = heads * v * (parts - 1.0);  // workgroups of the second launch, which all read M's
-    const double join = 1.8 * (m / 8.0) * (m / 8.0) * (1.5 * rest > kCus ? 1.5 * rest / kCus : 1.0);
-    const double t = n * (chain_cost(heads * (v + (parts - 2.0) * (v + m))) + chain_cost(rest)) + join * (parts - 2.0) + 15.0;
+    if (chunks < 2.0 * n) break;
+    const double parts = ceil(chunks / n);
+    const double first = heads * (v + (parts - 2.0) * (v + m));  // workgroups: of the first segment, and N's and M's
+    const double rest = heads * v * (parts - 1.0);               // of the next launch, which all read M's
+    const double join = 1.95 * (m / 8.0) * (m / 8.0) * rounds(0.75 * rest);
+    const double t = n * kPerChunk * (rounds(0.8 * first) + rounds(0.8 * rest)) + join * (parts - 2.0) + 10.5;
     if (t < best) {
       best = t;
       cut = n;

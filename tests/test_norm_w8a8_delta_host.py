@@ -223,3 +223,14 @@ def test_a_workspace_for_the_largest_call_serves_every_smaller_one(bq):
         assert size(less, fewer, *heads) <= size(tokens, count, *heads), (tokens, count, less, fewer, heads)
         need = chunked_need(bq, less, fewer, *heads)
         assert 0 < need <= size(less, fewer, *heads)
+
+
+@pytest.mark.parametrize("tokens,count,heads,cut", [
+    (8192, 1, 1, True), (9000, 1, 4, True), (16000, 1, 8, True), (16000, 2, 2, True),
+    # measured slower in every cut: 476 us at best and 413 in one chain, 192 (in 32s) and 176, 756 and 622
+    (16000, 1, 16, False), (6500, 1, 16, False), (24000, 1, 16, False), (2500, 1, 16, False), (16384, 1, 32, False),
+])
+def test_long_sequences_are_cut_where_that_measured_faster(bq, tokens, count, heads, cut):
+    sizes = (heads, heads, 128, 128)
+    chunk = chunked_need(bq, 1, 1, *sizes)  # one chunk of all heads
+    assert (chunked_need(bq, tokens, count, *sizes) > (tokens // 64 + count) * chunk) == cut
