@@ -53,6 +53,7 @@ EXPORTS = {
     "add_rms_norm_quantize_q8_1": (_I, [_P, _P, _P, _P, _U32, _U32, _D, _P]),
     "add_rms_norm_quantize_int8": (_I, [_P, _P, _P, _P, _U32, _U32, _D, _P]),
     "quantize_rows_int8": (_I, [_P, _P, _U32, _U32, _P]),
+    "w8a8_gemm_form": (_I, [_U32] * 4),
     "w8a8_gemm": (_I, [_P, _P, _P, _P, _U32, _U32, _U32, _P]),
     "gated_delta_rule_recurrent": (_I, [_P] * 10 + [_U32] * 7 + [_U64] * 6 + [_F, _I, _P]),
     "gated_delta_rule_chunked": (_I, [_P] * 11 + [_U64] + [_U32] * 7 + [_U64] * 6 + [_F, _I, _P]),
@@ -373,6 +374,14 @@ def w8a8_gemm(act_i8, w_i8, out, m: int, n: int, k: int, bias=None, stream=None)
     if bias is not None:
         _need(_bf16(bias, "bias"), _bf(1, n), "bias")
     _check(lib().w8a8_gemm(*_ptrs(act_i8, w_i8, bias, out), m, n, k, _stream(stream)))
+
+
+def w8a8_gemm_form(m: int, n: int, k: int, cus: int) -> int:
+    """The number of the kernel that w8a8_gemm takes on a device of so many compute units (a test hook)."""
+    form = lib().w8a8_gemm_form(m, n, k, cus)
+    if form < 0:
+        _check(form)
+    return form
 
 
 def _typed(t, kind, shape, what):

@@ -145,6 +145,7 @@ hipError_t launch_quantize_rows_int8(const void *x, void *out, uint32_t rows, ui
 // bias may be null
 hipError_t launch_w8a8_gemm(const void *act, const void *w, const void *bias, void *out, uint32_t m, uint32_t n,
                             uint32_t k, hipStream_t s);
+int w8a8_form(uint32_t m, uint32_t n, uint32_t k, uint32_t cus);
 
 // The gated delta rule's arguments: strides in values, heads of q and k are
 // shared by hv / hk value heads; slots and fresh may be null.

@@ -662,6 +662,12 @@ int w8a8_gemm(const void *act_i8, const void *w_i8, const void *bias_bf16, void 
   return hip_status(bqmm::launch_w8a8_gemm(act_i8, w_i8, bias_bf16, out_bf16, m, n, k, as_stream(stream)), name);
 }
 
+int w8a8_gemm_form(uint32_t m, uint32_t n, uint32_t k, uint32_t cus) {
+  REQUIRE(m >= 1 && n >= 1 && k >= 1 && cus >= 1, BQ_EINVAL, "w8a8_gemm_form: m=%u n=%u k=%u cus=%u must be >= 1", m, n, k,
+          cus);
+  return bqmm::w8a8_form(m, n, k, cus);
+}
+
 uint64_t gated_delta_rule_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hk, uint32_t hv, uint32_t dk,
                                           uint32_t dv) {
   if (hk == 0 || hv == 0 || hv % hk != 0 || dk == 0 || dk > 128 || dv == 0 || hv > 65535u || dv > 65535u || (uint64_t)hv * dv >= (1ull << 24) ||

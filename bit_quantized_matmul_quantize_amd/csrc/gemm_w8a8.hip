@@ -379,16 +379,17 @@ hipError_t launch_tiles(const uint8_t *act, const uint8_t *w, const Scales &s, u
   return launch_tile_kernel<kTm, kTn, kStages, false>(act, w, s, kp, tm, tn, tm * tn, (tm * tn + 7u) / 8u * 8u, st);
 }
 
-// Tiles of 256 x 256, one per CU at a time.  Whole rounds of them, and what is
+// Tiles of 256 x 256, one per CU at a time.  kQuarters: whole rounds of them, and what is
 // left over in quarters where at most two rounds of those suffice (4096 x 17408,
 // k = 5120: 64 of 1088 tiles are left over; 381 us, and 422 with a fifth round).
 bool quarters(uint32_t total, uint32_t cus) {
   const uint32_t left = total % cus;
   return total > cus && cus % 8u == 0u && left > 0u && 2u * left <= cus;
 }
+template <bool kQuarters>
 hipError_t launch_big_tiles(const uint8_t *act, const uint8_t *w, const Scales &s, uint32_t kp, uint32_t cus, hipStream_t st) {
   const uint32_t tm = (s.m + 255u) / 256u, tn = (s.n + 255u) / 256u, total = tm * tn, whole = total / cus * cus;
-  if (quarters(total, cus))
+  if (kQuarters)
     return launch_tile_kernel<4, 4, 2, true>(act, w, s, kp, tm, tn, whole, whole + 4u * (total - whole), st);
   return launch_tile_kernel<4, 4, 2, false>(act, w, s, kp, tm, tn, total, (total + 7u) / 8u * 8u, st);
 }
@@ -437,7 +438,24 @@ float cost(int form, uint32_t m, uint32_t n, uint32_t steps, uint32_t cus) {
   return f.base + (float)steps * ((float)rounds * f.round + last);
 }
 
+// The form that a call takes: one of the above, or what two of them run otherwise.
+enum { kRows4 = kForms, kQuartered };
+int form_of(uint32_t m, uint32_t n, uint32_t k, uint32_t cus) {
+  const uint32_t steps = (k + kRowPad - 1u) / kRowPad;
+  int form = kRows;
+  if (m > 16u)
+    for (int f = kRows + 1; f < kForms; ++f)
+      if (cost(f, m, n, steps, cus) < cost(form, m, n, steps, cus)) form = f;
+  // Few workgroups leave most CUs idle: eight waves each then, four otherwise (one row, k = 5120: n = 1000
+  // takes 4.0 us against 4.5, n = 17408 18.1 against 17.5).
+  if (form == kRows && (m + 15u) / 16u * ((n + 15u) / 16u) > 128u) form = kRows4;
+  if (form == kBig && quarters((m + 255u) / 256u * ((n + 255u) / 256u), cus)) form = kQuartered;
+  return form;
+}
+
 }  // namespace
+
+int w8a8_form(uint32_t m, uint32_t n, uint32_t k, uint32_t cus) { return form_of(m, n, k, cus); }
 
 hipError_t launch_w8a8_gemm(const void *act, const void *w, const void *bias, void *out, uint32_t m, uint32_t n,
                             uint32_t k, hipStream_t st) {
@@ -449,23 +467,17 @@ hipError_t launch_w8a8_gemm(const void *act, const void *w, const void *bias, vo
   int cus = 0;
   const hipError_t e = device_cu_count(&cus);
   if (e != hipSuccess) return e;
-  const uint32_t c = (uint32_t)(cus > 0 ? cus : 1), steps = kp / kStep;
-  int form = kRows;
-  if (m > 16u)
-    for (int f = kRows + 1; f < kForms; ++f)
-      if (cost(f, m, n, steps, c) < cost(form, m, n, steps, c)) form = f;
-  switch (form) {
-    case kRows:
-      // Few workgroups leave most CUs idle: eight waves each then, four otherwise (one row, k = 5120: n = 1000
-      // takes 4.0 us against 4.5, n = 17408 18.1 against 17.5).
-      return (m + 15u) / 16u * ((n + 15u) / 16u) <= 128u ? launch_rows<8>(ap, wp, s, kp, st)
-                                                          : launch_rows<4>(ap, wp, s, kp, st);
+  const uint32_t c = (uint32_t)(cus > 0 ? cus : 1);
+  switch (form_of(m, n, k, c)) {
+    case kRows: return launch_rows<8>(ap, wp, s, kp, st);
+    case kRows4: return launch_rows<4>(ap, wp, s, kp, st);
     case kT11: return launch_tiles<1, 1, 4>(ap, wp, s, kp, st);
     case kT12: return launch_tiles<1, 2, 4>(ap, wp, s, kp, st);
     case kT21: return launch_tiles<2, 1, 4>(ap, wp, s, kp, st);
     case kT22: return launch_tiles<2, 2, 4>(ap, wp, s, kp, st);
     case kT22Pair: return launch_tiles<2, 2, 2>(ap, wp, s, kp, st);
-    default: return launch_big_tiles(ap, wp, s, kp, c, st);
+    case kBig: return launch_big_tiles<false>(ap, wp, s, kp, c, st);
+    default: return launch_big_tiles<true>(ap, wp, s, kp, c, st);
   }
 }
 

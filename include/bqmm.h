@@ -381,6 +381,14 @@ int gated_delta_rule_chunked(const void *q_bf16, const void *k_bf16, const void 
                              uint64_t k_head, uint64_t v_token, uint64_t v_head, float scale, int l2norm,
                              void *stream);
 
+/* ---- test hook: the int8 product's form -------------------------------- */
+
+/* The kernel that w8a8_gemm takes for these sizes on a device of `cus` compute
+ * units: 0 and 7 few rows (eight waves, four); tiles of rows x columns: 1 64 x 64,
+ * 2 64 x 128, 3 128 x 64, 4 128 x 128, 5 128 x 128 two to a compute unit, 6 256 x 256,
+ * 8 256 x 256 with the last round in quarters.  Below 0: a status.  Runs nothing. */
+int w8a8_gemm_form(uint32_t m, uint32_t n, uint32_t k, uint32_t cus);
+
 /* ---- test hooks: integer block dot products ---------------------------- */
 
 /* Runs the MMQ kernel's own unpack and matrix-core path over the window
