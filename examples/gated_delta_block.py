@@ -85,6 +85,7 @@ class GatedDeltaBlock:
     def __call__(self, x, residual, state, starts, slots, fresh, b, prefill):
         """x, residual: [tokens, hidden] bf16, the residual is updated in place; returns the block's x."""
         m, hidden, hk, hv, dk, dv = x.shape[0], self.hidden, self.hk, self.hv, self.dk, self.dv
+        b = {name: t[:m] if t.dim() > 1 else t for name, t in b.items()}  # (they may be for more tokens)
         if self.qkvz == "q2_0":
             # both formats of the normalised rows; the second pass finds the sum in the residual
             bq.add_rms_norm_quantize_int8(x, residual, self.norm1, b["norm"], m, hidden)
