@@ -142,6 +142,21 @@ hipError_t launch_add_rms_norm_quantize_int8(const void *x, void *residual, cons
 hipError_t launch_add_rms_norm_quantize_q8_1(const void *x, void *residual, const void *weight, void *out,
                                              uint32_t m, uint32_t k, double eps, hipStream_t s);
 hipError_t launch_quantize_rows_int8(const void *x, void *out, uint32_t rows, uint32_t k, hipStream_t s);
+
+// A norm's rows of k values as an output pads them to a multiple of `to`, the
+// vectors of eight that a lane holds of such a row, and the threads that it takes.
+constexpr uint32_t kNormMaxThreads = 512;
+constexpr uint32_t kNormMaxVectors = 8;
+inline uint32_t norm_padded(uint32_t k, uint32_t to) { return (k + to - 1u) / to * to; }
+inline uint32_t norm_vectors(uint32_t kpad) {
+  const uint32_t nv = (kpad / 8u + kNormMaxThreads - 1u) / kNormMaxThreads;
+  return nv <= 2u ? nv : nv <= 4u ? 4u : 8u;
+}
+inline uint32_t norm_threads(uint32_t kpad) {
+  if (kpad > kNormMaxThreads * kNormMaxVectors * 8u) return kNormMaxThreads;
+  const uint32_t nv = norm_vectors(kpad);
+  return ((kpad / 8u + nv - 1u) / nv + 63u) / 64u * 64u;
+}
 // bias may be null
 hipError_t launch_w8a8_gemm(const void *act, const void *w, const void *bias, void *out, uint32_t m, uint32_t n,
                             uint32_t k, hipStream_t s);

@@ -54,6 +54,8 @@ constexpr uint32_t kMaxGridY = 65535u;
 // per row (padded to 256 in 32 bits), and output rows n.
 constexpr uint32_t kMaxK = 1u << 30;
 constexpr uint32_t kMaxRows = 1u << 31;
+// A launch has fewer than 2^32 threads in all.
+constexpr uint64_t kMaxThreads = 1ull << 32;
 
 #define REQUIRE(cond, status, ...) \
   do {                             \
@@ -476,11 +478,13 @@ bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 
 uint64_t i8_bytes(uint32_t rows, uint32_t k) { return (uint64_t)rows * (((uint64_t)k + 127u) / 128u * 128u + 4u); }
 
+// kpad: k as the output pads it
 int check_norm(const char *name, const void *x, const void *residual, const void *weight, const void *out, uint32_t m,
-               uint32_t k, double eps, uint64_t nout) {
+               uint32_t k, uint32_t kpad, double eps, uint64_t nout) {
   REQUIRE(x && weight && out, BQ_EINVAL, "%s: null pointer", name);
   REQUIRE(m >= 1 && k >= 1, BQ_EINVAL, "%s: m=%u k=%u must be >= 1", name, m, k);
-  REQUIRE(k <= kMaxK && m < kMaxRows, BQ_EINVAL, "%s: m=%u k=%u too large", name, m, k);
+  REQUIRE(k <= kMaxK && (uint64_t)m * bqmm::norm_threads(kpad) < kMaxThreads, BQ_EINVAL, "%s: m=%u k=%u too large", name, m,
+          k);
   REQUIRE(eps >= 0.0 && eps <= 1e30, BQ_EINVAL, "%s: eps=%g must be a number >= 0", name, eps);
   REQUIRE(aligned16(x) && aligned16(residual) && aligned16(weight) && aligned16(out), BQ_EALIGN,
           "%s: buffers must be 16-byte aligned", name);
@@ -502,8 +506,9 @@ uint64_t heads_span(uint32_t tokens, uint32_t heads, uint32_t d, uint32_t token,
 }
 
 // What the two forms of the delta rule check alike; *nothing is set where
-// there is nothing to do.
-int check_delta(const char *name, const bqmm::DeltaArgs &a, bool *nothing) {
+// there is nothing to do.  A workgroup has so many threads for so many columns
+// of a head's state.
+int check_delta(const char *name, const bqmm::DeltaArgs &a, uint32_t threads, uint32_t columns, bool *nothing) {
   *nothing = a.count == 0u;
   REQUIRE(a.hk >= 1 && a.hv >= 1 && a.hv % a.hk == 0, BQ_EINVAL, "%s: hk=%u must divide hv=%u", name, a.hk, a.hv);
   REQUIRE(a.dk >= 1 && a.dv >= 1, BQ_EINVAL, "%s: dk=%u dv=%u must be >= 1", name, a.dk, a.dv);
@@ -511,8 +516,8 @@ int check_delta(const char *name, const bqmm::DeltaArgs &a, bool *nothing) {
   REQUIRE(a.hv <= 65535u && a.dv <= 65535u && (uint64_t)a.hv * a.dv < (1ull << 24) && a.tokens < kMaxRows && a.count < kMaxRows && a.state_slots < kMaxRows,
           BQ_EINVAL, "%s: tokens=%u count=%u slots=%u hv=%u dv=%u too large", name, a.tokens, a.count, a.state_slots,
           a.hv, a.dv);
-  // one grid dimension: a workgroup for at most eight columns of a head's state
-  REQUIRE((uint64_t)a.count * a.hv < (1ull << 31) / ((a.dv + 7u) / 8u), BQ_EINVAL,
+  // (the launches round the heads up to eight)
+  REQUIRE((uint64_t)a.count * a.hv + 8u < kMaxThreads / threads / ((a.dv + columns - 1u) / columns), BQ_EINVAL,
           "%s: count=%u hv=%u dv=%u too large", name, a.count, a.hv, a.dv);
   if (*nothing) return BQ_OK;
   REQUIRE(a.starts, BQ_EINVAL, "%s: null pointer", name);
@@ -610,7 +615,8 @@ uint64_t int8_rows_bytes(uint32_t rows, uint32_t k) { return k > kMaxK ? 0 : i8_
 int add_rms_norm_bf16(const void *x_bf16, void *residual_bf16, const void *weight_bf16, void *out_bf16, uint32_t m,
                       uint32_t k, double eps, void *stream) {
   const char *name = "add_rms_norm_bf16";
-  const int st = check_norm(name, x_bf16, residual_bf16, weight_bf16, out_bf16, m, k, eps, bf16_bytes(m, k));
+  const int st = check_norm(name, x_bf16, residual_bf16, weight_bf16, out_bf16, m, k, bqmm::norm_padded(k, 8), eps,
+                            bf16_bytes(m, k));
   if (st != BQ_OK) return st;
   return hip_status(
       bqmm::launch_add_rms_norm_bf16(x_bf16, residual_bf16, weight_bf16, out_bf16, m, k, eps, as_stream(stream)), name);
@@ -619,7 +625,8 @@ int add_rms_norm_bf16(const void *x_bf16, void *residual_bf16, const void *weigh
 int add_rms_norm_quantize_q8_1(const void *x_bf16, void *residual_bf16, const void *weight_bf16, void *out_q8,
                                uint32_t m, uint32_t k, double eps, void *stream) {
   const char *name = "add_rms_norm_quantize_q8_1";
-  const int st = check_norm(name, x_bf16, residual_bf16, weight_bf16, out_q8, m, k, eps, q8_bytes(m, k));
+  const int st = check_norm(name, x_bf16, residual_bf16, weight_bf16, out_q8, m, k, bqmm::norm_padded(k, 256), eps,
+                            q8_bytes(m, k));
   if (st != BQ_OK) return st;
   return hip_status(bqmm::launch_add_rms_norm_quantize_q8_1(x_bf16, residual_bf16, weight_bf16, out_q8, m, k, eps,
                                                             as_stream(stream)),
@@ -629,7 +636,8 @@ int add_rms_norm_quantize_q8_1(const void *x_bf16, void *residual_bf16, const vo
 int add_rms_norm_quantize_int8(const void *x_bf16, void *residual_bf16, const void *weight_bf16, void *out_i8,
                                uint32_t m, uint32_t k, double eps, void *stream) {
   const char *name = "add_rms_norm_quantize_int8";
-  const int st = check_norm(name, x_bf16, residual_bf16, weight_bf16, out_i8, m, k, eps, i8_bytes(m, k));
+  const int st = check_norm(name, x_bf16, residual_bf16, weight_bf16, out_i8, m, k, bqmm::norm_padded(k, 128), eps,
+                            i8_bytes(m, k));
   if (st != BQ_OK) return st;
   return hip_status(bqmm::launch_add_rms_norm_quantize_int8(x_bf16, residual_bf16, weight_bf16, out_i8, m, k, eps,
                                                             as_stream(stream)),
@@ -640,7 +648,8 @@ int quantize_rows_int8(const void *x_bf16, void *out_i8, uint32_t rows, uint32_t
   const char *name = "quantize_rows_int8";
   REQUIRE(x_bf16 && out_i8, BQ_EINVAL, "%s: null pointer", name);
   REQUIRE(rows >= 1 && k >= 1, BQ_EINVAL, "%s: rows=%u k=%u must be >= 1", name, rows, k);
-  REQUIRE(k <= kMaxK && rows < kMaxRows, BQ_EINVAL, "%s: rows=%u k=%u too large", name, rows, k);
+  REQUIRE(k <= kMaxK && (uint64_t)rows * bqmm::norm_threads(bqmm::norm_padded(k, 128)) < kMaxThreads, BQ_EINVAL,
+          "%s: rows=%u k=%u too large", name, rows, k);
   REQUIRE(aligned16(x_bf16) && aligned16(out_i8), BQ_EALIGN, "%s: buffers must be 16-byte aligned", name);
   REQUIRE_DISJOINT(name, out_i8, i8_bytes(rows, k), x_bf16, bf16_bytes(rows, k), "the input");
   return hip_status(bqmm::launch_quantize_rows_int8(x_bf16, out_i8, rows, k, as_stream(stream)), name);
@@ -686,7 +695,7 @@ int gated_delta_rule_recurrent(const void *q_bf16, const void *k_bf16, const voi
   int st = delta_args("gated_delta_rule_recurrent", &a, q_bf16, k_bf16, v_bf16, g, beta, out_bf16, state, starts, slots, fresh, nullptr, tokens, count,
                  state_slots, hk, hv, dk, dv, q_token, q_head, k_token, k_head, v_token, v_head, scale, l2norm);
   bool nothing = false;
-  if (st == BQ_OK) st = check_delta("gated_delta_rule_recurrent", a, &nothing);
+  if (st == BQ_OK) st = check_delta("gated_delta_rule_recurrent", a, 64, 32, &nothing);
   if (st != BQ_OK) return st;
   return hip_status(nothing ? hipSuccess : bqmm::launch_delta_recurrent(a, as_stream(stream)),
                     "gated_delta_rule_recurrent");
@@ -704,11 +713,11 @@ int gated_delta_rule_chunked(const void *q_bf16, const void *k_bf16, const void 
   int st = delta_args(name, &a, q_bf16, k_bf16, v_bf16, g, beta, out_bf16, state, starts, slots, fresh, workspace, tokens, count,
                  state_slots, hk, hv, dk, dv, q_token, q_head, k_token, k_head, v_token, v_head, scale, l2norm);
   bool nothing = false;
-  if (st == BQ_OK) st = check_delta(name, a, &nothing);
+  if (st == BQ_OK) st = check_delta(name, a, 512, 16, &nothing);
   if (st != BQ_OK) return st;
   if (!nothing) {
-    REQUIRE(((uint64_t)tokens / 64u + count) * hv < (1ull << 31), BQ_EINVAL, "%s: tokens=%u count=%u hv=%u too large",
-            name, tokens, count, hv);
+    REQUIRE(((uint64_t)tokens / 64u + count) * hv < kMaxThreads / 256u, BQ_EINVAL,
+            "%s: tokens=%u count=%u hv=%u too large", name, tokens, count, hv);
     const uint64_t need = bqmm::delta_workspace_needed(tokens, count, hv, dk, dv);
     REQUIRE(workspace, BQ_EINVAL, "%s: null workspace", name);
     REQUIRE(workspace_bytes >= need, BQ_EINVAL, "%s: the workspace holds %llu bytes, %llu are needed", name,

@@ -29,9 +29,8 @@ namespace {
 
 enum { kOutBf16 = 0, kOutInt8 = 1, kOutQ81 = 2 };
 
-constexpr int kMaxThreads = 512;
-constexpr int kMaxNV = 8;
-constexpr uint32_t kMaxHeld = kMaxThreads * kMaxNV * 8u;  // 32768 values of a row in registers
+constexpr int kMaxThreads = kNormMaxThreads;
+constexpr uint32_t kMaxHeld = kNormMaxThreads * kNormMaxVectors * 8u;  // 32768 values of a row in registers
 
 // Eight bf16 values, two to a word.  Rows of odd length start at any even
 // address: 16-byte accesses with the alignment of a bf16 value (gfx950 takes
@@ -308,7 +307,7 @@ template <int kOut, bool kRes, bool kNorm>
 hipError_t launch_norm(const void *x, void *residual, const void *weight, void *out, uint32_t m, uint32_t k,
                        double eps, hipStream_t s) {
   const uint32_t to = kOut == kOutInt8 ? 128u : kOut == kOutQ81 ? 256u : 8u;
-  const uint32_t kpad = (k + to - 1u) / to * to;
+  const uint32_t kpad = norm_padded(k, to);
   const uint64_t scale_off = (uint64_t)m * kpad;
   const uint16_t *xp = static_cast<const uint16_t *>(x);
   uint16_t *rp = static_cast<uint16_t *>(residual);
@@ -322,12 +321,8 @@ hipError_t launch_norm(const void *x, void *residual, const void *weight, void *
   // As few vectors per lane as 512 lanes allow, and the lanes those take: k =
   // 5120 runs 320 lanes of two vectors, where 256 would leave half of every
   // third vector idle.
-  const uint32_t vecs = kpad / 8u;
-  uint32_t nv = (vecs + kMaxThreads - 1u) / kMaxThreads;
-  nv = nv <= 2u ? nv : nv <= 4u ? 4u : 8u;
-  const uint32_t lanes = (vecs + nv - 1u) / nv;
-  const uint32_t threads = (lanes + 63u) / 64u * 64u;
-  switch (nv) {
+  const uint32_t threads = norm_threads(kpad);
+  switch (norm_vectors(kpad)) {
     case 1: launch_held<1, kOut, kRes, kNorm>(xp, rp, wp, op, m, k, kpad, eps, scale_off, threads, s); break;
     case 2: launch_held<2, kOut, kRes, kNorm>(xp, rp, wp, op, m, k, kpad, eps, scale_off, threads, s); break;
     case 4: launch_held<4, kOut, kRes, kNorm>(xp, rp, wp, op, m, k, kpad, eps, scale_off, threads, s); break;

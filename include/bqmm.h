@@ -309,7 +309,9 @@ int silu_mul_bf16(const void *gate, const void *up, void *out, uint64_t count, v
  *                               scale = top / (127 sqrt(...)); zero codes where top is 0.
  * A row that holds a NaN or an infinity gives NaN: in bf16 where the formula
  * does, in int8 rows as a NaN scale; its q8_1 bytes are unspecified.  |h * weight|
- * has to stay below 2^128.  m, k >= 1; any k.  No two buffers may overlap. */
+ * has to stay below 2^128.  m, k >= 1; any k up to 2^30.  Up to 2^23 rows, and
+ * 2^26 of up to 512 values (a launch has fewer than 2^32 threads).  No two buffers
+ * may overlap. */
 int add_rms_norm_bf16(const void *x_bf16, void *residual_bf16, const void *weight_bf16, void *out_bf16,
                       uint32_t m, uint32_t k, double eps, void *stream);
 int add_rms_norm_quantize_q8_1(const void *x_bf16, void *residual_bf16, const void *weight_bf16, void *out_q8,
@@ -320,7 +322,8 @@ int add_rms_norm_quantize_int8(const void *x_bf16, void *residual_bf16, const vo
 /* bf16 rows [rows][k] -> int8 rows (weights [n][k] or activations [m][k]):
  * top = max |x| of the row, code = rint(127 x / top) (exact quotient, ties to
  * even), scale = top / 127; zero codes where top is 0.  A row that holds a NaN
- * or an infinity gets that as its scale, and zero codes.  rows, k >= 1. */
+ * or an infinity gets that as its scale, and zero codes.  rows, k >= 1, as many
+ * as in the norms. */
 int quantize_rows_int8(const void *x_bf16, void *out_i8, uint32_t rows, uint32_t k, void *stream);
 
 /* out[i][j] (bf16, [m][n]) = sum_t a[i][t] * w[j][t] * sa[i] * sw[j] + bias[j]:
@@ -351,7 +354,9 @@ int w8a8_gemm(const void *act_i8, const void *w_i8, const void *bias_bf16, void 
  * of no sequence are left alone.  An empty sequence keeps its state (zeros where
  * it is fresh).
  *
- * 1 <= dk <= 128, dv >= 1, hk divides hv, hv * dv < 2^24.  q, k, v, out 2-byte aligned, the
+ * 1 <= dk <= 128, dv >= 1, hk divides hv, hv * dv < 2^24.  A launch has fewer than
+ * 2^32 threads: count * hv * dv below 2^31 (_chunked: 2^27; dv in whole 32s and 16s),
+ * and (tokens / 64 + count) * hv below 2^24 (_chunked).  q, k, v, out 2-byte aligned, the
  * binary32 and int32 arrays 4-byte.  out and state overlap nothing else.
  * tokens = 0 is allowed (the token arrays may be NULL), and count = 0 (nothing
  * is done).  Captured into a graph, a call reads starts, slots and fresh at

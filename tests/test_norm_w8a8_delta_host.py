@@ -234,3 +234,29 @@ def test_long_sequences_are_cut_where_that_measured_faster(bq, tokens, count, he
     sizes = (heads, heads, 128, 128)
     chunk = chunked_need(bq, 1, 1, *sizes)  # one chunk of all heads
     assert (chunked_need(bq, tokens, count, *sizes) > (tokens // 64 + count) * chunk) == cut
+
+
+@pytest.mark.parametrize("k,rows", [(512, 1 << 26), (64, (1 << 31) - 1), (513, 1 << 25), (4096, 1 << 23), (70000, 1 << 23)])
+def test_more_threads_than_a_launch_has_are_refused(bq, k, rows):
+    """A launch's threads are counted in 32 bits."""
+    far = [at(1 << i) for i in (20, 21, 22, 23)]
+    for name in NORMS:
+        assert getattr(bq.lib(), name)(far[0], far[1], far[2], far[3], rows, k, 1e-6, None) == -1
+        assert "too large" in bq.lib().bq_last_error().decode()
+    assert bq.lib().quantize_rows_int8(far[0], far[3], rows, k, None) == -1
+    assert "too large" in bq.lib().bq_last_error().decode()
+
+
+@pytest.mark.parametrize("chunked,change", [
+    (False, dict(count=1 << 24, hk=1, hv=4, dv=32)), (False, dict(count=1 << 19, hk=1, hv=32, dv=128)),
+    (True, dict(count=1 << 15, hk=1, hv=32, dv=128)), (True, dict(count=1 << 21, hk=1, hv=4, dv=16)),
+    (True, dict(tokens=1 << 30, count=1, hk=1, hv=1, dv=1)), (True, dict(tokens=64, count=(1 << 24) - 16, hk=1, hv=1, dv=1, dk=1)),
+])
+def test_more_threads_than_a_delta_launch_has_are_refused(bq, chunked, change):
+    far = {k: at(1 << (20 + i)) for i, k in enumerate(("q", "k", "v", "g", "beta", "out", "state", "starts"))}
+    v = list(delta_args(**far, slots=None, fresh=None, state_slots=1, **change).values())
+    if chunked:
+        v[10:10] = [at(12), 1 << 62]
+    fn = bq.lib().gated_delta_rule_chunked if chunked else bq.lib().gated_delta_rule_recurrent
+    assert fn(*v) == -1
+    assert "too large" in bq.lib().bq_last_error().decode()
