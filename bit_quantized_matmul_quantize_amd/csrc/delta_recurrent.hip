@@ -25,6 +25,7 @@ namespace bqmm {
 namespace {
 
 constexpr float kNormEps = 1e-6f;
+constexpr uint32_t kQuads = 8;  // quads of columns that a wave takes (add_eighths sums over the lanes that share them)
 
 typedef float Float4 __attribute__((ext_vector_type(4), aligned(4)));
 template <int N>
@@ -70,7 +71,7 @@ __device__ __forceinline__ float add_eighths(float x) {
   return x + __shfl_xor(x, 32);
 }
 
-template <int kDk, int kQuads, bool kWhole>
+template <int kDk, bool kWhole>
 __global__ __launch_bounds__(64) void delta_recurrent_kernel(const DeltaArgs a) {
   constexpr int kGroups = 64 / kQuads;
   constexpr int kRows = kDk / kGroups;
@@ -128,7 +129,6 @@ __global__ __launch_bounds__(64) void delta_recurrent_kernel(const DeltaArgs a) 
       sum[9] = fmaf(q[i], q[i], sum[9]);
       sum[10] = fmaf(q[i], k[i], sum[10]);
     }
-    static_assert(kQuads == 8, "the lanes that share columns");
 #pragma unroll
     for (int j = 0; j < 11; ++j) sum[j] = add_eighths(sum[j]);
     const float rk = a.l2norm ? 1.0f / sqrtf(sum[8] + kNormEps) : 1.0f;
@@ -175,20 +175,20 @@ __global__ __launch_bounds__(64) void delta_recurrent_kernel(const DeltaArgs a) 
   }
 }
 
-template <int kDk, int kQuads>
+template <int kDk>
 hipError_t launch_recurrent(const DeltaArgs &a, hipStream_t s) {
   const uint64_t blocks = ((uint64_t)a.count * a.hv * ((a.dv + 4ull * kQuads - 1u) / (4ull * kQuads)) + 7u) / 8u * 8u;
   if (a.dk == (uint32_t)kDk && a.dv % 4u == 0u)
-    hipLaunchKernelGGL((delta_recurrent_kernel<kDk, kQuads, true>), dim3((uint32_t)blocks), dim3(64), 0, s, a);
+    hipLaunchKernelGGL((delta_recurrent_kernel<kDk, true>), dim3((uint32_t)blocks), dim3(64), 0, s, a);
   else
-    hipLaunchKernelGGL((delta_recurrent_kernel<kDk, kQuads, false>), dim3((uint32_t)blocks), dim3(64), 0, s, a);
+    hipLaunchKernelGGL((delta_recurrent_kernel<kDk, false>), dim3((uint32_t)blocks), dim3(64), 0, s, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_delta_recurrent(const DeltaArgs &a, hipStream_t s) {
-  return a.dk <= 64u ? launch_recurrent<64, 8>(a, s) : launch_recurrent<128, 8>(a, s);
+  return a.dk <= 64u ? launch_recurrent<64>(a, s) : launch_recurrent<128>(a, s);
 }
 
 }  // namespace bqmm

@@ -260,3 +260,9 @@ def test_more_threads_than_a_delta_launch_has_are_refused(bq, chunked, change):
     fn = bq.lib().gated_delta_rule_chunked if chunked else bq.lib().gated_delta_rule_recurrent
     assert fn(*v) == -1
     assert "too large" in bq.lib().bq_last_error().decode()
+
+
+def test_int8_rows_bytes_is_the_librarys(bq):
+    for rows in (1, 2, 3, 4096, (1 << 31) - 1):
+        for k in (1, 127, 128, 129, 2563, 131071, 1 << 30, (1 << 30) + 1, (1 << 32) - 1):
+            assert bq.int8_rows_bytes(rows, k) == bq.lib().int8_rows_bytes(rows, k), (rows, k)
