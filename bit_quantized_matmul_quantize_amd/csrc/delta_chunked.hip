@@ -40,7 +40,7 @@ typedef float v2f __attribute__((ext_vector_type(2)));
 
 constexpr int kChunk = 64;
 constexpr int kThreads = 256;
-constexpr uint32_t kCus = 256;
+constexpr uint32_t kCus = 256;  // of a whole card; on a part of it the choices that go by it are as right, and less fast
 constexpr float kNormEps = 1e-6f;
 constexpr float kNoDecay = -1e6f;  // exp of it is zero; sums of 64 of them stay exact to 2^-26
 
@@ -176,11 +176,11 @@ __device__ __forceinline__ float add_lanes(float x) {
 
 // A workgroup takes a chunk, a key head, and kHeads of its value heads, side by
 // side: they share the keys, the queries and their products, and each step's
-// waits.  Bound by those waits, not by memory (2048 tokens of 32 heads leave 33
-// MB in 16 us, one workgroup alone takes 9), so four workgroups share a CU: A
+// waits.  Bound by those waits, not by memory (2048 tokens of 32 heads leave 39
+// MB in 17 us, one workgroup alone takes 9), so four workgroups share a CU: A
 // lies where the keys and queries were, T in A's place, 128 registers a lane do.
-// (With places of their own, two a CU: packed prompts of 2322 tokens take 84.8
-// us in both launches, and 78.4 so.)
+// (With places of their own, two a CU, packed prompts of 2322 tokens took 84.8
+// us in both launches where they took 78.4 so.)
 template <int kDk, int kHeads, bool kWhole>
 __global__ __launch_bounds__(kThreads, 4) void delta_chunk_kernel(const DeltaArgs a) {
   constexpr int kRow = 2 * kStride;  // bf16 per staged row, which a row of A takes the place of
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(kThreads, 4) void delta_chunk_kernel(const DeltaArg
   const uint32_t tid = threadIdx.x, lane = tid & 63u, w = __builtin_amdgcn_readfirstlane(tid >> 6), lr = lane & 15u, lq = lane >> 4;
   const uint32_t sets = a.hv / kHeads;  // of value heads
   // From the last chunk to the first, so that what the second launch begins with was written last and is still in the
-  // caches (16384 tokens of 32 heads leave 262 MB: both launches 517 us, and 553 from the first on).
+  // caches (16384 tokens of 32 heads leave 313 MB: both launches 520 us, and 527 from the first on).
   const uint32_t place = gridDim.x / sets - 1u - blockIdx.x / sets, head0 = blockIdx.x % sets * kHeads, khead = head0 / (a.hv / a.hk);
 
   // the sequence that the place belongs to: the last whose first place is at or below it
@@ -464,12 +464,12 @@ __global__ __launch_bounds__(kThreads, 4) void delta_chunk_kernel(const DeltaArg
 // those have been used: the loads are spread over the step and have most of
 // its time to arrive.
 //
-// What bounds it is the chain itself, 1.3 us per chunk with every operand at
-// hand: three exchanges through LDS, and the latency of what lies between them.
-// So where there are more workgroups than CUs two should share one: 128
-// registers per lane allow it (packed prompts of 2322 tokens: the launch 63 us,
-// and 82 with the 142 that the compiler takes unasked; the kernels of odd sizes
-// would spill and keep theirs).
+// What bounds it is the chain itself, 1.45 us per chunk of one head alone: three
+// exchanges through LDS, and the latency of what lies between them (1.8 with a
+// workgroup on every CU, 2048 tokens of 32 heads; 1.8 where the operands pass
+// through the caches, 16384 tokens).  So where there are more workgroups than CUs
+// two should share one: 128 registers per lane allow it (the kernels of odd sizes
+// are not held to it; all but one fit too).
 constexpr int kScanThreads = 512;
 
 // Where a few long sequences leave most CUs without work, the chunks of a
@@ -481,8 +481,8 @@ constexpr int kScanThreads = 512;
 // from N and M of those before it, and runs it.
 //
 // That is up to three times the work, for a chain of two segments and a product
-// per segment instead of all chunks: one sequence of 8192 tokens takes 67 us with
-// one head (169 in one chain), 89 with four (182).
+// per segment instead of all chunks: one sequence of 9000 tokens takes 79 us with
+// one head (211 in one chain), 101 with four (221).
 enum { kChain = 0, kParts = 1, kRest = 2 };
 
 // What both kinds of waves know of their work.
@@ -538,10 +538,11 @@ constexpr int kKeyRow = 32 * kTiles + 16;
 // so that one access of the CU's cache serves them; the keys then go through
 // LDS before their first product, the queries change lanes.  As the operands lie
 // in the lanes each lane's 16 bytes are an access: 2900 a chunk, which is what
-// two workgroups on a CU wait for (packed prompts of 2322 tokens: 82.6 us, and
-// 86.8 so; 16384 tokens: 474 and 504).  A chain of 64 values has fewer, and the
-// way through LDS is longer (2048 tokens, packed, 1 head: 25.5 and 24.2 us);
-// in segments the registers would not do (8192 tokens, 1 head: 70.1 and 67.1).
+// two workgroups on a CU wait for (prompts of up to 927 tokens, 16 heads: 59.6 us
+// by quads, and 62.7 without; packed prompts of 2322 tokens 79.8 and 81.5; 16384
+// tokens 520 and 535).  A chain of 64 values has fewer, and the way through LDS is
+// longer (2048 tokens, packed, 1 head: 25.5 us by quads, and 24.2); nor do they
+// pay in segments (8192 tokens, 1 head: 72.9 by quads, and 72.3).
 template <int kTiles, bool kWhole, int kMode>
 constexpr bool kQuads = kTiles == 2 && kWhole && kMode == 0;
 // values per column of the state before a segment, likewise
@@ -1079,7 +1080,7 @@ __global__ __launch_bounds__(kScanThreads, kWhole ? 4 : 2) void delta_scan_kerne
   if constexpr (kMode == kChain) {
     if (place >= a.count) return;
     // Where the workgroups do not all start at once, the longest chains go first (8 prompts of 2 to 927 tokens, 16
-    // heads: 45.7 us, and 51.8 in their own order).
+    // heads: 59 us, and 62 to 65 in their own order).
     if (a.count > 1u && a.count <= 64u && a.count * a.hv * v_blocks > kCus) seq = by_length(a, place, lane);
   } else {
     const uint32_t in = a.segment * kChunk;

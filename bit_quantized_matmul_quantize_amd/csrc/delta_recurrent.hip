@@ -15,10 +15,12 @@
 //
 // Bound by memory where the batch is large: 8 dk dv bytes of state move for
 // 6 dk dv operations per token.  96 sequences of 32 heads of 128 x 128 (405 MB):
-// 72 us, 5.6 TB/s (a large copy reaches 5.2); 83 us without the non-temporal
+// 72 us, 5.6 TB/s (part of it in the 256 MB cache); 83 us without the non-temporal
 // hints (a state is not used again before the next token) and without a run of
-// heads per XCD.  One sequence (4.2 MB) 4.7 us, two dependent trips to memory
-// and a launch; 16 columns per wave 5.0, 8 columns 7.6, 64 columns 5.5.
+// heads per XCD.  One sequence (4.2 MB) 4.7 us: a launch and three dependent trips
+// to memory (the ranges; the state, q and k; g, beta and v, which the compiler
+// issues after the sums where dk is 128), and one more or two per further token,
+// whose loads wait for the stores of the one before.  16 columns per wave 5.0, 8 columns 7.6, 64 columns 5.5.
 #include "delta_common.h"
 
 namespace bqmm {

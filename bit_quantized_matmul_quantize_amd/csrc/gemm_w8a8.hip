@@ -380,8 +380,9 @@ hipError_t launch_tiles(const uint8_t *act, const uint8_t *w, const Scales &s, u
 }
 
 // Tiles of 256 x 256, one per CU at a time.  kQuarters: whole rounds of them, and what is
-// left over in quarters where at most two rounds of those suffice (4096 x 17408,
-// k = 5120: 64 of 1088 tiles are left over; 381 us, and 422 with a fifth round).
+// left over in quarters where at most two rounds of those suffice (4096 x 4352,
+// k = 4096: 16 of 272 tiles are left over; 85.3 us, and 118.8 with a second round;
+// 4096 x 5120, k = 17408: 64 of 320; 297, and 384).
 bool quarters(uint32_t total, uint32_t cus) {
   const uint32_t left = total % cus;
   return total > cus && cus % 8u == 0u && left > 0u && 2u * left <= cus;
@@ -422,9 +423,10 @@ constexpr Form kFormCosts[kForms] = {
     {64, 64, 2, 3.2f, 0.43f, 0.245f},  // 256 x 4096, k 4096: 11.2, 13.5 of the next two
     {64, 128, 1, 3.8f, 0.37f, 0.32f},  // 512 x 4096, k 4096: 15.7, 16.9 of 64 x 64, 18.4 of 128 x 128
     {128, 64, 1, 3.8f, 0.37f, 0.32f},
-    {128, 128, 1, 4.0f, 0.62f, 0.43f},  // four stages; 1024 x 4096, k 4096: 24.0, 28.2 with two, 30.0 of 64 x 128
-    {128, 128, 2, 4.0f, 1.13f, 0.79f},  // two stages, two workgroups a CU; 2048 x 4096, k 4096: 39.1, 46.8 with four, 53.8 of 256 x 256
-    {256, 256, 1, 6.0f, 2.2f, 2.2f},    // 4096 x 4096, k 4096: 75.6, 86.4 of 128 x 128
+    {128, 128, 1, 4.0f, 0.62f, 0.43f},  // four stages; 1024 x 4096, k 4096: 25.0, 30.2 with two, 55.5 of 256 x 256
+    {128, 128, 2, 4.0f, 1.13f, 0.79f},  // two stages, two workgroups a CU; 2048 x 4096, k 4096: 40.0, 47.1 with four, 60.6 of 256 x 256
+    // 8192 x 4096, k 4096: 139.9, 145.4 of 128 x 128 with two stages; at 4096 x 4096 a tie for the model, which takes those (77.4, and 75.0)
+    {256, 256, 1, 6.0f, 2.2f, 2.2f},
 };
 
 float cost(int form, uint32_t m, uint32_t n, uint32_t steps, uint32_t cus) {

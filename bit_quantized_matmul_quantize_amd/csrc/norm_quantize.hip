@@ -16,9 +16,9 @@
 //
 // Bound by memory: the row is read once, held in registers as t between the
 // reduction (sum of squares, largest |t|) and the output, and written once.
-// 4096 rows of 5120 with the residual to int8 (147 MB): 25.6 us, 5.7 TB/s; 36.5
-// us while the roundings to bf16 and the codes took twice the instructions
-// (the vector ALU then bound it as much as memory).  One row of 2048: 2.8 us.
+// 4096 rows of 5120 with the residual to int8 (147 MB): 24.0 us, 6.1 TB/s (part
+// of it in the 256 MB cache; a 2 x 2.1 GB copy reaches 4.8); 36.5 us while the roundings to bf16 and the codes took twice the instructions
+// (the vector ALU then bound it as much as memory).  One row of 2048: 2.7 us.
 // One workgroup per row; a lane owns kNV vectors of eight consecutive values
 // (16-byte loads), so a row of k values takes k / (8 kNV) lanes.  Rows beyond
 // kMaxHeld values are read a second time instead of being held.
