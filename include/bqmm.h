@@ -339,7 +339,8 @@ int w8a8_gemm(const void *act_i8, const void *w_i8, const void *bias_bf16, void 
  * (it reads key head h / (hv / hk)), with its state S [dk][dv] in binary32 and
  * for each token a = exp(g[token][h]), b = beta[token][h]:
  *   S = a S;  S = S + k (b (v - k^T S))^T;  out[token][h] = bf16_rne(scale q^T S).
- * With l2norm != 0, q and k are divided by sqrt(|.|^2 + 1e-6) first.
+ * With l2norm != 0, q and k are divided by sqrt(|.|^2 + 1e-6) first (in binary32:
+ * |q|^2 and |k|^2 have to stay below 2^128).
  *
  * q, k: bf16, head i of token t starts at t * q_token + i * q_head (values), its
  * dk values are consecutive; v likewise with dv (token strides below
