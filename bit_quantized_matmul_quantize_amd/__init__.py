@@ -57,6 +57,12 @@ EXPORTS = {
     "w8a8_gemm": (_I, [_P, _P, _P, _P, _U32, _U32, _U32, _P]),
     "gated_delta_rule_recurrent": (_I, [_P] * 10 + [_U32] * 7 + [_U64] * 6 + [_F, _I, _P]),
     "gated_delta_rule_chunked": (_I, [_P] * 11 + [_U64] + [_U32] * 7 + [_U64] * 6 + [_F, _I, _P]),
+    "kv_cache_page_bytes": (_U64, [_U32] * 4),
+    "paged_attention_workspace_bytes": (_U64, [_U32] * 5),
+    "rope_write_kv_cache": (_I, [_P] * 14 + [_U32] * 12 + [_U64] * 6 + [_F, _P]),
+    "read_kv_cache": (_I, [_P] * 7 + [_U32] * 8 + [_P]),
+    "paged_attention_decode": (_I, [_P] * 8 + [_U64] + [_U32] * 9 + [_U64] * 2 + [_U32, _F, _F, _P]),
+    "paged_attention_prefill": (_I, [_P] * 7 + [_U32] * 9 + [_U64] * 2 + [_U32, _F, _F, _P]),
     "q2_0_mmq_blockdots": (_I, [_P, _P, _P, _U32, _U32, _U32, _U32, _U32, _U32, _U32, _P]),
     "q4k_mmq_blockdots": (_I, [_P, _P, _P, _U32, _U32, _U32, _U32, _U32, _U32, _U32, _P]),
 }
@@ -452,6 +458,131 @@ def gated_delta_rule_chunked(q, k, v, g, beta, out, state, starts, workspace, sl
     """As gated_delta_rule_recurrent, for prompts; workspace: gated_delta_rule_workspace_bytes(...) bytes, uint8."""
     _delta(lib().gated_delta_rule_chunked, q, k, v, g, beta, out, state, starts, slots, fresh,
            (_u8(workspace, "workspace"),), scale, l2norm, stream)
+
+
+# ---- paged key-value cache ---------------------------------------------------
+
+def kv_cache_page_bytes(page: int, hk: int, d: int, bits: int = 16) -> int:
+    """Bytes of a page of the keys', or the values', cache: a cache of n pages is n times as many."""
+    return int(lib().kv_cache_page_bytes(page, hk, d, bits))
+
+
+def paged_attention_workspace_bytes(tokens: int, count: int, hq: int, hk: int, d: int) -> int:
+    """Enough for every paged_attention_decode of at most these tokens and sequences."""
+    return int(lib().paged_attention_workspace_bytes(tokens, count, hq, hk, d))
+
+
+def _paged(k_cache, v_cache, starts, lens, table, page, hk, d, bits):
+    """Of the sequences and caches of a call: (count, pages, width)."""
+    _u8(k_cache, "k_cache")
+    if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape:
+        raise ValueError(f"v_cache: expected the keys' bytes {tuple(k_cache.shape)}, got {v_cache.dtype} {tuple(v_cache.shape)}")
+    if starts.dim() != 1 or starts.numel() < 1 or table.dim() != 2:
+        raise ValueError("expected starts as [count + 1] and table as [count, width]")
+    count, width = starts.numel() - 1, table.shape[1]
+    _typed(starts, "torch.int32", (count + 1,), "starts")
+    _typed(lens, "torch.int32", (count,), "lens")
+    _typed(table, "torch.int32", (count, width), "table")
+    # (sizes that the library refuses give no bytes; it says why)
+    size = hk * page * (2 * d if bits == 16 else d + 4)
+    if size > 0 and _nbytes(k_cache) % size:
+        raise ValueError(f"k_cache: {_nbytes(k_cache)} bytes are no whole number of pages of {size}")
+    return count, _nbytes(k_cache) // size if size > 0 else 0, width
+
+
+def _on_device_of(q, *tensors):
+    """Device pointers of contiguous tensors that lie on q's device."""
+    for t in tensors:
+        if t is not None and t.get_device() != q.get_device():
+            _same_device(q, *tensors)
+            raise ValueError("expected a device tensor")
+    if q.get_device() < 0:
+        raise ValueError("expected a device tensor")
+    return _ptrs(*tensors)
+
+
+def rope_write_kv_cache(q, k, v, q_out, k_cache, v_cache, starts, lens, table, page: int, bits: int = 16, cos_sin=None,
+                        positions=None, axis=None, q_norm=None, k_norm=None, eps: float = 1e-6, stream=None):
+    """q: [tokens, hq, d], k, v: [tokens, hk, d] bf16, each head's values contiguous; q_out: [tokens, hq, d] bf16 (q and
+    q_out may be None); k_cache, v_cache: uint8, whole pages; starts: [count + 1], lens: [count], table: [count, width]
+    int32; cos_sin: [angles, 2, rot / 2] float32; positions: [tokens] or [axes, tokens] int32; axis: [rot / 2] uint8;
+    q_norm, k_norm: [d] bf16."""
+    if k.dim() != 3 or (q is None) != (q_out is None) or (q is not None and q.dim() != 3):
+        raise ValueError("expected q, k, v as [tokens, heads, d], and q_out with q alone")
+    tokens, hk, d = k.shape
+    hq, rot, angles, axes, qs = 0, 0, 0, 0, (0, 0)
+    if v.shape != k.shape:
+        raise ValueError(f"v: expected shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    if q is not None:
+        hq = q.shape[1]
+        if q.shape[0] != tokens or q.shape[2] != d:
+            raise ValueError(f"q: expected [{tokens}, heads, {d}], got {tuple(q.shape)}")
+        qs = _strides(q, "q")
+        _typed(q_out, "torch.bfloat16", (tokens, hq, d), "q_out")
+    if cos_sin is not None:
+        if cos_sin.dim() != 3:
+            raise ValueError("expected cos_sin as [angles, 2, rot / 2]")
+        angles, _, half = cos_sin.shape
+        _typed(cos_sin, "torch.float32", (angles, 2, half), "cos_sin")
+        rot = 2 * half
+    if axis is not None:
+        if positions is None or positions.dim() != 2:
+            raise ValueError("expected positions as [axes, tokens] with axis")
+        axes = positions.shape[0]
+        _typed(axis, "torch.uint8", (rot // 2,), "axis")
+        _typed(positions, "torch.int32", (axes, tokens), "positions")
+    elif positions is not None:
+        _typed(positions, "torch.int32", (tokens,), "positions")
+    for w, what in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if w is not None:
+            _typed(w, "torch.bfloat16", (d,), what)
+    count, pages, width = _paged(k_cache, v_cache, starts, lens, table, page, hk, d, bits)
+    rest = _on_device_of(k, q_out, k_cache, v_cache, starts, lens, table, cos_sin, positions, axis, q_norm, k_norm)
+    if v.get_device() != k.get_device() or (q is not None and q.get_device() != k.get_device()):
+        raise ValueError("q, k and v on different devices")
+    _check(lib().rope_write_kv_cache(None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), *rest, tokens, count,
+                                     pages, page, width, bits, hq, hk, d, rot, angles, axes, *qs, *_strides(k, "k"),
+                                     *_strides(v, "v"), eps, _stream(stream)))
+
+
+def read_kv_cache(k_cache, v_cache, k, v, starts, lens, table, page: int, bits: int = 16, stream=None):
+    """The new tokens' rows back: k, v: [tokens, hk, d] bf16; the others as in rope_write_kv_cache."""
+    if k.dim() != 3:
+        raise ValueError("expected k, v as [tokens, hk, d]")
+    tokens, hk, d = k.shape
+    _typed(k, "torch.bfloat16", (tokens, hk, d), "k")
+    _typed(v, "torch.bfloat16", (tokens, hk, d), "v")
+    count, pages, width = _paged(k_cache, v_cache, starts, lens, table, page, hk, d, bits)
+    _check(lib().read_kv_cache(*_ptrs(k_cache, v_cache, k, v, starts, lens, table), tokens, count, pages, page, width, bits,
+                               hk, d, _stream(stream)))
+
+
+def _attention(fn, q, k_cache, v_cache, out, starts, lens, table, workspace, hk, page, bits, scale, window, cap, stream):
+    if q.dim() != 3:
+        raise ValueError("expected q as [tokens, hq, d]")
+    tokens, hq, d = q.shape
+    qs = _strides(q, "q")
+    _typed(out, "torch.bfloat16", q.shape, "out")
+    count, pages, width = _paged(k_cache, v_cache, starts, lens, table, page, hk, d, bits)
+    rest = _on_device_of(q, k_cache, v_cache, out, starts, lens, table, *workspace)
+    _check(fn(q.data_ptr(), *rest, *map(_nbytes, workspace), tokens, count, pages, page, width, bits, hq, hk, d, *qs, window,
+              d ** -0.5 if scale is None else scale, cap, _stream(stream)))
+
+
+def paged_attention_decode(q, k_cache, v_cache, out, starts, lens, table, workspace, hk: int, page: int, bits: int = 16,
+                           scale: float | None = None, window: int = 0, cap: float = 0.0, stream=None):
+    """q: [tokens, hq, d] bf16, each head's values contiguous; out: [tokens, hq, d] bf16; k_cache, v_cache: uint8, whole
+    pages; starts: [count + 1], lens: [count], table: [count, width] int32; workspace:
+    paged_attention_workspace_bytes(...) bytes, uint8.  scale: d ** -0.5 by default."""
+    _attention(lib().paged_attention_decode, q, k_cache, v_cache, out, starts, lens, table, (_u8(workspace, "workspace"),),
+               hk, page, bits, scale, window, cap, stream)
+
+
+def paged_attention_prefill(q, k_cache, v_cache, out, starts, lens, table, hk: int, page: int, bits: int = 16,
+                            scale: float | None = None, window: int = 0, cap: float = 0.0, stream=None):
+    """As paged_attention_decode, for prompts."""
+    _attention(lib().paged_attention_prefill, q, k_cache, v_cache, out, starts, lens, table, (), hk, page, bits, scale,
+               window, cap, stream)
 
 
 def _blockdots(fn, act_q8, w, w_bytes, out_i32, m0, mt, n0, nt, m, n, k, stream):

@@ -32,7 +32,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["quantize.hip", "quantize_q4k.hip", "elementwise.hip", "gemv.hip", "gemv_mfma.hip",
            "gemv_q4k.hip", "mmq_q2.hip", "mmq_q4k.hip", "gemm_bf16.hip",
-           "norm_quantize.hip", "gemm_w8a8.hip", "delta_recurrent.hip", "delta_chunked.hip", "capi.cpp"]
+           "norm_quantize.hip", "gemm_w8a8.hip", "delta_recurrent.hip", "delta_chunked.hip",
+           "paged_cache.hip", "paged_decode.hip", "paged_prefill.hip", "capi.cpp"]
 
 COMMON = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",

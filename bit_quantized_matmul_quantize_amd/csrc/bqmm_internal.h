@@ -185,4 +185,30 @@ hipError_t launch_delta_chunked(const DeltaArgs &a, hipStream_t s);
 uint64_t delta_workspace_needed(uint32_t tokens, uint32_t count, uint32_t hv, uint32_t dk, uint32_t dv);
 uint64_t delta_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hv, uint32_t dk, uint32_t dv);
 
+// The paged key-value cache's arguments.  Strides of q, k and v in values; q, its
+// output and the rotation may be absent.
+struct PagedArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t *out;          // rotated q, or the attention's output: [tokens][hq][d]
+  uint16_t *k_out, *v_out;  // what is read back: [tokens][hk][d]
+  uint8_t *k_cache, *v_cache;
+  const int32_t *starts, *lens, *table, *positions;
+  const uint8_t *axis;
+  const float *cos_sin;
+  const uint16_t *q_norm, *k_norm;
+  uint8_t *workspace;
+  uint64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  uint32_t tokens, count, pages, page_shift, width, bits, hq, hk, d;
+  uint32_t rot, axes, angles;  // values of a head that are rotated; positions of a token; rows of cos_sin
+  uint32_t window;
+  float scale, cap, eps;
+};
+hipError_t launch_paged_write(const PagedArgs &a, hipStream_t s);
+hipError_t launch_paged_read(const PagedArgs &a, hipStream_t s);
+hipError_t launch_paged_decode(const PagedArgs &a, hipStream_t s);
+hipError_t launch_paged_prefill(const PagedArgs &a, hipStream_t s);
+// of the decoding form: for these sizes, and for these and every smaller tokens and count
+uint64_t paged_workspace_needed(uint32_t tokens, uint32_t count, uint32_t hq, uint32_t hk, uint32_t d);
+uint64_t paged_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hq, uint32_t hk, uint32_t d);
+
 }  // namespace bqmm

@@ -1,5 +1,6 @@
 // The C ABI: argument checks, then one launch (or two, for the dispatcher) on
 // the caller's stream.  Every check runs before any HIP call.
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -741,6 +742,273 @@ int gated_delta_rule_chunked(const void *q_bf16, const void *k_bf16, const void 
             BQ_EINVAL, "%s: the workspace overlaps slots or fresh", name);
   }
   return hip_status(nothing ? hipSuccess : bqmm::launch_delta_chunked(a, as_stream(stream)), name);
+}
+
+}  // extern "C"
+
+// ---- paged key-value cache and the attention over it -----------------------
+
+namespace {
+
+constexpr uint32_t kMaxPlaces = 1u << 30;  // tokens of a call or a sequence
+
+uint64_t block_bytes(uint32_t page, uint32_t d, uint32_t bits) {
+  return bits == 16u ? 2ull * page * d : (uint64_t)page * (d + 4ull);
+}
+
+bool page_ok(uint32_t page) { return page >= 16u && page <= 1024u && (page & (page - 1u)) == 0u; }
+
+// A strided [tokens][heads][d] bf16 array whose heads are read in 16-byte
+// pieces.  A stride that is never used (one token, one head) counts as zero,
+// whatever it is.
+int check_heads(const char *name, const char *what, const void *x, uint32_t tokens, uint32_t heads, uint64_t *token,
+                uint64_t *head) {
+  if (tokens <= 1u) *token = 0;
+  if (heads <= 1u) *head = 0;
+  REQUIRE(*token < (1ull << 31) && *head < (1ull << 31), BQ_EINVAL, "%s: the strides of %s are too large", name, what);
+  REQUIRE(aligned16(x) && *token % 8u == 0 && *head % 8u == 0, BQ_EALIGN, "%s: the heads of %s must be 16-byte aligned", name,
+          what);
+  return BQ_OK;
+}
+
+struct Range {
+  const void *p;
+  uint64_t n;
+  const char *what;
+};
+
+// What every call over a cache checks alike; *nothing is set where there is
+// nothing to do.
+int check_paged(const char *name, const bqmm::PagedArgs &a, uint32_t page, bool *nothing) {
+  *nothing = a.count == 0u || a.tokens == 0u;
+  REQUIRE(a.bits == 16u || a.bits == 8u, BQ_EUNSUPPORTED, "%s: bits=%u must be 16 or 8", name, a.bits);
+  REQUIRE(page_ok(page), BQ_EUNSUPPORTED, "%s: page=%u must be a power of two from 16 to 1024", name, page);
+  REQUIRE(a.d >= 16u && a.d <= 256u && a.d % 16u == 0, BQ_EUNSUPPORTED, "%s: d=%u must be a multiple of 16 up to 256", name, a.d);
+  REQUIRE(a.hk >= 1u && a.hk <= 65535u && a.hq <= 65535u, BQ_EINVAL, "%s: hq=%u hk=%u must be 1 to 65535", name, a.hq, a.hk);
+  REQUIRE(a.pages >= 1u && a.pages < (1u << 31) && a.width >= 1u && (uint64_t)a.width * page <= kMaxPlaces, BQ_EINVAL,
+          "%s: pages=%u width=%u must be >= 1, width * page at most 2^30", name, a.pages, a.width);
+  REQUIRE(a.tokens <= kMaxPlaces && a.count <= kMaxPlaces, BQ_EINVAL, "%s: tokens=%u count=%u too large", name, a.tokens, a.count);
+  if (*nothing) return BQ_OK;
+  REQUIRE(a.k_cache && a.v_cache && a.starts && a.lens && a.table, BQ_EINVAL, "%s: null pointer", name);
+  REQUIRE(aligned16(a.k_cache) && aligned16(a.v_cache), BQ_EALIGN, "%s: the caches must be 16-byte aligned", name);
+  REQUIRE(aligned_to(a.starts, 4) && aligned_to(a.lens, 4) && aligned_to(a.table, 4), BQ_EALIGN,
+          "%s: int32 arrays must be 4-byte aligned", name);
+  return BQ_OK;
+}
+
+uint64_t cache_bytes(const bqmm::PagedArgs &a) { return block_bytes(1u << a.page_shift, a.d, a.bits) * a.hk * a.pages; }
+
+// An output range against all that the call reads or writes besides.
+int check_apart(const char *name, const bqmm::PagedArgs &a, const Range &out, bool caches, const Range *more, int count) {
+  const Range all[5] = {{a.starts, 4ull * a.count + 4u, "starts"},
+                        {a.lens, 4ull * a.count, "lens"},
+                        {a.table, 4ull * a.count * a.width, "the table"},
+                        {caches ? a.k_cache : nullptr, cache_bytes(a), "the keys' cache"},
+                        {caches ? a.v_cache : nullptr, cache_bytes(a), "the values' cache"}};
+  for (const Range &r : all)
+    REQUIRE(!r.p || !overlap(out.p, out.n, r.p, r.n), BQ_EINVAL, "%s: %s overlaps %s", name, out.what, r.what);
+  for (int i = 0; i < count; ++i)
+    REQUIRE(!more[i].p || !overlap(out.p, out.n, more[i].p, more[i].n), BQ_EINVAL, "%s: %s overlaps %s", name, out.what,
+            more[i].what);
+  return BQ_OK;
+}
+
+bqmm::PagedArgs paged_args(void *k_cache, void *v_cache, const int32_t *starts, const int32_t *lens, const int32_t *table,
+                           uint32_t tokens, uint32_t count, uint32_t pages, uint32_t page, uint32_t width, uint32_t bits,
+                           uint32_t hq, uint32_t hk, uint32_t d) {
+  bqmm::PagedArgs a{};
+  a.k_cache = static_cast<uint8_t *>(k_cache);
+  a.v_cache = static_cast<uint8_t *>(v_cache);
+  a.starts = starts;
+  a.lens = lens;
+  a.table = table;
+  a.tokens = tokens;
+  a.count = count;
+  a.pages = pages;
+  a.page_shift = page_ok(page) ? (uint32_t)__builtin_ctz(page) : 4u;
+  a.width = width;
+  a.bits = bits;
+  a.hq = hq;
+  a.hk = hk;
+  a.d = d;
+  return a;
+}
+
+// Both forms of the attention.
+int check_attention(const char *name, bqmm::PagedArgs &a, uint32_t page, bool *nothing) {
+  int st = check_paged(name, a, page, nothing);
+  if (st != BQ_OK) return st;
+  REQUIRE(a.hq >= 1u && a.hq % a.hk == 0u, BQ_EINVAL, "%s: hk=%u must divide hq=%u", name, a.hk, a.hq);
+  REQUIRE(a.scale >= 0.0f && a.scale <= 1e30f, BQ_EINVAL, "%s: scale=%g must be a number >= 0", name, (double)a.scale);
+  REQUIRE(a.cap == 0.0f || (a.cap >= 1e-20f && a.cap <= 1e20f), BQ_EINVAL, "%s: cap=%g must be 0 or 1e-20 to 1e20", name, (double)a.cap);
+  REQUIRE(a.window <= kMaxPlaces, BQ_EINVAL, "%s: window=%u too large", name, a.window);
+  // rows of a key head, and workgroups of up to 256 threads, two slots of the workspace a tile
+  REQUIRE((uint64_t)a.tokens * (a.hq / a.hk) < (1ull << 30) &&
+              (uint64_t)a.hk * std::min<uint64_t>((uint64_t)a.tokens * (a.hq / a.hk), (uint64_t)a.tokens * (a.hq / a.hk) / 16u + a.count) < (1ull << 22) &&
+              (uint64_t)a.tokens * a.hq < (1ull << 24),
+          BQ_EINVAL, "%s: tokens=%u count=%u hq=%u too large", name, a.tokens, a.count, a.hq);
+  if (*nothing) return BQ_OK;
+  REQUIRE(a.q && a.out, BQ_EINVAL, "%s: null pointer", name);
+  st = check_heads(name, "q", a.q, a.tokens, a.hq, &a.q_token, &a.q_head);
+  if (st != BQ_OK) return st;
+  REQUIRE(aligned16(a.out), BQ_EALIGN, "%s: the output must be 16-byte aligned", name);
+  const Range q = {a.q, heads_span(a.tokens, a.hq, a.d, a.q_token, a.q_head), "q"};
+  return check_apart(name, a, {a.out, bf16_bytes((uint64_t)a.tokens * a.hq, a.d), "the output"}, true, &q, 1);
+}
+
+}  // namespace
+
+extern "C" {
+
+uint64_t kv_cache_page_bytes(uint32_t page, uint32_t hk, uint32_t d, uint32_t bits) {
+  if (!page_ok(page) || hk == 0 || hk > 65535u || d < 16u || d > 256u || d % 16u != 0 || (bits != 16u && bits != 8u)) return 0;
+  return block_bytes(page, d, bits) * hk;
+}
+
+int rope_write_kv_cache(const void *q_bf16, const void *k_bf16, const void *v_bf16, void *q_out_bf16, void *k_cache,
+                        void *v_cache, const int32_t *starts, const int32_t *lens, const int32_t *table,
+                        const float *cos_sin, const int32_t *positions, const uint8_t *axis, const void *q_norm_bf16,
+                        const void *k_norm_bf16, uint32_t tokens, uint32_t count, uint32_t pages, uint32_t page,
+                        uint32_t width, uint32_t bits, uint32_t hq, uint32_t hk, uint32_t d, uint32_t rot,
+                        uint32_t angles, uint32_t axes, uint64_t q_token, uint64_t q_head, uint64_t k_token,
+                        uint64_t k_head, uint64_t v_token, uint64_t v_head, float eps, void *stream) {
+  const char *name = "rope_write_kv_cache";
+  bqmm::PagedArgs a = paged_args(k_cache, v_cache, starts, lens, table, tokens, count, pages, page, width, bits, hq, hk, d);
+  bool nothing = false;
+  int st = check_paged(name, a, page, &nothing);
+  if (st != BQ_OK) return st;
+  REQUIRE(rot % 16u == 0 && rot <= d, BQ_EUNSUPPORTED, "%s: rot=%u must be a multiple of 16 up to d=%u", name, rot, d);
+  REQUIRE(eps >= 0.0f && eps <= 1e30f, BQ_EINVAL, "%s: eps=%g must be a number >= 0", name, (double)eps);
+  REQUIRE(axes <= 255u && (!axis || axes >= 1u), BQ_EINVAL, "%s: axes=%u must be 1 to 255", name, axes);
+  REQUIRE(!axis || positions, BQ_EINVAL, "%s: axes without positions", name);
+  REQUIRE(angles <= kMaxPlaces, BQ_EINVAL, "%s: angles=%u too large", name, angles);
+  // (a launch has fewer than 2^32 threads: 256 for each tile of 16 tokens, times the parts of the heads)
+  REQUIRE(std::min<uint64_t>(tokens, tokens / 16ull + 2ull * count) < (1ull << 23), BQ_EINVAL, "%s: tokens=%u count=%u too large",
+          name, tokens, count);
+  if (nothing) return hip_status(hipSuccess, name);
+  REQUIRE(k_bf16 && v_bf16 && (hq == 0 || (q_bf16 && q_out_bf16)) && (rot == 0 || (cos_sin && angles >= 1u)), BQ_EINVAL,
+          "%s: null pointer", name);
+  if ((st = check_heads(name, "q", hq ? q_bf16 : nullptr, tokens, hq, &q_token, &q_head)) != BQ_OK) return st;
+  if ((st = check_heads(name, "k", k_bf16, tokens, hk, &k_token, &k_head)) != BQ_OK) return st;
+  if ((st = check_heads(name, "v", v_bf16, tokens, hk, &v_token, &v_head)) != BQ_OK) return st;
+  REQUIRE((hq == 0 || aligned16(q_out_bf16)) && aligned16(q_norm_bf16) && aligned16(k_norm_bf16), BQ_EALIGN,
+          "%s: the output and the norms' weights must be 16-byte aligned", name);
+  REQUIRE(aligned_to(cos_sin, 4) && aligned_to(positions, 4), BQ_EALIGN, "%s: binary32 and int32 arrays must be 4-byte aligned",
+          name);
+  const Range in[9] = {{hq ? q_bf16 : nullptr, heads_span(tokens, hq ? hq : 1u, d, q_token, q_head), "q"},
+                       {k_bf16, heads_span(tokens, hk, d, k_token, k_head), "k"},
+                       {v_bf16, heads_span(tokens, hk, d, v_token, v_head), "v"},
+                       {rot ? cos_sin : nullptr, 4ull * angles * rot, "cos_sin"},
+                       {rot ? positions : nullptr, 4ull * tokens * (axis ? axes : 1u), "the positions"},
+                       {rot ? axis : nullptr, rot / 2u, "the axes"},
+                       {q_norm_bf16, bf16_bytes(1, d), "q_norm"},
+                       {k_norm_bf16, bf16_bytes(1, d), "k_norm"},
+                       {hq ? q_out_bf16 : nullptr, bf16_bytes((uint64_t)tokens * hq, d), "the output"}};
+  if (hq && (st = check_apart(name, a, in[8], true, in, 8)) != BQ_OK) return st;
+  if ((st = check_apart(name, a, {k_cache, cache_bytes(a), "the keys' cache"}, false, in, 8)) != BQ_OK) return st;
+  if ((st = check_apart(name, a, {v_cache, cache_bytes(a), "the values' cache"}, false, in, 8)) != BQ_OK) return st;
+  REQUIRE(!overlap(k_cache, cache_bytes(a), v_cache, cache_bytes(a)), BQ_EINVAL, "%s: the caches overlap", name);
+  a.q = static_cast<const uint16_t *>(q_bf16);
+  a.k = static_cast<const uint16_t *>(k_bf16);
+  a.v = static_cast<const uint16_t *>(v_bf16);
+  a.out = static_cast<uint16_t *>(q_out_bf16);
+  a.cos_sin = cos_sin;
+  a.positions = positions;
+  a.axis = axis;
+  a.q_norm = static_cast<const uint16_t *>(q_norm_bf16);
+  a.k_norm = static_cast<const uint16_t *>(k_norm_bf16);
+  a.rot = rot;
+  a.angles = angles;
+  a.axes = axes;
+  a.q_token = q_token;
+  a.q_head = q_head;
+  a.k_token = k_token;
+  a.k_head = k_head;
+  a.v_token = v_token;
+  a.v_head = v_head;
+  a.eps = eps;
+  return hip_status(bqmm::launch_paged_write(a, as_stream(stream)), name);
+}
+
+int read_kv_cache(const void *k_cache, const void *v_cache, void *k_bf16, void *v_bf16, const int32_t *starts,
+                  const int32_t *lens, const int32_t *table, uint32_t tokens, uint32_t count, uint32_t pages,
+                  uint32_t page, uint32_t width, uint32_t bits, uint32_t hk, uint32_t d, void *stream) {
+  const char *name = "read_kv_cache";
+  bqmm::PagedArgs a = paged_args(const_cast<void *>(k_cache), const_cast<void *>(v_cache), starts, lens, table, tokens, count,
+                                 pages, page, width, bits, 0, hk, d);
+  bool nothing = false;
+  int st = check_paged(name, a, page, &nothing);
+  if (st != BQ_OK) return st;
+  REQUIRE(std::min<uint64_t>(tokens, tokens / 16ull + 2ull * count) < (1ull << 23), BQ_EINVAL, "%s: tokens=%u count=%u too large",
+          name, tokens, count);
+  if (nothing) return hip_status(hipSuccess, name);
+  REQUIRE(k_bf16 && v_bf16, BQ_EINVAL, "%s: null pointer", name);
+  REQUIRE(aligned16(k_bf16) && aligned16(v_bf16), BQ_EALIGN, "%s: the outputs must be 16-byte aligned", name);
+  const Range k = {k_bf16, bf16_bytes((uint64_t)tokens * hk, d), "k"}, v = {v_bf16, k.n, "v"};
+  if ((st = check_apart(name, a, k, true, &v, 1)) != BQ_OK) return st;
+  if ((st = check_apart(name, a, v, true, &k, 1)) != BQ_OK) return st;
+  a.k_out = static_cast<uint16_t *>(k_bf16);
+  a.v_out = static_cast<uint16_t *>(v_bf16);
+  return hip_status(bqmm::launch_paged_read(a, as_stream(stream)), name);
+}
+
+uint64_t paged_attention_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hq, uint32_t hk, uint32_t d) {
+  if (hk == 0 || hk > 65535u || hq == 0 || hq > 65535u || hq % hk != 0 || d < 16u || d > 256u || d % 16u != 0 ||
+      tokens > kMaxPlaces || count > kMaxPlaces || (uint64_t)tokens * hq >= (1ull << 24))
+    return 0;
+  return bqmm::paged_workspace_bytes(tokens, count, hq, hk, d);
+}
+
+int paged_attention_decode(const void *q_bf16, const void *k_cache, const void *v_cache, void *out_bf16,
+                           const int32_t *starts, const int32_t *lens, const int32_t *table, void *workspace,
+                           uint64_t workspace_bytes, uint32_t tokens, uint32_t count, uint32_t pages, uint32_t page,
+                           uint32_t width, uint32_t bits, uint32_t hq, uint32_t hk, uint32_t d, uint64_t q_token,
+                           uint64_t q_head, uint32_t window, float scale, float cap, void *stream) {
+  const char *name = "paged_attention_decode";
+  bqmm::PagedArgs a = paged_args(const_cast<void *>(k_cache), const_cast<void *>(v_cache), starts, lens, table, tokens, count,
+                                 pages, page, width, bits, hq, hk, d);
+  a.q = static_cast<const uint16_t *>(q_bf16);
+  a.out = static_cast<uint16_t *>(out_bf16);
+  a.q_token = q_token;
+  a.q_head = q_head;
+  a.window = window;
+  a.scale = scale;
+  a.cap = cap;
+  a.workspace = static_cast<uint8_t *>(workspace);
+  bool nothing = false;
+  int st = check_attention(name, a, page, &nothing);
+  if (st != BQ_OK) return st;
+  if (nothing) return hip_status(hipSuccess, name);
+  const uint64_t need = bqmm::paged_workspace_needed(tokens, count, hq, hk, d);
+  REQUIRE(workspace, BQ_EINVAL, "%s: null workspace", name);
+  REQUIRE(workspace_bytes >= need, BQ_EINVAL, "%s: the workspace holds %llu bytes, %llu are needed", name,
+          (unsigned long long)workspace_bytes, (unsigned long long)need);
+  REQUIRE(aligned16(workspace), BQ_EALIGN, "%s: the workspace must be 16-byte aligned", name);
+  const Range other[2] = {{q_bf16, heads_span(tokens, hq, d, a.q_token, a.q_head), "q"},
+                          {out_bf16, bf16_bytes((uint64_t)tokens * hq, d), "the output"}};
+  if ((st = check_apart(name, a, {workspace, need, "the workspace"}, true, other, 2)) != BQ_OK) return st;
+  return hip_status(bqmm::launch_paged_decode(a, as_stream(stream)), name);
+}
+
+int paged_attention_prefill(const void *q_bf16, const void *k_cache, const void *v_cache, void *out_bf16,
+                            const int32_t *starts, const int32_t *lens, const int32_t *table, uint32_t tokens,
+                            uint32_t count, uint32_t pages, uint32_t page, uint32_t width, uint32_t bits, uint32_t hq,
+                            uint32_t hk, uint32_t d, uint64_t q_token, uint64_t q_head, uint32_t window, float scale,
+                            float cap, void *stream) {
+  const char *name = "paged_attention_prefill";
+  bqmm::PagedArgs a = paged_args(const_cast<void *>(k_cache), const_cast<void *>(v_cache), starts, lens, table, tokens, count,
+                                 pages, page, width, bits, hq, hk, d);
+  a.q = static_cast<const uint16_t *>(q_bf16);
+  a.out = static_cast<uint16_t *>(out_bf16);
+  a.q_token = q_token;
+  a.q_head = q_head;
+  a.window = window;
+  a.scale = scale;
+  a.cap = cap;
+  bool nothing = false;
+  const int st = check_attention(name, a, page, &nothing);
+  if (st != BQ_OK) return st;
+  return hip_status(nothing ? hipSuccess : bqmm::launch_paged_prefill(a, as_stream(stream)), name);
 }
 
 }  // extern "C"

@@ -1,0 +1,122 @@
+// What the kernels of the paged key-value cache share: where a token's values
+// lie, and which sequence and tile a workgroup takes.
+#pragma once
+
+#include "bqmm_internal.h"
+
+namespace bqmm {
+
+// Positions and lengths stay below this, so that their sums stay below 2^31.
+constexpr int32_t kMaxPlaces = 1 << 30;
+
+// A block holds a page's values of one key head: page * d values in units of 16
+// bytes, and behind int8 codes a binary32 scale per token.  In bytes:
+__host__ __device__ inline uint32_t paged_block_bytes(uint32_t page, uint32_t d, uint32_t bits) {
+  return bits == 16u ? page * d * 2u : page * (d + 4u);
+}
+
+// Sequence i's part of a call.
+struct PagedSpan {
+  uint32_t first;  // its first new token's row
+  uint32_t n;      // its new tokens
+  int32_t at;      // the place of its first new token in the sequence (below 0: before its beginning)
+  int32_t keys;    // the tokens that the cache holds of it
+};
+
+// Whatever starts and lens hold, rows stay inside [0, tokens) and places inside
+// the table.
+__device__ __forceinline__ PagedSpan paged_span(const PagedArgs &a, uint32_t i) {
+  const int64_t s0 = a.starts[i], s1 = a.starts[i + 1u], len = a.lens[i];
+  const int64_t lo = min(max(s0, (int64_t)0), (int64_t)a.tokens), hi = min(max(s1, (int64_t)0), (int64_t)a.tokens);
+  const int64_t at = len - s1 + lo, room = (int64_t)a.width << a.page_shift;
+  PagedSpan p;
+  p.first = (uint32_t)lo;
+  p.n = hi > lo ? (uint32_t)(hi - lo) : 0u;
+  p.at = (int32_t)min(max(at, (int64_t)-kMaxPlaces), (int64_t)kMaxPlaces);
+  p.keys = (int32_t)min(max(len, (int64_t)0), room);
+  return p;
+}
+
+// The sum over a wave's lanes up to and with this one's.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  const uint32_t lane = __lane_id();
+#pragma unroll
+  for (uint32_t d = 1; d < 64u; d *= 2u) {
+    const uint32_t u = __shfl_up(v, d, 64);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+
+// The sequence that item `item` belongs to, where sequence i has items(i) of
+// them, one sequence's after the other's, and the item's number there.  False
+// past the last.  Taken by whole waves: 64 sequences at a time.
+template <class Items>
+__device__ __forceinline__ bool paged_find(uint32_t item, uint32_t count, Items items, uint32_t *seq, uint32_t *inside) {
+  const uint32_t lane = __lane_id();
+  for (uint32_t base = 0; base < count; base += 64u) {
+    const uint32_t mine = base + lane < count ? items(base + lane) : 0u;
+    const uint32_t upto = count == 1u ? mine : wave_scan(mine);
+    const uint64_t past = __ballot(upto > item);
+    if (past) {
+      const uint32_t who = (uint32_t)__builtin_ctzll(past);
+      *seq = __builtin_amdgcn_readfirstlane(base + who);
+      const uint32_t before = (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), (int)who);
+      *inside = __builtin_amdgcn_readfirstlane(item - before);
+      return true;
+    }
+    item -= (uint32_t)__builtin_amdgcn_readlane((int)upto, count == 1u ? 0 : 63);
+  }
+  return false;
+}
+
+// ---- attention ------------------------------------------------------------------
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+// The running maximum of the scores (base 2) may lag by this, so that sums are
+// rescaled rarely: weights are at most 2^8, which costs no bits.
+constexpr float kSlack = 8.0f;
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// c tanh(x / c) = c (1 - 2 / (1 + exp(2 x / c)))
+__device__ __forceinline__ float capped(float x, float cap, float inv2) {
+  return cap - 2.0f * cap * __builtin_amdgcn_rcpf(1.0f + exp2_hw(x * inv2));
+}
+
+__device__ __forceinline__ v8bf as_bf(const v4u &u) { return __builtin_bit_cast(v8bf, u); }
+
+__device__ __forceinline__ uint32_t two_bf16(float lo, float hi) {
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  v2bf v;
+  v[0] = (__bf16)lo;
+  v[1] = (__bf16)hi;
+  return __builtin_bit_cast(uint32_t, v);
+}
+// Eight codes as bf16 (exact).
+__device__ __forceinline__ v4u bf16_of_codes(uint32_t a, uint32_t b) {
+  v4u r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w = i ? b : a;
+    const float x0 = (float)(int8_t)w, x1 = (float)(int8_t)(w >> 8), x2 = (float)(int8_t)(w >> 16), x3 = (float)(int8_t)(w >> 24);
+    r[2 * i] = __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302u);
+    r[2 * i + 1] = __builtin_amdgcn_perm(__float_as_uint(x3), __float_as_uint(x2), 0x07060302u);
+  }
+  return r;
+}
+
+__device__ __forceinline__ bool any_not_finite(const v4u &u) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bad |= (u[i] & 0x7F800000u) == 0x7F800000u || (u[i] & 0x7F80u) == 0x7F80u;
+  return bad;
+}
+
+}  // namespace bqmm

@@ -1,0 +1,555 @@
+// Attention of a few new tokens of each sequence over the paged key-value cache:
+//   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(s_j - max s),  s_j = scale q . k_j, capped,
+// in one pass over the cache with the running maximum and sum of the softmax.
+//
+// Bound by the cache's bytes.  The rows of one product are the new tokens' heads
+// that share a key head, 16 to a column block of the matrix instruction, so that
+// keys and values are read once for all of them.  Both come from memory straight
+// into the operands: S^T = K Q^T takes 16 keys by 32 values, which are units of
+// the cache as they lie there, and gives a lane four keys of one row; two or four
+// exchanges between the lanes of a wave turn these into the keys of a unit of v,
+// which O^T = V^T P^T takes as it lies.  No operand passes through LDS.
+//
+// Work: sequences are cut into runs of 64-key blocks, so that a launch of a
+// fixed size shares all keys of the call evenly, whatever the lengths are; the
+// runs' results are joined by a second launch.
+#include <algorithm>
+
+#include "paged_common.h"
+
+namespace bqmm {
+namespace {
+
+constexpr uint32_t kWaves = 4;
+constexpr uint32_t kBlock = 64;      // keys: the unit of the division of work
+constexpr uint32_t kLeast = 4;       // blocks of a run
+constexpr uint32_t kTarget = 1024;   // workgroups
+
+// ---- division of the work ------------------------------------------------------
+
+// Of sequence i: its blocks of rows, and the blocks of keys that any row sees.
+struct Job {
+  uint32_t rows, tiles, blocks;
+  int32_t first;  // the first of the blocks
+};
+__device__ __forceinline__ Job job_of(const PagedArgs &a, const PagedSpan &p, uint32_t tile_rows) {
+  Job j;
+  j.rows = p.n * (a.hq / a.hk);
+  j.tiles = (j.rows + tile_rows - 1u) / tile_rows;
+  const int32_t end = min(p.keys, max(p.at + (int32_t)p.n, 0));
+  const int32_t begin = a.window ? max((int32_t)min((int64_t)p.at + 1 - (int64_t)a.window, (int64_t)end), 0) : 0;
+  j.first = begin / (int32_t)kBlock;
+  j.blocks = j.tiles && end > begin ? (uint32_t)((end + (int32_t)kBlock - 1) / (int32_t)kBlock - j.first) : 0u;
+  return j;
+}
+
+// The blocks of a run: the least with which all runs fit into `slots`.  Each
+// tile adds at most one run to the quotient of all blocks.
+__device__ __forceinline__ uint32_t run_blocks(const PagedArgs &a, uint32_t tile_rows, uint32_t slots) {
+  uint64_t blocks = 0;
+  uint32_t tiles = 0;
+  for (uint32_t base = 0; base < a.count; base += 64u) {
+    const uint32_t i = base + __lane_id();
+    if (i < a.count) {
+      const Job j = job_of(a, paged_span(a, i), tile_rows);
+      blocks += (uint64_t)j.tiles * j.blocks;
+      tiles += j.tiles;
+    }
+  }
+#pragma unroll
+  for (uint32_t d = 1; d < 64u; d *= 2u) {
+    blocks += ((uint64_t)(uint32_t)__shfl_xor((int)(blocks >> 32), (int)d, 64) << 32) + (uint32_t)__shfl_xor((int)(uint32_t)blocks, (int)d, 64);
+    tiles += (uint32_t)__shfl_xor((int)tiles, (int)d, 64);
+  }
+  const uint32_t spare = slots > tiles ? slots - tiles : 1u;
+  return max(kLeast, (uint32_t)((blocks + spare - 1u) / spare));
+}
+
+__device__ __forceinline__ uint32_t runs_of(const Job &j, uint32_t per) { return max(1u, (j.blocks + per - 1u) / per); }
+
+struct Parts {
+  float *sums;    // [slots][hk][tile_rows][d]
+  float2 *stats;  // [slots][hk][tile_rows]: maximum (base 2) and sum
+};
+__host__ __device__ inline Parts parts_of(uint8_t *workspace, uint32_t slots, uint32_t hk, uint32_t tile_rows, uint32_t d) {
+  const uint64_t rows = (uint64_t)slots * hk * tile_rows;
+  return {reinterpret_cast<float *>(workspace), reinterpret_cast<float2 *>(workspace + rows * d * 4u)};
+}
+
+// ---- a run ------------------------------------------------------------------------
+
+// kDP: values of a head, rounded up; kNT: column blocks of 16 rows.
+template <uint32_t kDP, uint32_t kBits, uint32_t kNT>
+__global__ __launch_bounds__(64 * kWaves, 1) void paged_decode_kernel(PagedArgs a, uint32_t slots, float *sums, float2 *stats) {
+  constexpr uint32_t kUnit = 128u / kBits;        // values of a unit
+  constexpr uint32_t kKeys = kUnit * 4u;          // keys of a step: a unit of v for each group of 16 lanes
+  constexpr uint32_t kKT = kKeys / 16u;           // their tiles
+  constexpr uint32_t kKS = kDP / (kUnit * 4u);    // steps of a product over a head's values, in units
+  constexpr uint32_t kHalves = kBits == 16u ? 1u : 2u;  // operands of a unit
+  constexpr uint32_t kDB = kDP / 16u;             // blocks of a head's values
+  constexpr uint32_t kRows = 16u * kNT;
+  constexpr uint32_t kPitch = kDP + 4u;           // of a row of sums in LDS
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+
+  const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t r = lane & 15u, c = lane >> 4;
+  const uint32_t slot = blockIdx.x / a.hk, head = blockIdx.x % a.hk, g = a.hq / a.hk;
+  const uint32_t per = run_blocks(a, kRows, slots);
+  uint32_t seq, inside;
+  if (!paged_find(slot, a.count, [&](uint32_t i) {
+        const Job j = job_of(a, paged_span(a, i), kRows);
+        return j.tiles ? j.tiles * runs_of(j, per) : 0u;
+      }, &seq, &inside))
+    return;
+  const PagedSpan p = paged_span(a, seq);
+  const Job job = job_of(a, p, kRows);
+  const uint32_t runs = runs_of(job, per), tile = inside / runs, run = inside % runs;
+  const int32_t key_begin = (job.first + (int32_t)(run * per)) * (int32_t)kBlock;
+  const int32_t key_end = min((job.first + (int32_t)min((run + 1u) * per, job.blocks)) * (int32_t)kBlock, p.keys);
+
+  // this lane's rows: places, and the operand of q
+  const uint32_t page = 1u << a.page_shift, block = paged_block_bytes(page, a.d, kBits), units = a.d / kUnit;
+  int32_t pos[kNT], low[kNT];
+  v4u q[kNT][kKS * kHalves];
+#pragma unroll
+  for (uint32_t t = 0; t < kNT; ++t) {
+    const uint32_t row = tile * kRows + t * 16u + r, token = row / g, hh = row % g;
+    const bool live = row < job.rows;
+    pos[t] = live ? p.at + (int32_t)token : -1;
+    low[t] = a.window && live ? (int32_t)max((int64_t)pos[t] + 1 - (int64_t)a.window, (int64_t)0) : 0;
+    const uint16_t *from = a.q + (uint64_t)(p.first + (live ? token : 0u)) * a.q_token + (uint64_t)(head * g + hh) * a.q_head;
+#pragma unroll
+    for (uint32_t s = 0; s < kKS; ++s)
+#pragma unroll
+      for (uint32_t h = 0; h < kHalves; ++h) {
+        v4u v = {0, 0, 0, 0};
+        const uint32_t unit = 4u * s + c;
+        if (live && unit < units) v = *reinterpret_cast<const v4u *>(from + unit * kUnit + h * 8u);
+        q[t][s * kHalves + h] = v;
+      }
+  }
+  // where all of the tile's rows see a key: [all_low, all_pos]
+  int32_t all_pos, all_low;
+  {
+    const uint32_t row0 = tile * kRows, row1 = min(row0 + kRows, job.rows) - 1u;
+    all_pos = p.at + (int32_t)(row0 / g);
+    all_low = a.window ? (int32_t)max((int64_t)p.at + (int64_t)(row1 / g) + 1 - (int64_t)a.window, (int64_t)0) : 0;
+  }
+
+  const float scale2 = a.scale * kLog2e, cap2 = a.cap * kLog2e, inv2 = a.cap != 0.0f ? 2.0f * kLog2e / a.cap : 0.0f;
+  float m[kNT], l[kNT];
+  v4f o[kNT][kDB];
+#pragma unroll
+  for (uint32_t t = 0; t < kNT; ++t) {
+    m[t] = -INFINITY;
+    l[t] = 0.0f;
+#pragma unroll
+    for (uint32_t b = 0; b < kDB; ++b) o[t][b] = v4f{0, 0, 0, 0};
+  }
+
+  const int32_t *table = a.table + (uint64_t)seq * a.width;
+  const uint8_t *kc = a.k_cache + (uint64_t)head * block, *vc = a.v_cache + (uint64_t)head * block;
+  const uint64_t page_bytes = (uint64_t)block * a.hk;
+
+  for (int32_t key0 = key_begin + (int32_t)(wave * kKeys); key0 < key_end; key0 += (int32_t)(kWaves * kKeys)) {
+    // the pages of the step's tiles of 16 keys
+    uint32_t ids[kKT];
+    bool holes = false;
+#pragma unroll
+    for (uint32_t t = 0; t < kKT; ++t) {
+      const uint32_t at = (uint32_t)(key0 + (int32_t)(16u * t)) >> a.page_shift;
+      const uint32_t id = at < a.width ? (uint32_t)table[at] : ~0u;
+      ids[t] = __builtin_amdgcn_readfirstlane(id);
+      holes |= ids[t] >= a.pages;
+    }
+    // keys, scores
+    v4f x[kNT][kKT];
+#pragma unroll
+    for (uint32_t t = 0; t < kKT; ++t) {
+      const uint32_t id = ids[t] < a.pages ? ids[t] : 0u, off = (uint32_t)(key0 + (int32_t)(16u * t)) & (page - 1u);
+      const uint8_t *base = kc + id * page_bytes;
+#pragma unroll
+      for (uint32_t n = 0; n < kNT; ++n) x[n][t] = v4f{0, 0, 0, 0};
+#pragma unroll
+      for (uint32_t s = 0; s < kKS; ++s) {
+        const uint32_t unit = 4u * s + c;
+        v4u k = {0, 0, 0, 0};
+        if (unit < units) k = *reinterpret_cast<const v4u *>(base + (unit * page + off + r) * 16u);
+#pragma unroll
+        for (uint32_t h = 0; h < kHalves; ++h) {
+          const v4u kk = kBits == 16u ? k : bf16_of_codes(k[2 * h], k[2 * h + 1]);
+#pragma unroll
+          for (uint32_t n = 0; n < kNT; ++n)
+            x[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(kk), as_bf(q[n][s * kHalves + h]), x[n][t], 0, 0, 0);
+        }
+      }
+    }
+    // values: unit of keys 8 c.. or 16 c.. of the step
+    v4u v[kDB];
+    {
+      const uint32_t t = c * kUnit / 16u;
+      uint32_t id = ids[0];
+#pragma unroll
+      for (uint32_t i = 1; i < kKT; ++i) id = t == i ? ids[i] : id;
+      id = id < a.pages ? id : 0u;
+      const uint32_t off = (uint32_t)(key0 + (int32_t)(c * kUnit)) & (page - 1u);
+      const uint8_t *base = vc + id * page_bytes + ((uint64_t)(off / kUnit) * a.d + r) * 16u;
+#pragma unroll
+      for (uint32_t b = 0; b < kDB; ++b) {
+        v[b] = v4u{0, 0, 0, 0};
+        if (16u * b < a.d) v[b] = *reinterpret_cast<const v4u *>(base + b * 256u);
+      }
+    }
+    v4f ks[kKT], vs[kKT];
+    if constexpr (kBits == 8u) {
+#pragma unroll
+      for (uint32_t t = 0; t < kKT; ++t) {
+        const uint32_t id = ids[t] < a.pages ? ids[t] : 0u, off = (uint32_t)(key0 + (int32_t)(16u * t)) & (page - 1u);
+        const uint64_t at = id * page_bytes + page * a.d + (off + 4u * c) * 4u;
+        ks[t] = *reinterpret_cast<const v4f *>(kc + at);
+        vs[t] = *reinterpret_cast<const v4f *>(vc + at);
+      }
+    }
+    const bool whole = !holes && key0 + (int32_t)kKeys - 1 <= all_pos && key0 >= all_low && key0 + (int32_t)kKeys <= key_end;
+#pragma unroll
+    for (uint32_t n = 0; n < kNT; ++n) {
+#pragma unroll
+      for (uint32_t t = 0; t < kKT; ++t) {
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) {
+          float y = x[n][t][e];
+          if constexpr (kBits == 8u) y *= ks[t][e];
+          x[n][t][e] = a.cap != 0.0f ? capped(y * a.scale, cap2, inv2) : y * scale2;
+        }
+      }
+      if (!whole) {
+#pragma unroll
+        for (uint32_t t = 0; t < kKT; ++t)
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) {
+            const int32_t key = key0 + (int32_t)(16u * t + 4u * c + e);
+            const bool seen = key <= pos[n] && key >= low[n] && key < key_end && ids[t] < a.pages;
+            x[n][t][e] = seen ? x[n][t][e] : -INFINITY;
+          }
+      }
+      float top = x[n][0][0];
+#pragma unroll
+      for (uint32_t t = 0; t < kKT; ++t)
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) top = fmaxf(top, x[n][t][e]);
+      if (__ballot(top > m[n] + kSlack)) {
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const float next = fmaxf(m[n], top);
+        const float keep = m[n] == -INFINITY ? 0.0f : exp2_hw(m[n] - next);
+        m[n] = next;
+        l[n] *= keep;
+#pragma unroll
+        for (uint32_t b = 0; b < kDB; ++b) o[n][b] *= keep;
+      }
+      const float base = m[n] == -INFINITY ? 0.0f : m[n];
+      // weights, as the sum of two bf16: one would be off by 2^-9 of each weight
+      uint32_t hi[kKT][2], lo[kKT][2];
+#pragma unroll
+      for (uint32_t t = 0; t < kKT; ++t) {
+        float w[4];
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) {
+          const float s = x[n][t][e];
+          w[e] = exp2_hw(s - base);
+          l[n] += w[e];
+          if constexpr (kBits == 8u) w[e] = s == -INFINITY ? 0.0f : w[e] * vs[t][e];
+        }
+#pragma unroll
+        for (uint32_t e = 0; e < 2; ++e) {
+          hi[t][e] = two_bf16(w[2 * e], w[2 * e + 1]);
+          lo[t][e] = two_bf16(w[2 * e] - __uint_as_float(hi[t][e] << 16), w[2 * e + 1] - __uint_as_float(hi[t][e] & 0xFFFF0000u));
+        }
+      }
+      // to the lanes that hold the keys' values: lanes of group c have keys 4 c.. of
+      // every tile, and want the keys of their unit
+      v4u ph[kHalves], pl[kHalves];
+      auto turn = [&](uint32_t (&w)[kKT][2], v4u *out) {
+#pragma unroll
+        for (uint32_t e = 0; e < 2; ++e) {
+          if constexpr (kBits == 16u) {
+            const v2u s = __builtin_amdgcn_permlane32_swap(w[0][e], w[1][e], false, false);
+            const v2u f = __builtin_amdgcn_permlane16_swap(s.x, s.y, false, false);
+            out[0][e] = f.x;
+            out[0][2 + e] = f.y;
+          } else {
+            const v2u s0 = __builtin_amdgcn_permlane32_swap(w[0][e], w[2][e], false, false);
+            const v2u s1 = __builtin_amdgcn_permlane32_swap(w[1][e], w[3][e], false, false);
+            const v2u f0 = __builtin_amdgcn_permlane16_swap(s0.x, s1.x, false, false);
+            const v2u f1 = __builtin_amdgcn_permlane16_swap(s0.y, s1.y, false, false);
+            out[0][e] = f0.x;
+            out[0][2 + e] = f0.y;
+            out[kHalves - 1][e] = f1.x;
+            out[kHalves - 1][2 + e] = f1.y;
+          }
+        }
+      };
+      turn(hi, ph);
+      turn(lo, pl);
+      bool bad = false;
+      if constexpr (kBits == 16u) {
+        if (!whole) {
+#pragma unroll
+          for (uint32_t b = 0; b < kDB; ++b) bad |= any_not_finite(v[b]);
+          bad = __ballot(bad) != 0u;
+        }
+      }
+      if (!bad) {
+#pragma unroll
+        for (uint32_t b = 0; b < kDB; ++b) {
+          if (16u * b >= a.d) continue;
+#pragma unroll
+          for (uint32_t h = 0; h < kHalves; ++h) {
+            const v8bf vv = as_bf(kBits == 16u ? v[b] : bf16_of_codes(v[b][2 * h], v[b][2 * h + 1]));
+            o[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, as_bf(ph[h]), o[n][b], 0, 0, 0);
+            o[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, as_bf(pl[h]), o[n][b], 0, 0, 0);
+          }
+        }
+      } else {
+        // A NaN or an infinity among the values of a step that not every row sees
+        // whole: 0 * NaN must not reach the rows that do not see its key.  One
+        // key at a time, added where it is seen.
+        for (uint32_t key = 0; key < kKeys; ++key) {
+          const uint32_t e = key % 8u;
+          const bool here = c == key / 8u;
+          const int32_t place = key0 + (int32_t)key;
+          const bool seen = place <= pos[n] && place >= low[n] && place < key_end && ids[key / 16u] < a.pages;
+          const uint32_t keep = here ? (e & 1u ? 0xFFFF0000u : 0xFFFFu) : 0u;
+          v4u sel;
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i) sel[i] = e / 2u == i ? keep : 0u;
+#pragma unroll
+          for (uint32_t b = 0; b < kDB; ++b) {
+            if (16u * b >= a.d) continue;
+            v4f one = {0, 0, 0, 0};
+            one = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(v[b] & sel), as_bf(ph[0] & sel), one, 0, 0, 0);
+            one = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(v[b] & sel), as_bf(pl[0] & sel), one, 0, 0, 0);
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) o[n][b][i] += seen ? one[i] : 0.0f;
+          }
+        }
+      }
+    }
+  }
+
+  // the waves' results, two and two
+#pragma unroll
+  for (uint32_t n = 0; n < kNT; ++n) {
+    l[n] += __shfl_xor(l[n], 16, 64);
+    l[n] += __shfl_xor(l[n], 32, 64);
+  }
+  float *const shared = reinterpret_cast<float *>(lds);
+  float2 *const shared_stats = reinterpret_cast<float2 *>(lds + (kWaves / 2u) * kRows * kPitch * 4u);
+#pragma unroll
+  for (uint32_t half = kWaves / 2u; half >= 1u; half /= 2u) {
+    __syncthreads();
+    if (wave >= half && wave < 2u * half) {
+      const uint32_t at = wave - half;
+#pragma unroll
+      for (uint32_t n = 0; n < kNT; ++n) {
+        const uint32_t row = at * kRows + n * 16u + r;
+        if (c == 0u) shared_stats[row] = make_float2(m[n], l[n]);
+#pragma unroll
+        for (uint32_t b = 0; b < kDB; ++b) *reinterpret_cast<v4f *>(shared + row * kPitch + 16u * b + 4u * c) = o[n][b];
+      }
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (uint32_t n = 0; n < kNT; ++n) {
+        const uint32_t row = wave * kRows + n * 16u + r;
+        const float2 other = shared_stats[row];
+        const float next = fmaxf(m[n], other.x);
+        const float mine = m[n] == -INFINITY ? 0.0f : exp2_hw(m[n] - next);
+        const float theirs = other.x == -INFINITY ? 0.0f : exp2_hw(other.x - next);
+        l[n] = l[n] * mine + other.y * theirs;
+        m[n] = next;
+#pragma unroll
+        for (uint32_t b = 0; b < kDB; ++b) {
+          const v4f y = *reinterpret_cast<const v4f *>(shared + row * kPitch + 16u * b + 4u * c);
+          o[n][b] = o[n][b] * mine + y * theirs;
+        }
+      }
+    }
+  }
+  if (wave != 0u) return;
+#pragma unroll
+  for (uint32_t n = 0; n < kNT; ++n) {
+    const uint32_t row = tile * kRows + n * 16u + r;
+    if (row >= job.rows) continue;
+    if (runs == 1u) {
+      const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
+      uint16_t *to = a.out + ((uint64_t)(p.first + row / g) * a.hq + head * g + row % g) * a.d;
+#pragma unroll
+      for (uint32_t b = 0; b < kDB; ++b)
+        if (16u * b < a.d)
+          *reinterpret_cast<uint2 *>(to + 16u * b + 4u * c) =
+              make_uint2(pack_bf16x2(o[n][b][0] * inv, o[n][b][1] * inv), pack_bf16x2(o[n][b][2] * inv, o[n][b][3] * inv));
+    } else {
+      const uint64_t at = ((uint64_t)slot * a.hk + head) * kRows + n * 16u + r;
+      if (c == 0u) stats[at] = make_float2(m[n], l[n]);
+#pragma unroll
+      for (uint32_t b = 0; b < kDB; ++b)
+        if (16u * b < a.d) *reinterpret_cast<v4f *>(sums + at * a.d + 16u * b + 4u * c) = o[n][b];
+    }
+  }
+}
+
+// ---- joining the runs ----------------------------------------------------------------
+
+// A workgroup takes one row: lanes hold four of its values, groups of lanes share
+// the runs.
+constexpr uint32_t kJoinThreads = 256;
+
+__global__ __launch_bounds__(kJoinThreads) void paged_join_kernel(PagedArgs a, uint32_t tile_rows, uint32_t slots,
+                                                                  const float *sums, const float2 *stats) {
+  __shared__ v4f part[kJoinThreads];
+  __shared__ float part_sum[kJoinThreads / 4], most[4];
+  const uint32_t g = a.hq / a.hk, token = blockIdx.x, h = blockIdx.y, head = h / g;
+  const uint32_t per = run_blocks(a, tile_rows, slots);
+  // the token's sequence, and the slots before its own
+  uint32_t seq = 0, before = 0;
+  bool found = false;
+  for (uint32_t base = 0; base < a.count && !found; base += 64u) {
+    const uint32_t i = base + __lane_id();
+    uint32_t items = 0;
+    bool here = false;
+    if (i < a.count) {
+      const PagedSpan p = paged_span(a, i);
+      const Job j = job_of(a, p, tile_rows);
+      items = j.tiles ? j.tiles * runs_of(j, per) : 0u;
+      here = token >= p.first && token - p.first < p.n;
+    }
+    const uint32_t upto = a.count == 1u ? items : wave_scan(items);
+    const uint64_t who = __ballot(here);
+    if (who) {
+      const uint32_t w = (uint32_t)__builtin_ctzll(who);
+      seq = base + w;
+      before += (uint32_t)__builtin_amdgcn_readlane((int)(upto - items), (int)w);
+      found = true;
+    } else {
+      before += (uint32_t)__builtin_amdgcn_readlane((int)upto, a.count == 1u ? 0 : 63);
+    }
+  }
+  if (!found) return;
+  const PagedSpan p = paged_span(a, seq);
+  const Job job = job_of(a, p, tile_rows);
+  const uint32_t runs = runs_of(job, per);
+  // one run has written its rows itself (and starts that do not ascend give no
+  // runs past the last slot)
+  if (runs == 1u || before + job.tiles * runs > slots) return;
+  const uint32_t row = (token - p.first) * g + h % g, tile = row / tile_rows;
+  const uint64_t at0 = ((uint64_t)(before + tile * runs) * a.hk + head) * tile_rows + row % tile_rows, step = (uint64_t)a.hk * tile_rows;
+
+  float top = -INFINITY;
+  for (uint32_t i = threadIdx.x; i < runs; i += kJoinThreads) top = fmaxf(top, stats[at0 + i * step].x);
+#pragma unroll
+  for (uint32_t d = 1; d < 64u; d *= 2u) top = fmaxf(top, __shfl_xor(top, (int)d, 64));
+  if ((threadIdx.x & 63u) == 0u) most[threadIdx.x >> 6] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+
+  const uint32_t lanes = a.d / 4u, groups = kJoinThreads / lanes, lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
+  v4f sum = {0, 0, 0, 0};
+  float weight = 0.0f;
+  if (group < groups) {
+#pragma unroll 4
+    for (uint32_t i = group; i < runs; i += groups) {
+      const float2 s = stats[at0 + i * step];
+      const float w = s.x == -INFINITY ? 0.0f : exp2_hw(s.x - top);
+      weight += s.y * w;
+      sum += *reinterpret_cast<const v4f *>(sums + (at0 + i * step) * a.d + 4u * lane) * w;
+    }
+    part[threadIdx.x] = sum;
+    if (lane == 0u) part_sum[group] = weight;
+  }
+  __syncthreads();
+  if (group != 0u) return;
+  weight = part_sum[0];
+  for (uint32_t i = 1; i < groups; ++i) {
+    sum += part[i * lanes + lane];
+    weight += part_sum[i];
+  }
+  const float inv = weight == 0.0f ? 0.0f : 1.0f / weight;
+  *reinterpret_cast<uint2 *>(a.out + ((uint64_t)token * a.hq + h) * a.d + 4u * lane) =
+      make_uint2(pack_bf16x2(sum[0] * inv, sum[1] * inv), pack_bf16x2(sum[2] * inv, sum[3] * inv));
+}
+
+// ---- the launch ------------------------------------------------------------------
+
+struct Plan {
+  uint32_t blocks, tiles, slots;  // column blocks of a tile; tiles at most; slots of runs
+};
+
+Plan plan_of(uint32_t tokens, uint32_t count, uint32_t hq, uint32_t hk, uint32_t d) {
+  const uint32_t g = hq / hk;
+  const uint64_t rows = (uint64_t)tokens * g, mean = (rows + count - 1u) / count;
+  Plan p;
+  p.blocks = mean <= 16u ? 1u : mean <= 32u || d > 128u ? 2u : 4u;
+  const uint32_t tile = 16u * p.blocks;
+  // (of a sequence with rows: at most one tile that is not full)
+  p.tiles = (uint32_t)std::min<uint64_t>(rows / tile + std::min(count, tokens), (uint64_t)tokens * ((g + tile - 1u) / tile));
+  p.slots = std::max(2u * p.tiles, kTarget / hk);
+  return p;
+}
+
+template <uint32_t kDP, uint32_t kBits, uint32_t kNT>
+hipError_t launch(const PagedArgs &a, const Plan &plan, bool cut, hipStream_t s) {
+  const Parts parts = parts_of(a.workspace, plan.slots, a.hk, 16u * kNT, a.d);
+  constexpr uint32_t kLds = (kWaves / 2u) * 16u * kNT * ((kDP + 4u) * 4u + 8u);
+  auto *kernel = paged_decode_kernel<kDP, kBits, kNT>;
+  if (kLds > 65536u) {
+    const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void *>(kernel), (int)kLds);
+    if (e != hipSuccess) return e;
+  }
+  const uint32_t used = cut ? plan.slots : plan.tiles;
+  hipLaunchKernelGGL(kernel, dim3(used * a.hk), dim3(64 * kWaves), kLds, s, a, plan.slots, parts.sums, parts.stats);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !cut) return e;
+  hipLaunchKernelGGL(paged_join_kernel, dim3(a.tokens, a.hq), dim3(kJoinThreads), 0, s, a, 16u * kNT, plan.slots, parts.sums,
+                     parts.stats);
+  return hipGetLastError();
+}
+
+template <uint32_t kDP, uint32_t kBits>
+hipError_t launch_rows(const PagedArgs &a, const Plan &plan, bool cut, hipStream_t s) {
+  if (plan.blocks == 1u) return launch<kDP, kBits, 1>(a, plan, cut, s);
+  if constexpr (kDP <= 128u)
+    if (plan.blocks == 4u) return launch<kDP, kBits, 4>(a, plan, cut, s);
+  return launch<kDP, kBits, 2>(a, plan, cut, s);
+}
+
+}  // namespace
+
+hipError_t launch_paged_decode(const PagedArgs &a, hipStream_t s) {
+  const Plan plan = plan_of(a.tokens, a.count, a.hq, a.hk, a.d);
+  // no sequence can be longer than a run: nothing to join
+  const bool cut = ((uint64_t)a.width << a.page_shift) > kLeast * kBlock;
+  if (a.bits == 16u)
+    return a.d <= 64u ? launch_rows<64, 16>(a, plan, cut, s) : a.d <= 128u ? launch_rows<128, 16>(a, plan, cut, s) : launch_rows<256, 16>(a, plan, cut, s);
+  return a.d <= 64u ? launch_rows<64, 8>(a, plan, cut, s) : a.d <= 128u ? launch_rows<128, 8>(a, plan, cut, s) : launch_rows<256, 8>(a, plan, cut, s);
+}
+
+// For a call of at most these sizes: two slots a tile, or the target's.  Tiles of
+// 32 and 64 rows are taken where sequences have over half as many, so that all
+// tiles have at most 3 times the rows.
+uint64_t paged_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hq, uint32_t hk, uint32_t d) {
+  if (tokens == 0u || count == 0u) return 0;
+  const uint64_t g = hq / hk, rows = tokens * g, most = d > 128u ? 32u : 64u;
+  const uint64_t narrow = std::min<uint64_t>(rows + 16ull * std::min(count, tokens), tokens * 16ull * ((g + 15u) / 16u));
+  const uint64_t all = std::max(2u * std::max(3u * rows, narrow), std::max<uint64_t>(kTarget / hk, 1u) * most);
+  return all * hk * (4ull * d + 8u);
+}
+
+uint64_t paged_workspace_needed(uint32_t tokens, uint32_t count, uint32_t hq, uint32_t hk, uint32_t d) {
+  if (tokens == 0u || count == 0u) return 0;
+  const Plan p = plan_of(tokens, count, hq, hk, d);
+  return (uint64_t)p.slots * hk * 16u * p.blocks * (4u * d + 8u);
+}
+
+}  // namespace bqmm

@@ -48,6 +48,17 @@
  *     nibble).  w = d*sc_j*q - dmin*m_j.  256 weights in 144 bytes as on page
  *     layers/ops/q4k_mmq.rs (consts QK_K, Q4K_BLOCK_BYTES).
  *
+ *   Paged key-value cache: a pool of pages of P tokens (P a power of two, 16 to
+ *     1024), keys and values each a buffer of pages * kv_cache_page_bytes(P, hk,
+ *     d, bits) bytes.  Page p, key head h is the block p*hk + h: P*d values in
+ *     units of 16 bytes (U = 8 bf16 values, or 16 int8 codes), and behind the
+ *     codes a binary32 scale for each of the P tokens (value = scale * code).
+ *     A block is 2*P*d or P*(d + 4) bytes.  Value j of the page's token o:
+ *       keys:   ((j / U)*P + o)*U + j % U    (a unit: U values of a token)
+ *       values: ((o / U)*d + j)*U + o % U    (a unit: one value of U tokens),
+ *     which is what the attention's matrix instructions take.  A page holds all
+ *     of itself: copying its bytes moves it.
+ *
  * Alignment: weight, activation and q8_1 pointers must be 16-byte aligned
  * (BQ_EALIGN otherwise); bf16 row lengths used by vector loads are noted per
  * call.  Inputs and outputs must not overlap unless a call says so; every
@@ -115,6 +126,16 @@ uint64_t int8_rows_bytes(uint32_t rows, uint32_t k);
  * would refuse the sizes. */
 uint64_t gated_delta_rule_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hk, uint32_t hv,
                                           uint32_t dk, uint32_t dv);
+
+/* Bytes of one page of a cache's keys, or values: hk blocks (layout above); bits:
+ * 16 (bf16) or 8 (int8 with a scale per token and head).  0 where the calls would
+ * refuse the sizes. */
+uint64_t kv_cache_page_bytes(uint32_t page, uint32_t hk, uint32_t d, uint32_t bits);
+
+/* Workspace of paged_attention_decode for these heads and at most `tokens` tokens
+ * in at most `count` sequences: one that is allocated for the largest call serves
+ * every smaller one.  0 where the call would refuse the sizes. */
+uint64_t paged_attention_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hq, uint32_t hk, uint32_t d);
 
 /* ---- the hot path -------------------------------------------------------- */
 
@@ -386,6 +407,88 @@ int gated_delta_rule_chunked(const void *q_bf16, const void *k_bf16, const void 
                              uint32_t dk, uint32_t dv, uint64_t q_token, uint64_t q_head, uint64_t k_token,
                              uint64_t k_head, uint64_t v_token, uint64_t v_head, float scale, int l2norm,
                              void *stream);
+
+/* ---- attention over a paged key-value cache ------------------------------------
+ *
+ * What the four calls share.  k_cache, v_cache: `pages` pages of `page` tokens,
+ * `bits` a value (layout above), for hk key heads of d values; d a multiple of 16
+ * up to 256.  Sequence i has lens[i] tokens in the cache after this call, the last
+ * starts[i + 1] - starts[i] of them new: the rows [starts[i], starts[i + 1]) of the
+ * packed arrays, at the places lens[i] - (starts[i + 1] - starts[i]) on.  Place p
+ * of sequence i lies at offset p % page of page table[i*width + p / page].
+ *
+ * starts [count + 1] ascending, lens [count], table [count][width]: int32 on the
+ * device; captured into a graph, a call reads them at each replay.  Ranges outside
+ * [0, tokens) are cut off.  A place below 0, at width * page or beyond, or in a
+ * page whose number is not in [0, pages) is nowhere: nothing is written or read
+ * there, and no key is seen.  Tokens of no sequence are left alone; so are the rest
+ * of a page, and what it holds (a NaN, too) has no effect.
+ *
+ * tokens, count <= 2^30, width * page <= 2^30, at most 2^23 tiles of 16 tokens
+ * (tokens / 16 + 2 count).  The strides of q, k and v are in values, multiples of
+ * 8 below 2^31; their base pointers, the caches and outputs 16-byte aligned.
+ * Outputs and the caches that are written overlap nothing else.  tokens = 0 and
+ * count = 0 are allowed (nothing is done, pointers may be NULL). */
+
+/* Rotary positions, head norms and the write of the cache.  Per token and head of
+ * q and k, in binary32:
+ *   t[j] = x[j]   or, with a norm's weight,   x[j] * weight[j] / sqrt(mean_j(x[j]^2) + eps),
+ * then for f < rot / 2, with c = cos_sin[a][0][f], s = cos_sin[a][1][f]:
+ *   t[f], t[f + rot/2] = t[f] c - t[f + rot/2] s, t[f + rot/2] c + t[f] s;
+ * values from rot on stay.  a: the token's place where positions is NULL; else
+ * positions[token], or with several axes positions[axis[f]][token].  A position
+ * outside [0, angles), or an axis that is not below axes, rotates to NaN.
+ *   q_out = bf16_rne(t) of q: [tokens][hq][d]; hq = 0: no q, its pointers NULL
+ *   k_cache gets t of k, v_cache gets v.  bits = 16: bf16_rne.  bits = 8: per
+ *   token and head, with top = max |t|, code = rint(127 t / top) (the quotient in
+ *   binary32) and scale = top / 127; zero codes where top is 0.  A row that holds a
+ *   NaN or an infinity gets that as its scale, and zero codes.
+ * cos_sin: binary32 [angles][2][rot / 2], rot a multiple of 16 up to d (0: no
+ * rotation, cos_sin may be NULL).  positions: int32 [tokens] or [axes][tokens];
+ * axis: uint8 [rot / 2] or NULL.  q_norm, k_norm: bf16 [d] or NULL.  |x|^2 has to
+ * stay below 2^128.  No two tokens of a call may have the same place of a page. */
+int rope_write_kv_cache(const void *q_bf16, const void *k_bf16, const void *v_bf16, void *q_out_bf16, void *k_cache,
+                        void *v_cache, const int32_t *starts, const int32_t *lens, const int32_t *table,
+                        const float *cos_sin, const int32_t *positions, const uint8_t *axis, const void *q_norm_bf16,
+                        const void *k_norm_bf16, uint32_t tokens, uint32_t count, uint32_t pages, uint32_t page,
+                        uint32_t width, uint32_t bits, uint32_t hq, uint32_t hk, uint32_t d, uint32_t rot,
+                        uint32_t angles, uint32_t axes, uint64_t q_token, uint64_t q_head, uint64_t k_token,
+                        uint64_t k_head, uint64_t v_token, uint64_t v_head, float eps, void *stream);
+
+/* The sequences' new tokens back from the cache, as bf16 rows [tokens][hk][d]
+ * (int8: bf16_rne(scale * code)); to read a whole sequence, call all of its tokens
+ * new.  A token that is nowhere gives zeros. */
+int read_kv_cache(const void *k_cache, const void *v_cache, void *k_bf16, void *v_bf16, const int32_t *starts,
+                  const int32_t *lens, const int32_t *table, uint32_t tokens, uint32_t count, uint32_t pages,
+                  uint32_t page, uint32_t width, uint32_t bits, uint32_t hk, uint32_t d, void *stream);
+
+/* Causal attention of the new tokens over the cache, which holds them already.  For
+ * a token at place p and head h, which reads key head h / (hq / hk):
+ *   s_j = scale q . k_j, or cap * tanh(scale q . k_j / cap) where cap is not 0,
+ *   out = bf16_rne(sum_j w_j v_j / sum_j w_j),  w_j = exp(s_j - max s),
+ * over the keys j <= p of its sequence, and where window is not 0 j > p - window.
+ * A token that sees no key, or only keys with a score of -infinity, gives zeros.
+ * q: bf16, head h of token t starts at t * q_token + h * q_head; out: bf16
+ * [tokens][hq][d].  hk divides hq; tokens * hq < 2^24; scale >= 0.
+ *
+ * Products of bf16 values (int8 codes are exact in bf16) are summed in binary32,
+ * and so are the softmax's maximum and sum.  _decode takes the weights w_j as sums
+ * of two bf16, _prefill rounds them to one (2^-9 of each).  Both give a call's
+ * result bit for bit again.
+ * _decode reads each key once for up to 16, 32 or 64 rows (new tokens times hq /
+ * hk) and cuts sequences over the device: for decoding and for a few tokens each.
+ * _prefill: for prompts.  workspace: paged_attention_workspace_bytes(...) bytes for
+ * these sizes or larger ones, for this call alone until it has run. */
+int paged_attention_decode(const void *q_bf16, const void *k_cache, const void *v_cache, void *out_bf16,
+                           const int32_t *starts, const int32_t *lens, const int32_t *table, void *workspace,
+                           uint64_t workspace_bytes, uint32_t tokens, uint32_t count, uint32_t pages, uint32_t page,
+                           uint32_t width, uint32_t bits, uint32_t hq, uint32_t hk, uint32_t d, uint64_t q_token,
+                           uint64_t q_head, uint32_t window, float scale, float cap, void *stream);
+int paged_attention_prefill(const void *q_bf16, const void *k_cache, const void *v_cache, void *out_bf16,
+                            const int32_t *starts, const int32_t *lens, const int32_t *table, uint32_t tokens,
+                            uint32_t count, uint32_t pages, uint32_t page, uint32_t width, uint32_t bits, uint32_t hq,
+                            uint32_t hk, uint32_t d, uint64_t q_token, uint64_t q_head, uint32_t window, float scale,
+                            float cap, void *stream);
 
 /* ---- test hook: the int8 product's form -------------------------------- */
 
