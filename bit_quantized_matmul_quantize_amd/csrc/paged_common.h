@@ -112,6 +112,27 @@ __device__ __forceinline__ v4u bf16_of_codes(uint32_t a, uint32_t b) {
   return r;
 }
 
+// Of eight bf16: the finite ones, zero for the others; and 1 for +infinities (kind
+// 0), -infinities (1) or NaNs (2), zero for the others.
+__device__ __forceinline__ v4u finite_only(v4u u) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((u[i] & 0x7F80u) == 0x7F80u) u[i] &= 0xFFFF0000u;
+    if ((u[i] & 0x7F800000u) == 0x7F800000u) u[i] &= 0xFFFFu;
+  }
+  return u;
+}
+__device__ __forceinline__ v4u ones_where(const v4u &u, uint32_t kind) {
+  v4u r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = u[i] & 0xFFFFu, hi = u[i] >> 16;
+    const auto is = [&](uint32_t h) { return kind == 0u ? h == 0x7F80u : kind == 1u ? h == 0xFF80u : (h & 0x7FFFu) > 0x7F80u; };
+    r[i] = (is(lo) ? 0x3F80u : 0u) | (is(hi) ? 0x3F800000u : 0u);
+  }
+  return r;
+}
+
 __device__ __forceinline__ bool any_not_finite(const v4u &u) {
   bool bad = false;
 #pragma unroll

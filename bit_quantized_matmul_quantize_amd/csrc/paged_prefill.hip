@@ -52,13 +52,15 @@ __device__ __forceinline__ uint32_t tiles_of(const PagedArgs &a, const PagedSpan
   return (uint32_t)(((uint64_t)p.n * (a.hq / a.hk) + kRows - 1u) / kRows);
 }
 
-template <uint32_t kDP, uint32_t kBits>
+// kExact: a head has kDP values, and a page has at least a tile's keys.
+// kCap: scores are capped (both may be, unless kExact).
+template <uint32_t kDP, uint32_t kBits, bool kExact, bool kCap>
 __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_kernel(PagedArgs a) {
   using S = Shape<kDP, kBits>;
   constexpr uint32_t kKT = S::kKT, kSubs = S::kSubs;
   constexpr uint32_t kHalves = kKT / 32;  // halves of a tile: 32 keys
   constexpr uint32_t kDS = kDP / 16;      // steps of the first product
-  constexpr uint32_t kDB = kDP / 32;      // blocks of the second
+  constexpr uint32_t kDB = kDP / 32;      // blocks of the second, two steps each
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
   const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -95,13 +97,14 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
     }
   }
 
-  const uint32_t page = 1u << a.page_shift, block = paged_block_bytes(page, a.d, kBits);
+  const uint32_t d = kExact ? kDP : a.d;
+  const uint32_t page = 1u << a.page_shift, block = paged_block_bytes(page, d, kBits);
   const uint64_t page_bytes = (uint64_t)block * a.hk;
   const int32_t *table = a.table + (uint64_t)seq * a.width;
   const uint8_t *kc = a.k_cache + (uint64_t)head * block, *vc = a.v_cache + (uint64_t)head * block;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
 
-  if (a.d != kDP) {
+  if constexpr (!kExact) {
     for (uint32_t i = threadIdx.x * 16u; i < 2u * S::kStage; i += kThreads * 16u) *reinterpret_cast<v4u *>(lds + i) = v4u{0, 0, 0, 0};
     __syncthreads();
   }
@@ -123,41 +126,49 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
   // ---- bringing a tile: places in the tile that this thread brings
   constexpr uint32_t kParts = kBits == 16 ? S::kLoads : S::kCodes;
   constexpr uint32_t kUnit = 128 / kBits;
+  constexpr bool kFull = kParts * kThreads * 16 == S::kTile * kBits / 16;  // every thread has a unit in every part
   v4u kr[kBits == 8 ? kParts : 1], vr[kBits == 8 ? kParts : 1];
   float scale_r = 0.0f;
   auto bring = [&](int32_t key0, const uint32_t (&ids)[kSubs], uint32_t stage) {
     const uint32_t off0 = (uint32_t)key0 & (page - 1u);
-    const bool one_page = page >= kKT;
+    const bool one_page = kExact || page >= kKT;
     const uint32_t id0 = ids[0] < a.pages ? ids[0] : 0u;
-    const uint8_t *k0 = kc + id0 * page_bytes + off0 * 16u, *v0 = vc + id0 * page_bytes + (uint64_t)(off0 / kUnit) * a.d * 16u;
+    const uint8_t *k0 = kc + id0 * page_bytes + off0 * 16u, *v0 = vc + id0 * page_bytes + (uint64_t)(off0 / kUnit) * d * 16u;
 #pragma unroll
     for (uint32_t j = 0; j < kParts; ++j) {
       // (wave's 64 units follow each other, in LDS too)
       const uint32_t i = (wave + kWaves * j) * 64u + lane;
       const uint32_t ku = i / kKT, key = i % kKT, vg = i / kDP, dim = i % kDP;
-      const bool has_k = ku * kUnit < a.d, has_v = dim < a.d && vg * kUnit < kKT;
+      const bool has_k = (kExact && kFull) || ku * kUnit < d, has_v = (kExact && kFull) || (dim < d && vg * kUnit < kKT);
       if constexpr (kBits == 16) {
         const uint32_t to = lds0 + stage * S::kStage + (wave + kWaves * j) * 1024u;
-        if (one_page) {
+        if constexpr (kExact) {  // (uniform parts of the offsets belong to the scalar base)
+          constexpr uint32_t kRuns = 64 / kKT;
+          load_to_lds(to, (lane / kKT * page + lane % kKT) * 16u, k0 + (uint64_t)((wave + kWaves * j) * kRuns) * page * 16u);
+          load_to_lds(to + S::kTile, lane * 16u, v0 + (wave + kWaves * j) * 1024u);
+        } else if (one_page) {
           if (has_k) load_to_lds(to, (ku * page + key) * 16u, k0);
-          if (has_v) load_to_lds(to + S::kTile, (vg * a.d + dim) * 16u, v0);
+          if (has_v) load_to_lds(to + S::kTile, (vg * d + dim) * 16u, v0);
         } else {
           const uint32_t ks = key / 16u, vs = vg * kUnit / 16u;
           const uint32_t ko = (uint32_t)(key0 + (int32_t)key) & (page - 1u), vo = (uint32_t)(key0 + (int32_t)(vg * kUnit)) & (page - 1u);
           if (has_k) load_to_lds(to, kc + pick(ids, ks) * page_bytes + (ku * page + ko) * 16u);
-          if (has_v) load_to_lds(to + S::kTile, vc + pick(ids, vs) * page_bytes + ((uint64_t)(vo / kUnit) * a.d + dim) * 16u);
+          if (has_v) load_to_lds(to + S::kTile, vc + pick(ids, vs) * page_bytes + ((uint64_t)(vo / kUnit) * d + dim) * 16u);
         }
+      } else if (one_page) {
+        if (has_k) kr[j] = *reinterpret_cast<const v4u *>(k0 + (ku * page + key) * 16u);
+        if (has_v) vr[j] = *reinterpret_cast<const v4u *>(v0 + (vg * d + dim) * 16u);
       } else {
         const uint32_t ko = (uint32_t)(key0 + (int32_t)key) & (page - 1u), vo = (uint32_t)(key0 + (int32_t)(vg * kUnit)) & (page - 1u);
         if (has_k) kr[j] = *reinterpret_cast<const v4u *>(kc + pick(ids, key / 16u) * page_bytes + (ku * page + ko) * 16u);
-        if (has_v) vr[j] = *reinterpret_cast<const v4u *>(vc + pick(ids, vg) * page_bytes + ((uint64_t)(vo / kUnit) * a.d + dim) * 16u);
+        if (has_v) vr[j] = *reinterpret_cast<const v4u *>(vc + pick(ids, vg) * page_bytes + ((uint64_t)(vo / kUnit) * d + dim) * 16u);
       }
     }
     if constexpr (kBits == 8) {
       if (threadIdx.x < 2u * kKT) {
         const uint32_t key = threadIdx.x % kKT, ko = (uint32_t)(key0 + (int32_t)key) & (page - 1u);
         const uint8_t *from = threadIdx.x < kKT ? kc : vc;
-        scale_r = *reinterpret_cast<const float *>(from + pick(ids, key / 16u) * page_bytes + page * a.d + ko * 4u);
+        scale_r = *reinterpret_cast<const float *>(from + pick(ids, key / 16u) * page_bytes + page * d + ko * 4u);
       }
     }
   };
@@ -169,11 +180,11 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
       for (uint32_t j = 0; j < kParts; ++j) {
         const uint32_t i = (wave + kWaves * j) * 64u + lane;
         const uint32_t ku = i / kKT, key = i % kKT, vg = i / kDP, dim = i % kDP;
-        if (ku * kUnit < a.d) {
+        if ((kExact && kFull) || ku * kUnit < d) {
           *reinterpret_cast<v4u *>(to + (2u * ku * kKT + key) * 16u) = bf16_of_codes(kr[j][0], kr[j][1]);
           *reinterpret_cast<v4u *>(to + ((2u * ku + 1u) * kKT + key) * 16u) = bf16_of_codes(kr[j][2], kr[j][3]);
         }
-        if (dim < a.d && vg * kUnit < kKT) {
+        if ((kExact && kFull) || (dim < d && vg * kUnit < kKT)) {
           *reinterpret_cast<v4u *>(to + S::kTile + (2u * vg * kDP + dim) * 16u) = bf16_of_codes(vr[j][0], vr[j][1]);
           *reinterpret_cast<v4u *>(to + S::kTile + ((2u * vg + 1u) * kDP + dim) * 16u) = bf16_of_codes(vr[j][2], vr[j][3]);
         }
@@ -182,7 +193,10 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
     }
   };
 
-  const float scale2 = a.scale * kLog2e, cap2 = a.cap * kLog2e, inv2 = a.cap != 0.0f ? 2.0f * kLog2e / a.cap : 0.0f;
+  // scores base 2 are scale2 times the products; under a cap they are made of them at once
+  const bool cap = kExact ? kCap : a.cap != 0.0f;
+  const float scale2 = cap ? 1.0f : a.scale * kLog2e;
+  const float cap2 = a.cap * kLog2e, inv2 = cap ? 2.0f * kLog2e * a.scale / a.cap : 0.0f;
   float m = -INFINITY, l = 0.0f;
   v16f o[kDB];
 #pragma unroll
@@ -191,6 +205,151 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
     for (uint32_t i = 0; i < 16; ++i) o[b][i] = 0.0f;
   // the key of this lane's row of K in a half tile
   const uint32_t k_row = 16u * (r >> 4) + 8u * ((r >> 2) & 1u) + 4u * ((r >> 3) & 1u) + (r & 3u);
+  const uint32_t k_at = (half * kKT + k_row) * 16u, v_at = (half * kDP + r) * 16u;
+
+  // One tile.  hole: bit t where the tile's keys 16 t.. lie in no page; whole: all
+  // rows of the wave see all of it.
+  auto compute = [&](int32_t key0, uint32_t stage, uint32_t hole, bool whole) {
+    const uint8_t *kt = lds + stage * S::kStage + k_at, *vt = lds + stage * S::kStage + S::kTile + v_at;
+    const float *scales = reinterpret_cast<const float *>(lds + stage * S::kStage + 2u * S::kTile) + 8u * half;
+    // the operands of a half tile are read while the last one's are used
+    auto read_k = [&](uint32_t f, uint32_t s) { return *reinterpret_cast<const v4u *>(kt + (2u * s * kKT + 32u * f) * 16u); };
+    auto read_v = [&](uint32_t f, uint32_t i) {
+      return *reinterpret_cast<const v4u *>(vt + ((4u * f + 2u * (i / kDB)) * kDP + 32u * (i % kDB)) * 16u);
+    };
+    v16f x[kHalves];
+    v4u k[2][kDS], v[2][2 * kDB];
+#pragma unroll
+    for (uint32_t s = 0; s < kDS; ++s) k[0][s] = read_k(0, s);
+#pragma unroll
+    for (uint32_t f = 0; f < kHalves; ++f) {
+#pragma unroll
+      for (uint32_t i = 0; i < 16; ++i) x[f][i] = 0.0f;
+#pragma unroll
+      for (uint32_t s = 0; s < kDS; ++s) {
+        x[f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(k[f & 1][s]), as_bf(q[s]), x[f], 0, 0, 0);
+        if (f + 1u < kHalves)
+          k[~f & 1][s] = read_k(f + 1u, s);
+        else
+          v[0][s] = read_v(0, s);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    // x: of keys 32 f + 16 (i / 8) + 8 half + i % 8
+#pragma unroll
+    for (uint32_t f = 0; f < kHalves; ++f) {
+      if constexpr (kBits == 8) {
+#pragma unroll
+        for (uint32_t i = 0; i < 16; i += 4) {
+          const v4f s = *reinterpret_cast<const v4f *>(scales + 32u * f + 16u * (i / 8u) + i % 8u);
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) x[f][i + e] *= s[e];
+        }
+      }
+      if (cap) {
+#pragma unroll
+        for (uint32_t i = 0; i < 16; ++i) x[f][i] = capped(x[f][i], cap2, inv2);
+      }
+    }
+    // the keys 16 t.. of the tile that this row sees: of key0 + 16 t + 8 half + i, bit i
+    auto seen_of = [&](uint32_t t) {
+      const int32_t at = key0 + (int32_t)(16u * t + 8u * half), from = max(low - at, 0), to = min(min(pos, p.keys - 1) - at, 7);
+      return hole >> t & 1u || from > to ? 0u : (0xFFu >> (7 - to)) & (0xFFu << from);
+    };
+    if (!whole) {
+#pragma unroll
+      for (uint32_t f = 0; f < kHalves; ++f)
+#pragma unroll
+        for (uint32_t kk = 0; kk < 2; ++kk) {
+          uint32_t seen = seen_of(2u * f + kk);
+          asm volatile("" : "+v"(seen));  // (keeps this a branch: selects in every tile cost a tenth of it)
+#pragma unroll
+          for (uint32_t i = 0; i < 8; ++i) x[f][8u * kk + i] = seen >> i & 1u ? x[f][8u * kk + i] : -INFINITY;
+        }
+    }
+    float top = x[0][0];
+#pragma unroll
+    for (uint32_t f = 0; f < kHalves; ++f)
+#pragma unroll
+      for (uint32_t i = 0; i < 16; i += 2) top = fmaxf(fmaxf(x[f][i], x[f][i + 1]), top);
+    top *= scale2;
+    if (__ballot(top > m + kSlack)) {
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const float next = fmaxf(m, top);
+      const float keep = m == -INFINITY ? 0.0f : exp2_hw(m - next);
+      m = next;
+      l *= keep;
+#pragma unroll
+      for (uint32_t b = 0; b < kDB; ++b)
+#pragma unroll
+        for (uint32_t i = 0; i < 16; ++i) o[b][i] *= keep;
+    }
+    const float base = m == -INFINITY ? 0.0f : m;
+    // weights, rounded to bf16 for the matrix cores: 2^-8 of each at most, as the output is rounded
+    v4u w[kHalves][2];
+#pragma unroll
+    for (uint32_t f = 0; f < kHalves; ++f)
+#pragma unroll
+      for (uint32_t i = 0; i < 16; i += 2) {
+        float y0 = exp2_hw(fmaf(x[f][i], scale2, -base)), y1 = exp2_hw(fmaf(x[f][i + 1], scale2, -base));
+        l += y0 + y1;
+        if constexpr (kBits == 8) {
+          const float2 s = *reinterpret_cast<const float2 *>(scales + kKT + 32u * f + 16u * (i / 8u) + i % 8u);
+          y0 = x[f][i] == -INFINITY ? 0.0f : y0 * s.x;
+          y1 = x[f][i + 1] == -INFINITY ? 0.0f : y1 * s.y;
+        }
+        w[f][i / 8u][i % 8u / 2u] = two_bf16(y0, y1);
+      }
+    // A NaN or an infinity among the values of a tile that not every row sees whole:
+    // 0 * NaN must not reach the rows that do not see its key.  It counts as zero in
+    // the product, and is added afterwards where it is seen.
+    bool bad = false;
+    if (kBits == 16 && !whole) {
+#pragma unroll 1
+      for (uint32_t i = lane; i < S::kTile / 16u; i += 64u)
+        bad |= any_not_finite(*reinterpret_cast<const v4u *>(lds + stage * S::kStage + S::kTile + i * 16u));
+      bad = __ballot(bad) != 0u;
+    }
+#pragma unroll
+    for (uint32_t f = 0; f < kHalves; ++f) {
+      if (bad) {
+#pragma unroll
+        for (uint32_t i = 0; i < 2u * kDB; ++i) {
+          asm volatile("" : "+v"(v[f & 1][i]));
+          v[f & 1][i] = finite_only(v[f & 1][i]);
+        }
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < 2u * kDB; ++i) {
+        o[i % kDB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(v[f & 1][i]), as_bf(w[f][i / kDB]), o[i % kDB], 0, 0, 0);
+        if (f + 1u < kHalves) v[~f & 1][i] = read_v(f + 1u, i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (bad) {
+#pragma unroll 1
+      for (uint32_t t = 0; t < kSubs; ++t) {
+        const uint32_t seen = seen_of(t);
+        v4u ones;  // 1 for the keys that are seen
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) ones[i] = (seen >> (2u * i) & 1u ? 0x3F80u : 0u) | (seen >> (2u * i + 1u) & 1u ? 0x3F800000u : 0u);
+#pragma unroll
+        for (uint32_t b = 0; b < kDB; ++b) {
+          const v4u u = *reinterpret_cast<const v4u *>(vt + (2u * t * kDP + 32u * b) * 16u);
+#pragma unroll 1
+          for (uint32_t kind = 0; kind < 3u; ++kind) {  // infinities, the negative ones, NaNs: how many are seen
+            v16f n;
+#pragma unroll
+            for (uint32_t i = 0; i < 16; ++i) n[i] = 0.0f;
+            n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(ones_where(u, kind)), as_bf(ones), n, 0, 0, 0);
+            const float add = __uint_as_float(kind == 0u ? 0x7F800000u : kind == 1u ? 0xFF800000u : 0x7FC00000u);
+#pragma unroll
+            for (uint32_t i = 0; i < 16; ++i) o[b][i] += n[i] != 0.0f ? add : 0.0f;
+          }
+        }
+      }
+    }
+  };
 
   uint32_t ids[kSubs], next_ids[kSubs];
   ids_of(begin, ids);
@@ -202,139 +361,17 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
     // this tile has arrived, and nobody reads the other stage any more
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __syncthreads();
+    uint32_t hole = 0;
+#pragma unroll
+    for (uint32_t t = 0; t < kSubs; ++t) hole |= ids[t] >= a.pages ? 1u << t : 0u;
     const bool more = key0 + (int32_t)kKT < end;
     if (more) bring(key0 + (int32_t)kKT, next_ids, stage ^ 1u);
-    uint32_t after_ids[kSubs];
-    ids_of(key0 + 2 * (int32_t)kKT, after_ids);
-    if (key0 < any_end && key0 + (int32_t)kKT > any_low) {
-      const uint8_t *kt = lds + stage * S::kStage, *vt = kt + S::kTile;
-      const float *scales = reinterpret_cast<const float *>(vt + S::kTile);
-      uint32_t hole = 0;  // bit t: the tile's keys 16 t.. lie in no page
 #pragma unroll
-      for (uint32_t t = 0; t < kSubs; ++t) hole |= ids[t] >= a.pages ? 1u << t : 0u;
-      const bool whole = !hole && key0 >= whole_low && key0 + (int32_t)kKT <= whole_end;
-      v16f x[kHalves];
-#pragma unroll
-      for (uint32_t f = 0; f < kHalves; ++f) {
-#pragma unroll
-        for (uint32_t i = 0; i < 16; ++i) x[f][i] = 0.0f;
-#pragma unroll
-        for (uint32_t s = 0; s < kDS; ++s) {
-          const v4u k = *reinterpret_cast<const v4u *>(kt + ((2u * s + half) * kKT + 32u * f + k_row) * 16u);
-          x[f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(k), as_bf(q[s]), x[f], 0, 0, 0);
-        }
-      }
-      // x: scores base 2, of keys 32 f + 16 (i / 8) + 8 half + i % 8
-#pragma unroll
-      for (uint32_t f = 0; f < kHalves; ++f) {
-        if constexpr (kBits == 8) {
-#pragma unroll
-          for (uint32_t i = 0; i < 16; i += 4) {
-            const v4f s = *reinterpret_cast<const v4f *>(scales + 32u * f + 16u * (i / 8u) + 8u * half + i % 8u);
-#pragma unroll
-            for (uint32_t e = 0; e < 4; ++e) x[f][i + e] *= s[e];
-          }
-        }
-        if (a.cap != 0.0f) {
-#pragma unroll
-          for (uint32_t i = 0; i < 16; ++i) x[f][i] = capped(x[f][i] * a.scale, cap2, inv2);
-        } else {
-#pragma unroll
-          for (uint32_t i = 0; i < 16; ++i) x[f][i] *= scale2;
-        }
-        if (!whole) {
-#pragma unroll
-          for (uint32_t i = 0; i < 16; ++i) {
-            const int32_t key = key0 + (int32_t)(32u * f + 16u * (i / 8u) + 8u * half + i % 8u);
-            const bool seen = key <= pos && key >= low && key < p.keys && !(hole >> (2u * f + i / 8u) & 1u);
-            x[f][i] = seen ? x[f][i] : -INFINITY;
-          }
-        }
-      }
-      float top = x[0][0];
-#pragma unroll
-      for (uint32_t f = 0; f < kHalves; ++f)
-#pragma unroll
-        for (uint32_t i = 0; i < 16; ++i) top = fmaxf(top, x[f][i]);
-      if (__ballot(top > m + kSlack)) {
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float next = fmaxf(m, top);
-        const float keep = m == -INFINITY ? 0.0f : exp2_hw(m - next);
-        m = next;
-        l *= keep;
-#pragma unroll
-        for (uint32_t b = 0; b < kDB; ++b)
-#pragma unroll
-          for (uint32_t i = 0; i < 16; ++i) o[b][i] *= keep;
-      }
-      const float base = m == -INFINITY ? 0.0f : m;
-      // weights, rounded to bf16 for the matrix cores: 2^-9 of each, as the output is rounded
-      v4u w[kHalves][2];
-#pragma unroll
-      for (uint32_t f = 0; f < kHalves; ++f)
-#pragma unroll
-        for (uint32_t i = 0; i < 16; i += 2) {
-          float y0 = exp2_hw(x[f][i] - base), y1 = exp2_hw(x[f][i + 1] - base);
-          l += y0 + y1;
-          if constexpr (kBits == 8) {
-            const float2 s = *reinterpret_cast<const float2 *>(scales + kKT + 32u * f + 16u * (i / 8u) + 8u * half + i % 8u);
-            y0 = x[f][i] == -INFINITY ? 0.0f : y0 * s.x;
-            y1 = x[f][i + 1] == -INFINITY ? 0.0f : y1 * s.y;
-          }
-          w[f][i / 8u][i % 8u / 2u] = two_bf16(y0, y1);
-        }
-      bool bad = false;
-      if constexpr (kBits == 16) {
-        if (!whole) {
-#pragma unroll 1
-          for (uint32_t i = lane; i < S::kTile / 16u; i += 64u) bad |= any_not_finite(*reinterpret_cast<const v4u *>(vt + i * 16u));
-          bad = __ballot(bad) != 0u;
-        }
-      }
-      if (!bad) {
-#pragma unroll
-        for (uint32_t f = 0; f < kHalves; ++f)
-#pragma unroll
-          for (uint32_t kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (uint32_t b = 0; b < kDB; ++b) {
-              const v4u v = *reinterpret_cast<const v4u *>(vt + ((4u * f + 2u * kk + half) * kDP + 32u * b + r) * 16u);
-              o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(v), as_bf(w[f][kk]), o[b], 0, 0, 0);
-            }
-      } else {
-        // A NaN or an infinity among the values of a tile that not every row sees
-        // whole: 0 * NaN must not reach the rows that do not see its key.  One
-        // key at a time, added where it is seen.
-#pragma unroll 1
-        for (uint32_t key = 0; key < kKT; ++key) {
-          const uint32_t group = key / 8u, e = key % 8u;
-          const int32_t place = key0 + (int32_t)key;
-          const bool seen = place <= pos && place >= low && place < p.keys && !(hole >> (key / 16u) & 1u);
-          const bool here = half == (group & 1u);
-          const uint32_t keep = here ? (e & 1u ? 0xFFFF0000u : 0xFFFFu) : 0u;
-          v4u sel, mine = w[0][0];
-#pragma unroll
-          for (uint32_t i = 0; i < 4; ++i) sel[i] = e / 2u == i ? keep : 0u;
-#pragma unroll
-          for (uint32_t f = 0; f < kHalves; ++f)
-#pragma unroll
-            for (uint32_t kk = 0; kk < 2; ++kk) mine = group / 2u == 2u * f + kk ? w[f][kk] : mine;
-#pragma unroll
-          for (uint32_t b = 0; b < kDB; ++b) {
-            const v4u v = *reinterpret_cast<const v4u *>(vt + ((group / 2u * 2u + half) * kDP + 32u * b + r) * 16u);
-            v16f one;
-#pragma unroll
-            for (uint32_t i = 0; i < 16; ++i) one[i] = 0.0f;
-            one = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(v & sel), as_bf(mine & sel), one, 0, 0, 0);
-#pragma unroll
-            for (uint32_t i = 0; i < 16; ++i) o[b][i] += seen ? one[i] : 0.0f;
-          }
-        }
-      }
-    }
+    for (uint32_t t = 0; t < kSubs; ++t) ids[t] = next_ids[t];
+    ids_of(key0 + 2 * (int32_t)kKT, next_ids);
+    if (key0 < any_end && key0 + (int32_t)kKT > any_low)
+      compute(key0, stage, hole, !hole && key0 >= whole_low && key0 + (int32_t)kKT <= whole_end);
     if (more) settle(stage ^ 1u);
-#pragma unroll
-    for (uint32_t t = 0; t < kSubs; ++t) ids[t] = next_ids[t], next_ids[t] = after_ids[t];
   }
 
   // rows leave through LDS, where the stages were (each wave's own part)
@@ -350,19 +387,19 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
       *reinterpret_cast<uint2 *>(mine + r * S::kOutPitch + (32u * b + 2u * i + 4u * half) * 2u) =
           make_uint2(two_bf16(o[b][i] * inv, o[b][i + 1] * inv), two_bf16(o[b][i + 2] * inv, o[b][i + 3] * inv));
   __syncthreads();
-  const uint32_t pieces = a.d / 8u;
+  const uint32_t pieces = d / 8u;
   for (uint32_t i = lane; i < 32u * pieces; i += 64u) {
     const uint32_t at = i / pieces, piece = i % pieces, to = wrow0 + at;
     if (to >= rows) break;
-    *reinterpret_cast<uint4 *>(a.out + ((uint64_t)(p.first + to / g) * a.hq + head * g + to % g) * a.d + piece * 8u) =
+    *reinterpret_cast<uint4 *>(a.out + ((uint64_t)(p.first + to / g) * a.hq + head * g + to % g) * d + piece * 8u) =
         *reinterpret_cast<const uint4 *>(mine + at * S::kOutPitch + piece * 16u);
   }
 }
 
-template <uint32_t kDP, uint32_t kBits>
+template <uint32_t kDP, uint32_t kBits, bool kExact, bool kCap>
 hipError_t launch(const PagedArgs &a, hipStream_t s) {
   constexpr uint32_t kLds = Shape<kDP, kBits>::kLds;
-  auto *kernel = paged_prefill_kernel<kDP, kBits>;
+  auto *kernel = paged_prefill_kernel<kDP, kBits, kExact, kCap>;
   if (kLds > 65536u) {
     const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void *>(kernel), (int)kLds);
     if (e != hipSuccess) return e;
@@ -373,13 +410,19 @@ hipError_t launch(const PagedArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <uint32_t kDP, uint32_t kBits>
+hipError_t launch_exact(const PagedArgs &a, hipStream_t s) {
+  if (a.d != kDP || (1u << a.page_shift) < Shape<kDP, kBits>::kKT) return launch<kDP, kBits, false, false>(a, s);
+  return a.cap != 0.0f ? launch<kDP, kBits, true, true>(a, s) : launch<kDP, kBits, true, false>(a, s);
+}
+
 template <uint32_t kBits>
 hipError_t launch_heads(const PagedArgs &a, hipStream_t s) {
-  if (a.d <= 64u) return launch<64, kBits>(a, s);
-  if (a.d <= 96u) return launch<96, kBits>(a, s);
-  if (a.d <= 128u) return launch<128, kBits>(a, s);
-  if (a.d <= 192u) return launch<192, kBits>(a, s);
-  return launch<256, kBits>(a, s);
+  if (a.d <= 64u) return launch_exact<64, kBits>(a, s);
+  if (a.d <= 96u) return launch_exact<96, kBits>(a, s);
+  if (a.d <= 128u) return launch_exact<128, kBits>(a, s);
+  if (a.d <= 192u) return launch_exact<192, kBits>(a, s);
+  return launch_exact<256, kBits>(a, s);
 }
 
 }  // namespace
