@@ -112,8 +112,7 @@ __device__ __forceinline__ v4u bf16_of_codes(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Of eight bf16: the finite ones, zero for the others; and 1 for +infinities (kind
-// 0), -infinities (1) or NaNs (2), zero for the others.
+// Of eight bf16: the finite ones, zero for the others.
 __device__ __forceinline__ v4u finite_only(v4u u) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -122,15 +121,20 @@ __device__ __forceinline__ v4u finite_only(v4u u) {
   }
   return u;
 }
-__device__ __forceinline__ v4u ones_where(const v4u &u, uint32_t kind) {
+// The others: 1 for an infinity, 256 for a negative one, 65536 for a NaN, and what a
+// sum of up to 255 of each adds to a sum of finite values.
+__device__ __forceinline__ v4u not_finite_marks(const v4u &u) {
   v4u r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = u[i] & 0xFFFFu, hi = u[i] >> 16;
-    const auto is = [&](uint32_t h) { return kind == 0u ? h == 0x7F80u : kind == 1u ? h == 0xFF80u : (h & 0x7FFFu) > 0x7F80u; };
-    r[i] = (is(lo) ? 0x3F80u : 0u) | (is(hi) ? 0x3F800000u : 0u);
+    const auto mark = [](uint32_t h) { return (h & 0x7FFFu) > 0x7F80u ? 0x4780u : h == 0x7F80u ? 0x3F80u : h == 0xFF80u ? 0x4380u : 0u; };
+    r[i] = mark(u[i] & 0xFFFFu) | mark(u[i] >> 16) << 16;
   }
   return r;
+}
+__device__ __forceinline__ float of_marks(float sum) {
+  const uint32_t n = (uint32_t)sum, plus = n & 0xFFu, minus = n & 0xFF00u;
+  return n == 0u ? 0.0f : __uint_as_float(n >> 16 || (plus && minus) ? 0x7FC00000u : plus ? 0x7F800000u : 0xFF800000u);
 }
 
 __device__ __forceinline__ bool any_not_finite(const v4u &u) {

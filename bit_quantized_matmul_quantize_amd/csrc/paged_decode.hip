@@ -78,13 +78,14 @@ __host__ __device__ inline Parts parts_of(uint8_t *workspace, uint32_t slots, ui
 
 // ---- a run ------------------------------------------------------------------------
 
-// kDP: values of a head, rounded up; kNT: column blocks of 16 rows.
-template <uint32_t kDP, uint32_t kBits, uint32_t kNT>
-__global__ __launch_bounds__(64 * kWaves, 1) void paged_decode_kernel(PagedArgs a, uint32_t slots, float *sums, float2 *stats) {
+// kDP: values of a head, rounded up (kExact: as they are); kNT: column blocks of 16
+// rows.
+template <uint32_t kDP, uint32_t kBits, uint32_t kNT, bool kExact>
+__global__ __launch_bounds__(64 * kWaves, kDP * kNT <= (kBits == 16 ? 256 : 128) && kDP <= 128 ? 2 : 1) void paged_decode_kernel(PagedArgs a, uint32_t slots, float *sums, float2 *stats) {
   constexpr uint32_t kUnit = 128u / kBits;        // values of a unit
   constexpr uint32_t kKeys = kUnit * 4u;          // keys of a step: a unit of v for each group of 16 lanes
   constexpr uint32_t kKT = kKeys / 16u;           // their tiles
-  constexpr uint32_t kKS = kDP / (kUnit * 4u);    // steps of a product over a head's values, in units
+  constexpr uint32_t kKS = (kDP / kUnit + 3u) / 4u;  // steps of a product over a head's values: four units each
   constexpr uint32_t kHalves = kBits == 16u ? 1u : 2u;  // operands of a unit
   constexpr uint32_t kDB = kDP / 16u;             // blocks of a head's values
   constexpr uint32_t kRows = 16u * kNT;
@@ -108,8 +109,9 @@ __global__ __launch_bounds__(64 * kWaves, 1) void paged_decode_kernel(PagedArgs 
   const int32_t key_end = min((job.first + (int32_t)min((run + 1u) * per, job.blocks)) * (int32_t)kBlock, p.keys);
 
   // this lane's rows: places, and the operand of q
-  const uint32_t page = 1u << a.page_shift, block = paged_block_bytes(page, a.d, kBits), units = a.d / kUnit;
+  const uint32_t page = 1u << a.page_shift, d = kExact ? kDP : a.d, block = paged_block_bytes(page, d, kBits), units = d / kUnit;
   int32_t pos[kNT], low[kNT];
+  constexpr bool kShared = kDP > 128;  // q in LDS, where a lane's registers do not suffice
   v4u q[kNT][kKS * kHalves];
 #pragma unroll
   for (uint32_t t = 0; t < kNT; ++t) {
@@ -124,10 +126,20 @@ __global__ __launch_bounds__(64 * kWaves, 1) void paged_decode_kernel(PagedArgs 
       for (uint32_t h = 0; h < kHalves; ++h) {
         v4u v = {0, 0, 0, 0};
         const uint32_t unit = 4u * s + c;
+        const uint32_t i = t * kKS * kHalves + s * kHalves + h;
+        if (kShared && i % kWaves != wave) continue;
         if (live && unit < units) v = *reinterpret_cast<const v4u *>(from + unit * kUnit + h * 8u);
-        q[t][s * kHalves + h] = v;
+        if constexpr (kShared)
+          *reinterpret_cast<v4u *>(lds + (i * 64u + lane) * 16u) = v;
+        else
+          q[t][s * kHalves + h] = v;
       }
   }
+  if constexpr (kShared) __syncthreads();
+  auto q_of = [&](uint32_t n, uint32_t i) {
+    if constexpr (kShared) return *reinterpret_cast<const v4u *>(lds + ((n * kKS * kHalves + i) * 64u + lane) * 16u);
+    return q[n][i];
+  };
   // where all of the tile's rows see a key: [all_low, all_pos]
   int32_t all_pos, all_low;
   {
@@ -136,7 +148,9 @@ __global__ __launch_bounds__(64 * kWaves, 1) void paged_decode_kernel(PagedArgs 
     all_low = a.window ? (int32_t)max((int64_t)p.at + (int64_t)(row1 / g) + 1 - (int64_t)a.window, (int64_t)0) : 0;
   }
 
-  const float scale2 = a.scale * kLog2e, cap2 = a.cap * kLog2e, inv2 = a.cap != 0.0f ? 2.0f * kLog2e / a.cap : 0.0f;
+  // scores base 2 are scale2 times the products; under a cap they are made of them at once
+  const float scale2 = a.cap != 0.0f ? 1.0f : a.scale * kLog2e;
+  const float cap2 = a.cap * kLog2e, inv2 = a.cap != 0.0f ? 2.0f * kLog2e * a.scale / a.cap : 0.0f;
   float m[kNT], l[kNT];
   v4f o[kNT][kDB];
 #pragma unroll
@@ -151,41 +165,51 @@ __global__ __launch_bounds__(64 * kWaves, 1) void paged_decode_kernel(PagedArgs 
   const uint8_t *kc = a.k_cache + (uint64_t)head * block, *vc = a.v_cache + (uint64_t)head * block;
   const uint64_t page_bytes = (uint64_t)block * a.hk;
 
-  for (int32_t key0 = key_begin + (int32_t)(wave * kKeys); key0 < key_end; key0 += (int32_t)(kWaves * kKeys)) {
-    // the pages of the step's tiles of 16 keys
-    uint32_t ids[kKT];
-    bool holes = false;
+  // A step: 32 keys (int8: 64).  Values are on their way while the scores are made,
+  // the next step's keys while the softmax is.
+  constexpr int32_t kStride = (int32_t)(kWaves * kKeys);
+  auto ids_of = [&](int32_t key0, uint32_t (&ids)[kKT]) {  // the pages of its tiles of 16 keys
 #pragma unroll
     for (uint32_t t = 0; t < kKT; ++t) {
       const uint32_t at = (uint32_t)(key0 + (int32_t)(16u * t)) >> a.page_shift;
-      const uint32_t id = at < a.width ? (uint32_t)table[at] : ~0u;
-      ids[t] = __builtin_amdgcn_readfirstlane(id);
-      holes |= ids[t] >= a.pages;
+      ids[t] = __builtin_amdgcn_readfirstlane(at < a.width ? (uint32_t)table[at] : ~0u);
     }
-    // keys, scores
-    v4f x[kNT][kKT];
+  };
+  v4u k[kKT][kKS];
+  v4f ks[kKT];
+  auto load_k = [&](int32_t key0, const uint32_t (&ids)[kKT]) {
 #pragma unroll
     for (uint32_t t = 0; t < kKT; ++t) {
       const uint32_t id = ids[t] < a.pages ? ids[t] : 0u, off = (uint32_t)(key0 + (int32_t)(16u * t)) & (page - 1u);
-      const uint8_t *base = kc + id * page_bytes;
-#pragma unroll
-      for (uint32_t n = 0; n < kNT; ++n) x[n][t] = v4f{0, 0, 0, 0};
+      const uint8_t *base = kc + id * page_bytes + off * 16u;
 #pragma unroll
       for (uint32_t s = 0; s < kKS; ++s) {
-        const uint32_t unit = 4u * s + c;
-        v4u k = {0, 0, 0, 0};
-        if (unit < units) k = *reinterpret_cast<const v4u *>(base + (unit * page + off + r) * 16u);
-#pragma unroll
-        for (uint32_t h = 0; h < kHalves; ++h) {
-          const v4u kk = kBits == 16u ? k : bf16_of_codes(k[2 * h], k[2 * h + 1]);
-#pragma unroll
-          for (uint32_t n = 0; n < kNT; ++n)
-            x[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(kk), as_bf(q[n][s * kHalves + h]), x[n][t], 0, 0, 0);
+        if (kExact && 4u * s + 4u <= kDP / kUnit) {
+          k[t][s] = *reinterpret_cast<const v4u *>(base + (uint64_t)(4u * s) * page * 16u + (c * page + r) * 16u);
+        } else {  // (beyond the head's units: the first again, as zeros)
+          const bool has = 4u * s + c < units;
+          k[t][s] = *reinterpret_cast<const v4u *>(base + ((has ? 4u * s + c : 0u) * page + r) * 16u);
+          if (!has) k[t][s] = v4u{0, 0, 0, 0};
         }
       }
+      if constexpr (kBits == 8u) ks[t] = *reinterpret_cast<const v4f *>(kc + id * page_bytes + page * d + (off + 4u * c) * 4u);
     }
+  };
+
+  uint32_t ids[kKT], next_ids[kKT];
+  int32_t key0 = key_begin + (int32_t)(wave * kKeys);
+  if (key0 < key_end) {
+    ids_of(key0, ids);
+    load_k(key0, ids);
+    ids_of(key0 + kStride, next_ids);
+  }
+  for (; key0 < key_end; key0 += kStride) {
+    uint32_t hole = 0;  // bit t: the step's keys 16 t.. lie in no page
+#pragma unroll
+    for (uint32_t t = 0; t < kKT; ++t) hole |= ids[t] >= a.pages ? 1u << t : 0u;
     // values: unit of keys 8 c.. or 16 c.. of the step
     v4u v[kDB];
+    v4f vs[kKT];
     {
       const uint32_t t = c * kUnit / 16u;
       uint32_t id = ids[0];
@@ -193,34 +217,81 @@ __global__ __launch_bounds__(64 * kWaves, 1) void paged_decode_kernel(PagedArgs 
       for (uint32_t i = 1; i < kKT; ++i) id = t == i ? ids[i] : id;
       id = id < a.pages ? id : 0u;
       const uint32_t off = (uint32_t)(key0 + (int32_t)(c * kUnit)) & (page - 1u);
-      const uint8_t *base = vc + id * page_bytes + ((uint64_t)(off / kUnit) * a.d + r) * 16u;
+      const uint8_t *base = vc + id * page_bytes + ((uint64_t)(off / kUnit) * d + r) * 16u;
 #pragma unroll
       for (uint32_t b = 0; b < kDB; ++b) {
-        v[b] = v4u{0, 0, 0, 0};
-        if (16u * b < a.d) v[b] = *reinterpret_cast<const v4u *>(base + b * 256u);
+        // (beyond the head's values: the first again, whose sums are not taken)
+        v[b] = *reinterpret_cast<const v4u *>(base + (kExact || 16u * b < d ? b : 0u) * 256u);
+      }
+      if constexpr (kBits == 8u) {
+#pragma unroll
+        for (uint32_t i = 0; i < kKT; ++i) {
+          const uint32_t at = ids[i] < a.pages ? ids[i] : 0u, to = (uint32_t)(key0 + (int32_t)(16u * i)) & (page - 1u);
+          vs[i] = *reinterpret_cast<const v4f *>(vc + at * page_bytes + page * d + (to + 4u * c) * 4u);
+        }
       }
     }
-    v4f ks[kKT], vs[kKT];
+    __builtin_amdgcn_sched_barrier(0);
+    // scores
+    v4f x[kNT][kKT];
+#pragma unroll
+    for (uint32_t t = 0; t < kKT; ++t)
+#pragma unroll
+      for (uint32_t n = 0; n < kNT; ++n) x[n][t] = v4f{0, 0, 0, 0};
+    if constexpr (kBits == 8u) {  // (else the loop carries every code in a register of its own)
+#pragma unroll
+      for (uint32_t t = 0; t < kKT; ++t)
+#pragma unroll
+        for (uint32_t i = 0; i < kKS; ++i) asm volatile("" : "+v"(k[t][i]));
+    }
+    auto product = [&](uint32_t t, uint32_t s, uint32_t h, const v4u (&qq)[kNT]) {
+      const v4u kk = kBits == 16u ? k[t][s] : bf16_of_codes(k[t][s][2 * h], k[t][s][2 * h + 1]);
+#pragma unroll
+      for (uint32_t n = 0; n < kNT; ++n) x[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(kk), as_bf(qq[n]), x[n][t], 0, 0, 0);
+      if constexpr (kBits == 8u) __builtin_amdgcn_sched_barrier(0);  // (else all codes are unpacked at once)
+    };
+    if constexpr (kShared) {
+#pragma unroll
+      for (uint32_t i = 0; i < kKS * kHalves; ++i) {
+        v4u qq[kNT];
+#pragma unroll
+        for (uint32_t n = 0; n < kNT; ++n) qq[n] = q_of(n, i);
+#pragma unroll
+        for (uint32_t t = 0; t < kKT; ++t) product(t, i / kHalves, i % kHalves, qq);
+      }
+    } else {
+#pragma unroll
+      for (uint32_t t = 0; t < kKT; ++t)
+#pragma unroll
+        for (uint32_t i = 0; i < kKS * kHalves; ++i) {
+          v4u qq[kNT];
+#pragma unroll
+          for (uint32_t n = 0; n < kNT; ++n) qq[n] = q_of(n, i);
+          product(t, i / kHalves, i % kHalves, qq);
+        }
+    }
     if constexpr (kBits == 8u) {
 #pragma unroll
-      for (uint32_t t = 0; t < kKT; ++t) {
-        const uint32_t id = ids[t] < a.pages ? ids[t] : 0u, off = (uint32_t)(key0 + (int32_t)(16u * t)) & (page - 1u);
-        const uint64_t at = id * page_bytes + page * a.d + (off + 4u * c) * 4u;
-        ks[t] = *reinterpret_cast<const v4f *>(kc + at);
-        vs[t] = *reinterpret_cast<const v4f *>(vc + at);
-      }
+      for (uint32_t n = 0; n < kNT; ++n)
+#pragma unroll
+        for (uint32_t t = 0; t < kKT; ++t) x[n][t] *= ks[t];
     }
-    const bool whole = !holes && key0 + (int32_t)kKeys - 1 <= all_pos && key0 >= all_low && key0 + (int32_t)kKeys <= key_end;
+    __builtin_amdgcn_sched_barrier(0);
+    if (key0 + kStride < key_end) load_k(key0 + kStride, next_ids);
+#pragma unroll
+    for (uint32_t t = 0; t < kKT; ++t) ids[t] = next_ids[t];
+    ids_of(key0 + 2 * kStride, next_ids);
+    __builtin_amdgcn_sched_barrier(0);
+
+    const bool whole = !hole && key0 + (int32_t)kKeys - 1 <= all_pos && key0 >= all_low && key0 + (int32_t)kKeys <= key_end;
+    v4u ph[kNT][kHalves], pl[kNT][kHalves];  // the weights
 #pragma unroll
     for (uint32_t n = 0; n < kNT; ++n) {
+      if (a.cap != 0.0f) {
 #pragma unroll
-      for (uint32_t t = 0; t < kKT; ++t) {
+        for (uint32_t t = 0; t < kKT; ++t)
 #pragma unroll
-        for (uint32_t e = 0; e < 4; ++e) {
-          float y = x[n][t][e];
-          if constexpr (kBits == 8u) y *= ks[t][e];
-          x[n][t][e] = a.cap != 0.0f ? capped(y * a.scale, cap2, inv2) : y * scale2;
-        }
+          for (uint32_t e = 0; e < 4; ++e) x[n][t][e] = capped(x[n][t][e], cap2, inv2);
       }
       if (!whole) {
 #pragma unroll
@@ -228,15 +299,14 @@ __global__ __launch_bounds__(64 * kWaves, 1) void paged_decode_kernel(PagedArgs 
 #pragma unroll
           for (uint32_t e = 0; e < 4; ++e) {
             const int32_t key = key0 + (int32_t)(16u * t + 4u * c + e);
-            const bool seen = key <= pos[n] && key >= low[n] && key < key_end && ids[t] < a.pages;
+            const bool seen = key <= pos[n] && key >= low[n] && key < key_end && !(hole >> t & 1u);
             x[n][t][e] = seen ? x[n][t][e] : -INFINITY;
           }
       }
       float top = x[n][0][0];
 #pragma unroll
-      for (uint32_t t = 0; t < kKT; ++t)
-#pragma unroll
-        for (uint32_t e = 0; e < 4; ++e) top = fmaxf(top, x[n][t][e]);
+      for (uint32_t t = 0; t < kKT; ++t) top = fmaxf(fmaxf(fmaxf(x[n][t][0], x[n][t][1]), top), fmaxf(x[n][t][2], x[n][t][3]));
+      top *= scale2;
       if (__ballot(top > m[n] + kSlack)) {
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
@@ -248,7 +318,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void paged_decode_kernel(PagedArgs 
         for (uint32_t b = 0; b < kDB; ++b) o[n][b] *= keep;
       }
       const float base = m[n] == -INFINITY ? 0.0f : m[n];
-      // weights, as the sum of two bf16: one would be off by 2^-9 of each weight
+      // weights, as the sum of two bf16: one would be off by 2^-8 of each weight
       uint32_t hi[kKT][2], lo[kKT][2];
 #pragma unroll
       for (uint32_t t = 0; t < kKT; ++t) {
@@ -256,7 +326,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void paged_decode_kernel(PagedArgs 
 #pragma unroll
         for (uint32_t e = 0; e < 4; ++e) {
           const float s = x[n][t][e];
-          w[e] = exp2_hw(s - base);
+          w[e] = exp2_hw(fmaf(s, scale2, -base));
           l[n] += w[e];
           if constexpr (kBits == 8u) w[e] = s == -INFINITY ? 0.0f : w[e] * vs[t][e];
         }
@@ -268,7 +338,6 @@ __global__ __launch_bounds__(64 * kWaves, 1) void paged_decode_kernel(PagedArgs 
       }
       // to the lanes that hold the keys' values: lanes of group c have keys 4 c.. of
       // every tile, and want the keys of their unit
-      v4u ph[kHalves], pl[kHalves];
       auto turn = [&](uint32_t (&w)[kKT][2], v4u *out) {
 #pragma unroll
         for (uint32_t e = 0; e < 2; ++e) {
@@ -289,52 +358,58 @@ __global__ __launch_bounds__(64 * kWaves, 1) void paged_decode_kernel(PagedArgs 
           }
         }
       };
-      turn(hi, ph);
-      turn(lo, pl);
+      turn(hi, ph[n]);
+      turn(lo, pl[n]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kBits == 16u) {
       bool bad = false;
-      if constexpr (kBits == 16u) {
-        if (!whole) {
+      if (!whole) {
 #pragma unroll
-          for (uint32_t b = 0; b < kDB; ++b) bad |= any_not_finite(v[b]);
-          bad = __ballot(bad) != 0u;
-        }
+        for (uint32_t b = 0; b < kDB; ++b) bad |= any_not_finite(v[b]);
+        bad = __ballot(bad) != 0u;
       }
-      if (!bad) {
+      if (bad) {
+        // A NaN or an infinity among the values of a step that not every row sees
+        // whole: 0 * NaN must not reach the rows that do not see its key.  It is
+        // added here where it is seen, and counts as zero in the product.
+        v4u ones[kNT];  // 1 for the unit's keys that a row sees
+#pragma unroll
+        for (uint32_t n = 0; n < kNT; ++n) {
+          const int32_t at = key0 + (int32_t)(8u * c), from = max(low[n] - at, 0), to = min(min(pos[n], key_end - 1) - at, 7);
+          const uint32_t seen = hole >> (c / 2u) & 1u || from > to ? 0u : (0xFFu >> (7 - to)) & (0xFFu << from);
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i)
+            ones[n][i] = (seen >> (2u * i) & 1u ? 0x3F80u : 0u) | (seen >> (2u * i + 1u) & 1u ? 0x3F800000u : 0u);
+        }
 #pragma unroll
         for (uint32_t b = 0; b < kDB; ++b) {
-          if (16u * b >= a.d) continue;
+          asm volatile("" : "+v"(v[b]));  // (keeps this a branch)
+          const v4u mark = not_finite_marks(v[b]);
+          v[b] = finite_only(v[b]);
 #pragma unroll
-          for (uint32_t h = 0; h < kHalves; ++h) {
-            const v8bf vv = as_bf(kBits == 16u ? v[b] : bf16_of_codes(v[b][2 * h], v[b][2 * h + 1]));
-            o[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, as_bf(ph[h]), o[n][b], 0, 0, 0);
-            o[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, as_bf(pl[h]), o[n][b], 0, 0, 0);
+          for (uint32_t n = 0; n < kNT; ++n) {
+            v4f marks = {0, 0, 0, 0};
+            marks = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(mark), as_bf(ones[n]), marks, 0, 0, 0);
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) o[n][b][i] += of_marks(marks[i]);
           }
-        }
-      } else {
-        // A NaN or an infinity among the values of a step that not every row sees
-        // whole: 0 * NaN must not reach the rows that do not see its key.  One
-        // key at a time, added where it is seen.
-        for (uint32_t key = 0; key < kKeys; ++key) {
-          const uint32_t e = key % 8u;
-          const bool here = c == key / 8u;
-          const int32_t place = key0 + (int32_t)key;
-          const bool seen = place <= pos[n] && place >= low[n] && place < key_end && ids[key / 16u] < a.pages;
-          const uint32_t keep = here ? (e & 1u ? 0xFFFF0000u : 0xFFFFu) : 0u;
-          v4u sel;
-#pragma unroll
-          for (uint32_t i = 0; i < 4; ++i) sel[i] = e / 2u == i ? keep : 0u;
-#pragma unroll
-          for (uint32_t b = 0; b < kDB; ++b) {
-            if (16u * b >= a.d) continue;
-            v4f one = {0, 0, 0, 0};
-            one = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(v[b] & sel), as_bf(ph[0] & sel), one, 0, 0, 0);
-            one = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(v[b] & sel), as_bf(pl[0] & sel), one, 0, 0, 0);
-#pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) o[n][b][i] += seen ? one[i] : 0.0f;
-          }
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
+#pragma unroll
+    for (uint32_t b = 0; b < kDB; ++b)
+#pragma unroll
+      for (uint32_t h = 0; h < kHalves; ++h) {
+        const v4u u = kBits == 16u ? v[b] : bf16_of_codes(v[b][2 * h], v[b][2 * h + 1]);
+#pragma unroll
+        for (uint32_t n = 0; n < kNT; ++n) {
+          o[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(u), as_bf(ph[n][h]), o[n][b], 0, 0, 0);
+          o[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(u), as_bf(pl[n][h]), o[n][b], 0, 0, 0);
+        }
+        if constexpr (kBits == 8u) __builtin_amdgcn_sched_barrier(0);
+      }
   }
 
   // the waves' results, two and two
@@ -384,10 +459,10 @@ __global__ __launch_bounds__(64 * kWaves, 1) void paged_decode_kernel(PagedArgs 
     if (row >= job.rows) continue;
     if (runs == 1u) {
       const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
-      uint16_t *to = a.out + ((uint64_t)(p.first + row / g) * a.hq + head * g + row % g) * a.d;
+      uint16_t *to = a.out + ((uint64_t)(p.first + row / g) * a.hq + head * g + row % g) * d;
 #pragma unroll
       for (uint32_t b = 0; b < kDB; ++b)
-        if (16u * b < a.d)
+        if (16u * b < d)
           *reinterpret_cast<uint2 *>(to + 16u * b + 4u * c) =
               make_uint2(pack_bf16x2(o[n][b][0] * inv, o[n][b][1] * inv), pack_bf16x2(o[n][b][2] * inv, o[n][b][3] * inv));
     } else {
@@ -395,7 +470,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void paged_decode_kernel(PagedArgs 
       if (c == 0u) stats[at] = make_float2(m[n], l[n]);
 #pragma unroll
       for (uint32_t b = 0; b < kDB; ++b)
-        if (16u * b < a.d) *reinterpret_cast<v4f *>(sums + at * a.d + 16u * b + 4u * c) = o[n][b];
+        if (16u * b < d) *reinterpret_cast<v4f *>(sums + at * d + 16u * b + 4u * c) = o[n][b];
     }
   }
 }
@@ -490,19 +565,19 @@ Plan plan_of(uint32_t tokens, uint32_t count, uint32_t hq, uint32_t hk, uint32_t
   const uint32_t g = hq / hk;
   const uint64_t rows = (uint64_t)tokens * g, mean = (rows + count - 1u) / count;
   Plan p;
-  p.blocks = mean <= 16u ? 1u : mean <= 32u || d > 128u ? 2u : 4u;
+  p.blocks = mean <= 16u ? 1u : 2u;
   const uint32_t tile = 16u * p.blocks;
   // (of a sequence with rows: at most one tile that is not full)
   p.tiles = (uint32_t)std::min<uint64_t>(rows / tile + std::min(count, tokens), (uint64_t)tokens * ((g + tile - 1u) / tile));
-  p.slots = std::max(2u * p.tiles, kTarget / hk);
+  p.slots = p.tiles + std::max(kTarget / hk, std::min(4u * p.tiles, 4u * kTarget / hk)) + 1u;
   return p;
 }
 
-template <uint32_t kDP, uint32_t kBits, uint32_t kNT>
+template <uint32_t kDP, uint32_t kBits, uint32_t kNT, bool kExact>
 hipError_t launch(const PagedArgs &a, const Plan &plan, bool cut, hipStream_t s) {
   const Parts parts = parts_of(a.workspace, plan.slots, a.hk, 16u * kNT, a.d);
-  constexpr uint32_t kLds = (kWaves / 2u) * 16u * kNT * ((kDP + 4u) * 4u + 8u);
-  auto *kernel = paged_decode_kernel<kDP, kBits, kNT>;
+  constexpr uint32_t kLds = (kWaves / 2u) * 16u * kNT * ((kDP + 4u) * 4u + 8u);  // (more than a shared q takes)
+  auto *kernel = paged_decode_kernel<kDP, kBits, kNT, kExact>;
   if (kLds > 65536u) {
     const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void *>(kernel), (int)kLds);
     if (e != hipSuccess) return e;
@@ -518,10 +593,16 @@ hipError_t launch(const PagedArgs &a, const Plan &plan, bool cut, hipStream_t s)
 
 template <uint32_t kDP, uint32_t kBits>
 hipError_t launch_rows(const PagedArgs &a, const Plan &plan, bool cut, hipStream_t s) {
-  if (plan.blocks == 1u) return launch<kDP, kBits, 1>(a, plan, cut, s);
-  if constexpr (kDP <= 128u)
-    if (plan.blocks == 4u) return launch<kDP, kBits, 4>(a, plan, cut, s);
-  return launch<kDP, kBits, 2>(a, plan, cut, s);
+  if (plan.blocks == 1u) return a.d == kDP ? launch<kDP, kBits, 1, true>(a, plan, cut, s) : launch<kDP, kBits, 1, false>(a, plan, cut, s);
+  return a.d == kDP ? launch<kDP, kBits, 2, true>(a, plan, cut, s) : launch<kDP, kBits, 2, false>(a, plan, cut, s);
+}
+
+template <uint32_t kBits>
+hipError_t launch_heads(const PagedArgs &a, const Plan &plan, bool cut, hipStream_t s) {
+  if (a.d <= 64u) return launch_rows<64, kBits>(a, plan, cut, s);
+  if (a.d <= 96u) return launch_rows<96, kBits>(a, plan, cut, s);
+  if (a.d <= 128u) return launch_rows<128, kBits>(a, plan, cut, s);
+  return launch_rows<256, kBits>(a, plan, cut, s);
 }
 
 }  // namespace
@@ -530,20 +611,19 @@ hipError_t launch_paged_decode(const PagedArgs &a, hipStream_t s) {
   const Plan plan = plan_of(a.tokens, a.count, a.hq, a.hk, a.d);
   // no sequence can be longer than a run: nothing to join
   const bool cut = ((uint64_t)a.width << a.page_shift) > kLeast * kBlock;
-  if (a.bits == 16u)
-    return a.d <= 64u ? launch_rows<64, 16>(a, plan, cut, s) : a.d <= 128u ? launch_rows<128, 16>(a, plan, cut, s) : launch_rows<256, 16>(a, plan, cut, s);
-  return a.d <= 64u ? launch_rows<64, 8>(a, plan, cut, s) : a.d <= 128u ? launch_rows<128, 8>(a, plan, cut, s) : launch_rows<256, 8>(a, plan, cut, s);
+  return a.bits == 16u ? launch_heads<16>(a, plan, cut, s) : launch_heads<8>(a, plan, cut, s);
 }
 
-// For a call of at most these sizes: two slots a tile, or the target's.  Tiles of
-// 32 and 64 rows are taken where sequences have over half as many, so that all
-// tiles have at most 3 times the rows.
+// For a call of at most these sizes: five slots a tile, or one and the target's.
+// Tiles of 32 rows are taken where sequences have over half as many on average,
+// so that all of them have at most 3 times the rows.
 uint64_t paged_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hq, uint32_t hk, uint32_t d) {
   if (tokens == 0u || count == 0u) return 0;
-  const uint64_t g = hq / hk, rows = tokens * g, most = d > 128u ? 32u : 64u;
+  const uint64_t g = hq / hk, rows = tokens * g;
   const uint64_t narrow = std::min<uint64_t>(rows + 16ull * std::min(count, tokens), tokens * 16ull * ((g + 15u) / 16u));
-  const uint64_t all = std::max(2u * std::max(3u * rows, narrow), std::max<uint64_t>(kTarget / hk, 1u) * most);
-  return all * hk * (4ull * d + 8u);
+  const uint64_t all = std::max(3u * rows, narrow);
+  const uint64_t slots = all + std::max<uint64_t>(kTarget / hk * 32u, std::min<uint64_t>(4u * all, 4u * kTarget / hk * 32u)) + 32u;
+  return slots * hk * (4ull * d + 8u);
 }
 
 uint64_t paged_workspace_needed(uint32_t tokens, uint32_t count, uint32_t hq, uint32_t hk, uint32_t d) {

@@ -180,6 +180,7 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
       for (uint32_t j = 0; j < kParts; ++j) {
         const uint32_t i = (wave + kWaves * j) * 64u + lane;
         const uint32_t ku = i / kKT, key = i % kKT, vg = i / kDP, dim = i % kDP;
+        asm volatile("" : "+v"(kr[j]), "+v"(vr[j]));  // (else every code is carried in a register of its own)
         if ((kExact && kFull) || ku * kUnit < d) {
           *reinterpret_cast<v4u *>(to + (2u * ku * kKT + key) * 16u) = bf16_of_codes(kr[j][0], kr[j][1]);
           *reinterpret_cast<v4u *>(to + ((2u * ku + 1u) * kKT + key) * 16u) = bf16_of_codes(kr[j][2], kr[j][3]);
@@ -336,16 +337,13 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
 #pragma unroll
         for (uint32_t b = 0; b < kDB; ++b) {
           const v4u u = *reinterpret_cast<const v4u *>(vt + (2u * t * kDP + 32u * b) * 16u);
-#pragma unroll 1
-          for (uint32_t kind = 0; kind < 3u; ++kind) {  // infinities, the negative ones, NaNs: how many are seen
-            v16f n;
+          v16f marks;
 #pragma unroll
-            for (uint32_t i = 0; i < 16; ++i) n[i] = 0.0f;
-            n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(ones_where(u, kind)), as_bf(ones), n, 0, 0, 0);
-            const float add = __uint_as_float(kind == 0u ? 0x7F800000u : kind == 1u ? 0xFF800000u : 0x7FC00000u);
+          for (uint32_t i = 0; i < 16; ++i) marks[i] = 0.0f;
+          marks = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(not_finite_marks(u)), as_bf(ones), marks, 0, 0, 0);
 #pragma unroll
-            for (uint32_t i = 0; i < 16; ++i) o[b][i] += n[i] != 0.0f ? add : 0.0f;
-          }
+          for (uint32_t i = 0; i < 16; ++i) o[b][i] += of_marks(marks[i]);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
