@@ -78,10 +78,15 @@ __host__ __device__ inline Parts parts_of(uint8_t *workspace, uint32_t slots, ui
 
 // ---- a run ------------------------------------------------------------------------
 
+// Waves of a SIMD that the registers are to suffice for.
+constexpr int waves_of(uint32_t dp, uint32_t bits, uint32_t nt) {
+  return dp > 128u ? 1 : bits == 16u ? (nt == 1u && dp <= 96u ? 3 : 2) : nt == 1u ? (dp <= 64u ? 3 : 2) : dp <= 64u ? 2 : 1;
+}
+
 // kDP: values of a head, rounded up (kExact: as they are); kNT: column blocks of 16
 // rows.
 template <uint32_t kDP, uint32_t kBits, uint32_t kNT, bool kExact>
-__global__ __launch_bounds__(64 * kWaves, kDP * kNT <= (kBits == 16 ? 256 : 128) && kDP <= 128 ? 2 : 1) void paged_decode_kernel(PagedArgs a, uint32_t slots, float *sums, float2 *stats) {
+__global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits, kNT)) void paged_decode_kernel(PagedArgs a, uint32_t slots, float *sums, float2 *stats) {
   constexpr uint32_t kUnit = 128u / kBits;        // values of a unit
   constexpr uint32_t kKeys = kUnit * 4u;          // keys of a step: a unit of v for each group of 16 lanes
   constexpr uint32_t kKT = kKeys / 16u;           // their tiles
@@ -140,12 +145,15 @@ __global__ __launch_bounds__(64 * kWaves, kDP * kNT <= (kBits == 16 ? 256 : 128)
     if constexpr (kShared) return *reinterpret_cast<const v4u *>(lds + ((n * kKS * kHalves + i) * 64u + lane) * 16u);
     return q[n][i];
   };
-  // where all of the tile's rows see a key: [all_low, all_pos]
-  int32_t all_pos, all_low;
+  // keys that all of the tile's rows see lie in [all_low, all_pos], those that any
+  // does in [any_low, any_pos]
+  int32_t all_pos, all_low, any_pos, any_low;
   {
     const uint32_t row0 = tile * kRows, row1 = min(row0 + kRows, job.rows) - 1u;
     all_pos = p.at + (int32_t)(row0 / g);
-    all_low = a.window ? (int32_t)max((int64_t)p.at + (int64_t)(row1 / g) + 1 - (int64_t)a.window, (int64_t)0) : 0;
+    any_pos = p.at + (int32_t)(row1 / g);
+    any_low = a.window ? (int32_t)max((int64_t)all_pos + 1 - (int64_t)a.window, (int64_t)0) : 0;
+    all_low = a.window ? (int32_t)max((int64_t)any_pos + 1 - (int64_t)a.window, (int64_t)0) : 0;
   }
 
   // scores base 2 are scale2 times the products; under a cap they are made of them at once
@@ -168,7 +176,7 @@ __global__ __launch_bounds__(64 * kWaves, kDP * kNT <= (kBits == 16 ? 256 : 128)
   // A step: 32 keys (int8: 64).  Values are on their way while the scores are made,
   // the next step's keys while the softmax is.
   constexpr int32_t kStride = (int32_t)(kWaves * kKeys);
-  auto ids_of = [&](int32_t key0, uint32_t (&ids)[kKT]) {  // the pages of its tiles of 16 keys
+  auto ids_of = [&](int32_t key0, v4u &ids) {  // the pages of its tiles of 16 keys
 #pragma unroll
     for (uint32_t t = 0; t < kKT; ++t) {
       const uint32_t at = (uint32_t)(key0 + (int32_t)(16u * t)) >> a.page_shift;
@@ -177,7 +185,7 @@ __global__ __launch_bounds__(64 * kWaves, kDP * kNT <= (kBits == 16 ? 256 : 128)
   };
   v4u k[kKT][kKS];
   v4f ks[kKT];
-  auto load_k = [&](int32_t key0, const uint32_t (&ids)[kKT]) {
+  auto load_k = [&](int32_t key0, const v4u &ids) {
 #pragma unroll
     for (uint32_t t = 0; t < kKT; ++t) {
       const uint32_t id = ids[t] < a.pages ? ids[t] : 0u, off = (uint32_t)(key0 + (int32_t)(16u * t)) & (page - 1u);
@@ -196,44 +204,31 @@ __global__ __launch_bounds__(64 * kWaves, kDP * kNT <= (kBits == 16 ? 256 : 128)
     }
   };
 
-  uint32_t ids[kKT], next_ids[kKT];
-  int32_t key0 = key_begin + (int32_t)(wave * kKeys);
-  if (key0 < key_end) {
-    ids_of(key0, ids);
-    load_k(key0, ids);
-    ids_of(key0 + kStride, next_ids);
-  }
-  for (; key0 < key_end; key0 += kStride) {
-    uint32_t hole = 0;  // bit t: the step's keys 16 t.. lie in no page
+  v4u v[kDB];  // unit of keys 8 c.. or 16 c.. of the step
+  v4f vs[kKT];
+  auto load_v = [&](int32_t key0, const v4u &ids) {
+    const uint32_t t = c * kUnit / 16u;
+    uint32_t id = ids[0];
 #pragma unroll
-    for (uint32_t t = 0; t < kKT; ++t) hole |= ids[t] >= a.pages ? 1u << t : 0u;
-    // values: unit of keys 8 c.. or 16 c.. of the step
-    v4u v[kDB];
-    v4f vs[kKT];
-    {
-      const uint32_t t = c * kUnit / 16u;
-      uint32_t id = ids[0];
+    for (uint32_t i = 1; i < kKT; ++i) id = t == i ? ids[i] : id;
+    id = id < a.pages ? id : 0u;
+    const uint32_t off = (uint32_t)(key0 + (int32_t)(c * kUnit)) & (page - 1u);
+    const uint8_t *base = vc + id * page_bytes + ((uint64_t)(off / kUnit) * d + r) * 16u;
 #pragma unroll
-      for (uint32_t i = 1; i < kKT; ++i) id = t == i ? ids[i] : id;
-      id = id < a.pages ? id : 0u;
-      const uint32_t off = (uint32_t)(key0 + (int32_t)(c * kUnit)) & (page - 1u);
-      const uint8_t *base = vc + id * page_bytes + ((uint64_t)(off / kUnit) * d + r) * 16u;
+    for (uint32_t b = 0; b < kDB; ++b) {
+      // (beyond the head's values: the first again, whose sums are not taken)
+      v[b] = *reinterpret_cast<const v4u *>(base + (kExact || 16u * b < d ? b : 0u) * 256u);
+    }
+    if constexpr (kBits == 8u) {
 #pragma unroll
-      for (uint32_t b = 0; b < kDB; ++b) {
-        // (beyond the head's values: the first again, whose sums are not taken)
-        v[b] = *reinterpret_cast<const v4u *>(base + (kExact || 16u * b < d ? b : 0u) * 256u);
-      }
-      if constexpr (kBits == 8u) {
-#pragma unroll
-        for (uint32_t i = 0; i < kKT; ++i) {
-          const uint32_t at = ids[i] < a.pages ? ids[i] : 0u, to = (uint32_t)(key0 + (int32_t)(16u * i)) & (page - 1u);
-          vs[i] = *reinterpret_cast<const v4f *>(vc + at * page_bytes + page * d + (to + 4u * c) * 4u);
-        }
+      for (uint32_t i = 0; i < kKT; ++i) {
+        const uint32_t at = ids[i] < a.pages ? ids[i] : 0u, to = (uint32_t)(key0 + (int32_t)(16u * i)) & (page - 1u);
+        vs[i] = *reinterpret_cast<const v4f *>(vc + at * page_bytes + page * d + (to + 4u * c) * 4u);
       }
     }
-    __builtin_amdgcn_sched_barrier(0);
-    // scores
-    v4f x[kNT][kKT];
+  };
+  v4f x[kNT][kKT];
+  auto scores = [&] {
 #pragma unroll
     for (uint32_t t = 0; t < kKT; ++t)
 #pragma unroll
@@ -276,15 +271,11 @@ __global__ __launch_bounds__(64 * kWaves, kDP * kNT <= (kBits == 16 ? 256 : 128)
 #pragma unroll
         for (uint32_t t = 0; t < kKT; ++t) x[n][t] *= ks[t];
     }
-    __builtin_amdgcn_sched_barrier(0);
-    if (key0 + kStride < key_end) load_k(key0 + kStride, next_ids);
-#pragma unroll
-    for (uint32_t t = 0; t < kKT; ++t) ids[t] = next_ids[t];
-    ids_of(key0 + 2 * kStride, next_ids);
-    __builtin_amdgcn_sched_barrier(0);
-
-    const bool whole = !hole && key0 + (int32_t)kKeys - 1 <= all_pos && key0 >= all_low && key0 + (int32_t)kKeys <= key_end;
-    v4u ph[kNT][kHalves], pl[kNT][kHalves];  // the weights
+  };
+  // scores to weights, where the lanes' units of v want them.  hole: bit t where the
+  // step's keys 16 t.. lie in no page; whole: all rows see all keys.
+  v4u ph[kNT][kHalves], pl[kNT][kHalves];
+  auto weigh = [&](int32_t key0, uint32_t hole, bool whole) {
 #pragma unroll
     for (uint32_t n = 0; n < kNT; ++n) {
       if (a.cap != 0.0f) {
@@ -318,7 +309,7 @@ __global__ __launch_bounds__(64 * kWaves, kDP * kNT <= (kBits == 16 ? 256 : 128)
         for (uint32_t b = 0; b < kDB; ++b) o[n][b] *= keep;
       }
       const float base = m[n] == -INFINITY ? 0.0f : m[n];
-      // weights, as the sum of two bf16: one would be off by 2^-8 of each weight
+      // the sum of two bf16: one would be off by 2^-8 of each weight
       uint32_t hi[kKT][2], lo[kKT][2];
 #pragma unroll
       for (uint32_t t = 0; t < kKT; ++t) {
@@ -336,8 +327,7 @@ __global__ __launch_bounds__(64 * kWaves, kDP * kNT <= (kBits == 16 ? 256 : 128)
           lo[t][e] = two_bf16(w[2 * e] - __uint_as_float(hi[t][e] << 16), w[2 * e + 1] - __uint_as_float(hi[t][e] & 0xFFFF0000u));
         }
       }
-      // to the lanes that hold the keys' values: lanes of group c have keys 4 c.. of
-      // every tile, and want the keys of their unit
+      // lanes of group c have keys 4 c.. of every tile, and want the keys of their unit
       auto turn = [&](uint32_t (&w)[kKT][2], v4u *out) {
 #pragma unroll
         for (uint32_t e = 0; e < 2; ++e) {
@@ -361,43 +351,8 @@ __global__ __launch_bounds__(64 * kWaves, kDP * kNT <= (kBits == 16 ? 256 : 128)
       turn(hi, ph[n]);
       turn(lo, pl[n]);
     }
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (kBits == 16u) {
-      bool bad = false;
-      if (!whole) {
-#pragma unroll
-        for (uint32_t b = 0; b < kDB; ++b) bad |= any_not_finite(v[b]);
-        bad = __ballot(bad) != 0u;
-      }
-      if (bad) {
-        // A NaN or an infinity among the values of a step that not every row sees
-        // whole: 0 * NaN must not reach the rows that do not see its key.  It is
-        // added here where it is seen, and counts as zero in the product.
-        v4u ones[kNT];  // 1 for the unit's keys that a row sees
-#pragma unroll
-        for (uint32_t n = 0; n < kNT; ++n) {
-          const int32_t at = key0 + (int32_t)(8u * c), from = max(low[n] - at, 0), to = min(min(pos[n], key_end - 1) - at, 7);
-          const uint32_t seen = hole >> (c / 2u) & 1u || from > to ? 0u : (0xFFu >> (7 - to)) & (0xFFu << from);
-#pragma unroll
-          for (uint32_t i = 0; i < 4; ++i)
-            ones[n][i] = (seen >> (2u * i) & 1u ? 0x3F80u : 0u) | (seen >> (2u * i + 1u) & 1u ? 0x3F800000u : 0u);
-        }
-#pragma unroll
-        for (uint32_t b = 0; b < kDB; ++b) {
-          asm volatile("" : "+v"(v[b]));  // (keeps this a branch)
-          const v4u mark = not_finite_marks(v[b]);
-          v[b] = finite_only(v[b]);
-#pragma unroll
-          for (uint32_t n = 0; n < kNT; ++n) {
-            v4f marks = {0, 0, 0, 0};
-            marks = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(mark), as_bf(ones[n]), marks, 0, 0, 0);
-#pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) o[n][b][i] += of_marks(marks[i]);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-    }
+  };
+  auto add_products = [&] {
 #pragma unroll
     for (uint32_t b = 0; b < kDB; ++b)
 #pragma unroll
@@ -410,6 +365,96 @@ __global__ __launch_bounds__(64 * kWaves, kDP * kNT <= (kBits == 16 ? 256 : 128)
         }
         if constexpr (kBits == 8u) __builtin_amdgcn_sched_barrier(0);
       }
+  };
+  // Of a unit's eight keys (bf16), those in [from, to] that lie in a page: bit e.
+  auto seen_in = [&](int32_t key0, uint32_t hole, int32_t from, int32_t to) {
+    const int32_t at = key0 + (int32_t)(8u * c), lo = max(from - at, 0), hi = min(min(to, key_end - 1) - at, 7);
+    return hole >> (c / 2u) & 1u || lo > hi ? 0u : (0xFFu >> (7 - hi)) & (0xFFu << lo);
+  };
+  auto holes_of = [&](const v4u &ids) {
+    uint32_t hole = 0;
+#pragma unroll
+    for (uint32_t t = 0; t < kKT; ++t) hole |= ids[t] >= a.pages ? 1u << t : 0u;
+    return hole;
+  };
+  // 0 * NaN must not reach a row that does not see the NaN's key.  Codes are finite;
+  // of bf16, values that no row sees count as zero, and steps with keys that some
+  // rows see and others do not are left for the second loop.
+  auto mixed = [&](int32_t key0) {
+    const int32_t last = key0 + (int32_t)kKeys - 1;
+    return kBits == 16u && ((any_low < all_low && key0 < all_low && last >= any_low) || (all_pos < any_pos && key0 <= any_pos && last > all_pos));
+  };
+
+  v4u ids, next_ids;
+  const int32_t key_first = key_begin + (int32_t)(wave * kKeys);
+  if (key_first < key_end) {
+    ids_of(key_first, ids);
+    load_k(key_first, ids);
+    ids_of(key_first + kStride, next_ids);
+  }
+  for (int32_t key0 = key_first; key0 < key_end; key0 += kStride) {
+    const uint32_t hole = holes_of(ids);
+    load_v(key0, ids);
+    __builtin_amdgcn_sched_barrier(0);
+    scores();
+    __builtin_amdgcn_sched_barrier(0);
+    if (key0 + kStride < key_end) load_k(key0 + kStride, next_ids);
+    ids = next_ids;
+    ids_of(key0 + 2 * kStride, next_ids);
+    __builtin_amdgcn_sched_barrier(0);
+    if (mixed(key0)) continue;
+    const bool whole = !hole && key0 + (int32_t)kKeys - 1 <= all_pos && key0 >= all_low && key0 + (int32_t)kKeys <= key_end;
+    weigh(key0, hole, whole);
+    if (kBits == 16u && !whole) {
+      uint32_t seen = seen_in(key0, hole, any_low, any_pos);
+      asm volatile("" : "+v"(seen));  // (keeps this a branch)
+      v4u mask;
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) mask[i] = (seen >> (2u * i) & 1u ? 0xFFFFu : 0u) | (seen >> (2u * i + 1u) & 1u ? 0xFFFF0000u : 0u);
+#pragma unroll
+      for (uint32_t b = 0; b < kDB; ++b) v[b] &= mask;
+    }
+    add_products();
+  }
+  if constexpr (kBits == 16u) {
+    if (any_low < all_low || all_pos < any_pos) {
+#pragma unroll 1
+      for (int32_t key0 = key_first; key0 < key_end; key0 += kStride) {
+        if (!mixed(key0)) continue;
+        ids_of(key0, ids);
+        const uint32_t hole = holes_of(ids);
+        load_k(key0, ids);
+        load_v(key0, ids);
+        scores();
+        __builtin_amdgcn_sched_barrier(0);
+        weigh(key0, hole, false);
+        bool bad = false;
+#pragma unroll
+        for (uint32_t b = 0; b < kDB; ++b) bad |= any_not_finite(v[b]);
+        if (__ballot(bad)) {
+          // a NaN or an infinity is added where it is seen, and counts as zero in the product
+#pragma unroll
+          for (uint32_t b = 0; b < kDB; ++b) {
+            const v4u mark = not_finite_marks(v[b]);
+            v[b] = finite_only(v[b]);
+#pragma unroll
+            for (uint32_t n = 0; n < kNT; ++n) {
+              const uint32_t seen = seen_in(key0, hole, low[n], pos[n]);
+              v4u ones;
+#pragma unroll
+              for (uint32_t i = 0; i < 4; ++i)
+                ones[i] = (seen >> (2u * i) & 1u ? 0x3F80u : 0u) | (seen >> (2u * i + 1u) & 1u ? 0x3F800000u : 0u);
+              v4f marks = {0, 0, 0, 0};
+              marks = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(mark), as_bf(ones), marks, 0, 0, 0);
+#pragma unroll
+              for (uint32_t i = 0; i < 4; ++i) o[n][b][i] += of_marks(marks[i]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        add_products();
+      }
+    }
   }
 
   // the waves' results, two and two

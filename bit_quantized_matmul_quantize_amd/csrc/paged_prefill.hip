@@ -109,14 +109,14 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
     __syncthreads();
   }
 
-  auto ids_of = [&](int32_t key0, uint32_t (&ids)[kSubs]) {
+  auto ids_of = [&](int32_t key0, v4u &ids) {
 #pragma unroll
     for (uint32_t t = 0; t < kSubs; ++t) {
       const uint32_t at = (uint32_t)(key0 + (int32_t)(16u * t)) >> a.page_shift;
       ids[t] = __builtin_amdgcn_readfirstlane(at < a.width ? (uint32_t)table[at] : ~0u);
     }
   };
-  auto pick = [&](const uint32_t (&ids)[kSubs], uint32_t sub) {
+  auto pick = [&](const v4u &ids, uint32_t sub) {
     uint32_t id = ids[0];
 #pragma unroll
     for (uint32_t t = 1; t < kSubs; ++t) id = sub == t ? ids[t] : id;
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
   constexpr bool kFull = kParts * kThreads * 16 == S::kTile * kBits / 16;  // every thread has a unit in every part
   v4u kr[kBits == 8 ? kParts : 1], vr[kBits == 8 ? kParts : 1];
   float scale_r = 0.0f;
-  auto bring = [&](int32_t key0, const uint32_t (&ids)[kSubs], uint32_t stage) {
+  auto bring = [&](int32_t key0, const v4u &ids, uint32_t stage) {
     const uint32_t off0 = (uint32_t)key0 & (page - 1u);
     const bool one_page = kExact || page >= kKT;
     const uint32_t id0 = ids[0] < a.pages ? ids[0] : 0u;
@@ -349,7 +349,7 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
     }
   };
 
-  uint32_t ids[kSubs], next_ids[kSubs];
+  v4u ids, next_ids;
   ids_of(begin, ids);
   if (begin < end) bring(begin, ids, 0);
   settle(0);
@@ -364,8 +364,7 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
     for (uint32_t t = 0; t < kSubs; ++t) hole |= ids[t] >= a.pages ? 1u << t : 0u;
     const bool more = key0 + (int32_t)kKT < end;
     if (more) bring(key0 + (int32_t)kKT, next_ids, stage ^ 1u);
-#pragma unroll
-    for (uint32_t t = 0; t < kSubs; ++t) ids[t] = next_ids[t];
+    ids = next_ids;
     ids_of(key0 + 2 * (int32_t)kKT, next_ids);
     if (key0 < any_end && key0 + (int32_t)kKT > any_low)
       compute(key0, stage, hole, !hole && key0 >= whole_low && key0 + (int32_t)kKT <= whole_end);
