@@ -207,8 +207,7 @@ hipError_t launch_paged_write(const PagedArgs &a, hipStream_t s);
 hipError_t launch_paged_read(const PagedArgs &a, hipStream_t s);
 hipError_t launch_paged_decode(const PagedArgs &a, hipStream_t s);
 hipError_t launch_paged_prefill(const PagedArgs &a, hipStream_t s);
-// of the decoding form: for these sizes, and for these and every smaller tokens and count
-uint64_t paged_workspace_needed(uint32_t tokens, uint32_t count, uint32_t hq, uint32_t hk, uint32_t d);
-uint64_t paged_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hq, uint32_t hk, uint32_t d);
+// of the decoding form, for any tokens
+uint64_t paged_workspace_bytes(uint32_t hk, uint32_t d);
 
 }  // namespace bqmm

@@ -842,7 +842,7 @@ int check_attention(const char *name, bqmm::PagedArgs &a, uint32_t page, bool *n
   REQUIRE(a.scale >= 0.0f && a.scale <= 1e30f, BQ_EINVAL, "%s: scale=%g must be a number >= 0", name, (double)a.scale);
   REQUIRE(a.cap == 0.0f || (a.cap >= 1e-20f && a.cap <= 1e20f), BQ_EINVAL, "%s: cap=%g must be 0 or 1e-20 to 1e20", name, (double)a.cap);
   REQUIRE(a.window <= kMaxPlaces, BQ_EINVAL, "%s: window=%u too large", name, a.window);
-  // rows of a key head, and workgroups of up to 256 threads, two slots of the workspace a tile
+  // rows of a key head, and workgroups of up to 512 threads
   REQUIRE((uint64_t)a.tokens * (a.hq / a.hk) < (1ull << 30) &&
               (uint64_t)a.hk * std::min<uint64_t>((uint64_t)a.tokens * (a.hq / a.hk), (uint64_t)a.tokens * (a.hq / a.hk) / 16u + a.count) < (1ull << 22) &&
               (uint64_t)a.tokens * a.hq < (1ull << 24),
@@ -956,7 +956,7 @@ uint64_t paged_attention_workspace_bytes(uint32_t tokens, uint32_t count, uint32
   if (hk == 0 || hk > 65535u || hq == 0 || hq > 65535u || hq % hk != 0 || d < 16u || d > 256u || d % 16u != 0 ||
       tokens > kMaxPlaces || count > kMaxPlaces || (uint64_t)tokens * hq >= (1ull << 24))
     return 0;
-  return bqmm::paged_workspace_bytes(tokens, count, hq, hk, d);
+  return bqmm::paged_workspace_bytes(hk, d);  // (the same for any tokens)
 }
 
 int paged_attention_decode(const void *q_bf16, const void *k_cache, const void *v_cache, void *out_bf16,
@@ -979,7 +979,11 @@ int paged_attention_decode(const void *q_bf16, const void *k_cache, const void *
   int st = check_attention(name, a, page, &nothing);
   if (st != BQ_OK) return st;
   if (nothing) return hip_status(hipSuccess, name);
-  const uint64_t need = bqmm::paged_workspace_needed(tokens, count, hq, hk, d);
+  // (the blocks of 64 keys of all tiles of 16 rows are counted in 32 bits)
+  const uint64_t rows = (uint64_t)tokens * (hq / hk), tiles = std::min<uint64_t>(rows, rows / 16u + count);
+  REQUIRE(tiles * (((uint64_t)width * page + 63u) / 64u) < (1ull << 31), BQ_EINVAL,
+          "%s: tokens=%u count=%u over a table of %u pages too large", name, tokens, count, width);
+  const uint64_t need = bqmm::paged_workspace_bytes(hk, d);
   REQUIRE(workspace, BQ_EINVAL, "%s: null workspace", name);
   REQUIRE(workspace_bytes >= need, BQ_EINVAL, "%s: the workspace holds %llu bytes, %llu are needed", name,
           (unsigned long long)workspace_bytes, (unsigned long long)need);

@@ -10,9 +10,11 @@
 // exchanges between the lanes of a wave turn these into the keys of a unit of v,
 // which O^T = V^T P^T takes as it lies.  No operand passes through LDS.
 //
-// Work: sequences are cut into runs of 64-key blocks, so that a launch of a
-// fixed size shares all keys of the call evenly, whatever the lengths are; the
-// runs' results are joined by a second launch.
+// Work: the 64-key blocks of all sequences form one row, which a launch of a fixed
+// size cuts into equal runs, whatever the lengths are: as many workgroups as the
+// device holds at once, each with one run that may end and begin inside a sequence.
+// What such a sequence's parts give is joined by a second launch.  Where the table
+// has room for short sequences only, a workgroup takes one, and nothing is joined.
 #include <algorithm>
 
 #include "paged_common.h"
@@ -20,14 +22,15 @@
 namespace bqmm {
 namespace {
 
-constexpr uint32_t kWaves = 4;
-constexpr uint32_t kBlock = 64;      // keys: the unit of the division of work
-constexpr uint32_t kLeast = 4;       // blocks of a run
-constexpr uint32_t kTarget = 1024;   // workgroups
+constexpr uint32_t kBlock = 64;   // keys: the unit of the division of work
+constexpr uint32_t kLeast = 4;    // blocks of a run
+constexpr uint32_t kShort = 1024; // keys: sequences of up to so many are not cut
+constexpr uint32_t kCus = 256;
 
 // ---- division of the work ------------------------------------------------------
 
-// Of sequence i: its blocks of rows, and the blocks of keys that any row sees.
+// Of sequence i: its tiles of rows, and the blocks of keys that any row sees (at
+// least one, so that rows that see none are written too).
 struct Job {
   uint32_t rows, tiles, blocks;
   int32_t first;  // the first of the blocks
@@ -37,42 +40,37 @@ __device__ __forceinline__ Job job_of(const PagedArgs &a, const PagedSpan &p, ui
   j.rows = p.n * (a.hq / a.hk);
   j.tiles = (j.rows + tile_rows - 1u) / tile_rows;
   const int32_t end = min(p.keys, max(p.at + (int32_t)p.n, 0));
-  const int32_t begin = a.window ? max((int32_t)min((int64_t)p.at + 1 - (int64_t)a.window, (int64_t)end), 0) : 0;
+  const int32_t begin = a.window ? max(min(p.at + 1 - (int32_t)a.window, end), 0) : 0;
   j.first = begin / (int32_t)kBlock;
-  j.blocks = j.tiles && end > begin ? (uint32_t)((end + (int32_t)kBlock - 1) / (int32_t)kBlock - j.first) : 0u;
+  j.blocks = max((uint32_t)((end + (int32_t)kBlock - 1) / (int32_t)kBlock - j.first), 1u);
   return j;
 }
 
-// The blocks of a run: the least with which all runs fit into `slots`.  Each
-// tile adds at most one run to the quotient of all blocks.
-__device__ __forceinline__ uint32_t run_blocks(const PagedArgs &a, uint32_t tile_rows, uint32_t slots) {
-  uint64_t blocks = 0;
-  uint32_t tiles = 0;
-  for (uint32_t base = 0; base < a.count; base += 64u) {
-    const uint32_t i = base + __lane_id();
-    if (i < a.count) {
-      const Job j = job_of(a, paged_span(a, i), tile_rows);
-      blocks += (uint64_t)j.tiles * j.blocks;
-      tiles += j.tiles;
-    }
+// The blocks of all jobs together.
+__device__ __forceinline__ uint32_t all_blocks(const PagedArgs &a, uint32_t tile_rows) {
+  uint32_t blocks = 0;
+  for (uint32_t i = __lane_id(); i < a.count; i += 64u) {
+    const Job j = job_of(a, paged_span(a, i), tile_rows);
+    blocks += j.tiles * j.blocks;
   }
+  if (a.count > 1u) {
 #pragma unroll
-  for (uint32_t d = 1; d < 64u; d *= 2u) {
-    blocks += ((uint64_t)(uint32_t)__shfl_xor((int)(blocks >> 32), (int)d, 64) << 32) + (uint32_t)__shfl_xor((int)(uint32_t)blocks, (int)d, 64);
-    tiles += (uint32_t)__shfl_xor((int)tiles, (int)d, 64);
+    for (uint32_t d = 1; d < 64u; d *= 2u) blocks += (uint32_t)__shfl_xor((int)blocks, (int)d, 64);
   }
-  const uint32_t spare = slots > tiles ? slots - tiles : 1u;
-  return max(kLeast, (uint32_t)((blocks + spare - 1u) / spare));
+  return __builtin_amdgcn_readfirstlane(blocks);
 }
 
-__device__ __forceinline__ uint32_t runs_of(const Job &j, uint32_t per) { return max(1u, (j.blocks + per - 1u) / per); }
+// A run: per blocks.
+__device__ __forceinline__ uint32_t run_blocks(uint32_t blocks, uint32_t slots) { return max(kLeast, (blocks + slots - 1u) / slots); }
 
+// A run leaves at most two parts of tiles: one that begins with it (0), and one that
+// ends with it (1).
 struct Parts {
-  float *sums;    // [slots][hk][tile_rows][d]
-  float2 *stats;  // [slots][hk][tile_rows]: maximum (base 2) and sum
+  float *sums;    // [slots][2][hk][tile_rows][d]
+  float2 *stats;  // [slots][2][hk][tile_rows]: maximum (base 2) and sum
 };
 __host__ __device__ inline Parts parts_of(uint8_t *workspace, uint32_t slots, uint32_t hk, uint32_t tile_rows, uint32_t d) {
-  const uint64_t rows = (uint64_t)slots * hk * tile_rows;
+  const uint64_t rows = 2ull * slots * hk * tile_rows;
   return {reinterpret_cast<float *>(workspace), reinterpret_cast<float2 *>(workspace + rows * d * 4u)};
 }
 
@@ -85,8 +83,10 @@ constexpr int waves_of(uint32_t dp, uint32_t bits, uint32_t nt) {
 
 // kDP: values of a head, rounded up (kExact: as they are); kNT: column blocks of 16
 // rows.
-template <uint32_t kDP, uint32_t kBits, uint32_t kNT, bool kExact>
-__global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits, kNT)) void paged_decode_kernel(PagedArgs a, uint32_t slots, float *sums, float2 *stats) {
+// kCut: a workgroup takes a run of blocks, else one tile of rows and its sequence.
+template <uint32_t kDP, uint32_t kBits, uint32_t kNT, bool kExact, uint32_t kWaves, bool kCut>
+__global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits, kNT)) void paged_decode_kernel(PagedArgs a, uint32_t slots,
+                                                                                             float *sums, float2 *stats) {
   constexpr uint32_t kUnit = 128u / kBits;        // values of a unit
   constexpr uint32_t kKeys = kUnit * 4u;          // keys of a step: a unit of v for each group of 16 lanes
   constexpr uint32_t kKT = kKeys / 16u;           // their tiles
@@ -100,18 +100,27 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits, kNT)) void paged_
   const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t r = lane & 15u, c = lane >> 4;
   const uint32_t slot = blockIdx.x / a.hk, head = blockIdx.x % a.hk, g = a.hq / a.hk;
-  const uint32_t per = run_blocks(a, kRows, slots);
+  uint32_t at_block = 0, end_block = 1, run_begin = 0;
+  if constexpr (kCut) {
+    const uint32_t all = all_blocks(a, kRows), per = run_blocks(all, slots);
+    if ((uint64_t)slot * per >= all) return;
+    run_begin = at_block = slot * per;
+    end_block = min(at_block + per, all);
+  }
+  while (at_block < end_block) {
   uint32_t seq, inside;
-  if (!paged_find(slot, a.count, [&](uint32_t i) {
+  if (!paged_find(kCut ? at_block : slot, a.count, [&](uint32_t i) {
         const Job j = job_of(a, paged_span(a, i), kRows);
-        return j.tiles ? j.tiles * runs_of(j, per) : 0u;
+        return kCut ? j.tiles * j.blocks : j.tiles;
       }, &seq, &inside))
     return;
   const PagedSpan p = paged_span(a, seq);
   const Job job = job_of(a, p, kRows);
-  const uint32_t runs = runs_of(job, per), tile = inside / runs, run = inside % runs;
-  const int32_t key_begin = (job.first + (int32_t)(run * per)) * (int32_t)kBlock;
-  const int32_t key_end = min((job.first + (int32_t)min((run + 1u) * per, job.blocks)) * (int32_t)kBlock, p.keys);
+  const uint32_t tile = kCut ? inside / job.blocks : inside, skip = kCut ? inside % job.blocks : 0u;
+  const uint32_t take = kCut ? min(job.blocks - skip, end_block - at_block) : job.blocks;
+  const int32_t key_begin = (job.first + (int32_t)skip) * (int32_t)kBlock;
+  const int32_t key_end = min((job.first + (int32_t)(skip + take)) * (int32_t)kBlock, p.keys);
+  if constexpr (kCut) __syncthreads();  // LDS of the last part has been read
 
   // this lane's rows: places, and the operand of q
   const uint32_t page = 1u << a.page_shift, d = kExact ? kDP : a.d, block = paged_block_bytes(page, d, kBits), units = d / kUnit;
@@ -497,26 +506,29 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits, kNT)) void paged_
       }
     }
   }
-  if (wave != 0u) return;
+  if (wave == 0u) {
 #pragma unroll
-  for (uint32_t n = 0; n < kNT; ++n) {
-    const uint32_t row = tile * kRows + n * 16u + r;
-    if (row >= job.rows) continue;
-    if (runs == 1u) {
-      const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
-      uint16_t *to = a.out + ((uint64_t)(p.first + row / g) * a.hq + head * g + row % g) * d;
+    for (uint32_t n = 0; n < kNT; ++n) {
+      const uint32_t row = tile * kRows + n * 16u + r;
+      if (row >= job.rows) continue;
+      if (!kCut || take == job.blocks) {
+        const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
+        uint16_t *to = a.out + ((uint64_t)(p.first + row / g) * a.hq + head * g + row % g) * d;
 #pragma unroll
-      for (uint32_t b = 0; b < kDB; ++b)
-        if (16u * b < d)
-          *reinterpret_cast<uint2 *>(to + 16u * b + 4u * c) =
-              make_uint2(pack_bf16x2(o[n][b][0] * inv, o[n][b][1] * inv), pack_bf16x2(o[n][b][2] * inv, o[n][b][3] * inv));
-    } else {
-      const uint64_t at = ((uint64_t)slot * a.hk + head) * kRows + n * 16u + r;
-      if (c == 0u) stats[at] = make_float2(m[n], l[n]);
+        for (uint32_t b = 0; b < kDB; ++b)
+          if (16u * b < d)
+            *reinterpret_cast<uint2 *>(to + 16u * b + 4u * c) =
+                make_uint2(pack_bf16x2(o[n][b][0] * inv, o[n][b][1] * inv), pack_bf16x2(o[n][b][2] * inv, o[n][b][3] * inv));
+      } else {
+        const uint64_t at = ((uint64_t)(2u * slot + (at_block != run_begin)) * a.hk + head) * kRows + n * 16u + r;
+        if (c == 0u) stats[at] = make_float2(m[n], l[n]);
 #pragma unroll
-      for (uint32_t b = 0; b < kDB; ++b)
-        if (16u * b < d) *reinterpret_cast<v4f *>(sums + at * d + 16u * b + 4u * c) = o[n][b];
+        for (uint32_t b = 0; b < kDB; ++b)
+          if (16u * b < d) *reinterpret_cast<v4f *>(sums + at * d + 16u * b + 4u * c) = o[n][b];
+      }
     }
+  }
+  at_block += kCut ? take : 1u;
   }
 }
 
@@ -531,8 +543,8 @@ __global__ __launch_bounds__(kJoinThreads) void paged_join_kernel(PagedArgs a, u
   __shared__ v4f part[kJoinThreads];
   __shared__ float part_sum[kJoinThreads / 4], most[4];
   const uint32_t g = a.hq / a.hk, token = blockIdx.x, h = blockIdx.y, head = h / g;
-  const uint32_t per = run_blocks(a, tile_rows, slots);
-  // the token's sequence, and the slots before its own
+  const uint32_t per = run_blocks(all_blocks(a, tile_rows), slots);
+  // the token's sequence, and the blocks before its own
   uint32_t seq = 0, before = 0;
   bool found = false;
   for (uint32_t base = 0; base < a.count && !found; base += 64u) {
@@ -542,7 +554,7 @@ __global__ __launch_bounds__(kJoinThreads) void paged_join_kernel(PagedArgs a, u
     if (i < a.count) {
       const PagedSpan p = paged_span(a, i);
       const Job j = job_of(a, p, tile_rows);
-      items = j.tiles ? j.tiles * runs_of(j, per) : 0u;
+      items = j.tiles * j.blocks;
       here = token >= p.first && token - p.first < p.n;
     }
     const uint32_t upto = a.count == 1u ? items : wave_scan(items);
@@ -559,15 +571,19 @@ __global__ __launch_bounds__(kJoinThreads) void paged_join_kernel(PagedArgs a, u
   if (!found) return;
   const PagedSpan p = paged_span(a, seq);
   const Job job = job_of(a, p, tile_rows);
-  const uint32_t runs = runs_of(job, per);
+  const uint32_t row = (token - p.first) * g + h % g, tile = row / tile_rows;
+  const uint32_t begin = before + tile * job.blocks, slot0 = begin / per, runs = (begin + job.blocks - 1u) / per - slot0 + 1u;
   // one run has written its rows itself (and starts that do not ascend give no
   // runs past the last slot)
-  if (runs == 1u || before + job.tiles * runs > slots) return;
-  const uint32_t row = (token - p.first) * g + h % g, tile = row / tile_rows;
-  const uint64_t at0 = ((uint64_t)(before + tile * runs) * a.hk + head) * tile_rows + row % tile_rows, step = (uint64_t)a.hk * tile_rows;
+  if (runs == 1u || slot0 + runs > slots) return;
+  // part i: of run slot0 + i, all but the first begin with their run
+  const uint32_t second = begin != slot0 * per;
+  auto at_of = [&](uint32_t i) {
+    return ((uint64_t)(2u * (slot0 + i) + (i == 0u ? second : 0u)) * a.hk + head) * tile_rows + row % tile_rows;
+  };
 
   float top = -INFINITY;
-  for (uint32_t i = threadIdx.x; i < runs; i += kJoinThreads) top = fmaxf(top, stats[at0 + i * step].x);
+  for (uint32_t i = threadIdx.x; i < runs; i += kJoinThreads) top = fmaxf(top, stats[at_of(i)].x);
 #pragma unroll
   for (uint32_t d = 1; d < 64u; d *= 2u) top = fmaxf(top, __shfl_xor(top, (int)d, 64));
   if ((threadIdx.x & 63u) == 0u) most[threadIdx.x >> 6] = top;
@@ -580,10 +596,11 @@ __global__ __launch_bounds__(kJoinThreads) void paged_join_kernel(PagedArgs a, u
   if (group < groups) {
 #pragma unroll 4
     for (uint32_t i = group; i < runs; i += groups) {
-      const float2 s = stats[at0 + i * step];
+      const uint64_t at = at_of(i);
+      const float2 s = stats[at];
       const float w = s.x == -INFINITY ? 0.0f : exp2_hw(s.x - top);
       weight += s.y * w;
-      sum += *reinterpret_cast<const v4f *>(sums + (at0 + i * step) * a.d + 4u * lane) * w;
+      sum += *reinterpret_cast<const v4f *>(sums + at * a.d + 4u * lane) * w;
     }
     part[threadIdx.x] = sum;
     if (lane == 0u) part_sum[group] = weight;
@@ -603,78 +620,75 @@ __global__ __launch_bounds__(kJoinThreads) void paged_join_kernel(PagedArgs a, u
 // ---- the launch ------------------------------------------------------------------
 
 struct Plan {
-  uint32_t blocks, tiles, slots;  // column blocks of a tile; tiles at most; slots of runs
+  uint32_t blocks, slots, tiles;  // column blocks of a tile; runs; tiles at most
 };
 
-Plan plan_of(uint32_t tokens, uint32_t count, uint32_t hq, uint32_t hk, uint32_t d) {
-  const uint32_t g = hq / hk;
-  const uint64_t rows = (uint64_t)tokens * g, mean = (rows + count - 1u) / count;
+constexpr uint32_t kMostBlocks = 2;  // column blocks of 16 rows
+
+Plan plan_of(const PagedArgs &a) {
+  const uint32_t g = a.hq / a.hk;
+  const uint64_t rows = (uint64_t)a.tokens * g, mean = (rows + a.count - 1u) / a.count;
   Plan p;
-  p.blocks = mean <= 16u ? 1u : 2u;
-  const uint32_t tile = 16u * p.blocks;
+  p.blocks = mean <= 16u ? 1u : kMostBlocks;
+  const uint32_t tile = 16u * p.blocks, dp = a.d <= 64u ? 64u : a.d <= 96u ? 96u : a.d <= 128u ? 128u : 256u;
   // (of a sequence with rows: at most one tile that is not full)
-  p.tiles = (uint32_t)std::min<uint64_t>(rows / tile + std::min(count, tokens), (uint64_t)tokens * ((g + tile - 1u) / tile));
-  p.slots = p.tiles + std::max(kTarget / hk, std::min(4u * p.tiles, 4u * kTarget / hk)) + 1u;
+  p.tiles = (uint32_t)std::min<uint64_t>(rows / tile + std::min(a.count, a.tokens), (uint64_t)a.tokens * ((g + tile - 1u) / tile));
+  // as many workgroups as the device holds at once (four waves: one to a SIMD)
+  p.slots = std::max(kCus * (uint32_t)waves_of(dp, a.bits, p.blocks) / a.hk, 1u);
   return p;
 }
 
-template <uint32_t kDP, uint32_t kBits, uint32_t kNT, bool kExact>
-hipError_t launch(const PagedArgs &a, const Plan &plan, bool cut, hipStream_t s) {
+template <uint32_t kDP, uint32_t kBits, uint32_t kNT, bool kExact, uint32_t kWaves, bool kCut>
+hipError_t launch(const PagedArgs &a, const Plan &plan, hipStream_t s) {
   const Parts parts = parts_of(a.workspace, plan.slots, a.hk, 16u * kNT, a.d);
   constexpr uint32_t kLds = (kWaves / 2u) * 16u * kNT * ((kDP + 4u) * 4u + 8u);  // (more than a shared q takes)
-  auto *kernel = paged_decode_kernel<kDP, kBits, kNT, kExact>;
+  auto *kernel = paged_decode_kernel<kDP, kBits, kNT, kExact, kWaves, kCut>;
   if (kLds > 65536u) {
     const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void *>(kernel), (int)kLds);
     if (e != hipSuccess) return e;
   }
-  const uint32_t used = cut ? plan.slots : plan.tiles;
-  hipLaunchKernelGGL(kernel, dim3(used * a.hk), dim3(64 * kWaves), kLds, s, a, plan.slots, parts.sums, parts.stats);
+  hipLaunchKernelGGL(kernel, dim3((kCut ? plan.slots : plan.tiles) * a.hk), dim3(64 * kWaves), kLds, s, a, plan.slots, parts.sums,
+                     parts.stats);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !cut) return e;
+  if (e != hipSuccess || !kCut) return e;
   hipLaunchKernelGGL(paged_join_kernel, dim3(a.tokens, a.hq), dim3(kJoinThreads), 0, s, a, 16u * kNT, plan.slots, parts.sums,
                      parts.stats);
   return hipGetLastError();
 }
 
+template <uint32_t kDP, uint32_t kBits, uint32_t kNT>
+hipError_t launch_rows(const PagedArgs &a, const Plan &plan, hipStream_t s) {
+  constexpr uint32_t kWide = kDP * kNT <= 128u ? 8 : 4;  // waves for a whole sequence
+  if (((uint64_t)a.width << a.page_shift) <= kShort)
+    return a.d == kDP ? launch<kDP, kBits, kNT, true, kWide, false>(a, plan, s) : launch<kDP, kBits, kNT, false, kWide, false>(a, plan, s);
+  return a.d == kDP ? launch<kDP, kBits, kNT, true, 4, true>(a, plan, s) : launch<kDP, kBits, kNT, false, 4, true>(a, plan, s);
+}
+
 template <uint32_t kDP, uint32_t kBits>
-hipError_t launch_rows(const PagedArgs &a, const Plan &plan, bool cut, hipStream_t s) {
-  if (plan.blocks == 1u) return a.d == kDP ? launch<kDP, kBits, 1, true>(a, plan, cut, s) : launch<kDP, kBits, 1, false>(a, plan, cut, s);
-  return a.d == kDP ? launch<kDP, kBits, 2, true>(a, plan, cut, s) : launch<kDP, kBits, 2, false>(a, plan, cut, s);
+hipError_t launch_heads(const PagedArgs &a, const Plan &plan, hipStream_t s) {
+  return plan.blocks == 1u ? launch_rows<kDP, kBits, 1>(a, plan, s) : launch_rows<kDP, kBits, kMostBlocks>(a, plan, s);
 }
 
 template <uint32_t kBits>
-hipError_t launch_heads(const PagedArgs &a, const Plan &plan, bool cut, hipStream_t s) {
-  if (a.d <= 64u) return launch_rows<64, kBits>(a, plan, cut, s);
-  if (a.d <= 96u) return launch_rows<96, kBits>(a, plan, cut, s);
-  if (a.d <= 128u) return launch_rows<128, kBits>(a, plan, cut, s);
-  return launch_rows<256, kBits>(a, plan, cut, s);
+hipError_t launch_bits(const PagedArgs &a, const Plan &plan, hipStream_t s) {
+  if (a.d <= 64u) return launch_heads<64, kBits>(a, plan, s);
+  if (a.d <= 96u) return launch_heads<96, kBits>(a, plan, s);
+  if (a.d <= 128u) return launch_heads<128, kBits>(a, plan, s);
+  return launch_heads<256, kBits>(a, plan, s);
 }
 
 }  // namespace
 
 hipError_t launch_paged_decode(const PagedArgs &a, hipStream_t s) {
-  const Plan plan = plan_of(a.tokens, a.count, a.hq, a.hk, a.d);
-  // no sequence can be longer than a run: nothing to join
-  const bool cut = ((uint64_t)a.width << a.page_shift) > kLeast * kBlock;
-  return a.bits == 16u ? launch_heads<16>(a, plan, cut, s) : launch_heads<8>(a, plan, cut, s);
+  const Plan plan = plan_of(a);
+  return a.bits == 16u ? launch_bits<16>(a, plan, s) : launch_bits<8>(a, plan, s);
 }
 
-// For a call of at most these sizes: five slots a tile, or one and the target's.
-// Tiles of 32 rows are taken where sequences have over half as many on average,
-// so that all of them have at most 3 times the rows.
-uint64_t paged_workspace_bytes(uint32_t tokens, uint32_t count, uint32_t hq, uint32_t hk, uint32_t d) {
-  if (tokens == 0u || count == 0u) return 0;
-  const uint64_t g = hq / hk, rows = tokens * g;
-  const uint64_t narrow = std::min<uint64_t>(rows + 16ull * std::min(count, tokens), tokens * 16ull * ((g + 15u) / 16u));
-  const uint64_t all = std::max(3u * rows, narrow);
-  const uint64_t slots = all + std::max<uint64_t>(kTarget / hk * 32u, std::min<uint64_t>(4u * all, 4u * kTarget / hk * 32u)) + 32u;
-  return slots * hk * (4ull * d + 8u);
-}
-
-uint64_t paged_workspace_needed(uint32_t tokens, uint32_t count, uint32_t hq, uint32_t hk, uint32_t d) {
-  if (tokens == 0u || count == 0u) return 0;
-  const Plan p = plan_of(tokens, count, hq, hk, d);
-  return (uint64_t)p.slots * hk * 16u * p.blocks * (4u * d + 8u);
+// The two parts of each run, for tiles of the most rows and as many runs as any
+// form of the kernel has: what a call needs, whatever its tokens are.
+uint64_t paged_workspace_bytes(uint32_t hk, uint32_t d) {
+  const uint64_t slots = std::max(kCus * 3u / hk, 1u);
+  return 2u * slots * hk * 16u * kMostBlocks * (4ull * d + 8u);
 }
 
 }  // namespace bqmm
