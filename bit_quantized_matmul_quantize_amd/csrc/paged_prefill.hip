@@ -24,6 +24,7 @@ namespace {
 constexpr uint32_t kWaves = 4;
 constexpr uint32_t kThreads = 64 * kWaves;
 constexpr uint32_t kRows = 32 * kWaves;
+constexpr uint32_t kCus = 256;
 
 // 16 bytes a lane straight from memory into LDS: lane i's go to the wave's
 // destination + 16 i.  The kernel waits itself; no register is written.
@@ -52,6 +53,46 @@ __device__ __forceinline__ uint32_t tiles_of(const PagedArgs &a, const PagedSpan
   return (uint32_t)(((uint64_t)p.n * (a.hq / a.hk) + kRows - 1u) / kRows);
 }
 
+// The tile of rows that workgroup `item` of a key head takes: those with the most
+// keys first, since the last to end decide.  Sequences by their longest tile (up to
+// 64 of them; more are taken as they come), their tiles from the last one back.
+// Where all workgroups are on the device at once, two to a compute unit, the second
+// one of a unit is the shorter the longer the first is.
+__device__ __forceinline__ bool take_tile(const PagedArgs &a, uint32_t item, uint32_t *seq, uint32_t *tile) {
+  const uint32_t lane = __lane_id();
+  if (a.count > 64u) {
+    uint32_t inside;
+    if (!paged_find(item, a.count, [&](uint32_t i) { return tiles_of(a, paged_span(a, i)); }, seq, &inside)) return false;
+    *tile = tiles_of(a, paged_span(a, *seq)) - 1u - inside;
+    return true;
+  }
+  uint32_t mine = 0, keys = 0;
+  if (lane < a.count) {
+    const PagedSpan p = paged_span(a, lane);
+    mine = tiles_of(a, p);
+    keys = mine ? (uint32_t)min(p.keys, max(p.at + (int32_t)p.n, 0)) + 1u : 0u;
+    if (a.window) keys = min(keys, a.window + p.n);
+  }
+  uint32_t before = 0, all = mine;
+  if (a.count > 1u) {
+    all = 0;
+    for (uint32_t i = 0; i < a.count; ++i) {  // tiles of the sequences that come first
+      const uint32_t k = (uint32_t)__builtin_amdgcn_readlane((int)keys, (int)i), n = (uint32_t)__builtin_amdgcn_readlane((int)mine, (int)i);
+      before += k > keys || (k == keys && i < lane) ? n : 0u;
+      all += n;
+    }
+  }
+  all = __builtin_amdgcn_readfirstlane(all);
+  if (item >= all) return false;
+  const uint32_t half = kCus / a.hk;
+  if (all > half && all <= 2u * half && item >= half) item = all - 1u - (item - half);
+  const uint64_t who = __ballot(item >= before && item - before < mine);
+  const uint32_t w = (uint32_t)__builtin_ctzll(who);
+  *seq = __builtin_amdgcn_readfirstlane(w);
+  *tile = (uint32_t)__builtin_amdgcn_readlane((int)(mine - 1u - (item - before)), (int)w);
+  return true;
+}
+
 // kExact: a head has kDP values, and a page has at least a tile's keys.
 // kCap: scores are capped (both may be, unless kExact).
 template <uint32_t kDP, uint32_t kBits, bool kExact, bool kCap>
@@ -66,11 +107,10 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
   const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t r = lane & 31u, half = lane >> 5;
   const uint32_t head = blockIdx.x % a.hk, g = a.hq / a.hk;
-  uint32_t seq, inside;
-  if (!paged_find(blockIdx.x / a.hk, a.count, [&](uint32_t i) { return tiles_of(a, paged_span(a, i)); }, &seq, &inside)) return;
+  uint32_t seq, tile;
+  if (!take_tile(a, blockIdx.x / a.hk, &seq, &tile)) return;
   const PagedSpan p = paged_span(a, seq);
-  // the last tiles have the most keys: they begin first
-  const uint32_t tile = tiles_of(a, p) - 1u - inside, rows = p.n * g;
+  const uint32_t rows = p.n * g;
 
   // what rows see: key <= place, and key > place - window
   auto place_of = [&](uint32_t row) { return p.at + (int32_t)(row / g); };
@@ -418,7 +458,6 @@ hipError_t launch_heads(const PagedArgs &a, hipStream_t s) {
   if (a.d <= 64u) return launch_exact<64, kBits>(a, s);
   if (a.d <= 96u) return launch_exact<96, kBits>(a, s);
   if (a.d <= 128u) return launch_exact<128, kBits>(a, s);
-  if (a.d <= 192u) return launch_exact<192, kBits>(a, s);
   return launch_exact<256, kBits>(a, s);
 }
 
