@@ -36,6 +36,23 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, const uint8_t *from) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory", "m0");
 }
 
+// kRuns of them, 1024 bytes apart in memory and in LDS.
+template <uint32_t kRuns>
+__device__ __forceinline__ void load_run_to_lds(uint32_t lds, uint32_t offset, const uint8_t *base) {
+  static_assert(kRuns >= 2 && kRuns <= 4, "");
+  if constexpr (kRuns == 2)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\t"
+                 "global_load_lds_dwordx4 %1, %2 offset:1024" ::"s"(lds), "v"(offset), "s"(base) : "memory", "m0");
+  else if constexpr (kRuns == 3)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\t"
+                 "global_load_lds_dwordx4 %1, %2 offset:1024\n\tglobal_load_lds_dwordx4 %1, %2 offset:2048"
+                 ::"s"(lds), "v"(offset), "s"(base) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\t"
+                 "global_load_lds_dwordx4 %1, %2 offset:1024\n\tglobal_load_lds_dwordx4 %1, %2 offset:2048\n\t"
+                 "global_load_lds_dwordx4 %1, %2 offset:3072" ::"s"(lds), "v"(offset), "s"(base) : "memory", "m0");
+}
+
 // kDP: values of a head, rounded up (the ones beyond are zero).
 template <uint32_t kDP, uint32_t kBits>
 struct Shape {
@@ -149,67 +166,57 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
     __syncthreads();
   }
 
-  auto ids_of = [&](int32_t key0, v4u &ids) {
-#pragma unroll
-    for (uint32_t t = 0; t < kSubs; ++t) {
-      const uint32_t at = (uint32_t)(key0 + (int32_t)(16u * t)) >> a.page_shift;
-      ids[t] = __builtin_amdgcn_readfirstlane(at < a.width ? (uint32_t)table[at] : ~0u);
-    }
+  // The page of the tile's keys 16 t..: in the lanes 16 t.. (and those a tile later).
+  // A vector load: a scalar one would be waited for with the operands read from LDS.
+  auto id_of = [&](int32_t key0) {
+    const uint32_t at = (uint32_t)(key0 + (int32_t)(lane % kKT & ~15u)) >> a.page_shift;
+    return at < a.width ? (uint32_t)table[at] : ~0u;
   };
-  auto pick = [&](const v4u &ids, uint32_t sub) {
-    uint32_t id = ids[0];
-#pragma unroll
-    for (uint32_t t = 1; t < kSubs; ++t) id = sub == t ? ids[t] : id;
-    return id < a.pages ? id : 0u;
-  };
+  auto known = [&](uint32_t id) { return id < a.pages ? id : 0u; };
 
-  // ---- bringing a tile: places in the tile that this thread brings
+  // ---- bringing a tile: a wave's 64 units at a time follow each other, in LDS too
   constexpr uint32_t kParts = kBits == 16 ? S::kLoads : S::kCodes;
   constexpr uint32_t kUnit = 128 / kBits;
   constexpr bool kFull = kParts * kThreads * 16 == S::kTile * kBits / 16;  // every thread has a unit in every part
   v4u kr[kBits == 8 ? kParts : 1], vr[kBits == 8 ? kParts : 1];
   float scale_r = 0.0f;
-  auto bring = [&](int32_t key0, const v4u &ids, uint32_t stage) {
+  auto bring = [&](int32_t key0, uint32_t id, uint32_t stage) {
     const uint32_t off0 = (uint32_t)key0 & (page - 1u);
     const bool one_page = kExact || page >= kKT;
-    const uint32_t id0 = ids[0] < a.pages ? ids[0] : 0u;
+    const uint32_t id0 = known(__builtin_amdgcn_readfirstlane(id));
     const uint8_t *k0 = kc + id0 * page_bytes + off0 * 16u, *v0 = vc + id0 * page_bytes + (uint64_t)(off0 / kUnit) * d * 16u;
+    const uint8_t *mine = kc + known(id) * page_bytes;  // (its key is the same in all parts)
+    const uint32_t key = lane % kKT, ko = (uint32_t)(key0 + (int32_t)key) & (page - 1u);
+    if constexpr (kBits == 16 && kExact) {
+      const uint32_t to = lds0 + stage * S::kStage + wave * kParts * 1024u;
 #pragma unroll
-    for (uint32_t j = 0; j < kParts; ++j) {
-      // (wave's 64 units follow each other, in LDS too)
-      const uint32_t i = (wave + kWaves * j) * 64u + lane;
-      const uint32_t ku = i / kKT, key = i % kKT, vg = i / kDP, dim = i % kDP;
-      const bool has_k = (kExact && kFull) || ku * kUnit < d, has_v = (kExact && kFull) || (dim < d && vg * kUnit < kKT);
-      if constexpr (kBits == 16) {
-        const uint32_t to = lds0 + stage * S::kStage + (wave + kWaves * j) * 1024u;
-        if constexpr (kExact) {  // (uniform parts of the offsets belong to the scalar base)
-          constexpr uint32_t kRuns = 64 / kKT;
-          load_to_lds(to, (lane / kKT * page + lane % kKT) * 16u, k0 + (uint64_t)((wave + kWaves * j) * kRuns) * page * 16u);
-          load_to_lds(to + S::kTile, lane * 16u, v0 + (wave + kWaves * j) * 1024u);
-        } else if (one_page) {
-          if (has_k) load_to_lds(to, (ku * page + key) * 16u, k0);
-          if (has_v) load_to_lds(to + S::kTile, (vg * d + dim) * 16u, v0);
+      for (uint32_t j = 0; j < kParts; ++j)
+        load_to_lds(to + j * 1024u, (lane / kKT * page + key) * 16u, k0 + (uint64_t)((wave * kParts + j) * (64u / kKT)) * page * 16u);
+      load_run_to_lds<kParts>(to + S::kTile, lane * 16u, v0 + wave * kParts * 1024u);
+    } else {
+#pragma unroll
+      for (uint32_t j = 0; j < kParts; ++j) {
+        const uint32_t i = (wave * kParts + j) * 64u + lane, ku = i / kKT, vg = i / kDP, dim = i % kDP;
+        const bool has_k = (kExact && kFull) || ku * kUnit < d, has_v = (kExact && kFull) || (dim < d && vg * kUnit < kKT);
+        const uint32_t vo = (uint32_t)(key0 + (int32_t)(vg * kUnit)) & (page - 1u);
+        // (the lanes of a wave's 64 units may lie in two groups of keys where kDP is no multiple of 64)
+        const uint32_t sub = vg * kUnit / 16u * 16u;
+        const uint32_t vid = one_page ? id0 : known(kDP % 64u == 0u ? (uint32_t)__builtin_amdgcn_readlane((int)id, (int)__builtin_amdgcn_readfirstlane(sub % 64u)) : (uint32_t)__shfl((int)id, (int)(sub % 64u), 64));
+        const uint8_t *k_from = one_page ? k0 + (ku * page + key) * 16u : mine + (ku * page + ko) * 16u;
+        const uint8_t *v_from = one_page ? v0 + (vg * d + dim) * 16u : vc + vid * page_bytes + ((uint64_t)(vo / kUnit) * d + dim) * 16u;
+        if constexpr (kBits == 16) {
+          const uint32_t to = lds0 + stage * S::kStage + (wave * kParts + j) * 1024u;
+          if (has_k) load_to_lds(to, k_from);
+          if (has_v) load_to_lds(to + S::kTile, v_from);
         } else {
-          const uint32_t ks = key / 16u, vs = vg * kUnit / 16u;
-          const uint32_t ko = (uint32_t)(key0 + (int32_t)key) & (page - 1u), vo = (uint32_t)(key0 + (int32_t)(vg * kUnit)) & (page - 1u);
-          if (has_k) load_to_lds(to, kc + pick(ids, ks) * page_bytes + (ku * page + ko) * 16u);
-          if (has_v) load_to_lds(to + S::kTile, vc + pick(ids, vs) * page_bytes + ((uint64_t)(vo / kUnit) * d + dim) * 16u);
+          if (has_k) kr[j] = *reinterpret_cast<const v4u *>(k_from);
+          if (has_v) vr[j] = *reinterpret_cast<const v4u *>(v_from);
         }
-      } else if (one_page) {
-        if (has_k) kr[j] = *reinterpret_cast<const v4u *>(k0 + (ku * page + key) * 16u);
-        if (has_v) vr[j] = *reinterpret_cast<const v4u *>(v0 + (vg * d + dim) * 16u);
-      } else {
-        const uint32_t ko = (uint32_t)(key0 + (int32_t)key) & (page - 1u), vo = (uint32_t)(key0 + (int32_t)(vg * kUnit)) & (page - 1u);
-        if (has_k) kr[j] = *reinterpret_cast<const v4u *>(kc + pick(ids, key / 16u) * page_bytes + (ku * page + ko) * 16u);
-        if (has_v) vr[j] = *reinterpret_cast<const v4u *>(vc + pick(ids, vg) * page_bytes + ((uint64_t)(vo / kUnit) * d + dim) * 16u);
       }
     }
     if constexpr (kBits == 8) {
-      if (threadIdx.x < 2u * kKT) {
-        const uint32_t key = threadIdx.x % kKT, ko = (uint32_t)(key0 + (int32_t)key) & (page - 1u);
-        const uint8_t *from = threadIdx.x < kKT ? kc : vc;
-        scale_r = *reinterpret_cast<const float *>(from + pick(ids, key / 16u) * page_bytes + page * d + ko * 4u);
-      }
+      if (threadIdx.x < 2u * kKT)
+        scale_r = *reinterpret_cast<const float *>((threadIdx.x < kKT ? kc : vc) + known(id) * page_bytes + page * d + ko * 4u);
     }
   };
   // an int8 tile from registers into LDS
@@ -218,7 +225,7 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
       uint8_t *to = lds + stage * S::kStage;
 #pragma unroll
       for (uint32_t j = 0; j < kParts; ++j) {
-        const uint32_t i = (wave + kWaves * j) * 64u + lane;
+        const uint32_t i = (wave * kParts + j) * 64u + lane;
         const uint32_t ku = i / kKT, key = i % kKT, vg = i / kDP, dim = i % kDP;
         asm volatile("" : "+v"(kr[j]), "+v"(vr[j]));  // (else every code is carried in a register of its own)
         if ((kExact && kFull) || ku * kUnit < d) {
@@ -248,9 +255,9 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
   const uint32_t k_row = 16u * (r >> 4) + 8u * ((r >> 2) & 1u) + 4u * ((r >> 3) & 1u) + (r & 3u);
   const uint32_t k_at = (half * kKT + k_row) * 16u, v_at = (half * kDP + r) * 16u;
 
-  // One tile.  hole: bit t where the tile's keys 16 t.. lie in no page; whole: all
+  // One tile.  hole: bit 16 t where the tile's keys 16 t.. lie in no page; whole: all
   // rows of the wave see all of it.
-  auto compute = [&](int32_t key0, uint32_t stage, uint32_t hole, bool whole) {
+  auto compute = [&](int32_t key0, uint32_t stage, uint64_t hole, bool whole) {
     const uint8_t *kt = lds + stage * S::kStage + k_at, *vt = lds + stage * S::kStage + S::kTile + v_at;
     const float *scales = reinterpret_cast<const float *>(lds + stage * S::kStage + 2u * S::kTile) + 8u * half;
     // the operands of a half tile are read while the last one's are used
@@ -295,7 +302,7 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
     // the keys 16 t.. of the tile that this row sees: of key0 + 16 t + 8 half + i, bit i
     auto seen_of = [&](uint32_t t) {
       const int32_t at = key0 + (int32_t)(16u * t + 8u * half), from = max(low - at, 0), to = min(min(pos, p.keys - 1) - at, 7);
-      return hole >> t & 1u || from > to ? 0u : (0xFFu >> (7 - to)) & (0xFFu << from);
+      return hole >> (16u * t) & 1u || from > to ? 0u : (0xFFu >> (7 - to)) & (0xFFu << from);
     };
     if (!whole) {
 #pragma unroll
@@ -389,23 +396,20 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
     }
   };
 
-  v4u ids, next_ids;
-  ids_of(begin, ids);
-  if (begin < end) bring(begin, ids, 0);
+  uint32_t id = id_of(begin);
+  if (begin < end) bring(begin, id, 0);
   settle(0);
-  ids_of(begin + (int32_t)kKT, next_ids);
+  uint32_t next_id = id_of(begin + (int32_t)kKT);
   uint32_t stage = 0;
   for (int32_t key0 = begin; key0 < end; key0 += (int32_t)kKT, stage ^= 1u) {
     // this tile has arrived, and nobody reads the other stage any more
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __syncthreads();
-    uint32_t hole = 0;
-#pragma unroll
-    for (uint32_t t = 0; t < kSubs; ++t) hole |= ids[t] >= a.pages ? 1u << t : 0u;
+    const uint64_t hole = __ballot(id >= a.pages);
     const bool more = key0 + (int32_t)kKT < end;
-    if (more) bring(key0 + (int32_t)kKT, next_ids, stage ^ 1u);
-    ids = next_ids;
-    ids_of(key0 + 2 * (int32_t)kKT, next_ids);
+    if (more) bring(key0 + (int32_t)kKT, next_id, stage ^ 1u);
+    id = next_id;
+    next_id = id_of(key0 + 2 * (int32_t)kKT);
     if (key0 < any_end && key0 + (int32_t)kKT > any_low)
       compute(key0, stage, hole, !hole && key0 >= whole_low && key0 + (int32_t)kKT <= whole_end);
     if (more) settle(stage ^ 1u);
