@@ -22,6 +22,7 @@ namespace {
 
 constexpr uint32_t kTile = 16;     // places
 constexpr uint32_t kThreads = 256;
+constexpr uint32_t kGroups = 2048;  // workgroups, where there are heads to share out
 
 struct Tile {
   PagedSpan span;
@@ -52,8 +53,10 @@ __device__ __forceinline__ int64_t tile_page(const PagedArgs &a, const Tile &t) 
   return id < a.pages ? (int64_t)id : -1;
 }
 
-__device__ __forceinline__ void unpack8(const uint16_t *p, float *x) {
-  const uint4 r = *reinterpret_cast<const uint4 *>(p);
+struct __attribute__((aligned(4))) Float8 {
+  float x[8];
+};
+__device__ __forceinline__ void unpack8(const uint4 &r, float *x) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -62,7 +65,7 @@ __device__ __forceinline__ void unpack8(const uint16_t *p, float *x) {
   }
 }
 __device__ __forceinline__ uint4 pack8(const float *x) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  return make_uint4(two_bf16(x[0], x[1]), two_bf16(x[2], x[3]), two_bf16(x[4], x[5]), two_bf16(x[6], x[7]));
 }
 
 // Codes of 16 values whose row's largest magnitude has the bits `top`: the
@@ -103,8 +106,9 @@ __device__ __forceinline__ uint32_t top16(const float *x) {
 }
 
 // G: lanes of a row, each with two runs of 8 values.
+// Workgroups (.., y) with y < parts share the heads of q and k, the others those of v.
 template <uint32_t G>
-__global__ __launch_bounds__(kThreads) void paged_write_kernel(PagedArgs a) {
+__global__ __launch_bounds__(kThreads) void paged_write_kernel(PagedArgs a, uint32_t parts) {
   constexpr uint32_t kHeads = kThreads / (kTile * G);  // heads at once
   constexpr uint32_t kPitch = G * 16u;                 // of a token in the tile
   __shared__ __attribute__((aligned(16))) uint16_t turn[kHeads * kTile * kPitch];
@@ -117,51 +121,86 @@ __global__ __launch_bounds__(kThreads) void paged_write_kernel(PagedArgs a) {
   const bool mine = token >= t.low && token < t.high && lane < a.d / 16u;
   const uint64_t row = (uint64_t)t.span.first + (uint32_t)(t.place0 + (int32_t)token - t.span.at);
 
+  if (blockIdx.y < parts) {
   // this lane's runs of a head: a pair that is rotated, or two that are not
   const uint32_t pairs = a.rot / 16u;
   const bool turned = lane < pairs;
   const uint32_t run0 = turned ? lane : 2u * lane, run1 = turned ? lane + pairs : run0 + 1u;
+  // q and k: the first heads are on their way while the angles are looked up, the
+  // next ones while these are computed
+  const uint32_t heads = a.hq + a.hk, stride = parts * kHeads;
+  auto load = [&](uint32_t h, uint4 (&raw)[2]) {
+    if (mine && h < heads) {
+      const uint16_t *p = h < a.hq ? a.q + row * a.q_token + h * a.q_head : a.k + row * a.k_token + (h - a.hq) * a.k_head;
+      raw[0] = *reinterpret_cast<const uint4 *>(p + run0 * 8u);
+      raw[1] = *reinterpret_cast<const uint4 *>(p + run1 * 8u);
+    }
+  };
+  uint4 raw[2] = {};
+  load(blockIdx.y * kHeads + sub, raw);
   float c[8], s[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) c[e] = 1.0f, s[e] = 0.0f;
   if (mine && turned) {
     const float nan = __uint_as_float(0x7FC00000u);
-    int32_t angle = t.place0 + (int32_t)token;
-    if (a.positions && !a.axis) angle = a.positions[row];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t f = lane * 8u + e;
-      if (a.axis) angle = a.axis[f] < a.axes ? a.positions[(uint64_t)a.axis[f] * a.tokens + row] : -1;
+    if (!a.axis) {  // 
+      const int32_t angle = a.positions ? a.positions[row] : t.place0 + (int32_t)token;
       const bool known = (uint32_t)angle < a.angles;
-      const float *at = a.cos_sin + (uint64_t)(known ? angle : 0) * a.rot + f;
-      c[e] = known ? at[0] : nan;
-      s[e] = known ? at[a.rot / 2u] : nan;
+      const float *at = a.cos_sin + (uint64_t)(known ? angle : 0) * a.rot + lane * 8u;
+      const Float8 cv = *reinterpret_cast<const Float8 *>(at), sv = *reinterpret_cast<const Float8 *>(at + a.rot / 2u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] = known ? cv.x[e] : nan, s[e] = known ? sv.x[e] : nan;
+    } else {
+      int32_t angle[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t axis = a.axis[lane * 8u + e];
+        angle[e] = a.positions[(uint64_t)(axis < a.axes ? axis : 0u) * a.tokens + row];
+        if (axis >= a.axes) angle[e] = -1;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const bool known = (uint32_t)angle[e] < a.angles;
+        const float *at = a.cos_sin + (uint64_t)(known ? angle[e] : 0) * a.rot + lane * 8u + e;
+        c[e] = known ? at[0] : nan;
+        s[e] = known ? at[a.rot / 2u] : nan;
+      }
+    }
+  }
+  // the norms' weights of this lane's runs
+  uint4 wq[2] = {}, wk[2] = {};
+  if (lane < a.d / 16u) {
+    if (a.q_norm) {
+      wq[0] = *reinterpret_cast<const uint4 *>(a.q_norm + run0 * 8u);
+      wq[1] = *reinterpret_cast<const uint4 *>(a.q_norm + run1 * 8u);
+    }
+    if (a.k_norm) {
+      wk[0] = *reinterpret_cast<const uint4 *>(a.k_norm + run0 * 8u);
+      wk[1] = *reinterpret_cast<const uint4 *>(a.k_norm + run1 * 8u);
     }
   }
 
-  // q and k
-  for (uint32_t h0 = blockIdx.y * kHeads; h0 < a.hq + a.hk; h0 += gridDim.y * kHeads) {
+  for (uint32_t h0 = blockIdx.y * kHeads; h0 < heads; h0 += stride) {
     const uint32_t h = h0 + sub;
-    const bool is_q = h < a.hq, live = mine && h < a.hq + a.hk;
+    const bool is_q = h < a.hq, live = mine && h < heads;
     float x[16];
+    unpack8(raw[0], x);
+    unpack8(raw[1], x + 8);
+    if (!live) {  // (of no row: zeros)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = 0.0f;
-    if (live) {
-      const uint16_t *p = is_q ? a.q + row * a.q_token + h * a.q_head : a.k + row * a.k_token + (h - a.hq) * a.k_head;
-      unpack8(p + run0 * 8u, x);
-      unpack8(p + run1 * 8u, x + 8);
+      for (int e = 0; e < 16; ++e) x[e] = 0.0f;
     }
-    const uint16_t *norm = is_q ? a.q_norm : a.k_norm;
+    load(h + stride, raw);
     if (a.q_norm || a.k_norm) {
       float sum = 0.0f;
 #pragma unroll
       for (int e = 0; e < 16; ++e) sum = fmaf(x[e], x[e], sum);
       sum = row_sum(sum, G);
-      if (live && norm) {
+      if (live && (is_q ? a.q_norm : a.k_norm)) {
         const float r = 1.0f / sqrtf(sum / (float)a.d + a.eps);
         float w[16];
-        unpack8(norm + run0 * 8u, w);
-        unpack8(norm + run1 * 8u, w + 8);
+        unpack8(is_q ? wq[0] : wk[0], w);
+        unpack8(is_q ? wq[1] : wk[1], w + 8);
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = x[e] * r * w[e];
       }
@@ -200,10 +239,12 @@ __global__ __launch_bounds__(kThreads) void paged_write_kernel(PagedArgs a) {
       }
     }
   }
+    return;
+  }
   if (id < 0) return;  // (the whole workgroup)
 
   // v: turned in LDS, so that whole units leave
-  for (uint32_t h0 = blockIdx.y * kHeads; h0 < a.hk; h0 += gridDim.y * kHeads) {
+  for (uint32_t h0 = (blockIdx.y - parts) * kHeads; h0 < a.hk; h0 += (gridDim.y - parts) * kHeads) {
     const uint32_t h = h0 + sub;
     const bool live = mine && h < a.hk;
     uint16_t *to = turn + (sub * kTile + token) * kPitch;
@@ -220,9 +261,9 @@ __global__ __launch_bounds__(kThreads) void paged_write_kernel(PagedArgs a) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[e] = 0.0f;
       if (live) {
-        const uint16_t *p = a.v + row * a.v_token + h * a.v_head + lane * 16u;
-        unpack8(p, x);
-        unpack8(p + 8, x + 8);
+        const uint4 *p = reinterpret_cast<const uint4 *>(a.v + row * a.v_token + h * a.v_head) + 2u * lane;
+        unpack8(p[0], x);
+        unpack8(p[1], x + 8);
       }
       const uint32_t top = row_max(top16(x), G);
       if (live) {
@@ -332,22 +373,25 @@ uint32_t tiles_at_most(const PagedArgs &a) {
 
 hipError_t launch_paged_write(const PagedArgs &a, hipStream_t s) {
   const uint32_t G = a.d <= 16u ? 1u : a.d <= 32u ? 2u : a.d <= 64u ? 4u : a.d <= 128u ? 8u : 16u;
-  const uint32_t at_once = kThreads / (kTile * G), parts = (a.hq + a.hk + at_once - 1u) / at_once;
-  const uint32_t tiles = tiles_at_most(a);
-  const dim3 grid(tiles, std::min(parts, std::max(1u, 4096u / tiles)));
+  const uint32_t at_once = kThreads / (kTile * G), tiles = tiles_at_most(a);
+  const uint32_t all_qk = (a.hq + a.hk + at_once - 1u) / at_once, all_v = (a.hk + at_once - 1u) / at_once;
+  // as many workgroups for v as its share is
+  const uint32_t most = std::max(1u, kGroups / tiles), parts = std::min(all_qk, most);
+  const uint32_t parts_v = std::min(all_v, std::max(1u, (uint32_t)((uint64_t)parts * all_v / all_qk)));
+  const dim3 grid(tiles, parts + parts_v);
   switch (G) {
-    case 1: hipLaunchKernelGGL(paged_write_kernel<1>, grid, dim3(kThreads), 0, s, a); break;
-    case 2: hipLaunchKernelGGL(paged_write_kernel<2>, grid, dim3(kThreads), 0, s, a); break;
-    case 4: hipLaunchKernelGGL(paged_write_kernel<4>, grid, dim3(kThreads), 0, s, a); break;
-    case 8: hipLaunchKernelGGL(paged_write_kernel<8>, grid, dim3(kThreads), 0, s, a); break;
-    default: hipLaunchKernelGGL(paged_write_kernel<16>, grid, dim3(kThreads), 0, s, a);
+    case 1: hipLaunchKernelGGL(paged_write_kernel<1>, grid, dim3(kThreads), 0, s, a, parts); break;
+    case 2: hipLaunchKernelGGL(paged_write_kernel<2>, grid, dim3(kThreads), 0, s, a, parts); break;
+    case 4: hipLaunchKernelGGL(paged_write_kernel<4>, grid, dim3(kThreads), 0, s, a, parts); break;
+    case 8: hipLaunchKernelGGL(paged_write_kernel<8>, grid, dim3(kThreads), 0, s, a, parts); break;
+    default: hipLaunchKernelGGL(paged_write_kernel<16>, grid, dim3(kThreads), 0, s, a, parts);
   }
   return hipGetLastError();
 }
 
 hipError_t launch_paged_read(const PagedArgs &a, hipStream_t s) {
   const uint32_t tiles = tiles_at_most(a);
-  const dim3 grid(tiles, std::min(2u * a.hk, std::max(1u, 4096u / tiles)));
+  const dim3 grid(tiles, std::min(2u * a.hk, std::max(1u, kGroups / tiles)));
   hipLaunchKernelGGL(paged_read_kernel, grid, dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
