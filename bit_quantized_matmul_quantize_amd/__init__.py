@@ -477,28 +477,31 @@ def _paged(k_cache, v_cache, starts, lens, table, page, hk, d, bits):
     _u8(k_cache, "k_cache")
     if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape:
         raise ValueError(f"v_cache: expected the keys' bytes {tuple(k_cache.shape)}, got {v_cache.dtype} {tuple(v_cache.shape)}")
-    if starts.dim() != 1 or starts.numel() < 1 or table.dim() != 2:
+    shape = table.shape
+    if len(shape) != 2 or starts.dim() != 1 or starts.shape[0] < 1:
         raise ValueError("expected starts as [count + 1] and table as [count, width]")
-    count, width = starts.numel() - 1, table.shape[1]
-    _typed(starts, "torch.int32", (count + 1,), "starts")
-    _typed(lens, "torch.int32", (count,), "lens")
-    _typed(table, "torch.int32", (count, width), "table")
+    count, width = starts.shape[0] - 1, shape[1]
+    if _kinds.get(starts.dtype) != "torch.int32" or starts.dtype != lens.dtype or starts.dtype != table.dtype:
+        for t, what in ((starts, "starts"), (lens, "lens"), (table, "table")):
+            _typed(t, "torch.int32", t.shape, what)
+    if shape[0] != count:
+        raise ValueError(f"table: expected [{count}, width], got {tuple(shape)}")
+    if lens.shape != (count,):
+        raise ValueError(f"lens: expected shape {(count,)}, got {tuple(lens.shape)}")
     # (sizes that the library refuses give no bytes; it says why)
-    size = hk * page * (2 * d if bits == 16 else d + 4)
-    if size > 0 and _nbytes(k_cache) % size:
-        raise ValueError(f"k_cache: {_nbytes(k_cache)} bytes are no whole number of pages of {size}")
-    return count, _nbytes(k_cache) // size if size > 0 else 0, width
+    size, held = hk * page * (2 * d if bits == 16 else d + 4), k_cache.nbytes
+    if size > 0 and held % size:
+        raise ValueError(f"k_cache: {held} bytes are no whole number of pages of {size}")
+    return count, held // size if size > 0 else 0, width
 
 
-def _on_device_of(q, *tensors):
-    """Device pointers of contiguous tensors that lie on q's device."""
-    for t in tensors:
-        if t is not None and t.get_device() != q.get_device():
-            _same_device(q, *tensors)
-            raise ValueError("expected a device tensor")
-    if q.get_device() < 0:
+def _beside(q, *tensors):
+    """Device pointers of contiguous tensors that lie on q's device; the first is not None."""
+    ptrs = _ptrs(*tensors)
+    if q.get_device() != tensors[0].get_device():
+        _same_device(q, *tensors)
         raise ValueError("expected a device tensor")
-    return _ptrs(*tensors)
+    return ptrs
 
 
 def rope_write_kv_cache(q, k, v, q_out, k_cache, v_cache, starts, lens, table, page: int, bits: int = 16, cos_sin=None,
@@ -537,10 +540,11 @@ def rope_write_kv_cache(q, k, v, q_out, k_cache, v_cache, starts, lens, table, p
         if w is not None:
             _typed(w, "torch.bfloat16", (d,), what)
     count, pages, width = _paged(k_cache, v_cache, starts, lens, table, page, hk, d, bits)
-    rest = _on_device_of(k, q_out, k_cache, v_cache, starts, lens, table, cos_sin, positions, axis, q_norm, k_norm)
+    k_at, v_at, *rest = _beside(k, k_cache, v_cache, starts, lens, table, cos_sin, positions, axis, q_norm, k_norm, q_out)
     if v.get_device() != k.get_device() or (q is not None and q.get_device() != k.get_device()):
         raise ValueError("q, k and v on different devices")
-    _check(lib().rope_write_kv_cache(None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), *rest, tokens, count,
+    _check(lib().rope_write_kv_cache(None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), rest.pop(), k_at, v_at,
+                                     *rest, tokens, count,
                                      pages, page, width, bits, hq, hk, d, rot, angles, axes, *qs, *_strides(k, "k"),
                                      *_strides(v, "v"), eps, _stream(stream)))
 
@@ -564,7 +568,7 @@ def _attention(fn, q, k_cache, v_cache, out, starts, lens, table, workspace, hk,
     qs = _strides(q, "q")
     _typed(out, "torch.bfloat16", q.shape, "out")
     count, pages, width = _paged(k_cache, v_cache, starts, lens, table, page, hk, d, bits)
-    rest = _on_device_of(q, k_cache, v_cache, out, starts, lens, table, *workspace)
+    rest = _beside(q, k_cache, v_cache, out, starts, lens, table, *workspace)
     _check(fn(q.data_ptr(), *rest, *map(_nbytes, workspace), tokens, count, pages, page, width, bits, hq, hk, d, *qs, window,
               d ** -0.5 if scale is None else scale, cap, _stream(stream)))
 

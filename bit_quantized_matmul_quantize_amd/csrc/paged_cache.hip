@@ -22,7 +22,9 @@ namespace {
 
 constexpr uint32_t kTile = 16;     // places
 constexpr uint32_t kThreads = 256;
-constexpr uint32_t kGroups = 2048;  // workgroups, where there are heads to share out
+// Workgroups that the heads of a tile are shared out to: enough of them in all, and
+// four turns each where that leaves more (looking up the angles costs about two).
+constexpr uint32_t kEnough = 1024, kMore = 2048;
 
 struct Tile {
   PagedSpan span;
@@ -68,24 +70,22 @@ __device__ __forceinline__ uint4 pack8(const float *x) {
   return make_uint4(two_bf16(x[0], x[1]), two_bf16(x[2], x[3]), two_bf16(x[4], x[5]), two_bf16(x[6], x[7]));
 }
 
-// Codes of 16 values whose row's largest magnitude has the bits `top`: the
-// values are scaled by a power of two first, so that 127 / top is in range
-// whatever top is.  A row with a NaN or an infinity gets zero codes.
+// Codes of 16 values whose row's largest magnitude has the bits `top`.  127 / top is
+// in range from 2^-120 on; smaller rows are scaled up first.  A row with a NaN or
+// an infinity gets zero codes.
 __device__ __forceinline__ void quantize16(const float *x, uint32_t top, uint32_t *codes, float *scale) {
   const float t = __uint_as_float(top);
   const bool some = top != 0u && top < 0x7F800000u;
-  const int e = some ? __builtin_amdgcn_frexp_expf(t) : 0;
-  const float inv = some ? 127.0f / __builtin_amdgcn_ldexpf(t, -e) : 0.0f;
+  const float up = t < 0x1p-120f ? 0x1p+40f : 1.0f, inv = some ? 127.0f / (t * up) : 0.0f;
   *scale = t / 127.0f;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    uint32_t c = 0;
+    uint32_t c[4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const float y = some ? rintf(__builtin_amdgcn_ldexpf(x[4 * w + b], -e) * inv) : 0.0f;
-      c |= ((uint32_t)(int)y & 0xFFu) << (8 * b);
-    }
-    codes[w] = c;
+    for (int b = 0; b < 4; ++b) c[b] = (uint32_t)(int)(some ? rintf(x[4 * w + b] * up * inv) : 0.0f);
+    // the low bytes of four words
+    const uint32_t lo = __builtin_amdgcn_perm(c[1], c[0], 0x0C0C0400u), hi = __builtin_amdgcn_perm(c[3], c[2], 0x0C0C0400u);
+    codes[w] = lo | hi << 16;
   }
 }
 
@@ -226,7 +226,7 @@ __global__ __launch_bounds__(kThreads) void paged_write_kernel(PagedArgs a, uint
         *reinterpret_cast<uint4 *>(p + (uint64_t)run0 * page * 16u) = pack8(x);
         *reinterpret_cast<uint4 *>(p + (uint64_t)run1 * page * 16u) = pack8(x + 8);
       }
-    } else {
+    } else if (__any(!is_q && live)) {
       const uint32_t top = row_max(top16(x), G);
       if (!is_q && live && id >= 0) {
         uint32_t codes[4];
@@ -376,7 +376,7 @@ hipError_t launch_paged_write(const PagedArgs &a, hipStream_t s) {
   const uint32_t at_once = kThreads / (kTile * G), tiles = tiles_at_most(a);
   const uint32_t all_qk = (a.hq + a.hk + at_once - 1u) / at_once, all_v = (a.hk + at_once - 1u) / at_once;
   // as many workgroups for v as its share is
-  const uint32_t most = std::max(1u, kGroups / tiles), parts = std::min(all_qk, most);
+  const uint32_t parts = std::min(all_qk, std::max({1u, kEnough / tiles, std::min(kMore / tiles, all_qk / 4u)}));
   const uint32_t parts_v = std::min(all_v, std::max(1u, (uint32_t)((uint64_t)parts * all_v / all_qk)));
   const dim3 grid(tiles, parts + parts_v);
   switch (G) {
@@ -391,7 +391,7 @@ hipError_t launch_paged_write(const PagedArgs &a, hipStream_t s) {
 
 hipError_t launch_paged_read(const PagedArgs &a, hipStream_t s) {
   const uint32_t tiles = tiles_at_most(a);
-  const dim3 grid(tiles, std::min(2u * a.hk, std::max(1u, kGroups / tiles)));
+  const dim3 grid(tiles, std::min(2u * a.hk, std::max(1u, kMore / tiles)));
   hipLaunchKernelGGL(paged_read_kernel, grid, dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }

@@ -76,22 +76,26 @@ __host__ __device__ inline Parts parts_of(uint8_t *workspace, uint32_t slots, ui
 
 // ---- a run ------------------------------------------------------------------------
 
-// Waves of a SIMD that the registers are to suffice for.
-constexpr int waves_of(uint32_t dp, uint32_t bits, uint32_t nt) {
-  return dp > 128u ? 1 : bits == 16u ? (nt == 1u && dp <= 96u ? 3 : 2) : nt == 1u ? (dp <= 64u ? 3 : 2) : dp <= 64u ? 2 : 1;
-}
+// Waves of a SIMD that the registers are to suffice for.  Two where they do without
+// spills in the loop: one token of 96 sequences, heads of 80: 93 us, with three and
+// spills 105; eight tokens of 16 sequences, int8 heads of 128: 105 us, with one wave
+// 120; one of 16, bf16 heads of 256: 70 us with one, with two and spills 111.
+constexpr int waves_of(uint32_t dp, uint32_t bits) { return dp > 128u && bits == 16u ? 1 : 2; }
 
 // kDP: values of a head, rounded up (kExact: as they are); kNT: column blocks of 16
 // rows.
 // kCut: a workgroup takes a run of blocks, else one tile of rows and its sequence.
 template <uint32_t kDP, uint32_t kBits, uint32_t kNT, bool kExact, uint32_t kWaves, bool kCut>
-__global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits, kNT)) void paged_decode_kernel(PagedArgs a, uint32_t slots,
+__global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits)) void paged_decode_kernel(PagedArgs a, uint32_t slots,
                                                                                              float *sums, float2 *stats) {
   constexpr uint32_t kUnit = 128u / kBits;        // values of a unit
-  constexpr uint32_t kKeys = kUnit * 4u;          // keys of a step: a unit of v for each group of 16 lanes
+  constexpr uint32_t kKeys = kBits == 8u && kDP <= 128u ? 64 : 32;  // keys of a step
   constexpr uint32_t kKT = kKeys / 16u;           // their tiles
+  constexpr uint32_t kOwn = kKeys / 4u;           // keys of a group of 16 lanes: a unit of v, or half of one
+  typedef uint32_t Run __attribute__((ext_vector_type(kOwn * kBits / 32u)));  // its values of one dimension
   constexpr uint32_t kKS = (kDP / kUnit + 3u) / 4u;  // steps of a product over a head's values: four units each
-  constexpr uint32_t kHalves = kBits == 16u ? 1u : 2u;  // operands of a unit
+  constexpr uint32_t kHalves = kBits == 16u ? 1u : 2u;  // operands of a unit of k
+  constexpr uint32_t kHalvesV = kOwn / 8u;        // and of a group's keys of v
   constexpr uint32_t kDB = kDP / 16u;             // blocks of a head's values
   constexpr uint32_t kRows = 16u * kNT;
   constexpr uint32_t kPitch = kDP + 4u;           // of a row of sums in LDS
@@ -125,7 +129,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits, kNT)) void paged_
   // this lane's rows: places, and the operand of q
   const uint32_t page = 1u << a.page_shift, d = kExact ? kDP : a.d, block = paged_block_bytes(page, d, kBits), units = d / kUnit;
   int32_t pos[kNT], low[kNT];
-  constexpr bool kShared = kDP > 128;  // q in LDS, where a lane's registers do not suffice
+  constexpr bool kShared = kDP > 128 || kNT > 1;  // q in LDS, where a lane's registers do not suffice
   v4u q[kNT][kKS * kHalves];
 #pragma unroll
   for (uint32_t t = 0; t < kNT; ++t) {
@@ -213,20 +217,20 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits, kNT)) void paged_
     }
   };
 
-  v4u v[kDB];  // unit of keys 8 c.. or 16 c.. of the step
+  Run v[kDB];  // of keys kOwn c.. of the step
   v4f vs[kKT];
   auto load_v = [&](int32_t key0, const v4u &ids) {
-    const uint32_t t = c * kUnit / 16u;
+    const uint32_t t = c * kOwn / 16u;
     uint32_t id = ids[0];
 #pragma unroll
     for (uint32_t i = 1; i < kKT; ++i) id = t == i ? ids[i] : id;
     id = id < a.pages ? id : 0u;
-    const uint32_t off = (uint32_t)(key0 + (int32_t)(c * kUnit)) & (page - 1u);
-    const uint8_t *base = vc + id * page_bytes + ((uint64_t)(off / kUnit) * d + r) * 16u;
+    const uint32_t off = (uint32_t)(key0 + (int32_t)(c * kOwn)) & (page - 1u);
+    const uint8_t *base = vc + id * page_bytes + ((uint64_t)(off / kUnit) * d + r) * 16u + (kOwn < kUnit ? off % kUnit * (kBits / 8u) : 0u);
 #pragma unroll
     for (uint32_t b = 0; b < kDB; ++b) {
       // (beyond the head's values: the first again, whose sums are not taken)
-      v[b] = *reinterpret_cast<const v4u *>(base + (kExact || 16u * b < d ? b : 0u) * 256u);
+      v[b] = *reinterpret_cast<const Run *>(base + (kExact || 16u * b < d ? b : 0u) * 256u);
     }
     if constexpr (kBits == 8u) {
 #pragma unroll
@@ -283,7 +287,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits, kNT)) void paged_
   };
   // scores to weights, where the lanes' units of v want them.  hole: bit t where the
   // step's keys 16 t.. lie in no page; whole: all rows see all keys.
-  v4u ph[kNT][kHalves], pl[kNT][kHalves];
+  v4u ph[kNT][kHalvesV], pl[kNT][kHalvesV];
   auto weigh = [&](int32_t key0, uint32_t hole, bool whole) {
 #pragma unroll
     for (uint32_t n = 0; n < kNT; ++n) {
@@ -340,7 +344,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits, kNT)) void paged_
       auto turn = [&](uint32_t (&w)[kKT][2], v4u *out) {
 #pragma unroll
         for (uint32_t e = 0; e < 2; ++e) {
-          if constexpr (kBits == 16u) {
+          if constexpr (kKT == 2u) {
             const v2u s = __builtin_amdgcn_permlane32_swap(w[0][e], w[1][e], false, false);
             const v2u f = __builtin_amdgcn_permlane16_swap(s.x, s.y, false, false);
             out[0][e] = f.x;
@@ -352,8 +356,8 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits, kNT)) void paged_
             const v2u f1 = __builtin_amdgcn_permlane16_swap(s0.y, s1.y, false, false);
             out[0][e] = f0.x;
             out[0][2 + e] = f0.y;
-            out[kHalves - 1][e] = f1.x;
-            out[kHalves - 1][2 + e] = f1.y;
+            out[kHalvesV - 1][e] = f1.x;
+            out[kHalvesV - 1][2 + e] = f1.y;
           }
         }
       };
@@ -365,8 +369,12 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits, kNT)) void paged_
 #pragma unroll
     for (uint32_t b = 0; b < kDB; ++b)
 #pragma unroll
-      for (uint32_t h = 0; h < kHalves; ++h) {
-        const v4u u = kBits == 16u ? v[b] : bf16_of_codes(v[b][2 * h], v[b][2 * h + 1]);
+      for (uint32_t h = 0; h < kHalvesV; ++h) {
+        v4u u;
+        if constexpr (kBits == 16u)
+          u = v[b];
+        else
+          u = bf16_of_codes(v[b][2 * h], v[b][2 * h + 1]);
 #pragma unroll
         for (uint32_t n = 0; n < kNT; ++n) {
           o[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(u), as_bf(ph[n][h]), o[n][b], 0, 0, 0);
@@ -414,14 +422,16 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits, kNT)) void paged_
     if (mixed(key0)) continue;
     const bool whole = !hole && key0 + (int32_t)kKeys - 1 <= all_pos && key0 >= all_low && key0 + (int32_t)kKeys <= key_end;
     weigh(key0, hole, whole);
-    if (kBits == 16u && !whole) {
-      uint32_t seen = seen_in(key0, hole, any_low, any_pos);
-      asm volatile("" : "+v"(seen));  // (keeps this a branch)
-      v4u mask;
+    if constexpr (kBits == 16u) {
+      if (!whole) {
+        uint32_t seen = seen_in(key0, hole, any_low, any_pos);
+        asm volatile("" : "+v"(seen));  // (keeps this a branch)
+        v4u mask;
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) mask[i] = (seen >> (2u * i) & 1u ? 0xFFFFu : 0u) | (seen >> (2u * i + 1u) & 1u ? 0xFFFF0000u : 0u);
+        for (uint32_t i = 0; i < 4; ++i) mask[i] = (seen >> (2u * i) & 1u ? 0xFFFFu : 0u) | (seen >> (2u * i + 1u) & 1u ? 0xFFFF0000u : 0u);
 #pragma unroll
-      for (uint32_t b = 0; b < kDB; ++b) v[b] &= mask;
+        for (uint32_t b = 0; b < kDB; ++b) v[b] &= mask;
+      }
     }
     add_products();
   }
@@ -629,12 +639,13 @@ Plan plan_of(const PagedArgs &a) {
   const uint32_t g = a.hq / a.hk;
   const uint64_t rows = (uint64_t)a.tokens * g, mean = (rows + a.count - 1u) / a.count;
   Plan p;
-  p.blocks = mean <= 16u ? 1u : kMostBlocks;
+  // (wide int8 heads by 16 rows: 8 sequences of 4 tokens and 8 heads 46 us, by 32 53)
+  p.blocks = mean <= 16u || (a.d > 128u && a.bits == 8u) ? 1u : kMostBlocks;
   const uint32_t tile = 16u * p.blocks, dp = a.d <= 64u ? 64u : a.d <= 96u ? 96u : a.d <= 128u ? 128u : 256u;
   // (of a sequence with rows: at most one tile that is not full)
   p.tiles = (uint32_t)std::min<uint64_t>(rows / tile + std::min(a.count, a.tokens), (uint64_t)a.tokens * ((g + tile - 1u) / tile));
   // as many workgroups as the device holds at once (four waves: one to a SIMD)
-  p.slots = std::max(kCus * (uint32_t)waves_of(dp, a.bits, p.blocks) / a.hk, 1u);
+  p.slots = std::max(kCus * (uint32_t)waves_of(dp, a.bits) / a.hk, 1u);
   return p;
 }
 
@@ -666,7 +677,9 @@ hipError_t launch_rows(const PagedArgs &a, const Plan &plan, hipStream_t s) {
 
 template <uint32_t kDP, uint32_t kBits>
 hipError_t launch_heads(const PagedArgs &a, const Plan &plan, hipStream_t s) {
-  return plan.blocks == 1u ? launch_rows<kDP, kBits, 1>(a, plan, s) : launch_rows<kDP, kBits, kMostBlocks>(a, plan, s);
+  if constexpr (kDP <= 128u || kBits == 16u)
+    if (plan.blocks != 1u) return launch_rows<kDP, kBits, kMostBlocks>(a, plan, s);
+  return launch_rows<kDP, kBits, 1>(a, plan, s);
 }
 
 template <uint32_t kBits>
@@ -687,7 +700,7 @@ hipError_t launch_paged_decode(const PagedArgs &a, hipStream_t s) {
 // The two parts of each run, for tiles of the most rows and as many runs as any
 // form of the kernel has: what a call needs, whatever its tokens are.
 uint64_t paged_workspace_bytes(uint32_t hk, uint32_t d) {
-  const uint64_t slots = std::max(kCus * 3u / hk, 1u);
+  const uint64_t slots = std::max(kCus * 2u / hk, 1u);
   return 2u * slots * hk * 16u * kMostBlocks * (4ull * d + 8u);
 }
 
