@@ -15,6 +15,7 @@
 // operand of the second product as they are, given the order in which K's rows
 // are read: row 8 b + 4 h + j of the first product is key 16 (b / 2) + 8 h + 4 (b % 2) + j.
 #include <algorithm>
+#include <type_traits>
 
 #include "paged_common.h"
 
@@ -25,6 +26,10 @@ constexpr uint32_t kWaves = 4;
 constexpr uint32_t kThreads = 64 * kWaves;
 constexpr uint32_t kRows = 32 * kWaves;
 constexpr uint32_t kCus = 256;
+#ifndef AHEAD
+#define AHEAD 16
+#endif
+constexpr uint32_t kAheadWide = AHEAD;
 
 // 16 bytes a lane straight from memory into LDS: lane i's go to the wave's
 // destination + 16 i.  The kernel waits itself; no register is written.
@@ -134,7 +139,7 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
   auto low_of = [&](int32_t place) { return a.window ? (int32_t)max((int64_t)place + 1 - (int64_t)a.window, (int64_t)0) : 0; };
   const uint32_t row0 = tile * kRows, row1 = min(row0 + kRows, rows) - 1u;
   const int32_t end = min(p.keys, max(place_of(row1) + 1, 0));
-  const int32_t begin = low_of(place_of(row0)) / (int32_t)kKT * (int32_t)kKT;
+  const int32_t first = low_of(place_of(row0)), begin = first / (int32_t)kKT * (int32_t)kKT;  // keys that any row sees: [first, end)
   const uint32_t wrow0 = row0 + wave * 32u, wrow1 = min(wrow0 + 32u, rows) - 1u;
   const bool idle = wrow0 >= rows;
   // keys that all rows of the wave see lie in [whole_low, whole_end), those that any sees in [any_low, any_end)
@@ -255,33 +260,57 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
   const uint32_t k_row = 16u * (r >> 4) + 8u * ((r >> 2) & 1u) + 4u * ((r >> 3) & 1u) + (r & 3u);
   const uint32_t k_at = (half * kKT + k_row) * 16u, v_at = (half * kDP + r) * 16u;
 
+  // 0 * NaN must not reach a row that does not see the NaN's key.  Values that no row
+  // of the workgroup sees are zeroed in LDS.  A tile with a NaN or an infinity that
+  // some rows see and others do not is left for a second loop, in which it counts as
+  // zero in the product and is added afterwards where it is seen.  (Codes are finite.)
+  auto any_unseen = [&](int32_t key0, uint64_t hole) { return kBits == 16 && (hole || key0 + (int32_t)kKT > end || key0 < first); };
+  auto zero_unseen = [&](int32_t key0, uint32_t stage, uint64_t hole) {
+#pragma unroll 1
+    for (uint32_t i = threadIdx.x; i < S::kTile / 16u; i += kThreads) {
+      const uint32_t group = i / kDP;  // of eight keys
+      const int32_t at = key0 + (int32_t)(8u * group), from = max(first - at, 0), to = min(end - 1 - at, 7);
+      const uint32_t seen = hole >> (8u * group & ~15u) & 1u || from > to ? 0u : (0xFFu >> (7 - to)) & (0xFFu << from);
+      v4u *u = reinterpret_cast<v4u *>(lds + stage * S::kStage + S::kTile + i * 16u), v = *u;
+#pragma unroll
+      for (uint32_t e = 0; e < 4; ++e) v[e] &= (seen >> (2u * e) & 1u ? 0xFFFFu : 0u) | (seen >> (2u * e + 1u) & 1u ? 0xFFFF0000u : 0u);
+      *u = v;
+    }
+  };
+  auto not_finite = [&](uint32_t stage) {
+    bool bad = false;
+#pragma unroll 1
+    for (uint32_t i = lane; i < S::kTile / 16u; i += 64u)
+      bad |= any_not_finite(*reinterpret_cast<const v4u *>(lds + stage * S::kStage + S::kTile + i * 16u));
+    return __ballot(bad) != 0u;
+  };
+
   // One tile.  hole: bit 16 t where the tile's keys 16 t.. lie in no page; whole: all
-  // rows of the wave see all of it.
-  auto compute = [&](int32_t key0, uint32_t stage, uint64_t hole, bool whole) {
+  // rows of the wave see all of it; bad: it has values that are not finite.
+  auto compute = [&](auto bad, int32_t key0, uint32_t stage, uint64_t hole, bool whole) {
+    constexpr bool kBad = decltype(bad)::value;
     const uint8_t *kt = lds + stage * S::kStage + k_at, *vt = lds + stage * S::kStage + S::kTile + v_at;
     const float *scales = reinterpret_cast<const float *>(lds + stage * S::kStage + 2u * S::kTile) + 8u * half;
-    // the operands of a half tile are read while the last one's are used
-    auto read_k = [&](uint32_t f, uint32_t s) { return *reinterpret_cast<const v4u *>(kt + (2u * s * kKT + 32u * f) * 16u); };
-    auto read_v = [&](uint32_t f, uint32_t i) {
-      return *reinterpret_cast<const v4u *>(vt + ((4u * f + 2u * (i / kDB)) * kDP + 32u * (i % kDB)) * 16u);
+    // operands are read kAhead products before they are used, those of the second
+    // product's begin before the softmax
+    auto read_k = [&](uint32_t n) { return *reinterpret_cast<const v4u *>(kt + (2u * (n % kDS) * kKT + 32u * (n / kDS)) * 16u); };
+    auto read_v = [&](uint32_t n) {
+      return *reinterpret_cast<const v4u *>(vt + ((2u * (n / kDB)) * kDP + 32u * (n % kDB)) * 16u);
     };
+    constexpr uint32_t kAhead = kDP > 128 ? kAheadWide : 8, kFirst = kHalves * kDS, kSecond = kHalves * 2u * kDB;
     v16f x[kHalves];
-    v4u k[2][kDS], v[2][2 * kDB];
+    v4u ring[kAhead];
 #pragma unroll
-    for (uint32_t s = 0; s < kDS; ++s) k[0][s] = read_k(0, s);
+    for (uint32_t n = 0; n < kAhead; ++n) ring[n] = read_k(n);
 #pragma unroll
-    for (uint32_t f = 0; f < kHalves; ++f) {
+    for (uint32_t f = 0; f < kHalves; ++f)
 #pragma unroll
       for (uint32_t i = 0; i < 16; ++i) x[f][i] = 0.0f;
 #pragma unroll
-      for (uint32_t s = 0; s < kDS; ++s) {
-        x[f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(k[f & 1][s]), as_bf(q[s]), x[f], 0, 0, 0);
-        if (f + 1u < kHalves)
-          k[~f & 1][s] = read_k(f + 1u, s);
-        else
-          v[0][s] = read_v(0, s);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+    for (uint32_t n = 0; n < kFirst; ++n) {
+      x[n / kDS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(ring[n % kAhead]), as_bf(q[n % kDS]), x[n / kDS], 0, 0, 0);
+      ring[n % kAhead] = n + kAhead < kFirst ? read_k(n + kAhead) : read_v(n + kAhead - kFirst);
+      __builtin_amdgcn_sched_barrier(0);
     }
     // x: of keys 32 f + 16 (i / 8) + 8 half + i % 8
 #pragma unroll
@@ -348,33 +377,16 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
         }
         w[f][i / 8u][i % 8u / 2u] = two_bf16(y0, y1);
       }
-    // A NaN or an infinity among the values of a tile that not every row sees whole:
-    // 0 * NaN must not reach the rows that do not see its key.  It counts as zero in
-    // the product, and is added afterwards where it is seen.
-    bool bad = false;
-    if (kBits == 16 && !whole) {
-#pragma unroll 1
-      for (uint32_t i = lane; i < S::kTile / 16u; i += 64u)
-        bad |= any_not_finite(*reinterpret_cast<const v4u *>(lds + stage * S::kStage + S::kTile + i * 16u));
-      bad = __ballot(bad) != 0u;
+#pragma unroll
+    for (uint32_t n = 0; n < kSecond; ++n) {
+      // (the operand of product n, for the first and the second product the same place of the ring)
+      const uint32_t at = (kFirst + n) % kAhead, b = n % kDB, kk = n / kDB;
+      if constexpr (kBad) ring[at] = finite_only(ring[at]);
+      o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(ring[at]), as_bf(w[kk / 2u][kk % 2u]), o[b], 0, 0, 0);
+      if (n + kAhead < kSecond) ring[at] = read_v(n + kAhead);
+      if (n % kAhead == kAhead - 1u) __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (uint32_t f = 0; f < kHalves; ++f) {
-      if (bad) {
-#pragma unroll
-        for (uint32_t i = 0; i < 2u * kDB; ++i) {
-          asm volatile("" : "+v"(v[f & 1][i]));
-          v[f & 1][i] = finite_only(v[f & 1][i]);
-        }
-      }
-#pragma unroll
-      for (uint32_t i = 0; i < 2u * kDB; ++i) {
-        o[i % kDB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(v[f & 1][i]), as_bf(w[f][i / kDB]), o[i % kDB], 0, 0, 0);
-        if (f + 1u < kHalves) v[~f & 1][i] = read_v(f + 1u, i);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-    if (bad) {
+    if constexpr (kBad) {
 #pragma unroll 1
       for (uint32_t t = 0; t < kSubs; ++t) {
         const uint32_t seen = seen_of(t);
@@ -396,6 +408,9 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
     }
   };
 
+  auto whole_at = [&](int32_t key0, uint64_t hole) { return !hole && key0 >= whole_low && key0 + (int32_t)kKT <= whole_end; };
+  auto some_at = [&](int32_t key0) { return key0 < any_end && key0 + (int32_t)kKT > any_low; };
+  bool later = false;
   uint32_t id = id_of(begin);
   if (begin < end) bring(begin, id, 0);
   settle(0);
@@ -410,9 +425,37 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
     if (more) bring(key0 + (int32_t)kKT, next_id, stage ^ 1u);
     id = next_id;
     next_id = id_of(key0 + 2 * (int32_t)kKT);
-    if (key0 < any_end && key0 + (int32_t)kKT > any_low)
-      compute(key0, stage, hole, !hole && key0 >= whole_low && key0 + (int32_t)kKT <= whole_end);
+    if (any_unseen(key0, hole)) {
+      zero_unseen(key0, stage, hole);
+      __syncthreads();
+    }
+    if (some_at(key0)) {
+      const bool whole = whole_at(key0, hole);
+      if (kBits == 16 && !whole && not_finite(stage))
+        later = true;
+      else
+        compute(std::false_type{}, key0, stage, hole, whole);
+    }
     if (more) settle(stage ^ 1u);
+  }
+  if constexpr (kBits == 16) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (__syncthreads_or(later)) {
+#pragma unroll 1
+      for (int32_t key0 = begin; key0 < end; key0 += (int32_t)kKT) {
+        id = id_of(key0);
+        const uint64_t hole = __ballot(id >= a.pages);
+        bring(key0, id, 0);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (any_unseen(key0, hole)) {
+          zero_unseen(key0, 0, hole);
+          __syncthreads();
+        }
+        if (some_at(key0) && !whole_at(key0, hole) && not_finite(0)) compute(std::true_type{}, key0, 0, hole, false);
+        __syncthreads();
+      }
+    }
   }
 
   // rows leave through LDS, where the stages were (each wave's own part)
