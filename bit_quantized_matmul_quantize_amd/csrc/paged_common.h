@@ -99,6 +99,11 @@ __device__ __forceinline__ uint32_t two_bf16(float lo, float hi) {
   v[1] = (__bf16)hi;
   return __builtin_bit_cast(uint32_t, v);
 }
+// sum + the two values, in binary32.
+__device__ __forceinline__ float add_two_bf16(uint32_t two, float sum) {
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf, two), __builtin_bit_cast(v2bf, 0x3F803F80u), sum, false);
+}
 // Eight codes as bf16 (exact).
 __device__ __forceinline__ v4u bf16_of_codes(uint32_t a, uint32_t b) {
   v4u r;

@@ -15,7 +15,6 @@
 // operand of the second product as they are, given the order in which K's rows
 // are read: row 8 b + 4 h + j of the first product is key 16 (b / 2) + 8 h + 4 (b % 2) + j.
 #include <algorithm>
-#include <type_traits>
 
 #include "paged_common.h"
 
@@ -27,9 +26,8 @@ constexpr uint32_t kThreads = 64 * kWaves;
 constexpr uint32_t kRows = 32 * kWaves;
 constexpr uint32_t kCus = 256;
 #ifndef AHEAD
-#define AHEAD 16
+#define AHEAD 4
 #endif
-constexpr uint32_t kAheadWide = AHEAD;
 
 // 16 bytes a lane straight from memory into LDS: lane i's go to the wave's
 // destination + 16 i.  The kernel waits itself; no register is written.
@@ -44,8 +42,10 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, const uint8_t *from) {
 // kRuns of them, 1024 bytes apart in memory and in LDS.
 template <uint32_t kRuns>
 __device__ __forceinline__ void load_run_to_lds(uint32_t lds, uint32_t offset, const uint8_t *base) {
-  static_assert(kRuns >= 2 && kRuns <= 4, "");
-  if constexpr (kRuns == 2)
+  static_assert(kRuns >= 1 && kRuns <= 4, "");
+  if constexpr (kRuns == 1)
+    load_to_lds(lds, offset, base);
+  else if constexpr (kRuns == 2)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\t"
                  "global_load_lds_dwordx4 %1, %2 offset:1024" ::"s"(lds), "v"(offset), "s"(base) : "memory", "m0");
   else if constexpr (kRuns == 3)
@@ -118,7 +118,7 @@ __device__ __forceinline__ bool take_tile(const PagedArgs &a, uint32_t item, uin
 // kExact: a head has kDP values, and a page has at least a tile's keys.
 // kCap: scores are capped (both may be, unless kExact).
 template <uint32_t kDP, uint32_t kBits, bool kExact, bool kCap>
-__global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_kernel(PagedArgs a) {
+__global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a) {
   using S = Shape<kDP, kBits>;
   constexpr uint32_t kKT = S::kKT, kSubs = S::kSubs;
   constexpr uint32_t kHalves = kKT / 32;  // halves of a tile: 32 keys
@@ -184,44 +184,61 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
   constexpr uint32_t kUnit = 128 / kBits;
   constexpr bool kFull = kParts * kThreads * 16 == S::kTile * kBits / 16;  // every thread has a unit in every part
   v4u kr[kBits == 8 ? kParts : 1], vr[kBits == 8 ? kParts : 1];
-  float scale_r = 0.0f;
-  auto bring = [&](int32_t key0, uint32_t id, uint32_t stage) {
-    const uint32_t off0 = (uint32_t)key0 & (page - 1u);
+  float k_scale = 0.0f, v_scale = 0.0f;
+  auto bring_k = [&](int32_t key0, uint32_t id, uint32_t stage) {
+    const uint32_t off0 = (uint32_t)key0 & (page - 1u), key = lane % kKT, ko = (uint32_t)(key0 + (int32_t)key) & (page - 1u);
     const bool one_page = kExact || page >= kKT;
     const uint32_t id0 = known(__builtin_amdgcn_readfirstlane(id));
-    const uint8_t *k0 = kc + id0 * page_bytes + off0 * 16u, *v0 = vc + id0 * page_bytes + (uint64_t)(off0 / kUnit) * d * 16u;
+    const uint8_t *k0 = kc + id0 * page_bytes + off0 * 16u;
     const uint8_t *mine = kc + known(id) * page_bytes;  // (its key is the same in all parts)
-    const uint32_t key = lane % kKT, ko = (uint32_t)(key0 + (int32_t)key) & (page - 1u);
-    if constexpr (kBits == 16 && kExact) {
-      const uint32_t to = lds0 + stage * S::kStage + wave * kParts * 1024u;
 #pragma unroll
-      for (uint32_t j = 0; j < kParts; ++j)
-        load_to_lds(to + j * 1024u, (lane / kKT * page + key) * 16u, k0 + (uint64_t)((wave * kParts + j) * (64u / kKT)) * page * 16u);
-      load_run_to_lds<kParts>(to + S::kTile, lane * 16u, v0 + wave * kParts * 1024u);
-    } else {
-#pragma unroll
-      for (uint32_t j = 0; j < kParts; ++j) {
-        const uint32_t i = (wave * kParts + j) * 64u + lane, ku = i / kKT, vg = i / kDP, dim = i % kDP;
-        const bool has_k = (kExact && kFull) || ku * kUnit < d, has_v = (kExact && kFull) || (dim < d && vg * kUnit < kKT);
-        const uint32_t vo = (uint32_t)(key0 + (int32_t)(vg * kUnit)) & (page - 1u);
-        // (the lanes of a wave's 64 units may lie in two groups of keys where kDP is no multiple of 64)
-        const uint32_t sub = vg * kUnit / 16u * 16u;
-        const uint32_t vid = one_page ? id0 : known(kDP % 64u == 0u ? (uint32_t)__builtin_amdgcn_readlane((int)id, (int)__builtin_amdgcn_readfirstlane(sub % 64u)) : (uint32_t)__shfl((int)id, (int)(sub % 64u), 64));
-        const uint8_t *k_from = one_page ? k0 + (ku * page + key) * 16u : mine + (ku * page + ko) * 16u;
-        const uint8_t *v_from = one_page ? v0 + (vg * d + dim) * 16u : vc + vid * page_bytes + ((uint64_t)(vo / kUnit) * d + dim) * 16u;
-        if constexpr (kBits == 16) {
-          const uint32_t to = lds0 + stage * S::kStage + (wave * kParts + j) * 1024u;
-          if (has_k) load_to_lds(to, k_from);
-          if (has_v) load_to_lds(to + S::kTile, v_from);
-        } else {
-          if (has_k) kr[j] = *reinterpret_cast<const v4u *>(k_from);
-          if (has_v) vr[j] = *reinterpret_cast<const v4u *>(v_from);
+    for (uint32_t j = 0; j < kParts; ++j) {
+      const uint32_t to = lds0 + stage * S::kStage + (wave * kParts + j) * 1024u;
+      if constexpr (kBits == 16 && kExact) {
+        load_to_lds(to, (lane / kKT * page + key) * 16u, k0 + (uint64_t)((wave * kParts + j) * (64u / kKT)) * page * 16u);
+      } else {
+        const uint32_t ku = ((wave * kParts + j) * 64u + lane) / kKT;
+        const uint8_t *from = one_page ? k0 + (ku * page + key) * 16u : mine + (ku * page + ko) * 16u;
+        if ((kExact && kFull) || ku * kUnit < d) {
+          if constexpr (kBits == 16)
+            load_to_lds(to, from);
+          else
+            kr[j] = *reinterpret_cast<const v4u *>(from);
         }
       }
     }
     if constexpr (kBits == 8) {
-      if (threadIdx.x < 2u * kKT)
-        scale_r = *reinterpret_cast<const float *>((threadIdx.x < kKT ? kc : vc) + known(id) * page_bytes + page * d + ko * 4u);
+      if (threadIdx.x < kKT) k_scale = *reinterpret_cast<const float *>(kc + known(id) * page_bytes + page * d + ko * 4u);
+    }
+  };
+  auto bring_v = [&](int32_t key0, uint32_t id, uint32_t stage) {
+    const uint32_t off0 = (uint32_t)key0 & (page - 1u);
+    const bool one_page = kExact || page >= kKT;
+    const uint32_t id0 = known(__builtin_amdgcn_readfirstlane(id));
+    const uint8_t *v0 = vc + id0 * page_bytes + (uint64_t)(off0 / kUnit) * d * 16u;
+    const uint32_t to = lds0 + stage * S::kStage + S::kTile + wave * kParts * 1024u;
+    if constexpr (kBits == 16 && kExact) {
+      load_run_to_lds<kParts>(to, lane * 16u, v0 + wave * kParts * 1024u);
+    } else {
+#pragma unroll
+      for (uint32_t j = 0; j < kParts; ++j) {
+        const uint32_t i = (wave * kParts + j) * 64u + lane, vg = i / kDP, dim = i % kDP;
+        const uint32_t vo = (uint32_t)(key0 + (int32_t)(vg * kUnit)) & (page - 1u);
+        // (the lanes of a wave's 64 units may lie in two groups of keys where kDP is no multiple of 64)
+        const uint32_t sub = vg * kUnit / 16u * 16u;
+        const uint32_t vid = one_page ? id0 : known(kDP % 64u == 0u ? (uint32_t)__builtin_amdgcn_readlane((int)id, (int)__builtin_amdgcn_readfirstlane(sub % 64u)) : (uint32_t)__shfl((int)id, (int)(sub % 64u), 64));
+        const uint8_t *from = one_page ? v0 + (vg * d + dim) * 16u : vc + vid * page_bytes + ((uint64_t)(vo / kUnit) * d + dim) * 16u;
+        if ((kExact && kFull) || (dim < d && vg * kUnit < kKT)) {
+          if constexpr (kBits == 16)
+            load_to_lds(to + j * 1024u, from);
+          else
+            vr[j] = *reinterpret_cast<const v4u *>(from);
+        }
+      }
+    }
+    if constexpr (kBits == 8) {
+      const uint32_t ko = (uint32_t)(key0 + (int32_t)(lane % kKT)) & (page - 1u);
+      if (threadIdx.x < kKT) v_scale = *reinterpret_cast<const float *>(vc + known(id) * page_bytes + page * d + ko * 4u);
     }
   };
   // an int8 tile from registers into LDS
@@ -242,7 +259,11 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
           *reinterpret_cast<v4u *>(to + S::kTile + ((2u * vg + 1u) * kDP + dim) * 16u) = bf16_of_codes(vr[j][2], vr[j][3]);
         }
       }
-      if (threadIdx.x < 2u * kKT) reinterpret_cast<float *>(to + 2u * S::kTile)[threadIdx.x] = scale_r;
+      float *scales = reinterpret_cast<float *>(to + 2u * S::kTile);
+      if (threadIdx.x < kKT) {
+        scales[threadIdx.x] = k_scale;
+        scales[kKT + threadIdx.x] = v_scale;
+      }
     }
   };
 
@@ -260,12 +281,14 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
   const uint32_t k_row = 16u * (r >> 4) + 8u * ((r >> 2) & 1u) + 4u * ((r >> 3) & 1u) + (r & 3u);
   const uint32_t k_at = (half * kKT + k_row) * 16u, v_at = (half * kDP + r) * 16u;
 
-  // 0 * NaN must not reach a row that does not see the NaN's key.  Values that no row
-  // of the workgroup sees are zeroed in LDS.  A tile with a NaN or an infinity that
-  // some rows see and others do not is left for a second loop, in which it counts as
-  // zero in the product and is added afterwards where it is seen.  (Codes are finite.)
-  auto any_unseen = [&](int32_t key0, uint64_t hole) { return kBits == 16 && (hole || key0 + (int32_t)kKT > end || key0 < first); };
-  auto zero_unseen = [&](int32_t key0, uint32_t stage, uint64_t hole) {
+  // 0 * NaN must not reach a row that does not see the NaN's key.  Of tiles that not
+  // every row of the workgroup sees whole, values that no row sees and values that
+  // are not finite are zeroed in LDS; a second loop adds the latter where they are
+  // seen.  (Codes are finite.)
+  const int32_t all_low = low_of(place_of(row1)), all_end = min(p.keys, place_of(row0) + 1);  // seen by all rows
+  auto whole_for_all = [&](int32_t key0, uint64_t hole) { return !hole && key0 >= all_low && key0 + (int32_t)kKT <= all_end; };
+  auto zero_some = [&](int32_t key0, uint32_t stage, uint64_t hole) {  // returns whether some are not finite
+    bool bad = false;
 #pragma unroll 1
     for (uint32_t i = threadIdx.x; i < S::kTile / 16u; i += kThreads) {
       const uint32_t group = i / kDP;  // of eight keys
@@ -274,31 +297,31 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
       v4u *u = reinterpret_cast<v4u *>(lds + stage * S::kStage + S::kTile + i * 16u), v = *u;
 #pragma unroll
       for (uint32_t e = 0; e < 4; ++e) v[e] &= (seen >> (2u * e) & 1u ? 0xFFFFu : 0u) | (seen >> (2u * e + 1u) & 1u ? 0xFFFF0000u : 0u);
-      *u = v;
+      bad |= any_not_finite(v);
+      *u = finite_only(v);
     }
+    return __syncthreads_or(bad) != 0;
   };
-  auto not_finite = [&](uint32_t stage) {
-    bool bad = false;
-#pragma unroll 1
-    for (uint32_t i = lane; i < S::kTile / 16u; i += 64u)
-      bad |= any_not_finite(*reinterpret_cast<const v4u *>(lds + stage * S::kStage + S::kTile + i * 16u));
-    return __ballot(bad) != 0u;
+
+  auto whole_at = [&](int32_t key0, uint64_t hole) { return !hole && key0 >= whole_low && key0 + (int32_t)kKT <= whole_end; };
+  auto some_at = [&](int32_t key0) { return key0 < any_end && key0 + (int32_t)kKT > any_low; };
+  // the keys 16 t.. of a tile that this row sees: of key0 + 16 t + 8 half + i, bit i
+  auto seen_of = [&](int32_t key0, uint64_t hole, uint32_t t) {
+    const int32_t at = key0 + (int32_t)(16u * t + 8u * half), from = max(low - at, 0), to = min(min(pos, p.keys - 1) - at, 7);
+    return hole >> (16u * t) & 1u || from > to ? 0u : (0xFFu >> (7 - to)) & (0xFFu << from);
   };
 
   // One tile.  hole: bit 16 t where the tile's keys 16 t.. lie in no page; whole: all
-  // rows of the wave see all of it; bad: it has values that are not finite.
-  auto compute = [&](auto bad, int32_t key0, uint32_t stage, uint64_t hole, bool whole) {
-    constexpr bool kBad = decltype(bad)::value;
+  // rows of the wave see all of it.
+  auto compute = [&](int32_t key0, uint32_t stage, uint64_t hole, bool whole) {
     const uint8_t *kt = lds + stage * S::kStage + k_at, *vt = lds + stage * S::kStage + S::kTile + v_at;
     const float *scales = reinterpret_cast<const float *>(lds + stage * S::kStage + 2u * S::kTile) + 8u * half;
     // operands are read kAhead products before they are used, those of the second
-    // product's begin before the softmax
+    // product from before the softmax on
     auto read_k = [&](uint32_t n) { return *reinterpret_cast<const v4u *>(kt + (2u * (n % kDS) * kKT + 32u * (n / kDS)) * 16u); };
-    auto read_v = [&](uint32_t n) {
-      return *reinterpret_cast<const v4u *>(vt + ((2u * (n / kDB)) * kDP + 32u * (n % kDB)) * 16u);
-    };
-    constexpr uint32_t kAhead = kDP > 128 ? kAheadWide : 8, kFirst = kHalves * kDS, kSecond = kHalves * 2u * kDB;
-    v16f x[kHalves];
+    auto read_v = [&](uint32_t n) { return *reinterpret_cast<const v4u *>(vt + (2u * (n / kDB) * kDP + 32u * (n % kDB)) * 16u); };
+    constexpr uint32_t kAhead = kDP > 128 ? AHEAD : 8, kFirst = kHalves * kDS, kSecond = kHalves * 2u * kDB;
+    v16f x[kHalves];  // of keys 32 f + 16 (i / 8) + 8 half + i % 8
     v4u ring[kAhead];
 #pragma unroll
     for (uint32_t n = 0; n < kAhead; ++n) ring[n] = read_k(n);
@@ -312,7 +335,6 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
       ring[n % kAhead] = n + kAhead < kFirst ? read_k(n + kAhead) : read_v(n + kAhead - kFirst);
       __builtin_amdgcn_sched_barrier(0);
     }
-    // x: of keys 32 f + 16 (i / 8) + 8 half + i % 8
 #pragma unroll
     for (uint32_t f = 0; f < kHalves; ++f) {
       if constexpr (kBits == 8) {
@@ -328,17 +350,12 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
         for (uint32_t i = 0; i < 16; ++i) x[f][i] = capped(x[f][i], cap2, inv2);
       }
     }
-    // the keys 16 t.. of the tile that this row sees: of key0 + 16 t + 8 half + i, bit i
-    auto seen_of = [&](uint32_t t) {
-      const int32_t at = key0 + (int32_t)(16u * t + 8u * half), from = max(low - at, 0), to = min(min(pos, p.keys - 1) - at, 7);
-      return hole >> (16u * t) & 1u || from > to ? 0u : (0xFFu >> (7 - to)) & (0xFFu << from);
-    };
     if (!whole) {
 #pragma unroll
       for (uint32_t f = 0; f < kHalves; ++f)
 #pragma unroll
         for (uint32_t kk = 0; kk < 2; ++kk) {
-          uint32_t seen = seen_of(2u * f + kk);
+          uint32_t seen = seen_of(key0, hole, 2u * f + kk);
           asm volatile("" : "+v"(seen));  // (keeps this a branch: selects in every tile cost a tenth of it)
 #pragma unroll
           for (uint32_t i = 0; i < 8; ++i) x[f][8u * kk + i] = seen >> i & 1u ? x[f][8u * kk + i] : -INFINITY;
@@ -362,58 +379,41 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
         for (uint32_t i = 0; i < 16; ++i) o[b][i] *= keep;
     }
     const float base = m == -INFINITY ? 0.0f : m;
-    // weights, rounded to bf16 for the matrix cores: 2^-8 of each at most, as the output is rounded
+    // Weights, rounded to bf16 for the matrix cores: 2^-8 of each at most, as the
+    // output is rounded.  Their sum is that of the rounded ones (bf16), so that weights
+    // and sum are off together.
     v4u w[kHalves][2];
 #pragma unroll
     for (uint32_t f = 0; f < kHalves; ++f)
 #pragma unroll
       for (uint32_t i = 0; i < 16; i += 2) {
         float y0 = exp2_hw(fmaf(x[f][i], scale2, -base)), y1 = exp2_hw(fmaf(x[f][i + 1], scale2, -base));
-        l += y0 + y1;
         if constexpr (kBits == 8) {
+          l += y0 + y1;
           const float2 s = *reinterpret_cast<const float2 *>(scales + kKT + 32u * f + 16u * (i / 8u) + i % 8u);
           y0 = x[f][i] == -INFINITY ? 0.0f : y0 * s.x;
           y1 = x[f][i + 1] == -INFINITY ? 0.0f : y1 * s.y;
         }
-        w[f][i / 8u][i % 8u / 2u] = two_bf16(y0, y1);
+        const uint32_t two = two_bf16(y0, y1);
+        if constexpr (kBits == 16) l = add_two_bf16(two, l);
+        w[f][i / 8u][i % 8u / 2u] = two;
       }
 #pragma unroll
     for (uint32_t n = 0; n < kSecond; ++n) {
-      // (the operand of product n, for the first and the second product the same place of the ring)
       const uint32_t at = (kFirst + n) % kAhead, b = n % kDB, kk = n / kDB;
-      if constexpr (kBad) ring[at] = finite_only(ring[at]);
       o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(ring[at]), as_bf(w[kk / 2u][kk % 2u]), o[b], 0, 0, 0);
       if (n + kAhead < kSecond) ring[at] = read_v(n + kAhead);
-      if (n % kAhead == kAhead - 1u) __builtin_amdgcn_sched_barrier(0);
-    }
-    if constexpr (kBad) {
-#pragma unroll 1
-      for (uint32_t t = 0; t < kSubs; ++t) {
-        const uint32_t seen = seen_of(t);
-        v4u ones;  // 1 for the keys that are seen
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) ones[i] = (seen >> (2u * i) & 1u ? 0x3F80u : 0u) | (seen >> (2u * i + 1u) & 1u ? 0x3F800000u : 0u);
-#pragma unroll
-        for (uint32_t b = 0; b < kDB; ++b) {
-          const v4u u = *reinterpret_cast<const v4u *>(vt + (2u * t * kDP + 32u * b) * 16u);
-          v16f marks;
-#pragma unroll
-          for (uint32_t i = 0; i < 16; ++i) marks[i] = 0.0f;
-          marks = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(not_finite_marks(u)), as_bf(ones), marks, 0, 0, 0);
-#pragma unroll
-          for (uint32_t i = 0; i < 16; ++i) o[b][i] += of_marks(marks[i]);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
-  auto whole_at = [&](int32_t key0, uint64_t hole) { return !hole && key0 >= whole_low && key0 + (int32_t)kKT <= whole_end; };
-  auto some_at = [&](int32_t key0) { return key0 < any_end && key0 + (int32_t)kKT > any_low; };
   bool later = false;
   uint32_t id = id_of(begin);
-  if (begin < end) bring(begin, id, 0);
-  settle(0);
+  if (begin < end) {
+    bring_k(begin, id, 0);
+    bring_v(begin, id, 0);
+    settle(0);
+  }
   uint32_t next_id = id_of(begin + (int32_t)kKT);
   uint32_t stage = 0;
   for (int32_t key0 = begin; key0 < end; key0 += (int32_t)kKT, stage ^= 1u) {
@@ -422,37 +422,44 @@ __global__ __launch_bounds__(kThreads, kDP <= 128 ? 2 : 1) void paged_prefill_ke
     __syncthreads();
     const uint64_t hole = __ballot(id >= a.pages);
     const bool more = key0 + (int32_t)kKT < end;
-    if (more) bring(key0 + (int32_t)kKT, next_id, stage ^ 1u);
+    if (more) {
+      bring_k(key0 + (int32_t)kKT, next_id, stage ^ 1u);
+      bring_v(key0 + (int32_t)kKT, next_id, stage ^ 1u);
+    }
     id = next_id;
     next_id = id_of(key0 + 2 * (int32_t)kKT);
-    if (any_unseen(key0, hole)) {
-      zero_unseen(key0, stage, hole);
-      __syncthreads();
-    }
-    if (some_at(key0)) {
-      const bool whole = whole_at(key0, hole);
-      if (kBits == 16 && !whole && not_finite(stage))
-        later = true;
-      else
-        compute(std::false_type{}, key0, stage, hole, whole);
-    }
+    if (kBits == 16 && !whole_for_all(key0, hole)) later |= zero_some(key0, stage, hole);
+    if (some_at(key0)) compute(key0, stage, hole, whole_at(key0, hole));
     if (more) settle(stage ^ 1u);
   }
   if constexpr (kBits == 16) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    if (__syncthreads_or(later)) {
+    if (later) {  // (the same for the whole workgroup)
 #pragma unroll 1
       for (int32_t key0 = begin; key0 < end; key0 += (int32_t)kKT) {
         id = id_of(key0);
         const uint64_t hole = __ballot(id >= a.pages);
-        bring(key0, id, 0);
+        if (whole_for_all(key0, hole)) continue;
+        bring_v(key0, id, 0);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        if (any_unseen(key0, hole)) {
-          zero_unseen(key0, 0, hole);
-          __syncthreads();
+#pragma unroll 1
+        for (uint32_t t = 0; t < kSubs; ++t) {
+          const uint32_t seen = seen_of(key0, hole, t);
+          v4u ones;  // 1 for the keys that are seen
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i) ones[i] = (seen >> (2u * i) & 1u ? 0x3F80u : 0u) | (seen >> (2u * i + 1u) & 1u ? 0x3F800000u : 0u);
+#pragma unroll
+          for (uint32_t b = 0; b < kDB; ++b) {
+            const v4u u = *reinterpret_cast<const v4u *>(lds + S::kTile + v_at + (2u * t * kDP + 32u * b) * 16u);
+            v16f marks;
+#pragma unroll
+            for (uint32_t i = 0; i < 16; ++i) marks[i] = 0.0f;
+            marks = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(not_finite_marks(u)), as_bf(ones), marks, 0, 0, 0);
+#pragma unroll
+            for (uint32_t i = 0; i < 16; ++i) o[b][i] += of_marks(marks[i]);
+            __builtin_amdgcn_sched_barrier(0);
+          }
         }
-        if (some_at(key0) && !whole_at(key0, hole) && not_finite(0)) compute(std::true_type{}, key0, 0, hole, false);
         __syncthreads();
       }
     }

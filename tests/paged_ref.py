@@ -131,6 +131,7 @@ def attention(case, window=0, cap=0.0, scale=None):
 def bound(case, out, size, most, form, cap=0.0):
     """How far an output may be off: half a step of bf16, 2^-8 of it, and of sum p |v| / sum p:
     - the weights' rounding: 2^-16 as sums of two bf16 (the rest of the first is rounded by 2^-8 of 2^-8), 2^-8 as one;
+      as one the sum may be that of the rounded weights w (1 + e): sum w e (v - out) / sum w, 2^-8 of |out| more;
     - the score's error: d products summed in binary32 and a few roundings, (d + 8) 2^-24 of scale |q| . |k|, and under a
       cap 2^-21 of the cap (a hardware exponential and reciprocal); a weight moves by as much relative to itself, and the
       sum of the weights too: twice;
@@ -139,7 +140,8 @@ def bound(case, out, size, most, form, cap=0.0):
       of values up to 2^8 lose at most 2^(16 + 8 - 126) < 2^-100."""
     score = (case.d + 8) * 2.0 ** -24 * most + (2.0 ** -21 * cap if cap else 0.0)
     weight = 2.0 ** -16 if form == "decode" else 2.0 ** -8
-    return 2.0 ** -8 * np.abs(out) + size * (weight + 2 * score + 2.0 ** -14) * (1 + 2.0 ** -8) + 2.0 ** -100
+    halves = 1 if form == "decode" else 2
+    return halves * 2.0 ** -8 * np.abs(out) + size * (weight + 2 * score + 2.0 ** -14) * (1 + 2.0 ** -8) + 2.0 ** -100
 
 
 def rope(x, cos_sin, rows, norm, eps):
