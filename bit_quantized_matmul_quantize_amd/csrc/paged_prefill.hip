@@ -64,7 +64,7 @@ struct Shape {
   static constexpr uint32_t kKT = kDP <= 128 ? 64 : 32;      // keys of a tile
   static constexpr uint32_t kSubs = kKT / 16;                // parts of it that lie in one page
   static constexpr uint32_t kTile = kKT * kDP * 2;           // bytes of its keys, or values
-  static constexpr uint32_t kStage = 2 * kTile + (kBits == 8 ? 2 * kKT * 4 : 0);
+  static constexpr uint32_t kStage = 2 * kTile + (kBits == 8 ? 3 * kKT * 4 : 0);  // (and its scales)
   static constexpr uint32_t kLoads = kTile / 16 / kThreads;  // bf16: of a thread, for keys, and for values
   static constexpr uint32_t kCodes = (kTile / 32 + kThreads - 1) / kThreads;  // int8
   static constexpr uint32_t kOutPitch = kDP * 2 + 16;        // bytes of a row of the output in LDS
@@ -241,8 +241,10 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
       if (threadIdx.x < kKT) v_scale = *reinterpret_cast<const float *>(vc + known(id) * page_bytes + page * d + ko * 4u);
     }
   };
+  const int32_t all_low = low_of(place_of(row1)), all_end = min(p.keys, place_of(row0) + 1);  // seen by all rows
+  auto whole_for_all = [&](int32_t key0, uint64_t hole) { return !hole && key0 >= all_low && key0 + (int32_t)kKT <= all_end; };
   // an int8 tile from registers into LDS
-  auto settle = [&](uint32_t stage) {
+  auto settle = [&](uint32_t stage, bool whole) {
     if constexpr (kBits == 8) {
       uint8_t *to = lds + stage * S::kStage;
 #pragma unroll
@@ -262,7 +264,9 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
       float *scales = reinterpret_cast<float *>(to + 2u * S::kTile);
       if (threadIdx.x < kKT) {
         scales[threadIdx.x] = k_scale;
-        scales[kKT + threadIdx.x] = v_scale;
+        // (of a tile that some rows do not see whole, see below)
+        scales[kKT + threadIdx.x] = whole || (__float_as_uint(v_scale) & 0x7F800000u) != 0x7F800000u ? v_scale : 0.0f;
+        scales[2u * kKT + threadIdx.x] = v_scale;
       }
     }
   };
@@ -284,9 +288,8 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
   // 0 * NaN must not reach a row that does not see the NaN's key.  Of tiles that not
   // every row of the workgroup sees whole, values that no row sees and values that
   // are not finite are zeroed in LDS; a second loop adds the latter where they are
-  // seen.  (Codes are finite.)
-  const int32_t all_low = low_of(place_of(row1)), all_end = min(p.keys, place_of(row0) + 1);  // seen by all rows
-  auto whole_for_all = [&](int32_t key0, uint64_t hole) { return !hole && key0 >= all_low && key0 + (int32_t)kKT <= all_end; };
+  // seen.  Codes are finite, and their scales are made so: one that is not turns the
+  // sum of the weights of a row that sees it into NaN.
   auto zero_some = [&](int32_t key0, uint32_t stage, uint64_t hole) {  // returns whether some are not finite
     bool bad = false;
 #pragma unroll 1
@@ -312,8 +315,8 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
   };
 
   // One tile.  hole: bit 16 t where the tile's keys 16 t.. lie in no page; whole: all
-  // rows of the wave see all of it.
-  auto compute = [&](int32_t key0, uint32_t stage, uint64_t hole, bool whole) {
+  // rows of the wave see all of it, for_all: and those of the workgroup.
+  auto compute = [&](int32_t key0, uint32_t stage, uint64_t hole, bool whole, bool for_all) {
     const uint8_t *kt = lds + stage * S::kStage + k_at, *vt = lds + stage * S::kStage + S::kTile + v_at;
     const float *scales = reinterpret_cast<const float *>(lds + stage * S::kStage + 2u * S::kTile) + 8u * half;
     // operands are read kAhead products before they are used, those of the second
@@ -391,13 +394,21 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
         if constexpr (kBits == 8) {
           l += y0 + y1;
           const float2 s = *reinterpret_cast<const float2 *>(scales + kKT + 32u * f + 16u * (i / 8u) + i % 8u);
-          y0 = x[f][i] == -INFINITY ? 0.0f : y0 * s.x;
-          y1 = x[f][i + 1] == -INFINITY ? 0.0f : y1 * s.y;
+          y0 *= s.x;
+          y1 *= s.y;
         }
         const uint32_t two = two_bf16(y0, y1);
         if constexpr (kBits == 16) l = add_two_bf16(two, l);
         w[f][i / 8u][i % 8u / 2u] = two;
       }
+    if (kBits == 8 && !for_all) {
+#pragma unroll 1
+      for (uint32_t t = 0; t < kSubs; ++t) {
+        const uint32_t seen = seen_of(key0, hole, t);
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) l = seen >> i & 1u ? fmaf(scales[2u * kKT + 16u * t + i], 0.0f, l) : l;
+      }
+    }
 #pragma unroll
     for (uint32_t n = 0; n < kSecond; ++n) {
       const uint32_t at = (kFirst + n) % kAhead, b = n % kDB, kk = n / kDB;
@@ -412,7 +423,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
   if (begin < end) {
     bring_k(begin, id, 0);
     bring_v(begin, id, 0);
-    settle(0);
+    settle(0, whole_for_all(begin, __ballot(id >= a.pages)));
   }
   uint32_t next_id = id_of(begin + (int32_t)kKT);
   uint32_t stage = 0;
@@ -428,9 +439,10 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
     }
     id = next_id;
     next_id = id_of(key0 + 2 * (int32_t)kKT);
-    if (kBits == 16 && !whole_for_all(key0, hole)) later |= zero_some(key0, stage, hole);
-    if (some_at(key0)) compute(key0, stage, hole, whole_at(key0, hole));
-    if (more) settle(stage ^ 1u);
+    const bool for_all = whole_for_all(key0, hole);
+    if (kBits == 16 && !for_all) later |= zero_some(key0, stage, hole);
+    if (some_at(key0)) compute(key0, stage, hole, whole_at(key0, hole), for_all);
+    if (more) settle(stage ^ 1u, whole_for_all(key0 + (int32_t)kKT, __ballot(id >= a.pages)));
   }
   if constexpr (kBits == 16) {
     if (later) {  // (the same for the whole workgroup)

@@ -118,6 +118,26 @@ def test_nan_stays_with_the_tokens_that_see_it(gpu, form):
 
 
 @pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("hq,hk,page,window", [(4, 2, 16, 0), (2, 2, 64, 30), (16, 1, 32, 0)])
+def test_nan_scales_stay_with_the_tokens_that_see_them(gpu, form, hq, hk, page, window):
+    # int8 rows that held a NaN: zero codes, and the NaN as their scale; of a value, and of a key
+    case = Case([(40, 100), (200, 200)], hq, hk, 64, 8, page, 20)
+    clean = call(form, case, case.device(gpu), window=window)
+    for seq, place, keys in ((0, 75, False), (0, 90, True), (1, 130, False)):
+        codes, scales = np.zeros((hk, 64), dtype=np.int8), np.full(hk, np.nan, dtype=np.float32)
+        case.cache.put(keys, case.table[seq, place // page], place % page, (codes, scales))
+    out = call(form, case, case.device(gpu), window=window)
+    torch.cuda.synchronize()
+    near = (out.float() - clean.float()).abs() <= 2.0 ** -6 * clean.float().abs() + 2.0 ** -9
+    reach = window or 1 << 30
+    sees = torch.zeros(240, dtype=torch.bool)
+    for row in range(240):
+        seq, pos = (0, 60 + row) if row < 40 else (1, row - 40)
+        sees[row] = any(s == seq and p <= pos < p + reach for s, p in ((0, 75), (0, 90), (1, 130)))
+    assert out[sees.to(gpu)].isnan().all() and near[~sees.to(gpu)].all()
+
+
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("bits", [16, 8])
 def test_places_that_are_nowhere(gpu, form, bits):
     # a page in the middle that is outside the pool, tokens before the beginning, lengths beyond the table
