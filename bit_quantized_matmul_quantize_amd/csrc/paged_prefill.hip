@@ -24,7 +24,10 @@ namespace {
 constexpr uint32_t kWaves = 4;
 constexpr uint32_t kThreads = 64 * kWaves;
 constexpr uint32_t kRows = 32 * kWaves;
-constexpr uint32_t kCus = 256;
+#ifndef SPLIT
+#define SPLIT 512
+#endif
+constexpr uint32_t kFew = SPLIT;  // workgroups: up to so many take two groups of waves
 #ifndef AHEAD
 #define AHEAD 4
 #endif
@@ -78,8 +81,6 @@ __device__ __forceinline__ uint32_t tiles_of(const PagedArgs &a, const PagedSpan
 // The tile of rows that workgroup `item` of a key head takes: those with the most
 // keys first, since the last to end decide.  Sequences by their longest tile (up to
 // 64 of them; more are taken as they come), their tiles from the last one back.
-// Where all workgroups are on the device at once, two to a compute unit, the second
-// one of a unit is the shorter the longer the first is.
 __device__ __forceinline__ bool take_tile(const PagedArgs &a, uint32_t item, uint32_t *seq, uint32_t *tile) {
   const uint32_t lane = __lane_id();
   if (a.count > 64u) {
@@ -106,8 +107,6 @@ __device__ __forceinline__ bool take_tile(const PagedArgs &a, uint32_t item, uin
   }
   all = __builtin_amdgcn_readfirstlane(all);
   if (item >= all) return false;
-  const uint32_t half = kCus / a.hk;
-  if (all > half && all <= 2u * half && item >= half) item = all - 1u - (item - half);
   const uint64_t who = __ballot(item >= before && item - before < mine);
   const uint32_t w = (uint32_t)__builtin_ctzll(who);
   *seq = __builtin_amdgcn_readfirstlane(w);
@@ -117,16 +116,20 @@ __device__ __forceinline__ bool take_tile(const PagedArgs &a, uint32_t item, uin
 
 // kExact: a head has kDP values, and a page has at least a tile's keys.
 // kCap: scores are capped (both may be, unless kExact).
-template <uint32_t kDP, uint32_t kBits, bool kExact, bool kCap>
-__global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a) {
+// kGroups: groups of four waves; two of them share the tiles of keys of the same rows.
+template <uint32_t kDP, uint32_t kBits, bool kExact, bool kCap, uint32_t kGroups>
+__global__ __launch_bounds__(kThreads * kGroups, 2) void paged_prefill_kernel(PagedArgs a) {
   using S = Shape<kDP, kBits>;
   constexpr uint32_t kKT = S::kKT, kSubs = S::kSubs;
   constexpr uint32_t kHalves = kKT / 32;  // halves of a tile: 32 keys
   constexpr uint32_t kDS = kDP / 16;      // steps of the first product
   constexpr uint32_t kDB = kDP / 32;      // blocks of the second, two steps each
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  extern __shared__ __attribute__((aligned(16))) uint8_t all_lds[];
 
-  const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // a group's threads and LDS
+  const uint32_t group = kGroups == 1 ? 0u : __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads), thread = threadIdx.x % kThreads;
+  uint8_t *const lds = all_lds + group * (2u * S::kStage);
+  const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(thread >> 6);
   const uint32_t r = lane & 31u, half = lane >> 5;
   const uint32_t head = blockIdx.x % a.hk, g = a.hq / a.hk;
   uint32_t seq, tile;
@@ -167,7 +170,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
 
   if constexpr (!kExact) {
-    for (uint32_t i = threadIdx.x * 16u; i < 2u * S::kStage; i += kThreads * 16u) *reinterpret_cast<v4u *>(lds + i) = v4u{0, 0, 0, 0};
+    for (uint32_t i = thread * 16u; i < 2u * S::kStage; i += kThreads * 16u) *reinterpret_cast<v4u *>(lds + i) = v4u{0, 0, 0, 0};
     __syncthreads();
   }
 
@@ -208,7 +211,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
       }
     }
     if constexpr (kBits == 8) {
-      if (threadIdx.x < kKT) k_scale = *reinterpret_cast<const float *>(kc + known(id) * page_bytes + page * d + ko * 4u);
+      if (thread < kKT) k_scale = *reinterpret_cast<const float *>(kc + known(id) * page_bytes + page * d + ko * 4u);
     }
   };
   auto bring_v = [&](int32_t key0, uint32_t id, uint32_t stage) {
@@ -238,7 +241,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
     }
     if constexpr (kBits == 8) {
       const uint32_t ko = (uint32_t)(key0 + (int32_t)(lane % kKT)) & (page - 1u);
-      if (threadIdx.x < kKT) v_scale = *reinterpret_cast<const float *>(vc + known(id) * page_bytes + page * d + ko * 4u);
+      if (thread < kKT) v_scale = *reinterpret_cast<const float *>(vc + known(id) * page_bytes + page * d + ko * 4u);
     }
   };
   const int32_t all_low = low_of(place_of(row1)), all_end = min(p.keys, place_of(row0) + 1);  // seen by all rows
@@ -262,11 +265,11 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
         }
       }
       float *scales = reinterpret_cast<float *>(to + 2u * S::kTile);
-      if (threadIdx.x < kKT) {
-        scales[threadIdx.x] = k_scale;
+      if (thread < kKT) {
+        scales[thread] = k_scale;
         // (of a tile that some rows do not see whole, see below)
-        scales[kKT + threadIdx.x] = whole || (__float_as_uint(v_scale) & 0x7F800000u) != 0x7F800000u ? v_scale : 0.0f;
-        scales[2u * kKT + threadIdx.x] = v_scale;
+        scales[kKT + thread] = whole || (__float_as_uint(v_scale) & 0x7F800000u) != 0x7F800000u ? v_scale : 0.0f;
+        scales[2u * kKT + thread] = v_scale;
       }
     }
   };
@@ -290,20 +293,20 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
   // are not finite are zeroed in LDS; a second loop adds the latter where they are
   // seen.  Codes are finite, and their scales are made so: one that is not turns the
   // sum of the weights of a row that sees it into NaN.
-  auto zero_some = [&](int32_t key0, uint32_t stage, uint64_t hole) {  // returns whether some are not finite
+  auto zero_some = [&](int32_t key0, uint32_t stage, uint64_t hole) {  // gives whether some are not finite
     bool bad = false;
 #pragma unroll 1
-    for (uint32_t i = threadIdx.x; i < S::kTile / 16u; i += kThreads) {
-      const uint32_t group = i / kDP;  // of eight keys
-      const int32_t at = key0 + (int32_t)(8u * group), from = max(first - at, 0), to = min(end - 1 - at, 7);
-      const uint32_t seen = hole >> (8u * group & ~15u) & 1u || from > to ? 0u : (0xFFu >> (7 - to)) & (0xFFu << from);
+    for (uint32_t i = thread; i < S::kTile / 16u; i += kThreads) {
+      const uint32_t run = i / kDP;  // of eight keys
+      const int32_t at = key0 + (int32_t)(8u * run), from = max(first - at, 0), to = min(end - 1 - at, 7);
+      const uint32_t seen = hole >> (8u * run & ~15u) & 1u || from > to ? 0u : (0xFFu >> (7 - to)) & (0xFFu << from);
       v4u *u = reinterpret_cast<v4u *>(lds + stage * S::kStage + S::kTile + i * 16u), v = *u;
 #pragma unroll
       for (uint32_t e = 0; e < 4; ++e) v[e] &= (seen >> (2u * e) & 1u ? 0xFFFFu : 0u) | (seen >> (2u * e + 1u) & 1u ? 0xFFFF0000u : 0u);
       bad |= any_not_finite(v);
       *u = finite_only(v);
     }
-    return __syncthreads_or(bad) != 0;
+    return bad;
   };
 
   auto whole_at = [&](int32_t key0, uint64_t hole) { return !hole && key0 >= whole_low && key0 + (int32_t)kKT <= whole_end; };
@@ -321,7 +324,9 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
     const float *scales = reinterpret_cast<const float *>(lds + stage * S::kStage + 2u * S::kTile) + 8u * half;
     // operands are read kAhead products before they are used, those of the second
     // product from before the softmax on
-    auto read_k = [&](uint32_t n) { return *reinterpret_cast<const v4u *>(kt + (2u * (n % kDS) * kKT + 32u * (n / kDS)) * 16u); };
+    // (products that follow each other belong to different sums: one has to wait for
+    // the last one of its own)
+    auto read_k = [&](uint32_t n) { return *reinterpret_cast<const v4u *>(kt + (2u * (n / kHalves) * kKT + 32u * (n % kHalves)) * 16u); };
     auto read_v = [&](uint32_t n) { return *reinterpret_cast<const v4u *>(vt + (2u * (n / kDB) * kDP + 32u * (n % kDB)) * 16u); };
     constexpr uint32_t kAhead = kDP > 128 ? AHEAD : 8, kFirst = kHalves * kDS, kSecond = kHalves * 2u * kDB;
     v16f x[kHalves];  // of keys 32 f + 16 (i / 8) + 8 half + i % 8
@@ -334,7 +339,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
       for (uint32_t i = 0; i < 16; ++i) x[f][i] = 0.0f;
 #pragma unroll
     for (uint32_t n = 0; n < kFirst; ++n) {
-      x[n / kDS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(ring[n % kAhead]), as_bf(q[n % kDS]), x[n / kDS], 0, 0, 0);
+      x[n % kHalves] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf(ring[n % kAhead]), as_bf(q[n / kHalves]), x[n % kHalves], 0, 0, 0);
       ring[n % kAhead] = n + kAhead < kFirst ? read_k(n + kAhead) : read_v(n + kAhead - kFirst);
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -418,34 +423,73 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
     }
   };
 
+  // The groups take the tiles in turn; the loop is the same for all of the workgroup.
+  constexpr int32_t kStep = (int32_t)(kKT * kGroups);
+  const int32_t own = begin + (int32_t)(kKT * group);
+  // (of both groups' tiles: whether some rows of the workgroup do not see a key of them)
+  auto for_all_groups = [&](int32_t key0, uint32_t id, uint32_t other) {
+    if (kGroups == 1) return whole_for_all(key0, __ballot(id >= a.pages));
+    const int32_t base = key0 - (int32_t)(kKT * group);
+    return !__ballot(id >= a.pages || other >= a.pages) && base >= all_low && base + kStep <= all_end;
+  };
+  auto other_of = [&](int32_t key0) { return kGroups == 1 ? 0u : id_of(group ? key0 - (int32_t)kKT : key0 + (int32_t)kKT); };
   bool later = false;
-  uint32_t id = id_of(begin);
-  if (begin < end) {
-    bring_k(begin, id, 0);
-    bring_v(begin, id, 0);
-    settle(0, whole_for_all(begin, __ballot(id >= a.pages)));
+  uint32_t id = id_of(own), other = other_of(own);
+  if (own < end) {
+    bring_k(own, id, 0);
+    bring_v(own, id, 0);
+    settle(0, whole_for_all(own, __ballot(id >= a.pages)));
   }
-  uint32_t next_id = id_of(begin + (int32_t)kKT);
+  uint32_t next_id = id_of(own + kStep), next_other = other_of(own + kStep);
   uint32_t stage = 0;
-  for (int32_t key0 = begin; key0 < end; key0 += (int32_t)kKT, stage ^= 1u) {
+  for (int32_t base = begin, key0 = own; base < end; base += kStep, key0 += kStep, stage ^= 1u) {
     // this tile has arrived, and nobody reads the other stage any more
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __syncthreads();
     const uint64_t hole = __ballot(id >= a.pages);
-    const bool more = key0 + (int32_t)kKT < end;
+    const bool more = key0 + kStep < end;
     if (more) {
-      bring_k(key0 + (int32_t)kKT, next_id, stage ^ 1u);
-      bring_v(key0 + (int32_t)kKT, next_id, stage ^ 1u);
+      bring_k(key0 + kStep, next_id, stage ^ 1u);
+      bring_v(key0 + kStep, next_id, stage ^ 1u);
     }
+    if (kBits == 16 && !for_all_groups(key0, id, other)) later |= __syncthreads_or(key0 < end && zero_some(key0, stage, hole)) != 0;
     id = next_id;
-    next_id = id_of(key0 + 2 * (int32_t)kKT);
-    const bool for_all = whole_for_all(key0, hole);
-    if (kBits == 16 && !for_all) later |= zero_some(key0, stage, hole);
-    if (some_at(key0)) compute(key0, stage, hole, whole_at(key0, hole), for_all);
-    if (more) settle(stage ^ 1u, whole_for_all(key0 + (int32_t)kKT, __ballot(id >= a.pages)));
+    other = next_other;
+    next_id = id_of(key0 + 2 * kStep);
+    next_other = other_of(key0 + 2 * kStep);
+    if (key0 < end && some_at(key0)) compute(key0, stage, hole, whole_at(key0, hole), whole_for_all(key0, hole));
+    if (more) settle(stage ^ 1u, whole_for_all(key0 + kStep, __ballot(id >= a.pages)));
+  }
+  if constexpr (kGroups == 2) {
+    // the second group's sums to the first, through LDS
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    constexpr uint32_t kRuns = kDB * 4u;
+    v4f *const sums = reinterpret_cast<v4f *>(all_lds) + wave * (kRuns * 64u) + lane;
+    float2 *const stats = reinterpret_cast<float2 *>(all_lds + kRuns * 16u * kThreads) + thread;
+    if (group == 1u) {
+      *stats = make_float2(m, l);
+#pragma unroll
+      for (uint32_t i = 0; i < kRuns; ++i) sums[i * 64u] = v4f{o[i / 4u][i % 4u * 4u], o[i / 4u][i % 4u * 4u + 1u], o[i / 4u][i % 4u * 4u + 2u], o[i / 4u][i % 4u * 4u + 3u]};
+    }
+    __syncthreads();
+    if (group == 0u) {
+      const float2 theirs = *stats;
+      const float next = fmaxf(m, theirs.x);
+      const float f = m == -INFINITY ? 0.0f : exp2_hw(m - next), g2 = theirs.x == -INFINITY ? 0.0f : exp2_hw(theirs.x - next);
+      l = l * f + theirs.y * g2;
+#pragma unroll
+      for (uint32_t i = 0; i < kRuns; ++i) {
+        const v4f y = sums[i * 64u];
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) o[i / 4u][i % 4u * 4u + e] = o[i / 4u][i % 4u * 4u + e] * f + y[e] * g2;
+      }
+    }
   }
   if constexpr (kBits == 16) {
     if (later) {  // (the same for the whole workgroup)
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
 #pragma unroll 1
       for (int32_t key0 = begin; key0 < end; key0 += (int32_t)kKT) {
         id = id_of(key0);
@@ -482,14 +526,15 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
   __syncthreads();
   l += __shfl_xor(l, 32, 64);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint8_t *mine = lds + wave * 32u * S::kOutPitch;
+  if (group != 0u) return;
+  uint8_t *mine = all_lds + wave * 32u * S::kOutPitch;
 #pragma unroll
   for (uint32_t b = 0; b < kDB; ++b)
 #pragma unroll
     for (uint32_t i = 0; i < 16; i += 4)
       *reinterpret_cast<uint2 *>(mine + r * S::kOutPitch + (32u * b + 2u * i + 4u * half) * 2u) =
           make_uint2(two_bf16(o[b][i] * inv, o[b][i + 1] * inv), two_bf16(o[b][i + 2] * inv, o[b][i + 3] * inv));
-  __syncthreads();
+  __builtin_amdgcn_wave_barrier();  // (a wave's own rows: LDS is in order)
   const uint32_t pieces = d / 8u;
   for (uint32_t i = lane; i < 32u * pieces; i += 64u) {
     const uint32_t at = i / pieces, piece = i % pieces, to = wrow0 + at;
@@ -499,24 +544,32 @@ __global__ __launch_bounds__(kThreads, 2) void paged_prefill_kernel(PagedArgs a)
   }
 }
 
-template <uint32_t kDP, uint32_t kBits, bool kExact, bool kCap>
-hipError_t launch(const PagedArgs &a, hipStream_t s) {
-  constexpr uint32_t kLds = Shape<kDP, kBits>::kLds;
-  auto *kernel = paged_prefill_kernel<kDP, kBits, kExact, kCap>;
+template <uint32_t kDP, uint32_t kBits, bool kExact, bool kCap, uint32_t kGroups>
+hipError_t launch(const PagedArgs &a, uint32_t groups, hipStream_t s) {
+  using S = Shape<kDP, kBits>;
+  constexpr uint32_t kSums = (kDP * 2u + 8u) * kThreads;  // of the second group
+  constexpr uint32_t kLds = kGroups == 1 ? S::kLds : std::max(4u * S::kStage, kSums);
+  auto *kernel = paged_prefill_kernel<kDP, kBits, kExact, kCap, kGroups>;
   if (kLds > 65536u) {
     const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void *>(kernel), (int)kLds);
     if (e != hipSuccess) return e;
   }
+  hipLaunchKernelGGL(kernel, dim3(groups), dim3(kThreads * kGroups), kLds, s, a);
+  return hipGetLastError();
+}
+
+template <uint32_t kDP, uint32_t kBits, bool kExact, bool kCap>
+hipError_t launch_groups(const PagedArgs &a, hipStream_t s) {
   // (of a sequence with rows: at most one tile that is not full)
   const uint64_t rows = (uint64_t)a.tokens * (a.hq / a.hk), tiles = rows / kRows + std::min(a.count, a.tokens);
-  hipLaunchKernelGGL(kernel, dim3((uint32_t)(tiles * a.hk)), dim3(kThreads), kLds, s, a);
-  return hipGetLastError();
+  const uint32_t groups = (uint32_t)(tiles * a.hk);
+  return groups <= kFew ? launch<kDP, kBits, kExact, kCap, 2>(a, groups, s) : launch<kDP, kBits, kExact, kCap, 1>(a, groups, s);
 }
 
 template <uint32_t kDP, uint32_t kBits>
 hipError_t launch_exact(const PagedArgs &a, hipStream_t s) {
-  if (a.d != kDP || (1u << a.page_shift) < Shape<kDP, kBits>::kKT) return launch<kDP, kBits, false, false>(a, s);
-  return a.cap != 0.0f ? launch<kDP, kBits, true, true>(a, s) : launch<kDP, kBits, true, false>(a, s);
+  if (a.d != kDP || (1u << a.page_shift) < Shape<kDP, kBits>::kKT) return launch_groups<kDP, kBits, false, false>(a, s);
+  return a.cap != 0.0f ? launch_groups<kDP, kBits, true, true>(a, s) : launch_groups<kDP, kBits, true, false>(a, s);
 }
 
 template <uint32_t kBits>
