@@ -207,7 +207,7 @@ hipError_t launch_paged_write(const PagedArgs &a, hipStream_t s);
 hipError_t launch_paged_read(const PagedArgs &a, hipStream_t s);
 hipError_t launch_paged_decode(const PagedArgs &a, hipStream_t s);
 hipError_t launch_paged_prefill(const PagedArgs &a, hipStream_t s);
-// of the decoding form, for any tokens
-uint64_t paged_workspace_bytes(uint32_t hk, uint32_t d);
+// of the decoding form, for these and fewer tokens
+uint64_t paged_workspace_bytes(uint32_t tokens, uint32_t hq, uint32_t hk, uint32_t d);
 
 }  // namespace bqmm

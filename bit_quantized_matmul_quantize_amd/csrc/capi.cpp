@@ -956,7 +956,7 @@ uint64_t paged_attention_workspace_bytes(uint32_t tokens, uint32_t count, uint32
   if (hk == 0 || hk > 65535u || hq == 0 || hq > 65535u || hq % hk != 0 || d < 16u || d > 256u || d % 16u != 0 ||
       tokens > kMaxPlaces || count > kMaxPlaces || (uint64_t)tokens * hq >= (1ull << 24))
     return 0;
-  return bqmm::paged_workspace_bytes(hk, d);  // (the same for any tokens)
+  return bqmm::paged_workspace_bytes(tokens, hq, hk, d);  // (the same for any number of sequences)
 }
 
 int paged_attention_decode(const void *q_bf16, const void *k_cache, const void *v_cache, void *out_bf16,
@@ -983,7 +983,7 @@ int paged_attention_decode(const void *q_bf16, const void *k_cache, const void *
   const uint64_t rows = (uint64_t)tokens * (hq / hk), tiles = std::min<uint64_t>(rows, rows / 16u + count);
   REQUIRE(tiles * (((uint64_t)width * page + 63u) / 64u) < (1ull << 31), BQ_EINVAL,
           "%s: tokens=%u count=%u over a table of %u pages too large", name, tokens, count, width);
-  const uint64_t need = bqmm::paged_workspace_bytes(hk, d);
+  const uint64_t need = bqmm::paged_workspace_bytes(tokens, hq, hk, d);
   REQUIRE(workspace, BQ_EINVAL, "%s: null workspace", name);
   REQUIRE(workspace_bytes >= need, BQ_EINVAL, "%s: the workspace holds %llu bytes, %llu are needed", name,
           (unsigned long long)workspace_bytes, (unsigned long long)need);

@@ -68,10 +68,12 @@ __device__ __forceinline__ uint32_t run_blocks(uint32_t blocks, uint32_t slots) 
 struct Parts {
   float *sums;    // [slots][2][hk][tile_rows][d]
   float2 *stats;  // [slots][2][hk][tile_rows]: maximum (base 2) and sum
+  uint2 *where;   // [tokens][hq / hk]: a row's first part (slot, and 2^31 for a second part); its parts, and 2^16 its place in the tile
 };
-__host__ __device__ inline Parts parts_of(uint8_t *workspace, uint32_t slots, uint32_t hk, uint32_t tile_rows, uint32_t d) {
+Parts parts_of(uint8_t *workspace, uint32_t slots, uint32_t hk, uint32_t tile_rows, uint32_t d) {
   const uint64_t rows = 2ull * slots * hk * tile_rows;
-  return {reinterpret_cast<float *>(workspace), reinterpret_cast<float2 *>(workspace + rows * d * 4u)};
+  uint8_t *stats = workspace + rows * d * 4u;
+  return {reinterpret_cast<float *>(workspace), reinterpret_cast<float2 *>(stats), reinterpret_cast<uint2 *>(stats + rows * 8u)};
 }
 
 // ---- a run ------------------------------------------------------------------------
@@ -86,8 +88,7 @@ constexpr int waves_of(uint32_t dp, uint32_t bits) { return dp > 128u && bits ==
 // rows.
 // kCut: a workgroup takes a run of blocks, else one tile of rows and its sequence.
 template <uint32_t kDP, uint32_t kBits, uint32_t kNT, bool kExact, uint32_t kWaves, bool kCut>
-__global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits)) void paged_decode_kernel(PagedArgs a, uint32_t slots,
-                                                                                             float *sums, float2 *stats) {
+__global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits)) void paged_decode_kernel(PagedArgs a, uint32_t slots, Parts parts) {
   constexpr uint32_t kUnit = 128u / kBits;        // values of a unit
   constexpr uint32_t kKeys = kBits == 8u && kDP <= 128u ? 64 : 32;  // keys of a step
   constexpr uint32_t kKT = kKeys / 16u;           // their tiles
@@ -104,9 +105,10 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits)) void paged_decod
   const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t r = lane & 15u, c = lane >> 4;
   const uint32_t slot = blockIdx.x / a.hk, head = blockIdx.x % a.hk, g = a.hq / a.hk;
-  uint32_t at_block = 0, end_block = 1, run_begin = 0;
+  uint32_t at_block = 0, end_block = 1, run_begin = 0, per = 1;
   if constexpr (kCut) {
-    const uint32_t all = all_blocks(a, kRows), per = run_blocks(all, slots);
+    const uint32_t all = all_blocks(a, kRows);
+    per = run_blocks(all, slots);
     if ((uint64_t)slot * per >= all) return;
     run_begin = at_block = slot * per;
     end_block = min(at_block + per, all);
@@ -531,12 +533,19 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits)) void paged_decod
                 make_uint2(pack_bf16x2(o[n][b][0] * inv, o[n][b][1] * inv), pack_bf16x2(o[n][b][2] * inv, o[n][b][3] * inv));
       } else {
         const uint64_t at = ((uint64_t)(2u * slot + (at_block != run_begin)) * a.hk + head) * kRows + n * 16u + r;
-        if (c == 0u) stats[at] = make_float2(m[n], l[n]);
+        if (c == 0u) parts.stats[at] = make_float2(m[n], l[n]);
 #pragma unroll
         for (uint32_t b = 0; b < kDB; ++b)
-          if (16u * b < d) *reinterpret_cast<v4f *>(sums + at * d + 16u * b + 4u * c) = o[n][b];
+          if (16u * b < d) *reinterpret_cast<v4f *>(parts.sums + at * d + 16u * b + 4u * c) = o[n][b];
       }
     }
+  }
+  if (kCut && head == 0u && skip + take == job.blocks && threadIdx.x < kRows) {
+    // the tile's rows: where their parts begin, for the second launch
+    const uint32_t job_begin = at_block - skip, slot0 = job_begin / per, row = tile * kRows + threadIdx.x;
+    if (row < job.rows)
+      parts.where[(uint64_t)p.first * g + row] =
+          make_uint2(slot0 | (job_begin != slot0 * per ? 1u << 31 : 0u), (slot - slot0 + 1u) | threadIdx.x << 16);
   }
   at_block += kCut ? take : 1u;
   }
@@ -545,60 +554,28 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits)) void paged_decod
 // ---- joining the runs ----------------------------------------------------------------
 
 // A workgroup takes one row: lanes hold four of its values, groups of lanes share
-// the runs.
+// the parts.
 constexpr uint32_t kJoinThreads = 256;
 
-__global__ __launch_bounds__(kJoinThreads) void paged_join_kernel(PagedArgs a, uint32_t tile_rows, uint32_t slots,
-                                                                  const float *sums, const float2 *stats) {
+__global__ __launch_bounds__(kJoinThreads) void paged_join_kernel(PagedArgs a, uint32_t tile_rows, uint32_t slots, Parts parts) {
   __shared__ v4f part[kJoinThreads];
-  __shared__ float part_sum[kJoinThreads / 4], most[4];
+  __shared__ float part_sum[kJoinThreads / 4];
   const uint32_t g = a.hq / a.hk, token = blockIdx.x, h = blockIdx.y, head = h / g;
-  const uint32_t per = run_blocks(all_blocks(a, tile_rows), slots);
-  // the token's sequence, and the blocks before its own
-  uint32_t seq = 0, before = 0;
-  bool found = false;
-  for (uint32_t base = 0; base < a.count && !found; base += 64u) {
-    const uint32_t i = base + __lane_id();
-    uint32_t items = 0;
-    bool here = false;
-    if (i < a.count) {
-      const PagedSpan p = paged_span(a, i);
-      const Job j = job_of(a, p, tile_rows);
-      items = j.tiles * j.blocks;
-      here = token >= p.first && token - p.first < p.n;
-    }
-    const uint32_t upto = a.count == 1u ? items : wave_scan(items);
-    const uint64_t who = __ballot(here);
-    if (who) {
-      const uint32_t w = (uint32_t)__builtin_ctzll(who);
-      seq = base + w;
-      before += (uint32_t)__builtin_amdgcn_readlane((int)(upto - items), (int)w);
-      found = true;
-    } else {
-      before += (uint32_t)__builtin_amdgcn_readlane((int)upto, a.count == 1u ? 0 : 63);
-    }
-  }
-  if (!found) return;
-  const PagedSpan p = paged_span(a, seq);
-  const Job job = job_of(a, p, tile_rows);
-  const uint32_t row = (token - p.first) * g + h % g, tile = row / tile_rows;
-  const uint32_t begin = before + tile * job.blocks, slot0 = begin / per, runs = (begin + job.blocks - 1u) / per - slot0 + 1u;
-  // one run has written its rows itself (and starts that do not ascend give no
-  // runs past the last slot)
-  if (runs == 1u || slot0 + runs > slots) return;
-  // part i: of run slot0 + i, all but the first begin with their run
-  const uint32_t second = begin != slot0 * per;
+  const uint2 where = parts.where[(uint64_t)token * g + h % g];
+  const int32_t first = a.starts[0], last = a.starts[a.count];
+  const uint32_t slot0 = where.x & 0x7FFFFFFFu, runs = where.y & 0xFFFFu, row = where.y >> 16;
+  // One part: the row is written.  (Of a row of no sequence nobody has written
+  // where it is; nor do starts that do not ascend lead outside the parts.)
+  if (runs <= 1u || (int64_t)token < first || (int64_t)token >= last || slot0 >= slots || runs > slots - slot0 || row >= tile_rows)
+    return;
   auto at_of = [&](uint32_t i) {
-    return ((uint64_t)(2u * (slot0 + i) + (i == 0u ? second : 0u)) * a.hk + head) * tile_rows + row % tile_rows;
+    return ((uint64_t)(2u * (slot0 + i) + (i == 0u ? where.x >> 31 : 0u)) * a.hk + head) * tile_rows + row;
   };
 
   float top = -INFINITY;
-  for (uint32_t i = threadIdx.x; i < runs; i += kJoinThreads) top = fmaxf(top, stats[at_of(i)].x);
+  for (uint32_t i = threadIdx.x & 63u; i < runs; i += 64u) top = fmaxf(top, parts.stats[at_of(i)].x);
 #pragma unroll
   for (uint32_t d = 1; d < 64u; d *= 2u) top = fmaxf(top, __shfl_xor(top, (int)d, 64));
-  if ((threadIdx.x & 63u) == 0u) most[threadIdx.x >> 6] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
 
   const uint32_t lanes = a.d / 4u, groups = kJoinThreads / lanes, lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
   v4f sum = {0, 0, 0, 0};
@@ -607,10 +584,10 @@ __global__ __launch_bounds__(kJoinThreads) void paged_join_kernel(PagedArgs a, u
 #pragma unroll 4
     for (uint32_t i = group; i < runs; i += groups) {
       const uint64_t at = at_of(i);
-      const float2 s = stats[at];
+      const float2 s = parts.stats[at];
       const float w = s.x == -INFINITY ? 0.0f : exp2_hw(s.x - top);
       weight += s.y * w;
-      sum += *reinterpret_cast<const v4f *>(sums + at * a.d + 4u * lane) * w;
+      sum += *reinterpret_cast<const v4f *>(parts.sums + at * a.d + 4u * lane) * w;
     }
     part[threadIdx.x] = sum;
     if (lane == 0u) part_sum[group] = weight;
@@ -658,12 +635,10 @@ hipError_t launch(const PagedArgs &a, const Plan &plan, hipStream_t s) {
     const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void *>(kernel), (int)kLds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(kernel, dim3((kCut ? plan.slots : plan.tiles) * a.hk), dim3(64 * kWaves), kLds, s, a, plan.slots, parts.sums,
-                     parts.stats);
+  hipLaunchKernelGGL(kernel, dim3((kCut ? plan.slots : plan.tiles) * a.hk), dim3(64 * kWaves), kLds, s, a, plan.slots, parts);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !kCut) return e;
-  hipLaunchKernelGGL(paged_join_kernel, dim3(a.tokens, a.hq), dim3(kJoinThreads), 0, s, a, 16u * kNT, plan.slots, parts.sums,
-                     parts.stats);
+  hipLaunchKernelGGL(paged_join_kernel, dim3(a.tokens, a.hq), dim3(kJoinThreads), 0, s, a, 16u * kNT, plan.slots, parts);
   return hipGetLastError();
 }
 
@@ -697,11 +672,11 @@ hipError_t launch_paged_decode(const PagedArgs &a, hipStream_t s) {
   return a.bits == 16u ? launch_bits<16>(a, plan, s) : launch_bits<8>(a, plan, s);
 }
 
-// The two parts of each run, for tiles of the most rows and as many runs as any
-// form of the kernel has: what a call needs, whatever its tokens are.
-uint64_t paged_workspace_bytes(uint32_t hk, uint32_t d) {
+// The two parts of each run, for tiles of the most rows and as many runs as any form
+// of the kernel has, and where each row's are.
+uint64_t paged_workspace_bytes(uint32_t tokens, uint32_t hq, uint32_t hk, uint32_t d) {
   const uint64_t slots = std::max(kCus * 2u / hk, 1u);
-  return 2u * slots * hk * 16u * kMostBlocks * (4ull * d + 8u);
+  return 2u * slots * hk * 16u * kMostBlocks * (4ull * d + 8u) + 8ull * tokens * (hq / hk);
 }
 
 }  // namespace bqmm
