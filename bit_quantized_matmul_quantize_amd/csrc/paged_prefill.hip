@@ -24,13 +24,10 @@ namespace {
 constexpr uint32_t kWaves = 4;
 constexpr uint32_t kThreads = 64 * kWaves;
 constexpr uint32_t kRows = 32 * kWaves;
-#ifndef SPLIT
-#define SPLIT 512
-#endif
-constexpr uint32_t kFew = SPLIT;  // workgroups: up to so many take two groups of waves
-#ifndef AHEAD
-#define AHEAD 4
-#endif
+// Up to so many workgroups (two to a compute unit) take two groups of waves each: a
+// prompt of 1024 tokens 25 us (with one 27), of 2048 50 (53); one of 3000, with 752
+// workgroups, 98 (84).
+constexpr uint32_t kFew = 512;
 
 // 16 bytes a lane straight from memory into LDS: lane i's go to the wave's
 // destination + 16 i.  The kernel waits itself; no register is written.
@@ -328,7 +325,7 @@ __global__ __launch_bounds__(kThreads * kGroups, 2) void paged_prefill_kernel(Pa
     // the last one of its own)
     auto read_k = [&](uint32_t n) { return *reinterpret_cast<const v4u *>(kt + (2u * (n / kHalves) * kKT + 32u * (n % kHalves)) * 16u); };
     auto read_v = [&](uint32_t n) { return *reinterpret_cast<const v4u *>(vt + (2u * (n / kDB) * kDP + 32u * (n % kDB)) * 16u); };
-    constexpr uint32_t kAhead = kDP > 128 ? AHEAD : 8, kFirst = kHalves * kDS, kSecond = kHalves * 2u * kDB;
+    constexpr uint32_t kAhead = kDP > 128 ? 4 : 8, kFirst = kHalves * kDS, kSecond = kHalves * 2u * kDB;
     v16f x[kHalves];  // of keys 32 f + 16 (i / 8) + 8 half + i % 8
     v4u ring[kAhead];
 #pragma unroll
@@ -561,7 +558,7 @@ hipError_t launch(const PagedArgs &a, uint32_t groups, hipStream_t s) {
 template <uint32_t kDP, uint32_t kBits, bool kExact, bool kCap>
 hipError_t launch_groups(const PagedArgs &a, hipStream_t s) {
   // (of a sequence with rows: at most one tile that is not full)
-  const uint64_t rows = (uint64_t)a.tokens * (a.hq / a.hk), tiles = rows / kRows + std::min(a.count, a.tokens);
+  const uint64_t rows = (uint64_t)a.tokens * (a.hq / a.hk), tiles = (rows + (kRows - 1ull) * std::min(a.count, a.tokens)) / kRows;
   const uint32_t groups = (uint32_t)(tiles * a.hk);
   return groups <= kFew ? launch<kDP, kBits, kExact, kCap, 2>(a, groups, s) : launch<kDP, kBits, kExact, kCap, 1>(a, groups, s);
 }
