@@ -469,16 +469,20 @@ int read_kv_cache(const void *k_cache, const void *v_cache, void *k_bf16, void *
  * over the keys j <= p of its sequence, and where window is not 0 j > p - window.
  * A token that sees no key, or only keys with a score of -infinity, gives zeros.
  * q: bf16, head h of token t starts at t * q_token + h * q_head; out: bf16
- * [tokens][hq][d].  hk divides hq; tokens * hq < 2^24; scale >= 0.
+ * [tokens][hq][d].  hk divides hq; tokens * hq < 2^24; scale >= 0; hk * min(rows,
+ * rows / 16 + count) < 2^22 with rows = tokens * hq / hk.  _decode: its tiles of 16 or
+ * 32 rows times the table's blocks of 64 keys below 2^31.
  *
  * Products of bf16 values (int8 codes are exact in bf16) are summed in binary32,
  * and so are the softmax's maximum and sum.  _decode takes the weights w_j as sums
- * of two bf16, _prefill rounds them to one (2^-9 of each).  Both give a call's
- * result bit for bit again.
- * _decode reads each key once for up to 16, 32 or 64 rows (new tokens times hq /
- * hk) and cuts sequences over the device: for decoding and for a few tokens each.
- * _prefill: for prompts.  workspace: paged_attention_workspace_bytes(...) bytes for
- * these sizes or larger ones, for this call alone until it has run. */
+ * of two bf16, _prefill rounds them to one (by at most 2^-8 of each).  A call's
+ * result is the same bit for bit when it is called again.
+ * _decode reads each key once for 16 or 32 rows (new tokens times hq / hk) and cuts
+ * the sequences over the device where width * page is above 1024: for decoding and
+ * for a few tokens each.  _prefill: for prompts, 128 rows at a time.  workspace:
+ * paged_attention_workspace_bytes(...) bytes for these sizes or larger ones, 16-byte
+ * aligned, in any state before, and for this call alone until it has run: calls that
+ * may overlap in time need one each. */
 int paged_attention_decode(const void *q_bf16, const void *k_cache, const void *v_cache, void *out_bf16,
                            const int32_t *starts, const int32_t *lens, const int32_t *table, void *workspace,
                            uint64_t workspace_bytes, uint32_t tokens, uint32_t count, uint32_t pages, uint32_t page,
