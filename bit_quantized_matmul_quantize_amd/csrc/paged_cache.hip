@@ -7,7 +7,8 @@
 // axis; q goes out in bf16, k and v into the cache, in bf16 or as int8 codes
 // rint(127 t / top) with a scale top / 127 per token and head.
 //
-// Bound by bytes: 2 read and 2 or 1 + 4/d written a value, a few operations each.
+// Bound by bytes: 2 read and 2 or 1 + 4/d written a value, a few operations each: a
+// prompt of 8192, 32 heads over 8 of 128, in bf16 205 MB in 39 us, 5.2 TB/s.
 // A workgroup takes 16 consecutive places of a sequence, aligned to 16, so that
 // they lie in one page and fill whole 16-byte units of it: a unit of k is 8 or 16
 // values of one token, and a unit of v one value of 8 or 16 tokens, for which the
@@ -24,7 +25,10 @@ constexpr uint32_t kTile = 16;     // places
 constexpr uint32_t kThreads = 256;
 // Workgroups that the heads of a tile are shared out to: enough of them in all, and
 // four turns each where that leaves more (looking up the angles costs about two).
-constexpr uint32_t kEnough = 1024, kMore = 2048;
+// 2130 tokens of 6 sequences, 16 heads over 2 of 256, written and read: with 512 as
+// enough 24.3 us, with 1024 25.7; a prompt of 8192, 32 heads over 8: with up to 2048
+// 51 us, with 1024 55.
+constexpr uint32_t kEnough = 512, kMore = 2048;
 
 struct Tile {
   PagedSpan span;

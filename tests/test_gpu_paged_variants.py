@@ -66,6 +66,19 @@ def test_nan_in_cut_sequences(gpu, d, hq):
     assert ((out - clean).abs() <= 2.0 ** -7 * clean.abs() + 2.0 ** -14).all()
 
 
+def test_rows_of_no_sequence_beside_cut_ones(gpu):
+    # rows before the first and behind the last sequence stay as they were, whatever the workspace holds
+    case = widened(Case([(2, 900), (3, 1300)], 4, 2, 64, 16, 64, 450))
+    t = case.device(gpu)
+    whole = call("decode", case, t)
+    t["starts"] = torch.tensor([0, 2, 4], dtype=torch.int32, device=gpu)  # the second's last two of 1299 tokens
+    t["lens"] = torch.tensor([900, 1299], dtype=torch.int32, device=gpu)
+    for fill in (0x00, 0x01, 0xFF):
+        work = torch.full((bq.paged_attention_workspace_bytes(5, 2, 4, 2, 64),), fill, dtype=torch.uint8, device=gpu)
+        out = call("decode", case, t, None, work)
+        assert (out[4] == 7).all() and ((out[:4] - whole[:4]).abs() <= 2.0 ** -7 * whole[:4].abs() + 2.0 ** -14).all()
+
+
 # 65 sequences and more of 8 key heads: more than 512 workgroups of 128 rows
 MANY = [(1 + i % 3, 1 + (i * 29) % 60 + 3) for i in range(68)] + [(150, 150), (130, 300)]
 
