@@ -58,7 +58,7 @@ __device__ __forceinline__ void load_run_to_lds(uint32_t lds, uint32_t offset, c
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\t"
                  "global_load_lds_dwordx4 %1, %2 offset:1024\n\tglobal_load_lds_dwordx4 %1, %2 offset:2048\n\t"
-                 "global_load_lds_dwordx4 %1, %2 offset:3072" ::"s"(lds), "v"(offset), "s"(base) : "memory", "m0");
+                 "global_load_lds_dwordx4 %1, %2 offset:%3" ::"s"(lds), "v"(offset), "s"(base), "n"(3 * 1024) : "memory", "m0");
 }
 
 // kDP: values of a head, rounded up (the ones beyond are zero).
