@@ -88,6 +88,7 @@ Parts parts_of(uint8_t *workspace, uint32_t slots, uint32_t hk, uint32_t tile_ro
 // spills in the loop: one token of 96 sequences, heads of 80: 93 us, with three and
 // spills 105; eight tokens of 16 sequences, int8 heads of 128: 105 us, with one wave
 // 120; one of 16, bf16 heads of 256: 70 us with one, with two and spills 111.
+// (All with an older join, 2 to 3 us longer.)
 constexpr int waves_of(uint32_t dp, uint32_t bits) { return dp > 128u && bits == 16u ? 1 : 2; }
 
 // kDP: values of a head, rounded up (kExact: as they are); kNT: column blocks of 16
@@ -624,7 +625,8 @@ Plan plan_of(const PagedArgs &a) {
   Plan p;
   // (16 sequences up to 16384 keys, 8 tokens of 4 heads of 128 each: by 32 rows bf16 147 us,
   // int8 103, by 16 rows 177 and 112; 4 tokens of 8 heads of 256, bf16: 91 and 102)
-  // (wide int8 heads by 16 rows: 8 sequences of 4 tokens and 8 heads 46 us, by 32 53)
+  // (wide int8 heads by 16 rows: 8 sequences of 4 tokens and 8 heads 46 us, by 32 53,
+  // both with a join 3 us longer)
   p.blocks = mean <= 16u || (a.d > 128u && a.bits == 8u) ? 1u : kMostBlocks;
   const uint32_t tile = 16u * p.blocks, dp = a.d <= 64u ? 64u : a.d <= 96u ? 96u : a.d <= 128u ? 128u : 256u;
   // (of a sequence with rows: at most one tile that is not full)
