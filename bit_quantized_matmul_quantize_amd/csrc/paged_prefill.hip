@@ -460,7 +460,9 @@ __global__ __launch_bounds__(kThreads * kGroups, 2) void paged_prefill_kernel(Pa
       bring_k(key0 + kStep, next_id, stage ^ 1u);
       bring_v(key0 + kStep, next_id, stage ^ 1u);
     }
-    if (kBits == 16 && !for_all_groups(key0, id, other)) later |= __syncthreads_or(key0 < end && zero_some(key0, stage, hole)) != 0;
+    // (each group its own tile, and only where the second loop comes to it again)
+    if (kBits == 16 && !for_all_groups(key0, id, other))
+      later |= __syncthreads_or(key0 < end && !whole_for_all(key0, hole) && zero_some(key0, stage, hole)) != 0;
     id = next_id;
     other = next_other;
     next_id = id_of(key0 + 2 * kStep);
