@@ -85,6 +85,10 @@ constexpr float kSlack = 8.0f;
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// The products times this are the scores base 2.  Not 0 where the scale is, so that the
+// score of a key that is not seen stays -infinity; 2^-149 of any product is below 2^-20.
+__device__ __forceinline__ float scale_base2(float scale) { return fmaxf(scale * kLog2e, 0x1p-149f); }
+
 // c tanh(x / c) = c (1 - 2 / (1 + exp(2 x / c)))
 __device__ __forceinline__ float capped(float x, float cap, float inv2) {
   return cap - 2.0f * cap * __builtin_amdgcn_rcpf(1.0f + exp2_hw(x * inv2));

@@ -179,7 +179,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits)) void paged_decod
   }
 
   // scores base 2 are scale2 times the products; under a cap they are made of them at once
-  const float scale2 = a.cap != 0.0f ? 1.0f : a.scale * kLog2e;
+  const float scale2 = a.cap != 0.0f ? 1.0f : scale_base2(a.scale);
   const float cap2 = a.cap * kLog2e, inv2 = a.cap != 0.0f ? 2.0f * kLog2e * a.scale / a.cap : 0.0f;
   float m[kNT], l[kNT];
   v4f o[kNT][kDB];

@@ -284,7 +284,7 @@ __global__ __launch_bounds__(kThreads * kGroups, 2) void paged_prefill_kernel(Pa
 
   // scores base 2 are scale2 times the products; under a cap they are made of them at once
   const bool cap = kExact ? kCap : a.cap != 0.0f;
-  const float scale2 = cap ? 1.0f : a.scale * kLog2e;
+  const float scale2 = cap ? 1.0f : scale_base2(a.scale);
   const float cap2 = a.cap * kLog2e, inv2 = cap ? 2.0f * kLog2e * a.scale / a.cap : 0.0f;
   float m = -INFINITY, l = 0.0f;
   v16f o[kDB];

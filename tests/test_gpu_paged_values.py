@@ -1,11 +1,12 @@
 """The paged cache and the attention over it at the ends of their arguments' and values' ranges: values that are not
-finite, in tiles that all rows see and in tiles that some see (bounds: paged_ref.bound)."""
+finite, in tiles that all rows see and in tiles that some see; scales (bounds: paged_ref.bound)."""
 import numpy as np
 import pytest
 import torch
 
 from paged_ref import Case
-from test_gpu_paged_attention import FORMS, call
+from test_gpu_paged_attention import FORMS, call, check
+from test_gpu_paged_variants import widened
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +54,16 @@ def test_nan_in_tiles_that_all_rows_see(gpu, form, window, hole, d, page):
     out = call(form, case, case.device(gpu), window=window)
     torch.cuda.synchronize()
     check_planted(case, out, clean, 0, marks, window)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("scale,window,cap", [(0.0, 0, 0.0), (0.0, 50, 0.0), (0.0, 0, 3.0), (1e-45, 50, 0.0), (1e-30, 0, 0.0), (0.4, 50, 0.0), (0.4, 0, 3.0)])
+def test_scales(gpu, form, bits, scale, window, cap):
+    # scale 0: the mean of the values that are seen
+    print(f"scale {form} bits={bits} scale={scale} window={window} cap={cap}", flush=True)
+    for case in (Case([(3, 400), (1, 5), (20, 20), (2, 130)], 6, 2, 64, bits, 16, 900),
+                 widened(Case([(1, 1500), (7, 300), (2, 129)], 4, 1, 128, bits, 32, 901))):
+        out = call(form, case, case.device(gpu), window=window, cap=cap, scale=scale)
+        torch.cuda.synchronize()
+        check(form, case, out, window=window, cap=cap, scale=scale)
