@@ -202,6 +202,7 @@ struct PagedArgs {
   uint32_t rot, axes, angles;  // values of a head that are rotated; positions of a token; rows of cos_sin
   uint32_t window;
   float scale, cap, eps;
+  float scale2, cap2, cap_inv2, cap_inv;  // of the scores base 2: set by score_args
 };
 hipError_t launch_paged_write(const PagedArgs &a, hipStream_t s);
 hipError_t launch_paged_read(const PagedArgs &a, hipStream_t s);

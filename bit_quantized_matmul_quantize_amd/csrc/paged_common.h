@@ -2,6 +2,8 @@
 // lie, and which sequence and tile a workgroup takes.
 #pragma once
 
+#include <algorithm>
+
 #include "bqmm_internal.h"
 
 namespace bqmm {
@@ -85,13 +87,38 @@ constexpr float kSlack = 8.0f;
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// The products times this are the scores base 2.  Not 0 where the scale is, so that the
-// score of a key that is not seen stays -infinity; 2^-149 of any product is below 2^-20.
-__device__ __forceinline__ float scale_base2(float scale) { return fmaxf(scale * kLog2e, 0x1p-149f); }
+// Caps up to here take the short form of the cap below: off by at most 2^-22 of the cap,
+// 2^-16, as the weights of decoded tokens are.
+constexpr float kShortCap = 64.0f;
 
-// c tanh(x / c) = c (1 - 2 / (1 + exp(2 x / c)))
-__device__ __forceinline__ float capped(float x, float cap, float inv2) {
-  return cap - 2.0f * cap * __builtin_amdgcn_rcpf(1.0f + exp2_hw(x * inv2));
+// The arguments with what the kernels take of scale and cap.
+inline PagedArgs score_args(PagedArgs a) {
+  // Scores base 2 are the products times this, or made of them by the cap at once.  Not 0 where
+  // the scale is, so that the score of a key that is not seen stays -infinity; 2^-149 of any
+  // product is below 2^-20.
+  a.scale2 = a.cap != 0.0f ? 1.0f : std::max(a.scale * kLog2e, 0x1p-149f);
+  a.cap2 = a.cap * kLog2e;
+  // (beyond binary32 it would make a NaN of a product of 0)
+  a.cap_inv2 = a.cap != 0.0f ? std::min(2.0f * kLog2e * a.scale / a.cap, 3.0e38f) : 0.0f;
+  a.cap_inv = a.cap != 0.0f ? 1.0f / a.cap : 0.0f;
+  return a;
+}
+
+// Of a product x, s = scale x:  c tanh(s / c) = c (1 - 2 / (1 + exp(2 s / c))), base 2
+__device__ __forceinline__ float capped(float x, float cap2, float inv2) {
+  return cap2 - 2.0f * cap2 * __builtin_amdgcn_rcpf(1.0f + exp2_hw(x * inv2));
+}
+// The same, off by at most 2^-21 of the score, for large caps: where t = s / c is small, the
+// difference above leaves nothing of it; tanh(t) = t + t^3 p(t^2), with p fitted to [0, 0.625^2]
+// (to 2^-27 of tanh(t)).
+__device__ __forceinline__ float capped_large(float x, const PagedArgs &a) {
+  const float s = x * a.scale, t = s * a.cap_inv, u = t * t;
+  float p = fmaf(u, -0x1.76abe4p-8f, 0x1.5256cap-6f);
+  p = fmaf(u, p, -0x1.b84446p-5f);
+  p = fmaf(u, p, 0x1.110768p-3f);
+  p = fmaf(u, p, -0x1.555534p-2f);
+  const float low = s * kLog2e, far = a.cap2 - 2.0f * a.cap2 * __builtin_amdgcn_rcpf(1.0f + exp2_hw(t * (2.0f * kLog2e)));
+  return fabsf(t) < 0.625f ? fmaf(low * u, p, low) : far;
 }
 
 __device__ __forceinline__ v8bf as_bf(const v4u &u) { return __builtin_bit_cast(v8bf, u); }

@@ -19,8 +19,6 @@
 // device holds at once, each with one run that may end and begin inside a sequence.
 // What such a sequence's parts give is joined by a second launch.  Where the table
 // has room for short sequences only, a workgroup takes one, and nothing is joined.
-#include <algorithm>
-
 #include "paged_common.h"
 
 namespace bqmm {
@@ -178,9 +176,8 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits)) void paged_decod
     all_low = a.window ? (int32_t)max((int64_t)any_pos + 1 - (int64_t)a.window, (int64_t)0) : 0;
   }
 
-  // scores base 2 are scale2 times the products; under a cap they are made of them at once
-  const float scale2 = a.cap != 0.0f ? 1.0f : scale_base2(a.scale);
-  const float cap2 = a.cap * kLog2e, inv2 = a.cap != 0.0f ? 2.0f * kLog2e * a.scale / a.cap : 0.0f;
+  float scale2 = a.scale2, cap2 = a.cap2, inv2 = a.cap_inv2;
+  asm volatile("" : "+v"(scale2), "+v"(cap2), "+v"(inv2));  // (else loaded anew in each step)
   float m[kNT], l[kNT];
   v4f o[kNT][kDB];
 #pragma unroll
@@ -301,10 +298,17 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits)) void paged_decod
 #pragma unroll
     for (uint32_t n = 0; n < kNT; ++n) {
       if (a.cap != 0.0f) {
+        if (a.cap <= kShortCap) {
 #pragma unroll
-        for (uint32_t t = 0; t < kKT; ++t)
+          for (uint32_t t = 0; t < kKT; ++t)
 #pragma unroll
-          for (uint32_t e = 0; e < 4; ++e) x[n][t][e] = capped(x[n][t][e], cap2, inv2);
+            for (uint32_t e = 0; e < 4; ++e) x[n][t][e] = capped(x[n][t][e], cap2, inv2);
+        } else {
+#pragma unroll
+          for (uint32_t t = 0; t < kKT; ++t)
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e) x[n][t][e] = capped_large(x[n][t][e], a);
+        }
       }
       if (!whole) {
 #pragma unroll
@@ -679,7 +683,7 @@ hipError_t launch_bits(const PagedArgs &a, const Plan &plan, hipStream_t s) {
 
 hipError_t launch_paged_decode(const PagedArgs &a, hipStream_t s) {
   const Plan plan = plan_of(a);
-  return a.bits == 16u ? launch_bits<16>(a, plan, s) : launch_bits<8>(a, plan, s);
+  return a.bits == 16u ? launch_bits<16>(score_args(a), plan, s) : launch_bits<8>(score_args(a), plan, s);
 }
 
 // The two parts of each run, for tiles of the most rows and as many runs as any form

@@ -16,8 +16,6 @@
 // softmax needs no exchange between lanes, and the weights of its keys are an
 // operand of the second product as they are, given the order in which K's rows
 // are read: row 8 b + 4 h + j of the first product is key 16 (b / 2) + 8 h + 4 (b % 2) + j.
-#include <algorithm>
-
 #include "paged_common.h"
 
 namespace bqmm {
@@ -123,9 +121,9 @@ __device__ __forceinline__ bool take_tile(const PagedArgs &a, uint32_t item, uin
 }
 
 // kExact: a head has kDP values, and a page has at least a tile's keys.
-// kCap: scores are capped (both may be, unless kExact).
+// kCap: 0: scores are as they are; 1: capped, by up to kShortCap; 2: by more.
 // kGroups: groups of four waves; two of them share the tiles of keys of the same rows.
-template <uint32_t kDP, uint32_t kBits, bool kExact, bool kCap, uint32_t kGroups>
+template <uint32_t kDP, uint32_t kBits, bool kExact, int kCap, uint32_t kGroups>
 __global__ __launch_bounds__(kThreads * kGroups, 2) void paged_prefill_kernel(PagedArgs a) {
   using S = Shape<kDP, kBits>;
   constexpr uint32_t kKT = S::kKT, kSubs = S::kSubs;
@@ -282,10 +280,9 @@ __global__ __launch_bounds__(kThreads * kGroups, 2) void paged_prefill_kernel(Pa
     }
   };
 
-  // scores base 2 are scale2 times the products; under a cap they are made of them at once
-  const bool cap = kExact ? kCap : a.cap != 0.0f;
-  const float scale2 = cap ? 1.0f : scale_base2(a.scale);
-  const float cap2 = a.cap * kLog2e, inv2 = cap ? 2.0f * kLog2e * a.scale / a.cap : 0.0f;
+  // (vector registers: with more scalar ones the loop loads arguments anew for each tile)
+  float scale2 = a.scale2, cap2 = a.cap2, inv2 = a.cap_inv2;
+  asm volatile("" : "+v"(scale2), "+v"(cap2), "+v"(inv2));
   float m = -INFINITY, l = 0.0f;
   v16f o[kDB];
 #pragma unroll
@@ -361,9 +358,9 @@ __global__ __launch_bounds__(kThreads * kGroups, 2) void paged_prefill_kernel(Pa
           for (uint32_t e = 0; e < 4; ++e) x[f][i + e] *= s[e];
         }
       }
-      if (cap) {
+      if constexpr (kCap != 0) {
 #pragma unroll
-        for (uint32_t i = 0; i < 16; ++i) x[f][i] = capped(x[f][i], cap2, inv2);
+        for (uint32_t i = 0; i < 16; ++i) x[f][i] = kCap == 1 ? capped(x[f][i], cap2, inv2) : capped_large(x[f][i], a);
       }
     }
     if (!whole) {
@@ -554,7 +551,7 @@ __global__ __launch_bounds__(kThreads * kGroups, 2) void paged_prefill_kernel(Pa
   }
 }
 
-template <uint32_t kDP, uint32_t kBits, bool kExact, bool kCap, uint32_t kGroups>
+template <uint32_t kDP, uint32_t kBits, bool kExact, int kCap, uint32_t kGroups>
 hipError_t launch(const PagedArgs &a, uint32_t groups, hipStream_t s) {
   using S = Shape<kDP, kBits>;
   constexpr uint32_t kSums = (kDP * 2u + 8u) * kThreads;  // of the second group
@@ -568,7 +565,7 @@ hipError_t launch(const PagedArgs &a, uint32_t groups, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <uint32_t kDP, uint32_t kBits, bool kExact, bool kCap>
+template <uint32_t kDP, uint32_t kBits, bool kExact, int kCap>
 hipError_t launch_groups(const PagedArgs &a, hipStream_t s) {
   // (of a sequence with rows: at most one tile that is not full)
   const uint64_t rows = (uint64_t)a.tokens * (a.hq / a.hk), tiles = (rows + (kRows - 1ull) * std::min(a.count, a.tokens)) / kRows;
@@ -578,8 +575,10 @@ hipError_t launch_groups(const PagedArgs &a, hipStream_t s) {
 
 template <uint32_t kDP, uint32_t kBits>
 hipError_t launch_exact(const PagedArgs &a, hipStream_t s) {
-  if (a.d != kDP || (1u << a.page_shift) < Shape<kDP, kBits>::kKT) return launch_groups<kDP, kBits, false, false>(a, s);
-  return a.cap != 0.0f ? launch_groups<kDP, kBits, true, true>(a, s) : launch_groups<kDP, kBits, true, false>(a, s);
+  const bool exact = a.d == kDP && (1u << a.page_shift) >= Shape<kDP, kBits>::kKT;
+  if (a.cap == 0.0f) return exact ? launch_groups<kDP, kBits, true, 0>(a, s) : launch_groups<kDP, kBits, false, 0>(a, s);
+  if (a.cap <= kShortCap) return exact ? launch_groups<kDP, kBits, true, 1>(a, s) : launch_groups<kDP, kBits, false, 1>(a, s);
+  return launch_groups<kDP, kBits, false, 2>(a, s);  // (rare: for all heads and pages alike)
 }
 
 template <uint32_t kBits>
@@ -593,7 +592,7 @@ hipError_t launch_heads(const PagedArgs &a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_paged_prefill(const PagedArgs &a, hipStream_t s) {
-  return a.bits == 16u ? launch_heads<16>(a, s) : launch_heads<8>(a, s);
+  return a.bits == 16u ? launch_heads<16>(score_args(a), s) : launch_heads<8>(score_args(a), s);
 }
 
 }  // namespace bqmm

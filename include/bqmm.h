@@ -474,7 +474,8 @@ int read_kv_cache(const void *k_cache, const void *v_cache, void *k_bf16, void *
  * 32 rows times the table's blocks of 64 keys below 2^31.
  *
  * Products of bf16 values (int8 codes are exact in bf16) are summed in binary32,
- * and so are the softmax's maximum and sum.  _decode takes the weights w_j as sums
+ * and so are the softmax's maximum and sum; a cap leaves scores off by at most
+ * 2^-16, caps above 64 by 2^-21 of the score.  _decode takes the weights w_j as sums
  * of two bf16, _prefill rounds them to one (by at most 2^-8 of each).  A call's
  * result is the same bit for bit when it is called again.
  * _decode reads each key once for 16 or 32 rows (new tokens times hq / hk) and cuts

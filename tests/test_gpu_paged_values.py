@@ -1,10 +1,10 @@
 """The paged cache and the attention over it at the ends of their arguments' and values' ranges: values that are not
-finite, in tiles that all rows see and in tiles that some see; scales (bounds: paged_ref.bound)."""
+finite, in tiles that all rows see and in tiles that some see; scales and caps (bounds: paged_ref.bound)."""
 import numpy as np
 import pytest
 import torch
 
-from paged_ref import Case
+from paged_ref import Case, attention, bound
 from test_gpu_paged_attention import FORMS, call, check
 from test_gpu_paged_variants import widened
 
@@ -67,3 +67,32 @@ def test_scales(gpu, form, bits, scale, window, cap):
         out = call(form, case, case.device(gpu), window=window, cap=cap, scale=scale)
         torch.cuda.synchronize()
         check(form, case, out, window=window, cap=cap, scale=scale)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("cap,spread", [(50.0, 1.0), (64.0, 40.0), (65.0, 40.0), (100.0, 60.0), (1e3, 1.0), (1e3, 300.0), (1e5, 1.0), (1e6, 4.0),
+                                        (1e8, 1.0), (1e20, 1.0)])
+def test_caps(gpu, form, bits, page, cap, spread):
+    # the bound has no term that grows with the cap: caps that are far above the scores leave them as they are
+    print(f"cap {form} bits={bits} page={page} cap={cap} spread={spread}", flush=True)
+    for case in (Case([(3, 400), (1, 5), (20, 20), (2, 130)], 6, 2, 64, bits, page, 910, spread=spread),
+                 widened(Case([(1, 1500), (9, 300), (2, 129)], 4, 1, 128, bits, page, 911, spread=spread))):
+        out = call(form, case, case.device(gpu), cap=cap)
+        torch.cuda.synchronize()
+        ref, size, most = attention(case, cap=cap)
+        off = np.abs(out.double().cpu().numpy() - ref)
+        far = off - bound(case, ref, size, most, form)
+        assert np.isfinite(off).all() and far.max() <= 0, f"off by {off.max():.3e}, {far.max():.3e} over the bound"
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("bits", [16, 8])
+def test_caps_far_below_the_scores(gpu, form, bits):
+    # scale / cap is beyond binary32; a query of zeros, whose scores are 0
+    case = Case([(3, 400), (20, 20)], 6, 2, 64, bits, 16, 912)
+    case.packed[1] = 0
+    out = call(form, case, case.device(gpu), cap=1e-20, scale=1e30)
+    torch.cuda.synchronize()
+    check(form, case, out, cap=1e-20, scale=1e30)
