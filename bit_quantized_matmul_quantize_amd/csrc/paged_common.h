@@ -88,7 +88,7 @@ constexpr float kSlack = 8.0f;
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Caps up to here take the short form of the cap below: off by at most 2^-22 of the cap,
-// 2^-16, as the weights of decoded tokens are.
+// 2^-16, less than the weights' own rounding.
 constexpr float kShortCap = 64.0f;
 
 // The arguments with what the kernels take of scale and cap.

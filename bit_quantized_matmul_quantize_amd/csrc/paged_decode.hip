@@ -80,6 +80,9 @@ Parts parts_of(uint8_t *workspace, uint32_t slots, uint32_t hk, uint32_t tile_ro
   return {reinterpret_cast<float *>(workspace), reinterpret_cast<float2 *>(stats), reinterpret_cast<uint2 *>(stats + rows * 8u)};
 }
 
+// The bits of the next binary32 towards 0, of 0 itself.
+__device__ __forceinline__ uint32_t below(float w) { return __builtin_elementwise_sub_sat(__float_as_uint(w), 1u); }
+
 // ---- a run ------------------------------------------------------------------------
 
 // Waves of a SIMD that the registers are to suffice for.  Two where they do without
@@ -335,7 +338,9 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits)) void paged_decod
         for (uint32_t b = 0; b < kDB; ++b) o[n][b] *= keep;
       }
       const float base = m[n] == -INFINITY ? 0.0f : m[n];
-      // the sum of two bf16: one would be off by 2^-8 of each weight
+      // the sum of two bf16: one would be off by 2^-8 of each weight.  Over a bf16 cache the
+      // first is below the weight, so that the second is above 0 too, and an infinity of v
+      // times both stays one (by 2^-15 off, to the nearest by 2^-16; the same time).
       uint32_t hi[kKT][2], lo[kKT][2];
 #pragma unroll
       for (uint32_t t = 0; t < kKT; ++t) {
@@ -349,7 +354,10 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits)) void paged_decod
         }
 #pragma unroll
         for (uint32_t e = 0; e < 2; ++e) {
-          hi[t][e] = two_bf16(w[2 * e], w[2 * e + 1]);
+          if constexpr (kBits == 16u)
+            hi[t][e] = __builtin_amdgcn_perm(below(w[2 * e + 1]), below(w[2 * e]), 0x07060302u);
+          else
+            hi[t][e] = two_bf16(w[2 * e], w[2 * e + 1]);
           lo[t][e] = two_bf16(w[2 * e] - __uint_as_float(hi[t][e] << 16), w[2 * e + 1] - __uint_as_float(hi[t][e] & 0xFFFF0000u));
         }
       }

@@ -96,3 +96,25 @@ def test_caps_far_below_the_scores(gpu, form, bits):
     out = call(form, case, case.device(gpu), cap=1e-20, scale=1e30)
     torch.cuda.synchronize()
     check(form, case, out, cap=1e-20, scale=1e30)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("keys", [0, 4096])
+@pytest.mark.parametrize("d,hq", [(64, 4), (64, 16), (80, 4), (128, 4), (128, 16), (256, 4), (256, 16)])
+def test_infinities(gpu, form, keys, d, hq):
+    # each in a column of its own, in steps that all rows see and in steps that some see; and two that make a NaN
+    print(f"inf {form} keys={keys} d={d} hq={hq}", flush=True)
+    case = widened(Case([(20, 700), (1, 900), (9, 60)], hq, 2, d, 16, 64, 920 + d), keys)
+    clean = call(form, case, case.device(gpu))
+    inf = np.inf
+    marks = [[(3, 1, inf), (40, 2, -inf), (100, 3, inf), (333, 4, inf), (685, 5, -inf), (695, 6, inf), (50, 7, inf), (690, 7, -inf)],
+             [(0, 1, -inf), (31, 2, inf), (500, 3, inf), (899, 4, -inf)], [(54, 8, inf), (10, 9, -inf)]]
+    for seq, m in enumerate(marks):
+        planted(case, seq, m)
+    out = call(form, case, case.device(gpu))
+    torch.cuda.synchronize()
+    for seq, m in enumerate(marks):
+        rows = slice(int(case.starts[seq]), int(case.starts[seq + 1]))
+        one = Case.__new__(Case)
+        one.lens, one.starts = [case.lens[seq]], np.array([0, case.lens[seq][0]])
+        check_planted(one, out[rows], clean[rows], 0, m)
