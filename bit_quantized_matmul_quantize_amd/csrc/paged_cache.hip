@@ -74,19 +74,26 @@ __device__ __forceinline__ uint4 pack8(const float *x) {
   return make_uint4(two_bf16(x[0], x[1]), two_bf16(x[2], x[3]), two_bf16(x[4], x[5]), two_bf16(x[6], x[7]));
 }
 
-// Codes of 16 values whose row's largest magnitude has the bits `top`.  127 / top is
-// in range from 2^-120 on; smaller rows are scaled up first.  A row with a NaN or
-// an infinity gets zero codes.
+// Codes of 16 values whose row's largest magnitude has the bits `top`.  A row with a NaN
+// or an infinity gets zero codes.
 __device__ __forceinline__ void quantize16(const float *x, uint32_t top, uint32_t *codes, float *scale) {
-  const float t = __uint_as_float(top);
   const bool some = top != 0u && top < 0x7F800000u;
-  const float up = t < 0x1p-120f ? 0x1p+40f : 1.0f, inv = some ? 127.0f / (t * up) : 0.0f;
-  *scale = t / 127.0f;
+  // a power of two that brings top to [2^-29, 2): neither 127 t nor 1 / top nor 127 p overflows
+  const float p = ldexpf(1.0f, min(127 - (int)(top >> 23), 120));
+  const float t = some ? __uint_as_float(top) * p : 1.0f, mul = 127.0f * p, inv = 1.0f / t;
+  *scale = __uint_as_float(top) / 127.0f;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     uint32_t c[4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) c[b] = (uint32_t)(int)(some ? rintf(x[4 * w + b] * up * inv) : 0.0f);
+    for (int b = 0; b < 4; ++b) {
+      // the correctly rounded quotient: one residual step from a reciprocal that is itself
+      // correctly rounded (without it a half of the largest is off by a code for one row in nine)
+      const float num = x[4 * w + b] * mul, q0 = num * inv;
+      const float q = fmaf(fmaf(-q0, t, num), inv, q0);
+      // beside 1.5 * 2^23 only whole numbers are left, the nearest (ties to even), in the low bits
+      c[b] = some ? __float_as_uint(q + 12582912.0f) : 0u;
+    }
     // the low bytes of four words
     const uint32_t lo = __builtin_amdgcn_perm(c[1], c[0], 0x0C0C0400u), hi = __builtin_amdgcn_perm(c[3], c[2], 0x0C0C0400u);
     codes[w] = lo | hi << 16;

@@ -1,11 +1,13 @@
 """The paged cache and the attention over it at the ends of their arguments' and values' ranges: values that are not
-finite, in tiles that all rows see and in tiles that some see; scales and caps (bounds: paged_ref.bound)."""
+finite, in tiles that all rows see and in tiles that some see; scales and caps; ties between
+int8 codes (bounds: paged_ref.bound)."""
 import numpy as np
 import pytest
 import torch
 
-from paged_ref import Case, attention, bound
+from paged_ref import Cache, Case, attention, bound
 from test_gpu_paged_attention import FORMS, call, check
+from test_gpu_paged_cache import make, write
 from test_gpu_paged_variants import widened
 
 pytestmark = pytest.mark.gpu
@@ -118,3 +120,30 @@ def test_infinities(gpu, form, keys, d, hq):
         one = Case.__new__(Case)
         one.lens, one.starts = [case.lens[seq]], np.array([0, case.lens[seq][0]])
         check_planted(one, out[rows], clean[rows], 0, m)
+
+
+def test_codes_are_the_nearest(gpu):
+    # rows of all magnitudes; with halves of the largest value, whose quotients lie between two codes
+    n, hk, d = 400, 2, 64
+    c = make([(n, n)], 1, hk, d, 8, 16, 930, 0)
+    gen = torch.Generator().manual_seed(931)
+    top = torch.rand(n, 2 * hk, 1, generator=gen) + 1
+    x = torch.rand(n, 2 * hk, d, generator=gen) * 2 - 1
+    x[..., 0], x[..., 1], x[..., 2] = 1, 0.5, -0.5
+    power = torch.randint(-133, 127, (n, 2 * hk, 1), generator=gen).double()
+    x = (x.double() * (top.bfloat16().double() * torch.exp2(power)))
+    c.packed[:, d:d + 2 * hk * d] = x.bfloat16().flatten(1)
+    _, t = write(c, gpu)
+    got = Cache(c.cache.pages, 16, hk, d, 8)
+    got.k, got.v = t["k_cache"].cpu().numpy(), t["v_cache"].cpu().numpy()
+    x = c.packed[:, d:d + 2 * hk * d].float().numpy().reshape(n, 2 * hk, d)
+    for keys in (True, False):
+        rows = x[:, :hk] if keys else x[:, hk:]
+        for p in range(n):
+            for h in range(hk):
+                block, at = got._at(keys, c.table[0, p // 16], h)
+                big = np.abs(rows[p, h]).max()
+                scaled = rows[p, h].astype(np.float64) * 127  # exact; so is the nearest code of the quotient in 64 bits
+                want = np.rint(scaled / big) if big else np.zeros(d)
+                assert (block[:16 * d].view(np.int8)[at[p % 16]] == want).all(), (keys, p, h)
+                assert block[16 * d:].view(np.float32)[p % 16] == big / np.float32(127)
