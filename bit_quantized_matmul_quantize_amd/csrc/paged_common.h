@@ -81,8 +81,9 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
-// The running maximum of the scores (base 2) may lag by this, so that sums are
-// rescaled rarely: weights are at most 2^8, which costs no bits.
+// The running maximum of the scores (base 2) is set this far above the largest one, so that
+// it is raised, and sums are rescaled, rarely: weights are at most 1, and of the largest score
+// at least 2^-8, which costs no bits.
 constexpr float kSlack = 8.0f;
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }

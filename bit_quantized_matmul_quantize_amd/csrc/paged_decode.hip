@@ -327,10 +327,10 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits)) void paged_decod
 #pragma unroll
       for (uint32_t t = 0; t < kKT; ++t) top = fmaxf(fmaxf(fmaxf(x[n][t][0], x[n][t][1]), top), fmaxf(x[n][t][2], x[n][t][3]));
       top *= scale2;
-      if (__ballot(top > m[n] + kSlack)) {
+      if (__ballot(top > m[n])) {
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float next = fmaxf(m[n], top);
+        const float next = fmaxf(m[n], top + kSlack);
         const float keep = m[n] == -INFINITY ? 0.0f : exp2_hw(m[n] - next);
         m[n] = next;
         l[n] *= keep;

@@ -380,9 +380,9 @@ __global__ __launch_bounds__(kThreads * kGroups, 2) void paged_prefill_kernel(Pa
 #pragma unroll
       for (uint32_t i = 0; i < 16; i += 2) top = fmaxf(fmaxf(x[f][i], x[f][i + 1]), top);
     top *= scale2;
-    if (__ballot(top > m + kSlack)) {
+    if (__ballot(top > m)) {
       top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const float next = fmaxf(m, top);
+      const float next = fmaxf(m, top + kSlack);
       const float keep = m == -INFINITY ? 0.0f : exp2_hw(m - next);
       m = next;
       l *= keep;

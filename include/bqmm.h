@@ -468,6 +468,7 @@ int read_kv_cache(const void *k_cache, const void *v_cache, void *k_bf16, void *
  *   out = bf16_rne(sum_j w_j v_j / sum_j w_j),  w_j = exp(s_j - max s),
  * over the keys j <= p of its sequence, and where window is not 0 j > p - window.
  * A token that sees no key, or only keys with a score of -infinity, gives zeros.
+ * The sum of |v_j| over the keys that a token sees has to stay below 2^128.
  * NaNs and infinities of v reach the tokens that see them and no others; an infinity
  * whose weight is below 2^-90 of the largest, as itself or as a NaN.
  * q: bf16, head h of token t starts at t * q_token + h * q_head; out: bf16

@@ -1,6 +1,6 @@
 """The paged cache and the attention over it at the ends of their arguments' and values' ranges: values that are not
-finite, in tiles that all rows see and in tiles that some see; scales and caps; ties between
-int8 codes (bounds: paged_ref.bound)."""
+finite, in tiles that all rows see and in tiles that some see; the largest values; scales and caps; ties between int8
+codes (bounds: paged_ref.bound)."""
 import numpy as np
 import pytest
 import torch
@@ -147,3 +147,32 @@ def test_codes_are_the_nearest(gpu):
                 want = np.rint(scaled / big) if big else np.zeros(d)
                 assert (block[:16 * d].view(np.int8)[at[p % 16]] == want).all(), (keys, p, h)
                 assert block[16 * d:].view(np.float32)[p % 16] == big / np.float32(127)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("d,keys", [(64, 0), (64, 4096), (128, 0), (128, 4096), (256, 4096)])
+def test_large_values(gpu, form, bits, d, keys):
+    # values whose sum is just below 2^128, behind keys with lower scores (by a factor of 2^7.5 in the weights), so that
+    # the running maximum is one of those
+    n, low = (2000, 1152) if keys else (960, 512)
+    case = Case([(1, n), (40, n)], 2, 1, d, bits, 64, 940)
+    case.packed.zero_()
+    case.packed[:, 0:2 * d:d] = 1
+    for seq in range(2):
+        for p in range(n):
+            k, v = np.zeros((1, d)), np.full((1, d), 2.0 ** 116)
+            k[0, 0] = 0.0 if p < low else 5.1875
+            for rows, keyed in ((k, True), (v, False)):
+                case.rows[seq][0 if keyed else 1][p] = rows
+                if bits == 8:
+                    top = np.abs(rows).max()
+                    scale = np.float32(top / 127)
+                    rows = (np.rint(rows / (top or 1) * 127).astype(np.int8), np.full(1, scale, dtype=np.float32))
+                    case.rows[seq][0 if keyed else 1][p] = rows[0] * rows[1].astype(np.float64)[:, None]
+                case.cache.put(keyed, case.table[seq, p // 64], p % 64, rows)
+    if keys:
+        case = widened(case, keys)
+    out = call(form, case, case.device(gpu), scale=1.0)
+    torch.cuda.synchronize()
+    check(form, case, out, scale=1.0)
