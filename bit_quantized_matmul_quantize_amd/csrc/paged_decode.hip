@@ -85,18 +85,24 @@ __device__ __forceinline__ uint32_t below(float w) { return __builtin_elementwis
 
 // ---- a run ------------------------------------------------------------------------
 
-// Waves of a SIMD that the registers are to suffice for.  Two where they do without
-// spills in the loop: one token of 96 sequences, heads of 80: 93 us, with three and
-// spills 105; eight tokens of 16 sequences, int8 heads of 128: 105 us, with one wave
-// 120; one of 16, bf16 heads of 256: 70 us with one, with two and spills 111.
-// (All with an older join, 2 to 3 us longer.)
-constexpr int waves_of(uint32_t dp, uint32_t bits) { return dp > 128u && bits == 16u ? 1 : 2; }
+// Waves of a SIMD that the registers are to suffice for.  Two where they do with few spills:
+// one token of 96 sequences, heads of 80: 93 us, with three waves and spills 105; 8 tokens of
+// 16 sequences up to 16384, int8 heads of 128: 103 us, with one wave 114, bf16 heads of 96 103
+// and 115.  (32 rows of these spill up to 28 registers, nearly all outside the loop; of bf16
+// heads between 128 and 256 they spill 155 with one wave, too.)  One wave for a run of
+// 32 rows of bf16 heads of 128, where two spill 80 to 94: those 16 sequences 137 us, with two
+// 148, 64 of up to 8192 258 and 280 (128 of up to 2000: 192 and 186); a whole short sequence
+// spills 20 with two: 64 of up to 900 47.5 us, with one 58.  One for bf16 heads of 256: one
+// token of 16 sequences 68 us, with two and spills 111.
+constexpr int waves_of(uint32_t dp, uint32_t bits, uint32_t nt, bool cut) {
+  return bits == 16u && (dp > 128u || (dp > 96u && nt > 1u && cut)) ? 1 : 2;
+}
 
 // kDP: values of a head, rounded up (kExact: as they are); kNT: column blocks of 16
 // rows.
 // kCut: a workgroup takes a run of blocks, else one tile of rows and its sequence.
 template <uint32_t kDP, uint32_t kBits, uint32_t kNT, bool kExact, uint32_t kWaves, bool kCut>
-__global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits)) void paged_decode_kernel(PagedArgs a, uint32_t slots, Parts parts) {
+__global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits, kNT, kCut)) void paged_decode_kernel(PagedArgs a, uint32_t slots, Parts parts) {
   constexpr uint32_t kUnit = 128u / kBits;        // values of a unit
   constexpr uint32_t kKeys = kBits == 8u && kDP <= 128u ? 64 : 32;  // keys of a step
   constexpr uint32_t kKT = kKeys / 16u;           // their tiles
@@ -644,7 +650,7 @@ Plan plan_of(const PagedArgs &a) {
   // (of a sequence with rows: at most one tile that is not full)
   p.tiles = (uint32_t)std::min<uint64_t>(rows / tile + std::min(a.count, a.tokens), (uint64_t)a.tokens * ((g + tile - 1u) / tile));
   // as many workgroups as the device holds at once (four waves: one to a SIMD)
-  p.slots = std::max(kCus * (uint32_t)waves_of(dp, a.bits) / a.hk, 1u);
+  p.slots = std::max(kCus * (uint32_t)waves_of(dp, a.bits, p.blocks, true) / a.hk, 1u);
   return p;
 }
 
