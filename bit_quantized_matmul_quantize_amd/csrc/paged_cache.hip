@@ -133,123 +133,123 @@ __global__ __launch_bounds__(kThreads) void paged_write_kernel(PagedArgs a, uint
   const uint64_t row = (uint64_t)t.span.first + (uint32_t)(t.place0 + (int32_t)token - t.span.at);
 
   if (blockIdx.y < parts) {
-  // this lane's runs of a head: a pair that is rotated, or two that are not
-  const uint32_t pairs = a.rot / 16u;
-  const bool turned = lane < pairs;
-  const uint32_t run0 = turned ? lane : 2u * lane, run1 = turned ? lane + pairs : run0 + 1u;
-  // q and k: the first heads are on their way while the angles are looked up, the
-  // next ones while these are computed
-  const uint32_t heads = a.hq + a.hk, stride = parts * kHeads;
-  auto load = [&](uint32_t h, uint4 (&raw)[2]) {
-    if (mine && h < heads) {
-      const uint16_t *p = h < a.hq ? a.q + row * a.q_token + h * a.q_head : a.k + row * a.k_token + (h - a.hq) * a.k_head;
-      raw[0] = *reinterpret_cast<const uint4 *>(p + run0 * 8u);
-      raw[1] = *reinterpret_cast<const uint4 *>(p + run1 * 8u);
-    }
-  };
-  uint4 raw[2] = {};
-  load(blockIdx.y * kHeads + sub, raw);
-  float c[8], s[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) c[e] = 1.0f, s[e] = 0.0f;
-  if (mine && turned) {
-    const float nan = __uint_as_float(0x7FC00000u);
-    if (!a.axis) {  // 
-      const int32_t angle = a.positions ? a.positions[row] : t.place0 + (int32_t)token;
-      const bool known = (uint32_t)angle < a.angles;
-      const float *at = a.cos_sin + (uint64_t)(known ? angle : 0) * a.rot + lane * 8u;
-      const Float8 cv = *reinterpret_cast<const Float8 *>(at), sv = *reinterpret_cast<const Float8 *>(at + a.rot / 2u);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) c[e] = known ? cv.x[e] : nan, s[e] = known ? sv.x[e] : nan;
-    } else {
-      int32_t angle[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t axis = a.axis[lane * 8u + e];
-        angle[e] = a.positions[(uint64_t)(axis < a.axes ? axis : 0u) * a.tokens + row];
-        if (axis >= a.axes) angle[e] = -1;
+    // this lane's runs of a head: a pair that is rotated, or two that are not
+    const uint32_t pairs = a.rot / 16u;
+    const bool turned = lane < pairs;
+    const uint32_t run0 = turned ? lane : 2u * lane, run1 = turned ? lane + pairs : run0 + 1u;
+    // q and k: the first heads are on their way while the angles are looked up, the
+    // next ones while these are computed
+    const uint32_t heads = a.hq + a.hk, stride = parts * kHeads;
+    auto load = [&](uint32_t h, uint4 (&raw)[2]) {
+      if (mine && h < heads) {
+        const uint16_t *p = h < a.hq ? a.q + row * a.q_token + h * a.q_head : a.k + row * a.k_token + (h - a.hq) * a.k_head;
+        raw[0] = *reinterpret_cast<const uint4 *>(p + run0 * 8u);
+        raw[1] = *reinterpret_cast<const uint4 *>(p + run1 * 8u);
       }
+    };
+    uint4 raw[2] = {};
+    load(blockIdx.y * kHeads + sub, raw);
+    float c[8], s[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const bool known = (uint32_t)angle[e] < a.angles;
-        const float *at = a.cos_sin + (uint64_t)(known ? angle[e] : 0) * a.rot + lane * 8u + e;
-        c[e] = known ? at[0] : nan;
-        s[e] = known ? at[a.rot / 2u] : nan;
+    for (int e = 0; e < 8; ++e) c[e] = 1.0f, s[e] = 0.0f;
+    if (mine && turned) {
+      const float nan = __uint_as_float(0x7FC00000u);
+      if (!a.axis) {  // one row of the table a token, read as vectors
+        const int32_t angle = a.positions ? a.positions[row] : t.place0 + (int32_t)token;
+        const bool known = (uint32_t)angle < a.angles;
+        const float *at = a.cos_sin + (uint64_t)(known ? angle : 0) * a.rot + lane * 8u;
+        const Float8 cv = *reinterpret_cast<const Float8 *>(at), sv = *reinterpret_cast<const Float8 *>(at + a.rot / 2u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e] = known ? cv.x[e] : nan, s[e] = known ? sv.x[e] : nan;
+      } else {
+        int32_t angle[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t axis = a.axis[lane * 8u + e];
+          angle[e] = a.positions[(uint64_t)(axis < a.axes ? axis : 0u) * a.tokens + row];
+          if (axis >= a.axes) angle[e] = -1;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const bool known = (uint32_t)angle[e] < a.angles;
+          const float *at = a.cos_sin + (uint64_t)(known ? angle[e] : 0) * a.rot + lane * 8u + e;
+          c[e] = known ? at[0] : nan;
+          s[e] = known ? at[a.rot / 2u] : nan;
+        }
       }
     }
-  }
-  // the norms' weights of this lane's runs
-  uint4 wq[2] = {}, wk[2] = {};
-  if (lane < a.d / 16u) {
-    if (a.q_norm) {
-      wq[0] = *reinterpret_cast<const uint4 *>(a.q_norm + run0 * 8u);
-      wq[1] = *reinterpret_cast<const uint4 *>(a.q_norm + run1 * 8u);
+    // the norms' weights of this lane's runs
+    uint4 wq[2] = {}, wk[2] = {};
+    if (lane < a.d / 16u) {
+      if (a.q_norm) {
+        wq[0] = *reinterpret_cast<const uint4 *>(a.q_norm + run0 * 8u);
+        wq[1] = *reinterpret_cast<const uint4 *>(a.q_norm + run1 * 8u);
+      }
+      if (a.k_norm) {
+        wk[0] = *reinterpret_cast<const uint4 *>(a.k_norm + run0 * 8u);
+        wk[1] = *reinterpret_cast<const uint4 *>(a.k_norm + run1 * 8u);
+      }
     }
-    if (a.k_norm) {
-      wk[0] = *reinterpret_cast<const uint4 *>(a.k_norm + run0 * 8u);
-      wk[1] = *reinterpret_cast<const uint4 *>(a.k_norm + run1 * 8u);
-    }
-  }
 
-  for (uint32_t h0 = blockIdx.y * kHeads; h0 < heads; h0 += stride) {
-    const uint32_t h = h0 + sub;
-    const bool is_q = h < a.hq, live = mine && h < heads;
-    float x[16];
-    unpack8(raw[0], x);
-    unpack8(raw[1], x + 8);
-    if (!live) {  // (of no row: zeros)
+    for (uint32_t h0 = blockIdx.y * kHeads; h0 < heads; h0 += stride) {
+      const uint32_t h = h0 + sub;
+      const bool is_q = h < a.hq, live = mine && h < heads;
+      float x[16];
+      unpack8(raw[0], x);
+      unpack8(raw[1], x + 8);
+      if (!live) {  // (of no row: zeros)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = 0.0f;
-    }
-    load(h + stride, raw);
-    if (a.q_norm || a.k_norm) {
-      float sum = 0.0f;
+        for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+      }
+      load(h + stride, raw);
+      if (a.q_norm || a.k_norm) {
+        float sum = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) sum = fmaf(x[e], x[e], sum);
-      sum = row_sum(sum, G);
-      if (live && (is_q ? a.q_norm : a.k_norm)) {
-        const float r = 1.0f / sqrtf(sum / (float)a.d + a.eps);
-        float w[16];
-        unpack8(is_q ? wq[0] : wk[0], w);
-        unpack8(is_q ? wq[1] : wk[1], w + 8);
+        for (int e = 0; e < 16; ++e) sum = fmaf(x[e], x[e], sum);
+        sum = row_sum(sum, G);
+        if (live && (is_q ? a.q_norm : a.k_norm)) {
+          const float r = 1.0f / sqrtf(sum / (float)a.d + a.eps);
+          float w[16];
+          unpack8(is_q ? wq[0] : wk[0], w);
+          unpack8(is_q ? wq[1] : wk[1], w + 8);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = x[e] * r * w[e];
+          for (int e = 0; e < 16; ++e) x[e] = x[e] * r * w[e];
+        }
       }
-    }
-    if (turned) {
+      if (turned) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float u = x[e], v = x[e + 8];
-        x[e] = fmaf(u, c[e], -v * s[e]);
-        x[e + 8] = fmaf(v, c[e], u * s[e]);
+        for (int e = 0; e < 8; ++e) {
+          const float u = x[e], v = x[e + 8];
+          x[e] = fmaf(u, c[e], -v * s[e]);
+          x[e + 8] = fmaf(v, c[e], u * s[e]);
+        }
+      }
+      if (is_q) {
+        if (live) {
+          uint16_t *p = a.out + (row * a.hq + h) * a.d;
+          *reinterpret_cast<uint4 *>(p + run0 * 8u) = pack8(x);
+          *reinterpret_cast<uint4 *>(p + run1 * 8u) = pack8(x + 8);
+        }
+      }
+      if (a.bits == 16u) {
+        if (!is_q && live && id >= 0) {
+          uint8_t *p = a.k_cache + ((uint64_t)id * a.hk + (h - a.hq)) * block + (off + token) * 16u;
+          *reinterpret_cast<uint4 *>(p + (uint64_t)run0 * page * 16u) = pack8(x);
+          *reinterpret_cast<uint4 *>(p + (uint64_t)run1 * page * 16u) = pack8(x + 8);
+        }
+      } else if (__any(!is_q && live)) {
+        const uint32_t top = row_max(top16(x), G);
+        if (!is_q && live && id >= 0) {
+          uint32_t codes[4];
+          float scale;
+          quantize16(x, top, codes, &scale);
+          uint8_t *p = a.k_cache + ((uint64_t)id * a.hk + (h - a.hq)) * block;
+          *reinterpret_cast<uint2 *>(p + ((run0 / 2u) * page + off + token) * 16u + (run0 & 1u) * 8u) = make_uint2(codes[0], codes[1]);
+          *reinterpret_cast<uint2 *>(p + ((run1 / 2u) * page + off + token) * 16u + (run1 & 1u) * 8u) = make_uint2(codes[2], codes[3]);
+          if (lane == 0u) *reinterpret_cast<float *>(p + page * a.d + (off + token) * 4u) = scale;
+        }
       }
     }
-    if (is_q) {
-      if (live) {
-        uint16_t *p = a.out + (row * a.hq + h) * a.d;
-        *reinterpret_cast<uint4 *>(p + run0 * 8u) = pack8(x);
-        *reinterpret_cast<uint4 *>(p + run1 * 8u) = pack8(x + 8);
-      }
-    }
-    if (a.bits == 16u) {
-      if (!is_q && live && id >= 0) {
-        uint8_t *p = a.k_cache + ((uint64_t)id * a.hk + (h - a.hq)) * block + (off + token) * 16u;
-        *reinterpret_cast<uint4 *>(p + (uint64_t)run0 * page * 16u) = pack8(x);
-        *reinterpret_cast<uint4 *>(p + (uint64_t)run1 * page * 16u) = pack8(x + 8);
-      }
-    } else if (__any(!is_q && live)) {
-      const uint32_t top = row_max(top16(x), G);
-      if (!is_q && live && id >= 0) {
-        uint32_t codes[4];
-        float scale;
-        quantize16(x, top, codes, &scale);
-        uint8_t *p = a.k_cache + ((uint64_t)id * a.hk + (h - a.hq)) * block;
-        *reinterpret_cast<uint2 *>(p + ((run0 / 2u) * page + off + token) * 16u + (run0 & 1u) * 8u) = make_uint2(codes[0], codes[1]);
-        *reinterpret_cast<uint2 *>(p + ((run1 / 2u) * page + off + token) * 16u + (run1 & 1u) * 8u) = make_uint2(codes[2], codes[3]);
-        if (lane == 0u) *reinterpret_cast<float *>(p + page * a.d + (off + token) * 4u) = scale;
-      }
-    }
-  }
     return;
   }
   if (id < 0) return;  // (the whole workgroup)

@@ -128,451 +128,451 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(kDP, kBits, kNT, kCut)) void 
     end_block = min(at_block + per, all);
   }
   while (at_block < end_block) {
-  uint32_t seq, inside;
-  if (!paged_find(kCut ? at_block : slot, a.count, [&](uint32_t i) {
-        const Job j = job_of(a, paged_span(a, i), kRows);
-        return kCut ? j.tiles * j.blocks : j.tiles;
-      }, &seq, &inside))
-    return;
-  const PagedSpan p = paged_span(a, seq);
-  const Job job = job_of(a, p, kRows);
-  const uint32_t tile = kCut ? inside / job.blocks : inside, skip = kCut ? inside % job.blocks : 0u;
-  const uint32_t take = kCut ? min(job.blocks - skip, end_block - at_block) : job.blocks;
-  const int32_t key_begin = (job.first + (int32_t)skip) * (int32_t)kBlock;
-  const int32_t key_end = min((job.first + (int32_t)(skip + take)) * (int32_t)kBlock, p.keys);
-  if constexpr (kCut) __syncthreads();  // LDS of the last part has been read
+    uint32_t seq, inside;
+    if (!paged_find(kCut ? at_block : slot, a.count, [&](uint32_t i) {
+          const Job j = job_of(a, paged_span(a, i), kRows);
+          return kCut ? j.tiles * j.blocks : j.tiles;
+        }, &seq, &inside))
+      return;
+    const PagedSpan p = paged_span(a, seq);
+    const Job job = job_of(a, p, kRows);
+    const uint32_t tile = kCut ? inside / job.blocks : inside, skip = kCut ? inside % job.blocks : 0u;
+    const uint32_t take = kCut ? min(job.blocks - skip, end_block - at_block) : job.blocks;
+    const int32_t key_begin = (job.first + (int32_t)skip) * (int32_t)kBlock;
+    const int32_t key_end = min((job.first + (int32_t)(skip + take)) * (int32_t)kBlock, p.keys);
+    if constexpr (kCut) __syncthreads();  // LDS of the last part has been read
 
-  // this lane's rows: places, and the operand of q
-  const uint32_t page = 1u << a.page_shift, d = kExact ? kDP : a.d, block = paged_block_bytes(page, d, kBits), units = d / kUnit;
-  int32_t pos[kNT], low[kNT];
-  constexpr bool kShared = kDP > 128 || kNT > 1;  // q in LDS, where a lane's registers do not suffice
-  v4u q[kNT][kKS * kHalves];
+    // this lane's rows: places, and the operand of q
+    const uint32_t page = 1u << a.page_shift, d = kExact ? kDP : a.d, block = paged_block_bytes(page, d, kBits), units = d / kUnit;
+    int32_t pos[kNT], low[kNT];
+    constexpr bool kShared = kDP > 128 || kNT > 1;  // q in LDS, where a lane's registers do not suffice
+    v4u q[kNT][kKS * kHalves];
 #pragma unroll
-  for (uint32_t t = 0; t < kNT; ++t) {
-    const uint32_t row = tile * kRows + t * 16u + r, token = row / g, hh = row % g;
-    const bool live = row < job.rows;
-    pos[t] = live ? p.at + (int32_t)token : -1;
-    low[t] = a.window && live ? (int32_t)max((int64_t)pos[t] + 1 - (int64_t)a.window, (int64_t)0) : 0;
-    const uint16_t *from = a.q + (uint64_t)(p.first + (live ? token : 0u)) * a.q_token + (uint64_t)(head * g + hh) * a.q_head;
+    for (uint32_t t = 0; t < kNT; ++t) {
+      const uint32_t row = tile * kRows + t * 16u + r, token = row / g, hh = row % g;
+      const bool live = row < job.rows;
+      pos[t] = live ? p.at + (int32_t)token : -1;
+      low[t] = a.window && live ? (int32_t)max((int64_t)pos[t] + 1 - (int64_t)a.window, (int64_t)0) : 0;
+      const uint16_t *from = a.q + (uint64_t)(p.first + (live ? token : 0u)) * a.q_token + (uint64_t)(head * g + hh) * a.q_head;
 #pragma unroll
-    for (uint32_t s = 0; s < kKS; ++s)
+      for (uint32_t s = 0; s < kKS; ++s)
 #pragma unroll
-      for (uint32_t h = 0; h < kHalves; ++h) {
-        v4u v = {0, 0, 0, 0};
-        const uint32_t unit = 4u * s + c;
-        const uint32_t i = t * kKS * kHalves + s * kHalves + h;
-        if (kShared && i % kWaves != wave) continue;
-        if (live && unit < units) v = *reinterpret_cast<const v4u *>(from + unit * kUnit + h * 8u);
-        if constexpr (kShared)
-          *reinterpret_cast<v4u *>(lds + (i * 64u + lane) * 16u) = v;
-        else
-          q[t][s * kHalves + h] = v;
-      }
-  }
-  if constexpr (kShared) __syncthreads();
-  auto q_of = [&](uint32_t n, uint32_t i) {
-    if constexpr (kShared) return *reinterpret_cast<const v4u *>(lds + ((n * kKS * kHalves + i) * 64u + lane) * 16u);
-    return q[n][i];
-  };
-  // keys that all of the tile's rows see lie in [all_low, all_pos], those that any
-  // does in [any_low, any_pos]
-  int32_t all_pos, all_low, any_pos, any_low;
-  {
-    const uint32_t row0 = tile * kRows, row1 = min(row0 + kRows, job.rows) - 1u;
-    all_pos = p.at + (int32_t)(row0 / g);
-    any_pos = p.at + (int32_t)(row1 / g);
-    any_low = a.window ? (int32_t)max((int64_t)all_pos + 1 - (int64_t)a.window, (int64_t)0) : 0;
-    all_low = a.window ? (int32_t)max((int64_t)any_pos + 1 - (int64_t)a.window, (int64_t)0) : 0;
-  }
-
-  float scale2 = a.scale2, cap2 = a.cap2, inv2 = a.cap_inv2;
-  asm volatile("" : "+v"(scale2), "+v"(cap2), "+v"(inv2));  // (else loaded anew in each step)
-  float m[kNT], l[kNT];
-  v4f o[kNT][kDB];
-#pragma unroll
-  for (uint32_t t = 0; t < kNT; ++t) {
-    m[t] = -INFINITY;
-    l[t] = 0.0f;
-#pragma unroll
-    for (uint32_t b = 0; b < kDB; ++b) o[t][b] = v4f{0, 0, 0, 0};
-  }
-
-  const int32_t *table = a.table + (uint64_t)seq * a.width;
-  const uint8_t *kc = a.k_cache + (uint64_t)head * block, *vc = a.v_cache + (uint64_t)head * block;
-  const uint64_t page_bytes = (uint64_t)block * a.hk;
-
-  // A step: 32 keys (int8: 64).  Values are on their way while the scores are made,
-  // the next step's keys while the softmax is.
-  constexpr int32_t kStride = (int32_t)(kWaves * kKeys);
-  auto ids_of = [&](int32_t key0, v4u &ids) {  // the pages of its tiles of 16 keys
-#pragma unroll
-    for (uint32_t t = 0; t < kKT; ++t) {
-      const uint32_t at = (uint32_t)(key0 + (int32_t)(16u * t)) >> a.page_shift;
-      ids[t] = __builtin_amdgcn_readfirstlane(at < a.width ? (uint32_t)table[at] : ~0u);
+        for (uint32_t h = 0; h < kHalves; ++h) {
+          v4u v = {0, 0, 0, 0};
+          const uint32_t unit = 4u * s + c;
+          const uint32_t i = t * kKS * kHalves + s * kHalves + h;
+          if (kShared && i % kWaves != wave) continue;
+          if (live && unit < units) v = *reinterpret_cast<const v4u *>(from + unit * kUnit + h * 8u);
+          if constexpr (kShared)
+            *reinterpret_cast<v4u *>(lds + (i * 64u + lane) * 16u) = v;
+          else
+            q[t][s * kHalves + h] = v;
+        }
     }
-  };
-  v4u k[kKT][kKS];
-  v4f ks[kKT];
-  auto load_k = [&](int32_t key0, const v4u &ids) {
+    if constexpr (kShared) __syncthreads();
+    auto q_of = [&](uint32_t n, uint32_t i) {
+      if constexpr (kShared) return *reinterpret_cast<const v4u *>(lds + ((n * kKS * kHalves + i) * 64u + lane) * 16u);
+      return q[n][i];
+    };
+    // keys that all of the tile's rows see lie in [all_low, all_pos], those that any
+    // does in [any_low, any_pos]
+    int32_t all_pos, all_low, any_pos, any_low;
+    {
+      const uint32_t row0 = tile * kRows, row1 = min(row0 + kRows, job.rows) - 1u;
+      all_pos = p.at + (int32_t)(row0 / g);
+      any_pos = p.at + (int32_t)(row1 / g);
+      any_low = a.window ? (int32_t)max((int64_t)all_pos + 1 - (int64_t)a.window, (int64_t)0) : 0;
+      all_low = a.window ? (int32_t)max((int64_t)any_pos + 1 - (int64_t)a.window, (int64_t)0) : 0;
+    }
+
+    float scale2 = a.scale2, cap2 = a.cap2, inv2 = a.cap_inv2;
+    asm volatile("" : "+v"(scale2), "+v"(cap2), "+v"(inv2));  // (else loaded anew in each step)
+    float m[kNT], l[kNT];
+    v4f o[kNT][kDB];
 #pragma unroll
-    for (uint32_t t = 0; t < kKT; ++t) {
-      const uint32_t id = ids[t] < a.pages ? ids[t] : 0u, off = (uint32_t)(key0 + (int32_t)(16u * t)) & (page - 1u);
-      const uint8_t *base = kc + id * page_bytes + off * 16u;
+    for (uint32_t t = 0; t < kNT; ++t) {
+      m[t] = -INFINITY;
+      l[t] = 0.0f;
 #pragma unroll
-      for (uint32_t s = 0; s < kKS; ++s) {
-        if (kExact && 4u * s + 4u <= kDP / kUnit) {
-          k[t][s] = *reinterpret_cast<const v4u *>(base + (uint64_t)(4u * s) * page * 16u + (c * page + r) * 16u);
-        } else {  // (beyond the head's units: the first again, as zeros)
-          const bool has = 4u * s + c < units;
-          k[t][s] = *reinterpret_cast<const v4u *>(base + ((has ? 4u * s + c : 0u) * page + r) * 16u);
-          if (!has) k[t][s] = v4u{0, 0, 0, 0};
+      for (uint32_t b = 0; b < kDB; ++b) o[t][b] = v4f{0, 0, 0, 0};
+    }
+
+    const int32_t *table = a.table + (uint64_t)seq * a.width;
+    const uint8_t *kc = a.k_cache + (uint64_t)head * block, *vc = a.v_cache + (uint64_t)head * block;
+    const uint64_t page_bytes = (uint64_t)block * a.hk;
+
+    // A step: 32 keys (int8: 64).  Values are on their way while the scores are made,
+    // the next step's keys while the softmax is.
+    constexpr int32_t kStride = (int32_t)(kWaves * kKeys);
+    auto ids_of = [&](int32_t key0, v4u &ids) {  // the pages of its tiles of 16 keys
+#pragma unroll
+      for (uint32_t t = 0; t < kKT; ++t) {
+        const uint32_t at = (uint32_t)(key0 + (int32_t)(16u * t)) >> a.page_shift;
+        ids[t] = __builtin_amdgcn_readfirstlane(at < a.width ? (uint32_t)table[at] : ~0u);
+      }
+    };
+    v4u k[kKT][kKS];
+    v4f ks[kKT];
+    auto load_k = [&](int32_t key0, const v4u &ids) {
+#pragma unroll
+      for (uint32_t t = 0; t < kKT; ++t) {
+        const uint32_t id = ids[t] < a.pages ? ids[t] : 0u, off = (uint32_t)(key0 + (int32_t)(16u * t)) & (page - 1u);
+        const uint8_t *base = kc + id * page_bytes + off * 16u;
+#pragma unroll
+        for (uint32_t s = 0; s < kKS; ++s) {
+          if (kExact && 4u * s + 4u <= kDP / kUnit) {
+            k[t][s] = *reinterpret_cast<const v4u *>(base + (uint64_t)(4u * s) * page * 16u + (c * page + r) * 16u);
+          } else {  // (beyond the head's units: the first again, as zeros)
+            const bool has = 4u * s + c < units;
+            k[t][s] = *reinterpret_cast<const v4u *>(base + ((has ? 4u * s + c : 0u) * page + r) * 16u);
+            if (!has) k[t][s] = v4u{0, 0, 0, 0};
+          }
+        }
+        if constexpr (kBits == 8u) ks[t] = *reinterpret_cast<const v4f *>(kc + id * page_bytes + page * d + (off + 4u * c) * 4u);
+      }
+    };
+
+    Run v[kDB];  // of keys kOwn c.. of the step
+    v4f vs[kKT];
+    auto load_v = [&](int32_t key0, const v4u &ids) {
+      const uint32_t t = c * kOwn / 16u;
+      uint32_t id = ids[0];
+#pragma unroll
+      for (uint32_t i = 1; i < kKT; ++i) id = t == i ? ids[i] : id;
+      id = id < a.pages ? id : 0u;
+      const uint32_t off = (uint32_t)(key0 + (int32_t)(c * kOwn)) & (page - 1u);
+      const uint8_t *base = vc + id * page_bytes + ((uint64_t)(off / kUnit) * d + r) * 16u + (kOwn < kUnit ? off % kUnit * (kBits / 8u) : 0u);
+#pragma unroll
+      for (uint32_t b = 0; b < kDB; ++b) {
+        // (beyond the head's values: the first again, whose sums are not taken)
+        v[b] = *reinterpret_cast<const Run *>(base + (kExact || 16u * b < d ? b : 0u) * 256u);
+      }
+      if constexpr (kBits == 8u) {
+#pragma unroll
+        for (uint32_t i = 0; i < kKT; ++i) {
+          const uint32_t at = ids[i] < a.pages ? ids[i] : 0u, to = (uint32_t)(key0 + (int32_t)(16u * i)) & (page - 1u);
+          vs[i] = *reinterpret_cast<const v4f *>(vc + at * page_bytes + page * d + (to + 4u * c) * 4u);
         }
       }
-      if constexpr (kBits == 8u) ks[t] = *reinterpret_cast<const v4f *>(kc + id * page_bytes + page * d + (off + 4u * c) * 4u);
-    }
-  };
-
-  Run v[kDB];  // of keys kOwn c.. of the step
-  v4f vs[kKT];
-  auto load_v = [&](int32_t key0, const v4u &ids) {
-    const uint32_t t = c * kOwn / 16u;
-    uint32_t id = ids[0];
-#pragma unroll
-    for (uint32_t i = 1; i < kKT; ++i) id = t == i ? ids[i] : id;
-    id = id < a.pages ? id : 0u;
-    const uint32_t off = (uint32_t)(key0 + (int32_t)(c * kOwn)) & (page - 1u);
-    const uint8_t *base = vc + id * page_bytes + ((uint64_t)(off / kUnit) * d + r) * 16u + (kOwn < kUnit ? off % kUnit * (kBits / 8u) : 0u);
-#pragma unroll
-    for (uint32_t b = 0; b < kDB; ++b) {
-      // (beyond the head's values: the first again, whose sums are not taken)
-      v[b] = *reinterpret_cast<const Run *>(base + (kExact || 16u * b < d ? b : 0u) * 256u);
-    }
-    if constexpr (kBits == 8u) {
-#pragma unroll
-      for (uint32_t i = 0; i < kKT; ++i) {
-        const uint32_t at = ids[i] < a.pages ? ids[i] : 0u, to = (uint32_t)(key0 + (int32_t)(16u * i)) & (page - 1u);
-        vs[i] = *reinterpret_cast<const v4f *>(vc + at * page_bytes + page * d + (to + 4u * c) * 4u);
-      }
-    }
-  };
-  v4f x[kNT][kKT];
-  auto scores = [&] {
-#pragma unroll
-    for (uint32_t t = 0; t < kKT; ++t)
-#pragma unroll
-      for (uint32_t n = 0; n < kNT; ++n) x[n][t] = v4f{0, 0, 0, 0};
-    if constexpr (kBits == 8u) {  // (else the loop carries every code in a register of its own)
-#pragma unroll
-      for (uint32_t t = 0; t < kKT; ++t)
-#pragma unroll
-        for (uint32_t i = 0; i < kKS; ++i) asm volatile("" : "+v"(k[t][i]));
-    }
-    auto product = [&](uint32_t t, uint32_t s, uint32_t h, const v4u (&qq)[kNT]) {
-      const v4u kk = kBits == 16u ? k[t][s] : bf16_of_codes(k[t][s][2 * h], k[t][s][2 * h + 1]);
-#pragma unroll
-      for (uint32_t n = 0; n < kNT; ++n) x[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(kk), as_bf(qq[n]), x[n][t], 0, 0, 0);
-      if constexpr (kBits == 8u) __builtin_amdgcn_sched_barrier(0);  // (else all codes are unpacked at once)
     };
-    if constexpr (kShared) {
-#pragma unroll
-      for (uint32_t i = 0; i < kKS * kHalves; ++i) {
-        v4u qq[kNT];
-#pragma unroll
-        for (uint32_t n = 0; n < kNT; ++n) qq[n] = q_of(n, i);
-#pragma unroll
-        for (uint32_t t = 0; t < kKT; ++t) product(t, i / kHalves, i % kHalves, qq);
-      }
-    } else {
+    v4f x[kNT][kKT];
+    auto scores = [&] {
 #pragma unroll
       for (uint32_t t = 0; t < kKT; ++t)
+#pragma unroll
+        for (uint32_t n = 0; n < kNT; ++n) x[n][t] = v4f{0, 0, 0, 0};
+      if constexpr (kBits == 8u) {  // (else the loop carries every code in a register of its own)
+#pragma unroll
+        for (uint32_t t = 0; t < kKT; ++t)
+#pragma unroll
+          for (uint32_t i = 0; i < kKS; ++i) asm volatile("" : "+v"(k[t][i]));
+      }
+      auto product = [&](uint32_t t, uint32_t s, uint32_t h, const v4u (&qq)[kNT]) {
+        const v4u kk = kBits == 16u ? k[t][s] : bf16_of_codes(k[t][s][2 * h], k[t][s][2 * h + 1]);
+#pragma unroll
+        for (uint32_t n = 0; n < kNT; ++n) x[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(kk), as_bf(qq[n]), x[n][t], 0, 0, 0);
+        if constexpr (kBits == 8u) __builtin_amdgcn_sched_barrier(0);  // (else all codes are unpacked at once)
+      };
+      if constexpr (kShared) {
 #pragma unroll
         for (uint32_t i = 0; i < kKS * kHalves; ++i) {
           v4u qq[kNT];
 #pragma unroll
           for (uint32_t n = 0; n < kNT; ++n) qq[n] = q_of(n, i);
-          product(t, i / kHalves, i % kHalves, qq);
+#pragma unroll
+          for (uint32_t t = 0; t < kKT; ++t) product(t, i / kHalves, i % kHalves, qq);
         }
-    }
-    if constexpr (kBits == 8u) {
-#pragma unroll
-      for (uint32_t n = 0; n < kNT; ++n)
-#pragma unroll
-        for (uint32_t t = 0; t < kKT; ++t) x[n][t] *= ks[t];
-    }
-  };
-  // scores to weights, where the lanes' units of v want them.  hole: bit t where the
-  // step's keys 16 t.. lie in no page; whole: all rows see all keys.
-  v4u ph[kNT][kHalvesV], pl[kNT][kHalvesV];
-  auto weigh = [&](int32_t key0, uint32_t hole, bool whole) {
-#pragma unroll
-    for (uint32_t n = 0; n < kNT; ++n) {
-      if (a.cap != 0.0f) {
-        if (a.cap <= kShortCap) {
-#pragma unroll
-          for (uint32_t t = 0; t < kKT; ++t)
-#pragma unroll
-            for (uint32_t e = 0; e < 4; ++e) x[n][t][e] = capped(x[n][t][e], cap2, inv2);
-        } else {
-#pragma unroll
-          for (uint32_t t = 0; t < kKT; ++t)
-#pragma unroll
-            for (uint32_t e = 0; e < 4; ++e) x[n][t][e] = capped_large(x[n][t][e], a);
-        }
-      }
-      if (!whole) {
+      } else {
 #pragma unroll
         for (uint32_t t = 0; t < kKT; ++t)
 #pragma unroll
-          for (uint32_t e = 0; e < 4; ++e) {
-            const int32_t key = key0 + (int32_t)(16u * t + 4u * c + e);
-            const bool seen = key <= pos[n] && key >= low[n] && key < key_end && !(hole >> t & 1u);
-            x[n][t][e] = seen ? x[n][t][e] : -INFINITY;
+          for (uint32_t i = 0; i < kKS * kHalves; ++i) {
+            v4u qq[kNT];
+#pragma unroll
+            for (uint32_t n = 0; n < kNT; ++n) qq[n] = q_of(n, i);
+            product(t, i / kHalves, i % kHalves, qq);
           }
       }
-      float top = x[n][0][0];
+      if constexpr (kBits == 8u) {
 #pragma unroll
-      for (uint32_t t = 0; t < kKT; ++t) top = fmaxf(fmaxf(fmaxf(x[n][t][0], x[n][t][1]), top), fmaxf(x[n][t][2], x[n][t][3]));
-      top *= scale2;
-      if (__ballot(top > m[n])) {
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float next = fmaxf(m[n], top + kSlack);
-        const float keep = m[n] == -INFINITY ? 0.0f : exp2_hw(m[n] - next);
-        m[n] = next;
-        l[n] *= keep;
+        for (uint32_t n = 0; n < kNT; ++n)
 #pragma unroll
-        for (uint32_t b = 0; b < kDB; ++b) o[n][b] *= keep;
+          for (uint32_t t = 0; t < kKT; ++t) x[n][t] *= ks[t];
       }
-      const float base = m[n] == -INFINITY ? 0.0f : m[n];
-      // the sum of two bf16: one would be off by 2^-8 of each weight.  Over a bf16 cache the
-      // first is below the weight, so that the second is above 0 too, and an infinity of v
-      // times both stays one (by 2^-15 off, to the nearest by 2^-16; the same time).
-      uint32_t hi[kKT][2], lo[kKT][2];
+    };
+    // scores to weights, where the lanes' units of v want them.  hole: bit t where the
+    // step's keys 16 t.. lie in no page; whole: all rows see all keys.
+    v4u ph[kNT][kHalvesV], pl[kNT][kHalvesV];
+    auto weigh = [&](int32_t key0, uint32_t hole, bool whole) {
 #pragma unroll
-      for (uint32_t t = 0; t < kKT; ++t) {
-        float w[4];
+      for (uint32_t n = 0; n < kNT; ++n) {
+        if (a.cap != 0.0f) {
+          if (a.cap <= kShortCap) {
 #pragma unroll
-        for (uint32_t e = 0; e < 4; ++e) {
-          const float s = x[n][t][e];
-          w[e] = exp2_hw(fmaf(s, scale2, -base));
-          l[n] += w[e];
-          if constexpr (kBits == 8u) w[e] = s == -INFINITY ? 0.0f : w[e] * vs[t][e];
-        }
+            for (uint32_t t = 0; t < kKT; ++t)
 #pragma unroll
-        for (uint32_t e = 0; e < 2; ++e) {
-          if constexpr (kBits == 16u)
-            hi[t][e] = __builtin_amdgcn_perm(below(w[2 * e + 1]), below(w[2 * e]), 0x07060302u);
-          else
-            hi[t][e] = two_bf16(w[2 * e], w[2 * e + 1]);
-          lo[t][e] = two_bf16(w[2 * e] - __uint_as_float(hi[t][e] << 16), w[2 * e + 1] - __uint_as_float(hi[t][e] & 0xFFFF0000u));
-        }
-      }
-      // lanes of group c have keys 4 c.. of every tile, and want the keys of their unit
-      auto turn = [&](uint32_t (&w)[kKT][2], v4u *out) {
-#pragma unroll
-        for (uint32_t e = 0; e < 2; ++e) {
-          if constexpr (kKT == 2u) {
-            const v2u s = __builtin_amdgcn_permlane32_swap(w[0][e], w[1][e], false, false);
-            const v2u f = __builtin_amdgcn_permlane16_swap(s.x, s.y, false, false);
-            out[0][e] = f.x;
-            out[0][2 + e] = f.y;
+              for (uint32_t e = 0; e < 4; ++e) x[n][t][e] = capped(x[n][t][e], cap2, inv2);
           } else {
-            const v2u s0 = __builtin_amdgcn_permlane32_swap(w[0][e], w[2][e], false, false);
-            const v2u s1 = __builtin_amdgcn_permlane32_swap(w[1][e], w[3][e], false, false);
-            const v2u f0 = __builtin_amdgcn_permlane16_swap(s0.x, s1.x, false, false);
-            const v2u f1 = __builtin_amdgcn_permlane16_swap(s0.y, s1.y, false, false);
-            out[0][e] = f0.x;
-            out[0][2 + e] = f0.y;
-            out[kHalvesV - 1][e] = f1.x;
-            out[kHalvesV - 1][2 + e] = f1.y;
+#pragma unroll
+            for (uint32_t t = 0; t < kKT; ++t)
+#pragma unroll
+              for (uint32_t e = 0; e < 4; ++e) x[n][t][e] = capped_large(x[n][t][e], a);
           }
         }
-      };
-      turn(hi, ph[n]);
-      turn(lo, pl[n]);
-    }
-  };
-  auto add_products = [&] {
+        if (!whole) {
 #pragma unroll
-    for (uint32_t b = 0; b < kDB; ++b)
+          for (uint32_t t = 0; t < kKT; ++t)
 #pragma unroll
-      for (uint32_t h = 0; h < kHalvesV; ++h) {
-        v4u u;
-        if constexpr (kBits == 16u)
-          u = v[b];
-        else
-          u = bf16_of_codes(v[b][2 * h], v[b][2 * h + 1]);
-#pragma unroll
-        for (uint32_t n = 0; n < kNT; ++n) {
-          o[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(u), as_bf(ph[n][h]), o[n][b], 0, 0, 0);
-          o[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(u), as_bf(pl[n][h]), o[n][b], 0, 0, 0);
-        }
-        if constexpr (kBits == 8u) __builtin_amdgcn_sched_barrier(0);
-      }
-  };
-  // Of a unit's eight keys (bf16), those in [from, to] that lie in a page: bit e.
-  auto seen_in = [&](int32_t key0, uint32_t hole, int32_t from, int32_t to) {
-    const int32_t at = key0 + (int32_t)(8u * c), lo = max(from - at, 0), hi = min(min(to, key_end - 1) - at, 7);
-    return hole >> (c / 2u) & 1u || lo > hi ? 0u : (0xFFu >> (7 - hi)) & (0xFFu << lo);
-  };
-  auto holes_of = [&](const v4u &ids) {
-    uint32_t hole = 0;
-#pragma unroll
-    for (uint32_t t = 0; t < kKT; ++t) hole |= ids[t] >= a.pages ? 1u << t : 0u;
-    return hole;
-  };
-  // 0 * NaN must not reach a row that does not see the NaN's key.  Codes are finite;
-  // of bf16, values that no row sees count as zero, and steps with keys that some
-  // rows see and others do not are left for the second loop.
-  auto mixed = [&](int32_t key0) {
-    const int32_t last = key0 + (int32_t)kKeys - 1;
-    return kBits == 16u && ((any_low < all_low && key0 < all_low && last >= any_low) || (all_pos < any_pos && key0 <= any_pos && last > all_pos));
-  };
-
-  v4u ids, next_ids;
-  const int32_t key_first = key_begin + (int32_t)(wave * kKeys);
-  if (key_first < key_end) {
-    ids_of(key_first, ids);
-    load_k(key_first, ids);
-    ids_of(key_first + kStride, next_ids);
-  }
-  for (int32_t key0 = key_first; key0 < key_end; key0 += kStride) {
-    const uint32_t hole = holes_of(ids);
-    load_v(key0, ids);
-    __builtin_amdgcn_sched_barrier(0);
-    scores();
-    __builtin_amdgcn_sched_barrier(0);
-    if (key0 + kStride < key_end) load_k(key0 + kStride, next_ids);
-    ids = next_ids;
-    ids_of(key0 + 2 * kStride, next_ids);
-    __builtin_amdgcn_sched_barrier(0);
-    if (mixed(key0)) continue;
-    const bool whole = !hole && key0 + (int32_t)kKeys - 1 <= all_pos && key0 >= all_low && key0 + (int32_t)kKeys <= key_end;
-    weigh(key0, hole, whole);
-    if constexpr (kBits == 16u) {
-      if (!whole) {
-        uint32_t seen = seen_in(key0, hole, any_low, any_pos);
-        asm volatile("" : "+v"(seen));  // (keeps this a branch)
-        v4u mask;
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) mask[i] = (seen >> (2u * i) & 1u ? 0xFFFFu : 0u) | (seen >> (2u * i + 1u) & 1u ? 0xFFFF0000u : 0u);
-#pragma unroll
-        for (uint32_t b = 0; b < kDB; ++b) v[b] &= mask;
-      }
-    }
-    add_products();
-  }
-  if constexpr (kBits == 16u) {
-    if (any_low < all_low || all_pos < any_pos) {
-#pragma unroll 1
-      for (int32_t key0 = key_first; key0 < key_end; key0 += kStride) {
-        if (!mixed(key0)) continue;
-        ids_of(key0, ids);
-        const uint32_t hole = holes_of(ids);
-        load_k(key0, ids);
-        load_v(key0, ids);
-        scores();
-        __builtin_amdgcn_sched_barrier(0);
-        weigh(key0, hole, false);
-        bool bad = false;
-#pragma unroll
-        for (uint32_t b = 0; b < kDB; ++b) bad |= any_not_finite(v[b]);
-        if (__ballot(bad)) {
-          // a NaN or an infinity is added where it is seen, and counts as zero in the product
-#pragma unroll
-          for (uint32_t b = 0; b < kDB; ++b) {
-            const v4u mark = not_finite_marks(v[b]);
-            v[b] = finite_only(v[b]);
-#pragma unroll
-            for (uint32_t n = 0; n < kNT; ++n) {
-              const uint32_t seen = seen_in(key0, hole, low[n], pos[n]);
-              v4u ones;
-#pragma unroll
-              for (uint32_t i = 0; i < 4; ++i)
-                ones[i] = (seen >> (2u * i) & 1u ? 0x3F80u : 0u) | (seen >> (2u * i + 1u) & 1u ? 0x3F800000u : 0u);
-              v4f marks = {0, 0, 0, 0};
-              marks = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(mark), as_bf(ones), marks, 0, 0, 0);
-#pragma unroll
-              for (uint32_t i = 0; i < 4; ++i) o[n][b][i] += of_marks(marks[i]);
+            for (uint32_t e = 0; e < 4; ++e) {
+              const int32_t key = key0 + (int32_t)(16u * t + 4u * c + e);
+              const bool seen = key <= pos[n] && key >= low[n] && key < key_end && !(hole >> t & 1u);
+              x[n][t][e] = seen ? x[n][t][e] : -INFINITY;
             }
-            __builtin_amdgcn_sched_barrier(0);
+        }
+        float top = x[n][0][0];
+#pragma unroll
+        for (uint32_t t = 0; t < kKT; ++t) top = fmaxf(fmaxf(fmaxf(x[n][t][0], x[n][t][1]), top), fmaxf(x[n][t][2], x[n][t][3]));
+        top *= scale2;
+        if (__ballot(top > m[n])) {
+          top = fmaxf(top, __shfl_xor(top, 16, 64));
+          top = fmaxf(top, __shfl_xor(top, 32, 64));
+          const float next = fmaxf(m[n], top + kSlack);
+          const float keep = m[n] == -INFINITY ? 0.0f : exp2_hw(m[n] - next);
+          m[n] = next;
+          l[n] *= keep;
+#pragma unroll
+          for (uint32_t b = 0; b < kDB; ++b) o[n][b] *= keep;
+        }
+        const float base = m[n] == -INFINITY ? 0.0f : m[n];
+        // the sum of two bf16: one would be off by 2^-8 of each weight.  Over a bf16 cache the
+        // first is below the weight, so that the second is above 0 too, and an infinity of v
+        // times both stays one (by 2^-15 off, to the nearest by 2^-16; the same time).
+        uint32_t hi[kKT][2], lo[kKT][2];
+#pragma unroll
+        for (uint32_t t = 0; t < kKT; ++t) {
+          float w[4];
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) {
+            const float s = x[n][t][e];
+            w[e] = exp2_hw(fmaf(s, scale2, -base));
+            l[n] += w[e];
+            if constexpr (kBits == 8u) w[e] = s == -INFINITY ? 0.0f : w[e] * vs[t][e];
+          }
+#pragma unroll
+          for (uint32_t e = 0; e < 2; ++e) {
+            if constexpr (kBits == 16u)
+              hi[t][e] = __builtin_amdgcn_perm(below(w[2 * e + 1]), below(w[2 * e]), 0x07060302u);
+            else
+              hi[t][e] = two_bf16(w[2 * e], w[2 * e + 1]);
+            lo[t][e] = two_bf16(w[2 * e] - __uint_as_float(hi[t][e] << 16), w[2 * e + 1] - __uint_as_float(hi[t][e] & 0xFFFF0000u));
           }
         }
-        add_products();
+        // lanes of group c have keys 4 c.. of every tile, and want the keys of their unit
+        auto turn = [&](uint32_t (&w)[kKT][2], v4u *out) {
+#pragma unroll
+          for (uint32_t e = 0; e < 2; ++e) {
+            if constexpr (kKT == 2u) {
+              const v2u s = __builtin_amdgcn_permlane32_swap(w[0][e], w[1][e], false, false);
+              const v2u f = __builtin_amdgcn_permlane16_swap(s.x, s.y, false, false);
+              out[0][e] = f.x;
+              out[0][2 + e] = f.y;
+            } else {
+              const v2u s0 = __builtin_amdgcn_permlane32_swap(w[0][e], w[2][e], false, false);
+              const v2u s1 = __builtin_amdgcn_permlane32_swap(w[1][e], w[3][e], false, false);
+              const v2u f0 = __builtin_amdgcn_permlane16_swap(s0.x, s1.x, false, false);
+              const v2u f1 = __builtin_amdgcn_permlane16_swap(s0.y, s1.y, false, false);
+              out[0][e] = f0.x;
+              out[0][2 + e] = f0.y;
+              out[kHalvesV - 1][e] = f1.x;
+              out[kHalvesV - 1][2 + e] = f1.y;
+            }
+          }
+        };
+        turn(hi, ph[n]);
+        turn(lo, pl[n]);
       }
-    }
-  }
+    };
+    auto add_products = [&] {
+#pragma unroll
+      for (uint32_t b = 0; b < kDB; ++b)
+#pragma unroll
+        for (uint32_t h = 0; h < kHalvesV; ++h) {
+          v4u u;
+          if constexpr (kBits == 16u)
+            u = v[b];
+          else
+            u = bf16_of_codes(v[b][2 * h], v[b][2 * h + 1]);
+#pragma unroll
+          for (uint32_t n = 0; n < kNT; ++n) {
+            o[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(u), as_bf(ph[n][h]), o[n][b], 0, 0, 0);
+            o[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(u), as_bf(pl[n][h]), o[n][b], 0, 0, 0);
+          }
+          if constexpr (kBits == 8u) __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // Of a unit's eight keys (bf16), those in [from, to] that lie in a page: bit e.
+    auto seen_in = [&](int32_t key0, uint32_t hole, int32_t from, int32_t to) {
+      const int32_t at = key0 + (int32_t)(8u * c), lo = max(from - at, 0), hi = min(min(to, key_end - 1) - at, 7);
+      return hole >> (c / 2u) & 1u || lo > hi ? 0u : (0xFFu >> (7 - hi)) & (0xFFu << lo);
+    };
+    auto holes_of = [&](const v4u &ids) {
+      uint32_t hole = 0;
+#pragma unroll
+      for (uint32_t t = 0; t < kKT; ++t) hole |= ids[t] >= a.pages ? 1u << t : 0u;
+      return hole;
+    };
+    // 0 * NaN must not reach a row that does not see the NaN's key.  Codes are finite;
+    // of bf16, values that no row sees count as zero, and steps with keys that some
+    // rows see and others do not are left for the second loop.
+    auto mixed = [&](int32_t key0) {
+      const int32_t last = key0 + (int32_t)kKeys - 1;
+      return kBits == 16u && ((any_low < all_low && key0 < all_low && last >= any_low) || (all_pos < any_pos && key0 <= any_pos && last > all_pos));
+    };
 
-  // the waves' results, two and two
-#pragma unroll
-  for (uint32_t n = 0; n < kNT; ++n) {
-    l[n] += __shfl_xor(l[n], 16, 64);
-    l[n] += __shfl_xor(l[n], 32, 64);
-  }
-  float *const shared = reinterpret_cast<float *>(lds);
-  float2 *const shared_stats = reinterpret_cast<float2 *>(lds + (kWaves / 2u) * kRows * kPitch * 4u);
-#pragma unroll
-  for (uint32_t half = kWaves / 2u; half >= 1u; half /= 2u) {
-    __syncthreads();
-    if (wave >= half && wave < 2u * half) {
-      const uint32_t at = wave - half;
-#pragma unroll
-      for (uint32_t n = 0; n < kNT; ++n) {
-        const uint32_t row = at * kRows + n * 16u + r;
-        if (c == 0u) shared_stats[row] = make_float2(m[n], l[n]);
-#pragma unroll
-        for (uint32_t b = 0; b < kDB; ++b) *reinterpret_cast<v4f *>(shared + row * kPitch + 16u * b + 4u * c) = o[n][b];
-      }
+    v4u ids, next_ids;
+    const int32_t key_first = key_begin + (int32_t)(wave * kKeys);
+    if (key_first < key_end) {
+      ids_of(key_first, ids);
+      load_k(key_first, ids);
+      ids_of(key_first + kStride, next_ids);
     }
-    __syncthreads();
-    if (wave < half) {
+    for (int32_t key0 = key_first; key0 < key_end; key0 += kStride) {
+      const uint32_t hole = holes_of(ids);
+      load_v(key0, ids);
+      __builtin_amdgcn_sched_barrier(0);
+      scores();
+      __builtin_amdgcn_sched_barrier(0);
+      if (key0 + kStride < key_end) load_k(key0 + kStride, next_ids);
+      ids = next_ids;
+      ids_of(key0 + 2 * kStride, next_ids);
+      __builtin_amdgcn_sched_barrier(0);
+      if (mixed(key0)) continue;
+      const bool whole = !hole && key0 + (int32_t)kKeys - 1 <= all_pos && key0 >= all_low && key0 + (int32_t)kKeys <= key_end;
+      weigh(key0, hole, whole);
+      if constexpr (kBits == 16u) {
+        if (!whole) {
+          uint32_t seen = seen_in(key0, hole, any_low, any_pos);
+          asm volatile("" : "+v"(seen));  // (keeps this a branch)
+          v4u mask;
 #pragma unroll
-      for (uint32_t n = 0; n < kNT; ++n) {
-        const uint32_t row = wave * kRows + n * 16u + r;
-        const float2 other = shared_stats[row];
-        const float next = fmaxf(m[n], other.x);
-        const float mine = m[n] == -INFINITY ? 0.0f : exp2_hw(m[n] - next);
-        const float theirs = other.x == -INFINITY ? 0.0f : exp2_hw(other.x - next);
-        l[n] = l[n] * mine + other.y * theirs;
-        m[n] = next;
+          for (uint32_t i = 0; i < 4; ++i) mask[i] = (seen >> (2u * i) & 1u ? 0xFFFFu : 0u) | (seen >> (2u * i + 1u) & 1u ? 0xFFFF0000u : 0u);
 #pragma unroll
-        for (uint32_t b = 0; b < kDB; ++b) {
-          const v4f y = *reinterpret_cast<const v4f *>(shared + row * kPitch + 16u * b + 4u * c);
-          o[n][b] = o[n][b] * mine + y * theirs;
+          for (uint32_t b = 0; b < kDB; ++b) v[b] &= mask;
+        }
+      }
+      add_products();
+    }
+    if constexpr (kBits == 16u) {
+      if (any_low < all_low || all_pos < any_pos) {
+#pragma unroll 1
+        for (int32_t key0 = key_first; key0 < key_end; key0 += kStride) {
+          if (!mixed(key0)) continue;
+          ids_of(key0, ids);
+          const uint32_t hole = holes_of(ids);
+          load_k(key0, ids);
+          load_v(key0, ids);
+          scores();
+          __builtin_amdgcn_sched_barrier(0);
+          weigh(key0, hole, false);
+          bool bad = false;
+#pragma unroll
+          for (uint32_t b = 0; b < kDB; ++b) bad |= any_not_finite(v[b]);
+          if (__ballot(bad)) {
+            // a NaN or an infinity is added where it is seen, and counts as zero in the product
+#pragma unroll
+            for (uint32_t b = 0; b < kDB; ++b) {
+              const v4u mark = not_finite_marks(v[b]);
+              v[b] = finite_only(v[b]);
+#pragma unroll
+              for (uint32_t n = 0; n < kNT; ++n) {
+                const uint32_t seen = seen_in(key0, hole, low[n], pos[n]);
+                v4u ones;
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i)
+                  ones[i] = (seen >> (2u * i) & 1u ? 0x3F80u : 0u) | (seen >> (2u * i + 1u) & 1u ? 0x3F800000u : 0u);
+                v4f marks = {0, 0, 0, 0};
+                marks = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(mark), as_bf(ones), marks, 0, 0, 0);
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i) o[n][b][i] += of_marks(marks[i]);
+              }
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          }
+          add_products();
         }
       }
     }
-  }
-  if (wave == 0u) {
+
+    // the waves' results, two and two
 #pragma unroll
     for (uint32_t n = 0; n < kNT; ++n) {
-      const uint32_t row = tile * kRows + n * 16u + r;
-      if (row >= job.rows) continue;
-      if (!kCut || take == job.blocks) {
-        const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
-        uint16_t *to = a.out + ((uint64_t)(p.first + row / g) * a.hq + head * g + row % g) * d;
+      l[n] += __shfl_xor(l[n], 16, 64);
+      l[n] += __shfl_xor(l[n], 32, 64);
+    }
+    float *const shared = reinterpret_cast<float *>(lds);
+    float2 *const shared_stats = reinterpret_cast<float2 *>(lds + (kWaves / 2u) * kRows * kPitch * 4u);
 #pragma unroll
-        for (uint32_t b = 0; b < kDB; ++b)
-          if (16u * b < d)
-            *reinterpret_cast<uint2 *>(to + 16u * b + 4u * c) =
-                make_uint2(pack_bf16x2(o[n][b][0] * inv, o[n][b][1] * inv), pack_bf16x2(o[n][b][2] * inv, o[n][b][3] * inv));
-      } else {
-        const uint64_t at = ((uint64_t)(2u * slot + (at_block != run_begin)) * a.hk + head) * kRows + n * 16u + r;
-        if (c == 0u) parts.stats[at] = make_float2(m[n], l[n]);
+    for (uint32_t half = kWaves / 2u; half >= 1u; half /= 2u) {
+      __syncthreads();
+      if (wave >= half && wave < 2u * half) {
+        const uint32_t at = wave - half;
 #pragma unroll
-        for (uint32_t b = 0; b < kDB; ++b)
-          if (16u * b < d) *reinterpret_cast<v4f *>(parts.sums + at * d + 16u * b + 4u * c) = o[n][b];
+        for (uint32_t n = 0; n < kNT; ++n) {
+          const uint32_t row = at * kRows + n * 16u + r;
+          if (c == 0u) shared_stats[row] = make_float2(m[n], l[n]);
+#pragma unroll
+          for (uint32_t b = 0; b < kDB; ++b) *reinterpret_cast<v4f *>(shared + row * kPitch + 16u * b + 4u * c) = o[n][b];
+        }
+      }
+      __syncthreads();
+      if (wave < half) {
+#pragma unroll
+        for (uint32_t n = 0; n < kNT; ++n) {
+          const uint32_t row = wave * kRows + n * 16u + r;
+          const float2 other = shared_stats[row];
+          const float next = fmaxf(m[n], other.x);
+          const float mine = m[n] == -INFINITY ? 0.0f : exp2_hw(m[n] - next);
+          const float theirs = other.x == -INFINITY ? 0.0f : exp2_hw(other.x - next);
+          l[n] = l[n] * mine + other.y * theirs;
+          m[n] = next;
+#pragma unroll
+          for (uint32_t b = 0; b < kDB; ++b) {
+            const v4f y = *reinterpret_cast<const v4f *>(shared + row * kPitch + 16u * b + 4u * c);
+            o[n][b] = o[n][b] * mine + y * theirs;
+          }
+        }
       }
     }
-  }
-  if (kCut && head == 0u && skip + take == job.blocks && threadIdx.x < kRows) {
-    // the tile's rows: where their parts begin, for the second launch
-    const uint32_t job_begin = at_block - skip, slot0 = job_begin / per, row = tile * kRows + threadIdx.x;
-    if (row < job.rows)
-      parts.where[(uint64_t)p.first * g + row] =
-          make_uint2(slot0 | (job_begin != slot0 * per ? 1u << 31 : 0u), (slot - slot0 + 1u) | threadIdx.x << 16);
-  }
-  at_block += kCut ? take : 1u;
+    if (wave == 0u) {
+#pragma unroll
+      for (uint32_t n = 0; n < kNT; ++n) {
+        const uint32_t row = tile * kRows + n * 16u + r;
+        if (row >= job.rows) continue;
+        if (!kCut || take == job.blocks) {
+          const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
+          uint16_t *to = a.out + ((uint64_t)(p.first + row / g) * a.hq + head * g + row % g) * d;
+#pragma unroll
+          for (uint32_t b = 0; b < kDB; ++b)
+            if (16u * b < d)
+              *reinterpret_cast<uint2 *>(to + 16u * b + 4u * c) =
+                  make_uint2(pack_bf16x2(o[n][b][0] * inv, o[n][b][1] * inv), pack_bf16x2(o[n][b][2] * inv, o[n][b][3] * inv));
+        } else {
+          const uint64_t at = ((uint64_t)(2u * slot + (at_block != run_begin)) * a.hk + head) * kRows + n * 16u + r;
+          if (c == 0u) parts.stats[at] = make_float2(m[n], l[n]);
+#pragma unroll
+          for (uint32_t b = 0; b < kDB; ++b)
+            if (16u * b < d) *reinterpret_cast<v4f *>(parts.sums + at * d + 16u * b + 4u * c) = o[n][b];
+        }
+      }
+    }
+    if (kCut && head == 0u && skip + take == job.blocks && threadIdx.x < kRows) {
+      // the tile's rows: where their parts begin, for the second launch
+      const uint32_t job_begin = at_block - skip, slot0 = job_begin / per, row = tile * kRows + threadIdx.x;
+      if (row < job.rows)
+        parts.where[(uint64_t)p.first * g + row] =
+            make_uint2(slot0 | (job_begin != slot0 * per ? 1u << 31 : 0u), (slot - slot0 + 1u) | threadIdx.x << 16);
+    }
+    at_block += kCut ? take : 1u;
   }
 }
 
