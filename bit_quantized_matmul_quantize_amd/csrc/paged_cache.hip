@@ -8,7 +8,8 @@
 // rint(127 t / top) with a scale top / 127 per token and head.
 //
 // Bound by bytes: 2 read and 2 or 1 + 4/d written a value, a few operations each: a
-// prompt of 8192, 32 heads over 8 of 128, in bf16 205 MB in 39 us, 5.2 TB/s.
+// prompt of 8192, 32 heads over 8 of 128, in bf16 205 MB in 50 us, 4.1 TB/s (39 us where the
+// last call's lie in the 256 MB cache).
 // A workgroup takes 16 consecutive places of a sequence, aligned to 16, so that
 // they lie in one page and fill whole 16-byte units of it: a unit of k is 8 or 16
 // values of one token, and a unit of v one value of 8 or 16 tokens, for which the

@@ -3,8 +3,8 @@
 // in one pass over the cache with the running maximum and sum of the softmax.
 //
 // Bound by the cache's bytes: 64 tokens of 64 sequences up to 8192, 32 heads over 8 of
-// 128, read 1.1 GB in 199 us, 5.6 TB/s; one token behind 130000 in int8 274 MB in 54 us,
-// 5.1 TB/s; and a join of 5 to 6 us.  With several rows over an int8 cache, by the codes'
+// 128, read 1.1 GB in 201 us, 5.5 TB/s; one token behind 130000 in int8 274 MB in 61 us,
+// 4.5 TB/s; and a join of 5 to 6 us.  With several rows over an int8 cache, by the codes'
 // way to bf16 between the loads and the products of two waves a SIMD: 8 sequences of 4
 // tokens, 16 heads over 2 of 256, 74 MB in 38 us.  The rows of one product are the new tokens' heads
 // that share a key head, 16 to a column block of the matrix instruction, so that
@@ -26,8 +26,8 @@ namespace {
 
 constexpr uint32_t kBlock = 64;   // keys: the unit of the division of work
 constexpr uint32_t kLeast = 4;    // blocks of a run: one token behind 5000 16.2 us, with 8 17.5, with 1 16.3
-// Keys: sequences of up to so many are not cut: one token behind 700 11 us, cut and
-// joined 14.
+// Keys: where the table has room for up to so many, sequences are not cut: one token behind
+// 700 11.5 us, cut and joined (behind a table for 8192) 14.6.
 constexpr uint32_t kShort = 1024;
 constexpr uint32_t kCus = 256;
 
