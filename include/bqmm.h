@@ -446,7 +446,8 @@ int gated_delta_rule_chunked(const void *q_bf16, const void *k_bf16, const void 
  * cos_sin: binary32 [angles][2][rot / 2], rot a multiple of 16 up to d (0: no
  * rotation, cos_sin may be NULL).  positions: int32 [tokens] or [axes][tokens];
  * axis: uint8 [rot / 2] or NULL.  q_norm, k_norm: bf16 [d] or NULL.  |x|^2 has to
- * stay below 2^128, and mean(x^2) + eps be at least 2^-120.  No two tokens of a call may have the same place of a page. */
+ * stay below 2^128, and mean(x^2) + eps be at least 2^-120.  No two tokens of a
+ * call may have the same place of a page. */
 int rope_write_kv_cache(const void *q_bf16, const void *k_bf16, const void *v_bf16, void *q_out_bf16, void *k_cache,
                         void *v_cache, const int32_t *starts, const int32_t *lens, const int32_t *table,
                         const float *cos_sin, const int32_t *positions, const uint8_t *axis, const void *q_norm_bf16,
